@@ -16,6 +16,8 @@ Two layers:
 """
 from __future__ import annotations
 
+import array
+import collections
 import ctypes
 import os
 
@@ -56,6 +58,12 @@ TR_OP_ROW_SUM = 6
 TR_OP_ROW_MAX = 7
 TR_OP_ROW_MIN = 8
 TR_OP_ROW_MINMAX = 9
+TR_F32, TR_BF16, TR_F16 = 0, 1, 2
+TR_NORM_RMS, TR_NORM_LAYER = 0, 1
+TR_BLOCK_POST, TR_BLOCK_PRE = 1, 2
+TR_TOTAL_L2, TR_TOTAL_MAX = 0, 1
+NORM_KINDS = {"rmsnorm": TR_NORM_RMS, "layernorm": TR_NORM_LAYER}
+TOTAL_KINDS = {"l2": TR_TOTAL_L2, "max": TR_TOTAL_MAX}
 TR_PLAN_FLAG_PARAMS_IN_REGISTERS = 1
 TR_PLAN_FLAG_PARAMS_IN_SHARED = 2
 TR_PLAN_FLAG_TWO_ROWS = 4
@@ -127,6 +135,15 @@ SIGNATURES = {
     "tr_layernorm_backward_f32": ([_P, _P, _P, _P, _P, _P, _I64, _I64, _F, _I32, _P, ctypes.c_size_t, _P], _I32),
     "tr_norm_backward_workspace_bytes": ([_I64, _I64, ctypes.POINTER(ctypes.c_size_t)], _I32),
     "tr_add_layernorm_f32": ([_P, _P, _P, _P, _P, _P, _I64, _I64, _F, _I32, _P], _I32),
+    "tr_gated_residual_norm": ([_I32, _I32, _I32, _P, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _I64, _I64, _F, _F, _F,
+                                _I32, _P], _I32),
+    "tr_gated_residual_norm_backward": ([_I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P,
+                                         _P, _I64, _I64, _F, _F, _F, _I32, _P, ctypes.c_size_t, _P], _I32),
+    "tr_gated_residual_norm_backward_workspace_bytes": ([_I32, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)], _I32),
+    "tr_global_norm": ([_I32, _P, _P, _P, _I64, _P, _P, ctypes.c_size_t, _P], _I32),
+    "tr_clip_by_norm": ([_P, _P, _P, _P, _I64, _P, _F, _F, _P], _I32),
+    "tr_clip_global_norm": ([_I32, _P, _P, _P, _P, _I64, _F, _F, _P, _P, ctypes.c_size_t, _P], _I32),
+    "tr_global_norm_workspace_bytes": ([_I64, ctypes.POINTER(ctypes.c_size_t)], _I32),
     "tr_plan_describe": ([_I32, _I64, _I64, _I32, ctypes.POINTER(tr_plan)], _I32),
     "tr_plan_select_for": ([ctypes.POINTER(tr_device_desc), _I32, _I64, _I64, _I32, _I32,
                             ctypes.POINTER(tr_plan)], _I32),
@@ -537,6 +554,277 @@ def layernorm_backward(x, gamma, dy, eps=1e-5, order="unordered", want_params=Tr
                                             None if ws is None else ws.data_ptr(), n, _stream_handle(stream)),
            "layernorm_backward")
     return dx, dgamma, dbeta
+
+
+# ------------------------------------------------------------ block norms
+
+GatedResidualNormGrads = collections.namedtuple(
+    "GatedResidualNormGrads", "dx dbranch dpost_weight dpost_bias dgate dweight dbias")
+
+
+def _dtype_code(dtype):
+    import torch
+    code = {torch.float32: TR_F32, torch.bfloat16: TR_BF16, torch.float16: TR_F16}.get(dtype)
+    if code is None:
+        raise TypeError(f"float32, bfloat16 or float16 expected, got {dtype}")
+    return code
+
+
+class _On:
+    """Makes a device, or the stream asked for, current for a call (what the call allocates
+    then belongs to the stream it runs on); gives the stream's handle."""
+
+    def __init__(self, device, stream):
+        import torch
+        self._device, self._guard = device, None
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+            self._guard = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != device.index:
+            self._guard = torch.cuda.device(device)
+        self._current = torch.cuda.current_stream
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return self._current(self._device).cuda_stream
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _rows_like(t, name, like):
+    """Pointer of a matrix that must match `like` (None: null)."""
+    if t is None:
+        return None
+    if t.dtype != like.dtype or t.device != like.device:
+        raise TypeError(f"{name} must be a {like.dtype} tensor on {like.device}")
+    if t.shape != like.shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(like.shape)} tensor")
+    return t.data_ptr()
+
+
+def _floats(t, name, shape, device):
+    """Pointer of a float32 vector or matrix of `shape` (None: null)."""
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.device != device:
+        raise TypeError(f"{name} must be a float32 tensor on {device}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor")
+    return t.data_ptr()
+
+
+def _block(first, name, gate, kind, post, pre):
+    """What both directions check and derive: (kind, dtype, norms, rows, cols, gate pointer, gate rows)."""
+    import torch
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    dtype = _dtype_code(first.dtype)
+    if first.dim() != 2 or not first.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 2-D (rows x cols) tensor")
+    rows, cols = first.shape
+    gp, groups = None, 0
+    if gate is not None:
+        if gate.dim() == 1:
+            gate = gate.unsqueeze(0)
+        groups = gate.shape[0]
+        gp = _floats(gate, "gate", (groups, cols), first.device)
+    code = NORM_KINDS[kind] if isinstance(kind, str) else int(kind)
+    return code, dtype, (TR_BLOCK_POST if post else 0) | (TR_BLOCK_PRE if pre else 0), rows, cols, gp, groups
+
+
+def gated_residual_norm(x, branch, post_weight=None, post_bias=None, gate=None, weight=None, bias=None, eps=1e-5,
+                        kind="rmsnorm", post=True, pre=True, residual_scale=1.0, branch_scale=1.0, out=None, h_out=None,
+                        want_h=True, order="unordered", stream=None):
+    """The end of one block and the start of the next:
+    ``h = residual_scale * x + branch_scale * gate * post(branch)`` and ``y = pre(h)``; returns (y, h).
+
+    x, branch: (rows, cols) of float32, bfloat16 or float16. `kind` ("rmsnorm" or
+    "layernorm") names both norms; post=False or pre=False leaves one out (without pre, y is
+    None). Weights, biases: float32 vectors. gate: None, a float32 vector, or
+    (groups, cols), each row for rows // groups consecutive rows of x. want_h=False
+    does not write h (None is returned)."""
+    import torch
+    code, dtype, norms, r, c, gp, groups = _block(x, "x", gate, kind, post, pre)
+    dev = x.device
+    bp = _rows_like(branch, "branch", x)
+    pwp, pbp = _floats(post_weight, "post_weight", (c,), dev), _floats(post_bias, "post_bias", (c,), dev)
+    wp, wbp = _floats(weight, "weight", (c,), dev), _floats(bias, "bias", (c,), dev)
+    with _On(dev, stream) as handle:
+        y = (torch.empty_like(x) if out is None else out) if pre or out is not None else None
+        h = (torch.empty_like(x) if h_out is None else h_out) if want_h or h_out is not None else None
+        _check(load().tr_gated_residual_norm(code, dtype, norms, x.data_ptr(), bp, pwp, pbp, gp, groups, wp, wbp,
+                                             _rows_like(h, "h_out", x), _rows_like(y, "out", x), r, c, residual_scale,
+                                             branch_scale, eps, _order(order), handle), "gated_residual_norm")
+    return y, h
+
+
+def gated_residual_norm_backward_workspace_bytes(rows, cols, kind="rmsnorm"):
+    n = ctypes.c_size_t(0)
+    code = NORM_KINDS[kind] if isinstance(kind, str) else int(kind)
+    _check(load().tr_gated_residual_norm_backward_workspace_bytes(code, rows, cols, ctypes.byref(n)),
+           "gated_residual_norm_backward_workspace_bytes")
+    return n.value
+
+
+def gated_residual_norm_backward(h, branch, dy=None, dh=None, post_weight=None, post_bias=None, gate=None, weight=None,
+                                 eps=1e-5, kind="rmsnorm", post=True, pre=True, residual_scale=1.0, branch_scale=1.0,
+                                 want_params=True, dx=None, dbranch=None, workspace=None, order="unordered", stream=None):
+    """The gradients of ``gated_residual_norm`` from its h and branch, the gradient dy of
+    y (with pre) and dh of h (None: zero). Returns GatedResidualNormGrads: dx, dbranch (the inputs' type),
+    dpost_weight, dpost_bias, dgate (the gate's shape), dweight, dbias (float32; None where
+    there is no such norm, bias or gate, or with want_params=False)."""
+    import torch
+    code, dtype, norms, r, c, gp, groups = _block(branch, "branch", gate, kind, post, pre)
+    dev = branch.device
+    f32 = dict(device=dev, dtype=torch.float32)
+    hp = _rows_like(h, "h", branch)
+    dyp, dhp = _rows_like(dy, "dy", branch), _rows_like(dh, "dh", branch)
+    pwp, pbp = _floats(post_weight, "post_weight", (c,), dev), _floats(post_bias, "post_bias", (c,), dev)
+    wp = _floats(weight, "weight", (c,), dev)
+    layer = code == TR_NORM_LAYER
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    wsp, n = None, 0
+    with _On(dev, stream) as handle:
+        dx = torch.empty_like(branch) if dx is None else dx
+        dbranch = torch.empty_like(branch) if dbranch is None else dbranch
+        vector = lambda want: torch.empty(c, **f32) if want_params and want else None  # noqa: E731
+        dpw, dpb, dw, db = vector(post), vector(post and layer), vector(pre), vector(pre and layer)
+        dg = torch.empty_like(gate) if want_params and gate is not None else None
+        if want_params:
+            if workspace is None:
+                workspace = torch.empty(max(16, gated_residual_norm_backward_workspace_bytes(r, c, code)),
+                                        dtype=torch.uint8, device=dev)
+            elif not workspace.is_contiguous() or workspace.device != dev:
+                raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+            wsp, n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        _check(load().tr_gated_residual_norm_backward(
+            code, dtype, norms, hp, branch.data_ptr(), dyp, dhp, pwp, pbp, gp, groups, wp, _rows_like(dx, "dx", branch),
+            _rows_like(dbranch, "dbranch", branch), ptr(dpw), ptr(dpb), ptr(dg), ptr(dw), ptr(db), r, c, residual_scale,
+            branch_scale, eps, _order(order), wsp, n, handle), "gated_residual_norm_backward")
+    return GatedResidualNormGrads(dx, dbranch, dpw, dpb, dg, dw, db)
+
+
+# ------------------------------------------------------------ lists of tensors
+
+def _dense(t):
+    """Whether t's elements fill one range of memory (in any order of its dimensions)."""
+    if t.is_contiguous():
+        return True
+    step = 1
+    for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != step:
+            return False
+        step *= size
+    return True
+
+
+def _tensor_list(tensors, name, device=None):
+    """(pointers, element counts, dtype codes) of a list of dense CUDA tensors on one device, and the device."""
+    codes = []
+    for t in tensors:
+        if not t.is_cuda:
+            raise TypeError(f"{name} must hold CUDA tensors")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"{name} must be on one device")
+        codes.append(_dtype_code(t.dtype))
+        if not _dense(t):
+            raise ValueError(f"{name} must hold dense tensors (no gaps and no repeated elements)")
+    return (array.array("Q", [t.data_ptr() for t in tensors]), array.array("q", [t.numel() for t in tensors]),
+            array.array("i", codes), device)
+
+
+def _out_pointers(tensors, outs, device):
+    if outs is None:
+        return None
+    outs = list(outs)
+    if len(outs) != len(tensors):
+        raise ValueError("out must hold one tensor for each tensor")
+    for t, o in zip(tensors, outs):
+        if o.dtype != t.dtype or o.device != device:
+            raise TypeError("out must hold tensors of the tensors' types, on their device")
+        # elements are matched by their place in memory
+        if o.shape != t.shape or not ((t.is_contiguous() and o.is_contiguous()) or (o.stride() == t.stride() and _dense(o))):
+            raise ValueError("out must hold tensors of the tensors' shapes and order of elements")
+    return array.array("Q", [o.data_ptr() for o in outs])
+
+
+def _address(a):
+    return None if a is None else a.buffer_info()[0]
+
+
+def _norm_result(out, device, name):
+    import torch
+    if out is None:
+        return torch.empty((), device=device, dtype=torch.float32)
+    if out.dtype != torch.float32 or out.numel() != 1 or out.device != device:
+        raise TypeError(f"{name} must be one float32 on {device}")
+    return out
+
+
+def _norm_workspace(count, device):
+    import torch
+    n = ctypes.c_size_t(0)
+    _check(load().tr_global_norm_workspace_bytes(count, ctypes.byref(n)), "global_norm_workspace_bytes")
+    return torch.empty(n.value, dtype=torch.uint8, device=device)
+
+
+def _list_device(tensors, device):
+    import torch
+    if not tensors and device is None:
+        return torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
+def global_norm(tensors, kind="l2", out=None, stream=None):
+    """The norm over all elements of a list of dense CUDA tensors (float32, bfloat16 or
+    float16, mixed as they come): "l2", the square root of the sum of squares, or "max", the
+    largest magnitude. Returns one float32 on the device (nothing waits)."""
+    tensors = list(tensors)
+    ptrs, numels, codes, device = _tensor_list(tensors, "tensors", None if out is None else out.device)
+    device = _list_device(tensors, device)
+    code = TOTAL_KINDS[kind] if isinstance(kind, str) else int(kind)
+    with _On(device, stream) as handle:
+        norm = _norm_result(out, device, "out")
+        ws = _norm_workspace(len(tensors), device)
+        _check(load().tr_global_norm(code, _address(ptrs), _address(numels), _address(codes), len(tensors),
+                                     norm.data_ptr(), ws.data_ptr(), ws.numel(), handle), "global_norm")
+    return norm
+
+
+def clip_by_norm(tensors, norm, max_norm, eps=1e-6, out=None, stream=None):
+    """Scale every tensor of a list by min(1, max_norm / (norm + eps)), where norm is
+    one float32 on the device, in place or into the tensors of `out`."""
+    tensors = list(tensors)
+    ptrs, numels, codes, device = _tensor_list(tensors, "tensors", norm.device)
+    norm = _norm_result(norm, device, "norm")
+    outs = _out_pointers(tensors, out, device)
+    with _On(device, stream) as handle:
+        _check(load().tr_clip_by_norm(_address(ptrs), _address(outs), _address(numels), _address(codes), len(tensors),
+                                      norm.data_ptr(), max_norm, eps, handle), "clip_by_norm")
+
+
+def clip_global_norm(tensors, max_norm, kind="l2", eps=1e-6, out=None, norm_out=None, stream=None):
+    """``global_norm`` of a list, then ``clip_by_norm`` with it. Returns the norm before
+    clipping (one float32 on the device)."""
+    tensors = list(tensors)
+    ptrs, numels, codes, device = _tensor_list(tensors, "tensors", None if norm_out is None else norm_out.device)
+    device = _list_device(tensors, device)
+    outs = _out_pointers(tensors, out, device)
+    code = TOTAL_KINDS[kind] if isinstance(kind, str) else int(kind)
+    with _On(device, stream) as handle:
+        norm = _norm_result(norm_out, device, "norm_out")
+        ws = _norm_workspace(len(tensors), device)
+        _check(load().tr_clip_global_norm(code, _address(ptrs), _address(outs), _address(numels), _address(codes),
+                                          len(tensors), max_norm, eps, norm.data_ptr(), ws.data_ptr(), ws.numel(),
+                                          handle), "clip_global_norm")
+    return norm
 
 
 def cross_entropy(logits, labels, out=None, order="unordered", stream=None):

@@ -1,0 +1,107 @@
+// Block norms: host/device interface of the gated residual norm and its backward.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include <cuda_runtime.h>
+
+#include "tr.h"
+
+namespace tr {
+
+// h = rs x + bs gate post(a), y = pre(h); see tr.h. Absent vectors are null.
+struct BlockArgs {
+    const void* x;
+    const void* a;  // the branch
+    void* h;
+    void* y;
+    const float* post_w;
+    const float* post_b;
+    const float* gate;
+    const float* pre_w;
+    const float* pre_b;
+    int64_t rows;
+    int64_t group_rows;  // rows that share a gate row (rows when there is no gate)
+    int cols;
+    int post, pre;  // which norms there are
+    float rs, bs, eps;
+};
+
+struct BlockBwArgs {
+    const void* h;
+    const void* a;
+    const void* dy;
+    const void* dh;
+    void* dx;
+    void* da;
+    const float* post_w;
+    const float* post_b;
+    const float* gate;
+    const float* pre_w;
+    float* dgate;
+    float* dpost_w;
+    float* dpost_b;
+    float* dpre_w;
+    float* dpre_b;
+    int64_t rows;
+    int64_t group_rows;
+    int64_t groups;   // gate rows (1 when there is no gate)
+    int64_t slices;   // slabs per group (0: each slab takes whole groups)
+    int64_t slabs;    // row slabs, each with its own column partials
+    int cols;
+    int post, pre;
+    int sums;         // column gradients are wanted
+    float rs, bs, eps;
+    float* stats;     // re-read path: kBlockStats floats a row
+    float* part;      // slabs x vectors x cols partial column sums
+};
+
+// The rows of a slab. With slices > 0 a slab is one of the `slices` equal parts
+// of a group's rows, so its sums belong to one gate row; otherwise it is a run of
+// whole groups, and the kernel finishes each group's gate gradient by itself.
+struct SlabRows {
+    int64_t begin, end;
+};
+__host__ __device__ inline SlabRows slab_rows(const BlockBwArgs& a, int64_t s) {
+    if (a.slices > 0) {
+        const int64_t g = s / a.slices, i = s % a.slices;
+        return SlabRows{g * a.group_rows + a.group_rows * i / a.slices, g * a.group_rows + a.group_rows * (i + 1) / a.slices};
+    }
+    return SlabRows{a.groups * s / a.slabs * a.group_rows, a.groups * (s + 1) / a.slabs * a.group_rows};
+}
+
+constexpr int kBlockStats = 8;      // mean h, 1/sigma h, mean u, mean u hh, mean a, 1/sigma a (padded)
+constexpr int kBlockMaxSlabs = 320;  // two CTAs on each of 152 SMs, and some
+
+// Column-partial vectors of a slab: sum dy hh, sum D ah (or gate D ah), and for
+// LayerNorm sum dy and sum D (or gate D) too.
+inline int block_vectors(int kind) { return kind == TR_NORM_LAYER ? 4 : 2; }
+
+// The most slabs a backward pass uses: every slab costs block_vectors() x cols
+// floats, so rows too long for the cached kernels take fewer (at 2^22 floats a vector in all).
+inline int64_t block_slab_limit(int64_t rows, int64_t cols) {
+    int64_t n = kBlockMaxSlabs;
+    if (cols > 16384) n = (1LL << 22) / cols;
+    if (n < 1) n = 1;
+    return n < rows ? n : (rows < 1 ? 1 : rows);
+}
+
+// Choose the slabs for at most `target` of them.
+inline void block_slabs(BlockBwArgs* a, int64_t target) {
+    if (target < 1) target = 1;
+    int64_t s = target / a->groups;
+    if (s > a->group_rows) s = a->group_rows;
+    if (s < 2 && a->groups > 1) {  // whole groups
+        a->slices = 0;
+        a->slabs = target < a->groups ? target : a->groups;
+    } else {
+        a->slices = s < 1 ? 1 : s;
+        a->slabs = a->groups * a->slices;
+    }
+}
+
+cudaError_t launch_block_forward(int kind, int dtype, const BlockArgs& a, cudaStream_t stream);
+cudaError_t launch_block_backward(int kind, int dtype, const BlockBwArgs& a, cudaStream_t stream);
+
+}  // namespace tr

@@ -299,6 +299,104 @@ tr_status tr_axis_minmax_f32(const float* x, float* out_min, float* out_max, int
 tr_status tr_axis_launch_shape(int32_t sm_count, int32_t op, tr_order order, int64_t outer, int64_t extent,
                                int64_t inner, int32_t* splits, int64_t* tiles);
 
+/* ---- block norms ---------------------------------------------------------
+ * The end of one network block and the start of the next in one pass over the
+ * rows: the block's output ("branch") is normalised, gated, scaled and added to
+ * the residual stream, and the sum is normalised again for the next block:
+ *
+ *   n = post(branch)                       (TR_BLOCK_POST; else n = branch)
+ *   h = residual_scale x + branch_scale gate n
+ *   y = pre(h)                             (TR_BLOCK_PRE; else y is not written)
+ *
+ * Both norms are RMSNorm (v / sqrt(mean(v^2) + eps) * w) or both LayerNorm
+ * ((v - mean) / sqrt(var + eps) * w + b), as tr_norm_kind says; a weight may be
+ * NULL (1), a bias NULL (0; RMSNorm takes none). `norms` is a mask of
+ * TR_BLOCK_POST and TR_BLOCK_PRE, at least one. gate is NULL (1) or gate_rows x
+ * cols floats, where gate_rows divides rows: rows r with the same
+ * r / (rows / gate_rows) share a gate row (1: a gate per channel; the batch: a
+ * gate per sequence; rows: a gate per token).
+ *
+ * x, branch, h and y (and the gradients dy, dh, dx and dbranch) are rows x cols
+ * of `dtype`; weights, biases, the gate and their gradients are floats. All
+ * arithmetic is binary32: y is the norm of the unrounded h, and each output is
+ * rounded once. h may be NULL when y is written. No output may overlap an
+ * input or another output. Pointers to 16-bit types must be 2-byte aligned.
+ *
+ * Backward: from the saved h and branch, with dy the gradient of y (required
+ * with TR_BLOCK_PRE, NULL without) and dh that of h (NULL: 0; required
+ * without TR_BLOCK_PRE),
+ *   D   = dh + the gradient of pre at h against dy
+ *   dx  = residual_scale D,  dbranch = the gradient of branch_scale gate post(branch) against D
+ *   dpre_w, dpre_b, dpost_w, dpost_b: cols floats, dgate: gate_rows x cols
+ *   floats, each NULL when not wanted (a gradient of a norm that is off, of a
+ *   RMSNorm's bias or of no gate must be NULL).
+ * h is not read without TR_BLOCK_PRE, nor branch when there is neither
+ * TR_BLOCK_POST nor dgate: they may then be NULL.
+ * The column gradients need a caller-owned, 16-byte-aligned workspace of
+ * tr_gated_residual_norm_backward_workspace_bytes (none when all are NULL). All sums
+ * have a fixed order: results repeat bit for bit on one device.
+ *
+ * rows = 0 writes zeros to the column gradients and nothing else. order must be
+ * TR_ORDER_UNORDERED_TREE: the others return TR_ERR_UNSUPPORTED. No call
+ * allocates or waits, and all may be captured into a graph. */
+typedef enum tr_dtype { TR_F32 = 0, TR_BF16 = 1, TR_F16 = 2 } tr_dtype;
+typedef enum tr_norm_kind { TR_NORM_RMS = 0, TR_NORM_LAYER = 1 } tr_norm_kind;
+#define TR_BLOCK_POST 1
+#define TR_BLOCK_PRE 2
+
+tr_status tr_gated_residual_norm(tr_norm_kind kind, tr_dtype dtype, int32_t norms, const void* x, const void* branch,
+                                 const float* post_w, const float* post_b, const float* gate, int64_t gate_rows,
+                                 const float* pre_w, const float* pre_b, void* h, void* y, int64_t rows, int64_t cols,
+                                 float residual_scale, float branch_scale, float eps, tr_order order,
+                                 cudaStream_t stream);
+tr_status tr_gated_residual_norm_backward(tr_norm_kind kind, tr_dtype dtype, int32_t norms, const void* h,
+                                          const void* branch, const void* dy, const void* dh, const float* post_w,
+                                          const float* post_b, const float* gate, int64_t gate_rows,
+                                          const float* pre_w, void* dx, void* dbranch, float* dpost_w, float* dpost_b,
+                                          float* dgate, float* dpre_w, float* dpre_b, int64_t rows, int64_t cols,
+                                          float residual_scale, float branch_scale, float eps, tr_order order,
+                                          void* workspace, size_t workspace_bytes, cudaStream_t stream);
+/* Host only: workspace bytes of a backward pass of rows x cols. */
+tr_status tr_gated_residual_norm_backward_workspace_bytes(tr_norm_kind kind, int64_t rows, int64_t cols, size_t* bytes);
+
+/* ---- norms over a list of tensors -----------------------------------------
+ * The global norm of a list of gradients, and clipping by it. A list is `count`
+ * tensors: device pointers `tensors`, element counts `numels` (>= 0; a
+ * tensor of 0 elements may be NULL) and types `dtypes` (tr_dtype), three host
+ * arrays that are read before the call returns. A tensor is any dense range of
+ * memory aligned to its element; a list may mix types.
+ *
+ * tr_global_norm: *norm (one device float) = the square root of the sum of
+ * all elements' squares (TR_TOTAL_L2), or the largest absolute value
+ * (TR_TOTAL_MAX); 0 for an empty list. An element that is NaN makes the norm
+ * NaN. Squares that leave binary32's range are summed in binary64, so the norm is finite
+ * whenever it can be represented. Sums have a fixed order: results repeat bit for bit on
+ * one device. Tensors may overlap one another: they are only read.
+ *
+ * tr_clip_by_norm: outs[i] = tensors[i] * min(1, max_norm / (*norm + eps)),
+ * rounded to the tensor's type, with *norm read on the device (a norm computed
+ * earlier, or combined over several processes). A NaN norm gives NaN. outs NULL: in place; else outs[i] has
+ * tensors[i]'s count and type and is tensors[i] itself or overlaps no tensor of the list.
+ * Tensors that are written may not overlap one another.
+ *
+ * tr_clip_global_norm: both: the norm is written to *norm, and the tensors are
+ * scaled by it. max_norm and eps must be >= 0 and not NaN (max_norm may be infinite).
+ *
+ * *norm may not overlap a tensor. The norm needs a caller-owned, 16-byte-aligned
+ * workspace of tr_global_norm_workspace_bytes(count). No call allocates or waits, and all may be
+ * captured into a graph (which keeps the pointers). */
+typedef enum tr_total_kind { TR_TOTAL_L2 = 0, TR_TOTAL_MAX = 1 } tr_total_kind;
+
+tr_status tr_global_norm(tr_total_kind kind, const void* const* tensors, const int64_t* numels, const int32_t* dtypes,
+                         int64_t count, float* norm, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+tr_status tr_clip_by_norm(const void* const* tensors, void* const* outs, const int64_t* numels, const int32_t* dtypes,
+                          int64_t count, const float* norm, float max_norm, float eps, cudaStream_t stream);
+tr_status tr_clip_global_norm(tr_total_kind kind, const void* const* tensors, void* const* outs,
+                              const int64_t* numels, const int32_t* dtypes, int64_t count, float max_norm, float eps,
+                              float* norm, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+/* Host only: workspace bytes of the norm of `count` tensors. */
+tr_status tr_global_norm_workspace_bytes(int64_t count, size_t* bytes);
+
 /* ---- no-allocation entry point ----------------------------------------- */
 
 /* Softmax, RMSNorm or LayerNorm of few long rows with no device allocation on
