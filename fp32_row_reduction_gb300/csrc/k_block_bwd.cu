@@ -14,6 +14,7 @@
 
 #include "tr_block.cuh"
 #include "tr_block.h"
+#include "tr_launch.h"
 
 namespace tr {
 namespace block {
@@ -276,24 +277,37 @@ cudaError_t bwd_launch(const BlockBwArgs& in, cudaStream_t stream) {
     bwd_columns_kernel<T, LAYER><<<dim3(tiles, static_cast<unsigned>(a.slabs)), kTile * 8, 0, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    bwd_finish_kernel<LAYER><<<tiles, 1024, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_block_finish(LAYER ? TR_NORM_LAYER : TR_NORM_RMS, a, stream);
 }
 
 template <class T>
-cudaError_t bwd_kind(int kind, const BlockBwArgs& a, cudaStream_t stream) {
+cudaError_t bwd_read(int kind, const BlockBwArgs& a, cudaStream_t stream) {
     return kind == TR_NORM_LAYER ? bwd_launch<T, true>(a, stream) : bwd_launch<T, false>(a, stream);
 }
 
 }  // namespace block
 
+cudaError_t launch_block_finish(int kind, const BlockBwArgs& a, cudaStream_t stream) {
+    const dim3 tiles(static_cast<unsigned>((a.cols + block::kTile - 1) / block::kTile));
+    return kind == TR_NORM_LAYER ? launch_dependent(block::bwd_finish_kernel<true>, tiles, 1024, 0, stream, a)
+                                 : launch_dependent(block::bwd_finish_kernel<false>, tiles, 1024, 0, stream, a);
+}
+
 cudaError_t launch_block_backward(int kind, int dtype, const BlockBwArgs& a, cudaStream_t stream) {
+    bool done = false;
+    cudaError_t e = cudaErrorInvalidValue;
     switch (dtype) {
-        case TR_F32: return block::bwd_kind<float>(kind, a, stream);
-        case TR_BF16: return block::bwd_kind<__nv_bfloat16>(kind, a, stream);
-        case TR_F16: return block::bwd_kind<__half>(kind, a, stream);
+        case TR_F32:
+            e = launch_block_backward_f32(kind, a, &done, stream);
+            return done ? e : block::bwd_read<float>(kind, a, stream);
+        case TR_BF16:
+            e = launch_block_backward_bf16(kind, a, &done, stream);
+            return done ? e : block::bwd_read<__nv_bfloat16>(kind, a, stream);
+        case TR_F16:
+            e = launch_block_backward_f16(kind, a, &done, stream);
+            return done ? e : block::bwd_read<__half>(kind, a, stream);
     }
-    return cudaErrorInvalidValue;
+    return e;
 }
 
 }  // namespace tr

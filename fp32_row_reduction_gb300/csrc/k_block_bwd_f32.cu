@@ -1,0 +1,10 @@
+// The on-chip backward of the gated residual norm on float rows.
+#include "tr_block_bwd.cuh"
+
+namespace tr {
+
+cudaError_t launch_block_backward_f32(int kind, const BlockBwArgs& a, bool* done, cudaStream_t stream) {
+    return kind == TR_NORM_LAYER ? block::bwd_kind<float, true>(a, done, stream) : block::bwd_kind<float, false>(a, done, stream);
+}
+
+}  // namespace tr

@@ -72,17 +72,16 @@ __host__ __device__ inline SlabRows slab_rows(const BlockBwArgs& a, int64_t s) {
 }
 
 constexpr int kBlockStats = 8;      // mean h, 1/sigma h, mean u, mean u hh, mean a, 1/sigma a (padded)
-constexpr int kBlockMaxSlabs = 320;  // two CTAs on each of 152 SMs, and some
-
 // Column-partial vectors of a slab: sum dy hh, sum D ah (or gate D ah), and for
 // LayerNorm sum dy and sum D (or gate D) too.
 inline int block_vectors(int kind) { return kind == TR_NORM_LAYER ? 4 : 2; }
 
-// The most slabs a backward pass uses: every slab costs block_vectors() x cols
-// floats, so rows too long for the cached kernels take fewer (at 2^22 floats a vector in all).
+// The most slabs a backward pass uses. A slab costs block_vectors() x cols floats: short
+// rows may have many (teams of one warp, several a CTA), rows of up to 16384 columns two for each of
+// 160 SMs, longer ones 2^22 floats a vector in all.
 inline int64_t block_slab_limit(int64_t rows, int64_t cols) {
-    int64_t n = kBlockMaxSlabs;
-    if (cols > 16384) n = (1LL << 22) / cols;
+    int64_t n = cols > 16384 ? (1LL << 22) / cols : (1LL << 20) / cols;
+    if (cols <= 16384) n = n < 320 ? 320 : (n > 4096 ? 4096 : n);
     if (n < 1) n = 1;
     return n < rows ? n : (rows < 1 ? 1 : rows);
 }
@@ -103,5 +102,11 @@ inline void block_slabs(BlockBwArgs* a, int64_t target) {
 
 cudaError_t launch_block_forward(int kind, int dtype, const BlockArgs& a, cudaStream_t stream);
 cudaError_t launch_block_backward(int kind, int dtype, const BlockBwArgs& a, cudaStream_t stream);
+// The backward of rows that fit on the chip; *done is false (and nothing launched) for others.
+cudaError_t launch_block_backward_f32(int kind, const BlockBwArgs& a, bool* done, cudaStream_t stream);
+cudaError_t launch_block_backward_bf16(int kind, const BlockBwArgs& a, bool* done, cudaStream_t stream);
+cudaError_t launch_block_backward_f16(int kind, const BlockBwArgs& a, bool* done, cudaStream_t stream);
+// The column gradients from the slabs' partials.
+cudaError_t launch_block_finish(int kind, const BlockBwArgs& a, cudaStream_t stream);
 
 }  // namespace tr

@@ -5,13 +5,16 @@
 
 #include <algorithm>
 #include <cmath>
+#include <map>
+#include <mutex>
 #include <new>
-#include <utility>
+#include <tuple>
 #include <vector>
 
 #include "tr.h"
 #include "tr_block.h"
 #include "tr_internal.h"
+#include "tr_launch.h"
 #include "tr_list.h"
 
 namespace tr {
@@ -242,7 +245,31 @@ tr_status guarded(const char* w, F&& f) {
     }
 }
 
+std::mutex g_launch_mu;
+std::map<std::tuple<int, const void*, int, size_t>, int> g_resident;
+
 }  // namespace
+
+int resident_ctas(const void* kernel, int threads, size_t smem) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lock(g_launch_mu);
+    const auto key = std::make_tuple(dev, kernel, threads, smem);
+    const auto it = g_resident.find(key);
+    if (it != g_resident.end()) return it->second;
+    int per = 0, sms = 0, optin = 0;
+    cudaFuncAttributes fa;
+    // the kernel's limit is raised once, as far as the device lets it
+    cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
+    if (e == cudaSuccess && smem > 0)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - static_cast<int>(fa.sharedSizeBytes));
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
+    if (e != cudaSuccess) return 0;  // not kept: the launch reports the error
+    return g_resident[key] = per * sms;
+}
+
 }  // namespace tr
 
 using namespace tr;
