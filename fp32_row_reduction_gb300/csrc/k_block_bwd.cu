@@ -289,8 +289,8 @@ cudaError_t bwd_read(int kind, const BlockBwArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_block_finish(int kind, const BlockBwArgs& a, cudaStream_t stream) {
     const dim3 tiles(static_cast<unsigned>((a.cols + block::kTile - 1) / block::kTile));
-    return kind == TR_NORM_LAYER ? launch_dependent(block::bwd_finish_kernel<true>, tiles, 1024, 0, stream, a)
-                                 : launch_dependent(block::bwd_finish_kernel<false>, tiles, 1024, 0, stream, a);
+    return kind == TR_NORM_LAYER ? launch_dependent(block::bwd_finish_kernel<true>, tiles, 1024, 0, 1, stream, a)
+                                 : launch_dependent(block::bwd_finish_kernel<false>, tiles, 1024, 0, 1, stream, a);
 }
 
 cudaError_t launch_block_backward(int kind, int dtype, const BlockBwArgs& a, cudaStream_t stream) {

@@ -246,15 +246,15 @@ tr_status guarded(const char* w, F&& f) {
 }
 
 std::mutex g_launch_mu;
-std::map<std::tuple<int, const void*, int, size_t>, int> g_resident;
+std::map<std::tuple<int, const void*, int, size_t, int>, int> g_resident;
 
 }  // namespace
 
-int resident_ctas(const void* kernel, int threads, size_t smem) {
+int resident_ctas(const void* kernel, int threads, size_t smem, int cluster) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     std::lock_guard<std::mutex> lock(g_launch_mu);
-    const auto key = std::make_tuple(dev, kernel, threads, smem);
+    const auto key = std::make_tuple(dev, kernel, threads, smem, cluster);
     const auto it = g_resident.find(key);
     if (it != g_resident.end()) return it->second;
     int per = 0, sms = 0, optin = 0;
@@ -266,8 +266,25 @@ int resident_ctas(const void* kernel, int threads, size_t smem) {
     if (e == cudaSuccess && smem > 0)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - static_cast<int>(fa.sharedSizeBytes));
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
+    int ctas = per * sms;
+    if (e == cudaSuccess && cluster > 1) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = cluster;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+        ctas = clusters * cluster;
+    }
     if (e != cudaSuccess) return 0;  // not kept: the launch reports the error
-    return g_resident[key] = per * sms;
+    return g_resident[key] = ctas;
 }
 
 }  // namespace tr

@@ -1,19 +1,23 @@
 // The gated residual norm's backward with the rows on chip (see k_block_bwd.cu for
 // the formulas).
 //
-// HBM-bound: h, a, dy and dh are read and dx and da written once. A team of W warps
-// takes a row at a time, thread t owning the same S x E columns (E elements are 16 bytes) of
-// every row of its slab, so the column sums stay in its registers until the slab
-// ends. Rows come through a ring of shared-memory stages filled by cp.async while the row
-// before is worked on. The row sums need two exchanges between the team's warps
-// (LayerNorm three: means first, then everything about them).
+// HBM-bound: h, a, dy and dh are read and dx and da written once. A team of warps
+// takes a row at a time; a thread owns the same C = 4 or 8 columns of every row of its
+// slab, so the column sums stay in its registers (32-bit) until the slab ends. Rows come through a
+// ring of shared-memory stages filled by cp.async. Rows too long for 16 warps are split
+// over a cluster of 2, 4 or 8 CTAs.
+//
+// With 16-bit types the work per byte is what limits: at 4096 columns a SM has 2090 cycles to
+// the row. So the arithmetic is on pairs (f32x2), and the exchanges between warps are as few
+// as the dependences allow: the next row's statistics travel with this row's sum of
+// q ah, one exchange a row (LayerNorm two: means, then what is taken about them).
 //
 // Two layouts of a row over the threads:
 // * aligned rows (every row of every matrix starts on 16 bytes): slot s of thread t is the
 //   16 bytes s x team + t; a thread reads back what it copied itself, so no barrier;
 // * other rows: the 16-byte granules that cover the row are copied as they lie, the
 //   team meets at a barrier, and element k of thread t is column k x team + t, which any phase
-//   reads without bank conflicts.
+//   reads and writes without bank conflicts or partial sectors.
 #pragma once
 
 #include <algorithm>
@@ -26,125 +30,172 @@ namespace tr {
 namespace block {
 
 constexpr int kBwMaxWarps = 16;
-constexpr int kBwMaxStages = 4;
-constexpr int kBwMaxSums = 3;  // row sums of one exchange
+constexpr int kBwMaxStages = 8;
+constexpr int kBwMaxCluster = 8;
 
 // How a launch maps rows onto threads and shared memory.
 struct BwShape {
-    int warps;         // a team's
+    int warps;         // a team's in one CTA
     int teams;         // of a CTA
-    int stages;        // of a team's ring
-    int tensors;       // matrices read: h and dy (pre), a, dh, in this order
+    int cluster;       // CTAs of a row
+    int cta_vecs;      // 16-byte slots of a row in one CTA
+    int stages;        // of a team's ring (3 or more: two rows are at work, the others on their way)
+    int tensors;       // matrices read
     int tensor_bytes;  // shared memory of one matrix's row
 };
 
-// Shared memory of the teams' exchanges.
-__host__ __device__ inline int bwd_fixed_bytes(const BwShape& g) { return g.teams * 2 * kBwMaxSums * kBwMaxWarps * 4; }
+// Shared memory of the teams' exchanges: two halves of 8 floats for each warp of a row.
+__host__ __device__ inline int bwd_team_bytes(const BwShape& g) { return 2 * 8 * 4 * g.warps * g.cluster; }
+__host__ __device__ inline int bwd_fixed_bytes(const BwShape& g) { return (g.teams * bwd_team_bytes(g) + 127) / 128 * 128; }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-// At most `n` groups of this thread still in flight.
-__device__ __forceinline__ void cp_async_wait_n(int n) {
-    switch (n) {
-        case 0: cp_async_wait<0>(); break;
-        case 1: cp_async_wait<1>(); break;
-        case 2: cp_async_wait<2>(); break;
-        default: cp_async_wait<3>(); break;
-    }
-}
-
-// A barrier of one team's threads (a team of one warp needs no more than the warp's own).
-__device__ __forceinline__ void team_barrier(int team, int warps) {
-    if (warps == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(warps * 32) : "memory");
-}
-
-// N sums over a team's threads. `slot` holds 2 x kBwMaxSums x kBwMaxWarps floats of the team; the
-// halves alternate, so consecutive sums need one barrier each.
-template <int N>
-__device__ __forceinline__ void team_sums(float (&v)[N], float* slot, int& buf, int team, int warps) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kFull, v[i], o);
-    if (warps == 1) return;
-    float* s = slot + buf * kBwMaxSums * kBwMaxWarps;
-    buf ^= 1;
-    const int lane = threadIdx.x & 31;
-    const int w = static_cast<int>(threadIdx.x >> 5) - team * warps;
-    if (lane < N) {  // lane i stores sum i
-        float mine = v[0];
-#pragma unroll
-        for (int i = 1; i < N; ++i) mine = lane == i ? v[i] : mine;
-        s[lane * kBwMaxWarps + w] = mine;
-    }
-    team_barrier(team, warps);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        float t = 0.0f;
-        for (int j = 0; j < warps; j += 4) {  // slots past the team's warps hold zero
-            const float4 q = *reinterpret_cast<const float4*>(s + i * kBwMaxWarps + j);
-            t += (q.x + q.y) + (q.z + q.w);
-        }
-        v[i] = t;
-    }
-}
-
-template <class T, bool LAYER, int S, bool ODD>
-__global__ void __launch_bounds__(32 * kBwMaxWarps)
-    bwd_kernel(const BlockBwArgs p, const BwShape g) {
-    constexpr int E = 16 / static_cast<int>(sizeof(T));
-    constexpr int C = S * E;       // columns of a thread
-    constexpr int V = LAYER ? 4 : 2;
-    constexpr int N1 = kBwMaxSums, N3 = LAYER ? 2 : 1;
-    // the parameters of a thread's columns stay in registers where the column sums leave room
-    constexpr bool PREG = LAYER ? C <= 8 : C <= 16;
-    extern __shared__ uint4 smem[];
-    const int team_threads = g.warps * 32;
-    const int team = static_cast<int>(threadIdx.x) / team_threads;
-    const int t = static_cast<int>(threadIdx.x) - team * team_threads;
-    const int cols = p.cols;
-    const float inv_n = 1.0f / static_cast<float>(cols);
-    float* slot = reinterpret_cast<float*>(smem) + team * (2 * N1 * kBwMaxWarps);
-    for (int i = t; i < 2 * N1 * kBwMaxWarps; i += team_threads) slot[i] = 0.0f;
+// The on-chip kernel of one team's view: sums over the row's warps.
+template <bool CLUSTER>
+struct Exchange {
+    float* slot;   // this CTA's, 2 x 8 x entries floats
+    int entries;   // warps of the row
+    int entry;     // this warp's place among them
+    int team, warps;
     int buf = 0;
+
+    // v[0 .. N-1] (N = 4 or 8) summed over the row. One halving step per bit of the value's index
+    // (N/2 + N/4 + ... shuffles instead of 5 N): lane 8 i (4 i) ends with value i.
+    template <int N>
+    __device__ __forceinline__ void sums(float (&v)[N]) {
+        static_assert(N == 4 || N == 8, "");
+        const int lane = threadIdx.x & 31;
+        float r = warp_halves<N>(v, lane);
+        constexpr int kLanes = 32 / N;  // lanes that hold the same value
+        if (!CLUSTER && entries == 1) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = __shfl_sync(kFull, r, i * kLanes);
+            return;
+        }
+        float* s = slot + buf * 8 * entries;
+        buf ^= 1;
+        if constexpr (CLUSTER) {
+            cg::cluster_group cl = cg::this_cluster();
+            const int ctas = static_cast<int>(cl.num_blocks());
+            // the lanes of a value store it to one CTA each
+            for (int c = lane % kLanes; c < ctas; c += kLanes)
+                *cl.map_shared_rank(s + entry * N + lane / kLanes, c) = r;
+            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        } else {
+            if (lane % kLanes == 0) s[entry * N + lane / kLanes] = r;
+            asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(warps * 32) : "memory");
+        }
+        // 16 entries at a time, half of a value set a lane
+        float t[N / 2] = {};
+        for (int e = lane & 15; e < entries; e += 16) {
+            const float* q = s + e * N + (lane >> 4) * (N / 2);
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) t[i] += q[i];
+        }
+        r = half_warp_halves<N / 2>(t, lane);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(kFull, r, i * kLanes);
+    }
+
+private:
+    template <int N>
+    static __device__ __forceinline__ float halve(float (&v)[N], int lane, int bit, float (&o)[N / 2]) {
+        const bool up = lane & bit;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const float keep = up ? v[i + N / 2] : v[i], send = up ? v[i] : v[i + N / 2];
+            o[i] = keep + __shfl_xor_sync(kFull, send, bit);
+        }
+        return o[0];
+    }
+    // N values over the lanes below `bit` x 2
+    template <int N, int BIT>
+    static __device__ __forceinline__ float halves(float (&v)[N], int lane) {
+        if constexpr (N == 1) {
+            float r = v[0];
+#pragma unroll
+            for (int o = BIT; o >= 1; o >>= 1) r += __shfl_xor_sync(kFull, r, o);
+            return r;
+        } else {
+            float o[N / 2];
+            halve<N>(v, lane, BIT, o);
+            return halves<N / 2, BIT / 2>(o, lane);
+        }
+    }
+    template <int N>
+    static __device__ __forceinline__ float warp_halves(float (&v)[N], int lane) { return halves<N, 16>(v, lane); }
+    template <int N>
+    static __device__ __forceinline__ float half_warp_halves(float (&v)[N], int lane) { return halves<N, 8>(v, lane); }
+};
+
+// A pair of adjacent elements of a type.
+__device__ __forceinline__ float2 pair_of(uint32_t q, __nv_bfloat16) {
+    return make_float2(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
+}
+__device__ __forceinline__ float2 pair_of(uint32_t q, __half) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&q));
+}
+__device__ __forceinline__ uint32_t bits_of(float2 v, __nv_bfloat16) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ uint32_t bits_of(float2 v, __half) {
+    const __half2 b = __floats2half2_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+template <class T, bool LAYER, int S, bool ODD, bool CLUSTER>
+__global__ void __launch_bounds__(32 * kBwMaxWarps) bwd_kernel(const BlockBwArgs p, const BwShape g) {
+    constexpr int E = 16 / static_cast<int>(sizeof(T));
+    constexpr int P = E / 2;       // pairs of a slot
+    constexpr int K = S * P;       // pairs of a thread
+    constexpr int V = LAYER ? 4 : 2;
+    extern __shared__ uint4 smem[];
+    const int tt = g.warps * 32;  // a team's threads in this CTA
+    const int team = CLUSTER ? 0 : static_cast<int>(threadIdx.x) / tt;
+    const int t = static_cast<int>(threadIdx.x) - team * tt;
+    const int rank = CLUSTER ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
+    const int cols = p.cols;
+    const int col0 = rank * g.cta_vecs * E;                 // this CTA's first column
+    const int mine = min(cols - col0, g.cta_vecs * E);      // and how many it has
+    const int vecs = mine / E;                              // aligned rows: 16-byte slots
+    const float inv_n = 1.0f / static_cast<float>(cols);
+    Exchange<CLUSTER> ex{reinterpret_cast<float*>(smem) + team * (bwd_team_bytes(g) / 4), g.warps * g.cluster,
+                         rank * g.warps + (t >> 5), team, g.warps};
     const int stage_bytes = g.tensors * g.tensor_bytes;
     char* ring = reinterpret_cast<char*>(smem) + bwd_fixed_bytes(g) + team * g.stages * stage_bytes;
-    team_barrier(team, g.warps);
+    if constexpr (CLUSTER) cg::this_cluster().sync();  // every CTA of the cluster runs before it is written to
     pdl_enter();
 
-    auto column = [&](int s, int e) { return ODD ? t + team_threads * (s * E + e) : (t + team_threads * s) * E + e; };
-    const int vecs = cols / E;  // aligned rows: 16-byte slots of a row
+    // column (of this CTA) of element e of slot s
+    auto column = [&](int s, int e) { return ODD ? t + tt * (s * E + e) : (t + tt * s) * E + e; };
+    // whether slot s (pair j of it, in the odd layout element by element) is inside the row
+    auto in = [&](int s, int e) { return ODD ? column(s, e) < mine : t + tt * s < vecs; };
 
-    const int64_t index = static_cast<int64_t>(blockIdx.x) * g.teams + team;
-    if (index >= p.slabs) return;
+    const int64_t index = CLUSTER ? blockIdx.x / g.cluster : static_cast<int64_t>(blockIdx.x) * g.teams + team;
+    if (index >= p.slabs) return;  // (a whole cluster, or a whole team)
     const SlabRows slab = slab_rows(p, index);
+
     // ---- the ring: h and dy (pre), a, dh, each where there is one ----
     const bool need_a = p.post || p.dgate;
     const int at_dy = p.pre ? g.tensor_bytes : 0;
     const int at_a = p.pre ? 2 * g.tensor_bytes : 0;
     const int at_dh = at_a + (need_a ? g.tensor_bytes : 0);
     const int64_t row_bytes = static_cast<int64_t>(cols) * static_cast<int>(sizeof(T));
+    const int64_t base = static_cast<int64_t>(col0) * static_cast<int>(sizeof(T));
     auto fetch_one = [&](const void* matrix, int64_t row, char* to) {
-        const char* from = static_cast<const char*>(matrix) + row * row_bytes;
+        const char* from = static_cast<const char*>(matrix) + (row * row_bytes + base);
         if constexpr (!ODD) {
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                const int k = t + team_threads * s;
+                const int k = t + tt * s;
                 if (k < vecs) cp_async16(smem_addr(to) + k * 16, from + k * 16);
             }
         } else {
             const int phase = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15);
-            const int granules = (phase + static_cast<int>(row_bytes) + 15) >> 4;
+            const int granules = (phase + mine * static_cast<int>(sizeof(T)) + 15) >> 4;
             const char* lo = static_cast<const char*>(matrix);
             const char* hi = lo + p.rows * row_bytes;
-            for (int k = t; k < granules; k += team_threads) {
+            for (int k = t; k < granules; k += tt) {
                 const char* q = from - phase + k * 16;
                 if (q >= lo && q + 16 <= hi) {
                     cp_async16(smem_addr(to) + k * 16, q);
@@ -169,140 +220,231 @@ __global__ void __launch_bounds__(32 * kBwMaxWarps)
         }
         cp_async_commit();
     };
-    // E columns of slot s of the matrix at `m` (whose row starts `phase` bytes in); 0 outside the row
-    auto load = [&](const char* m, int phase, int s, float (&v)[E]) {
+    // the pairs of slot s of the matrix staged at `m`; 0 outside the row
+    auto load = [&](const char* m, const void* matrix, int64_t row, int s, float2 (&v)[P]) {
         if constexpr (!ODD) {
-            if (t + team_threads * s < vecs) {
-                const uint4 q = *reinterpret_cast<const uint4*>(m + (t + team_threads * s) * 16);
-                const T* e = reinterpret_cast<const T*>(&q);
-#pragma unroll
-                for (int i = 0; i < E; ++i) v[i] = to_float(e[i]);
+            uint4 q = make_uint4(0, 0, 0, 0);
+            if (t + tt * s < vecs) q = *reinterpret_cast<const uint4*>(m + (t + tt * s) * 16);
+            if constexpr (sizeof(T) == 4) {
+                v[0] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+                v[1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
             } else {
-#pragma unroll
-                for (int i = 0; i < E; ++i) v[i] = 0.0f;
+                v[0] = pair_of(q.x, T());
+                v[1] = pair_of(q.y, T());
+                v[2 % P] = pair_of(q.z, T());
+                v[3 % P] = pair_of(q.w, T());
             }
         } else {
+            const int phase = static_cast<int>((reinterpret_cast<uintptr_t>(matrix) + (row * row_bytes + base)) & 15);
             const T* e = reinterpret_cast<const T*>(m + phase);
 #pragma unroll
-            for (int i = 0; i < E; ++i) v[i] = column(s, i) < cols ? to_float(e[column(s, i)]) : 0.0f;
+            for (int j = 0; j < P; ++j) {
+                v[j].x = in(s, 2 * j) ? to_float(e[column(s, 2 * j)]) : 0.0f;
+                v[j].y = in(s, 2 * j + 1) ? to_float(e[column(s, 2 * j + 1)]) : 0.0f;
+            }
         }
     };
-    auto store = [&](void* out, int64_t row, int s, const float (&v)[E]) {
+    auto store = [&](void* out, int64_t row, int s, const float2 (&v)[P]) {
         if constexpr (!ODD) {
-            const int k = t + team_threads * s;
-            if (k < vecs) {
+            if (t + tt * s < vecs) {
                 uint4 q;
-                T* e = reinterpret_cast<T*>(&q);
-#pragma unroll
-                for (int i = 0; i < E; ++i) e[i] = from_float<T>(v[i]);
-                *reinterpret_cast<uint4*>(static_cast<char*>(out) + row * row_bytes + k * 16) = q;
+                if constexpr (sizeof(T) == 4) {
+                    q = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+                } else {
+                    q = make_uint4(bits_of(v[0], T()), bits_of(v[1], T()), bits_of(v[2 % P], T()), bits_of(v[3 % P], T()));
+                }
+                *reinterpret_cast<uint4*>(static_cast<char*>(out) + (row * row_bytes + base) + (t + tt * s) * 16) = q;
             }
         } else {
-            T* o = static_cast<T*>(out) + row * cols;
+            T* o = static_cast<T*>(out) + row * cols + col0;
 #pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (column(s, i) < cols) o[column(s, i)] = from_float<T>(v[i]);
+            for (int j = 0; j < P; ++j) {
+                if (in(s, 2 * j)) o[column(s, 2 * j)] = from_float<T>(v[j].x);
+                if (in(s, 2 * j + 1)) o[column(s, 2 * j + 1)] = from_float<T>(v[j].y);
+            }
         }
     };
-    // E floats of a parameter vector at slot s's columns
-    auto param = [&](const float* w, int s, float absent, float (&v)[E]) {
-        if (!ODD && w && aligned16(w)) {
+    // a parameter vector (from this CTA's first column on) at slot s's columns
+    auto param = [&](const float* w, int s, float absent, float2 (&v)[P]) {
 #pragma unroll
-            for (int i = 0; i < E; i += 4) {
-                float4 q = make_float4(absent, absent, absent, absent);
-                if (t + team_threads * s < vecs) q = ld_param4(w + column(s, i));
-                v[i] = q.x;
-                v[i + 1] = q.y;
-                v[i + 2] = q.z;
-                v[i + 3] = q.w;
-            }
+        for (int j = 0; j < P; ++j) v[j] = both(absent);
+        if (!w) return;
+        if (!ODD && aligned16(w)) {
+            if (t + tt * s < vecs)
+#pragma unroll
+                for (int j = 0; j < P; j += 2) {
+                    const float4 q = ld_param4(w + column(s, 2 * j));
+                    v[j] = make_float2(q.x, q.y);
+                    v[j + 1] = make_float2(q.z, q.w);
+                }
         } else {
 #pragma unroll
-            for (int i = 0; i < E; ++i) v[i] = w && column(s, i) < cols ? __ldg(w + column(s, i)) : absent;
+            for (int j = 0; j < P; ++j) {
+                if (in(s, 2 * j)) v[j].x = __ldg(w + column(s, 2 * j));
+                if (in(s, 2 * j + 1)) v[j].y = __ldg(w + column(s, 2 * j + 1));
+            }
         }
     };
+    auto at0 = [&](const float* w) { return w ? w + col0 : nullptr; };
 
     // the slab's column sums dy hh and dy; those of the running gate row, D ah and D
-    float sum0[C] = {}, sumA[C] = {};
-    float sum1[LAYER ? C : 1] = {}, sumB[LAYER ? C : 1] = {};
-
-    float w_reg[PREG ? C : 1], q_reg[PREG ? C : 1];  // w;  bs gate w_post
-    const float* gate_row = nullptr;
-    auto load_w = [&](int s, float (&v)[E]) { param(p.pre ? p.pre_w : nullptr, s, 1.0f, v); };
-    auto load_q = [&](int s, float (&v)[E]) {
-        float o[E];
-        param(p.post ? p.post_w : nullptr, s, 1.0f, o);
-        param(gate_row, s, 1.0f, v);
+    float2 sum0[K], sumA[K], sum1[LAYER ? K : 1], sumB[LAYER ? K : 1];
+    float2 w[K], qw[K];  // the pre-norm's weight; bs gate w_post
 #pragma unroll
-        for (int i = 0; i < E; ++i) v[i] *= p.bs * o[i];
-    };
-    auto get_w = [&](int s, float (&v)[E]) {
-        if constexpr (PREG) {
+    for (int k = 0; k < K; ++k) {
+        sum0[k] = sumA[k] = both(0.0f);
+        if constexpr (LAYER) sum1[k] = sumB[k] = both(0.0f);
+    }
 #pragma unroll
-            for (int i = 0; i < E; ++i) v[i] = w_reg[s * E + i];
-        } else {
-            load_w(s, v);
-        }
-    };
-    auto get_q = [&](int s, float (&v)[E]) {
-        if constexpr (PREG) {
+    for (int s = 0; s < S; ++s) {
+        float2 v[P];
+        param(p.pre ? at0(p.pre_w) : nullptr, s, 1.0f, v);
 #pragma unroll
-            for (int i = 0; i < E; ++i) v[i] = q_reg[s * E + i];
-        } else {
-            load_q(s, v);
-        }
-    };
+        for (int j = 0; j < P; ++j) w[s * P + j] = v[j];
+    }
+    auto gate_row = [&](int64_t row) { return p.gate ? p.gate + row / p.group_rows * cols + col0 : nullptr; };
     auto enter_group = [&](int64_t row) {
-        gate_row = p.gate ? p.gate + row / p.group_rows * cols : nullptr;
-        if constexpr (PREG) {
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                float v[E];
-                load_q(s, v);
-#pragma unroll
-                for (int i = 0; i < E; ++i) q_reg[s * E + i] = v[i];
-            }
-        }
-    };
-    if constexpr (PREG) {
+        const float* gr = gate_row(row);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float v[E];
-            load_w(s, v);
+            float2 o[P], v[P];
+            param(p.post ? at0(p.post_w) : nullptr, s, 1.0f, o);
+            param(gr, s, 1.0f, v);
 #pragma unroll
-            for (int i = 0; i < E; ++i) w_reg[s * E + i] = v[i];
+            for (int j = 0; j < P; ++j) qw[s * P + j] = __fmul2_rn(v[j], __fmul2_rn(both(p.bs), o[j]));
         }
-    }
-
+    };
     // a whole group is done: its gate gradient is final, and its share of the post-norm's column
     // sums goes to the slab's partials, which no other thread touches
-    float* const part = p.part + index * V * cols;
     bool flushed = false;
     auto leave_group = [&](int64_t row) {
+        const float* gr = gate_row(row);
+        float* dg = p.dgate ? p.dgate + row / p.group_rows * cols + col0 : nullptr;
+        float* part = p.part + index * V * cols + col0;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float o[E], ob[E], gate[E];
-            param(p.post ? p.post_w : nullptr, s, 1.0f, o);
-            param(p.post ? p.post_b : nullptr, s, 0.0f, ob);
-            param(gate_row, s, 1.0f, gate);
-            float* dg = p.dgate ? p.dgate + row / p.group_rows * cols : nullptr;
+            float2 o[P], ob[P], gate[P];
+            param(p.post ? at0(p.post_w) : nullptr, s, 1.0f, o);
+            param(p.post ? at0(p.post_b) : nullptr, s, 0.0f, ob);
+            param(gr, s, 1.0f, gate);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const int c = column(s, i), k = s * E + i;
-                if (c >= cols) continue;
-                if (dg) dg[c] = p.bs * (LAYER ? fmaf(o[i], sumA[k], ob[i] * sumB[LAYER ? k : 0]) : o[i] * sumA[k]);
-                part[cols + c] = fmaf(gate[i], sumA[k], flushed ? part[cols + c] : 0.0f);
-                sumA[k] = 0.0f;
-                if constexpr (LAYER) {
-                    part[3 * cols + c] = fmaf(gate[i], sumB[k], flushed ? part[3 * cols + c] : 0.0f);
-                    sumB[k] = 0.0f;
-                }
+            for (int j = 0; j < P; ++j) {
+                const int k = s * P + j;
+                auto one = [&](int c, float wt, float bias, float gt, float a, float b) {
+                    if (dg) dg[c] = p.bs * (LAYER ? fmaf(wt, a, bias * b) : wt * a);
+                    part[cols + c] = fmaf(gt, a, flushed ? part[cols + c] : 0.0f);
+                    if constexpr (LAYER) part[3 * cols + c] = fmaf(gt, b, flushed ? part[3 * cols + c] : 0.0f);
+                };
+                const float2 b = LAYER ? sumB[LAYER ? k : 0] : both(0.0f);
+                if (in(s, 2 * j)) one(column(s, 2 * j), o[j].x, ob[j].x, gate[j].x, sumA[k].x, b.x);
+                if (in(s, 2 * j + 1)) one(column(s, 2 * j + 1), o[j].y, ob[j].y, gate[j].y, sumA[k].y, b.y);
+                sumA[k] = both(0.0f);
+                if constexpr (LAYER) sumB[k] = both(0.0f);
             }
         }
         flushed = true;
     };
+    // v - m inside the row (the means' tail columns count for nothing)
+    auto centred = [&](float2 v, float m, int s, int j) {
+        float2 c = __fadd2_rn(v, both(-m));
+        if (!in(s, 2 * j)) c.x = 0.0f;
+        if (!in(s, 2 * j + 1)) c.y = 0.0f;
+        return c;
+    };
 
+    // ---- a row's statistics ----
+    float mean_h = 0.0f, mean_a = 0.0f, c1 = 0.0f;  // LayerNorm: means of h, a, u
+    auto sums_of_means = [&](const char* m, int64_t row, float (&v)[3]) {
+        float2 h2 = both(0.0f), a2 = both(0.0f), u2 = both(0.0f);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            float2 x[P], y[P];
+            if (p.pre) {
+                load(m, p.h, row, s, x);
+                load(m + at_dy, p.dy, row, s, y);
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    h2 = __fadd2_rn(h2, x[j]);
+                    u2 = __ffma2_rn(y[j], w[s * P + j], u2);
+                }
+            }
+            if (p.post) {
+                load(m + at_a, p.a, row, s, x);
+#pragma unroll
+                for (int j = 0; j < P; ++j) a2 = __fadd2_rn(a2, x[j]);
+            }
+        }
+        v[0] = h2.x + h2.y;
+        v[1] = a2.x + a2.y;
+        v[2] = u2.x + u2.y;
+    };
+    // sums of (h - mean)^2, (a - mean)^2 and u (h - mean)
+    auto sums_about = [&](const char* m, int64_t row, float mh, float ma, float (&v)[3]) {
+        float2 h2 = both(0.0f), a2 = both(0.0f), u2 = both(0.0f);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            float2 x[P], y[P];
+            if (p.pre) {
+                load(m, p.h, row, s, x);
+                load(m + at_dy, p.dy, row, s, y);
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const float2 c = LAYER ? centred(x[j], mh, s, j) : x[j];
+                    h2 = __ffma2_rn(c, c, h2);
+                    u2 = __ffma2_rn(__fmul2_rn(y[j], w[s * P + j]), c, u2);
+                }
+            }
+            if (p.post) {
+                load(m + at_a, p.a, row, s, x);
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const float2 c = LAYER ? centred(x[j], ma, s, j) : x[j];
+                    a2 = __ffma2_rn(c, c, a2);
+                }
+            }
+        }
+        v[0] = h2.x + h2.y;
+        v[1] = a2.x + a2.y;
+        v[2] = u2.x + u2.y;
+    };
+    // D = dh + r_h (u - c1 - (h - mean) k2) with k2 = r_h^2 mean(u (h - mean))
+    float rh = 0.0f, ra = 0.0f, k2 = 0.0f;
+    auto statistics = [&](float sh, float sa, float su) {
+        if (p.pre) {
+            rh = 1.0f / sqrtf(sh * inv_n + p.eps);
+            k2 = su * inv_n * rh * rh;
+        }
+        if (p.post) ra = 1.0f / sqrtf(sa * inv_n + p.eps);
+    };
+
+    // ---- the first row ----
     for (int i = 0; i + 1 < g.stages; ++i) fetch(slab.begin + i, i);
+    cp_async_wait_n(g.stages - 2);
+    auto odd_barrier = [&]() {
+        if constexpr (CLUSTER) __syncthreads();
+        else team_barrier(team, g.warps);
+    };
+    if constexpr (ODD) odd_barrier();
+    if constexpr (LAYER) {
+        float v[3], x[4];
+        sums_of_means(ring, slab.begin, v);
+        x[0] = v[0];
+        x[1] = v[1];
+        x[2] = v[2];
+        x[3] = 0.0f;
+        ex.template sums<4>(x);
+        mean_h = x[0] * inv_n;
+        mean_a = x[1] * inv_n;
+        c1 = x[2] * inv_n;
+    }
+    {
+        float v[3];
+        sums_about(ring, slab.begin, mean_h, mean_a, v);
+        float x[4] = {v[0], v[1], v[2], 0.0f};
+        ex.template sums<4>(x);
+        statistics(x[0], x[1], x[2]);
+    }
+
     int stage = 0, fill = g.stages - 1;
     int64_t left = 0;  // rows of the running group still to come
     for (int64_t row = slab.begin; row < slab.end; ++row) {
@@ -310,221 +452,204 @@ __global__ void __launch_bounds__(32 * kBwMaxWarps)
             enter_group(row);
             left = p.slices > 0 ? slab.end - slab.begin : p.group_rows;
         }
-        cp_async_wait_n(g.stages - 2);
-        if constexpr (ODD) team_barrier(team, g.warps);
-        // (every thread of the team is done with the row before: the exchanges below follow its last
-        // reads in the odd layout, and an aligned row's slots are the thread's own)
+        if constexpr (ODD) {  // the next row is here, and every thread is done with the row before
+            cp_async_wait_n(g.stages - 3);
+            odd_barrier();
+        }
         fetch(row + g.stages - 1, fill);
         fill = fill + 1 == g.stages ? 0 : fill + 1;
         const char* m = ring + stage * stage_bytes;
         stage = stage + 1 == g.stages ? 0 : stage + 1;
-        const char *mh = m, *mdy = m + at_dy, *ma = m + at_a, *mdh = m + at_dh;
-        const int64_t off = row * row_bytes;
-        auto phase_of = [&](const void* base) {
-            return ODD ? static_cast<int>((reinterpret_cast<uintptr_t>(base) + off) & 15) : 0;
-        };
-        const int fh = phase_of(p.h), fdy = phase_of(p.dy), fa = phase_of(p.a), fdh = phase_of(p.dh);
+        const char* next = ring + stage * stage_bytes;
 
-        float mean_h = 0.0f, mean_a = 0.0f, c1 = 0.0f;
-        if constexpr (LAYER) {
-            float v[N1] = {0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                float x[E], y[E], w[E];
-                if (p.pre) {
-                    load(mh, fh, s, x);
-                    load(mdy, fdy, s, y);
-                    get_w(s, w);
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        v[0] += x[i];
-                        v[2] = fmaf(y[i], w[i], v[2]);
-                    }
-                }
-                if (p.post) {
-                    load(ma, fa, s, x);
-#pragma unroll
-                    for (int i = 0; i < E; ++i) v[1] += x[i];
-                }
-            }
-            team_sums<N1>(v, slot, buf, team, g.warps);
-            mean_h = v[0] * inv_n;
-            mean_a = v[1] * inv_n;
-            c1 = v[2] * inv_n;
-        }
-        float rh = 0.0f, ra = 0.0f, k2 = 0.0f;  // k2 = r_h^2 mean(u (h - mean)): D = dh + r_h (u - c1 - (h - mean) k2)
-        {
-            float v[N1] = {0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                float x[E], y[E], w[E];
-                if (p.pre) {
-                    load(mh, fh, s, x);
-                    load(mdy, fdy, s, y);
-                    get_w(s, w);
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        const float c = LAYER && column(s, i) < cols ? x[i] - mean_h : x[i];
-                        v[0] = fmaf(c, c, v[0]);
-                        v[2] = fmaf(y[i] * w[i], c, v[2]);
-                    }
-                }
-                if (p.post) {
-                    load(ma, fa, s, x);
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        const float c = LAYER && column(s, i) < cols ? x[i] - mean_a : x[i];
-                        v[1] = fmaf(c, c, v[1]);
-                    }
-                }
-            }
-            team_sums<N1>(v, slot, buf, team, g.warps);
-            if (p.pre) {
-                rh = 1.0f / sqrtf(v[0] * inv_n + p.eps);
-                k2 = v[2] * inv_n * rh * rh;
-            }
-            if (p.post) ra = 1.0f / sqrtf(v[1] * inv_n + p.eps);
-        }
-        // D, the column sums, dx, and the sums of q and q ah
-        float d[C];
-        float v[N3] = {};
+        // D, dx, the column sums of the pre-norm, and the sums of q (a - mean) and q
+        float2 d[K];
+        float2 qa = both(0.0f), qs = both(0.0f);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float x[E], y[E], w[E], o[E];
+            float2 x[P], y[P], o[P];
             if (p.dh) {
-                load(mdh, fdh, s, o);
+                load(m + at_dh, p.dh, row, s, o);
             } else {
 #pragma unroll
-                for (int i = 0; i < E; ++i) o[i] = 0.0f;
+                for (int j = 0; j < P; ++j) o[j] = both(0.0f);
             }
             if (p.pre) {
-                load(mh, fh, s, x);
-                load(mdy, fdy, s, y);
-                get_w(s, w);
+                load(m, p.h, row, s, x);
+                load(m + at_dy, p.dy, row, s, y);
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const float c = x[i] - mean_h;
-                    sum0[s * E + i] = fmaf(y[i] * rh, c, sum0[s * E + i]);
-                    if (LAYER) sum1[LAYER ? s * E + i : 0] += y[i];
-                    const float u = fmaf(y[i], w[i], -c1);
-                    o[i] = fmaf(rh, fmaf(-c, k2, u), o[i]);
+                for (int j = 0; j < P; ++j) {
+                    const int k = s * P + j;
+                    const float2 c = LAYER ? __fadd2_rn(x[j], both(-mean_h)) : x[j];
+                    sum0[k] = __ffma2_rn(__fmul2_rn(y[j], both(rh)), c, sum0[k]);
+                    if constexpr (LAYER) sum1[k] = __fadd2_rn(sum1[k], y[j]);
+                    const float2 u = LAYER ? __ffma2_rn(y[j], w[k], both(-c1)) : __fmul2_rn(y[j], w[k]);
+                    o[j] = __ffma2_rn(both(rh), __ffma2_rn(c, both(-k2), u), o[j]);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                d[s * E + i] = o[i];
-                o[i] *= p.rs;
+            for (int j = 0; j < P; ++j) {
+                d[s * P + j] = o[j];
+                o[j] = __fmul2_rn(o[j], both(p.rs));
             }
             store(p.dx, row, s, o);
-            if (need_a) {
-                load(ma, fa, s, x);
-                if (p.post) {
-                    get_q(s, w);
+            if (p.post) {
+                load(m + at_a, p.a, row, s, x);
 #pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        const float c = LAYER && column(s, i) < cols ? x[i] - mean_a : x[i];
-                        const float q = d[s * E + i] * w[i];
-                        v[0] = fmaf(q, c, v[0]);
-                        if (LAYER && column(s, i) < cols) v[N3 - 1] += q;
+                for (int j = 0; j < P; ++j) {
+                    float2 q = __fmul2_rn(d[s * P + j], qw[s * P + j]);
+                    const float2 c = LAYER ? centred(x[j], mean_a, s, j) : x[j];
+                    qa = __ffma2_rn(q, c, qa);
+                    if constexpr (LAYER) {
+                        if (!in(s, 2 * j)) q.x = 0.0f;
+                        if (!in(s, 2 * j + 1)) q.y = 0.0f;
+                        qs = __fadd2_rn(qs, q);
                     }
                 }
             }
         }
-        if (p.post) team_sums<N3>(v, slot, buf, team, g.warps);
-        const float e1 = LAYER ? v[N3 - 1] * inv_n : 0.0f;
-        const float e2 = v[0] * inv_n * ra * ra;
+        // the next row's first sums travel with this row's last ones
+        const bool more = row + 1 < slab.end;
+        if constexpr (!ODD) cp_async_wait_n(g.stages - 2);
+        float v[3] = {0.0f, 0.0f, 0.0f};
+        float e1 = 0.0f, e2;
+        float next_h = 0.0f, next_a = 0.0f, next_c1 = 0.0f;
+        float x4[4];
+        if constexpr (LAYER) {
+            if (more) sums_of_means(next, row + 1, v);
+            float x8[8] = {qa.x + qa.y, qs.x + qs.y, v[0], v[1], v[2], 0.0f, 0.0f, 0.0f};
+            ex.template sums<8>(x8);
+            e1 = x8[1] * inv_n;
+            e2 = x8[0] * inv_n * ra * ra;
+            next_h = x8[2] * inv_n;
+            next_a = x8[3] * inv_n;
+            next_c1 = x8[4] * inv_n;
+        } else {
+            if (more) sums_about(next, row + 1, 0.0f, 0.0f, v);
+            x4[0] = v[0];
+            x4[1] = v[1];
+            x4[2] = v[2];
+            x4[3] = qa.x + qa.y;
+            ex.template sums<4>(x4);
+            e2 = x4[3] * inv_n * ra * ra;
+        }
+        // da, and the column sums of the post-norm and the gate
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float x[E], w[E], o[E];
-            get_q(s, w);
-            if (need_a) load(ma, fa, s, x);
+            float2 x[P], o[P];
+            if (need_a) load(m + at_a, p.a, row, s, x);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const int k = s * E + i;
-                float q = d[k] * w[i];
+            for (int j = 0; j < P; ++j) {
+                const int k = s * P + j;
+                float2 q = __fmul2_rn(d[k], qw[k]);
                 if (need_a) {
-                    float ah = x[i];
+                    float2 ah = x[j];
                     if (p.post) {
-                        const float c = x[i] - mean_a;
-                        q = ra * (fmaf(-c, e2, q) - e1);
-                        ah = c * ra;
+                        const float2 c = LAYER ? __fadd2_rn(x[j], both(-mean_a)) : x[j];
+                        q = __ffma2_rn(c, both(-e2), q);
+                        if constexpr (LAYER) q = __fadd2_rn(q, both(-e1));
+                        q = __fmul2_rn(q, both(ra));
+                        ah = __fmul2_rn(c, both(ra));
                     }
-                    sumA[k] = fmaf(d[k], ah, sumA[k]);
-                    if (LAYER) sumB[LAYER ? k : 0] += d[k];
+                    sumA[k] = __ffma2_rn(d[k], ah, sumA[k]);
+                    if constexpr (LAYER) sumB[k] = __fadd2_rn(sumB[k], d[k]);
                 }
-                o[i] = q;
+                o[j] = q;
             }
             store(p.da, row, s, o);
         }
         if (--left == 0 && p.slices == 0 && p.sums) leave_group(row);
-    }
-    if (!p.sums) return;
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int c = column(s, i), k = s * E + i;
-            if (c >= cols) continue;
-            part[c] = sum0[k];
-            if (p.slices > 0) part[cols + c] = sumA[k];
-            if constexpr (LAYER) {
-                part[2 * cols + c] = sum1[k];
-                if (p.slices > 0) part[3 * cols + c] = sumB[k];
-            }
+        if constexpr (LAYER) {
+            mean_h = next_h;
+            mean_a = next_a;
+            c1 = next_c1;
+            v[0] = v[1] = v[2] = 0.0f;
+            if (more) sums_about(next, row + 1, mean_h, mean_a, v);
+            x4[0] = v[0];
+            x4[1] = v[1];
+            x4[2] = v[2];
+            x4[3] = 0.0f;
+            ex.template sums<4>(x4);
         }
+        statistics(x4[0], x4[1], x4[2]);
+    }
+    if (p.sums) {
+        float* part = p.part + index * V * cols + col0;
+        auto one = [&](int c, float a0, float a1, float b0, float b1) {
+            part[c] = a0;
+            if (p.slices > 0) part[cols + c] = a1;
+            if constexpr (LAYER) {
+                part[2 * cols + c] = b0;
+                if (p.slices > 0) part[3 * cols + c] = b1;
+            }
+        };
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const int k = s * P + j, l = LAYER ? k : 0;
+                const float2 b0 = LAYER ? sum1[l] : both(0.0f), b1 = LAYER ? sumB[l] : both(0.0f);
+                if (in(s, 2 * j)) one(column(s, 2 * j), sum0[k].x, sumA[k].x, b0.x, b1.x);
+                if (in(s, 2 * j + 1)) one(column(s, 2 * j + 1), sum0[k].y, sumA[k].y, b0.y, b1.y);
+            }
+    }
+    if constexpr (CLUSTER) cg::this_cluster().sync();  // no CTA leaves while another may still write to it
 }
 
 // ---- host side -------------------------------------------------------------
 
-// The layout of a pass over `tensors` matrices, or warps = 0 when the row does not fit:
-// as few slots a thread as 16 warps allow, the warps the row needs, several teams in a CTA for short
-// rows, and as many stages (2 .. 4) as leave two CTAs an SM, or one.
-template <class T, bool LAYER>
+// The layout of a pass over `tensors` matrices, or warps = 0 when a row does not fit:
+// 8 columns a thread at most, the fewest CTAs a row that this allows with three stages of ring,
+// several teams in a CTA for short rows, and more stages as far as they leave two CTAs an SM where
+// the threads do.
+template <class T>
 BwShape bwd_shape(int cols, int tensors, bool odd, int* slots) {
     constexpr int E = 16 / static_cast<int>(sizeof(T));
+    constexpr int kMaxSlots = 8 / E;
+    constexpr int kLimit = 226 * 1024;
     BwShape g = {};
     const int vecs = (cols + E - 1) / E;
-    const int s = (vecs + 32 * kBwMaxWarps - 1) / (32 * kBwMaxWarps);
-    if (s > 4 || s * E > (LAYER ? 16 : 32)) return g;
-    *slots = s;
-    g.warps = (vecs + 32 * s - 1) / (32 * s);
-    g.teams = std::max(1, 8 / g.warps);
-    g.tensors = tensors;
-    g.tensor_bytes = vecs * 16 + (odd ? 16 : 0);
-    const int stage = g.teams * tensors * g.tensor_bytes;
-    const int fixed = bwd_fixed_bytes(g);
-    const int most = s * E <= 8 ? 2 : 1;  // CTAs an SM the registers allow for full teams
-    for (g.stages = kBwMaxStages; g.stages > 2; --g.stages)
-        if (most * (fixed + g.stages * stage + 1024) <= 227 * 1024) break;
-    if (fixed + g.stages * stage > 226 * 1024) g.warps = 0;
+    for (g.cluster = 1; g.cluster <= kBwMaxCluster; g.cluster *= 2) {
+        g.cta_vecs = (vecs + g.cluster - 1) / g.cluster;
+        const int s = (g.cta_vecs + 32 * kBwMaxWarps - 1) / (32 * kBwMaxWarps);
+        if (s > kMaxSlots) continue;
+        *slots = s;
+        g.warps = (g.cta_vecs + 32 * s - 1) / (32 * s);
+        g.teams = g.cluster > 1 ? 1 : std::max(1, 8 / g.warps);
+        g.tensors = tensors;
+        g.tensor_bytes = g.cta_vecs * 16 + (odd ? 16 : 0);
+        const int stage = g.teams * tensors * g.tensor_bytes;
+        const int fixed = bwd_fixed_bytes(g);
+        const int ctas = g.teams * g.warps <= 8 ? 2 : 1;
+        for (g.stages = kBwMaxStages; g.stages > 3; --g.stages)
+            if (ctas * (fixed + g.stages * stage + 1024) <= kLimit) break;
+        if (fixed + g.stages * stage <= kLimit) return g;
+    }
+    g.warps = 0;
     return g;
 }
 
-template <class T, bool LAYER, int S, bool ODD>
+template <class T, bool LAYER, int S, bool ODD, bool CLUSTER>
 cudaError_t bwd_go(const BlockBwArgs& in, const BwShape& g, cudaStream_t stream) {
     BlockBwArgs a = in;
     const int threads = g.teams * g.warps * 32;
     const size_t smem = bwd_fixed_bytes(g) + static_cast<size_t>(g.teams) * g.stages * g.tensors * g.tensor_bytes;
-    const auto kernel = bwd_kernel<T, LAYER, S, ODD>;
-    const int64_t ctas = resident_ctas(reinterpret_cast<const void*>(kernel), threads, smem);
+    const auto kernel = bwd_kernel<T, LAYER, S, ODD, CLUSTER>;
+    const int64_t ctas = resident_ctas(reinterpret_cast<const void*>(kernel), threads, smem, g.cluster);
     if (ctas < 1) return cudaErrorInvalidConfiguration;
-    block_slabs(&a, std::min(ctas * g.teams, block_slab_limit(a.rows, a.cols)));
-    const unsigned grid = static_cast<unsigned>((a.slabs + g.teams - 1) / g.teams);
-    cudaError_t e = launch_dependent(kernel, dim3(grid), threads, smem, stream, a, g);
+    block_slabs(&a, std::min(ctas * g.teams / g.cluster, block_slab_limit(a.rows, a.cols)));
+    const unsigned grid = static_cast<unsigned>((a.slabs + g.teams - 1) / g.teams * g.cluster);
+    cudaError_t e = launch_dependent(kernel, dim3(grid), threads, smem, g.cluster, stream, a, g);
     if (e != cudaSuccess || !a.sums) return e;
     return launch_block_finish(LAYER ? TR_NORM_LAYER : TR_NORM_RMS, a, stream);
 }
 
-template <class T, bool LAYER, bool ODD>
+template <class T, bool LAYER, bool ODD, bool CLUSTER>
 cudaError_t bwd_slots(int slots, const BlockBwArgs& a, const BwShape& g, cudaStream_t stream) {
-    constexpr int E = 16 / static_cast<int>(sizeof(T));
-    switch (slots) {
-        case 1: return bwd_go<T, LAYER, 1, ODD>(a, g, stream);
-        case 2: return bwd_go<T, LAYER, 2, ODD>(a, g, stream);
-        case 3: if constexpr (3 * E <= (LAYER ? 16 : 32)) return bwd_go<T, LAYER, 3, ODD>(a, g, stream); break;
-        case 4: if constexpr (4 * E <= (LAYER ? 16 : 32)) return bwd_go<T, LAYER, 4, ODD>(a, g, stream); break;
+    if constexpr (sizeof(T) == 4) {
+        if (slots == 2) return bwd_go<T, LAYER, 2, ODD, CLUSTER>(a, g, stream);
     }
-    return cudaErrorInvalidValue;
+    return bwd_go<T, LAYER, 1, ODD, CLUSTER>(a, g, stream);
 }
 
 template <class T, bool LAYER>
@@ -536,10 +661,12 @@ cudaError_t bwd_kind(const BlockBwArgs& a, bool* done, cudaStream_t stream) {
     for (const void* m : read) odd |= reinterpret_cast<uintptr_t>(m) % 16 != 0;
     for (const void* m : written) odd |= reinterpret_cast<uintptr_t>(m) % 16 != 0;
     int slots = 0;
-    const BwShape g = bwd_shape<T, LAYER>(a.cols, tensors, odd, &slots);
+    const BwShape g = bwd_shape<T>(a.cols, tensors, odd, &slots);
     *done = g.warps > 0;
     if (!*done) return cudaSuccess;
-    return odd ? bwd_slots<T, LAYER, true>(slots, a, g, stream) : bwd_slots<T, LAYER, false>(slots, a, g, stream);
+    if (g.cluster > 1)
+        return odd ? bwd_slots<T, LAYER, true, true>(slots, a, g, stream) : bwd_slots<T, LAYER, false, true>(slots, a, g, stream);
+    return odd ? bwd_slots<T, LAYER, true, false>(slots, a, g, stream) : bwd_slots<T, LAYER, false, false>(slots, a, g, stream);
 }
 
 }  // namespace block
