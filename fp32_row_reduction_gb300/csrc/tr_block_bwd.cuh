@@ -8,9 +8,10 @@
 // over a cluster of 2, 4 or 8 CTAs.
 //
 // With 16-bit types the work per byte is what limits: at 4096 columns a SM has 2090 cycles to
-// the row. So the arithmetic is on pairs (f32x2), and the exchanges between warps are as few
-// as the dependences allow: the next row's statistics travel with this row's sum of
-// q ah, one exchange a row (LayerNorm two: means, then what is taken about them).
+// the row. So the arithmetic is on pairs (f32x2), which norms there are is known when the kernel is
+// compiled, and there is one exchange between warps a row: the next row's statistics travel with
+// this row's sum of q ah. LayerNorm's squares are taken about the warp's own mean and moved to the
+// row's when the warps meet (Chan, Golub and LeVeque 1979), so it needs no second exchange.
 //
 // Two layouts of a row over the threads:
 // * aligned rows (every row of every matrix starts on 16 bytes): slot s of thread t is the
@@ -30,7 +31,7 @@ namespace tr {
 namespace block {
 
 constexpr int kBwMaxWarps = 16;
-constexpr int kBwMaxStages = 8;
+constexpr int kBwMaxStages = 4;
 constexpr int kBwMaxCluster = 8;
 
 // How a launch maps rows onto threads and shared memory.
@@ -44,86 +45,121 @@ struct BwShape {
     int tensor_bytes;  // shared memory of one matrix's row
 };
 
-// Shared memory of the teams' exchanges: two halves of 8 floats for each warp of a row.
-__host__ __device__ inline int bwd_team_bytes(const BwShape& g) { return 2 * 8 * 4 * g.warps * g.cluster; }
+// Shared memory of the teams' exchanges: for each warp of a row two halves of 8 floats, and its columns.
+__host__ __device__ inline int bwd_team_bytes(const BwShape& g) { return (2 * 8 + 4) * 4 * g.warps * g.cluster; }
 __host__ __device__ inline int bwd_fixed_bytes(const BwShape& g) { return (g.teams * bwd_team_bytes(g) + 127) / 128 * 128; }
 
-// The on-chip kernel of one team's view: sums over the row's warps.
+// N values summed over the lanes below 2 x BIT, in one halving step per bit of the value's index
+// (N/2 + N/4 + ... + the other bits: 6 shuffles for 4 values over a warp, not 20). The lanes
+// whose upper bits are i end with value i.
+template <int N, int BIT>
+__device__ __forceinline__ float halving_sums(const float (&v)[N], int lane) {
+    if constexpr (N == 1) {
+        float r = v[0];
+#pragma unroll
+        for (int o = BIT; o >= 1; o >>= 1) r += __shfl_xor_sync(kFull, r, o);
+        return r;
+    } else {
+        const bool up = lane & BIT;
+        float o[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const float keep = up ? v[i + N / 2] : v[i], send = up ? v[i] : v[i + N / 2];
+            o[i] = keep + __shfl_xor_sync(kFull, send, BIT);
+        }
+        return halving_sums<N / 2, BIT / 2>(o, lane);
+    }
+}
+
+// One team's exchange: sums over all warps of a row.
 template <bool CLUSTER>
 struct Exchange {
-    float* slot;   // this CTA's, 2 x 8 x entries floats
+    float* slot;   // this CTA's: 2 x 8 x entries floats, then the entries' column counts
     int entries;   // warps of the row
     int entry;     // this warp's place among them
     int team, warps;
     int buf = 0;
 
-    // v[0 .. N-1] (N = 4 or 8) summed over the row. One halving step per bit of the value's index
-    // (N/2 + N/4 + ... shuffles instead of 5 N): lane 8 i (4 i) ends with value i.
-    template <int N>
-    __device__ __forceinline__ void sums(float (&v)[N]) {
-        static_assert(N == 4 || N == 8, "");
+    // this warp's value i (held by lanes 8 i ..) into place `at + i` of its entry, in every CTA
+    __device__ __forceinline__ void put(float r, int at, int stride) {
         const int lane = threadIdx.x & 31;
-        float r = warp_halves<N>(v, lane);
-        constexpr int kLanes = 32 / N;  // lanes that hold the same value
-        if (!CLUSTER && entries == 1) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = __shfl_sync(kFull, r, i * kLanes);
-            return;
-        }
-        float* s = slot + buf * 8 * entries;
-        buf ^= 1;
-        if constexpr (CLUSTER) {
+        float* s = slot + buf * 8 * entries + entry * stride + at + (lane >> 3);
+        if constexpr (CLUSTER) {  // the eight lanes of a value store it to a CTA each
             cg::cluster_group cl = cg::this_cluster();
-            const int ctas = static_cast<int>(cl.num_blocks());
-            // the lanes of a value store it to one CTA each
-            for (int c = lane % kLanes; c < ctas; c += kLanes)
-                *cl.map_shared_rank(s + entry * N + lane / kLanes, c) = r;
-            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+            if ((lane & 7) < static_cast<int>(cl.num_blocks())) *cl.map_shared_rank(s, lane & 7) = r;
         } else {
-            if (lane % kLanes == 0) s[entry * N + lane / kLanes] = r;
-            asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(warps * 32) : "memory");
+            if ((lane & 7) == 0) *s = r;
         }
-        // 16 entries at a time, half of a value set a lane
-        float t[N / 2] = {};
-        for (int e = lane & 15; e < entries; e += 16) {
-            const float* q = s + e * N + (lane >> 4) * (N / 2);
+    }
+    __device__ __forceinline__ const float* meet() {
+        if constexpr (CLUSTER) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        else team_barrier(team, warps);
+        const float* s = slot + buf * 8 * entries;
+        buf ^= 1;  // (the other half is free: every warp has read it before it came to this barrier)
+        return s;
+    }
+    static __device__ __forceinline__ void spread(float r, float (&v)[4]) {
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i) t[i] += q[i];
-        }
-        r = half_warp_halves<N / 2>(t, lane);
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(kFull, r, i * kLanes);
+        for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(kFull, r, 8 * i);
     }
 
-private:
-    template <int N>
-    static __device__ __forceinline__ float halve(float (&v)[N], int lane, int bit, float (&o)[N / 2]) {
-        const bool up = lane & bit;
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            const float keep = up ? v[i + N / 2] : v[i], send = up ? v[i] : v[i + N / 2];
-            o[i] = keep + __shfl_xor_sync(kFull, send, bit);
+    // v summed over the row
+    __device__ __forceinline__ void sums(float (&v)[4]) {
+        const int lane = threadIdx.x & 31;
+        float r = halving_sums<4, 16>(v, lane);
+        if (!CLUSTER && entries == 1) return spread(r, v);
+        put(r, 0, 4);
+        const float* s = meet();
+        float t[2] = {0.0f, 0.0f};  // 16 entries at a time, two values a lane
+        for (int e = lane & 15; e < entries; e += 16) {
+            const float2 q = *reinterpret_cast<const float2*>(s + e * 4 + (lane >> 4) * 2);
+            t[0] += q.x;
+            t[1] += q.y;
         }
-        return o[0];
+        spread(halving_sums<2, 8>(t, lane), v);
     }
-    // N values over the lanes below `bit` x 2
-    template <int N, int BIT>
-    static __device__ __forceinline__ float halves(float (&v)[N], int lane) {
-        if constexpr (N == 1) {
-            float r = v[0];
-#pragma unroll
-            for (int o = BIT; o >= 1; o >>= 1) r += __shfl_xor_sync(kFull, r, o);
-            return r;
-        } else {
-            float o[N / 2];
-            halve<N>(v, lane, BIT, o);
-            return halves<N / 2, BIT / 2>(o, lane);
+
+    // The warp's sums of h, a and u, and of q (v); then about(mean h, mean a, w), which gives the sums of
+    // squares and products about those means of the warp's own columns in w[0 .. 2] (w[3]: as it is). At the end v holds
+    // the row's sums and w those about the row's means.
+    template <class F>
+    __device__ __forceinline__ void moments(float (&v)[4], float (&w)[4], float inv_n, F&& about) {
+        const int lane = threadIdx.x & 31;
+        float* counts = slot + 16 * entries;
+        const float r = halving_sums<4, 16>(v, lane);
+        const float inv = 1.0f / counts[entry];
+        about(__shfl_sync(kFull, r, 0) * inv, __shfl_sync(kFull, r, 8) * inv, w);
+        const float rw = halving_sums<4, 16>(w, lane);
+        if (!CLUSTER && entries == 1) {
+            spread(r, v);
+            spread(rw, w);
+            return;
         }
+        put(r, 0, 8);
+        put(rw, 4, 8);
+        const float* s = meet();
+        float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int e = lane; e < entries; e += 32) {
+            const float4 q = *reinterpret_cast<const float4*>(s + e * 8);
+            t[0] += q.x;
+            t[1] += q.y;
+            t[2] += q.z;
+            t[3] += q.w;
+        }
+        spread(halving_sums<4, 16>(t, lane), v);
+        const float mh = v[0] * inv_n, ma = v[1] * inv_n;
+        t[0] = t[1] = t[2] = t[3] = 0.0f;
+        for (int e = lane; e < entries; e += 32) {
+            const float4 q = *reinterpret_cast<const float4*>(s + e * 8), z = *reinterpret_cast<const float4*>(s + e * 8 + 4);
+            const float n = counts[e];
+            const float dh = q.x / n - mh, da = q.y / n - ma;  // the entry's means about the row's
+            t[0] += fmaf(n * dh, dh, z.x);
+            t[1] += fmaf(n * da, da, z.y);
+            t[2] += fmaf(dh, q.z, z.z);
+            t[3] += z.w;
+        }
+        spread(halving_sums<4, 16>(t, lane), w);
     }
-    template <int N>
-    static __device__ __forceinline__ float warp_halves(float (&v)[N], int lane) { return halves<N, 16>(v, lane); }
-    template <int N>
-    static __device__ __forceinline__ float half_warp_halves(float (&v)[N], int lane) { return halves<N, 8>(v, lane); }
 };
 
 // A pair of adjacent elements of a type.
@@ -143,12 +179,15 @@ __device__ __forceinline__ uint32_t bits_of(float2 v, __half) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-template <class T, bool LAYER, int S, bool ODD, bool CLUSTER>
-__global__ void __launch_bounds__(32 * kBwMaxWarps) bwd_kernel(const BlockBwArgs p, const BwShape g) {
+// MODE: the norms there are, a mask of TR_BLOCK_POST and TR_BLOCK_PRE; 0: as p says.
+template <class T, bool LAYER, int S, bool ODD, bool CLUSTER, int MODE, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p, const BwShape g) {
     constexpr int E = 16 / static_cast<int>(sizeof(T));
     constexpr int P = E / 2;       // pairs of a slot
     constexpr int K = S * P;       // pairs of a thread
     constexpr int V = LAYER ? 4 : 2;
+    const bool pre = MODE ? (MODE & TR_BLOCK_PRE) != 0 : p.pre != 0;
+    const bool post = MODE ? (MODE & TR_BLOCK_POST) != 0 : p.post != 0;
     extern __shared__ uint4 smem[];
     const int tt = g.warps * 32;  // a team's threads in this CTA
     const int team = CLUSTER ? 0 : static_cast<int>(threadIdx.x) / tt;
@@ -163,6 +202,19 @@ __global__ void __launch_bounds__(32 * kBwMaxWarps) bwd_kernel(const BlockBwArgs
                          rank * g.warps + (t >> 5), team, g.warps};
     const int stage_bytes = g.tensors * g.tensor_bytes;
     char* ring = reinterpret_cast<char*>(smem) + bwd_fixed_bytes(g) + team * g.stages * stage_bytes;
+    if constexpr (LAYER) {  // the columns of each warp of the row
+        float* counts = ex.slot + 16 * ex.entries;
+        for (int e = t; e < ex.entries; e += tt) {
+            const int first = e / g.warps * g.cta_vecs * E, there = min(cols - first, g.cta_vecs * E);
+            int n = 0;
+            for (int k = 0; k < (ODD ? S * E : S); ++k) {
+                const int left = (ODD ? there : there / E) - (e % g.warps * 32 + tt * k);
+                n += max(0, min(32, left)) * (ODD ? 1 : E);
+            }
+            counts[e] = static_cast<float>(max(1, n));
+        }
+        team_barrier(team, g.warps);
+    }
     if constexpr (CLUSTER) cg::this_cluster().sync();  // every CTA of the cluster runs before it is written to
     pdl_enter();
 
@@ -176,9 +228,9 @@ __global__ void __launch_bounds__(32 * kBwMaxWarps) bwd_kernel(const BlockBwArgs
     const SlabRows slab = slab_rows(p, index);
 
     // ---- the ring: h and dy (pre), a, dh, each where there is one ----
-    const bool need_a = p.post || p.dgate;
-    const int at_dy = p.pre ? g.tensor_bytes : 0;
-    const int at_a = p.pre ? 2 * g.tensor_bytes : 0;
+    const bool need_a = post || p.dgate;
+    const int at_dy = pre ? g.tensor_bytes : 0;
+    const int at_a = pre ? 2 * g.tensor_bytes : 0;
     const int at_dh = at_a + (need_a ? g.tensor_bytes : 0);
     const int64_t row_bytes = static_cast<int64_t>(cols) * static_cast<int>(sizeof(T));
     const int64_t base = static_cast<int64_t>(col0) * static_cast<int>(sizeof(T));
@@ -211,7 +263,7 @@ __global__ void __launch_bounds__(32 * kBwMaxWarps) bwd_kernel(const BlockBwArgs
     auto fetch = [&](int64_t row, int stage) {
         if (row < slab.end) {
             char* to = ring + stage * stage_bytes;
-            if (p.pre) {
+            if (pre) {
                 fetch_one(p.h, row, to);
                 fetch_one(p.dy, row, to + at_dy);
             }
@@ -298,7 +350,7 @@ __global__ void __launch_bounds__(32 * kBwMaxWarps) bwd_kernel(const BlockBwArgs
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         float2 v[P];
-        param(p.pre ? at0(p.pre_w) : nullptr, s, 1.0f, v);
+        param(pre ? at0(p.pre_w) : nullptr, s, 1.0f, v);
 #pragma unroll
         for (int j = 0; j < P; ++j) w[s * P + j] = v[j];
     }
@@ -308,7 +360,7 @@ __global__ void __launch_bounds__(32 * kBwMaxWarps) bwd_kernel(const BlockBwArgs
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             float2 o[P], v[P];
-            param(p.post ? at0(p.post_w) : nullptr, s, 1.0f, o);
+            param(post ? at0(p.post_w) : nullptr, s, 1.0f, o);
             param(gr, s, 1.0f, v);
 #pragma unroll
             for (int j = 0; j < P; ++j) qw[s * P + j] = __fmul2_rn(v[j], __fmul2_rn(both(p.bs), o[j]));
@@ -324,8 +376,8 @@ __global__ void __launch_bounds__(32 * kBwMaxWarps) bwd_kernel(const BlockBwArgs
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             float2 o[P], ob[P], gate[P];
-            param(p.post ? at0(p.post_w) : nullptr, s, 1.0f, o);
-            param(p.post ? at0(p.post_b) : nullptr, s, 0.0f, ob);
+            param(post ? at0(p.post_w) : nullptr, s, 1.0f, o);
+            param(post ? at0(p.post_b) : nullptr, s, 0.0f, ob);
             param(gr, s, 1.0f, gate);
 #pragma unroll
             for (int j = 0; j < P; ++j) {
@@ -344,22 +396,34 @@ __global__ void __launch_bounds__(32 * kBwMaxWarps) bwd_kernel(const BlockBwArgs
         }
         flushed = true;
     };
-    // v - m inside the row (the means' tail columns count for nothing)
-    auto centred = [&](float2 v, float m, int s, int j) {
+    // f(pair, whether its elements are in the row) for the pairs of slot s that are (in part) in the row
+    auto pairs = [&](int s, auto&& f) {
+        if constexpr (ODD) {
+#pragma unroll
+            for (int j = 0; j < P; ++j) f(j, in(s, 2 * j), in(s, 2 * j + 1));
+        } else {
+            if (in(s, 0))
+#pragma unroll
+                for (int j = 0; j < P; ++j) f(j, true, true);
+        }
+    };
+    auto about = [&](float2 v, float m, bool x_in, bool y_in) {  // v - m; 0 outside the row
+        if constexpr (!LAYER) return v;
         float2 c = __fadd2_rn(v, both(-m));
-        if (!in(s, 2 * j)) c.x = 0.0f;
-        if (!in(s, 2 * j + 1)) c.y = 0.0f;
+        if (!x_in) c.x = 0.0f;
+        if (!y_in) c.y = 0.0f;
         return c;
     };
 
     // ---- a row's statistics ----
     float mean_h = 0.0f, mean_a = 0.0f, c1 = 0.0f;  // LayerNorm: means of h, a, u
-    auto sums_of_means = [&](const char* m, int64_t row, float (&v)[3]) {
+    // LayerNorm: the thread's sums of h, a and u
+    auto plain_sums = [&](const char* m, int64_t row, float (&v)[4]) {
         float2 h2 = both(0.0f), a2 = both(0.0f), u2 = both(0.0f);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             float2 x[P], y[P];
-            if (p.pre) {
+            if (pre) {
                 load(m, p.h, row, s, x);
                 load(m + at_dy, p.dy, row, s, y);
 #pragma unroll
@@ -368,7 +432,7 @@ __global__ void __launch_bounds__(32 * kBwMaxWarps) bwd_kernel(const BlockBwArgs
                     u2 = __ffma2_rn(y[j], w[s * P + j], u2);
                 }
             }
-            if (p.post) {
+            if (post) {
                 load(m + at_a, p.a, row, s, x);
 #pragma unroll
                 for (int j = 0; j < P; ++j) a2 = __fadd2_rn(a2, x[j]);
@@ -378,71 +442,80 @@ __global__ void __launch_bounds__(32 * kBwMaxWarps) bwd_kernel(const BlockBwArgs
         v[1] = a2.x + a2.y;
         v[2] = u2.x + u2.y;
     };
-    // sums of (h - mean)^2, (a - mean)^2 and u (h - mean)
-    auto sums_about = [&](const char* m, int64_t row, float mh, float ma, float (&v)[3]) {
+    // the thread's sums of (h - mh)^2, (a - ma)^2 and u (h - mh)
+    auto square_sums = [&](const char* m, int64_t row, float mh, float ma, float (&v)[4]) {
         float2 h2 = both(0.0f), a2 = both(0.0f), u2 = both(0.0f);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             float2 x[P], y[P];
-            if (p.pre) {
+            if (pre) {
                 load(m, p.h, row, s, x);
                 load(m + at_dy, p.dy, row, s, y);
-#pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    const float2 c = LAYER ? centred(x[j], mh, s, j) : x[j];
+                pairs(s, [&](int j, bool xi, bool yi) {
+                    const float2 c = about(x[j], mh, xi, yi);
                     h2 = __ffma2_rn(c, c, h2);
                     u2 = __ffma2_rn(__fmul2_rn(y[j], w[s * P + j]), c, u2);
-                }
+                });
             }
-            if (p.post) {
+            if (post) {
                 load(m + at_a, p.a, row, s, x);
-#pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    const float2 c = LAYER ? centred(x[j], ma, s, j) : x[j];
+                pairs(s, [&](int j, bool xi, bool yi) {
+                    const float2 c = about(x[j], ma, xi, yi);
                     a2 = __ffma2_rn(c, c, a2);
-                }
+                });
             }
         }
         v[0] = h2.x + h2.y;
         v[1] = a2.x + a2.y;
         v[2] = u2.x + u2.y;
     };
-    // D = dh + r_h (u - c1 - (h - mean) k2) with k2 = r_h^2 mean(u (h - mean))
+    // The statistics of row `row` staged at m (none when it is not there: `more` is false), with the sums of q
+    // and q (a - mean) of the row before, which end in qs and qa. D = dh + r_h (u - c1 - (h - mean) k2) with
+    // k2 = r_h^2 mean(u (h - mean)). rsqrtf is good to 2^-22, as the sums are.
     float rh = 0.0f, ra = 0.0f, k2 = 0.0f;
-    auto statistics = [&](float sh, float sa, float su) {
-        if (p.pre) {
-            rh = 1.0f / sqrtf(sh * inv_n + p.eps);
-            k2 = su * inv_n * rh * rh;
+    auto statistics = [&](const char* m, int64_t row, bool more, float& qs, float& qa, auto&& between) {
+        [[maybe_unused]] float v[4] = {0.0f, 0.0f, 0.0f, qs};
+        float w4[4] = {0.0f, 0.0f, 0.0f, qa};
+        if constexpr (LAYER) {
+            if (more) plain_sums(m, row, v);
+            ex.moments(v, w4, inv_n, [&](float mh, float ma, float (&o)[4]) {
+                if (more) square_sums(m, row, mh, ma, o);
+            });
+            qs = v[3];
+        } else {
+            if (more) square_sums(m, row, 0.0f, 0.0f, w4);
+            ex.sums(w4);
         }
-        if (p.post) ra = 1.0f / sqrtf(sa * inv_n + p.eps);
+        qa = w4[3];
+        between();
+        if constexpr (LAYER) {
+            mean_h = v[0] * inv_n;
+            mean_a = v[1] * inv_n;
+            c1 = v[2] * inv_n;
+        }
+        if (pre) {
+            rh = rsqrtf(fmaf(w4[0], inv_n, p.eps));
+            k2 = w4[2] * inv_n * rh * rh;
+        }
+        if (post) ra = rsqrtf(fmaf(w4[1], inv_n, p.eps));
     };
 
     // ---- the first row ----
-    for (int i = 0; i + 1 < g.stages; ++i) fetch(slab.begin + i, i);
-    cp_async_wait_n(g.stages - 2);
+    // (the ring is three or four stages; a wait leaves the later rows' copies in flight)
+    auto wait = [&](int newer) {
+        if (g.stages == 3) newer == 1 ? cp_async_wait<0>() : cp_async_wait<1>();
+        else newer == 1 ? cp_async_wait<1>() : cp_async_wait<2>();
+    };
     auto odd_barrier = [&]() {
         if constexpr (CLUSTER) __syncthreads();
         else team_barrier(team, g.warps);
     };
+    for (int i = 0; i + 1 < g.stages; ++i) fetch(slab.begin + i, i);
+    wait(2);
     if constexpr (ODD) odd_barrier();
-    if constexpr (LAYER) {
-        float v[3], x[4];
-        sums_of_means(ring, slab.begin, v);
-        x[0] = v[0];
-        x[1] = v[1];
-        x[2] = v[2];
-        x[3] = 0.0f;
-        ex.template sums<4>(x);
-        mean_h = x[0] * inv_n;
-        mean_a = x[1] * inv_n;
-        c1 = x[2] * inv_n;
-    }
     {
-        float v[3];
-        sums_about(ring, slab.begin, mean_h, mean_a, v);
-        float x[4] = {v[0], v[1], v[2], 0.0f};
-        ex.template sums<4>(x);
-        statistics(x[0], x[1], x[2]);
+        float qs = 0.0f, qa = 0.0f;
+        statistics(ring, slab.begin, true, qs, qa, [] {});
     }
 
     int stage = 0, fill = g.stages - 1;
@@ -453,7 +526,7 @@ __global__ void __launch_bounds__(32 * kBwMaxWarps) bwd_kernel(const BlockBwArgs
             left = p.slices > 0 ? slab.end - slab.begin : p.group_rows;
         }
         if constexpr (ODD) {  // the next row is here, and every thread is done with the row before
-            cp_async_wait_n(g.stages - 3);
+            wait(1);
             odd_barrier();
         }
         fetch(row + g.stages - 1, fill);
@@ -463,8 +536,8 @@ __global__ void __launch_bounds__(32 * kBwMaxWarps) bwd_kernel(const BlockBwArgs
         const char* next = ring + stage * stage_bytes;
 
         // D, dx, the column sums of the pre-norm, and the sums of q (a - mean) and q
-        float2 d[K];
-        float2 qa = both(0.0f), qs = both(0.0f);
+        float2 d[K], av[K];
+        float2 qa2 = both(0.0f), qs2 = both(0.0f);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             float2 x[P], y[P], o[P];
@@ -474,7 +547,7 @@ __global__ void __launch_bounds__(32 * kBwMaxWarps) bwd_kernel(const BlockBwArgs
 #pragma unroll
                 for (int j = 0; j < P; ++j) o[j] = both(0.0f);
             }
-            if (p.pre) {
+            if (pre) {
                 load(m, p.h, row, s, x);
                 load(m + at_dy, p.dy, row, s, y);
 #pragma unroll
@@ -493,85 +566,50 @@ __global__ void __launch_bounds__(32 * kBwMaxWarps) bwd_kernel(const BlockBwArgs
                 o[j] = __fmul2_rn(o[j], both(p.rs));
             }
             store(p.dx, row, s, o);
-            if (p.post) {
+            if (need_a) {
                 load(m + at_a, p.a, row, s, x);
 #pragma unroll
+                for (int j = 0; j < P; ++j) av[s * P + j] = LAYER && post ? __fadd2_rn(x[j], both(-mean_a)) : x[j];
+                if (post)
+                    pairs(s, [&](int j, bool xi, bool yi) {
+                        float2 q = __fmul2_rn(d[s * P + j], qw[s * P + j]);
+                        if (!xi) q.x = 0.0f;
+                        if (!yi) q.y = 0.0f;
+                        qa2 = __ffma2_rn(q, av[s * P + j], qa2);
+                        if constexpr (LAYER) qs2 = __fadd2_rn(qs2, q);
+                    });
+            }
+        }
+        // the next row's statistics travel with this row's sums
+        if constexpr (!ODD) wait(2);
+        float qs = qs2.x + qs2.y, qa = qa2.x + qa2.y;
+        statistics(next, row + 1, row + 1 < slab.end, qs, qa, [&] {
+            // da, and the column sums of the post-norm and the gate
+            const float e1 = qs * inv_n, e2 = qa * inv_n * ra * ra;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                float2 o[P];
+#pragma unroll
                 for (int j = 0; j < P; ++j) {
-                    float2 q = __fmul2_rn(d[s * P + j], qw[s * P + j]);
-                    const float2 c = LAYER ? centred(x[j], mean_a, s, j) : x[j];
-                    qa = __ffma2_rn(q, c, qa);
-                    if constexpr (LAYER) {
-                        if (!in(s, 2 * j)) q.x = 0.0f;
-                        if (!in(s, 2 * j + 1)) q.y = 0.0f;
-                        qs = __fadd2_rn(qs, q);
+                    const int k = s * P + j;
+                    float2 q = __fmul2_rn(d[k], qw[k]);
+                    if (need_a) {
+                        float2 ah = av[k];
+                        if (post) {
+                            q = __ffma2_rn(av[k], both(-e2), q);
+                            if constexpr (LAYER) q = __fadd2_rn(q, both(-e1));
+                            q = __fmul2_rn(q, both(ra));
+                            ah = __fmul2_rn(av[k], both(ra));
+                        }
+                        sumA[k] = __ffma2_rn(d[k], ah, sumA[k]);
+                        if constexpr (LAYER) sumB[k] = __fadd2_rn(sumB[k], d[k]);
                     }
+                    o[j] = q;
                 }
+                store(p.da, row, s, o);
             }
-        }
-        // the next row's first sums travel with this row's last ones
-        const bool more = row + 1 < slab.end;
-        if constexpr (!ODD) cp_async_wait_n(g.stages - 2);
-        float v[3] = {0.0f, 0.0f, 0.0f};
-        float e1 = 0.0f, e2;
-        float next_h = 0.0f, next_a = 0.0f, next_c1 = 0.0f;
-        float x4[4];
-        if constexpr (LAYER) {
-            if (more) sums_of_means(next, row + 1, v);
-            float x8[8] = {qa.x + qa.y, qs.x + qs.y, v[0], v[1], v[2], 0.0f, 0.0f, 0.0f};
-            ex.template sums<8>(x8);
-            e1 = x8[1] * inv_n;
-            e2 = x8[0] * inv_n * ra * ra;
-            next_h = x8[2] * inv_n;
-            next_a = x8[3] * inv_n;
-            next_c1 = x8[4] * inv_n;
-        } else {
-            if (more) sums_about(next, row + 1, 0.0f, 0.0f, v);
-            x4[0] = v[0];
-            x4[1] = v[1];
-            x4[2] = v[2];
-            x4[3] = qa.x + qa.y;
-            ex.template sums<4>(x4);
-            e2 = x4[3] * inv_n * ra * ra;
-        }
-        // da, and the column sums of the post-norm and the gate
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            float2 x[P], o[P];
-            if (need_a) load(m + at_a, p.a, row, s, x);
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                const int k = s * P + j;
-                float2 q = __fmul2_rn(d[k], qw[k]);
-                if (need_a) {
-                    float2 ah = x[j];
-                    if (p.post) {
-                        const float2 c = LAYER ? __fadd2_rn(x[j], both(-mean_a)) : x[j];
-                        q = __ffma2_rn(c, both(-e2), q);
-                        if constexpr (LAYER) q = __fadd2_rn(q, both(-e1));
-                        q = __fmul2_rn(q, both(ra));
-                        ah = __fmul2_rn(c, both(ra));
-                    }
-                    sumA[k] = __ffma2_rn(d[k], ah, sumA[k]);
-                    if constexpr (LAYER) sumB[k] = __fadd2_rn(sumB[k], d[k]);
-                }
-                o[j] = q;
-            }
-            store(p.da, row, s, o);
-        }
-        if (--left == 0 && p.slices == 0 && p.sums) leave_group(row);
-        if constexpr (LAYER) {
-            mean_h = next_h;
-            mean_a = next_a;
-            c1 = next_c1;
-            v[0] = v[1] = v[2] = 0.0f;
-            if (more) sums_about(next, row + 1, mean_h, mean_a, v);
-            x4[0] = v[0];
-            x4[1] = v[1];
-            x4[2] = v[2];
-            x4[3] = 0.0f;
-            ex.template sums<4>(x4);
-        }
-        statistics(x4[0], x4[1], x4[2]);
+            if (--left == 0 && p.slices == 0 && p.sums) leave_group(row);
+        });
     }
     if (p.sums) {
         float* part = p.part + index * V * cols + col0;
@@ -598,10 +636,9 @@ __global__ void __launch_bounds__(32 * kBwMaxWarps) bwd_kernel(const BlockBwArgs
 
 // ---- host side -------------------------------------------------------------
 
-// The layout of a pass over `tensors` matrices, or warps = 0 when a row does not fit:
-// 8 columns a thread at most, the fewest CTAs a row that this allows with three stages of ring,
-// several teams in a CTA for short rows, and more stages as far as they leave two CTAs an SM where
-// the threads do.
+// The layout of a pass over `tensors` matrices, or warps = 0 when a row does not fit: 8 columns
+// a thread at most, the fewest CTAs a row that this allows with three stages of ring (four where they
+// fit), and several teams in a CTA for short rows.
 template <class T>
 BwShape bwd_shape(int cols, int tensors, bool odd, int* slots) {
     constexpr int E = 16 / static_cast<int>(sizeof(T));
@@ -620,21 +657,19 @@ BwShape bwd_shape(int cols, int tensors, bool odd, int* slots) {
         g.tensor_bytes = g.cta_vecs * 16 + (odd ? 16 : 0);
         const int stage = g.teams * tensors * g.tensor_bytes;
         const int fixed = bwd_fixed_bytes(g);
-        const int ctas = g.teams * g.warps <= 8 ? 2 : 1;
-        for (g.stages = kBwMaxStages; g.stages > 3; --g.stages)
-            if (ctas * (fixed + g.stages * stage + 1024) <= kLimit) break;
-        if (fixed + g.stages * stage <= kLimit) return g;
+        for (g.stages = kBwMaxStages; g.stages >= 3; --g.stages)
+            if (fixed + g.stages * stage <= kLimit) return g;
     }
     g.warps = 0;
     return g;
 }
 
-template <class T, bool LAYER, int S, bool ODD, bool CLUSTER>
+template <class T, bool LAYER, int S, bool ODD, bool CLUSTER, int MODE, int THREADS, int CTAS>
 cudaError_t bwd_go(const BlockBwArgs& in, const BwShape& g, cudaStream_t stream) {
     BlockBwArgs a = in;
     const int threads = g.teams * g.warps * 32;
     const size_t smem = bwd_fixed_bytes(g) + static_cast<size_t>(g.teams) * g.stages * g.tensors * g.tensor_bytes;
-    const auto kernel = bwd_kernel<T, LAYER, S, ODD, CLUSTER>;
+    const auto kernel = bwd_kernel<T, LAYER, S, ODD, CLUSTER, MODE, THREADS, CTAS>;
     const int64_t ctas = resident_ctas(reinterpret_cast<const void*>(kernel), threads, smem, g.cluster);
     if (ctas < 1) return cudaErrorInvalidConfiguration;
     block_slabs(&a, std::min(ctas * g.teams / g.cluster, block_slab_limit(a.rows, a.cols)));
@@ -644,12 +679,23 @@ cudaError_t bwd_go(const BlockBwArgs& in, const BwShape& g, cudaStream_t stream)
     return launch_block_finish(LAYER ? TR_NORM_LAYER : TR_NORM_RMS, a, stream);
 }
 
-template <class T, bool LAYER, bool ODD, bool CLUSTER>
-cudaError_t bwd_slots(int slots, const BlockBwArgs& a, const BwShape& g, cudaStream_t stream) {
-    if constexpr (sizeof(T) == 4) {
-        if (slots == 2) return bwd_go<T, LAYER, 2, ODD, CLUSTER>(a, g, stream);
+// Aligned rows of one CTA are compiled for each pair of norms, and for CTAs of at most 320 threads
+// with registers for two an SM.
+template <class T, bool LAYER, int S, int MODE>
+cudaError_t bwd_aligned(const BlockBwArgs& a, const BwShape& g, cudaStream_t stream) {
+    if constexpr (S == 1) {
+        if (g.teams * g.warps <= 10) return bwd_go<T, LAYER, S, false, false, MODE, 320, 2>(a, g, stream);
     }
-    return bwd_go<T, LAYER, 1, ODD, CLUSTER>(a, g, stream);
+    return bwd_go<T, LAYER, S, false, false, MODE, 512, 1>(a, g, stream);
+}
+
+template <class T, bool LAYER, int S>
+cudaError_t bwd_slots(bool odd, const BlockBwArgs& a, const BwShape& g, cudaStream_t stream) {
+    if (g.cluster > 1)
+        return odd ? bwd_go<T, LAYER, S, true, true, 0, 512, 1>(a, g, stream) : bwd_go<T, LAYER, S, false, true, 0, 512, 1>(a, g, stream);
+    if (odd) return bwd_go<T, LAYER, S, true, false, 0, 512, 1>(a, g, stream);
+    if (a.pre && a.post) return bwd_aligned<T, LAYER, S, TR_BLOCK_PRE | TR_BLOCK_POST>(a, g, stream);
+    return a.pre ? bwd_aligned<T, LAYER, S, TR_BLOCK_PRE>(a, g, stream) : bwd_aligned<T, LAYER, S, TR_BLOCK_POST>(a, g, stream);
 }
 
 template <class T, bool LAYER>
@@ -664,9 +710,10 @@ cudaError_t bwd_kind(const BlockBwArgs& a, bool* done, cudaStream_t stream) {
     const BwShape g = bwd_shape<T>(a.cols, tensors, odd, &slots);
     *done = g.warps > 0;
     if (!*done) return cudaSuccess;
-    if (g.cluster > 1)
-        return odd ? bwd_slots<T, LAYER, true, true>(slots, a, g, stream) : bwd_slots<T, LAYER, false, true>(slots, a, g, stream);
-    return odd ? bwd_slots<T, LAYER, true, false>(slots, a, g, stream) : bwd_slots<T, LAYER, false, false>(slots, a, g, stream);
+    if constexpr (sizeof(T) == 4) {
+        if (slots == 2) return bwd_slots<T, LAYER, 2>(odd, a, g, stream);
+    }
+    return bwd_slots<T, LAYER, 1>(odd, a, g, stream);
 }
 
 }  // namespace block
