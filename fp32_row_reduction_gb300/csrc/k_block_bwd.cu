@@ -183,86 +183,95 @@ __global__ void __launch_bounds__(kTile * 8) bwd_columns_kernel(const BlockBwArg
 
 // ---- the slabs' partials to the column gradients --------------------------------
 
-// kTile columns a CTA, 32 warps. Warp w adds slabs w, w + 32, ...; with slices the
-// warps first share out the groups, `per` (a power of two) warps to a group.
-template <bool LAYER>
-__global__ void __launch_bounds__(1024) bwd_finish_kernel(const BlockBwArgs p) {
-    constexpr int V = LAYER ? 4 : 2;
-    __shared__ float red[32][2][kTile];
-    pdl_enter();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int cols = p.cols;
-    const int c = static_cast<int>(blockIdx.x) * kTile + lane;
-    const bool ok = c < cols;
-    auto part = [&](int64_t s, int v) { return ok ? p.part[(s * V + v) * cols + c] : 0.0f; };
-    auto total = [&](float v0, float v1, float& t0, float& t1) {  // over the warps, for warp 0
-        red[w][0][lane] = v0;
-        red[w][1][lane] = v1;
-        __syncthreads();
-        t0 = t1 = 0.0f;
-        if (w == 0)
-#pragma unroll 8
-            for (int i = 0; i < 32; ++i) {
-                t0 += red[i][0][lane];
-                t1 += red[i][1][lane];
-            }
-        __syncthreads();
-    };
-    if (p.pre) {
-        float s0 = 0.0f, s1 = 0.0f, t0, t1;
-        for (int64_t s = w; s < p.slabs; s += 32) {
-            s0 += part(s, 0);
-            if (LAYER) s1 += part(s, 2 % V);
-        }
-        total(s0, s1, t0, t1);
-        if (w == 0 && ok) {
-            if (p.dpre_w) p.dpre_w[c] = t0;
-            if (LAYER && p.dpre_b) p.dpre_b[c] = t1;
-        }
+// A CTA of 1024 threads takes TILE columns, 1024 / TILE slabs at a time; TILE is chosen so that the
+// columns make about as many CTAs as there are SMs (short rows have few columns and many slabs). The
+// partials are read from L2, so what counts is how many loads are under way: four slabs' a thread.
+// With slices the threads of a column first share out the groups, `per` (a power of two) to each.
+constexpr int kFinishThreads = 1024;
+
+// v: a column's sums of slabs first, first + step, ... < end, of the vectors in the mask `want`.
+template <int V>
+__device__ __forceinline__ void slab_sums(const float* part, int cols, int64_t first, int64_t end, int64_t step,
+                                          unsigned want, float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 0.0f;
+    int64_t s = first;
+    for (; s + 3 * step < end; s += 4 * step) {
+        float q[4][V];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int i = 0; i < V; ++i) q[u][i] = (want >> i) & 1 ? part[((s + u * step) * V + i) * cols] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += (q[0][i] + q[1][i]) + (q[2][i] + q[3][i]);
     }
-    if (!p.post && !p.dgate) return;
+    for (; s < end; s += step)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if ((want >> i) & 1) v[i] += part[(s * V + i) * cols];
+}
+
+template <bool LAYER, int TILE>
+__global__ void __launch_bounds__(kFinishThreads) bwd_finish_kernel(const BlockBwArgs p) {
+    constexpr int V = LAYER ? 4 : 2;
+    constexpr int SUBS = kFinishThreads / TILE;
+    __shared__ float red[V][SUBS][TILE];
+    pdl_enter();
+    const int lane = static_cast<int>(threadIdx.x) % TILE, sub = static_cast<int>(threadIdx.x) / TILE;
+    const int cols = p.cols;
+    const int c = static_cast<int>(blockIdx.x) * TILE + lane;
+    const bool ok = c < cols;
+    const float* part = p.part + (ok ? c : 0);
+    // v[i] over the `per` threads from each multiple of `per` on, for the first of them
+    auto tree = [&](float (&v)[V], int per) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V; ++i) red[i][sub][lane] = v[i];
+        for (int o = per / 2; o >= 1; o >>= 1) {
+            __syncthreads();
+            if (sub % per < o)
+#pragma unroll
+                for (int i = 0; i < V; ++i) red[i][sub][lane] += red[i][sub + o][lane];
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = red[i][sub][lane];
+    };
+    const bool need_a = p.post || p.dgate;
+    const bool sliced = need_a && p.slices > 0;  // the second vectors are sums of single gate rows
+    // vectors 0 and 2 (dy hh, dy), and 1 and 3 where they are the slab's own
+    const unsigned own = (p.pre ? 5u : 0u) | (need_a && !sliced ? 10u : 0u);
+    float v[V];
+    slab_sums<V>(part, cols, sub, p.slabs, SUBS, own, v);
     const float ow = ok && p.post && p.post_w ? p.post_w[c] : 1.0f;
     const float ob = ok && p.post && p.post_b ? p.post_b[c] : 0.0f;
-    float x0 = 0.0f, x1 = 0.0f;  // gate D ah, gate D
-    if (p.slices == 0) {
-        for (int64_t s = w; s < p.slabs; s += 32) {
-            x0 += part(s, 1);
-            if (LAYER) x1 += part(s, 3 % V);
-        }
-    } else {
-        int per = 32;
-        while (per > 1 && 32 / per < p.groups) per >>= 1;
-        const int at_once = 32 / per, mine = w / per, sub = w % per;
-        for (int64_t g0 = 0; g0 < p.groups; g0 += at_once) {
-            const int64_t g = g0 + mine;
-            float s0 = 0.0f, s1 = 0.0f;
+    if (sliced) {
+        int per = SUBS;
+        while (per > 1 && SUBS / per < p.groups) per >>= 1;
+        float x0 = 0.0f, x1 = 0.0f;  // gate D ah, gate D
+        for (int64_t g0 = 0; g0 < p.groups; g0 += SUBS / per) {
+            const int64_t g = g0 + sub / per;
+            float t[V] = {};
             if (g < p.groups)
-                for (int64_t i = sub; i < p.slices; i += per) {
-                    s0 += part(g * p.slices + i, 1);
-                    if (LAYER) s1 += part(g * p.slices + i, 3 % V);
-                }
-            red[w][0][lane] = s0;
-            red[w][1][lane] = s1;
-            __syncthreads();
-            if (sub == 0 && g < p.groups && ok) {
-                s0 = s1 = 0.0f;
-                for (int i = 0; i < per; ++i) {
-                    s0 += red[w + i][0][lane];
-                    s1 += red[w + i][1][lane];
-                }
+                slab_sums<V>(part, cols, g * p.slices + sub % per, (g + 1) * p.slices, per, 10u, t);
+            tree(t, per);
+            if (sub % per == 0 && g < p.groups && ok) {
+                const float s0 = t[1], s1 = LAYER ? t[V - 1] : 0.0f;
                 if (p.dgate) p.dgate[g * cols + c] = p.bs * (ow * s0 + ob * s1);
                 const float gate = p.gate ? p.gate[g * cols + c] : 1.0f;
-                x0 += gate * s0;
-                x1 += gate * s1;
+                x0 = fmaf(gate, s0, x0);
+                x1 = fmaf(gate, s1, x1);
             }
-            __syncthreads();
         }
+        v[1] = x0;
+        if (LAYER) v[V - 1] = x1;
     }
-    float t0, t1;
-    total(x0, x1, t0, t1);
-    if (w == 0 && ok && p.post) {
-        if (p.dpost_w) p.dpost_w[c] = p.bs * t0;
-        if (LAYER && p.dpost_b) p.dpost_b[c] = p.bs * t1;
+    tree(v, SUBS);
+    if (sub != 0 || !ok) return;
+    if (p.pre && p.dpre_w) p.dpre_w[c] = v[0];
+    if (p.post && p.dpost_w) p.dpost_w[c] = p.bs * v[1];
+    if constexpr (LAYER) {
+        if (p.pre && p.dpre_b) p.dpre_b[c] = v[2];
+        if (p.post && p.dpost_b) p.dpost_b[c] = p.bs * v[3];
     }
 }
 
@@ -287,10 +296,21 @@ cudaError_t bwd_read(int kind, const BlockBwArgs& a, cudaStream_t stream) {
 
 }  // namespace block
 
+template <bool LAYER>
+static cudaError_t finish(const BlockBwArgs& a, cudaStream_t stream) {
+    using block::bwd_finish_kernel;
+    using block::kFinishThreads;
+    auto go = [&](auto kernel, int tile) {
+        return launch_dependent(kernel, dim3(static_cast<unsigned>((a.cols + tile - 1) / tile)), kFinishThreads, 0, 1, stream, a);
+    };
+    // about one CTA an SM (152); rows of one sector (8 floats) are the least that is read whole
+    if (a.cols >= 32 * 128) return go(bwd_finish_kernel<LAYER, 32>, 32);
+    if (a.cols >= 16 * 128) return go(bwd_finish_kernel<LAYER, 16>, 16);
+    return go(bwd_finish_kernel<LAYER, 8>, 8);
+}
+
 cudaError_t launch_block_finish(int kind, const BlockBwArgs& a, cudaStream_t stream) {
-    const dim3 tiles(static_cast<unsigned>((a.cols + block::kTile - 1) / block::kTile));
-    return kind == TR_NORM_LAYER ? launch_dependent(block::bwd_finish_kernel<true>, tiles, 1024, 0, 1, stream, a)
-                                 : launch_dependent(block::bwd_finish_kernel<false>, tiles, 1024, 0, 1, stream, a);
+    return kind == TR_NORM_LAYER ? finish<true>(a, stream) : finish<false>(a, stream);
 }
 
 cudaError_t launch_block_backward(int kind, int dtype, const BlockBwArgs& a, cudaStream_t stream) {

@@ -71,26 +71,34 @@ __global__ void __launch_bounds__(kReadThreads) fwd_read_kernel(const BlockArgs 
 }
 
 template <class T, bool LAYER>
-cudaError_t fwd_launch(const BlockArgs& a, cudaStream_t stream) {
+cudaError_t fwd_read_launch(const BlockArgs& a, cudaStream_t stream) {
     const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(a.rows, 1 << 20));
     fwd_read_kernel<T, LAYER><<<ctas, kReadThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
 template <class T>
-cudaError_t fwd_kind(int kind, const BlockArgs& a, cudaStream_t stream) {
-    return kind == TR_NORM_LAYER ? fwd_launch<T, true>(a, stream) : fwd_launch<T, false>(a, stream);
+cudaError_t fwd_read(int kind, const BlockArgs& a, cudaStream_t stream) {
+    return kind == TR_NORM_LAYER ? fwd_read_launch<T, true>(a, stream) : fwd_read_launch<T, false>(a, stream);
 }
 
 }  // namespace block
 
 cudaError_t launch_block_forward(int kind, int dtype, const BlockArgs& a, cudaStream_t stream) {
+    bool done = false;
+    cudaError_t e = cudaErrorInvalidValue;
     switch (dtype) {
-        case TR_F32: return block::fwd_kind<float>(kind, a, stream);
-        case TR_BF16: return block::fwd_kind<__nv_bfloat16>(kind, a, stream);
-        case TR_F16: return block::fwd_kind<__half>(kind, a, stream);
+        case TR_F32:
+            e = launch_block_forward_f32(kind, a, &done, stream);
+            return done ? e : block::fwd_read<float>(kind, a, stream);
+        case TR_BF16:
+            e = launch_block_forward_bf16(kind, a, &done, stream);
+            return done ? e : block::fwd_read<__nv_bfloat16>(kind, a, stream);
+        case TR_F16:
+            e = launch_block_forward_f16(kind, a, &done, stream);
+            return done ? e : block::fwd_read<__half>(kind, a, stream);
     }
-    return cudaErrorInvalidValue;
+    return e;
 }
 
 }  // namespace tr

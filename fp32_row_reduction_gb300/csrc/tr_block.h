@@ -102,6 +102,10 @@ inline void block_slabs(BlockBwArgs* a, int64_t target) {
 
 cudaError_t launch_block_forward(int kind, int dtype, const BlockArgs& a, cudaStream_t stream);
 cudaError_t launch_block_backward(int kind, int dtype, const BlockBwArgs& a, cudaStream_t stream);
+// The forward of rows that fit on the chip; *done is false (and nothing launched) for others.
+cudaError_t launch_block_forward_f32(int kind, const BlockArgs& a, bool* done, cudaStream_t stream);
+cudaError_t launch_block_forward_bf16(int kind, const BlockArgs& a, bool* done, cudaStream_t stream);
+cudaError_t launch_block_forward_f16(int kind, const BlockArgs& a, bool* done, cudaStream_t stream);
 // The backward of rows that fit on the chip; *done is false (and nothing launched) for others.
 cudaError_t launch_block_backward_f32(int kind, const BlockBwArgs& a, bool* done, cudaStream_t stream);
 cudaError_t launch_block_backward_bf16(int kind, const BlockBwArgs& a, bool* done, cudaStream_t stream);

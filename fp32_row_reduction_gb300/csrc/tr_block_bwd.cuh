@@ -1,187 +1,24 @@
 // The gated residual norm's backward with the rows on chip (see k_block_bwd.cu for
 // the formulas).
 //
-// HBM-bound: h, a, dy and dh are read and dx and da written once. A team of warps
-// takes a row at a time; a thread owns the same C = 4 or 8 columns of every row of its
-// slab, so the column sums stay in its registers (32-bit) until the slab ends. Rows come through a
-// ring of shared-memory stages filled by cp.async. Rows too long for 16 warps are split
-// over a cluster of 2, 4 or 8 CTAs.
+// HBM-bound: h, a, dy and dh are read and dx and da written once. A thread owns the same columns of
+// every row of its slab, so the column sums stay in its registers (32-bit) until the slab ends.
 //
 // With 16-bit types the work per byte is what limits: at 4096 columns a SM has 2090 cycles to
 // the row. So the arithmetic is on pairs (f32x2), which norms there are is known when the kernel is
 // compiled, and there is one exchange between warps a row: the next row's statistics travel with
 // this row's sum of q ah. LayerNorm's squares are taken about the warp's own mean and moved to the
 // row's when the warps meet (Chan, Golub and LeVeque 1979), so it needs no second exchange.
-//
-// Two layouts of a row over the threads:
-// * aligned rows (every row of every matrix starts on 16 bytes): slot s of thread t is the
-//   16 bytes s x team + t; a thread reads back what it copied itself, so no barrier;
-// * other rows: the 16-byte granules that cover the row are copied as they lie, the
-//   team meets at a barrier, and element k of thread t is column k x team + t, which any phase
-//   reads and writes without bank conflicts or partial sectors.
 #pragma once
 
-#include <algorithm>
-
-#include "tr_block.cuh"
-#include "tr_block.h"
-#include "tr_launch.h"
+#include "tr_block_rows.cuh"
 
 namespace tr {
 namespace block {
 
-constexpr int kBwMaxWarps = 16;
-constexpr int kBwMaxStages = 4;
-constexpr int kBwMaxCluster = 8;
-
-// How a launch maps rows onto threads and shared memory.
-struct BwShape {
-    int warps;         // a team's in one CTA
-    int teams;         // of a CTA
-    int cluster;       // CTAs of a row
-    int cta_vecs;      // 16-byte slots of a row in one CTA
-    int stages;        // of a team's ring (3 or more: two rows are at work, the others on their way)
-    int tensors;       // matrices read
-    int tensor_bytes;  // shared memory of one matrix's row
-};
-
-// Shared memory of the teams' exchanges: for each warp of a row two halves of 8 floats, and its columns.
-__host__ __device__ inline int bwd_team_bytes(const BwShape& g) { return (2 * 8 + 4) * 4 * g.warps * g.cluster; }
-__host__ __device__ inline int bwd_fixed_bytes(const BwShape& g) { return (g.teams * bwd_team_bytes(g) + 127) / 128 * 128; }
-
-// N values summed over the lanes below 2 x BIT, in one halving step per bit of the value's index
-// (N/2 + N/4 + ... + the other bits: 6 shuffles for 4 values over a warp, not 20). The lanes
-// whose upper bits are i end with value i.
-template <int N, int BIT>
-__device__ __forceinline__ float halving_sums(const float (&v)[N], int lane) {
-    if constexpr (N == 1) {
-        float r = v[0];
-#pragma unroll
-        for (int o = BIT; o >= 1; o >>= 1) r += __shfl_xor_sync(kFull, r, o);
-        return r;
-    } else {
-        const bool up = lane & BIT;
-        float o[N / 2];
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            const float keep = up ? v[i + N / 2] : v[i], send = up ? v[i] : v[i + N / 2];
-            o[i] = keep + __shfl_xor_sync(kFull, send, BIT);
-        }
-        return halving_sums<N / 2, BIT / 2>(o, lane);
-    }
-}
-
-// One team's exchange: sums over all warps of a row.
-template <bool CLUSTER>
-struct Exchange {
-    float* slot;   // this CTA's: 2 x 8 x entries floats, then the entries' column counts
-    int entries;   // warps of the row
-    int entry;     // this warp's place among them
-    int team, warps;
-    int buf = 0;
-
-    // this warp's value i (held by lanes 8 i ..) into place `at + i` of its entry, in every CTA
-    __device__ __forceinline__ void put(float r, int at, int stride) {
-        const int lane = threadIdx.x & 31;
-        float* s = slot + buf * 8 * entries + entry * stride + at + (lane >> 3);
-        if constexpr (CLUSTER) {  // the eight lanes of a value store it to a CTA each
-            cg::cluster_group cl = cg::this_cluster();
-            if ((lane & 7) < static_cast<int>(cl.num_blocks())) *cl.map_shared_rank(s, lane & 7) = r;
-        } else {
-            if ((lane & 7) == 0) *s = r;
-        }
-    }
-    __device__ __forceinline__ const float* meet() {
-        if constexpr (CLUSTER) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-        else team_barrier(team, warps);
-        const float* s = slot + buf * 8 * entries;
-        buf ^= 1;  // (the other half is free: every warp has read it before it came to this barrier)
-        return s;
-    }
-    static __device__ __forceinline__ void spread(float r, float (&v)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(kFull, r, 8 * i);
-    }
-
-    // v summed over the row
-    __device__ __forceinline__ void sums(float (&v)[4]) {
-        const int lane = threadIdx.x & 31;
-        float r = halving_sums<4, 16>(v, lane);
-        if (!CLUSTER && entries == 1) return spread(r, v);
-        put(r, 0, 4);
-        const float* s = meet();
-        float t[2] = {0.0f, 0.0f};  // 16 entries at a time, two values a lane
-        for (int e = lane & 15; e < entries; e += 16) {
-            const float2 q = *reinterpret_cast<const float2*>(s + e * 4 + (lane >> 4) * 2);
-            t[0] += q.x;
-            t[1] += q.y;
-        }
-        spread(halving_sums<2, 8>(t, lane), v);
-    }
-
-    // The warp's sums of h, a and u, and of q (v); then about(mean h, mean a, w), which gives the sums of
-    // squares and products about those means of the warp's own columns in w[0 .. 2] (w[3]: as it is). At the end v holds
-    // the row's sums and w those about the row's means.
-    template <class F>
-    __device__ __forceinline__ void moments(float (&v)[4], float (&w)[4], float inv_n, F&& about) {
-        const int lane = threadIdx.x & 31;
-        float* counts = slot + 16 * entries;
-        const float r = halving_sums<4, 16>(v, lane);
-        const float inv = 1.0f / counts[entry];
-        about(__shfl_sync(kFull, r, 0) * inv, __shfl_sync(kFull, r, 8) * inv, w);
-        const float rw = halving_sums<4, 16>(w, lane);
-        if (!CLUSTER && entries == 1) {
-            spread(r, v);
-            spread(rw, w);
-            return;
-        }
-        put(r, 0, 8);
-        put(rw, 4, 8);
-        const float* s = meet();
-        float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int e = lane; e < entries; e += 32) {
-            const float4 q = *reinterpret_cast<const float4*>(s + e * 8);
-            t[0] += q.x;
-            t[1] += q.y;
-            t[2] += q.z;
-            t[3] += q.w;
-        }
-        spread(halving_sums<4, 16>(t, lane), v);
-        const float mh = v[0] * inv_n, ma = v[1] * inv_n;
-        t[0] = t[1] = t[2] = t[3] = 0.0f;
-        for (int e = lane; e < entries; e += 32) {
-            const float4 q = *reinterpret_cast<const float4*>(s + e * 8), z = *reinterpret_cast<const float4*>(s + e * 8 + 4);
-            const float n = counts[e];
-            const float dh = q.x / n - mh, da = q.y / n - ma;  // the entry's means about the row's
-            t[0] += fmaf(n * dh, dh, z.x);
-            t[1] += fmaf(n * da, da, z.y);
-            t[2] += fmaf(dh, q.z, z.z);
-            t[3] += z.w;
-        }
-        spread(halving_sums<4, 16>(t, lane), w);
-    }
-};
-
-// A pair of adjacent elements of a type.
-__device__ __forceinline__ float2 pair_of(uint32_t q, __nv_bfloat16) {
-    return make_float2(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
-}
-__device__ __forceinline__ float2 pair_of(uint32_t q, __half) {
-    return __half22float2(*reinterpret_cast<const __half2*>(&q));
-}
-__device__ __forceinline__ uint32_t bits_of(float2 v, __nv_bfloat16) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
-    return *reinterpret_cast<const uint32_t*>(&b);
-}
-__device__ __forceinline__ uint32_t bits_of(float2 v, __half) {
-    const __half2 b = __floats2half2_rn(v.x, v.y);
-    return *reinterpret_cast<const uint32_t*>(&b);
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-
 // MODE: the norms there are, a mask of TR_BLOCK_POST and TR_BLOCK_PRE; 0: as p says.
 template <class T, bool LAYER, int S, bool ODD, bool CLUSTER, int MODE, int THREADS, int CTAS>
-__global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p, const BwShape g) {
+__global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p, const RowShape g) {
     constexpr int E = 16 / static_cast<int>(sizeof(T));
     constexpr int P = E / 2;       // pairs of a slot
     constexpr int K = S * P;       // pairs of a thread
@@ -194,34 +31,16 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
     const int t = static_cast<int>(threadIdx.x) - team * tt;
     const int rank = CLUSTER ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
     const int cols = p.cols;
-    const int col0 = rank * g.cta_vecs * E;                 // this CTA's first column
-    const int mine = min(cols - col0, g.cta_vecs * E);      // and how many it has
-    const int vecs = mine / E;                              // aligned rows: 16-byte slots
+    const int col0 = rank * g.cta_vecs * E;  // this CTA's first column
+    const Lanes<T, S, ODD> ln(t, tt, cols, col0, g.cta_vecs);
     const float inv_n = 1.0f / static_cast<float>(cols);
-    Exchange<CLUSTER> ex{reinterpret_cast<float*>(smem) + team * (bwd_team_bytes(g) / 4), g.warps * g.cluster,
-                         rank * g.warps + (t >> 5), team, g.warps};
+    Exchange<CLUSTER, 4> ex{reinterpret_cast<float*>(smem) + team * (team_bytes(g) / 4), g.warps * g.cluster,
+                            rank * g.warps + (t >> 5), team, g.warps};
     const int stage_bytes = g.tensors * g.tensor_bytes;
-    char* ring = reinterpret_cast<char*>(smem) + bwd_fixed_bytes(g) + team * g.stages * stage_bytes;
-    if constexpr (LAYER) {  // the columns of each warp of the row
-        float* counts = ex.slot + 16 * ex.entries;
-        for (int e = t; e < ex.entries; e += tt) {
-            const int first = e / g.warps * g.cta_vecs * E, there = min(cols - first, g.cta_vecs * E);
-            int n = 0;
-            for (int k = 0; k < (ODD ? S * E : S); ++k) {
-                const int left = (ODD ? there : there / E) - (e % g.warps * 32 + tt * k);
-                n += max(0, min(32, left)) * (ODD ? 1 : E);
-            }
-            counts[e] = static_cast<float>(max(1, n));
-        }
-        team_barrier(team, g.warps);
-    }
+    char* ring = reinterpret_cast<char*>(smem) + fixed_bytes(g) + team * g.stages * stage_bytes;
+    if constexpr (LAYER) ex.template count_columns<S, E, ODD>(cols, g.cta_vecs, t);
     if constexpr (CLUSTER) cg::this_cluster().sync();  // every CTA of the cluster runs before it is written to
     pdl_enter();
-
-    // column (of this CTA) of element e of slot s
-    auto column = [&](int s, int e) { return ODD ? t + tt * (s * E + e) : (t + tt * s) * E + e; };
-    // whether slot s (pair j of it, in the odd layout element by element) is inside the row
-    auto in = [&](int s, int e) { return ODD ? column(s, e) < mine : t + tt * s < vecs; };
 
     const int64_t index = CLUSTER ? blockIdx.x / g.cluster : static_cast<int64_t>(blockIdx.x) * g.teams + team;
     if (index >= p.slabs) return;  // (a whole cluster, or a whole team)
@@ -232,110 +51,17 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
     const int at_dy = pre ? g.tensor_bytes : 0;
     const int at_a = pre ? 2 * g.tensor_bytes : 0;
     const int at_dh = at_a + (need_a ? g.tensor_bytes : 0);
-    const int64_t row_bytes = static_cast<int64_t>(cols) * static_cast<int>(sizeof(T));
-    const int64_t base = static_cast<int64_t>(col0) * static_cast<int>(sizeof(T));
-    auto fetch_one = [&](const void* matrix, int64_t row, char* to) {
-        const char* from = static_cast<const char*>(matrix) + (row * row_bytes + base);
-        if constexpr (!ODD) {
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const int k = t + tt * s;
-                if (k < vecs) cp_async16(smem_addr(to) + k * 16, from + k * 16);
-            }
-        } else {
-            const int phase = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15);
-            const int granules = (phase + mine * static_cast<int>(sizeof(T)) + 15) >> 4;
-            const char* lo = static_cast<const char*>(matrix);
-            const char* hi = lo + p.rows * row_bytes;
-            for (int k = t; k < granules; k += tt) {
-                const char* q = from - phase + k * 16;
-                if (q >= lo && q + 16 <= hi) {
-                    cp_async16(smem_addr(to) + k * 16, q);
-                } else {  // the matrix's own first or last granule: its elements alone
-                    for (int e = 0; e < E; ++e) {
-                        const char* qe = q + e * static_cast<int>(sizeof(T));
-                        if (qe >= lo && qe < hi) reinterpret_cast<T*>(to)[k * E + e] = *reinterpret_cast<const T*>(qe);
-                    }
-                }
-            }
-        }
-    };
     auto fetch = [&](int64_t row, int stage) {
         if (row < slab.end) {
             char* to = ring + stage * stage_bytes;
             if (pre) {
-                fetch_one(p.h, row, to);
-                fetch_one(p.dy, row, to + at_dy);
+                ln.fetch(p.h, p.rows, row, to);
+                ln.fetch(p.dy, p.rows, row, to + at_dy);
             }
-            if (need_a) fetch_one(p.a, row, to + at_a);
-            if (p.dh) fetch_one(p.dh, row, to + at_dh);
+            if (need_a) ln.fetch(p.a, p.rows, row, to + at_a);
+            if (p.dh) ln.fetch(p.dh, p.rows, row, to + at_dh);
         }
         cp_async_commit();
-    };
-    // the pairs of slot s of the matrix staged at `m`; 0 outside the row
-    auto load = [&](const char* m, const void* matrix, int64_t row, int s, float2 (&v)[P]) {
-        if constexpr (!ODD) {
-            uint4 q = make_uint4(0, 0, 0, 0);
-            if (t + tt * s < vecs) q = *reinterpret_cast<const uint4*>(m + (t + tt * s) * 16);
-            if constexpr (sizeof(T) == 4) {
-                v[0] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
-                v[1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
-            } else {
-                v[0] = pair_of(q.x, T());
-                v[1] = pair_of(q.y, T());
-                v[2 % P] = pair_of(q.z, T());
-                v[3 % P] = pair_of(q.w, T());
-            }
-        } else {
-            const int phase = static_cast<int>((reinterpret_cast<uintptr_t>(matrix) + (row * row_bytes + base)) & 15);
-            const T* e = reinterpret_cast<const T*>(m + phase);
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                v[j].x = in(s, 2 * j) ? to_float(e[column(s, 2 * j)]) : 0.0f;
-                v[j].y = in(s, 2 * j + 1) ? to_float(e[column(s, 2 * j + 1)]) : 0.0f;
-            }
-        }
-    };
-    auto store = [&](void* out, int64_t row, int s, const float2 (&v)[P]) {
-        if constexpr (!ODD) {
-            if (t + tt * s < vecs) {
-                uint4 q;
-                if constexpr (sizeof(T) == 4) {
-                    q = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
-                } else {
-                    q = make_uint4(bits_of(v[0], T()), bits_of(v[1], T()), bits_of(v[2 % P], T()), bits_of(v[3 % P], T()));
-                }
-                *reinterpret_cast<uint4*>(static_cast<char*>(out) + (row * row_bytes + base) + (t + tt * s) * 16) = q;
-            }
-        } else {
-            T* o = static_cast<T*>(out) + row * cols + col0;
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                if (in(s, 2 * j)) o[column(s, 2 * j)] = from_float<T>(v[j].x);
-                if (in(s, 2 * j + 1)) o[column(s, 2 * j + 1)] = from_float<T>(v[j].y);
-            }
-        }
-    };
-    // a parameter vector (from this CTA's first column on) at slot s's columns
-    auto param = [&](const float* w, int s, float absent, float2 (&v)[P]) {
-#pragma unroll
-        for (int j = 0; j < P; ++j) v[j] = both(absent);
-        if (!w) return;
-        if (!ODD && aligned16(w)) {
-            if (t + tt * s < vecs)
-#pragma unroll
-                for (int j = 0; j < P; j += 2) {
-                    const float4 q = ld_param4(w + column(s, 2 * j));
-                    v[j] = make_float2(q.x, q.y);
-                    v[j + 1] = make_float2(q.z, q.w);
-                }
-        } else {
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                if (in(s, 2 * j)) v[j].x = __ldg(w + column(s, 2 * j));
-                if (in(s, 2 * j + 1)) v[j].y = __ldg(w + column(s, 2 * j + 1));
-            }
-        }
     };
     auto at0 = [&](const float* w) { return w ? w + col0 : nullptr; };
 
@@ -350,7 +76,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         float2 v[P];
-        param(pre ? at0(p.pre_w) : nullptr, s, 1.0f, v);
+        ln.param(pre ? at0(p.pre_w) : nullptr, s, 1.0f, v);
 #pragma unroll
         for (int j = 0; j < P; ++j) w[s * P + j] = v[j];
     }
@@ -360,8 +86,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             float2 o[P], v[P];
-            param(post ? at0(p.post_w) : nullptr, s, 1.0f, o);
-            param(gr, s, 1.0f, v);
+            ln.param(post ? at0(p.post_w) : nullptr, s, 1.0f, o);
+            ln.param(gr, s, 1.0f, v);
 #pragma unroll
             for (int j = 0; j < P; ++j) qw[s * P + j] = __fmul2_rn(v[j], __fmul2_rn(both(p.bs), o[j]));
         }
@@ -376,9 +102,9 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             float2 o[P], ob[P], gate[P];
-            param(post ? at0(p.post_w) : nullptr, s, 1.0f, o);
-            param(post ? at0(p.post_b) : nullptr, s, 0.0f, ob);
-            param(gr, s, 1.0f, gate);
+            ln.param(post ? at0(p.post_w) : nullptr, s, 1.0f, o);
+            ln.param(post ? at0(p.post_b) : nullptr, s, 0.0f, ob);
+            ln.param(gr, s, 1.0f, gate);
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 const int k = s * P + j;
@@ -388,24 +114,13 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
                     if constexpr (LAYER) part[3 * cols + c] = fmaf(gt, b, flushed ? part[3 * cols + c] : 0.0f);
                 };
                 const float2 b = LAYER ? sumB[LAYER ? k : 0] : both(0.0f);
-                if (in(s, 2 * j)) one(column(s, 2 * j), o[j].x, ob[j].x, gate[j].x, sumA[k].x, b.x);
-                if (in(s, 2 * j + 1)) one(column(s, 2 * j + 1), o[j].y, ob[j].y, gate[j].y, sumA[k].y, b.y);
+                if (ln.in(s, 2 * j)) one(ln.column(s, 2 * j), o[j].x, ob[j].x, gate[j].x, sumA[k].x, b.x);
+                if (ln.in(s, 2 * j + 1)) one(ln.column(s, 2 * j + 1), o[j].y, ob[j].y, gate[j].y, sumA[k].y, b.y);
                 sumA[k] = both(0.0f);
                 if constexpr (LAYER) sumB[k] = both(0.0f);
             }
         }
         flushed = true;
-    };
-    // f(pair, whether its elements are in the row) for the pairs of slot s that are (in part) in the row
-    auto pairs = [&](int s, auto&& f) {
-        if constexpr (ODD) {
-#pragma unroll
-            for (int j = 0; j < P; ++j) f(j, in(s, 2 * j), in(s, 2 * j + 1));
-        } else {
-            if (in(s, 0))
-#pragma unroll
-                for (int j = 0; j < P; ++j) f(j, true, true);
-        }
     };
     auto about = [&](float2 v, float m, bool x_in, bool y_in) {  // v - m; 0 outside the row
         if constexpr (!LAYER) return v;
@@ -424,8 +139,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
         for (int s = 0; s < S; ++s) {
             float2 x[P], y[P];
             if (pre) {
-                load(m, p.h, row, s, x);
-                load(m + at_dy, p.dy, row, s, y);
+                ln.load(m, p.h, row, s, x);
+                ln.load(m + at_dy, p.dy, row, s, y);
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
                     h2 = __fadd2_rn(h2, x[j]);
@@ -433,7 +148,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
                 }
             }
             if (post) {
-                load(m + at_a, p.a, row, s, x);
+                ln.load(m + at_a, p.a, row, s, x);
 #pragma unroll
                 for (int j = 0; j < P; ++j) a2 = __fadd2_rn(a2, x[j]);
             }
@@ -449,17 +164,17 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
         for (int s = 0; s < S; ++s) {
             float2 x[P], y[P];
             if (pre) {
-                load(m, p.h, row, s, x);
-                load(m + at_dy, p.dy, row, s, y);
-                pairs(s, [&](int j, bool xi, bool yi) {
+                ln.load(m, p.h, row, s, x);
+                ln.load(m + at_dy, p.dy, row, s, y);
+                ln.pairs(s, [&](int j, bool xi, bool yi) {
                     const float2 c = about(x[j], mh, xi, yi);
                     h2 = __ffma2_rn(c, c, h2);
                     u2 = __ffma2_rn(__fmul2_rn(y[j], w[s * P + j]), c, u2);
                 });
             }
             if (post) {
-                load(m + at_a, p.a, row, s, x);
-                pairs(s, [&](int j, bool xi, bool yi) {
+                ln.load(m + at_a, p.a, row, s, x);
+                ln.pairs(s, [&](int j, bool xi, bool yi) {
                     const float2 c = about(x[j], ma, xi, yi);
                     a2 = __ffma2_rn(c, c, a2);
                 });
@@ -478,9 +193,14 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
         float w4[4] = {0.0f, 0.0f, 0.0f, qa};
         if constexpr (LAYER) {
             if (more) plain_sums(m, row, v);
-            ex.moments(v, w4, inv_n, [&](float mh, float ma, float (&o)[4]) {
-                if (more) square_sums(m, row, mh, ma, o);
-            });
+            ex.template moments<2>(
+                v, w4, inv_n,
+                [&](const float (&mean)[2], float (&o)[4]) {
+                    if (more) square_sums(m, row, mean[0], mean[1], o);
+                },
+                [](int i, float n, const float (&d)[2], const float (&sum)[4]) {
+                    return i < 2 ? n * d[i < 2 ? i : 0] * d[i < 2 ? i : 0] : i == 2 ? d[0] * sum[2] : 0.0f;
+                });
             qs = v[3];
         } else {
             if (more) square_sums(m, row, 0.0f, 0.0f, w4);
@@ -501,17 +221,12 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
     };
 
     // ---- the first row ----
-    // (the ring is three or four stages; a wait leaves the later rows' copies in flight)
-    auto wait = [&](int newer) {
-        if (g.stages == 3) newer == 1 ? cp_async_wait<0>() : cp_async_wait<1>();
-        else newer == 1 ? cp_async_wait<1>() : cp_async_wait<2>();
-    };
     auto odd_barrier = [&]() {
         if constexpr (CLUSTER) __syncthreads();
         else team_barrier(team, g.warps);
     };
     for (int i = 0; i + 1 < g.stages; ++i) fetch(slab.begin + i, i);
-    wait(2);
+    ring_wait(g.stages, 2);
     if constexpr (ODD) odd_barrier();
     {
         float qs = 0.0f, qa = 0.0f;
@@ -526,7 +241,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
             left = p.slices > 0 ? slab.end - slab.begin : p.group_rows;
         }
         if constexpr (ODD) {  // the next row is here, and every thread is done with the row before
-            wait(1);
+            ring_wait(g.stages, 1);
             odd_barrier();
         }
         fetch(row + g.stages - 1, fill);
@@ -542,14 +257,14 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
         for (int s = 0; s < S; ++s) {
             float2 x[P], y[P], o[P];
             if (p.dh) {
-                load(m + at_dh, p.dh, row, s, o);
+                ln.load(m + at_dh, p.dh, row, s, o);
             } else {
 #pragma unroll
                 for (int j = 0; j < P; ++j) o[j] = both(0.0f);
             }
             if (pre) {
-                load(m, p.h, row, s, x);
-                load(m + at_dy, p.dy, row, s, y);
+                ln.load(m, p.h, row, s, x);
+                ln.load(m + at_dy, p.dy, row, s, y);
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
                     const int k = s * P + j;
@@ -565,13 +280,13 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
                 d[s * P + j] = o[j];
                 o[j] = __fmul2_rn(o[j], both(p.rs));
             }
-            store(p.dx, row, s, o);
+            ln.store(p.dx, row, s, o);
             if (need_a) {
-                load(m + at_a, p.a, row, s, x);
+                ln.load(m + at_a, p.a, row, s, x);
 #pragma unroll
                 for (int j = 0; j < P; ++j) av[s * P + j] = LAYER && post ? __fadd2_rn(x[j], both(-mean_a)) : x[j];
                 if (post)
-                    pairs(s, [&](int j, bool xi, bool yi) {
+                    ln.pairs(s, [&](int j, bool xi, bool yi) {
                         float2 q = __fmul2_rn(d[s * P + j], qw[s * P + j]);
                         if (!xi) q.x = 0.0f;
                         if (!yi) q.y = 0.0f;
@@ -581,7 +296,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
             }
         }
         // the next row's statistics travel with this row's sums
-        if constexpr (!ODD) wait(2);
+        if constexpr (!ODD) ring_wait(g.stages, 2);
         float qs = qs2.x + qs2.y, qa = qa2.x + qa2.y;
         statistics(next, row + 1, row + 1 < slab.end, qs, qa, [&] {
             // da, and the column sums of the post-norm and the gate
@@ -606,7 +321,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
                     }
                     o[j] = q;
                 }
-                store(p.da, row, s, o);
+                ln.store(p.da, row, s, o);
             }
             if (--left == 0 && p.slices == 0 && p.sums) leave_group(row);
         });
@@ -627,8 +342,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
             for (int j = 0; j < P; ++j) {
                 const int k = s * P + j, l = LAYER ? k : 0;
                 const float2 b0 = LAYER ? sum1[l] : both(0.0f), b1 = LAYER ? sumB[l] : both(0.0f);
-                if (in(s, 2 * j)) one(column(s, 2 * j), sum0[k].x, sumA[k].x, b0.x, b1.x);
-                if (in(s, 2 * j + 1)) one(column(s, 2 * j + 1), sum0[k].y, sumA[k].y, b0.y, b1.y);
+                if (ln.in(s, 2 * j)) one(ln.column(s, 2 * j), sum0[k].x, sumA[k].x, b0.x, b1.x);
+                if (ln.in(s, 2 * j + 1)) one(ln.column(s, 2 * j + 1), sum0[k].y, sumA[k].y, b0.y, b1.y);
             }
     }
     if constexpr (CLUSTER) cg::this_cluster().sync();  // no CTA leaves while another may still write to it
@@ -636,39 +351,11 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
 
 // ---- host side -------------------------------------------------------------
 
-// The layout of a pass over `tensors` matrices, or warps = 0 when a row does not fit: 8 columns
-// a thread at most, the fewest CTAs a row that this allows with three stages of ring (four where they
-// fit), and several teams in a CTA for short rows.
-template <class T>
-BwShape bwd_shape(int cols, int tensors, bool odd, int* slots) {
-    constexpr int E = 16 / static_cast<int>(sizeof(T));
-    constexpr int kMaxSlots = 8 / E;
-    constexpr int kLimit = 226 * 1024;
-    BwShape g = {};
-    const int vecs = (cols + E - 1) / E;
-    for (g.cluster = 1; g.cluster <= kBwMaxCluster; g.cluster *= 2) {
-        g.cta_vecs = (vecs + g.cluster - 1) / g.cluster;
-        const int s = (g.cta_vecs + 32 * kBwMaxWarps - 1) / (32 * kBwMaxWarps);
-        if (s > kMaxSlots) continue;
-        *slots = s;
-        g.warps = (g.cta_vecs + 32 * s - 1) / (32 * s);
-        g.teams = g.cluster > 1 ? 1 : std::max(1, 8 / g.warps);
-        g.tensors = tensors;
-        g.tensor_bytes = g.cta_vecs * 16 + (odd ? 16 : 0);
-        const int stage = g.teams * tensors * g.tensor_bytes;
-        const int fixed = bwd_fixed_bytes(g);
-        for (g.stages = kBwMaxStages; g.stages >= 3; --g.stages)
-            if (fixed + g.stages * stage <= kLimit) return g;
-    }
-    g.warps = 0;
-    return g;
-}
-
 template <class T, bool LAYER, int S, bool ODD, bool CLUSTER, int MODE, int THREADS, int CTAS>
-cudaError_t bwd_go(const BlockBwArgs& in, const BwShape& g, cudaStream_t stream) {
+cudaError_t bwd_go(const BlockBwArgs& in, const RowShape& g, cudaStream_t stream) {
     BlockBwArgs a = in;
     const int threads = g.teams * g.warps * 32;
-    const size_t smem = bwd_fixed_bytes(g) + static_cast<size_t>(g.teams) * g.stages * g.tensors * g.tensor_bytes;
+    const size_t smem = row_smem(g);
     const auto kernel = bwd_kernel<T, LAYER, S, ODD, CLUSTER, MODE, THREADS, CTAS>;
     const int64_t ctas = resident_ctas(reinterpret_cast<const void*>(kernel), threads, smem, g.cluster);
     if (ctas < 1) return cudaErrorInvalidConfiguration;
@@ -682,7 +369,7 @@ cudaError_t bwd_go(const BlockBwArgs& in, const BwShape& g, cudaStream_t stream)
 // Aligned rows of one CTA are compiled for each pair of norms, and for CTAs of at most 320 threads
 // with registers for two an SM.
 template <class T, bool LAYER, int S, int MODE>
-cudaError_t bwd_aligned(const BlockBwArgs& a, const BwShape& g, cudaStream_t stream) {
+cudaError_t bwd_aligned(const BlockBwArgs& a, const RowShape& g, cudaStream_t stream) {
     if constexpr (S == 1) {
         if (g.teams * g.warps <= 10) return bwd_go<T, LAYER, S, false, false, MODE, 320, 2>(a, g, stream);
     }
@@ -690,7 +377,7 @@ cudaError_t bwd_aligned(const BlockBwArgs& a, const BwShape& g, cudaStream_t str
 }
 
 template <class T, bool LAYER, int S>
-cudaError_t bwd_slots(bool odd, const BlockBwArgs& a, const BwShape& g, cudaStream_t stream) {
+cudaError_t bwd_slots(bool odd, const BlockBwArgs& a, const RowShape& g, cudaStream_t stream) {
     if (g.cluster > 1)
         return odd ? bwd_go<T, LAYER, S, true, true, 0, 512, 1>(a, g, stream) : bwd_go<T, LAYER, S, false, true, 0, 512, 1>(a, g, stream);
     if (odd) return bwd_go<T, LAYER, S, true, false, 0, 512, 1>(a, g, stream);
@@ -701,13 +388,10 @@ cudaError_t bwd_slots(bool odd, const BlockBwArgs& a, const BwShape& g, cudaStre
 template <class T, bool LAYER>
 cudaError_t bwd_kind(const BlockBwArgs& a, bool* done, cudaStream_t stream) {
     const int tensors = (a.pre ? 2 : 0) + (a.post || a.dgate ? 1 : 0) + (a.dh ? 1 : 0);
-    const void* read[4] = {a.pre ? a.h : nullptr, a.pre ? a.dy : nullptr, a.post || a.dgate ? a.a : nullptr, a.dh};
-    const void* written[2] = {a.dx, a.da};
-    bool odd = a.cols % (16 / static_cast<int>(sizeof(T))) != 0;
-    for (const void* m : read) odd |= reinterpret_cast<uintptr_t>(m) % 16 != 0;
-    for (const void* m : written) odd |= reinterpret_cast<uintptr_t>(m) % 16 != 0;
+    const bool odd = !rows_aligned(static_cast<int64_t>(a.cols) * static_cast<int>(sizeof(T)),
+                                   {a.pre ? a.h : nullptr, a.pre ? a.dy : nullptr, a.post || a.dgate ? a.a : nullptr, a.dh, a.dx, a.da});
     int slots = 0;
-    const BwShape g = bwd_shape<T>(a.cols, tensors, odd, &slots);
+    const RowShape g = row_shape<T>(a.cols, tensors, odd, 1, &slots);
     *done = g.warps > 0;
     if (!*done) return cudaSuccess;
     if constexpr (sizeof(T) == 4) {
