@@ -19,6 +19,8 @@ from __future__ import annotations
 import array
 import collections
 import ctypes
+import functools
+import operator
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -562,64 +564,61 @@ GatedResidualNormGrads = collections.namedtuple(
     "GatedResidualNormGrads", "dx dbranch dpost_weight dpost_bias dgate dweight dbias")
 
 
-def _dtype_code(dtype):
+@functools.lru_cache(maxsize=None)
+def _dtype_codes():
     import torch
-    code = {torch.float32: TR_F32, torch.bfloat16: TR_BF16, torch.float16: TR_F16}.get(dtype)
+    return {torch.float32: TR_F32, torch.bfloat16: TR_BF16, torch.float16: TR_F16}
+
+
+def _dtype_code(dtype):
+    code = _dtype_codes().get(dtype)
     if code is None:
         raise TypeError(f"float32, bfloat16 or float16 expected, got {dtype}")
     return code
 
 
-class _On:
-    """Makes a device, or the stream asked for, current for a call (what the call allocates
-    then belongs to the stream it runs on); gives the stream's handle."""
+def _switch(index, stream):
+    """What has to be entered before a call on tensors of device `index`: the stream asked for (what
+    the call allocates then belongs to the stream it runs on), the device when it is not current, or None."""
+    import torch
+    if stream is not None:
+        if stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+        return torch.cuda.stream(stream)
+    return None if torch.cuda.current_device() == index else torch.cuda.device(index)
 
-    def __init__(self, device, stream):
-        import torch
-        self._device, self._guard = device, None
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-            self._guard = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != device.index:
-            self._guard = torch.cuda.device(device)
-        self._current = torch.cuda.current_stream
 
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self._current(self._device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+@functools.lru_cache(maxsize=None)
+def _current_stream():
+    """The function that gives a device's current stream handle (torch's direct one where it has it)."""
+    import torch
+    return getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _rows_like(t, name, like):
     """Pointer of a matrix that must match `like` (None: null)."""
     if t is None:
         return None
-    if t.dtype != like.dtype or t.device != like.device:
+    if t.dtype is not like.dtype or t.get_device() != like.get_device():
         raise TypeError(f"{name} must be a {like.dtype} tensor on {like.device}")
     if t.shape != like.shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {tuple(like.shape)} tensor")
     return t.data_ptr()
 
 
-def _floats(t, name, shape, device):
+def _floats(t, name, shape, index):
     """Pointer of a float32 vector or matrix of `shape` (None: null)."""
-    import torch
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.device != device:
-        raise TypeError(f"{name} must be a float32 tensor on {device}")
+    if _dtype_codes().get(t.dtype) != TR_F32 or t.get_device() != index:
+        raise TypeError(f"{name} must be a float32 tensor on cuda:{index}")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor")
     return t.data_ptr()
 
 
 def _block(first, name, gate, kind, post, pre):
-    """What both directions check and derive: (kind, dtype, norms, rows, cols, gate pointer, gate rows)."""
+    """What both directions check and derive: (kind, dtype, norms, rows, cols, device, gate pointer, gate rows)."""
     import torch
     if not isinstance(first, torch.Tensor) or not first.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -627,14 +626,13 @@ def _block(first, name, gate, kind, post, pre):
     if first.dim() != 2 or not first.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 2-D (rows x cols) tensor")
     rows, cols = first.shape
+    index = first.get_device()
     gp, groups = None, 0
     if gate is not None:
-        if gate.dim() == 1:
-            gate = gate.unsqueeze(0)
-        groups = gate.shape[0]
-        gp = _floats(gate, "gate", (groups, cols), first.device)
+        groups = 1 if gate.dim() == 1 else gate.shape[0]
+        gp = _floats(gate, "gate", (cols,) if gate.dim() == 1 else (groups, cols), index)
     code = NORM_KINDS[kind] if isinstance(kind, str) else int(kind)
-    return code, dtype, (TR_BLOCK_POST if post else 0) | (TR_BLOCK_PRE if pre else 0), rows, cols, gp, groups
+    return code, dtype, (TR_BLOCK_POST if post else 0) | (TR_BLOCK_PRE if pre else 0), rows, cols, index, gp, groups
 
 
 def gated_residual_norm(x, branch, post_weight=None, post_bias=None, gate=None, weight=None, bias=None, eps=1e-5,
@@ -649,17 +647,20 @@ def gated_residual_norm(x, branch, post_weight=None, post_bias=None, gate=None, 
     (groups, cols), each row for rows // groups consecutive rows of x. want_h=False
     does not write h (None is returned)."""
     import torch
-    code, dtype, norms, r, c, gp, groups = _block(x, "x", gate, kind, post, pre)
-    dev = x.device
-    bp = _rows_like(branch, "branch", x)
-    pwp, pbp = _floats(post_weight, "post_weight", (c,), dev), _floats(post_bias, "post_bias", (c,), dev)
-    wp, wbp = _floats(weight, "weight", (c,), dev), _floats(bias, "bias", (c,), dev)
-    with _On(dev, stream) as handle:
-        y = (torch.empty_like(x) if out is None else out) if pre or out is not None else None
-        h = (torch.empty_like(x) if h_out is None else h_out) if want_h or h_out is not None else None
-        _check(load().tr_gated_residual_norm(code, dtype, norms, x.data_ptr(), bp, pwp, pbp, gp, groups, wp, wbp,
-                                             _rows_like(h, "h_out", x), _rows_like(y, "out", x), r, c, residual_scale,
-                                             branch_scale, eps, _order(order), handle), "gated_residual_norm")
+    code, dtype, norms, r, c, index, gp, groups = _block(x, "x", gate, kind, post, pre)
+    switch = _switch(index, stream)
+    if switch is not None:
+        with switch:
+            return gated_residual_norm(x, branch, post_weight, post_bias, gate, weight, bias, eps, kind, post, pre,
+                                       residual_scale, branch_scale, out, h_out, want_h, order)
+    vec = (c,)
+    y = out if out is not None or not pre else torch.empty_like(x)
+    h = h_out if h_out is not None or not want_h else torch.empty_like(x)
+    _check(load().tr_gated_residual_norm(
+        code, dtype, norms, x.data_ptr(), _rows_like(branch, "branch", x), _floats(post_weight, "post_weight", vec, index),
+        _floats(post_bias, "post_bias", vec, index), gp, groups, _floats(weight, "weight", vec, index),
+        _floats(bias, "bias", vec, index), _rows_like(h, "h_out", x), _rows_like(y, "out", x), r, c, residual_scale,
+        branch_scale, eps, _order(order), _current_stream()(index)), "gated_residual_norm")
     return y, h
 
 
@@ -677,35 +678,50 @@ def gated_residual_norm_backward(h, branch, dy=None, dh=None, post_weight=None, 
     """The gradients of ``gated_residual_norm`` from its h and branch, the gradient dy of
     y (with pre) and dh of h (None: zero). Returns GatedResidualNormGrads: dx, dbranch (the inputs' type),
     dpost_weight, dpost_bias, dgate (the gate's shape), dweight, dbias (float32; None where
-    there is no such norm, bias or gate, or with want_params=False)."""
+    there is no such norm, bias or gate, or with want_params=False; the vectors lie one after the
+    other in one allocation)."""
     import torch
-    code, dtype, norms, r, c, gp, groups = _block(branch, "branch", gate, kind, post, pre)
-    dev = branch.device
-    f32 = dict(device=dev, dtype=torch.float32)
-    hp = _rows_like(h, "h", branch)
-    dyp, dhp = _rows_like(dy, "dy", branch), _rows_like(dh, "dh", branch)
-    pwp, pbp = _floats(post_weight, "post_weight", (c,), dev), _floats(post_bias, "post_bias", (c,), dev)
-    wp = _floats(weight, "weight", (c,), dev)
-    layer = code == TR_NORM_LAYER
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    wsp, n = None, 0
-    with _On(dev, stream) as handle:
-        dx = torch.empty_like(branch) if dx is None else dx
-        dbranch = torch.empty_like(branch) if dbranch is None else dbranch
-        vector = lambda want: torch.empty(c, **f32) if want_params and want else None  # noqa: E731
-        dpw, dpb, dw, db = vector(post), vector(post and layer), vector(pre), vector(pre and layer)
-        dg = torch.empty_like(gate) if want_params and gate is not None else None
-        if want_params:
-            if workspace is None:
-                workspace = torch.empty(max(16, gated_residual_norm_backward_workspace_bytes(r, c, code)),
-                                        dtype=torch.uint8, device=dev)
-            elif not workspace.is_contiguous() or workspace.device != dev:
-                raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-            wsp, n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        _check(load().tr_gated_residual_norm_backward(
-            code, dtype, norms, hp, branch.data_ptr(), dyp, dhp, pwp, pbp, gp, groups, wp, _rows_like(dx, "dx", branch),
-            _rows_like(dbranch, "dbranch", branch), ptr(dpw), ptr(dpb), ptr(dg), ptr(dw), ptr(db), r, c, residual_scale,
-            branch_scale, eps, _order(order), wsp, n, handle), "gated_residual_norm_backward")
+    code, dtype, norms, r, c, index, gp, groups = _block(branch, "branch", gate, kind, post, pre)
+    switch = _switch(index, stream)
+    if switch is not None:
+        with switch:
+            return gated_residual_norm_backward(h, branch, dy, dh, post_weight, post_bias, gate, weight, eps, kind, post, pre,
+                                                residual_scale, branch_scale, want_params, dx, dbranch, workspace, order)
+    vec = (c,)
+    if dx is None:
+        dx = torch.empty_like(branch)
+    if dbranch is None:
+        dbranch = torch.empty_like(branch)
+    dpw = dpb = dg = dw = db = None
+    ppw = ppb = pg = pw = pb = wsp = None
+    n = 0
+    if want_params:
+        layer = code == TR_NORM_LAYER
+        grads = torch.empty((bool(post) + bool(pre)) * (1 + layer), c, device=branch.device, dtype=torch.float32)
+        rows, p, step = list(grads.unbind(0)), grads.data_ptr(), 4 * c
+        if post:
+            dpw, ppw, p = rows.pop(0), p, p + step
+            if layer:
+                dpb, ppb, p = rows.pop(0), p, p + step
+        if pre:
+            dw, pw, p = rows.pop(0), p, p + step
+            if layer:
+                db, pb = rows.pop(0), p
+        if gate is not None:
+            dg = torch.empty_like(gate)
+            pg = dg.data_ptr()
+        if workspace is None:
+            n = gated_residual_norm_backward_workspace_bytes(r, c, code)
+            workspace = torch.empty(max(16, n), dtype=torch.uint8, device=branch.device)
+        elif not workspace.is_contiguous() or workspace.get_device() != index:
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+        wsp, n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(load().tr_gated_residual_norm_backward(
+        code, dtype, norms, _rows_like(h, "h", branch), branch.data_ptr(), _rows_like(dy, "dy", branch),
+        _rows_like(dh, "dh", branch), _floats(post_weight, "post_weight", vec, index),
+        _floats(post_bias, "post_bias", vec, index), gp, groups, _floats(weight, "weight", vec, index),
+        _rows_like(dx, "dx", branch), _rows_like(dbranch, "dbranch", branch), ppw, ppb, pg, pw, pb, r, c, residual_scale,
+        branch_scale, eps, _order(order), wsp, n, _current_stream()(index)), "gated_residual_norm_backward")
     return GatedResidualNormGrads(dx, dbranch, dpw, dpb, dg, dw, db)
 
 
@@ -723,63 +739,63 @@ def _dense(t):
     return True
 
 
-def _tensor_list(tensors, name, device=None):
-    """(pointers, element counts, dtype codes) of a list of dense CUDA tensors on one device, and the device."""
-    codes = []
-    for t in tensors:
-        if not t.is_cuda:
-            raise TypeError(f"{name} must hold CUDA tensors")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name} must be on one device")
-        codes.append(_dtype_code(t.dtype))
-        if not _dense(t):
-            raise ValueError(f"{name} must hold dense tensors (no gaps and no repeated elements)")
-    return (array.array("Q", [t.data_ptr() for t in tensors]), array.array("q", [t.numel() for t in tensors]),
-            array.array("i", codes), device)
+_shape_of, _dtype_of, _cuda_of = (operator.attrgetter(k) for k in ("shape", "dtype", "is_cuda"))
 
 
-def _out_pointers(tensors, outs, device):
+def _tensor_list(tensors, name, index=None):
+    """(pointers, element counts, dtype codes) of a list of dense CUDA tensors on one device, and the
+    device; `index` is it where the call has another tensor too. (Lists may be long: each check is one pass.)"""
+    import torch
+    T = torch.Tensor
+    if not all(map(_cuda_of, tensors)):
+        raise TypeError(f"{name} must hold CUDA tensors")
+    devices = set(map(T.get_device, tensors))
+    if index is not None:
+        devices.add(index)
+    if len(devices) > 1:
+        raise ValueError(f"{name} must be on one device")
+    codes = array.array("i", map(_dtype_code, map(_dtype_of, tensors)))
+    if not all(map(T.is_contiguous, tensors)) and not all(map(_dense, tensors)):
+        raise ValueError(f"{name} must hold dense tensors (no gaps and no repeated elements)")
+    index = devices.pop() if devices else torch.cuda.current_device()
+    return (array.array("Q", map(T.data_ptr, tensors)), array.array("q", map(T.numel, tensors)), codes, index)
+
+
+def _out_pointers(tensors, outs, index):
     if outs is None:
         return None
-    outs = list(outs)
+    import torch
+    T = torch.Tensor
     if len(outs) != len(tensors):
         raise ValueError("out must hold one tensor for each tensor")
-    for t, o in zip(tensors, outs):
-        if o.dtype != t.dtype or o.device != device:
-            raise TypeError("out must hold tensors of the tensors' types, on their device")
-        # elements are matched by their place in memory
-        if o.shape != t.shape or not ((t.is_contiguous() and o.is_contiguous()) or (o.stride() == t.stride() and _dense(o))):
-            raise ValueError("out must hold tensors of the tensors' shapes and order of elements")
-    return array.array("Q", [o.data_ptr() for o in outs])
+    if set(map(T.get_device, outs)) - {index} or list(map(_dtype_of, outs)) != list(map(_dtype_of, tensors)):
+        raise TypeError("out must hold tensors of the tensors' types, on their device")
+    # elements are matched by their place in memory
+    same = list(map(_shape_of, outs)) == list(map(_shape_of, tensors))
+    if not same or not (all(map(T.is_contiguous, tensors)) and all(map(T.is_contiguous, outs)) or
+                        all(o.stride() == t.stride() and _dense(o) for t, o in zip(tensors, outs))):
+        raise ValueError("out must hold tensors of the tensors' shapes and order of elements")
+    return array.array("Q", map(T.data_ptr, outs))
 
 
 def _address(a):
     return None if a is None else a.buffer_info()[0]
 
 
-def _norm_result(out, device, name):
+def _one_float(t, index, name):
     import torch
-    if out is None:
-        return torch.empty((), device=device, dtype=torch.float32)
-    if out.dtype != torch.float32 or out.numel() != 1 or out.device != device:
-        raise TypeError(f"{name} must be one float32 on {device}")
-    return out
+    if t is None:
+        return torch.empty((), device=torch.device("cuda", index), dtype=torch.float32)
+    if _dtype_codes().get(t.dtype) != TR_F32 or t.numel() != 1 or t.get_device() != index:
+        raise TypeError(f"{name} must be one float32 on cuda:{index}")
+    return t
 
 
-def _norm_workspace(count, device):
+def _norm_workspace(count, index):
     import torch
     n = ctypes.c_size_t(0)
     _check(load().tr_global_norm_workspace_bytes(count, ctypes.byref(n)), "global_norm_workspace_bytes")
-    return torch.empty(n.value, dtype=torch.uint8, device=device)
-
-
-def _list_device(tensors, device):
-    import torch
-    if not tensors and device is None:
-        return torch.device("cuda", torch.cuda.current_device())
-    return device
+    return torch.empty(n.value, dtype=torch.uint8, device=torch.device("cuda", index))
 
 
 def global_norm(tensors, kind="l2", out=None, stream=None):
@@ -787,14 +803,16 @@ def global_norm(tensors, kind="l2", out=None, stream=None):
     float16, mixed as they come): "l2", the square root of the sum of squares, or "max", the
     largest magnitude. Returns one float32 on the device (nothing waits)."""
     tensors = list(tensors)
-    ptrs, numels, codes, device = _tensor_list(tensors, "tensors", None if out is None else out.device)
-    device = _list_device(tensors, device)
+    ptrs, numels, codes, index = _tensor_list(tensors, "tensors", None if out is None else out.get_device())
+    switch = _switch(index, stream)
+    if switch is not None:
+        with switch:
+            return global_norm(tensors, kind, out)
+    norm = _one_float(out, index, "out")
+    ws = _norm_workspace(len(tensors), index)
     code = TOTAL_KINDS[kind] if isinstance(kind, str) else int(kind)
-    with _On(device, stream) as handle:
-        norm = _norm_result(out, device, "out")
-        ws = _norm_workspace(len(tensors), device)
-        _check(load().tr_global_norm(code, _address(ptrs), _address(numels), _address(codes), len(tensors),
-                                     norm.data_ptr(), ws.data_ptr(), ws.numel(), handle), "global_norm")
+    _check(load().tr_global_norm(code, _address(ptrs), _address(numels), _address(codes), len(tensors), norm.data_ptr(),
+                                 ws.data_ptr(), ws.numel(), _current_stream()(index)), "global_norm")
     return norm
 
 
@@ -802,28 +820,35 @@ def clip_by_norm(tensors, norm, max_norm, eps=1e-6, out=None, stream=None):
     """Scale every tensor of a list by min(1, max_norm / (norm + eps)), where norm is
     one float32 on the device, in place or into the tensors of `out`."""
     tensors = list(tensors)
-    ptrs, numels, codes, device = _tensor_list(tensors, "tensors", norm.device)
-    norm = _norm_result(norm, device, "norm")
-    outs = _out_pointers(tensors, out, device)
-    with _On(device, stream) as handle:
-        _check(load().tr_clip_by_norm(_address(ptrs), _address(outs), _address(numels), _address(codes), len(tensors),
-                                      norm.data_ptr(), max_norm, eps, handle), "clip_by_norm")
+    out = None if out is None else list(out)
+    ptrs, numels, codes, index = _tensor_list(tensors, "tensors", norm.get_device())
+    switch = _switch(index, stream)
+    if switch is not None:
+        with switch:
+            return clip_by_norm(tensors, norm, max_norm, eps, out)
+    outs = _out_pointers(tensors, out, index)
+    _check(load().tr_clip_by_norm(_address(ptrs), _address(outs), _address(numels), _address(codes), len(tensors),
+                                  _one_float(norm, index, "norm").data_ptr(), max_norm, eps, _current_stream()(index)),
+           "clip_by_norm")
 
 
 def clip_global_norm(tensors, max_norm, kind="l2", eps=1e-6, out=None, norm_out=None, stream=None):
     """``global_norm`` of a list, then ``clip_by_norm`` with it. Returns the norm before
     clipping (one float32 on the device)."""
     tensors = list(tensors)
-    ptrs, numels, codes, device = _tensor_list(tensors, "tensors", None if norm_out is None else norm_out.device)
-    device = _list_device(tensors, device)
-    outs = _out_pointers(tensors, out, device)
+    out = None if out is None else list(out)
+    ptrs, numels, codes, index = _tensor_list(tensors, "tensors", None if norm_out is None else norm_out.get_device())
+    switch = _switch(index, stream)
+    if switch is not None:
+        with switch:
+            return clip_global_norm(tensors, max_norm, kind, eps, out, norm_out)
+    outs = _out_pointers(tensors, out, index)
+    norm = _one_float(norm_out, index, "norm_out")
+    ws = _norm_workspace(len(tensors), index)
     code = TOTAL_KINDS[kind] if isinstance(kind, str) else int(kind)
-    with _On(device, stream) as handle:
-        norm = _norm_result(norm_out, device, "norm_out")
-        ws = _norm_workspace(len(tensors), device)
-        _check(load().tr_clip_global_norm(code, _address(ptrs), _address(outs), _address(numels), _address(codes),
-                                          len(tensors), max_norm, eps, norm.data_ptr(), ws.data_ptr(), ws.numel(),
-                                          handle), "clip_global_norm")
+    _check(load().tr_clip_global_norm(code, _address(ptrs), _address(outs), _address(numels), _address(codes), len(tensors),
+                                      max_norm, eps, norm.data_ptr(), ws.data_ptr(), ws.numel(), _current_stream()(index)),
+           "clip_global_norm")
     return norm
 
 

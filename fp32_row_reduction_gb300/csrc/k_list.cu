@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "tr_block.cuh"
+#include "tr_launch.h"
 #include "tr_list.h"
 
 namespace tr {
@@ -60,12 +61,23 @@ struct Largest {
     __device__ __forceinline__ double value() const { return static_cast<double>(__uint_as_float(bits)); }
 };
 
-// The elements of 16 bytes as floats.
-template <class T>
-__device__ __forceinline__ void unpack(uint4 q, float (&v)[16 / sizeof(T)]) {
-    const T* e = reinterpret_cast<const T*>(&q);
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(16 / sizeof(T)); ++i) v[i] = to_float(e[i]);
+// Where a tile of a tensor lies: `base` is the tensor's 16-byte boundary, [begin, end) its bytes from there.
+struct Place {
+    const char* base;
+    int64_t begin, end, at;  // at: this thread's first byte of the tile
+    bool whole;              // all of the tile is in the tensor
+};
+template <int N>
+__device__ __forceinline__ Place place_of(const TensorList<N>& l, int i, uint32_t t) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(l.in[i]);
+    const int64_t tile = static_cast<int64_t>(t - l.first[i]) * kListTileBytes;
+    Place q;
+    q.base = reinterpret_cast<const char*>(p & ~static_cast<uintptr_t>(15));
+    q.begin = static_cast<int64_t>(p & 15);
+    q.end = q.begin + l.numel[i] * (l.dtype[i] == TR_F32 ? 4 : 2);
+    q.at = tile + 16 * static_cast<int64_t>(threadIdx.x);
+    q.whole = tile >= q.begin && tile + kListTileBytes <= q.end;
+    return q;
 }
 
 __device__ __forceinline__ uint4 ld16(const char* p) {
@@ -77,53 +89,85 @@ __device__ __forceinline__ uint4 ld16(const char* p) {
     return v;
 }
 
-// A tile's elements, kUnroll groups of 16 / sizeof(T) a thread; absent ones are zero.
-// base: the tensor's 16-byte boundary; [begin, end): its bytes counted from there.
-template <class T>
-__device__ __forceinline__ void load_tile(const char* base, int64_t begin, int64_t end, int64_t tile,
-                                          float (&v)[kUnroll * 16 / sizeof(T)]) {
-    constexpr int E = 16 / sizeof(T);
-    uint4 q[kUnroll];
-    const int64_t at = tile * kListTileBytes + 16 * static_cast<int64_t>(threadIdx.x);
+// A thread's 16-byte words of a tile; elements outside the tensor (of 2 or 4 bytes) are zero.
+__device__ __forceinline__ void load_tile(const Place& p, int size, uint4 (&q)[kUnroll]) {
+    if (p.whole) {
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) q[j] = ld16(p.base + p.at + j * 16 * kListThreads);
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
-        const int64_t b = at + j * 16 * kListThreads;
+        const int64_t b = p.at + j * 16 * kListThreads;
         q[j] = make_uint4(0, 0, 0, 0);
-        if (b >= begin && b + 16 <= end) {
-            q[j] = ld16(base + b);
-        } else if (b + 16 > begin && b < end) {
-            T* e = reinterpret_cast<T*>(&q[j]);
+        if (b >= p.begin && b + 16 <= p.end) {
+            q[j] = ld16(p.base + b);
+        } else if (b + 16 > p.begin && b < p.end) {
+            uint32_t* word = reinterpret_cast<uint32_t*>(&q[j]);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const int64_t bi = b + i * static_cast<int>(sizeof(T));
-                if (bi >= begin && bi < end) e[i] = *reinterpret_cast<const T*>(base + bi);
+            for (int i = 0; i < 4; ++i) {
+                const int64_t bi = b + 4 * i;
+                if (size == 4) {
+                    if (bi >= p.begin && bi < p.end) word[i] = *reinterpret_cast<const uint32_t*>(p.base + bi);
+                } else {
+                    if (bi >= p.begin && bi < p.end) word[i] = *reinterpret_cast<const uint16_t*>(p.base + bi);
+                    if (bi + 2 >= p.begin && bi + 2 < p.end)
+                        word[i] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p.base + bi + 2)) << 16;
+                }
             }
         }
     }
+}
+
+// The elements of 16 bytes as floats.
+template <class T>
+__device__ __forceinline__ void unpack(const uint4 (&q)[kUnroll], float (&v)[kUnroll * 16 / sizeof(T)]) {
+    constexpr int E = 16 / sizeof(T);
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
-        float f[E];
-        unpack<T>(q[j], f);
+        const T* e = reinterpret_cast<const T*>(&q[j]);
 #pragma unroll
-        for (int i = 0; i < E; ++i) v[j * E + i] = f[i];
+        for (int i = 0; i < E; ++i) v[j * E + i] = to_float(e[i]);
     }
 }
 
-// f(tensor index, tile of the tensor) for the CTA's run of tiles.
-template <int N, class F>
+// The CTA's run of tiles, in order or from its end: the next tile's words are on their way while
+// f(tensor, place, words) works on one.
+template <bool BACKWARD, int N, class F>
 __device__ __forceinline__ void for_run(const TensorList<N>& l, F&& f) {
     const uint32_t tiles = l.first[l.count];
-    uint32_t t = static_cast<uint32_t>(static_cast<uint64_t>(tiles) * blockIdx.x / gridDim.x);
+    const uint32_t begin = static_cast<uint32_t>(static_cast<uint64_t>(tiles) * blockIdx.x / gridDim.x);
     const uint32_t end = static_cast<uint32_t>(static_cast<uint64_t>(tiles) * (blockIdx.x + 1) / gridDim.x);
+    if (begin >= end) return;
+    uint32_t t = BACKWARD ? end - 1 : begin;
     int lo = 0, hi = l.count - 1;  // the last tensor that starts at or before t
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (l.first[mid] <= t) lo = mid;
         else hi = mid - 1;
     }
-    for (; t < end; ++t) {
-        while (l.first[lo + 1] <= t) ++lo;
-        f(lo, static_cast<int64_t>(t - l.first[lo]));
+    uint4 q[kUnroll];
+    Place p = place_of(l, lo, t);
+    load_tile(p, l.dtype[lo] == TR_F32 ? 4 : 2, q);
+    for (uint32_t n = end - begin; n > 0; --n) {
+        uint4 ahead[kUnroll];
+        const int i = lo;
+        Place next = p;
+        if (n > 1) {
+            if (BACKWARD) {
+                --t;
+                while (l.first[lo] > t) --lo;
+            } else {
+                ++t;
+                while (l.first[lo + 1] <= t) ++lo;
+            }
+            next = place_of(l, lo, t);
+            load_tile(next, l.dtype[lo] == TR_F32 ? 4 : 2, ahead);
+        }
+        f(i, p, q);
+        p = next;
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) q[j] = ahead[j];
     }
 }
 
@@ -131,18 +175,15 @@ template <class R, int N>
 __global__ void __launch_bounds__(kListThreads) norm_kernel(const __grid_constant__ TensorList<N> l, double* part) {
     pdl_enter();
     R r;
-    for_run(l, [&](int i, int64_t tile) {
-        const uintptr_t p = reinterpret_cast<uintptr_t>(l.in[i]);
-        const char* base = reinterpret_cast<const char*>(p & ~static_cast<uintptr_t>(15));
-        const int64_t begin = static_cast<int64_t>(p & 15);
+    for_run<false>(l, [&](int i, const Place&, const uint4 (&q)[kUnroll]) {
         if (l.dtype[i] == TR_F32) {
             float v[kUnroll * 4];
-            load_tile<float>(base, begin, begin + l.numel[i] * 4, tile, v);
+            unpack<float>(q, v);
             r.add(v);
         } else {
             float v[kUnroll * 8];
-            if (l.dtype[i] == TR_BF16) load_tile<__nv_bfloat16>(base, begin, begin + l.numel[i] * 2, tile, v);
-            else load_tile<__half>(base, begin, begin + l.numel[i] * 2, tile, v);
+            if (l.dtype[i] == TR_BF16) unpack<__nv_bfloat16>(q, v);
+            else unpack<__half>(q, v);
             r.add(v);
         }
     });
@@ -184,31 +225,40 @@ __global__ void __launch_bounds__(kListThreads) total_kernel(int kind, const dou
     if (threadIdx.x == 0) *norm = t;
 }
 
+// A tile scaled into `out`. Where out has another place within 16 bytes than in, the tile goes element by
+// element, neighbours to neighbours: 2 or 4 bytes a lane, but whole sectors.
 template <class T>
-__device__ __forceinline__ void scale_tile(const char* in, char* out, int64_t numel, int64_t tile, float f) {
+__device__ __forceinline__ void scale_tile(const char* in, char* out, const Place& p, const uint4 (&q)[kUnroll], float f) {
     constexpr int E = 16 / sizeof(T);
-    const uintptr_t p = reinterpret_cast<uintptr_t>(in);
-    const char* base = reinterpret_cast<const char*>(p & ~static_cast<uintptr_t>(15));
-    const int64_t begin = static_cast<int64_t>(p & 15), end = begin + numel * static_cast<int64_t>(sizeof(T));
+    if (((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(in)) & 15) != 0) {
+        const T* from = reinterpret_cast<const T*>(in);
+        T* to = reinterpret_cast<T*>(out);
+        const int64_t n = (p.end - p.begin) / static_cast<int64_t>(sizeof(T));
+        const int64_t first = (p.at - 16 * static_cast<int64_t>(threadIdx.x) - p.begin) / static_cast<int64_t>(sizeof(T)) + threadIdx.x;
+#pragma unroll 8
+        for (int k = 0; k < kUnroll * E; ++k) {
+            const int64_t e = first + k * kListThreads;
+            if (e >= 0 && e < n) to[e] = from_float<T>(to_float(from[e]) * f);
+        }
+        return;
+    }
     float v[kUnroll * E];
-    load_tile<T>(base, begin, end, tile, v);
-    char* to = out - begin;
-    const bool phase = ((reinterpret_cast<uintptr_t>(out) ^ p) & 15) == 0;
-    const int64_t at = tile * kListTileBytes + 16 * static_cast<int64_t>(threadIdx.x);
+    unpack<T>(q, v);
+    char* to = out - p.begin + p.at;
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
-        const int64_t b = at + j * 16 * kListThreads;
-        uint4 q;
-        T* e = reinterpret_cast<T*>(&q);
+        const int64_t b = p.at + j * 16 * kListThreads;
+        uint4 o;
+        T* e = reinterpret_cast<T*>(&o);
 #pragma unroll
         for (int i = 0; i < E; ++i) e[i] = from_float<T>(v[j * E + i] * f);
-        if (phase && b >= begin && b + 16 <= end) {
-            *reinterpret_cast<uint4*>(to + b) = q;
+        if (p.whole || (b >= p.begin && b + 16 <= p.end)) {
+            __stcs(reinterpret_cast<uint4*>(to + j * 16 * kListThreads), o);
         } else {
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 const int64_t bi = b + i * static_cast<int>(sizeof(T));
-                if (bi >= begin && bi < end) *reinterpret_cast<T*>(to + bi) = e[i];
+                if (bi >= p.begin && bi < p.end) reinterpret_cast<T*>(to + j * 16 * kListThreads)[i] = e[i];
             }
         }
     }
@@ -223,10 +273,11 @@ __global__ void __launch_bounds__(kListThreads)
     if (write && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
     const float ratio = max_norm / (total + eps);
     const float f = ratio > 1.0f ? 1.0f : ratio;  // a NaN stays
-    for_run(l, [&](int i, int64_t tile) {
-        if (l.dtype[i] == TR_F32) scale_tile<float>(l.in[i], l.out[i], l.numel[i], tile, f);
-        else if (l.dtype[i] == TR_BF16) scale_tile<__nv_bfloat16>(l.in[i], l.out[i], l.numel[i], tile, f);
-        else scale_tile<__half>(l.in[i], l.out[i], l.numel[i], tile, f);
+    // from the end of the run, which the norm's pass read last
+    for_run<true>(l, [&](int i, const Place& p, const uint4 (&q)[kUnroll]) {
+        if (l.dtype[i] == TR_F32) scale_tile<float>(l.in[i], l.out[i], p, q, f);
+        else if (l.dtype[i] == TR_BF16) scale_tile<__nv_bfloat16>(l.in[i], l.out[i], p, q, f);
+        else scale_tile<__half>(l.in[i], l.out[i], p, q, f);
     });
 }
 
@@ -242,25 +293,19 @@ void copy_list(Dst* d, const Src& s) {
 
 // CTAs of a launch: what the device holds at once, but no more than there are tiles.
 int list_ctas(const void* kernel, uint32_t tiles) {
-    int dev = 0, sms = 0, per = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kListThreads, 0) != cudaSuccess)
-        return 0;
-    return static_cast<int>(std::min<int64_t>(tiles, std::min(kListMaxCtas, std::max(1, per) * sms)));
+    return static_cast<int>(std::min<int64_t>(tiles, std::min(kListMaxCtas, resident_ctas(kernel, kListThreads, 0))));
 }
 
 template <class R>
 cudaError_t norm_launch(const TensorList<kListMax>& l, double* part, int* ctas, cudaStream_t stream) {
     *ctas = list_ctas(reinterpret_cast<const void*>(norm_kernel<R, kListMax>), l.first[l.count]);
-    if (*ctas < 1) return cudaGetLastError();
+    if (*ctas < 1) return cudaErrorInvalidConfiguration;
     if (l.count <= kListFew) {
         TensorList<kListFew> few;
         copy_list(&few, l);
-        norm_kernel<R, kListFew><<<*ctas, kListThreads, 0, stream>>>(few, part);
-    } else {
-        norm_kernel<R, kListMax><<<*ctas, kListThreads, 0, stream>>>(l, part);
+        return launch_dependent(norm_kernel<R, kListFew>, dim3(*ctas), kListThreads, 0, 1, stream, few, part);
     }
-    return cudaGetLastError();
+    return launch_dependent(norm_kernel<R, kListMax>, dim3(*ctas), kListThreads, 0, 1, stream, l, part);
 }
 
 }  // namespace list
@@ -271,22 +316,19 @@ cudaError_t launch_list_norm(int kind, const TensorList<kListMax>& l, double* pa
 }
 
 cudaError_t launch_list_total(int kind, const double* part, int n, float* norm, cudaStream_t stream) {
-    list::total_kernel<<<1, kListThreads, 0, stream>>>(kind, part, n, norm);
-    return cudaGetLastError();
+    return launch_dependent(list::total_kernel, dim3(1), kListThreads, 0, 1, stream, kind, part, n, norm);
 }
 
 cudaError_t launch_list_scale(int kind, const TensorList<kListMax>& l, const double* part, int n, float* norm, int write,
                               float max_norm, float eps, cudaStream_t stream) {
     const int ctas = list::list_ctas(reinterpret_cast<const void*>(list::scale_kernel<kListMax>), l.first[l.count]);
-    if (ctas < 1) return cudaGetLastError();
+    if (ctas < 1) return cudaErrorInvalidConfiguration;
     if (l.count <= kListFew) {
         TensorList<kListFew> few;
         list::copy_list(&few, l);
-        list::scale_kernel<kListFew><<<ctas, kListThreads, 0, stream>>>(few, kind, part, n, norm, write, max_norm, eps);
-    } else {
-        list::scale_kernel<kListMax><<<ctas, kListThreads, 0, stream>>>(l, kind, part, n, norm, write, max_norm, eps);
+        return launch_dependent(list::scale_kernel<kListFew>, dim3(ctas), kListThreads, 0, 1, stream, few, kind, part, n, norm, write, max_norm, eps);
     }
-    return cudaGetLastError();
+    return launch_dependent(list::scale_kernel<kListMax>, dim3(ctas), kListThreads, 0, 1, stream, l, kind, part, n, norm, write, max_norm, eps);
 }
 
 }  // namespace tr

@@ -315,7 +315,7 @@ tr_status tr_gated_residual_norm(tr_norm_kind kind, tr_dtype dtype, int32_t norm
     if (s != TR_OK) return s;
     BlockArgs a{x, branch, h, y, post_w, post_b, gate, pre_w, pre_b, rows, gate ? rows / gate_rows : rows,
                 static_cast<int>(cols), norms & TR_BLOCK_POST ? 1 : 0, pre ? 1 : 0, residual_scale, branch_scale, eps};
-    return cuda_status(launch_block_forward(kind, dtype, a, stream), w);
+    return guarded(w, [&] { return cuda_status(launch_block_forward(kind, dtype, a, stream), w); });
 }
 
 tr_status tr_gated_residual_norm_backward_workspace_bytes(tr_norm_kind kind, int64_t rows, int64_t cols, size_t* bytes) {
@@ -399,7 +399,7 @@ tr_status tr_gated_residual_norm_backward(tr_norm_kind kind, tr_dtype dtype, int
         a.stats = static_cast<float*>(workspace);
         a.part = a.stats + stats_bytes(rows) / sizeof(float);
     }
-    return cuda_status(launch_block_backward(kind, dtype, a, stream), w);
+    return guarded(w, [&] { return cuda_status(launch_block_backward(kind, dtype, a, stream), w); });
 }
 
 tr_status tr_global_norm_workspace_bytes(int64_t count, size_t* bytes) {
