@@ -664,12 +664,16 @@ def gated_residual_norm(x, branch, post_weight=None, post_bias=None, gate=None, 
     return y, h
 
 
-def gated_residual_norm_backward_workspace_bytes(rows, cols, kind="rmsnorm"):
+@functools.lru_cache(maxsize=256)
+def _block_workspace_bytes(code, rows, cols):
     n = ctypes.c_size_t(0)
-    code = NORM_KINDS[kind] if isinstance(kind, str) else int(kind)
     _check(load().tr_gated_residual_norm_backward_workspace_bytes(code, rows, cols, ctypes.byref(n)),
            "gated_residual_norm_backward_workspace_bytes")
     return n.value
+
+
+def gated_residual_norm_backward_workspace_bytes(rows, cols, kind="rmsnorm"):
+    return _block_workspace_bytes(NORM_KINDS[kind] if isinstance(kind, str) else int(kind), rows, cols)
 
 
 def gated_residual_norm_backward(h, branch, dy=None, dh=None, post_weight=None, post_bias=None, gate=None, weight=None,
@@ -678,8 +682,7 @@ def gated_residual_norm_backward(h, branch, dy=None, dh=None, post_weight=None, 
     """The gradients of ``gated_residual_norm`` from its h and branch, the gradient dy of
     y (with pre) and dh of h (None: zero). Returns GatedResidualNormGrads: dx, dbranch (the inputs' type),
     dpost_weight, dpost_bias, dgate (the gate's shape), dweight, dbias (float32; None where
-    there is no such norm, bias or gate, or with want_params=False; the vectors lie one after the
-    other in one allocation)."""
+    there is no such norm, bias or gate, or with want_params=False)."""
     import torch
     code, dtype, norms, r, c, index, gp, groups = _block(branch, "branch", gate, kind, post, pre)
     switch = _switch(index, stream)
@@ -696,26 +699,30 @@ def gated_residual_norm_backward(h, branch, dy=None, dh=None, post_weight=None, 
     ppw = ppb = pg = pw = pb = wsp = None
     n = 0
     if want_params:
-        layer = code == TR_NORM_LAYER
-        grads = torch.empty((bool(post) + bool(pre)) * (1 + layer), c, device=branch.device, dtype=torch.float32)
-        rows, p, step = list(grads.unbind(0)), grads.data_ptr(), 4 * c
+        dev, f32, layer = branch.device, torch.float32, code == TR_NORM_LAYER
         if post:
-            dpw, ppw, p = rows.pop(0), p, p + step
+            dpw = torch.empty(c, device=dev, dtype=f32)
+            ppw = dpw.data_ptr()
             if layer:
-                dpb, ppb, p = rows.pop(0), p, p + step
+                dpb = torch.empty(c, device=dev, dtype=f32)
+                ppb = dpb.data_ptr()
         if pre:
-            dw, pw, p = rows.pop(0), p, p + step
+            dw = torch.empty(c, device=dev, dtype=f32)
+            pw = dw.data_ptr()
             if layer:
-                db, pb = rows.pop(0), p
+                db = torch.empty(c, device=dev, dtype=f32)
+                pb = db.data_ptr()
         if gate is not None:
             dg = torch.empty_like(gate)
             pg = dg.data_ptr()
         if workspace is None:
-            n = gated_residual_norm_backward_workspace_bytes(r, c, code)
-            workspace = torch.empty(max(16, n), dtype=torch.uint8, device=branch.device)
-        elif not workspace.is_contiguous() or workspace.get_device() != index:
-            raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
-        wsp, n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+            n = _block_workspace_bytes(code, r, c)
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        else:
+            if not workspace.is_contiguous() or workspace.get_device() != index:
+                raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+            n = workspace.numel() * workspace.element_size()
+        wsp = workspace.data_ptr()
     _check(load().tr_gated_residual_norm_backward(
         code, dtype, norms, _rows_like(h, "h", branch), branch.data_ptr(), _rows_like(dy, "dy", branch),
         _rows_like(dh, "dh", branch), _floats(post_weight, "post_weight", vec, index),
@@ -754,7 +761,10 @@ def _tensor_list(tensors, name, index=None):
         devices.add(index)
     if len(devices) > 1:
         raise ValueError(f"{name} must be on one device")
-    codes = array.array("i", map(_dtype_code, map(_dtype_of, tensors)))
+    try:
+        codes = array.array("i", map(_dtype_codes().__getitem__, map(_dtype_of, tensors)))
+    except KeyError as e:
+        raise TypeError(f"{name} must hold float32, bfloat16 or float16 tensors, got {e.args[0]}") from None
     if not all(map(T.is_contiguous, tensors)) and not all(map(_dense, tensors)):
         raise ValueError(f"{name} must hold dense tensors (no gaps and no repeated elements)")
     index = devices.pop() if devices else torch.cuda.current_device()

@@ -7,8 +7,8 @@
 // With 16-bit types the work per byte is what limits: at 4096 columns a SM has 2090 cycles to
 // the row. So the arithmetic is on pairs (f32x2), which norms there are is known when the kernel is
 // compiled, and there is one exchange between warps a row: the next row's statistics travel with
-// this row's sum of q ah. LayerNorm's squares are taken about the warp's own mean and moved to the
-// row's when the warps meet (Chan, Golub and LeVeque 1979), so it needs no second exchange.
+// this row's sum of q ah. LayerNorm's sums are taken about a shift that each warp finds for itself
+// (lane_mean), so means and variances need no second exchange and no second pass.
 #pragma once
 
 #include "tr_block_rows.cuh"
@@ -17,12 +17,13 @@ namespace tr {
 namespace block {
 
 // MODE: the norms there are, a mask of TR_BLOCK_POST and TR_BLOCK_PRE; 0: as p says.
-template <class T, bool LAYER, int S, bool ODD, bool CLUSTER, int MODE, int THREADS, int CTAS>
+template <class T, bool LAYER, int S, int LAYOUT, bool CLUSTER, int MODE, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p, const RowShape g) {
     constexpr int E = 16 / static_cast<int>(sizeof(T));
     constexpr int P = E / 2;       // pairs of a slot
     constexpr int K = S * P;       // pairs of a thread
     constexpr int V = LAYER ? 4 : 2;
+    constexpr bool ODD = LAYOUT == LAYOUT_ODD;
     const bool pre = MODE ? (MODE & TR_BLOCK_PRE) != 0 : p.pre != 0;
     const bool post = MODE ? (MODE & TR_BLOCK_POST) != 0 : p.post != 0;
     extern __shared__ uint4 smem[];
@@ -32,13 +33,14 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
     const int rank = CLUSTER ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
     const int cols = p.cols;
     const int col0 = rank * g.cta_vecs * E;  // this CTA's first column
-    const Lanes<T, S, ODD> ln(t, tt, cols, col0, g.cta_vecs);
+    const Lanes<T, S, LAYOUT> ln(t, tt, cols, col0, g.cta_vecs);
     const float inv_n = 1.0f / static_cast<float>(cols);
-    Exchange<CLUSTER, 4> ex{reinterpret_cast<float*>(smem) + team * (team_bytes(g) / 4), g.warps * g.cluster,
+    Exchange<CLUSTER, LAYER ? 8 : 4> ex{reinterpret_cast<float*>(smem) + team * (team_bytes(g) / 4), g.warps * g.cluster,
                             rank * g.warps + (t >> 5), team, g.warps};
     const int stage_bytes = g.tensors * g.tensor_bytes;
+    using Start = RowStart<T, ODD>;
+    char* starts = reinterpret_cast<char*>(smem) + team * team_bytes(g) + exchange_bytes(g) + (t >> 5) * g.stages * g.sampled;
     char* ring = reinterpret_cast<char*>(smem) + fixed_bytes(g) + team * g.stages * stage_bytes;
-    if constexpr (LAYER) ex.template count_columns<S, E, ODD>(cols, g.cta_vecs, t);
     if constexpr (CLUSTER) cg::this_cluster().sync();  // every CTA of the cluster runs before it is written to
     pdl_enter();
 
@@ -60,6 +62,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
             }
             if (need_a) ln.fetch(p.a, p.rows, row, to + at_a);
             if (p.dh) ln.fetch(p.dh, p.rows, row, to + at_dh);
+            if constexpr (LAYER) {
+                if (pre) Start::fetch(p.h, row, ln.row_bytes, starts + stage * g.sampled);
+                if (post) Start::fetch(p.a, row, ln.row_bytes, starts + stage * g.sampled + kRowStartBytes);
+            }
         }
         cp_async_commit();
     };
@@ -122,102 +128,87 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
         }
         flushed = true;
     };
-    auto about = [&](float2 v, float m, bool x_in, bool y_in) {  // v - m; 0 outside the row
-        if constexpr (!LAYER) return v;
-        float2 c = __fadd2_rn(v, both(-m));
-        if (!x_in) c.x = 0.0f;
-        if (!y_in) c.y = 0.0f;
-        return c;
-    };
-
     // ---- a row's statistics ----
     float mean_h = 0.0f, mean_a = 0.0f, c1 = 0.0f;  // LayerNorm: means of h, a, u
-    // LayerNorm: the thread's sums of h, a and u
-    auto plain_sums = [&](const char* m, int64_t row, float (&v)[4]) {
-        float2 h2 = both(0.0f), a2 = both(0.0f), u2 = both(0.0f);
+    float rh = 0.0f, ra = 0.0f, k2 = 0.0f;
+    // The statistics of row `row` in `stage` (when it is there: `more`), with the sums of q and q (a - mean) of the
+    // row before, which end in qs and qa for between(). D = dh + r_h (u - c1 - (h - mean) k2) with
+    // k2 = r_h^2 mean(u (h - mean)). rsqrtf is good to 2^-22, as the sums are.
+    auto statistics = [&](int stage, int64_t row, bool more, float& qs, float& qa, auto&& between) {
+        const char* m = ring + stage * stage_bytes;
+        float sh = 0.0f, sa = 0.0f;
+        // sums of squares of h and a, and of u h, u, h and a (all about the shifts)
+        float2 hh = both(0.0f), aa = both(0.0f), uh = both(0.0f), u1 = both(0.0f), h1 = both(0.0f), a1 = both(0.0f);
+        if constexpr (LAYER) {
+            __syncwarp();
+            if (pre && more) sh = lane_mean(Start::get(p.h, row, cols, starts + stage * g.sampled));
+            if (post && more) sa = lane_mean(Start::get(p.a, row, cols, starts + stage * g.sampled + kRowStartBytes));
+        }
+        if (more) {
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            float2 x[P], y[P];
-            if (pre) {
-                ln.load(m, p.h, row, s, x);
-                ln.load(m + at_dy, p.dy, row, s, y);
-#pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    h2 = __fadd2_rn(h2, x[j]);
-                    u2 = __ffma2_rn(y[j], w[s * P + j], u2);
+            for (int s = 0; s < S; ++s) {
+                float2 x[P], y[P];
+                auto shifted = [&](float2 v, float shift, bool xi, bool yi) {
+                    if constexpr (!LAYER) return v;
+                    float2 c = __fadd2_rn(v, both(-shift));
+                    if (!xi) c.x = 0.0f;
+                    if (!yi) c.y = 0.0f;
+                    return c;
+                };
+                if (pre) {
+                    ln.load(m, p.h, row, s, x);
+                    ln.load(m + at_dy, p.dy, row, s, y);
+                    ln.pairs(s, [&](int j, bool xi, bool yi) {
+                        const float2 c = shifted(x[j], sh, xi, yi);
+                        const float2 u = __fmul2_rn(y[j], w[s * P + j]);
+                        hh = __ffma2_rn(c, c, hh);
+                        uh = __ffma2_rn(u, c, uh);
+                        if constexpr (LAYER) {
+                            h1 = __fadd2_rn(h1, c);
+                            u1 = __fadd2_rn(u1, u);
+                        }
+                    });
+                }
+                if (post) {
+                    ln.load(m + at_a, p.a, row, s, x);
+                    ln.pairs(s, [&](int j, bool xi, bool yi) {
+                        const float2 c = shifted(x[j], sa, xi, yi);
+                        aa = __ffma2_rn(c, c, aa);
+                        if constexpr (LAYER) a1 = __fadd2_rn(a1, c);
+                    });
                 }
             }
-            if (post) {
-                ln.load(m + at_a, p.a, row, s, x);
-#pragma unroll
-                for (int j = 0; j < P; ++j) a2 = __fadd2_rn(a2, x[j]);
-            }
         }
-        v[0] = h2.x + h2.y;
-        v[1] = a2.x + a2.y;
-        v[2] = u2.x + u2.y;
-    };
-    // the thread's sums of (h - mh)^2, (a - ma)^2 and u (h - mh)
-    auto square_sums = [&](const char* m, int64_t row, float mh, float ma, float (&v)[4]) {
-        float2 h2 = both(0.0f), a2 = both(0.0f), u2 = both(0.0f);
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            float2 x[P], y[P];
-            if (pre) {
-                ln.load(m, p.h, row, s, x);
-                ln.load(m + at_dy, p.dy, row, s, y);
-                ln.pairs(s, [&](int j, bool xi, bool yi) {
-                    const float2 c = about(x[j], mh, xi, yi);
-                    h2 = __ffma2_rn(c, c, h2);
-                    u2 = __ffma2_rn(__fmul2_rn(y[j], w[s * P + j]), c, u2);
-                });
-            }
-            if (post) {
-                ln.load(m + at_a, p.a, row, s, x);
-                ln.pairs(s, [&](int j, bool xi, bool yi) {
-                    const float2 c = about(x[j], ma, xi, yi);
-                    a2 = __ffma2_rn(c, c, a2);
-                });
-            }
-        }
-        v[0] = h2.x + h2.y;
-        v[1] = a2.x + a2.y;
-        v[2] = u2.x + u2.y;
-    };
-    // The statistics of row `row` staged at m (none when it is not there: `more` is false), with the sums of q
-    // and q (a - mean) of the row before, which end in qs and qa. D = dh + r_h (u - c1 - (h - mean) k2) with
-    // k2 = r_h^2 mean(u (h - mean)). rsqrtf is good to 2^-22, as the sums are.
-    float rh = 0.0f, ra = 0.0f, k2 = 0.0f;
-    auto statistics = [&](const char* m, int64_t row, bool more, float& qs, float& qa, auto&& between) {
-        [[maybe_unused]] float v[4] = {0.0f, 0.0f, 0.0f, qs};
-        float w4[4] = {0.0f, 0.0f, 0.0f, qa};
+        float sq_h, sq_a, sum_uh, next_h = 0.0f, next_a = 0.0f, next_c1 = 0.0f;
         if constexpr (LAYER) {
-            if (more) plain_sums(m, row, v);
-            ex.template moments<2>(
-                v, w4, inv_n,
-                [&](const float (&mean)[2], float (&o)[4]) {
-                    if (more) square_sums(m, row, mean[0], mean[1], o);
-                },
-                [](int i, float n, const float (&d)[2], const float (&sum)[4]) {
-                    return i < 2 ? n * d[i < 2 ? i : 0] * d[i < 2 ? i : 0] : i == 2 ? d[0] * sum[2] : 0.0f;
-                });
-            qs = v[3];
+            float v[8] = {hh.x + hh.y, aa.x + aa.y, uh.x + uh.y, qa, u1.x + u1.y, h1.x + h1.y, a1.x + a1.y, qs};
+            ex.sums(v);
+            qa = v[3];
+            qs = v[7];
+            const float dh = v[5] * inv_n, da = v[6] * inv_n;  // the means, from the shifts
+            sq_h = squares_about_mean(v[0], v[5], dh);
+            sq_a = squares_about_mean(v[1], v[6], da);
+            sum_uh = fmaf(-dh, v[4], v[2]);
+            next_h = sh + dh;
+            next_a = sa + da;
+            next_c1 = v[4] * inv_n;
         } else {
-            if (more) square_sums(m, row, 0.0f, 0.0f, w4);
-            ex.sums(w4);
+            float v[4] = {hh.x + hh.y, aa.x + aa.y, uh.x + uh.y, qa};
+            ex.sums(v);
+            qa = v[3];
+            sq_h = v[0];
+            sq_a = v[1];
+            sum_uh = v[2];
         }
-        qa = w4[3];
         between();
-        if constexpr (LAYER) {
-            mean_h = v[0] * inv_n;
-            mean_a = v[1] * inv_n;
-            c1 = v[2] * inv_n;
-        }
+        mean_h = next_h;
+        mean_a = next_a;
+        c1 = next_c1;
         if (pre) {
-            rh = rsqrtf(fmaf(w4[0], inv_n, p.eps));
-            k2 = w4[2] * inv_n * rh * rh;
+            rh = rsqrtf(fmaf(sq_h, inv_n, p.eps));
+            k2 = sum_uh * inv_n * rh * rh;
         }
-        if (post) ra = rsqrtf(fmaf(w4[1], inv_n, p.eps));
+        if (post) ra = rsqrtf(fmaf(sq_a, inv_n, p.eps));
     };
 
     // ---- the first row ----
@@ -230,7 +221,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
     if constexpr (ODD) odd_barrier();
     {
         float qs = 0.0f, qa = 0.0f;
-        statistics(ring, slab.begin, true, qs, qa, [] {});
+        statistics(0, slab.begin, true, qs, qa, [] {});
     }
 
     int stage = 0, fill = g.stages - 1;
@@ -248,7 +239,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
         fill = fill + 1 == g.stages ? 0 : fill + 1;
         const char* m = ring + stage * stage_bytes;
         stage = stage + 1 == g.stages ? 0 : stage + 1;
-        const char* next = ring + stage * stage_bytes;
+        const bool more = row + 1 < slab.end;
 
         // D, dx, the column sums of the pre-norm, and the sums of q (a - mean) and q
         float2 d[K], av[K];
@@ -298,7 +289,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
         // the next row's statistics travel with this row's sums
         if constexpr (!ODD) ring_wait(g.stages, 2);
         float qs = qs2.x + qs2.y, qa = qa2.x + qa2.y;
-        statistics(next, row + 1, row + 1 < slab.end, qs, qa, [&] {
+        statistics(stage, row + 1, more, qs, qa, [&] {
             // da, and the column sums of the post-norm and the gate
             const float e1 = qs * inv_n, e2 = qa * inv_n * ra * ra;
 #pragma unroll
@@ -351,12 +342,12 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
 
 // ---- host side -------------------------------------------------------------
 
-template <class T, bool LAYER, int S, bool ODD, bool CLUSTER, int MODE, int THREADS, int CTAS>
+template <class T, bool LAYER, int S, int LAYOUT, bool CLUSTER, int MODE, int THREADS, int CTAS>
 cudaError_t bwd_go(const BlockBwArgs& in, const RowShape& g, cudaStream_t stream) {
     BlockBwArgs a = in;
     const int threads = g.teams * g.warps * 32;
     const size_t smem = row_smem(g);
-    const auto kernel = bwd_kernel<T, LAYER, S, ODD, CLUSTER, MODE, THREADS, CTAS>;
+    const auto kernel = bwd_kernel<T, LAYER, S, LAYOUT, CLUSTER, MODE, THREADS, CTAS>;
     const int64_t ctas = resident_ctas(reinterpret_cast<const void*>(kernel), threads, smem, g.cluster);
     if (ctas < 1) return cudaErrorInvalidConfiguration;
     block_slabs(&a, std::min(ctas * g.teams / g.cluster, block_slab_limit(a.rows, a.cols)));
@@ -366,23 +357,27 @@ cudaError_t bwd_go(const BlockBwArgs& in, const RowShape& g, cudaStream_t stream
     return launch_block_finish(LAYER ? TR_NORM_LAYER : TR_NORM_RMS, a, stream);
 }
 
-// Aligned rows of one CTA are compiled for each pair of norms, and for CTAs of at most 320 threads
+// Full rows of one CTA are compiled for each pair of norms, and for CTAs of at most 320 threads
 // with registers for two an SM.
 template <class T, bool LAYER, int S, int MODE>
-cudaError_t bwd_aligned(const BlockBwArgs& a, const RowShape& g, cudaStream_t stream) {
+cudaError_t bwd_full(const BlockBwArgs& a, const RowShape& g, cudaStream_t stream) {
     if constexpr (S == 1) {
-        if (g.teams * g.warps <= 10) return bwd_go<T, LAYER, S, false, false, MODE, 320, 2>(a, g, stream);
+        if (g.teams * g.warps <= 10) return bwd_go<T, LAYER, S, LAYOUT_FULL, false, MODE, 320, 2>(a, g, stream);
     }
-    return bwd_go<T, LAYER, S, false, false, MODE, 512, 1>(a, g, stream);
+    return bwd_go<T, LAYER, S, LAYOUT_FULL, false, MODE, 512, 1>(a, g, stream);
 }
 
 template <class T, bool LAYER, int S>
-cudaError_t bwd_slots(bool odd, const BlockBwArgs& a, const RowShape& g, cudaStream_t stream) {
-    if (g.cluster > 1)
-        return odd ? bwd_go<T, LAYER, S, true, true, 0, 512, 1>(a, g, stream) : bwd_go<T, LAYER, S, false, true, 0, 512, 1>(a, g, stream);
-    if (odd) return bwd_go<T, LAYER, S, true, false, 0, 512, 1>(a, g, stream);
-    if (a.pre && a.post) return bwd_aligned<T, LAYER, S, TR_BLOCK_PRE | TR_BLOCK_POST>(a, g, stream);
-    return a.pre ? bwd_aligned<T, LAYER, S, TR_BLOCK_PRE>(a, g, stream) : bwd_aligned<T, LAYER, S, TR_BLOCK_POST>(a, g, stream);
+cudaError_t bwd_slots(int layout, const BlockBwArgs& a, const RowShape& g, cudaStream_t stream) {
+    if (g.cluster > 1) {
+        if (layout == LAYOUT_FULL) return bwd_go<T, LAYER, S, LAYOUT_FULL, true, 0, 512, 1>(a, g, stream);
+        if (layout == LAYOUT_ALIGNED) return bwd_go<T, LAYER, S, LAYOUT_ALIGNED, true, 0, 512, 1>(a, g, stream);
+        return bwd_go<T, LAYER, S, LAYOUT_ODD, true, 0, 512, 1>(a, g, stream);
+    }
+    if (layout == LAYOUT_ODD) return bwd_go<T, LAYER, S, LAYOUT_ODD, false, 0, 512, 1>(a, g, stream);
+    if (layout == LAYOUT_ALIGNED) return bwd_go<T, LAYER, S, LAYOUT_ALIGNED, false, 0, 512, 1>(a, g, stream);
+    if (a.pre && a.post) return bwd_full<T, LAYER, S, TR_BLOCK_PRE | TR_BLOCK_POST>(a, g, stream);
+    return a.pre ? bwd_full<T, LAYER, S, TR_BLOCK_PRE>(a, g, stream) : bwd_full<T, LAYER, S, TR_BLOCK_POST>(a, g, stream);
 }
 
 template <class T, bool LAYER>
@@ -391,13 +386,14 @@ cudaError_t bwd_kind(const BlockBwArgs& a, bool* done, cudaStream_t stream) {
     const bool odd = !rows_aligned(static_cast<int64_t>(a.cols) * static_cast<int>(sizeof(T)),
                                    {a.pre ? a.h : nullptr, a.pre ? a.dy : nullptr, a.post || a.dgate ? a.a : nullptr, a.dh, a.dx, a.da});
     int slots = 0;
-    const RowShape g = row_shape<T>(a.cols, tensors, odd, 1, &slots);
+    const RowShape g = row_shape<T>(a.cols, tensors, odd, LAYER, 1, &slots);
     *done = g.warps > 0;
     if (!*done) return cudaSuccess;
+    const int layout = odd ? LAYOUT_ODD : row_full<T>(g, a.cols, slots) ? LAYOUT_FULL : LAYOUT_ALIGNED;
     if constexpr (sizeof(T) == 4) {
-        if (slots == 2) return bwd_slots<T, LAYER, 2>(odd, a, g, stream);
+        if (slots == 2) return bwd_slots<T, LAYER, 2>(layout, a, g, stream);
     }
-    return bwd_slots<T, LAYER, 1>(odd, a, g, stream);
+    return bwd_slots<T, LAYER, 1>(layout, a, g, stream);
 }
 
 }  // namespace block

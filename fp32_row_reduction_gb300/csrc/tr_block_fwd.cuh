@@ -2,8 +2,9 @@
 //
 // HBM-bound: x and a are read, h and y written once. A row's y waits for the statistics of h, which
 // wait for those of a; so that a row costs one exchange between its warps, the sum over h of a row
-// travels with the sum over a of the next one. The parameters of a thread's columns stay in its
-// registers for all its rows.
+// travels with the sum over a of the next one. LayerNorm's sums are taken about a shift that each warp
+// finds for itself (lane_mean; for h from the same elements' own x and a). The parameters of a thread's columns
+// stay in its registers for all its rows.
 #pragma once
 
 #include "tr_block_rows.cuh"
@@ -11,11 +12,12 @@
 namespace tr {
 namespace block {
 
-template <class T, bool LAYER, int S, bool ODD, bool CLUSTER>
-__global__ void __launch_bounds__(512, 2) fwd_kernel(const BlockArgs p, const RowShape g, const int64_t slabs) {
+template <class T, bool LAYER, int S, int LAYOUT, bool CLUSTER, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, const RowShape g, const int64_t slabs) {
     constexpr int E = 16 / static_cast<int>(sizeof(T));
     constexpr int P = E / 2;  // pairs of a slot
     constexpr int K = S * P;  // pairs of a thread
+    constexpr bool ODD = LAYOUT == LAYOUT_ODD;
     extern __shared__ uint4 smem[];
     const int tt = g.warps * 32;  // a team's threads in this CTA
     const int team = CLUSTER ? 0 : static_cast<int>(threadIdx.x) / tt;
@@ -23,13 +25,14 @@ __global__ void __launch_bounds__(512, 2) fwd_kernel(const BlockArgs p, const Ro
     const int rank = CLUSTER ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
     const int cols = p.cols;
     const int col0 = rank * g.cta_vecs * E;  // this CTA's first column
-    const Lanes<T, S, ODD> ln(t, tt, cols, col0, g.cta_vecs);
+    const Lanes<T, S, LAYOUT> ln(t, tt, cols, col0, g.cta_vecs);
     const float inv_n = 1.0f / static_cast<float>(cols);
-    Exchange<CLUSTER, 2> ex{reinterpret_cast<float*>(smem) + team * (team_bytes(g) / 4), g.warps * g.cluster,
+    Exchange<CLUSTER, LAYER ? 4 : 2> ex{reinterpret_cast<float*>(smem) + team * (team_bytes(g) / 4), g.warps * g.cluster,
                             rank * g.warps + (t >> 5), team, g.warps};
     const int stage_bytes = g.tensors * g.tensor_bytes;
+    using Start = RowStart<T, ODD>;
+    char* starts = reinterpret_cast<char*>(smem) + team * team_bytes(g) + exchange_bytes(g) + (t >> 5) * g.stages * g.sampled;
     char* ring = reinterpret_cast<char*>(smem) + fixed_bytes(g) + team * g.stages * stage_bytes;
-    if constexpr (LAYER) ex.template count_columns<S, E, ODD>(cols, g.cta_vecs, t);
     if constexpr (CLUSTER) cg::this_cluster().sync();  // every CTA of the cluster runs before it is written to
     pdl_enter();
 
@@ -42,6 +45,10 @@ __global__ void __launch_bounds__(512, 2) fwd_kernel(const BlockArgs p, const Ro
             char* to = ring + stage * stage_bytes;
             ln.fetch(p.a, p.rows, row, to);
             ln.fetch(p.x, p.rows, row, to + g.tensor_bytes);
+            if constexpr (LAYER) {
+                Start::fetch(p.a, row, ln.row_bytes, starts + stage * g.sampled);
+                if (p.pre) Start::fetch(p.x, row, ln.row_bytes, starts + stage * g.sampled + kRowStartBytes);
+            }
         }
         cp_async_commit();
     };
@@ -53,12 +60,18 @@ __global__ void __launch_bounds__(512, 2) fwd_kernel(const BlockArgs p, const Ro
 
     auto at0 = [&](const float* w) { return w ? w + col0 : nullptr; };
     float2 gw[K], w[K];  // bs gate w_post;  the pre-norm's weight
+    float2 gb[LAYER ? K : 1], b[LAYER ? K : 1];  // bs gate b_post;  the pre-norm's bias
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         float2 v[P];
         ln.param(at0(p.pre_w), s, 1.0f, v);
 #pragma unroll
         for (int j = 0; j < P; ++j) w[s * P + j] = v[j];
+        if constexpr (LAYER) {
+            ln.param(at0(p.pre_b), s, 0.0f, v);
+#pragma unroll
+            for (int j = 0; j < P; ++j) b[s * P + j] = v[j];
+        }
     }
     auto gate_row = [&](int64_t row) { return p.gate ? p.gate + row / p.group_rows * cols + col0 : nullptr; };
     auto enter_group = [&](int64_t row) {
@@ -70,88 +83,92 @@ __global__ void __launch_bounds__(512, 2) fwd_kernel(const BlockArgs p, const Ro
             ln.param(gr, s, 1.0f, v);
 #pragma unroll
             for (int j = 0; j < P; ++j) gw[s * P + j] = __fmul2_rn(v[j], __fmul2_rn(both(p.bs), o[j]));
+            if constexpr (LAYER) {
+                ln.param(at0(p.post_b), s, 0.0f, o);
+#pragma unroll
+                for (int j = 0; j < P; ++j) gb[s * P + j] = __fmul2_rn(v[j], __fmul2_rn(both(p.bs), o[j]));
+            }
         }
     };
-    auto about = [&](float2 v, float m, bool x_in, bool y_in) {  // v - m; 0 outside the row
-        if constexpr (!LAYER) return v;
-        float2 c = __fadd2_rn(v, both(-m));
-        if (!x_in) c.x = 0.0f;
-        if (!y_in) c.y = 0.0f;
-        return c;
+    // LayerNorm: the parameters at the lane's element of a row's start: bs gate w_post, bs gate b_post
+    const int probe = static_cast<int>(threadIdx.x & 31) % cols;
+    float probe_w = 1.0f, probe_b = 0.0f;
+    auto enter_probe = [&](int64_t row) {
+        const float gt = p.bs * (p.gate ? __ldg(p.gate + row / p.group_rows * cols + probe) : 1.0f);
+        probe_w = gt * (p.post_w ? __ldg(p.post_w + probe) : 1.0f);
+        probe_b = gt * (p.post_b ? __ldg(p.post_b + probe) : 0.0f);
     };
 
     float2 h[K];
     float ra = 1.0f, ma = 0.0f;  // of the row at work
     float rh = 1.0f, mh = 0.0f;
-    // the sums over h (where `this_row`) and over a of row `row` staged at m (where `next_row`)
-    auto statistics = [&](const char* m, int64_t row, bool this_row, bool next_row) {
-        float q[2] = {0.0f, 0.0f};  // squares of h, of a
-        auto squares = [&](float mean_h, float mean_a, float (&o)[2]) {
-            float2 h2 = both(0.0f), a2 = both(0.0f);
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                if (p.pre && this_row)
-                    ln.pairs(s, [&](int j, bool xi, bool yi) {
-                        const float2 c = about(h[s * P + j], mean_h, xi, yi);
-                        h2 = __ffma2_rn(c, c, h2);
-                    });
-                if (p.post && next_row) {
-                    float2 x[P];
-                    ln.load(m, p.a, row, s, x);
-                    ln.pairs(s, [&](int j, bool xi, bool yi) {
-                        const float2 c = about(x[j], mean_a, xi, yi);
-                        a2 = __ffma2_rn(c, c, a2);
-                    });
-                }
-            }
-            o[0] = h2.x + h2.y;
-            o[1] = a2.x + a2.y;
+    // the sums over h about sh (where `this_row`) and over a of row `row` staged at m about sa (where `next_row`)
+    auto statistics = [&](const char* m, int64_t row, bool this_row, bool next_row, float sh, float sa) {
+        float2 hh = both(0.0f), aa = both(0.0f), h1 = both(0.0f), a1 = both(0.0f);
+        auto shifted = [&](float2 v, float shift, bool xi, bool yi) {
+            if constexpr (!LAYER) return v;
+            float2 c = __fadd2_rn(v, both(-shift));
+            if (!xi) c.x = 0.0f;
+            if (!yi) c.y = 0.0f;
+            return c;
         };
-        float v[2] = {0.0f, 0.0f};
-        if constexpr (LAYER) {
-            float2 h2 = both(0.0f), a2 = both(0.0f);
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                if (p.pre && this_row)
-#pragma unroll
-                    for (int j = 0; j < P; ++j) h2 = __fadd2_rn(h2, h[s * P + j]);
-                if (p.post && next_row) {
-                    float2 x[P];
-                    ln.load(m, p.a, row, s, x);
-#pragma unroll
-                    for (int j = 0; j < P; ++j) a2 = __fadd2_rn(a2, x[j]);
-                }
+        for (int s = 0; s < S; ++s) {
+            if (p.pre && this_row)
+                ln.pairs(s, [&](int j, bool xi, bool yi) {
+                    const float2 c = shifted(h[s * P + j], sh, xi, yi);
+                    hh = __ffma2_rn(c, c, hh);
+                    if constexpr (LAYER) h1 = __fadd2_rn(h1, c);
+                });
+            if (p.post && next_row) {
+                float2 x[P];
+                ln.load(m, p.a, row, s, x);
+                ln.pairs(s, [&](int j, bool xi, bool yi) {
+                    const float2 c = shifted(x[j], sa, xi, yi);
+                    aa = __ffma2_rn(c, c, aa);
+                    if constexpr (LAYER) a1 = __fadd2_rn(a1, c);
+                });
             }
-            v[0] = h2.x + h2.y;
-            v[1] = a2.x + a2.y;
-            ex.template moments<2>(
-                v, q, inv_n, [&](const float (&mean)[2], float (&o)[2]) { squares(mean[0], mean[1], o); },
-                [](int i, float n, const float (&d)[2], const float (&)[2]) { return n * d[i] * d[i]; });
+        }
+        float sq_h, sq_a;
+        if constexpr (LAYER) {
+            float v[4] = {hh.x + hh.y, aa.x + aa.y, h1.x + h1.y, a1.x + a1.y};
+            ex.sums(v);
+            const float dh = v[2] * inv_n, da = v[3] * inv_n;  // the means, from the shifts
+            sq_h = squares_about_mean(v[0], v[2], dh);
+            sq_a = squares_about_mean(v[1], v[3], da);
+            mh = sh + dh;
+            if (p.post) ma = sa + da;
         } else {
-            squares(0.0f, 0.0f, q);
-            ex.sums(q);
+            float v[2] = {hh.x + hh.y, aa.x + aa.y};
+            ex.sums(v);
+            sq_h = v[0];
+            sq_a = v[1];
         }
         // rsqrtf is good to 2^-22, as the sums are
-        rh = rsqrtf(fmaf(q[0], inv_n, p.eps));
-        if (p.post) ra = rsqrtf(fmaf(q[1], inv_n, p.eps));
-        if constexpr (LAYER) {
-            mh = v[0] * inv_n;
-            if (p.post) ma = v[1] * inv_n;
-        }
+        rh = rsqrtf(fmaf(sq_h, inv_n, p.eps));
+        if (p.post) ra = rsqrtf(fmaf(sq_a, inv_n, p.eps));
     };
 
     int64_t left = 0;  // rows of the running gate row still to come
     if (begin < end) {
         enter_group(begin);
+        if constexpr (LAYER) enter_probe(begin);
         left = p.group_rows - begin % p.group_rows;
     }
     ring_wait(g.stages, 2);
     if constexpr (ODD) odd_barrier();
-    if (p.post) statistics(ring, begin, false, begin < end);
+    float a_here = 0.0f;  // LayerNorm: the lane's element of a
+    if constexpr (LAYER) {
+        __syncwarp();
+        a_here = Start::get(p.a, begin, cols, starts);
+    }
+    if (p.post) statistics(ring, begin, false, true, 0.0f, LAYER ? lane_mean(a_here) : 0.0f);
     int stage = 0, fill = g.stages - 1;
     for (int64_t row = begin; row < end; ++row) {
         if (left == 0) {
             enter_group(row);
+            if constexpr (LAYER) enter_probe(row);
             left = p.group_rows;
         }
         --left;
@@ -161,56 +178,53 @@ __global__ void __launch_bounds__(512, 2) fwd_kernel(const BlockArgs p, const Ro
         }
         fetch(row + g.stages - 1, fill);
         fill = fill + 1 == g.stages ? 0 : fill + 1;
+        [[maybe_unused]] const int here = stage;
         const char* m = ring + stage * stage_bytes;
         stage = stage + 1 == g.stages ? 0 : stage + 1;
         const char* next = ring + stage * stage_bytes;
+        const bool more = row + 1 < end;
+        float h_here = 0.0f;
+        if constexpr (LAYER) {
+            if (p.pre) {
+                const float x_here = Start::get(p.x, row, cols, starts + here * g.sampled + kRowStartBytes);
+                h_here = fmaf((a_here - ma) * ra, probe_w, fmaf(p.rs, x_here, probe_b));
+            }
+        }
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             float2 x[P], v[P];
             ln.load(m, p.a, row, s, v);
             ln.load(m + g.tensor_bytes, p.x, row, s, x);
-            float2 b[LAYER ? P : 1], gt[LAYER ? P : 1];
-            if constexpr (LAYER) {
-                // bs gate b_post: read where there is a bias
-                if (p.post_b) {
-                    ln.param(at0(p.post_b), s, 0.0f, b);
-                    ln.param(gate_row(row), s, 1.0f, gt);
-#pragma unroll
-                    for (int j = 0; j < P; ++j) x[j] = __ffma2_rn(both(p.rs), x[j], __fmul2_rn(__fmul2_rn(both(p.bs), gt[j]), b[j]));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < P; ++j) x[j] = __fmul2_rn(both(p.rs), x[j]);
-                }
-            }
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 const int k = s * P + j;
                 const float2 c = LAYER ? __fadd2_rn(v[j], both(-ma)) : v[j];
                 const float2 n = __fmul2_rn(c, both(ra));
-                h[k] = LAYER ? __ffma2_rn(n, gw[k], x[j]) : __ffma2_rn(n, gw[k], __fmul2_rn(both(p.rs), x[j]));
-                if constexpr (!ODD) {
-                    if (!ln.in(s, 0)) h[k] = both(0.0f);
-                } else {
-                    if (!ln.in(s, 2 * j)) h[k].x = 0.0f;
-                    if (!ln.in(s, 2 * j + 1)) h[k].y = 0.0f;
-                }
+                h[k] = __ffma2_rn(n, gw[k], LAYER ? __ffma2_rn(both(p.rs), x[j], gb[LAYER ? k : 0]) : __fmul2_rn(both(p.rs), x[j]));
+                if (!ln.in(s, 2 * j)) h[k].x = 0.0f;
+                if (!ln.in(s, 2 * j + 1)) h[k].y = 0.0f;
                 v[j] = h[k];
             }
             if (p.h) ln.store(p.h, row, s, v);
         }
         if constexpr (!ODD) ring_wait(g.stages, 2);
-        statistics(next, row + 1, true, row + 1 < end);
+        float a_next = 0.0f;
+        if constexpr (LAYER) {
+            __syncwarp();
+            if (more) a_next = Start::get(p.a, row + 1, cols, starts + stage * g.sampled);
+        }
+        statistics(next, row + 1, true, more, LAYER ? lane_mean(h_here) : 0.0f, LAYER ? lane_mean(a_next) : 0.0f);
+        a_here = a_next;
         if (p.pre) {
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                float2 o[P], b[P];
-                if constexpr (LAYER) ln.param(at0(p.pre_b), s, 0.0f, b);
+                float2 o[P];
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
                     const int k = s * P + j;
                     const float2 c = LAYER ? __fadd2_rn(h[k], both(-mh)) : h[k];
                     const float2 n = __fmul2_rn(c, both(rh));
-                    o[j] = LAYER ? __ffma2_rn(n, w[k], b[j]) : __fmul2_rn(n, w[k]);
+                    o[j] = LAYER ? __ffma2_rn(n, w[k], b[LAYER ? k : 0]) : __fmul2_rn(n, w[k]);
                 }
                 ln.store(p.y, row, s, o);
             }
@@ -221,11 +235,11 @@ __global__ void __launch_bounds__(512, 2) fwd_kernel(const BlockArgs p, const Ro
 
 // ---- host side -------------------------------------------------------------
 
-template <class T, bool LAYER, int S, bool ODD, bool CLUSTER>
-cudaError_t fwd_go(const BlockArgs& a, const RowShape& g, cudaStream_t stream) {
+template <class T, bool LAYER, int S, int LAYOUT, bool CLUSTER, int THREADS, int CTAS>
+cudaError_t fwd_go_with(const BlockArgs& a, const RowShape& g, cudaStream_t stream) {
     const int threads = g.teams * g.warps * 32;
     const size_t smem = row_smem(g);
-    const auto kernel = fwd_kernel<T, LAYER, S, ODD, CLUSTER>;
+    const auto kernel = fwd_kernel<T, LAYER, S, LAYOUT, CLUSTER, THREADS, CTAS>;
     const int64_t ctas = resident_ctas(reinterpret_cast<const void*>(kernel), threads, smem, g.cluster);
     if (ctas < 1) return cudaErrorInvalidConfiguration;
     const int64_t slabs = std::min(a.rows, ctas * g.teams / g.cluster);
@@ -233,23 +247,43 @@ cudaError_t fwd_go(const BlockArgs& a, const RowShape& g, cudaStream_t stream) {
     return launch_dependent(kernel, dim3(grid), threads, smem, g.cluster, stream, a, g, slabs);
 }
 
+// 64 registers are enough for RMSNorm's rows (1024 threads an SM); LayerNorm's biases take more, so CTAs of at
+// most 320 threads are compiled for two an SM, and larger ones run one.
+template <class T, bool LAYER, int S, int LAYOUT, bool CLUSTER>
+cudaError_t fwd_go(const BlockArgs& a, const RowShape& g, cudaStream_t stream) {
+    if constexpr (!LAYER) {
+        return fwd_go_with<T, LAYER, S, LAYOUT, CLUSTER, 512, 2>(a, g, stream);
+    } else {
+        if constexpr (!CLUSTER && S == 1 && LAYOUT == LAYOUT_FULL)
+            if (g.teams * g.warps <= 10) return fwd_go_with<T, LAYER, S, LAYOUT, CLUSTER, 320, 2>(a, g, stream);
+        return fwd_go_with<T, LAYER, S, LAYOUT, CLUSTER, 512, 1>(a, g, stream);
+    }
+}
+
+template <class T, bool LAYER, int S, bool CLUSTER>
+cudaError_t fwd_layout(int layout, const BlockArgs& a, const RowShape& g, cudaStream_t stream) {
+    if (layout == LAYOUT_FULL) return fwd_go<T, LAYER, S, LAYOUT_FULL, CLUSTER>(a, g, stream);
+    if (layout == LAYOUT_ALIGNED) return fwd_go<T, LAYER, S, LAYOUT_ALIGNED, CLUSTER>(a, g, stream);
+    return fwd_go<T, LAYER, S, LAYOUT_ODD, CLUSTER>(a, g, stream);
+}
+
 template <class T, bool LAYER, int S>
-cudaError_t fwd_slots(bool odd, const BlockArgs& a, const RowShape& g, cudaStream_t stream) {
-    if (g.cluster > 1) return odd ? fwd_go<T, LAYER, S, true, true>(a, g, stream) : fwd_go<T, LAYER, S, false, true>(a, g, stream);
-    return odd ? fwd_go<T, LAYER, S, true, false>(a, g, stream) : fwd_go<T, LAYER, S, false, false>(a, g, stream);
+cudaError_t fwd_slots(int layout, const BlockArgs& a, const RowShape& g, cudaStream_t stream) {
+    return g.cluster > 1 ? fwd_layout<T, LAYER, S, true>(layout, a, g, stream) : fwd_layout<T, LAYER, S, false>(layout, a, g, stream);
 }
 
 template <class T, bool LAYER>
 cudaError_t fwd_kind(const BlockArgs& a, bool* done, cudaStream_t stream) {
     const bool odd = !rows_aligned(static_cast<int64_t>(a.cols) * static_cast<int>(sizeof(T)), {a.x, a.a, a.h, a.y});
     int slots = 0;
-    const RowShape g = row_shape<T>(a.cols, 2, odd, 2, &slots);
+    const RowShape g = row_shape<T>(a.cols, 2, odd, LAYER, 2, &slots);
     *done = g.warps > 0;
     if (!*done) return cudaSuccess;
+    const int layout = odd ? LAYOUT_ODD : row_full<T>(g, a.cols, slots) ? LAYOUT_FULL : LAYOUT_ALIGNED;
     if constexpr (sizeof(T) == 4) {
-        if (slots == 2) return fwd_slots<T, LAYER, 2>(odd, a, g, stream);
+        if (slots == 2) return fwd_slots<T, LAYER, 2>(layout, a, g, stream);
     }
-    return fwd_slots<T, LAYER, 1>(odd, a, g, stream);
+    return fwd_slots<T, LAYER, 1>(layout, a, g, stream);
 }
 
 }  // namespace block

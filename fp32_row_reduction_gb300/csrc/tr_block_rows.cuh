@@ -34,11 +34,13 @@ struct RowShape {
     int stages;        // of a team's ring, 3 or 4: two rows are at work, the others on their way
     int tensors;       // matrices read
     int tensor_bytes;  // shared memory of one matrix's row
+    int sampled;       // bytes of a stage that each warp keeps for itself (LayerNorm's shifts; see RowStart)
 };
 
-// Shared memory of a team's exchanges (up to four values): for each warp of a row two halves of 8 floats, its
-// columns and their reciprocal; of all teams; and of the whole CTA.
-__host__ __device__ inline int team_bytes(const RowShape& g) { return (2 * 8 + 2) * 4 * g.warps * g.cluster; }
+// Shared memory of a team's exchanges (up to eight values: two halves of 8 floats for each warp of a row) and row
+// starts; of all teams; and of the whole CTA.
+__host__ __device__ inline int exchange_bytes(const RowShape& g) { return 2 * 8 * 4 * g.warps * g.cluster; }
+__host__ __device__ inline int team_bytes(const RowShape& g) { return exchange_bytes(g) + g.warps * g.stages * g.sampled; }
 __host__ __device__ inline int fixed_bytes(const RowShape& g) { return (g.teams * team_bytes(g) + 127) / 128 * 128; }
 inline int row_smem(const RowShape& g) { return fixed_bytes(g) + g.teams * g.stages * g.tensors * g.tensor_bytes; }
 
@@ -71,125 +73,98 @@ __device__ __forceinline__ float halving_sums(const float (&v)[N], int lane) {
     }
 }
 
-// One team's exchange: N (2 or 4) sums over all warps of a row.
+// One team's exchange: N (2, 4 or 8) sums over all warps of a row.
 template <bool CLUSTER, int N>
 struct Exchange {
     static constexpr int kLanes = 32 / N;  // lanes of a warp that end with the same value
-    float* slot;   // this CTA's: 2 x 2 N x entries floats, then the entries' column counts
+    float* slot;   // this CTA's: 2 x N x entries floats; the halves alternate
     int entries;   // warps of the row
     int entry;     // this warp's place among them
     int team, warps;
     int buf = 0;
 
-    // this warp's value i (held by lanes kLanes i ..) into place `at + i` of its entry, in every CTA
-    __device__ __forceinline__ void put(float r, int at, int stride) {
-        const int lane = threadIdx.x & 31, l = lane % kLanes;
-        float* s = slot + buf * 2 * N * entries + entry * stride + at + lane / kLanes;
-        if constexpr (CLUSTER) {  // the lanes of a value (8 or more) store it to a CTA each
-            cg::cluster_group cl = cg::this_cluster();
-            if (l < static_cast<int>(cl.num_blocks())) *cl.map_shared_rank(s, l) = r;
-        } else {
-            if (l == 0) *s = r;
-        }
-    }
-    __device__ __forceinline__ const float* meet() {
-        if constexpr (CLUSTER) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-        else team_barrier(team, warps);
-        const float* s = slot + buf * 2 * N * entries;
-        buf ^= 1;  // (the other half is free: every warp has read it before it came to this barrier)
-        return s;
-    }
     static __device__ __forceinline__ void spread(float r, float (&v)[N]) {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = __shfl_sync(kFull, r, kLanes * i);
-    }
-    // f(entry) for this lane's entries: `per` lanes take one each at a time (a CTA's warps are at most 16)
-    template <class F>
-    __device__ __forceinline__ void each(int first, int per, F&& f) const {
-        if constexpr (CLUSTER) {
-            for (int e = first; e < entries; e += per) f(e);
-        } else {
-            if (first < entries) f(first);
-        }
     }
 
     // v summed over the row
     __device__ __forceinline__ void sums(float (&v)[N]) {
         const int lane = threadIdx.x & 31;
-        float r = halving_sums<N, 16>(v, lane);
+        const float r = halving_sums<N, 16>(v, lane);  // value i in lanes kLanes i ..
         if (!CLUSTER && entries == 1) return spread(r, v);
-        put(r, 0, N);
-        const float* s = meet() + (lane >> 4) * (N / 2);
-        float t[N / 2] = {};  // half the values a lane
-        each(lane & 15, 16, [&](int e) {
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) t[i] += s[e * N + i];
-        });
+        float* s = slot + buf * N * entries;
+        buf ^= 1;  // (the half this call writes is free: every warp read it before the last barrier)
+        float* mine = s + entry * N + lane / kLanes;
+        if constexpr (CLUSTER) {  // the lanes of a value store it to the CTAs in turn
+            cg::cluster_group cl = cg::this_cluster();
+            const int ctas = static_cast<int>(cl.num_blocks());
+            for (int c = lane % kLanes; c < ctas; c += kLanes) *cl.map_shared_rank(mine, c) = r;
+            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        } else {
+            if (lane % kLanes == 0) *mine = r;
+            team_barrier(team, warps);
+        }
+        // 16 entries at a time, half the values a lane
+        float t[N / 2] = {};
+        auto take = [&](int e) {
+            const float* q = s + e * N + (lane >> 4) * (N / 2);
+            if constexpr (N == 8) {
+                const float4 f = *reinterpret_cast<const float4*>(q);
+                t[0] += f.x;
+                t[1] += f.y;
+                t[2 % (N / 2)] += f.z;
+                t[3 % (N / 2)] += f.w;
+            } else if constexpr (N == 4) {
+                const float2 f = *reinterpret_cast<const float2*>(q);
+                t[0] += f.x;
+                t[1 % (N / 2)] += f.y;
+            } else {
+                t[0] += *q;
+            }
+        };
+        if constexpr (CLUSTER) {
+            for (int e = lane & 15; e < entries; e += 16) take(e);
+        } else {
+            if ((lane & 15) < entries) take(lane & 15);
+        }
         spread(halving_sums<N / 2, 8>(t, lane), v);
     }
+};
 
-    // LayerNorm's sums. v: the thread's plain sums; about(means, w): given the warp's own means of the first
-    // CENTRED values, the thread's sums w of squares and products about them. At the end v holds the row's
-    // sums. w[i] are moved from the warps' means to the row's by shift(i, n, d, sums): what value i of an entry
-    // of n columns gains when its means are d from the row's.
-    template <int CENTRED, class A, class S>
-    __device__ __forceinline__ void moments(float (&v)[N], float (&w)[N], float inv_n, A&& about, S&& shift) {
-        const int lane = threadIdx.x & 31;
-        const float* counts = slot + 4 * N * entries;  // columns, and their reciprocals
-        const float r = halving_sums<N, 16>(v, lane);
-        float m[CENTRED];
-        const float inv = counts[entries + entry];
+// A shift for a row's LayerNorm sums: the mean of its first 32 elements, which every warp of the row finds
+// alike. Sums are taken about it in one pass, and the variance is S2 / n - (S1 / n)^2; the cancellation
+// costs 1 + (shift - mean)^2 / variance of precision: 1 + 1/32 for independent elements, and at worst 1 + n / 32 (all of
+// the row's spread in the 32).
+__device__ __forceinline__ float lane_mean(float v) {
 #pragma unroll
-        for (int i = 0; i < CENTRED; ++i) m[i] = __shfl_sync(kFull, r, kLanes * i) * inv;
-        about(m, w);
-        const float rw = halving_sums<N, 16>(w, lane);
-        if (!CLUSTER && entries == 1) {
-            spread(r, v);
-            spread(rw, w);
-            return;
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v * (1.0f / 32.0f);
+}
+// The sum of squares about the mean, from the sums s2 of squares and s1 about a shift that is d off the mean. A
+// rounding below zero counts as zero; what is infinite or no number stays so.
+__device__ __forceinline__ float squares_about_mean(float s2, float s1, float d) {
+    return fabsf(s2) <= 3.0e38f ? fmaxf(fmaf(-d, s1, s2), 0.0f) : s2;
+}
+// A warp's own copy of a row's first 32 elements, which come with the row: loading them when they are
+// needed would wait for the saturated memory (twice the time of the whole kernel), and another warp's
+// copy could only be read after a barrier.
+constexpr int kRowStartBytes = 128;
+template <class T, bool ODD>
+struct RowStart {
+    static __device__ __forceinline__ void fetch(const void* matrix, int64_t row, int64_t row_bytes, char* to) {
+        if constexpr (!ODD) {
+            const int lane = threadIdx.x & 31;
+            const int n = static_cast<int>(min(static_cast<int64_t>(32 * sizeof(T)), row_bytes)) >> 4;
+            if (lane < n) cp_async16(smem_addr(to) + lane * 16, static_cast<const char*>(matrix) + (row * row_bytes + lane * 16));
         }
-        put(r, 0, 2 * N);
-        put(rw, N, 2 * N);
-        const float* s = meet();
-        float q[N] = {}, t[N] = {};
-        each(lane, 32, [&](int e) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                q[i] = s[e * 2 * N + i];
-                t[i] += q[i];
-            }
-        });
-        spread(halving_sums<N, 16>(t, lane), v);
-#pragma unroll
-        for (int i = 0; i < N; ++i) t[i] = 0.0f;
-        each(lane, 32, [&](int e) {
-            if constexpr (CLUSTER)
-#pragma unroll
-                for (int i = 0; i < N; ++i) q[i] = s[e * 2 * N + i];
-            const float n = counts[e], rn = counts[entries + e];
-            float d[CENTRED];
-#pragma unroll
-            for (int i = 0; i < CENTRED; ++i) d[i] = fmaf(q[i], rn, -v[i] * inv_n);
-#pragma unroll
-            for (int i = 0; i < N; ++i) t[i] += s[e * 2 * N + N + i] + shift(i, n, d, q);
-        });
-        spread(halving_sums<N, 16>(t, lane), w);
     }
-    // The entries' column counts for moments().
-    template <int S, int E, bool ODD>
-    __device__ __forceinline__ void count_columns(int cols, int cta_vecs, int t) {
-        float* counts = slot + 4 * N * entries;
-        for (int e = t; e < entries; e += warps * 32) {
-            const int there = min(cols - e / warps * cta_vecs * E, cta_vecs * E);
-            int n = 0;
-            for (int k = 0; k < (ODD ? S * E : S); ++k) {
-                const int left = (ODD ? there : there / E) - (e % warps * 32 + warps * 32 * k);
-                n += max(0, min(32, left)) * (ODD ? 1 : E);
-            }
-            counts[e] = static_cast<float>(n);  // (0: a warp past the end of the row's last part)
-            counts[entries + e] = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
-        }
-        team_barrier(team, warps);
+    // this lane's element (rows shorter than 32 are gone over again); after the row's copies and __syncwarp()
+    static __device__ __forceinline__ float get(const void* matrix, int64_t row, int cols, const char* from) {
+        const int lane = static_cast<int>(threadIdx.x & 31);
+        const int c = cols < 32 ? lane % cols : lane;
+        if constexpr (ODD) return to_float(static_cast<const T*>(matrix)[row * cols + c]);
+        return to_float(reinterpret_cast<const T*>(from)[c]);
     }
 };
 
@@ -210,10 +185,14 @@ __device__ __forceinline__ uint32_t bits_of(float2 v, __half) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// A thread's share of a row, in one of the two layouts. `mine` columns of the row, from byte `base`
-// on, belong to this CTA.
-template <class T, int S, bool ODD>
+// How a row lies over the threads: aligned with all slots of all threads in the row (no test is left in the
+// inner loops, which are short of issue slots), aligned, or in the odd layout.
+enum Layout : int { LAYOUT_FULL, LAYOUT_ALIGNED, LAYOUT_ODD };
+
+// A thread's share of a row. `mine` columns of the row, from byte `base` on, belong to this CTA.
+template <class T, int S, int LAYOUT>
 struct Lanes {
+    static constexpr bool ODD = LAYOUT == LAYOUT_ODD, FULL = LAYOUT == LAYOUT_FULL;
     static constexpr int E = 16 / static_cast<int>(sizeof(T));  // elements of a slot
     static constexpr int P = E / 2;                             // pairs
     int t, tt;   // thread of the team, and its threads
@@ -227,7 +206,7 @@ struct Lanes {
 
     // column (of this CTA) of element e of slot s, and whether it is in the row
     __device__ __forceinline__ int column(int s, int e) const { return ODD ? t + tt * (s * E + e) : (t + tt * s) * E + e; }
-    __device__ __forceinline__ bool in(int s, int e) const { return ODD ? column(s, e) < mine : t + tt * s < vecs; }
+    __device__ __forceinline__ bool in(int s, int e) const { return FULL || (ODD ? column(s, e) < mine : t + tt * s < vecs); }
     // f(pair, are its elements in the row) for the pairs of slot s that are (in part) in the row
     template <class F>
     __device__ __forceinline__ void pairs(int s, F&& f) const {
@@ -248,7 +227,7 @@ struct Lanes {
 #pragma unroll
             for (int s = 0; s < S; ++s) {
                 const int k = t + tt * s;
-                if (k < vecs) cp_async16(smem_addr(to) + k * 16, from + k * 16);
+                if (FULL || k < vecs) cp_async16(smem_addr(to) + k * 16, from + k * 16);
             }
         } else {
             const int phase = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15);
@@ -272,7 +251,7 @@ struct Lanes {
     __device__ __forceinline__ void load(const char* m, const void* matrix, int64_t row, int s, float2 (&v)[P]) const {
         if constexpr (!ODD) {
             uint4 q = make_uint4(0, 0, 0, 0);
-            if (t + tt * s < vecs) q = *reinterpret_cast<const uint4*>(m + (t + tt * s) * 16);
+            if (FULL || t + tt * s < vecs) q = *reinterpret_cast<const uint4*>(m + (t + tt * s) * 16);
             if constexpr (sizeof(T) == 4) {
                 v[0] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
                 v[1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
@@ -295,7 +274,7 @@ struct Lanes {
     __device__ __forceinline__ void store(void* out, int64_t row, int s, const float2 (&v)[P]) const {
         char* to = static_cast<char*>(out) + (row * row_bytes + base);
         if constexpr (!ODD) {
-            if (t + tt * s < vecs) {
+            if (FULL || t + tt * s < vecs) {
                 uint4 q;
                 if constexpr (sizeof(T) == 4) {
                     q = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
@@ -319,7 +298,7 @@ struct Lanes {
         for (int j = 0; j < P; ++j) v[j] = both(absent);
         if (!w) return;
         if (!ODD && aligned16(w)) {
-            if (t + tt * s < vecs)
+            if (FULL || t + tt * s < vecs)
 #pragma unroll
                 for (int j = 0; j < P; j += 2) {
                     const float4 q = ld_param4(w + column(s, 2 * j));
@@ -342,7 +321,7 @@ struct Lanes {
 // a thread at most, the fewest CTAs a row that this allows with three stages of ring (four where
 // they leave `ctas` CTAs an SM), and several teams in a CTA for short rows.
 template <class T>
-RowShape row_shape(int cols, int tensors, bool odd, int ctas, int* slots) {
+RowShape row_shape(int cols, int tensors, bool odd, bool layer, int ctas, int* slots) {
     constexpr int E = 16 / static_cast<int>(sizeof(T));
     constexpr int kMaxSlots = 8 / E;
     constexpr int kLimit = 226 * 1024;
@@ -357,12 +336,19 @@ RowShape row_shape(int cols, int tensors, bool odd, int ctas, int* slots) {
         g.teams = g.cluster > 1 ? 1 : std::max(1, 8 / g.warps);
         g.tensors = tensors;
         g.tensor_bytes = g.cta_vecs * 16 + (odd ? 16 : 0);
+        g.sampled = layer && !odd ? 2 * kRowStartBytes : 0;
         g.stages = 4;
         if (ctas * (row_smem(g) + 1024) > kLimit) g.stages = 3;
         if (row_smem(g) <= kLimit) return g;
     }
     g.warps = 0;
     return g;
+}
+
+// Whether all of a row's slots are in the row: every CTA has the same, and a team's threads all have theirs.
+template <class T>
+bool row_full(const RowShape& g, int cols, int slots) {
+    return g.cta_vecs == g.warps * 32 * slots && static_cast<int64_t>(g.cta_vecs) * g.cluster * (16 / static_cast<int>(sizeof(T))) == cols;
 }
 
 // Whether every row of these matrices starts and ends on 16 bytes.
