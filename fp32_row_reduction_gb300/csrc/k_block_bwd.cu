@@ -183,96 +183,125 @@ __global__ void __launch_bounds__(kTile * 8) bwd_columns_kernel(const BlockBwArg
 
 // ---- the slabs' partials to the column gradients --------------------------------
 
-// A CTA of 1024 threads takes TILE columns, 1024 / TILE slabs at a time; TILE is chosen so that the
-// columns make about as many CTAs as there are SMs (short rows have few columns and many slabs). The
-// partials are read from L2, so what counts is how many loads are under way: four slabs' a thread.
-// With slices the threads of a column first share out the groups, `per` (a power of two) to each.
+// A CTA of 1024 threads takes TILE columns, 1024 / TILE slabs at a time (TILE 8, one sector, for short rows, whose
+// columns are few and slabs many). The partials come from L2 and latency is all there is: eight slabs' loads are
+// under way at once, and the threads of a column meet twice, not in a tree of barriers.
 constexpr int kFinishThreads = 1024;
 
-// v: a column's sums of slabs first, first + step, ... < end, of the vectors in the mask `want`.
-template <int V>
-__device__ __forceinline__ void slab_sums(const float* part, int cols, int64_t first, int64_t end, int64_t step,
-                                          unsigned want, float (&v)[V]) {
+// v[i] += a column's sum of vector vecs[i] of slabs first, first + step, ... < end.
+template <int N>
+__device__ __forceinline__ void slab_sums(const float* part, int64_t slab_floats, const int64_t (&at)[N], int64_t first,
+                                          int64_t end, int64_t step, float (&v)[N]) {
+    for (int64_t s = first; s < end; s += 8 * step) {
+        float q[8][N];
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = 0.0f;
-    int64_t s = first;
-    for (; s + 3 * step < end; s += 4 * step) {
-        float q[4][V];
+        for (int u = 0; u < 8; ++u)
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+            for (int i = 0; i < N; ++i) q[u][i] = s + u * step < end ? part[(s + u * step) * slab_floats + at[i]] : 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) q[u][i] = (want >> i) & 1 ? part[((s + u * step) * V + i) * cols] : 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] += (q[0][i] + q[1][i]) + (q[2][i] + q[3][i]);
+        for (int i = 0; i < N; ++i)
+            v[i] += ((q[0][i] + q[1][i]) + (q[2][i] + q[3][i])) + ((q[4][i] + q[5][i]) + (q[6][i] + q[7][i]));
     }
-    for (; s < end; s += step)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if ((want >> i) & 1) v[i] += part[(s * V + i) * cols];
 }
 
 template <bool LAYER, int TILE>
 __global__ void __launch_bounds__(kFinishThreads) bwd_finish_kernel(const BlockBwArgs p) {
     constexpr int V = LAYER ? 4 : 2;
+    constexpr int H = V / 2;  // vectors of a norm: dy hh, dy (pre); D ah, D (post)
     constexpr int SUBS = kFinishThreads / TILE;
-    __shared__ float red[V][SUBS][TILE];
-    pdl_enter();
-    const int lane = static_cast<int>(threadIdx.x) % TILE, sub = static_cast<int>(threadIdx.x) / TILE;
+    constexpr int PAD = TILE + 1;
+    __shared__ float red[V][SUBS * PAD];
+    __shared__ float sum[V][TILE];
+    const int tid = static_cast<int>(threadIdx.x), lane = tid % TILE, sub = tid / TILE;
     const int cols = p.cols;
     const int c = static_cast<int>(blockIdx.x) * TILE + lane;
     const bool ok = c < cols;
+    const int64_t slab_floats = static_cast<int64_t>(V) * cols;
     const float* part = p.part + (ok ? c : 0);
-    // v[i] over the `per` threads from each multiple of `per` on, for the first of them
-    auto tree = [&](float (&v)[V], int per) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < V; ++i) red[i][sub][lane] = v[i];
-        for (int o = per / 2; o >= 1; o >>= 1) {
-            __syncthreads();
-            if (sub % per < o)
-#pragma unroll
-                for (int i = 0; i < V; ++i) red[i][sub][lane] += red[i][sub + o][lane];
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = red[i][sub][lane];
-    };
+    // (inputs, not results of the kernel before: they may be read while it ends)
+    const float ow = ok && p.post && p.post_w ? __ldg(p.post_w + c) : 1.0f;
+    const float ob = ok && p.post && p.post_b ? __ldg(p.post_b + c) : 0.0f;
     const bool need_a = p.post || p.dgate;
-    const bool sliced = need_a && p.slices > 0;  // the second vectors are sums of single gate rows
-    // vectors 0 and 2 (dy hh, dy), and 1 and 3 where they are the slab's own
-    const unsigned own = (p.pre ? 5u : 0u) | (need_a && !sliced ? 10u : 0u);
-    float v[V];
-    slab_sums<V>(part, cols, sub, p.slabs, SUBS, own, v);
-    const float ow = ok && p.post && p.post_w ? p.post_w[c] : 1.0f;
-    const float ob = ok && p.post && p.post_b ? p.post_b[c] : 0.0f;
-    if (sliced) {
+    const bool single = p.groups == 1;              // one gate row: its sums are the columns' own
+    const bool grouped = p.slices > 0 && !single;  // several gate rows of several slabs each
+    const float g0 = ok && p.gate && single ? __ldg(p.gate + c) : 1.0f;
+    pdl_enter();
+
+    float pre[H] = {}, post[H] = {};
+    int64_t at_pre[H], at_post[H];
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+        at_pre[i] = static_cast<int64_t>(2 * i) * cols;
+        at_post[i] = static_cast<int64_t>(2 * i + 1) * cols;
+    }
+    if (p.pre) slab_sums<H>(part, slab_floats, at_pre, sub, p.slabs, SUBS, pre);
+    if (need_a && !grouped) slab_sums<H>(part, slab_floats, at_post, sub, p.slabs, SUBS, post);
+    if (need_a && grouped) {
+        // `per` (a power of two) threads of a column to each gate row
         int per = SUBS;
         while (per > 1 && SUBS / per < p.groups) per >>= 1;
-        float x0 = 0.0f, x1 = 0.0f;  // gate D ah, gate D
-        for (int64_t g0 = 0; g0 < p.groups; g0 += SUBS / per) {
-            const int64_t g = g0 + sub / per;
-            float t[V] = {};
-            if (g < p.groups)
-                slab_sums<V>(part, cols, g * p.slices + sub % per, (g + 1) * p.slices, per, 10u, t);
-            tree(t, per);
-            if (sub % per == 0 && g < p.groups && ok) {
-                const float s0 = t[1], s1 = LAYER ? t[V - 1] : 0.0f;
-                if (p.dgate) p.dgate[g * cols + c] = p.bs * (ow * s0 + ob * s1);
-                const float gate = p.gate ? p.gate[g * cols + c] : 1.0f;
-                x0 = fmaf(gate, s0, x0);
-                x1 = fmaf(gate, s1, x1);
+        const int member = sub & (per - 1);
+        for (int64_t g = sub / per; g < p.groups; g += SUBS / per) {
+            float t[H] = {};
+            slab_sums<H>(part, slab_floats, at_post, g * p.slices + member, (g + 1) * p.slices, per, t);
+            if (per > 1) {  // (then there is one round: the threads without a gate row come with zeros below)
+#pragma unroll
+                for (int i = 0; i < H; ++i) post[i] = t[i];
+                break;
             }
+            const float b = H > 1 ? t[H - 1] : 0.0f;
+            if (ok && p.dgate) p.dgate[g * cols + c] = p.bs * (ow * t[0] + ob * b);
+            const float gate = ok ? p.gate[g * cols + c] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < H; ++i) post[i] = fmaf(gate, t[i], post[i]);
         }
-        v[1] = x0;
-        if (LAYER) v[V - 1] = x1;
+        if (per > 1) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) red[i][sub * PAD + lane] = post[i];
+            __syncthreads();
+            const int64_t g = sub / per;
+#pragma unroll
+            for (int i = 0; i < H; ++i) post[i] = 0.0f;
+            if (member == 0 && g < p.groups) {
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+                    for (int k = 0; k < per; ++k) post[i] += red[i][(sub + k) * PAD + lane];
+                const float b = H > 1 ? post[H - 1] : 0.0f;
+                if (ok && p.dgate) p.dgate[g * cols + c] = p.bs * (ow * post[0] + ob * b);
+                const float gate = ok ? p.gate[g * cols + c] : 0.0f;
+#pragma unroll
+                for (int i = 0; i < H; ++i) post[i] *= gate;
+            }
+            __syncthreads();
+        }
     }
-    tree(v, SUBS);
+    // over the threads of a column: a warp to each column and vector
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+        red[i][sub * PAD + lane] = pre[i];
+        red[H + i][sub * PAD + lane] = post[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = tid / 32; q < V * TILE; q += kFinishThreads / 32) {
+        const float* r = red[q / TILE] + q % TILE;
+        float t = 0.0f;
+#pragma unroll
+        for (int k = tid % 32; k < SUBS; k += 32) t += r[k * PAD];
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
+        if (tid % 32 == 0) sum[q / TILE][q % TILE] = t;
+    }
+    __syncthreads();
     if (sub != 0 || !ok) return;
-    if (p.pre && p.dpre_w) p.dpre_w[c] = v[0];
-    if (p.post && p.dpost_w) p.dpost_w[c] = p.bs * v[1];
+    if (p.pre && p.dpre_w) p.dpre_w[c] = sum[0][lane];
+    const float a = sum[H][lane];
+    if (p.post && p.dpost_w) p.dpost_w[c] = p.bs * (single ? g0 * a : a);
     if constexpr (LAYER) {
-        if (p.pre && p.dpre_b) p.dpre_b[c] = v[2];
-        if (p.post && p.dpost_b) p.dpost_b[c] = p.bs * v[3];
+        if (p.pre && p.dpre_b) p.dpre_b[c] = sum[1][lane];
+        if (p.post && p.dpost_b) p.dpost_b[c] = p.bs * (single ? g0 * sum[V - 1][lane] : sum[V - 1][lane]);
     }
+    if (single && p.dgate) p.dgate[c] = p.bs * (ow * a + (LAYER ? ob * sum[V - 1][lane] : 0.0f));
 }
 
 template <class T, bool LAYER>
@@ -303,10 +332,7 @@ static cudaError_t finish(const BlockBwArgs& a, cudaStream_t stream) {
     auto go = [&](auto kernel, int tile) {
         return launch_dependent(kernel, dim3(static_cast<unsigned>((a.cols + tile - 1) / tile)), kFinishThreads, 0, 1, stream, a);
     };
-    // about one CTA an SM (152); rows of one sector (8 floats) are the least that is read whole
-    if (a.cols >= 32 * 128) return go(bwd_finish_kernel<LAYER, 32>, 32);
-    if (a.cols >= 16 * 128) return go(bwd_finish_kernel<LAYER, 16>, 16);
-    return go(bwd_finish_kernel<LAYER, 8>, 8);
+    return a.cols > 1024 ? go(bwd_finish_kernel<LAYER, 32>, 32) : go(bwd_finish_kernel<LAYER, 8>, 8);
 }
 
 cudaError_t launch_block_finish(int kind, const BlockBwArgs& a, cudaStream_t stream) {

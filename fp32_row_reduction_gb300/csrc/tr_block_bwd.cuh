@@ -17,7 +17,7 @@ namespace tr {
 namespace block {
 
 // MODE: the norms there are, a mask of TR_BLOCK_POST and TR_BLOCK_PRE; 0: as p says.
-template <class T, bool LAYER, int S, int LAYOUT, bool CLUSTER, int MODE, int THREADS, int CTAS>
+template <class T, bool LAYER, int S, int LAYOUT, bool CLUSTER, int MODE, int THREADS, int CTAS, bool SPARAM>
 __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p, const RowShape g) {
     constexpr int E = 16 / static_cast<int>(sizeof(T));
     constexpr int P = E / 2;       // pairs of a slot
@@ -73,7 +73,35 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
 
     // the slab's column sums dy hh and dy; those of the running gate row, D ah and D
     float2 sum0[K], sumA[K], sum1[LAYER ? K : 1], sumB[LAYER ? K : 1];
-    float2 w[K], qw[K];  // the pre-norm's weight; bs gate w_post
+    // the pre-norm's weight, and bs gate w_post: in registers, or (SPARAM) in the thread's own part of shared
+    // memory, two pairs to a 16-byte word
+    float2 w[SPARAM ? 1 : K], qw[SPARAM ? 1 : K];
+    float4* own = reinterpret_cast<float4*>(reinterpret_cast<char*>(smem) + team * team_bytes(g) + exchange_bytes(g) +
+                                            g.warps * g.stages * g.sampled) + t;
+    auto put_pairs = [&](int which, float2 (&reg)[SPARAM ? 1 : K], int s, const float2 (&v)[P]) {
+#pragma unroll
+        for (int j = 0; j < P; j += 2) {
+            if constexpr (SPARAM) {
+                own[(which * K + s * P + j) / 2 * tt] = make_float4(v[j].x, v[j].y, v[j + 1].x, v[j + 1].y);
+            } else {
+                reg[s * P + j] = v[j];
+                reg[s * P + j + 1] = v[j + 1];
+            }
+        }
+    };
+    auto get_pairs = [&](int which, const float2 (&reg)[SPARAM ? 1 : K], int s, float2 (&v)[P]) {
+#pragma unroll
+        for (int j = 0; j < P; j += 2) {
+            if constexpr (SPARAM) {
+                const float4 q = own[(which * K + s * P + j) / 2 * tt];
+                v[j] = make_float2(q.x, q.y);
+                v[j + 1] = make_float2(q.z, q.w);
+            } else {
+                v[j] = reg[s * P + j];
+                v[j + 1] = reg[s * P + j + 1];
+            }
+        }
+    };
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         sum0[k] = sumA[k] = both(0.0f);
@@ -83,8 +111,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
     for (int s = 0; s < S; ++s) {
         float2 v[P];
         ln.param(pre ? at0(p.pre_w) : nullptr, s, 1.0f, v);
-#pragma unroll
-        for (int j = 0; j < P; ++j) w[s * P + j] = v[j];
+        put_pairs(0, w, s, v);
     }
     auto gate_row = [&](int64_t row) { return p.gate ? p.gate + row / p.group_rows * cols + col0 : nullptr; };
     auto enter_group = [&](int64_t row) {
@@ -95,7 +122,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
             ln.param(post ? at0(p.post_w) : nullptr, s, 1.0f, o);
             ln.param(gr, s, 1.0f, v);
 #pragma unroll
-            for (int j = 0; j < P; ++j) qw[s * P + j] = __fmul2_rn(v[j], __fmul2_rn(both(p.bs), o[j]));
+            for (int j = 0; j < P; ++j) v[j] = __fmul2_rn(v[j], __fmul2_rn(both(p.bs), o[j]));
+            put_pairs(1, qw, s, v);
         }
     };
     // a whole group is done: its gate gradient is final, and its share of the post-norm's column
@@ -105,25 +133,40 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
         const float* gr = gate_row(row);
         float* dg = p.dgate ? p.dgate + row / p.group_rows * cols + col0 : nullptr;
         float* part = p.part + index * V * cols + col0;
+        // part += gate v
+        auto add = [&](float* o, int s, const float2 (&gate)[P], const float2* v) {
+            float2 x[P];
+#pragma unroll
+            for (int j = 0; j < P; ++j) x[j] = both(0.0f);
+            if (flushed) ln.get_floats(o, s, x);
+#pragma unroll
+            for (int j = 0; j < P; ++j) x[j] = __ffma2_rn(gate[j], v[j], x[j]);
+            ln.put_floats(o, s, x);
+        };
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float2 o[P], ob[P], gate[P];
-            ln.param(post ? at0(p.post_w) : nullptr, s, 1.0f, o);
-            ln.param(post ? at0(p.post_b) : nullptr, s, 0.0f, ob);
-            ln.param(gr, s, 1.0f, gate);
+            float2 o[P], gate[P];
+            if (dg) {
+                ln.param(post ? at0(p.post_w) : nullptr, s, p.bs, o);
+                const float scale = post && p.post_w ? p.bs : 1.0f;
+#pragma unroll
+                for (int j = 0; j < P; ++j) o[j] = __fmul2_rn(__fmul2_rn(o[j], both(scale)), sumA[s * P + j]);
+                if constexpr (LAYER) {
+                    ln.param(post ? at0(p.post_b) : nullptr, s, 0.0f, gate);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) o[j] = __ffma2_rn(__fmul2_rn(gate[j], both(p.bs)), sumB[LAYER ? s * P + j : 0], o[j]);
+                }
+                ln.put_floats(dg, s, o);
+            }
+            if (post) {
+                ln.param(gr, s, 1.0f, gate);
+                add(part + cols, s, gate, sumA + s * P);
+                if constexpr (LAYER) add(part + 3 * cols, s, gate, sumB + s * P);
+            }
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                const int k = s * P + j;
-                auto one = [&](int c, float wt, float bias, float gt, float a, float b) {
-                    if (dg) dg[c] = p.bs * (LAYER ? fmaf(wt, a, bias * b) : wt * a);
-                    part[cols + c] = fmaf(gt, a, flushed ? part[cols + c] : 0.0f);
-                    if constexpr (LAYER) part[3 * cols + c] = fmaf(gt, b, flushed ? part[3 * cols + c] : 0.0f);
-                };
-                const float2 b = LAYER ? sumB[LAYER ? k : 0] : both(0.0f);
-                if (ln.in(s, 2 * j)) one(ln.column(s, 2 * j), o[j].x, ob[j].x, gate[j].x, sumA[k].x, b.x);
-                if (ln.in(s, 2 * j + 1)) one(ln.column(s, 2 * j + 1), o[j].y, ob[j].y, gate[j].y, sumA[k].y, b.y);
-                sumA[k] = both(0.0f);
-                if constexpr (LAYER) sumB[k] = both(0.0f);
+                sumA[s * P + j] = both(0.0f);
+                if constexpr (LAYER) sumB[s * P + j] = both(0.0f);
             }
         }
         flushed = true;
@@ -158,9 +201,11 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
                 if (pre) {
                     ln.load(m, p.h, row, s, x);
                     ln.load(m + at_dy, p.dy, row, s, y);
+                    float2 wv[P];
+                    get_pairs(0, w, s, wv);
                     ln.pairs(s, [&](int j, bool xi, bool yi) {
                         const float2 c = shifted(x[j], sh, xi, yi);
-                        const float2 u = __fmul2_rn(y[j], w[s * P + j]);
+                        const float2 u = __fmul2_rn(y[j], wv[j]);
                         hh = __ffma2_rn(c, c, hh);
                         uh = __ffma2_rn(u, c, uh);
                         if constexpr (LAYER) {
@@ -242,7 +287,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
         const bool more = row + 1 < slab.end;
 
         // D, dx, the column sums of the pre-norm, and the sums of q (a - mean) and q
-        float2 d[K], av[K];
+        float2 d[K], av[SPARAM ? 1 : K];  // D, and a - mean (SPARAM: taken from the ring again)
         float2 qa2 = both(0.0f), qs2 = both(0.0f);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
@@ -256,13 +301,15 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
             if (pre) {
                 ln.load(m, p.h, row, s, x);
                 ln.load(m + at_dy, p.dy, row, s, y);
+                float2 wv[P];
+                get_pairs(0, w, s, wv);
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
                     const int k = s * P + j;
                     const float2 c = LAYER ? __fadd2_rn(x[j], both(-mean_h)) : x[j];
                     sum0[k] = __ffma2_rn(__fmul2_rn(y[j], both(rh)), c, sum0[k]);
                     if constexpr (LAYER) sum1[k] = __fadd2_rn(sum1[k], y[j]);
-                    const float2 u = LAYER ? __ffma2_rn(y[j], w[k], both(-c1)) : __fmul2_rn(y[j], w[k]);
+                    const float2 u = LAYER ? __ffma2_rn(y[j], wv[j], both(-c1)) : __fmul2_rn(y[j], wv[j]);
                     o[j] = __ffma2_rn(both(rh), __ffma2_rn(c, both(-k2), u), o[j]);
                 }
             }
@@ -275,13 +322,18 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
             if (need_a) {
                 ln.load(m + at_a, p.a, row, s, x);
 #pragma unroll
-                for (int j = 0; j < P; ++j) av[s * P + j] = LAYER && post ? __fadd2_rn(x[j], both(-mean_a)) : x[j];
+                for (int j = 0; j < P; ++j) {
+                    if (LAYER && post) x[j] = __fadd2_rn(x[j], both(-mean_a));
+                    if constexpr (!SPARAM) av[s * P + j] = x[j];
+                }
+                float2 qv[P];
+                get_pairs(1, qw, s, qv);
                 if (post)
                     ln.pairs(s, [&](int j, bool xi, bool yi) {
-                        float2 q = __fmul2_rn(d[s * P + j], qw[s * P + j]);
+                        float2 q = __fmul2_rn(d[s * P + j], qv[j]);
                         if (!xi) q.x = 0.0f;
                         if (!yi) q.y = 0.0f;
-                        qa2 = __ffma2_rn(q, av[s * P + j], qa2);
+                        qa2 = __ffma2_rn(q, x[j], qa2);
                         if constexpr (LAYER) qs2 = __fadd2_rn(qs2, q);
                     });
             }
@@ -294,18 +346,30 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
             const float e1 = qs * inv_n, e2 = qa * inv_n * ra * ra;
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                float2 o[P];
+                float2 o[P], qv[P], c[P];
+                get_pairs(1, qw, s, qv);
+                if constexpr (SPARAM) {
+                    if (need_a) {
+                        ln.load(m + at_a, p.a, row, s, c);
+                        if (LAYER && post)
+#pragma unroll
+                            for (int j = 0; j < P; ++j) c[j] = __fadd2_rn(c[j], both(-mean_a));
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < P; ++j) c[j] = av[s * P + j];
+                }
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
                     const int k = s * P + j;
-                    float2 q = __fmul2_rn(d[k], qw[k]);
+                    float2 q = __fmul2_rn(d[k], qv[j]);
                     if (need_a) {
-                        float2 ah = av[k];
+                        float2 ah = c[j];
                         if (post) {
-                            q = __ffma2_rn(av[k], both(-e2), q);
+                            q = __ffma2_rn(c[j], both(-e2), q);
                             if constexpr (LAYER) q = __fadd2_rn(q, both(-e1));
                             q = __fmul2_rn(q, both(ra));
-                            ah = __fmul2_rn(av[k], both(ra));
+                            ah = __fmul2_rn(c[j], both(ra));
                         }
                         sumA[k] = __ffma2_rn(d[k], ah, sumA[k]);
                         if constexpr (LAYER) sumB[k] = __fadd2_rn(sumB[k], d[k]);
@@ -319,35 +383,38 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
     }
     if (p.sums) {
         float* part = p.part + index * V * cols + col0;
-        auto one = [&](int c, float a0, float a1, float b0, float b1) {
-            part[c] = a0;
-            if (p.slices > 0) part[cols + c] = a1;
-            if constexpr (LAYER) {
-                part[2 * cols + c] = b0;
-                if (p.slices > 0) part[3 * cols + c] = b1;
-            }
+        auto slot_of = [&](const float2* v, int s, float2 (&o)[P]) {
+#pragma unroll
+            for (int j = 0; j < P; ++j) o[j] = v[s * P + j];
         };
 #pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                const int k = s * P + j, l = LAYER ? k : 0;
-                const float2 b0 = LAYER ? sum1[l] : both(0.0f), b1 = LAYER ? sumB[l] : both(0.0f);
-                if (ln.in(s, 2 * j)) one(ln.column(s, 2 * j), sum0[k].x, sumA[k].x, b0.x, b1.x);
-                if (ln.in(s, 2 * j + 1)) one(ln.column(s, 2 * j + 1), sum0[k].y, sumA[k].y, b0.y, b1.y);
+        for (int s = 0; s < S; ++s) {
+            float2 o[P];
+            slot_of(sum0, s, o);
+            if (pre) ln.put_floats(part, s, o);
+            slot_of(sumA, s, o);
+            if (p.slices > 0) ln.put_floats(part + cols, s, o);
+            if constexpr (LAYER) {
+                slot_of(sum1, s, o);
+                if (pre) ln.put_floats(part + 2 * cols, s, o);
+                slot_of(sumB, s, o);
+                if (p.slices > 0) ln.put_floats(part + 3 * cols, s, o);
             }
+        }
     }
     if constexpr (CLUSTER) cg::this_cluster().sync();  // no CTA leaves while another may still write to it
 }
 
 // ---- host side -------------------------------------------------------------
 
-template <class T, bool LAYER, int S, int LAYOUT, bool CLUSTER, int MODE, int THREADS, int CTAS>
-cudaError_t bwd_go(const BlockBwArgs& in, const RowShape& g, cudaStream_t stream) {
+template <class T, bool LAYER, int S, int LAYOUT, bool CLUSTER, int MODE, int THREADS, int CTAS, bool SPARAM = false>
+cudaError_t bwd_go(const BlockBwArgs& in, const RowShape& shape, cudaStream_t stream) {
     BlockBwArgs a = in;
+    RowShape g = shape;
+    if (!SPARAM) g.params = 0;
     const int threads = g.teams * g.warps * 32;
     const size_t smem = row_smem(g);
-    const auto kernel = bwd_kernel<T, LAYER, S, LAYOUT, CLUSTER, MODE, THREADS, CTAS>;
+    const auto kernel = bwd_kernel<T, LAYER, S, LAYOUT, CLUSTER, MODE, THREADS, CTAS, SPARAM>;
     const int64_t ctas = resident_ctas(reinterpret_cast<const void*>(kernel), threads, smem, g.cluster);
     if (ctas < 1) return cudaErrorInvalidConfiguration;
     block_slabs(&a, std::min(ctas * g.teams / g.cluster, block_slab_limit(a.rows, a.cols)));
@@ -362,7 +429,7 @@ cudaError_t bwd_go(const BlockBwArgs& in, const RowShape& g, cudaStream_t stream
 template <class T, bool LAYER, int S, int MODE>
 cudaError_t bwd_full(const BlockBwArgs& a, const RowShape& g, cudaStream_t stream) {
     if constexpr (S == 1) {
-        if (g.teams * g.warps <= 10) return bwd_go<T, LAYER, S, LAYOUT_FULL, false, MODE, 320, 2>(a, g, stream);
+        if (g.teams * g.warps <= 10) return bwd_go<T, LAYER, S, LAYOUT_FULL, false, MODE, 320, 2, LAYER && sizeof(T) == 2>(a, g, stream);
     }
     return bwd_go<T, LAYER, S, LAYOUT_FULL, false, MODE, 512, 1>(a, g, stream);
 }
@@ -386,7 +453,7 @@ cudaError_t bwd_kind(const BlockBwArgs& a, bool* done, cudaStream_t stream) {
     const bool odd = !rows_aligned(static_cast<int64_t>(a.cols) * static_cast<int>(sizeof(T)),
                                    {a.pre ? a.h : nullptr, a.pre ? a.dy : nullptr, a.post || a.dgate ? a.a : nullptr, a.dh, a.dx, a.da});
     int slots = 0;
-    const RowShape g = row_shape<T>(a.cols, tensors, odd, LAYER, 1, &slots);
+    const RowShape g = row_shape<T>(a.cols, tensors, odd, LAYER, 1, LAYER && sizeof(T) == 2 ? 64 : 0, &slots);
     *done = g.warps > 0;
     if (!*done) return cudaSuccess;
     const int layout = odd ? LAYOUT_ODD : row_full<T>(g, a.cols, slots) ? LAYOUT_FULL : LAYOUT_ALIGNED;

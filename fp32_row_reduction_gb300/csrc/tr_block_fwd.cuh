@@ -276,7 +276,7 @@ template <class T, bool LAYER>
 cudaError_t fwd_kind(const BlockArgs& a, bool* done, cudaStream_t stream) {
     const bool odd = !rows_aligned(static_cast<int64_t>(a.cols) * static_cast<int>(sizeof(T)), {a.x, a.a, a.h, a.y});
     int slots = 0;
-    const RowShape g = row_shape<T>(a.cols, 2, odd, LAYER, 2, &slots);
+    const RowShape g = row_shape<T>(a.cols, 2, odd, LAYER, 2, 0, &slots);
     *done = g.warps > 0;
     if (!*done) return cudaSuccess;
     const int layout = odd ? LAYOUT_ODD : row_full<T>(g, a.cols, slots) ? LAYOUT_FULL : LAYOUT_ALIGNED;

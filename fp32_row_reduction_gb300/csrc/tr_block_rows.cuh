@@ -34,13 +34,16 @@ struct RowShape {
     int stages;        // of a team's ring, 3 or 4: two rows are at work, the others on their way
     int tensors;       // matrices read
     int tensor_bytes;  // shared memory of one matrix's row
+    int params;        // bytes of parameters a thread keeps in shared memory (0: in its registers)
     int sampled;       // bytes of a stage that each warp keeps for itself (LayerNorm's shifts; see RowStart)
 };
 
 // Shared memory of a team's exchanges (up to eight values: two halves of 8 floats for each warp of a row) and row
 // starts; of all teams; and of the whole CTA.
 __host__ __device__ inline int exchange_bytes(const RowShape& g) { return 2 * 8 * 4 * g.warps * g.cluster; }
-__host__ __device__ inline int team_bytes(const RowShape& g) { return exchange_bytes(g) + g.warps * g.stages * g.sampled; }
+__host__ __device__ inline int team_bytes(const RowShape& g) {
+    return exchange_bytes(g) + g.warps * (g.stages * g.sampled + 32 * g.params);
+}
 __host__ __device__ inline int fixed_bytes(const RowShape& g) { return (g.teams * team_bytes(g) + 127) / 128 * 128; }
 inline int row_smem(const RowShape& g) { return fixed_bytes(g) + g.teams * g.stages * g.tensors * g.tensor_bytes; }
 
@@ -292,6 +295,39 @@ struct Lanes {
             }
         }
     }
+    // floats of slot s's columns to a vector (from this CTA's first column on): 16 bytes at a time where the
+    // layout allows it (a thread's columns are adjacent, so single floats would go 32 sectors to a store)
+    __device__ __forceinline__ void put_floats(float* o, int s, const float2 (&v)[P]) const {
+        if (!ODD && aligned16(o)) {
+            if (FULL || t + tt * s < vecs)
+#pragma unroll
+                for (int j = 0; j < P; j += 2)
+                    *reinterpret_cast<float4*>(o + column(s, 2 * j)) = make_float4(v[j].x, v[j].y, v[j + 1].x, v[j + 1].y);
+        } else {
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                if (in(s, 2 * j)) o[column(s, 2 * j)] = v[j].x;
+                if (in(s, 2 * j + 1)) o[column(s, 2 * j + 1)] = v[j].y;
+            }
+        }
+    }
+    __device__ __forceinline__ void get_floats(const float* o, int s, float2 (&v)[P]) const {
+        if (!ODD && aligned16(o)) {
+            if (FULL || t + tt * s < vecs)
+#pragma unroll
+                for (int j = 0; j < P; j += 2) {
+                    const float4 q = *reinterpret_cast<const float4*>(o + column(s, 2 * j));
+                    v[j] = make_float2(q.x, q.y);
+                    v[j + 1] = make_float2(q.z, q.w);
+                }
+        } else {
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                if (in(s, 2 * j)) v[j].x = o[column(s, 2 * j)];
+                if (in(s, 2 * j + 1)) v[j].y = o[column(s, 2 * j + 1)];
+            }
+        }
+    }
     // a parameter vector (from this CTA's first column on) at slot s's columns
     __device__ __forceinline__ void param(const float* w, int s, float absent, float2 (&v)[P]) const {
 #pragma unroll
@@ -321,7 +357,7 @@ struct Lanes {
 // a thread at most, the fewest CTAs a row that this allows with three stages of ring (four where
 // they leave `ctas` CTAs an SM), and several teams in a CTA for short rows.
 template <class T>
-RowShape row_shape(int cols, int tensors, bool odd, bool layer, int ctas, int* slots) {
+RowShape row_shape(int cols, int tensors, bool odd, bool layer, int ctas, int params, int* slots) {
     constexpr int E = 16 / static_cast<int>(sizeof(T));
     constexpr int kMaxSlots = 8 / E;
     constexpr int kLimit = 226 * 1024;
@@ -337,6 +373,7 @@ RowShape row_shape(int cols, int tensors, bool odd, bool layer, int ctas, int* s
         g.tensors = tensors;
         g.tensor_bytes = g.cta_vecs * 16 + (odd ? 16 : 0);
         g.sampled = layer && !odd ? 2 * kRowStartBytes : 0;
+        g.params = g.cluster == 1 ? params : 0;
         g.stages = 4;
         if (ctas * (row_smem(g) + 1024) > kLimit) g.stages = 3;
         if (row_smem(g) <= kLimit) return g;
