@@ -453,7 +453,7 @@ cudaError_t bwd_kind(const BlockBwArgs& a, bool* done, cudaStream_t stream) {
     const bool odd = !rows_aligned(static_cast<int64_t>(a.cols) * static_cast<int>(sizeof(T)),
                                    {a.pre ? a.h : nullptr, a.pre ? a.dy : nullptr, a.post || a.dgate ? a.a : nullptr, a.dh, a.dx, a.da});
     int slots = 0;
-    const RowShape g = row_shape<T>(a.cols, tensors, odd, LAYER, 1, LAYER && sizeof(T) == 2 ? 64 : 0, &slots);
+    const RowShape g = row_shape<T>(a.cols, tensors, odd, LAYER, 1, LAYER && sizeof(T) == 2 ? 64 : 0, 8, &slots);
     *done = g.warps > 0;
     if (!*done) return cudaSuccess;
     const int layout = odd ? LAYOUT_ODD : row_full<T>(g, a.cols, slots) ? LAYOUT_FULL : LAYOUT_ALIGNED;

@@ -251,7 +251,7 @@ cudaError_t fwd_go_with(const BlockArgs& a, const RowShape& g, cudaStream_t stre
 // most 320 threads are compiled for two an SM, and larger ones run one.
 template <class T, bool LAYER, int S, int LAYOUT, bool CLUSTER>
 cudaError_t fwd_go(const BlockArgs& a, const RowShape& g, cudaStream_t stream) {
-    if constexpr (!LAYER) {
+    if constexpr (!LAYER && S * 16 / sizeof(T) <= 8) {
         return fwd_go_with<T, LAYER, S, LAYOUT, CLUSTER, 512, 2>(a, g, stream);
     } else {
         if constexpr (!CLUSTER && S == 1 && LAYOUT == LAYOUT_FULL)
@@ -276,12 +276,14 @@ template <class T, bool LAYER>
 cudaError_t fwd_kind(const BlockArgs& a, bool* done, cudaStream_t stream) {
     const bool odd = !rows_aligned(static_cast<int64_t>(a.cols) * static_cast<int>(sizeof(T)), {a.x, a.a, a.h, a.y});
     int slots = 0;
-    const RowShape g = row_shape<T>(a.cols, 2, odd, LAYER, 2, 0, &slots);
+    const RowShape g = row_shape<T>(a.cols, 2, odd, LAYER, 2, 0, 16, &slots);
     *done = g.warps > 0;
     if (!*done) return cudaSuccess;
     const int layout = odd ? LAYOUT_ODD : row_full<T>(g, a.cols, slots) ? LAYOUT_FULL : LAYOUT_ALIGNED;
+    if (slots == 2) return fwd_slots<T, LAYER, 2>(layout, a, g, stream);
     if constexpr (sizeof(T) == 4) {
-        if (slots == 2) return fwd_slots<T, LAYER, 2>(layout, a, g, stream);
+        if (slots == 3) return fwd_slots<T, LAYER, 3>(layout, a, g, stream);
+        if (slots == 4) return fwd_slots<T, LAYER, 4>(layout, a, g, stream);
     }
     return fwd_slots<T, LAYER, 1>(layout, a, g, stream);
 }

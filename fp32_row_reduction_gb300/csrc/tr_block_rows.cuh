@@ -357,9 +357,9 @@ struct Lanes {
 // a thread at most, the fewest CTAs a row that this allows with three stages of ring (four where
 // they leave `ctas` CTAs an SM), and several teams in a CTA for short rows.
 template <class T>
-RowShape row_shape(int cols, int tensors, bool odd, bool layer, int ctas, int params, int* slots) {
+RowShape row_shape(int cols, int tensors, bool odd, bool layer, int ctas, int params, int most, int* slots) {
     constexpr int E = 16 / static_cast<int>(sizeof(T));
-    constexpr int kMaxSlots = 8 / E;
+    const int kMaxSlots = most / E;
     constexpr int kLimit = 226 * 1024;
     RowShape g = {};
     const int vecs = (cols + E - 1) / E;
