@@ -26,6 +26,7 @@ struct BlockArgs {
     int cols;
     int post, pre;  // which norms there are
     float rs, bs, eps;
+    unsigned* err;  // device error word (clusters' bounded waits; set by the launch)
 };
 
 struct BlockBwArgs {
@@ -55,6 +56,7 @@ struct BlockBwArgs {
     float rs, bs, eps;
     float* stats;     // re-read path: kBlockStats floats a row
     float* part;      // slabs x vectors x cols partial column sums
+    unsigned* err;    // device error word (clusters' bounded waits; set by the launch)
 };
 
 // The rows of a slab. With slices > 0 a slab is one of the `slices` equal parts

@@ -247,8 +247,20 @@ tr_status guarded(const char* w, F&& f) {
 
 std::mutex g_launch_mu;
 std::map<std::tuple<int, const void*, int, size_t, int>, int> g_resident;
+std::map<int, unsigned*> g_error_words;
 
 }  // namespace
+
+unsigned* device_error_word() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+    std::lock_guard<std::mutex> lock(g_launch_mu);
+    const auto it = g_error_words.find(dev);
+    if (it != g_error_words.end()) return it->second;
+    void* p = nullptr;
+    if (device_error_symbol(&p) != cudaSuccess) return nullptr;
+    return g_error_words[dev] = static_cast<unsigned*>(p);
+}
 
 int resident_ctas(const void* kernel, int threads, size_t smem, int cluster) {
     int dev = 0;
@@ -314,7 +326,7 @@ tr_status tr_gated_residual_norm(tr_norm_kind kind, tr_dtype dtype, int32_t norm
     s = check_ranges(w, in, out);
     if (s != TR_OK) return s;
     BlockArgs a{x, branch, h, y, post_w, post_b, gate, pre_w, pre_b, rows, gate ? rows / gate_rows : rows,
-                static_cast<int>(cols), norms & TR_BLOCK_POST ? 1 : 0, pre ? 1 : 0, residual_scale, branch_scale, eps};
+                static_cast<int>(cols), norms & TR_BLOCK_POST ? 1 : 0, pre ? 1 : 0, residual_scale, branch_scale, eps, nullptr};
     return guarded(w, [&] { return cuda_status(launch_block_forward(kind, dtype, a, stream), w); });
 }
 

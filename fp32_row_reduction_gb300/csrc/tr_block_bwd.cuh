@@ -35,11 +35,13 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
     const int col0 = rank * g.cta_vecs * E;  // this CTA's first column
     const Lanes<T, S, LAYOUT> ln(t, tt, cols, col0, g.cta_vecs);
     const float inv_n = 1.0f / static_cast<float>(cols);
-    Exchange<CLUSTER, LAYER ? 8 : 4> ex{reinterpret_cast<float*>(smem) + team * (team_bytes(g) / 4), g.warps * g.cluster,
-                            rank * g.warps + (t >> 5), team, g.warps};
+    char* const team_smem = reinterpret_cast<char*>(smem) + team * team_bytes(g);
+    Exchange<CLUSTER, LAYER ? 8 : 4> ex{reinterpret_cast<float*>(team_smem + 16), g.warps * g.cluster, rank * g.warps + (t >> 5),
+                                     team, g.warps, reinterpret_cast<uint64_t*>(team_smem), p.err};
+    ex.init();
     const int stage_bytes = g.tensors * g.tensor_bytes;
     using Start = RowStart<T, ODD>;
-    char* starts = reinterpret_cast<char*>(smem) + team * team_bytes(g) + exchange_bytes(g) + (t >> 5) * g.stages * g.sampled;
+    char* starts = team_smem + exchange_bytes(g) + (t >> 5) * g.stages * g.sampled;
     char* ring = reinterpret_cast<char*>(smem) + fixed_bytes(g) + team * g.stages * stage_bytes;
     if constexpr (CLUSTER) cg::this_cluster().sync();  // every CTA of the cluster runs before it is written to
     pdl_enter();
@@ -76,8 +78,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
     // the pre-norm's weight, and bs gate w_post: in registers, or (SPARAM) in the thread's own part of shared
     // memory, two pairs to a 16-byte word
     float2 w[SPARAM ? 1 : K], qw[SPARAM ? 1 : K];
-    float4* own = reinterpret_cast<float4*>(reinterpret_cast<char*>(smem) + team * team_bytes(g) + exchange_bytes(g) +
-                                            g.warps * g.stages * g.sampled) + t;
+    float4* own = reinterpret_cast<float4*>(team_smem + exchange_bytes(g) + g.warps * g.stages * g.sampled) + t;
     auto put_pairs = [&](int which, float2 (&reg)[SPARAM ? 1 : K], int s, const float2 (&v)[P]) {
 #pragma unroll
         for (int j = 0; j < P; j += 2) {
@@ -412,6 +413,7 @@ cudaError_t bwd_go(const BlockBwArgs& in, const RowShape& shape, cudaStream_t st
     BlockBwArgs a = in;
     RowShape g = shape;
     if (!SPARAM) g.params = 0;
+    if (CLUSTER && !(a.err = device_error_word())) return cudaErrorInvalidValue;
     const int threads = g.teams * g.warps * 32;
     const size_t smem = row_smem(g);
     const auto kernel = bwd_kernel<T, LAYER, S, LAYOUT, CLUSTER, MODE, THREADS, CTAS, SPARAM>;
@@ -453,7 +455,7 @@ cudaError_t bwd_kind(const BlockBwArgs& a, bool* done, cudaStream_t stream) {
     const bool odd = !rows_aligned(static_cast<int64_t>(a.cols) * static_cast<int>(sizeof(T)),
                                    {a.pre ? a.h : nullptr, a.pre ? a.dy : nullptr, a.post || a.dgate ? a.a : nullptr, a.dh, a.dx, a.da});
     int slots = 0;
-    const RowShape g = row_shape<T>(a.cols, tensors, odd, LAYER, 1, LAYER && sizeof(T) == 2 ? 64 : 0, 8, &slots);
+    const RowShape g = row_shape<T>(a.cols, tensors, odd, LAYER, 4, LAYER && sizeof(T) == 2 ? 64 : 0, 8, &slots);
     *done = g.warps > 0;
     if (!*done) return cudaSuccess;
     const int layout = odd ? LAYOUT_ODD : row_full<T>(g, a.cols, slots) ? LAYOUT_FULL : LAYOUT_ALIGNED;

@@ -27,11 +27,13 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
     const int col0 = rank * g.cta_vecs * E;  // this CTA's first column
     const Lanes<T, S, LAYOUT> ln(t, tt, cols, col0, g.cta_vecs);
     const float inv_n = 1.0f / static_cast<float>(cols);
-    Exchange<CLUSTER, LAYER ? 4 : 2> ex{reinterpret_cast<float*>(smem) + team * (team_bytes(g) / 4), g.warps * g.cluster,
-                            rank * g.warps + (t >> 5), team, g.warps};
+    char* const team_smem = reinterpret_cast<char*>(smem) + team * team_bytes(g);
+    Exchange<CLUSTER, LAYER ? 4 : 2> ex{reinterpret_cast<float*>(team_smem + 16), g.warps * g.cluster, rank * g.warps + (t >> 5),
+                                     team, g.warps, reinterpret_cast<uint64_t*>(team_smem), p.err};
+    ex.init();
     const int stage_bytes = g.tensors * g.tensor_bytes;
     using Start = RowStart<T, ODD>;
-    char* starts = reinterpret_cast<char*>(smem) + team * team_bytes(g) + exchange_bytes(g) + (t >> 5) * g.stages * g.sampled;
+    char* starts = team_smem + exchange_bytes(g) + (t >> 5) * g.stages * g.sampled;
     char* ring = reinterpret_cast<char*>(smem) + fixed_bytes(g) + team * g.stages * stage_bytes;
     if constexpr (CLUSTER) cg::this_cluster().sync();  // every CTA of the cluster runs before it is written to
     pdl_enter();
@@ -236,7 +238,9 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
 // ---- host side -------------------------------------------------------------
 
 template <class T, bool LAYER, int S, int LAYOUT, bool CLUSTER, int THREADS, int CTAS>
-cudaError_t fwd_go_with(const BlockArgs& a, const RowShape& g, cudaStream_t stream) {
+cudaError_t fwd_go_with(const BlockArgs& in, const RowShape& g, cudaStream_t stream) {
+    BlockArgs a = in;
+    if (CLUSTER && !(a.err = device_error_word())) return cudaErrorInvalidValue;
     const int threads = g.teams * g.warps * 32;
     const size_t smem = row_smem(g);
     const auto kernel = fwd_kernel<T, LAYER, S, LAYOUT, CLUSTER, THREADS, CTAS>;
@@ -276,7 +280,9 @@ template <class T, bool LAYER>
 cudaError_t fwd_kind(const BlockArgs& a, bool* done, cudaStream_t stream) {
     const bool odd = !rows_aligned(static_cast<int64_t>(a.cols) * static_cast<int>(sizeof(T)), {a.x, a.a, a.h, a.y});
     int slots = 0;
-    const RowShape g = row_shape<T>(a.cols, 2, odd, LAYER, 2, 0, 16, &slots);
+    // a third stage is all RMSNorm wants (16384 x 4096 bf16: 84 us, with a fourth 94: more loads under way only
+    // keep the stores waiting); LayerNorm's longer rows of work hide behind four (16384 x 2048: 48 us, with three 55)
+    const RowShape g = row_shape<T>(a.cols, 2, odd, LAYER, LAYER ? 4 : 3, 0, 16, &slots);
     *done = g.warps > 0;
     if (!*done) return cudaSuccess;
     const int layout = odd ? LAYOUT_ODD : row_full<T>(g, a.cols, slots) ? LAYOUT_FULL : LAYOUT_ALIGNED;

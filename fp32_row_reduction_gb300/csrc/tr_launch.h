@@ -11,6 +11,9 @@ namespace tr {
 // kernel, size and device), its dynamic shared memory allowed; 0 when it cannot run.
 int resident_ctas(const void* kernel, int threads, size_t smem, int cluster = 1);
 
+// The current device's error word (null when it cannot be found).
+unsigned* device_error_word();
+
 // Launch so that this grid's start may overlap the previous kernel's end (the kernel
 // waits in pdl_enter); TR_DISABLE_PDL=1 turns the overlap off.
 bool dependent_launches();
