@@ -746,17 +746,18 @@ def _dense(t):
     return True
 
 
-_shape_of, _dtype_of, _cuda_of = (operator.attrgetter(k) for k in ("shape", "dtype", "is_cuda"))
+_dtype_of = operator.attrgetter("dtype")
 
 
 def _tensor_list(tensors, name, index=None):
-    """(pointers, element counts, dtype codes) of a list of dense CUDA tensors on one device, and the
-    device; `index` is it where the call has another tensor too. (Lists may be long: each check is one pass.)"""
+    """A list of dense CUDA tensors on one device: (pointers, element counts, dtype codes), whether all
+    are contiguous, and the device; `index` is it where the call has another tensor too. (Lists may be
+    long: each check is one pass.)"""
     import torch
     T = torch.Tensor
-    if not all(map(_cuda_of, tensors)):
-        raise TypeError(f"{name} must hold CUDA tensors")
     devices = set(map(T.get_device, tensors))
+    if -1 in devices:
+        raise TypeError(f"{name} must hold CUDA tensors")
     if index is not None:
         devices.add(index)
     if len(devices) > 1:
@@ -765,27 +766,28 @@ def _tensor_list(tensors, name, index=None):
         codes = array.array("i", map(_dtype_codes().__getitem__, map(_dtype_of, tensors)))
     except KeyError as e:
         raise TypeError(f"{name} must hold float32, bfloat16 or float16 tensors, got {e.args[0]}") from None
-    if not all(map(T.is_contiguous, tensors)) and not all(map(_dense, tensors)):
+    contiguous = all(map(T.is_contiguous, tensors))
+    if not contiguous and not all(map(_dense, tensors)):
         raise ValueError(f"{name} must hold dense tensors (no gaps and no repeated elements)")
     index = devices.pop() if devices else torch.cuda.current_device()
-    return (array.array("Q", map(T.data_ptr, tensors)), array.array("q", map(T.numel, tensors)), codes, index)
+    return (array.array("Q", map(T.data_ptr, tensors)), array.array("q", map(T.numel, tensors)), codes), contiguous, index
 
 
-def _out_pointers(tensors, outs, index):
+def _out_pointers(tensors, arrays, contiguous, outs, index):
+    """Pointers of the tensors to write (None: in place), which are matched by their place in memory: contiguous
+    tensors of the same counts, or tensors of the same shapes and strides."""
     if outs is None:
         return None
-    import torch
-    T = torch.Tensor
     if len(outs) != len(tensors):
         raise ValueError("out must hold one tensor for each tensor")
-    if set(map(T.get_device, outs)) - {index} or list(map(_dtype_of, outs)) != list(map(_dtype_of, tensors)):
-        raise TypeError("out must hold tensors of the tensors' types, on their device")
-    # elements are matched by their place in memory
-    same = list(map(_shape_of, outs)) == list(map(_shape_of, tensors))
-    if not same or not (all(map(T.is_contiguous, tensors)) and all(map(T.is_contiguous, outs)) or
-                        all(o.stride() == t.stride() and _dense(o) for t, o in zip(tensors, outs))):
-        raise ValueError("out must hold tensors of the tensors' shapes and order of elements")
-    return array.array("Q", map(T.data_ptr, outs))
+    (ptrs, numels, codes), also, _ = _tensor_list(outs, "out", index)
+    if codes != arrays[2]:
+        raise TypeError("out must hold tensors of the tensors' types")
+    same = numels == arrays[1] if contiguous and also else all(
+        o.shape == t.shape and o.stride() == t.stride() for t, o in zip(tensors, outs))
+    if not same:
+        raise ValueError("out must hold tensors of the tensors' sizes and order of elements")
+    return ptrs
 
 
 def _address(a):
@@ -813,7 +815,7 @@ def global_norm(tensors, kind="l2", out=None, stream=None):
     float16, mixed as they come): "l2", the square root of the sum of squares, or "max", the
     largest magnitude. Returns one float32 on the device (nothing waits)."""
     tensors = list(tensors)
-    ptrs, numels, codes, index = _tensor_list(tensors, "tensors", None if out is None else out.get_device())
+    (ptrs, numels, codes), _, index = _tensor_list(tensors, "tensors", None if out is None else out.get_device())
     switch = _switch(index, stream)
     if switch is not None:
         with switch:
@@ -828,15 +830,16 @@ def global_norm(tensors, kind="l2", out=None, stream=None):
 
 def clip_by_norm(tensors, norm, max_norm, eps=1e-6, out=None, stream=None):
     """Scale every tensor of a list by min(1, max_norm / (norm + eps)), where norm is
-    one float32 on the device, in place or into the tensors of `out`."""
+    one float32 on the device, in place or into the tensors of `out` (of the same types and sizes)."""
     tensors = list(tensors)
     out = None if out is None else list(out)
-    ptrs, numels, codes, index = _tensor_list(tensors, "tensors", norm.get_device())
+    arrays, contiguous, index = _tensor_list(tensors, "tensors", norm.get_device())
     switch = _switch(index, stream)
     if switch is not None:
         with switch:
             return clip_by_norm(tensors, norm, max_norm, eps, out)
-    outs = _out_pointers(tensors, out, index)
+    outs = _out_pointers(tensors, arrays, contiguous, out, index)
+    ptrs, numels, codes = arrays
     _check(load().tr_clip_by_norm(_address(ptrs), _address(outs), _address(numels), _address(codes), len(tensors),
                                   _one_float(norm, index, "norm").data_ptr(), max_norm, eps, _current_stream()(index)),
            "clip_by_norm")
@@ -847,12 +850,13 @@ def clip_global_norm(tensors, max_norm, kind="l2", eps=1e-6, out=None, norm_out=
     clipping (one float32 on the device)."""
     tensors = list(tensors)
     out = None if out is None else list(out)
-    ptrs, numels, codes, index = _tensor_list(tensors, "tensors", None if norm_out is None else norm_out.get_device())
+    arrays, contiguous, index = _tensor_list(tensors, "tensors", None if norm_out is None else norm_out.get_device())
     switch = _switch(index, stream)
     if switch is not None:
         with switch:
             return clip_global_norm(tensors, max_norm, kind, eps, out, norm_out)
-    outs = _out_pointers(tensors, out, index)
+    outs = _out_pointers(tensors, arrays, contiguous, out, index)
+    ptrs, numels, codes = arrays
     norm = _one_float(norm_out, index, "norm_out")
     ws = _norm_workspace(len(tensors), index)
     code = TOTAL_KINDS[kind] if isinstance(kind, str) else int(kind)

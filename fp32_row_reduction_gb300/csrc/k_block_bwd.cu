@@ -183,29 +183,37 @@ __global__ void __launch_bounds__(kTile * 8) bwd_columns_kernel(const BlockBwArg
 
 // ---- the slabs' partials to the column gradients --------------------------------
 
-// A CTA of 1024 threads takes TILE columns, 1024 / TILE slabs at a time (TILE 8, one sector, for short rows, whose
-// columns are few and slabs many). The partials come from L2 and latency is all there is: eight slabs' loads are
-// under way at once, and the threads of a column meet twice, not in a tree of barriers.
-constexpr int kFinishThreads = 1024;
+// A CTA of 512 threads takes TILE columns, 512 / TILE slabs at a time (TILE 8, one sector, for short rows, whose
+// columns are few and slabs many). The partials come from L2 and latency is all there is: 16 loads a thread are
+// under way at once, two CTAs fit an SM, and the threads of a column meet twice, not in a tree of barriers.
+constexpr int kFinishThreads = 512;
 
-// v[i] += a column's sum of vector vecs[i] of slabs first, first + step, ... < end.
+// v[i] += a column's sum of vector first_vector + stride i of slabs first, first + step, ... < end.
 template <int N>
-__device__ __forceinline__ void slab_sums(const float* part, int64_t slab_floats, const int64_t (&at)[N], int64_t first,
-                                          int64_t end, int64_t step, float (&v)[N]) {
-    for (int64_t s = first; s < end; s += 8 * step) {
-        float q[8][N];
+__device__ __forceinline__ void slab_sums(const float* part, int cols, int vectors, int first_vector, int stride, int first,
+                                          int end, int step, float (&v)[N]) {
+    constexpr int U = 16 / N;
+    const int64_t slab_floats = static_cast<int64_t>(vectors) * cols, vector_floats = static_cast<int64_t>(stride) * cols;
+    for (int s = first; s < end; s += U * step) {
+        const float* q0 = part + s * slab_floats + static_cast<int64_t>(first_vector) * cols;
+        float q[U][N];
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < N; ++i) q[u][i] = s + u * step < end ? part[(s + u * step) * slab_floats + at[i]] : 0.0f;
+            for (int i = 0; i < N; ++i) q[u][i] = s + u * step < end ? q0[u * step * slab_floats + i * vector_floats] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            v[i] += ((q[0][i] + q[1][i]) + (q[2][i] + q[3][i])) + ((q[4][i] + q[5][i]) + (q[6][i] + q[7][i]));
+        for (int o = U / 2; o >= 1; o /= 2)
+#pragma unroll
+            for (int u = 0; u < o; ++u)
+#pragma unroll
+                for (int i = 0; i < N; ++i) q[u][i] += q[u + o][i];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += q[0][i];
     }
 }
 
 template <bool LAYER, int TILE>
-__global__ void __launch_bounds__(kFinishThreads) bwd_finish_kernel(const BlockBwArgs p) {
+__global__ void __launch_bounds__(kFinishThreads, 2) bwd_finish_kernel(const BlockBwArgs p) {
     constexpr int V = LAYER ? 4 : 2;
     constexpr int H = V / 2;  // vectors of a norm: dy hh, dy (pre); D ah, D (post)
     constexpr int SUBS = kFinishThreads / TILE;
@@ -216,7 +224,6 @@ __global__ void __launch_bounds__(kFinishThreads) bwd_finish_kernel(const BlockB
     const int cols = p.cols;
     const int c = static_cast<int>(blockIdx.x) * TILE + lane;
     const bool ok = c < cols;
-    const int64_t slab_floats = static_cast<int64_t>(V) * cols;
     const float* part = p.part + (ok ? c : 0);
     // (inputs, not results of the kernel before: they may be read while it ends)
     const float ow = ok && p.post && p.post_w ? __ldg(p.post_w + c) : 1.0f;
@@ -228,14 +235,19 @@ __global__ void __launch_bounds__(kFinishThreads) bwd_finish_kernel(const BlockB
     pdl_enter();
 
     float pre[H] = {}, post[H] = {};
-    int64_t at_pre[H], at_post[H];
+    const int slabs = static_cast<int>(p.slabs), slices = static_cast<int>(p.slices);
+    if (p.pre && need_a && !grouped) {
+        float all[V] = {};
+        slab_sums<V>(part, cols, V, 0, 1, sub, slabs, SUBS, all);
 #pragma unroll
-    for (int i = 0; i < H; ++i) {
-        at_pre[i] = static_cast<int64_t>(2 * i) * cols;
-        at_post[i] = static_cast<int64_t>(2 * i + 1) * cols;
+        for (int i = 0; i < H; ++i) {
+            pre[i] = all[2 * i];
+            post[i] = all[2 * i + 1];
+        }
+    } else {
+        if (p.pre) slab_sums<H>(part, cols, V, 0, 2, sub, slabs, SUBS, pre);
+        if (need_a && !grouped) slab_sums<H>(part, cols, V, 1, 2, sub, slabs, SUBS, post);
     }
-    if (p.pre) slab_sums<H>(part, slab_floats, at_pre, sub, p.slabs, SUBS, pre);
-    if (need_a && !grouped) slab_sums<H>(part, slab_floats, at_post, sub, p.slabs, SUBS, post);
     if (need_a && grouped) {
         // `per` (a power of two) threads of a column to each gate row
         int per = SUBS;
@@ -243,7 +255,7 @@ __global__ void __launch_bounds__(kFinishThreads) bwd_finish_kernel(const BlockB
         const int member = sub & (per - 1);
         for (int64_t g = sub / per; g < p.groups; g += SUBS / per) {
             float t[H] = {};
-            slab_sums<H>(part, slab_floats, at_post, g * p.slices + member, (g + 1) * p.slices, per, t);
+            slab_sums<H>(part, cols, V, 1, 2, static_cast<int>(g) * slices + member, static_cast<int>(g + 1) * slices, per, t);
             if (per > 1) {  // (then there is one round: the threads without a gate row come with zeros below)
 #pragma unroll
                 for (int i = 0; i < H; ++i) post[i] = t[i];

@@ -213,7 +213,7 @@ tr_status list_norm(const char* w, int kind, const ListCall& c, float* norm, voi
     return cuda_status(for_launches(c, [&](const TensorList<kListMax>& l) {
                            if (*n + kListMaxCtas > cap) return cudaErrorInvalidValue;
                            int ctas = 0;
-                           const cudaError_t e = launch_list_norm(kind, l, part + *n, &ctas, stream);
+                           const cudaError_t e = launch_list_norm(kind, l, part + *n, c.outs != nullptr, &ctas, stream);
                            *n += ctas;
                            return e;
                        }), w);

@@ -31,8 +31,9 @@ struct TensorList {
 inline int64_t list_launches(int64_t count) { return count < 1 ? 1 : (count + kListMax - 1) / kListMax; }
 
 // One partial norm a CTA (the sum of squares, or the largest magnitude).
-// *ctas: the partials written, from `part` on.
-cudaError_t launch_list_norm(int kind, const TensorList<kListMax>& list, double* part, int* ctas, cudaStream_t stream);
+// *ctas: the partials written, from `part` on; again: the list is scaled next (its end is kept in L2).
+cudaError_t launch_list_norm(int kind, const TensorList<kListMax>& list, double* part, bool again, int* ctas,
+                             cudaStream_t stream);
 // The norm from n partials.
 cudaError_t launch_list_total(int kind, const double* part, int n, float* norm, cudaStream_t stream);
 // out = in * min(1, max_norm / (norm + eps)); with n partials the norm is theirs (and is
