@@ -762,15 +762,19 @@ def _tensor_list(tensors, name, index=None):
         devices.add(index)
     if len(devices) > 1:
         raise ValueError(f"{name} must be on one device")
-    try:
-        codes = array.array("i", map(_dtype_codes().__getitem__, map(_dtype_of, tensors)))
-    except KeyError as e:
-        raise TypeError(f"{name} must hold float32, bfloat16 or float16 tensors, got {e.args[0]}") from None
+    code_of, kinds = _dtype_codes(), set(map(_dtype_of, tensors))
+    if not kinds <= code_of.keys():
+        raise TypeError(f"{name} must hold float32, bfloat16 or float16 tensors")
+    if len(kinds) == 1:
+        codes = array.array("i", [code_of[kinds.pop()]]) * len(tensors)
+    else:
+        codes = array.array("i", list(map(code_of.__getitem__, map(_dtype_of, tensors))))
     contiguous = all(map(T.is_contiguous, tensors))
     if not contiguous and not all(map(_dense, tensors)):
         raise ValueError(f"{name} must hold dense tensors (no gaps and no repeated elements)")
     index = devices.pop() if devices else torch.cuda.current_device()
-    return (array.array("Q", map(T.data_ptr, tensors)), array.array("q", map(T.numel, tensors)), codes), contiguous, index
+    return ((array.array("Q", list(map(T.data_ptr, tensors))), array.array("q", list(map(T.numel, tensors))), codes),
+            contiguous, index)
 
 
 def _out_pointers(tensors, arrays, contiguous, outs, index):
@@ -803,11 +807,16 @@ def _one_float(t, index, name):
     return t
 
 
-def _norm_workspace(count, index):
-    import torch
+@functools.lru_cache(maxsize=256)
+def _norm_workspace_bytes(count):
     n = ctypes.c_size_t(0)
     _check(load().tr_global_norm_workspace_bytes(count, ctypes.byref(n)), "global_norm_workspace_bytes")
-    return torch.empty(n.value, dtype=torch.uint8, device=torch.device("cuda", index))
+    return n.value
+
+
+def _norm_workspace(count, index):
+    import torch
+    return torch.empty(_norm_workspace_bytes(count), dtype=torch.uint8, device=torch.device("cuda", index))
 
 
 def global_norm(tensors, kind="l2", out=None, stream=None):

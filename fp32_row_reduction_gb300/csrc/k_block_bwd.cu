@@ -19,84 +19,82 @@
 namespace tr {
 namespace block {
 
-constexpr int kReadThreads = 512;
 constexpr int kTile = 32;  // columns of a column-sum CTA
 
 // ---- rows of any length, type and alignment, read again for each pass ----------
 
 // dx, da and the row's statistics.
-template <class T, bool LAYER>
+template <class T, bool LAYER, bool PRE, bool POST>
 __global__ void __launch_bounds__(kReadThreads) bwd_read_kernel(const BlockBwArgs p) {
-    constexpr int W = kReadThreads / 32;
-    __shared__ float slot[2][W];
+    __shared__ ReadRow::WarpSums warp_sums[2];
+    __shared__ ReadRow::CtaSums cta_sums[2];
     pdl_enter();
-    int buf = 0;
     const int cols = p.cols;
-    const float n = static_cast<float>(cols);
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const float inv_n = 1.0f / static_cast<float>(cols);
+    ReadRow rr(cols, warp_sums, cta_sums);
+    const int ctas = static_cast<int>(cg::this_cluster().num_blocks());
+    const ReadParam pre_w(p.pre_w, 1), post_w(p.post_w, 1);
+    const int start = static_cast<int>(threadIdx.x & 31) % cols;  // the lane's element of a row's start (see lane_mean)
+    for (int64_t row = blockIdx.x / ctas; row < p.rows; row += gridDim.x / ctas) {
         const int64_t at = row * cols;
         const T* hr = static_cast<const T*>(p.h) + at;
         const T* ar = static_cast<const T*>(p.a) + at;
         const T* dyr = static_cast<const T*>(p.dy) + at;
-        const T* dhr = p.dh ? static_cast<const T*>(p.dh) + at : nullptr;
-        const float* gr = p.gate ? p.gate + row / p.group_rows * cols : nullptr;
-        auto mean_of = [&](auto&& f) {
-            LongSum s;
-            for (int c = threadIdx.x; c < cols; c += kReadThreads) s.add(f(c));
-            float v[1] = {s.value()};
-            cta_sums<1, W>(v, slot, buf);
-            return v[0] / n;
-        };
-        auto statistics = [&](const T* v, float& mean, float& r) {
-            mean = LAYER ? mean_of([&](int c) { return to_float(v[c]); }) : 0.0f;
-            const float m = mean;
-            r = 1.0f / sqrtf(mean_of([&](int c) {
-                const float d = to_float(v[c]) - m;
-                return d * d;
-            }) + p.eps);
-        };
-        float mh = 0.0f, rh = 0.0f, c1 = 0.0f, c2 = 0.0f, ma = 0.0f, ra = 0.0f;
-        auto u_of = [&](int c) { return to_float(dyr[c]) * (p.pre_w ? __ldg(p.pre_w + c) : 1.0f); };
-        auto hh_of = [&](int c) { return (to_float(hr[c]) - mh) * rh; };
-        auto ah_of = [&](int c) { return (to_float(ar[c]) - ma) * ra; };
-        if (p.pre) {
-            statistics(hr, mh, rh);
-            if (LAYER) c1 = mean_of(u_of);
-            c2 = mean_of([&](int c) { return u_of(c) * hh_of(c); });
-        }
+        const bool has_dh = p.dh != nullptr;
+        const T* dhr = has_dh ? static_cast<const T*>(p.dh) + at : dyr;  // (without dh there is dy, and no branch)
+        const ReadParam gate(p.gate ? p.gate + row / p.group_rows * cols : nullptr, 1);
+        auto u_of = [&](int c) { return to_float(dyr[c]) * pre_w(c); };
+        // squares of h and a, u h, u, h and a, about shifts
+        const float kh = LAYER && PRE ? lane_mean(to_float(hr[start])) : 0.0f;
+        const float ka = LAYER && POST ? lane_mean(to_float(ar[start])) : 0.0f;
+        float s[6];
+        rr.sums<6>([&](int c) {
+            const float h = PRE ? to_float(hr[c]) - kh : 0.0f, a = POST ? to_float(ar[c]) - ka : 0.0f;
+            const float u = PRE ? u_of(c) : 0.0f;
+            return Values<6>{{h * h, a * a, u * h, LAYER ? u : 0.0f, LAYER ? h : 0.0f, LAYER ? a : 0.0f}};
+        }, s);
+        const float off_h = s[4] * inv_n, off_a = s[5] * inv_n;
+        const float mh = kh + off_h, ma = ka + off_a, c1 = s[3] * inv_n;
+        const float rh = PRE ? rsqrtf(fmaf(LAYER ? squares_about_mean(s[0], s[4], off_h) : s[0], inv_n, p.eps)) : 0.0f;
+        const float ra = POST ? rsqrtf(fmaf(LAYER ? squares_about_mean(s[1], s[5], off_a) : s[1], inv_n, p.eps)) : 0.0f;
+        const float c2 = fmaf(-off_h, s[3], s[2]) * inv_n * rh;
+        auto ah_of = [&](int c) { return POST ? (to_float(ar[c]) - ma) * ra : 0.0f; };
         auto d_of = [&](int c) {
-            float d = dhr ? to_float(dhr[c]) : 0.0f;
-            if (p.pre) d += rh * (u_of(c) - c1 - hh_of(c) * c2);
-            return d;
+            const float v = to_float(dhr[c]);
+            const float d = has_dh ? v : 0.0f;
+            return PRE ? d + rh * (u_of(c) - c1 - (to_float(hr[c]) - mh) * rh * c2) : d;
         };
-        auto q_of = [&](float d, int c) {
-            float q = p.bs * d;
-            if (gr) q *= __ldg(gr + c);
-            if (p.post && p.post_w) q *= __ldg(p.post_w + c);
-            return q;
-        };
-        float e1 = 0.0f, e2 = 0.0f;
-        if (p.post) {
-            statistics(ar, ma, ra);
-            if (LAYER) e1 = mean_of([&](int c) { return q_of(d_of(c), c); });
-            e2 = mean_of([&](int c) { return q_of(d_of(c), c) * ah_of(c); });
+        auto q_of = [&](float d, int c) { return p.bs * d * gate(c) * (POST ? post_w(c) : 1.0f); };
+        float e[2] = {0.0f, 0.0f};
+        if (POST) {
+            rr.sums<2>([&](int c) {
+                const float q = q_of(d_of(c), c);
+                return Values<2>{{LAYER ? q : 0.0f, q * ah_of(c)}};
+            }, e);
+            e[0] *= inv_n;
+            e[1] *= inv_n;
         }
-        if (p.sums && threadIdx.x == 0) {
-            float* s = p.stats + row * kBlockStats;
-            s[0] = mh;
-            s[1] = rh;
-            s[2] = c1;
-            s[3] = c2;
-            s[4] = ma;
-            s[5] = ra;
+        if (p.sums && threadIdx.x == 0 && rr.begin == 0) {
+            float* st = p.stats + row * kBlockStats;
+            st[0] = mh;
+            st[1] = rh;
+            st[2] = c1;
+            st[3] = c2;
+            st[4] = ma;
+            st[5] = ra;
         }
-        for (int c = threadIdx.x; c < cols; c += kReadThreads) {
-            const float d = d_of(c);
-            const float q = q_of(d, c);
-            static_cast<T*>(p.dx)[at + c] = from_float<T>(p.rs * d);
-            static_cast<T*>(p.da)[at + c] = from_float<T>(p.post ? ra * (q - e1 - ah_of(c) * e2) : q);
-        }
+        rr.columns(
+            [&](int c) {
+                const float d = d_of(c);
+                const float q = q_of(d, c);
+                return Values<2>{{p.rs * d, POST ? ra * (q - e[0] - ah_of(c) * e[1]) : q}};
+            },
+            [&](int c, const Values<2>& v) {
+                static_cast<T*>(p.dx)[at + c] = from_float<T>(v.v[0]);
+                static_cast<T*>(p.da)[at + c] = from_float<T>(v.v[1]);
+            });
     }
+    if (ctas > 1) cg::this_cluster().sync();  // no CTA leaves while another may still write to it
 }
 
 // The column sums of one slab over kTile columns, from the rows' statistics:
@@ -319,13 +317,17 @@ __global__ void __launch_bounds__(kFinishThreads, 2) bwd_finish_kernel(const Blo
 template <class T, bool LAYER>
 cudaError_t bwd_launch(const BlockBwArgs& in, cudaStream_t stream) {
     BlockBwArgs a = in;
-    block_slabs(&a, block_slab_limit(a.rows, a.cols));
     const unsigned tiles = static_cast<unsigned>((a.cols + kTile - 1) / kTile);
-    bwd_read_kernel<T, LAYER><<<static_cast<unsigned>(std::min<int64_t>(a.rows, 1 << 20)), kReadThreads, 0, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
+    // as many slabs as the column tiles leave of about 16 CTAs an SM
+    block_slabs(&a, std::min<int64_t>(block_slab_limit(a.rows, a.cols), std::max(1u, 16 * 152 / tiles)));
+    const int ctas = read_cluster(a.rows, a.cols);
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.rows, 1 << 20)) * ctas;
+    const auto kernel = a.pre && a.post ? bwd_read_kernel<T, LAYER, true, true>
+                        : a.pre         ? bwd_read_kernel<T, LAYER, true, false>
+                                        : bwd_read_kernel<T, LAYER, false, true>;
+    cudaError_t e = launch_dependent(kernel, dim3(grid), kReadThreads, 0, ctas, stream, a);
     if (e != cudaSuccess || !a.sums) return e;
-    bwd_columns_kernel<T, LAYER><<<dim3(tiles, static_cast<unsigned>(a.slabs)), kTile * 8, 0, stream>>>(a);
-    e = cudaGetLastError();
+    e = launch_dependent(bwd_columns_kernel<T, LAYER>, dim3(tiles, static_cast<unsigned>(a.slabs)), kTile * 8, 0, 1, stream, a);
     if (e != cudaSuccess) return e;
     return launch_block_finish(LAYER ? TR_NORM_LAYER : TR_NORM_RMS, a, stream);
 }

@@ -1,80 +1,72 @@
 // The gated residual norm, forward: h = rs x + bs gate post(a), y = pre(h).
 //
 // Each row needs the statistics of a before h exists, and those of h before y:
-// two dependent row sums (LayerNorm: four, each variance about its mean).
+// two dependent row sums. Rows that fit the chip take tr_block_fwd.cuh's kernel.
 #include <algorithm>
 
 #include "tr_block.cuh"
 #include "tr_block.h"
+#include "tr_launch.h"
 
 namespace tr {
 namespace block {
 
-constexpr int kReadThreads = 512;
-
-// Rows of any length, type and alignment: a CTA per row, the row read again (from
-// the caches) for each pass.
+// Rows of any length, type and alignment: a CTA or, for few long rows, a cluster to a row, which is read again
+// (from the caches) for each pass.
 template <class T, bool LAYER>
 __global__ void __launch_bounds__(kReadThreads) fwd_read_kernel(const BlockArgs p) {
-    constexpr int W = kReadThreads / 32;
-    __shared__ float slot[2][W];
+    __shared__ ReadRow::WarpSums warp_sums[2];
+    __shared__ ReadRow::CtaSums cta_sums[2];
     pdl_enter();
-    int buf = 0;
     const int cols = p.cols;
-    const float n = static_cast<float>(cols);
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const float inv_n = 1.0f / static_cast<float>(cols);
+    ReadRow rr(cols, warp_sums, cta_sums);
+    const int ctas = static_cast<int>(cg::this_cluster().num_blocks());
+    const ReadParam post_w(p.post_w, 1), post_b(p.post_b, 0), pre_w(p.pre_w, 1), pre_b(p.pre_b, 0);
+    const int start = static_cast<int>(threadIdx.x & 31) % cols;  // the lane's element of a row's start (see lane_mean)
+    for (int64_t row = blockIdx.x / ctas; row < p.rows; row += gridDim.x / ctas) {
         const T* xr = static_cast<const T*>(p.x) + row * cols;
         const T* ar = static_cast<const T*>(p.a) + row * cols;
-        const float* gr = p.gate ? p.gate + row / p.group_rows * cols : nullptr;
-        auto row_sum = [&](auto&& f) {
-            LongSum s;
-            for (int c = threadIdx.x; c < cols; c += kReadThreads) s.add(f(c));
-            float v[1] = {s.value()};
-            cta_sums<1, W>(v, slot, buf);
-            return v[0];
-        };
-        // mean and 1 / sqrt(mean square about it + eps) of v(c)
+        const ReadParam gate(p.gate ? p.gate + row / p.group_rows * cols : nullptr, 1);
+        // mean and 1 / sqrt(mean square about it + eps) of v(column)
         auto statistics = [&](auto&& v, float& mean, float& r) {
-            mean = LAYER ? row_sum(v) / n : 0.0f;
-            const float m = mean;
-            const float var = row_sum([&](int c) {
-                const float d = v(c) - m;
-                return d * d;
-            }) / n;
-            r = 1.0f / sqrtf(var + p.eps);
+            const float shift = LAYER ? lane_mean(v(start)) : 0.0f;
+            float s[2];
+            rr.sums<2>([&](int c) {
+                const float d = v(c) - shift;
+                return Values<2>{{d * d, LAYER ? d : 0.0f}};
+            }, s);
+            const float off = s[1] * inv_n;
+            mean = shift + off;
+            r = rsqrtf(fmaf(LAYER ? squares_about_mean(s[0], s[1], off) : s[0], inv_n, p.eps));
         };
         float ma = 0.0f, ra = 1.0f;
         if (p.post) statistics([&](int c) { return to_float(ar[c]); }, ma, ra);
         auto h_of = [&](int c) {
-            float v = to_float(ar[c]);
-            if (p.post) {
-                v = (v - ma) * ra;
-                if (p.post_w) v *= __ldg(p.post_w + c);
-                if (p.post_b) v += __ldg(p.post_b + c);
-            }
-            if (gr) v *= __ldg(gr + c);
-            return p.rs * to_float(xr[c]) + p.bs * v;
+            const float n = (to_float(ar[c]) - ma) * ra;
+            const float scaled = LAYER ? fmaf(n, post_w(c), post_b(c)) : n * post_w(c);
+            return p.rs * to_float(xr[c]) + p.bs * (scaled * gate(c));
         };
         float mh = 0.0f, rh = 1.0f;
         if (p.pre) statistics(h_of, mh, rh);
-        for (int c = threadIdx.x; c < cols; c += kReadThreads) {
-            const float h = h_of(c);
-            if (p.h) static_cast<T*>(p.h)[row * cols + c] = from_float<T>(h);
-            if (p.pre) {
-                float y = (h - mh) * rh;
-                if (p.pre_w) y *= __ldg(p.pre_w + c);
-                if (p.pre_b) y += __ldg(p.pre_b + c);
-                static_cast<T*>(p.y)[row * cols + c] = from_float<T>(y);
-            }
-        }
+        rr.columns(
+            [&](int c) {
+                const float h = h_of(c), n = (h - mh) * rh;
+                return Values<2>{{h, LAYER ? fmaf(n, pre_w(c), pre_b(c)) : n * pre_w(c)}};
+            },
+            [&](int c, const Values<2>& v) {
+                if (p.h) static_cast<T*>(p.h)[row * cols + c] = from_float<T>(v.v[0]);
+                if (p.pre) static_cast<T*>(p.y)[row * cols + c] = from_float<T>(v.v[1]);
+            });
     }
+    if (ctas > 1) cg::this_cluster().sync();  // no CTA leaves while another may still write to it
 }
 
 template <class T, bool LAYER>
 cudaError_t fwd_read_launch(const BlockArgs& a, cudaStream_t stream) {
-    const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(a.rows, 1 << 20));
-    fwd_read_kernel<T, LAYER><<<ctas, kReadThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    const int ctas = read_cluster(a.rows, a.cols);
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.rows, 1 << 20)) * ctas;
+    return launch_dependent(fwd_read_kernel<T, LAYER>, dim3(grid), kReadThreads, 0, ctas, stream, a);
 }
 
 template <class T>

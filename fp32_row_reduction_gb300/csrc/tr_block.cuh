@@ -23,46 +23,118 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { re
 template <>
 __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
 
-// A long sum in two levels: binary32 over 32 terms at a time, their totals in
-// binary64, so that a row of 2^24 columns loses no more than a short one.
+constexpr int kReadCluster = 8;  // most CTAs of a row that is read again for each pass
+
+// A shift for a row's LayerNorm sums: the mean of its first 32 elements, which every warp of the row finds
+// alike. Sums are taken about it in one pass, and the variance is S2 / n - (S1 / n)^2; the cancellation
+// costs 1 + (shift - mean)^2 / variance of precision: 1 + 1/32 for independent elements, and at worst 1 + n / 32 (all of
+// the row's spread in the 32).
+__device__ __forceinline__ float lane_mean(float v) {
+    v *= 1.0f / 32.0f;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+// The sum of squares about the mean, from the sums s2 of squares and s1 about a shift that is d off the mean. A
+// rounding below zero counts as zero; what is infinite or no number stays so.
+__device__ __forceinline__ float squares_about_mean(float s2, float s1, float d) {
+    return fabsf(s2) <= 3.0e38f ? fmaxf(fmaf(-d, s1, s2), 0.0f) : s2;
+}
+// A long sum with the rounding error of each step added up beside it (Knuth's two-sum), so that a row of 2^24 columns
+// loses no more than a short one. (Totals in binary64 made the kernels twice as slow.)
 struct LongSum {
-    float part = 0.0f;
-    double total = 0.0;
-    int n = 0;
+    float s = 0.0f, c = 0.0f;
     __device__ __forceinline__ void add(float v) {
-        part += v;
-        if (++n == 32) {
-            total += static_cast<double>(part);
-            part = 0.0f;
-            n = 0;
-        }
+        const float t = s + v, w = t - s;
+        c += (s - (t - w)) + (v - w);
+        s = t;
     }
-    __device__ __forceinline__ float value() const { return static_cast<float>(total + static_cast<double>(part)); }
+    __device__ __forceinline__ float value() const { return fabsf(s) <= 3.0e38f ? s + c : s; }
 };
 
-// N sums over a CTA of WARPS warps in one exchange (every thread gets them).
-// `buf` alternates between the halves of `slot`, so consecutive sums need one barrier each.
-template <int N, int WARPS>
-__device__ __forceinline__ void cta_sums(float (&v)[N], float (*slot)[N * WARPS], int& buf) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kFull, v[i], o);
-    float* s = slot[buf];
-    buf ^= 1;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0)
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[i * WARPS + (threadIdx.x >> 5)] = v[i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        float t = lane < WARPS ? s[i * WARPS + lane] : 0.0f;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
-        v[i] = t;
+// A parameter vector that may be absent, read without a branch (loads of several columns can then be under way
+// together): an absent one is a single value that every column reads.
+__device__ const float g_block_values[2] = {0.0f, 1.0f};
+struct ReadParam {
+    const float* p;
+    int step;
+    __device__ __forceinline__ ReadParam(const float* w, int absent) : p(w ? w : g_block_values + absent), step(w ? 1 : 0) {}
+    __device__ __forceinline__ float operator()(int c) const { return __ldg(p + static_cast<int64_t>(step) * c); }
+};
+
+// The share of a row's columns that a CTA of a cluster has, and sums over all of the row.
+constexpr int kReadThreads = 1024;
+constexpr int kReadSums = 6;  // most sums of one pass
+template <int N>
+struct Values {
+    float v[N];
+};
+struct ReadRow {
+    static constexpr int kWarps = kReadThreads / 32;
+    // two halves that alternate, so consecutive sums need one barrier each
+    using WarpSums = float[kReadSums][kWarps];
+    using CtaSums = float[kReadSums][kReadCluster];
+    int begin, end;  // columns
+    WarpSums* warp;
+    CtaSums* cta;
+    int buf = 0;
+
+    __device__ __forceinline__ ReadRow(int cols, WarpSums* warp_, CtaSums* cta_) : warp(warp_), cta(cta_) {
+        const cg::cluster_group cl = cg::this_cluster();
+        const int64_t n = cl.num_blocks(), r = cl.block_rank();
+        begin = static_cast<int>(cols * r / n);
+        end = static_cast<int>(cols * (r + 1) / n);
     }
-}
+    // f(column) for this thread's columns, four loads deep: f gives what g(column, value) then takes
+    template <class F, class G>
+    __device__ __forceinline__ void columns(F&& f, G&& g) const {
+        int c = begin + static_cast<int>(threadIdx.x);
+        for (; c + 3 * kReadThreads < end; c += 4 * kReadThreads) {
+            const auto v0 = f(c), v1 = f(c + kReadThreads), v2 = f(c + 2 * kReadThreads), v3 = f(c + 3 * kReadThreads);
+            g(c, v0);
+            g(c + kReadThreads, v1);
+            g(c + 2 * kReadThreads, v2);
+            g(c + 3 * kReadThreads, v3);
+        }
+        for (; c < end; c += kReadThreads) g(c, f(c));
+    }
+    // N sums of f(column) over the row, four columns' values added before they meet the sum
+    template <int N, class F>
+    __device__ __forceinline__ void sums(F&& f, float (&out)[N]) {
+        LongSum s[N];
+        int c = begin + static_cast<int>(threadIdx.x);
+        for (; c + 3 * kReadThreads < end; c += 4 * kReadThreads) {
+            const Values<N> v0 = f(c), v1 = f(c + kReadThreads), v2 = f(c + 2 * kReadThreads), v3 = f(c + 3 * kReadThreads);
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i].add((v0.v[i] + v1.v[i]) + (v2.v[i] + v3.v[i]));
+        }
+        for (; c < end; c += kReadThreads) {
+            const Values<N> v = f(c);
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i].add(v.v[i]);
+        }
+        const int lane = threadIdx.x & 31;
+        cg::cluster_group cl = cg::this_cluster();
+        const int n = static_cast<int>(cl.num_blocks()), rank = static_cast<int>(cl.block_rank());
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            out[i] = warp_allreduce<SumOp, 32>(s[i].value());
+            if (lane == 0) warp[buf][i][threadIdx.x >> 5] = out[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) out[i] = warp_allreduce<SumOp, 32>(lane < kWarps ? warp[buf][i][lane] : 0.0f);
+        if (n > 1) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (static_cast<int>(threadIdx.x) < n) *cl.map_shared_rank(&cta[buf][i][rank], threadIdx.x) = out[i];
+            cl.sync();
+#pragma unroll
+            for (int i = 0; i < N; ++i) out[i] = warp_allreduce<SumOp, 32>(lane < n ? cta[buf][i][lane] : 0.0f);
+        }
+        buf ^= 1;
+    }
+};
 
 // cp.async: 16 bytes to shared memory past the registers and L1.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {

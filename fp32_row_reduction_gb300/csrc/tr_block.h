@@ -102,6 +102,14 @@ inline void block_slabs(BlockBwArgs* a, int64_t target) {
     }
 }
 
+// CTAs (1 .. 8) of a row in the kernels that read rows again for each pass: as many as keep about 152 SMs
+// busy with few rows, but no fewer than 4096 columns each.
+inline int read_cluster(int64_t rows, int64_t cols) {
+    int n = 1;
+    while (n < 8 && rows * n * 2 <= 152 && cols / (n * 2) >= 4096) n *= 2;
+    return n;
+}
+
 cudaError_t launch_block_forward(int kind, int dtype, const BlockArgs& a, cudaStream_t stream);
 cudaError_t launch_block_backward(int kind, int dtype, const BlockBwArgs& a, cudaStream_t stream);
 // The forward of rows that fit on the chip; *done is false (and nothing launched) for others.

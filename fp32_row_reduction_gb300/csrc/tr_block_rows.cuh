@@ -92,7 +92,9 @@ struct Exchange {
     unsigned* err;
     int buf = 0;
     unsigned phase = 0;  // of both mbarriers, one bit each
-    bool lost = false;   // a wait gave up (the error word says so): no more waits, the results are void
+    // A wait that gives up sets the error word, and the results are void. Later waits of the kernel are
+    // short then, but there still is one for every phase: no CTA ends with stores to it under way.
+    unsigned limit_ns = 2000000000u;
 
     static __device__ __forceinline__ void spread(float r, float (&v)[N]) {
 #pragma unroll
@@ -131,8 +133,8 @@ struct Exchange {
                              "r"(__float_as_uint(r)), "r"(signal)
                              : "memory");
             }
-            if (!lost && !wait(bar, (phase >> buf) & 1)) {
-                lost = true;
+            if (!wait(bar, (phase >> buf) & 1, limit_ns)) {
+                limit_ns = 1000000u;
                 atomicOr(err, kErrWaitTimeout);
             }
             phase ^= 1u << buf;
@@ -168,8 +170,7 @@ struct Exchange {
     }
 
 private:
-    // Waits for the phase, for two seconds at most.
-    static __device__ __forceinline__ bool wait(uint64_t* bar, unsigned parity) {
+    static __device__ __forceinline__ bool wait(uint64_t* bar, unsigned parity, unsigned limit_ns) {
         auto done = [&]() {
             uint32_t ok;
             asm volatile(
@@ -183,26 +184,12 @@ private:
         };
         if (done()) return true;
         const unsigned long long t0 = global_ns();
-        while (global_ns() - t0 < 2000000000ull)
+        while (global_ns() - t0 < limit_ns)
             if (done()) return true;
         return false;
     }
 };
 
-// A shift for a row's LayerNorm sums: the mean of its first 32 elements, which every warp of the row finds
-// alike. Sums are taken about it in one pass, and the variance is S2 / n - (S1 / n)^2; the cancellation
-// costs 1 + (shift - mean)^2 / variance of precision: 1 + 1/32 for independent elements, and at worst 1 + n / 32 (all of
-// the row's spread in the 32).
-__device__ __forceinline__ float lane_mean(float v) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    return v * (1.0f / 32.0f);
-}
-// The sum of squares about the mean, from the sums s2 of squares and s1 about a shift that is d off the mean. A
-// rounding below zero counts as zero; what is infinite or no number stays so.
-__device__ __forceinline__ float squares_about_mean(float s2, float s1, float d) {
-    return fabsf(s2) <= 3.0e38f ? fmaxf(fmaf(-d, s1, s2), 0.0f) : s2;
-}
 // A warp's own copy of a row's first 32 elements, which come with the row: loading them when they are
 // needed would wait for the saturated memory (twice the time of the whole kernel), and another warp's
 // copy could only be read after a barrier.
