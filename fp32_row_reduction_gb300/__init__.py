@@ -756,10 +756,10 @@ def _tensor_list(tensors, name, index=None):
     import torch
     T = torch.Tensor
     devices = set(map(T.get_device, tensors))
-    if -1 in devices:
-        raise TypeError(f"{name} must hold CUDA tensors")
     if index is not None:
         devices.add(index)
+    if -1 in devices:
+        raise TypeError(f"{name} must hold CUDA tensors, as every tensor of the call")
     if len(devices) > 1:
         raise ValueError(f"{name} must be on one device")
     code_of, kinds = _dtype_codes(), set(map(_dtype_of, tensors))

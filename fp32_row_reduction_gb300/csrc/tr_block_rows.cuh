@@ -1,6 +1,6 @@
 // A team of warps on the rows of a slab: the pieces that both directions of the block norms share.
 //
-// A thread owns the same C = 4 or 8 columns of every row. Rows come through a ring of shared-memory
+// A thread owns the same 4 to 16 columns of every row. Rows come through a ring of shared-memory
 // stages filled by cp.async; rows too long for 16 warps are split over a cluster of 2, 4 or 8 CTAs,
 // whose warps exchange their sums through distributed shared memory.
 //

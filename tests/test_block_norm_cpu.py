@@ -172,7 +172,10 @@ def test_helpers_refuse_host_tensors():
         tr.gated_residual_norm(x, x)
     with pytest.raises(TypeError):
         tr.gated_residual_norm_backward(x, x, x)
-    for f in (tr.global_norm, lambda t: tr.clip_global_norm(t, 1.0), lambda t: tr.clip_by_norm(t, t[0], 1.0)):
+    one = torch.zeros(())
+    for f in (tr.global_norm, lambda t: tr.clip_global_norm(t, 1.0), lambda t: tr.clip_by_norm(t, one, 1.0),
+              lambda t: tr.global_norm([], out=one), lambda t: tr.clip_global_norm([], 1.0, norm_out=one),
+              lambda t: tr.clip_by_norm([], one, 1.0)):
         with pytest.raises(TypeError):
             f([x])
 
