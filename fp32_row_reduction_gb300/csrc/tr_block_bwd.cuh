@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
                                      team, g.warps, reinterpret_cast<uint64_t*>(team_smem), p.err};
     ex.init();
     const int stage_bytes = g.tensors * g.tensor_bytes;
-    using Start = RowStart<T, ODD>;
+    using Start = RowStart<T, LAYOUT, CLUSTER>;
     char* starts = team_smem + exchange_bytes(g) + (t >> 5) * g.stages * g.sampled;
     char* ring = reinterpret_cast<char*>(smem) + fixed_bytes(g) + team * g.stages * stage_bytes;
     if constexpr (CLUSTER) cg::this_cluster().sync();  // every CTA of the cluster runs before it is written to
@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
         float2 hh = both(0.0f), aa = both(0.0f), uh = both(0.0f), u1 = both(0.0f), h1 = both(0.0f), a1 = both(0.0f);
         if constexpr (LAYER) {
             __syncwarp();
-            if (pre && more) sh = lane_mean(Start::get(p.h, row, cols, starts + stage * g.sampled));
-            if (post && more) sa = lane_mean(Start::get(p.a, row, cols, starts + stage * g.sampled + kRowStartBytes));
+            if (pre && more) sh = lane_mean(Start::get(p.h, row, cols, starts + stage * g.sampled, m));
+            if (post && more) sa = lane_mean(Start::get(p.a, row, cols, starts + stage * g.sampled + kRowStartBytes, m + at_a));
         }
         if (more) {
 #pragma unroll
@@ -426,12 +426,12 @@ cudaError_t bwd_go(const BlockBwArgs& in, const RowShape& shape, cudaStream_t st
     return launch_block_finish(LAYER ? TR_NORM_LAYER : TR_NORM_RMS, a, stream);
 }
 
-// Full rows of one CTA are compiled for each pair of norms, and for CTAs of at most 320 threads
-// with registers for two an SM.
+// Full rows of one CTA are compiled for each pair of norms. 128 registers a thread let two CTAs of 256 threads
+// share an SM; CTAs of 9 or 10 warps are compiled for two an SM with 96.
 template <class T, bool LAYER, int S, int MODE>
 cudaError_t bwd_full(const BlockBwArgs& a, const RowShape& g, cudaStream_t stream) {
     if constexpr (S == 1) {
-        if (g.teams * g.warps <= 10) return bwd_go<T, LAYER, S, LAYOUT_FULL, false, MODE, 320, 2, LAYER && sizeof(T) == 2>(a, g, stream);
+        if (g.teams * g.warps > 8 && g.teams * g.warps <= 10) return bwd_go<T, LAYER, S, LAYOUT_FULL, false, MODE, 320, 2, LAYER && sizeof(T) == 2>(a, g, stream);
     }
     return bwd_go<T, LAYER, S, LAYOUT_FULL, false, MODE, 512, 1>(a, g, stream);
 }

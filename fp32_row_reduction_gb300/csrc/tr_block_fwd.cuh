@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
                                      team, g.warps, reinterpret_cast<uint64_t*>(team_smem), p.err};
     ex.init();
     const int stage_bytes = g.tensors * g.tensor_bytes;
-    using Start = RowStart<T, ODD>;
+    using Start = RowStart<T, LAYOUT, CLUSTER>;
     char* starts = team_smem + exchange_bytes(g) + (t >> 5) * g.stages * g.sampled;
     char* ring = reinterpret_cast<char*>(smem) + fixed_bytes(g) + team * g.stages * stage_bytes;
     if constexpr (CLUSTER) cg::this_cluster().sync();  // every CTA of the cluster runs before it is written to
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
     float a_here = 0.0f;  // LayerNorm: the lane's element of a
     if constexpr (LAYER) {
         __syncwarp();
-        a_here = Start::get(p.a, begin, cols, starts);
+        a_here = Start::get(p.a, begin, cols, starts, ring);
     }
     if (p.post) statistics(ring, begin, false, true, 0.0f, LAYER ? lane_mean(a_here) : 0.0f);
     int stage = 0, fill = g.stages - 1;
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
         float h_here = 0.0f;
         if constexpr (LAYER) {
             if (p.pre) {
-                const float x_here = Start::get(p.x, row, cols, starts + here * g.sampled + kRowStartBytes);
+                const float x_here = Start::get(p.x, row, cols, starts + here * g.sampled + kRowStartBytes, m + g.tensor_bytes);
                 h_here = fmaf((a_here - ma) * ra, probe_w, fmaf(p.rs, x_here, probe_b));
             }
         }
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
         float a_next = 0.0f;
         if constexpr (LAYER) {
             __syncwarp();
-            if (more) a_next = Start::get(p.a, row + 1, cols, starts + stage * g.sampled);
+            if (more) a_next = Start::get(p.a, row + 1, cols, starts + stage * g.sampled, next);
         }
         statistics(next, row + 1, true, more, LAYER ? lane_mean(h_here) : 0.0f, LAYER ? lane_mean(a_next) : 0.0f);
         a_here = a_next;
@@ -258,7 +258,7 @@ cudaError_t fwd_go(const BlockArgs& a, const RowShape& g, cudaStream_t stream) {
     if constexpr (!LAYER && S * 16 / sizeof(T) <= 8) {
         return fwd_go_with<T, LAYER, S, LAYOUT, CLUSTER, 512, 2>(a, g, stream);
     } else {
-        if constexpr (!CLUSTER && S == 1 && LAYOUT == LAYOUT_FULL)
+        if constexpr (!CLUSTER && S == 1)
             if (g.teams * g.warps <= 10) return fwd_go_with<T, LAYER, S, LAYOUT, CLUSTER, 320, 2>(a, g, stream);
         return fwd_go_with<T, LAYER, S, LAYOUT, CLUSTER, 512, 1>(a, g, stream);
     }

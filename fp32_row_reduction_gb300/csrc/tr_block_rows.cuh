@@ -190,25 +190,36 @@ private:
     }
 };
 
-// A warp's own copy of a row's first 32 elements, which come with the row: loading them when they are
-// needed would wait for the saturated memory (twice the time of the whole kernel), and another warp's
-// copy could only be read after a barrier.
+// How a row lies over the threads: aligned with all slots of all threads in the row (no test is left in the
+// inner loops, which are short of issue slots), aligned, or in the odd layout.
+enum Layout : int { LAYOUT_FULL, LAYOUT_ALIGNED, LAYOUT_ODD };
+
+// Where a warp finds a row's first 32 elements. Loading them from memory when they are needed would wait for
+// its full queues (twice the time of the whole kernel), so:
+// * aligned rows: every warp copies them for itself, with the row (another warp's copy could only be read
+//   after a barrier);
+// * other rows in one CTA: in the ring, after the barrier that the layout has anyway;
+// * other rows of a cluster: in memory all the same.
 constexpr int kRowStartBytes = 128;
-template <class T, bool ODD>
+template <class T, int LAYOUT, bool CLUSTER>
 struct RowStart {
+    static constexpr bool OWN = LAYOUT != LAYOUT_ODD;
     static __device__ __forceinline__ void fetch(const void* matrix, int64_t row, int64_t row_bytes, char* to) {
-        if constexpr (!ODD) {
+        if constexpr (OWN) {
             const int lane = threadIdx.x & 31;
             const int n = static_cast<int>(min(static_cast<int64_t>(32 * sizeof(T)), row_bytes)) >> 4;
             if (lane < n) cp_async16(smem_addr(to) + lane * 16, static_cast<const char*>(matrix) + (row * row_bytes + lane * 16));
         }
     }
-    // this lane's element (rows shorter than 32 are gone over again); after the row's copies and __syncwarp()
-    static __device__ __forceinline__ float get(const void* matrix, int64_t row, int cols, const char* from) {
+    // This lane's element (rows shorter than 32 are gone over again): own: the warp's copy, after the row's copies
+    // and __syncwarp(); staged: the row in the ring.
+    static __device__ __forceinline__ float get(const void* matrix, int64_t row, int cols, const char* own, const char* staged) {
         const int lane = static_cast<int>(threadIdx.x & 31);
         const int c = cols < 32 ? lane % cols : lane;
-        if constexpr (ODD) return to_float(static_cast<const T*>(matrix)[row * cols + c]);
-        return to_float(reinterpret_cast<const T*>(from)[c]);
+        if constexpr (OWN) return to_float(reinterpret_cast<const T*>(own)[c]);
+        const T* start = static_cast<const T*>(matrix) + row * cols;
+        if constexpr (CLUSTER) return to_float(start[c]);
+        return to_float(reinterpret_cast<const T*>(staged + (reinterpret_cast<uintptr_t>(start) & 15))[c]);
     }
 };
 
@@ -228,10 +239,6 @@ __device__ __forceinline__ uint32_t bits_of(float2 v, __half) {
     return *reinterpret_cast<const uint32_t*>(&b);
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-
-// How a row lies over the threads: aligned with all slots of all threads in the row (no test is left in the
-// inner loops, which are short of issue slots), aligned, or in the odd layout.
-enum Layout : int { LAYOUT_FULL, LAYOUT_ALIGNED, LAYOUT_ODD };
 
 // A thread's share of a row. `mine` columns of the row, from byte `base` on, belong to this CTA.
 template <class T, int S, int LAYOUT>

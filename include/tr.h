@@ -333,12 +333,20 @@ tr_status tr_axis_launch_shape(int32_t sm_count, int32_t op, tr_order order, int
  * h is not read without TR_BLOCK_PRE, nor branch when there is neither
  * TR_BLOCK_POST nor dgate: they may then be NULL.
  * The column gradients need a caller-owned, 16-byte-aligned workspace of
- * tr_gated_residual_norm_backward_workspace_bytes (none when all are NULL). All sums
- * have a fixed order: results repeat bit for bit on one device.
+ * tr_gated_residual_norm_backward_workspace_bytes (none when all are NULL); calls that
+ * may run at the same time need one each. All sums have a fixed order: results
+ * repeat bit for bit on one device.
+ *
+ * LayerNorm's variance is taken in one pass about the mean of the row's first 32
+ * elements: rounding errors of the variance grow by 1 + (that mean - the row's
+ * mean)^2 / variance, 1 + cols / 32 at most. RMSNorm's squares are plain sums.
+ * Values whose squares leave binary32's range give infinite sums (and outputs of 0).
  *
  * rows = 0 writes zeros to the column gradients and nothing else. order must be
  * TR_ORDER_UNORDERED_TREE: the others return TR_ERR_UNSUPPORTED. No call
- * allocates or waits, and all may be captured into a graph. */
+ * allocates or waits on the host, and all may be captured into a graph, the first
+ * call of a process too. Rows that are split over several thread blocks meet in
+ * bounded waits (two seconds): one that gave up is reported by tr_last_device_error. */
 typedef enum tr_dtype { TR_F32 = 0, TR_BF16 = 1, TR_F16 = 2 } tr_dtype;
 typedef enum tr_norm_kind { TR_NORM_RMS = 0, TR_NORM_LAYER = 1 } tr_norm_kind;
 #define TR_BLOCK_POST 1
@@ -383,8 +391,9 @@ tr_status tr_gated_residual_norm_backward_workspace_bytes(tr_norm_kind kind, int
  * scaled by it. max_norm and eps must be >= 0 and not NaN (max_norm may be infinite).
  *
  * *norm may not overlap a tensor. The norm needs a caller-owned, 16-byte-aligned
- * workspace of tr_global_norm_workspace_bytes(count). No call allocates or waits, and all may be
- * captured into a graph (which keeps the pointers). */
+ * workspace of tr_global_norm_workspace_bytes(count); calls that may run at the same time
+ * need one each. No call allocates or waits, and all may be captured into a graph (which
+ * keeps the pointers). */
 typedef enum tr_total_kind { TR_TOTAL_L2 = 0, TR_TOTAL_MAX = 1 } tr_total_kind;
 
 tr_status tr_global_norm(tr_total_kind kind, const void* const* tensors, const int64_t* numels, const int32_t* dtypes,
