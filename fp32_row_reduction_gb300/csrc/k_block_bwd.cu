@@ -346,7 +346,10 @@ static cudaError_t finish(const BlockBwArgs& a, cudaStream_t stream) {
     auto go = [&](auto kernel, int tile) {
         return launch_dependent(kernel, dim3(static_cast<unsigned>((a.cols + tile - 1) / tile)), kFinishThreads, 0, 1, stream, a);
     };
-    return a.cols > 1024 ? go(bwd_finish_kernel<LAYER, 32>, 32) : go(bwd_finish_kernel<LAYER, 8>, 8);
+    // the widest tile that still makes a CTA for each of 152 SMs
+    if (a.cols >= 32 * 152) return go(bwd_finish_kernel<LAYER, 32>, 32);
+    if (a.cols >= 16 * 152) return go(bwd_finish_kernel<LAYER, 16>, 16);
+    return go(bwd_finish_kernel<LAYER, 8>, 8);
 }
 
 cudaError_t launch_block_finish(int kind, const BlockBwArgs& a, cudaStream_t stream) {
