@@ -595,14 +595,14 @@ def _current_stream():
     return getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _rows_like(t, name, like):
-    """Pointer of a matrix that must match `like` (None: null)."""
+def _rows_like(t, name, dtype, shape, index):
+    """Pointer of a contiguous matrix of the call's type and shape (None: null)."""
     if t is None:
         return None
-    if t.dtype is not like.dtype or t.get_device() != like.get_device():
-        raise TypeError(f"{name} must be a {like.dtype} tensor on {like.device}")
-    if t.shape != like.shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {tuple(like.shape)} tensor")
+    if t.dtype is not dtype or t.get_device() != index:
+        raise TypeError(f"{name} must be a {dtype} tensor on cuda:{index}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor")
     return t.data_ptr()
 
 
@@ -653,14 +653,15 @@ def gated_residual_norm(x, branch, post_weight=None, post_bias=None, gate=None, 
         with switch:
             return gated_residual_norm(x, branch, post_weight, post_bias, gate, weight, bias, eps, kind, post, pre,
                                        residual_scale, branch_scale, out, h_out, want_h, order)
-    vec = (c,)
+    vec, dt, shape = (c,), x.dtype, x.shape
     y = out if out is not None or not pre else torch.empty_like(x)
     h = h_out if h_out is not None or not want_h else torch.empty_like(x)
     _check(load().tr_gated_residual_norm(
-        code, dtype, norms, x.data_ptr(), _rows_like(branch, "branch", x), _floats(post_weight, "post_weight", vec, index),
-        _floats(post_bias, "post_bias", vec, index), gp, groups, _floats(weight, "weight", vec, index),
-        _floats(bias, "bias", vec, index), _rows_like(h, "h_out", x), _rows_like(y, "out", x), r, c, residual_scale,
-        branch_scale, eps, _order(order), _current_stream()(index)), "gated_residual_norm")
+        code, dtype, norms, x.data_ptr(), _rows_like(branch, "branch", dt, shape, index),
+        _floats(post_weight, "post_weight", vec, index), _floats(post_bias, "post_bias", vec, index), gp, groups,
+        _floats(weight, "weight", vec, index), _floats(bias, "bias", vec, index), _rows_like(h, "h_out", dt, shape, index),
+        _rows_like(y, "out", dt, shape, index), r, c, residual_scale, branch_scale, eps, _order(order),
+        _current_stream()(index)), "gated_residual_norm")
     return y, h
 
 
@@ -690,7 +691,7 @@ def gated_residual_norm_backward(h, branch, dy=None, dh=None, post_weight=None, 
         with switch:
             return gated_residual_norm_backward(h, branch, dy, dh, post_weight, post_bias, gate, weight, eps, kind, post, pre,
                                                 residual_scale, branch_scale, want_params, dx, dbranch, workspace, order)
-    vec = (c,)
+    vec, dt, shape = (c,), branch.dtype, branch.shape
     if dx is None:
         dx = torch.empty_like(branch)
     if dbranch is None:
@@ -724,11 +725,11 @@ def gated_residual_norm_backward(h, branch, dy=None, dh=None, post_weight=None, 
             n = workspace.numel() * workspace.element_size()
         wsp = workspace.data_ptr()
     _check(load().tr_gated_residual_norm_backward(
-        code, dtype, norms, _rows_like(h, "h", branch), branch.data_ptr(), _rows_like(dy, "dy", branch),
-        _rows_like(dh, "dh", branch), _floats(post_weight, "post_weight", vec, index),
+        code, dtype, norms, _rows_like(h, "h", dt, shape, index), branch.data_ptr(), _rows_like(dy, "dy", dt, shape, index),
+        _rows_like(dh, "dh", dt, shape, index), _floats(post_weight, "post_weight", vec, index),
         _floats(post_bias, "post_bias", vec, index), gp, groups, _floats(weight, "weight", vec, index),
-        _rows_like(dx, "dx", branch), _rows_like(dbranch, "dbranch", branch), ppw, ppb, pg, pw, pb, r, c, residual_scale,
-        branch_scale, eps, _order(order), wsp, n, _current_stream()(index)), "gated_residual_norm_backward")
+        _rows_like(dx, "dx", dt, shape, index), _rows_like(dbranch, "dbranch", dt, shape, index), ppw, ppb, pg, pw, pb, r, c,
+        residual_scale, branch_scale, eps, _order(order), wsp, n, _current_stream()(index)), "gated_residual_norm_backward")
     return GatedResidualNormGrads(dx, dbranch, dpw, dpb, dg, dw, db)
 
 
