@@ -19,7 +19,6 @@
 
 #include "tr.h"
 #include "tr_internal.h"
-#include "tr_launch.h"
 #include "tr_plan.h"
 
 namespace tr {
@@ -392,8 +391,6 @@ RowArgs blank_args(const float* x, int64_t rows, int64_t cols) {
 void set_last_error(const char* what, const char* detail) { t_last_error = std::string(what) + ": " + detail; }
 
 cudaError_t device_error_symbol(void** out) { return cudaGetSymbolAddress(out, g_device_error); }
-
-bool dependent_launches() { return g_pdl; }
 
 int debug_flags_now() {
     std::lock_guard<std::mutex> lock(g_mu);

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <map>
 #include <mutex>
 #include <new>
@@ -250,6 +251,14 @@ std::map<std::tuple<int, const void*, int, size_t, int>, int> g_resident;
 std::map<int, unsigned*> g_error_words;
 
 }  // namespace
+
+bool dependent_launches() {
+    static const bool on = [] {
+        const char* v = std::getenv("TR_DISABLE_PDL");
+        return !(v && v[0] == '1');
+    }();
+    return on;
+}
 
 unsigned* device_error_word() {
     int dev = 0;
