@@ -1,6 +1,7 @@
 // The gated residual norm with the rows on chip: h = rs x + bs gate post(a), y = pre(h).
 //
-// HBM-bound: x and a are read, h and y written once. A row's y waits for the statistics of h, which
+// HBM-bound: x and a are read, h and y written once (16384 x 4096 bf16: RMSNorm 83 us, 95% of the measured copy rate,
+// LayerNorm 88 us). A row's y waits for the statistics of h, which
 // wait for those of a; so that a row costs one exchange between its warps, the sum over h of a row
 // travels with the sum over a of the next one. LayerNorm's sums are taken about a shift that each warp
 // finds for itself (lane_mean; for h from the same elements' own x and a). The parameters of a thread's columns
@@ -28,11 +29,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
     const Lanes<T, S, LAYOUT> ln(t, tt, cols, col0, g.cta_vecs);
     const float inv_n = 1.0f / static_cast<float>(cols);
     char* const team_smem = reinterpret_cast<char*>(smem) + team * team_bytes(g);
-    Exchange<CLUSTER, LAYER ? 4 : 2> ex{reinterpret_cast<float*>(team_smem + 16), g.warps * g.cluster, rank * g.warps + (t >> 5),
-                                     team, g.warps, reinterpret_cast<uint64_t*>(team_smem), p.err};
+    Exchange<CLUSTER, LAYER ? 4 : 2> ex(team_smem, g.warps * g.cluster, rank * g.warps + (t >> 5), team, g.warps, p.err);
     ex.init();
     const int stage_bytes = g.tensors * g.tensor_bytes;
-    using Start = RowStart<T, LAYOUT, CLUSTER>;
+    const RowStart<T, LAYOUT, CLUSTER> row_start(cols, ln.row_bytes);  // LayerNorm's
     char* starts = team_smem + exchange_bytes(g) + (t >> 5) * g.stages * g.sampled;
     char* ring = reinterpret_cast<char*>(smem) + fixed_bytes(g) + team * g.stages * stage_bytes;
     if constexpr (CLUSTER) cg::this_cluster().sync();  // every CTA of the cluster runs before it is written to
@@ -48,8 +48,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
             ln.fetch(p.a, p.rows, row, to);
             ln.fetch(p.x, p.rows, row, to + g.tensor_bytes);
             if constexpr (LAYER) {
-                Start::fetch(p.a, row, ln.row_bytes, starts + stage * g.sampled);
-                if (p.pre) Start::fetch(p.x, row, ln.row_bytes, starts + stage * g.sampled + kRowStartBytes);
+                row_start.fetch(p.a, row, starts + stage * g.sampled);
+                if (p.pre) row_start.fetch(p.x, row, starts + stage * g.sampled + kRowStartBytes);
             }
         }
         cp_async_commit();
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
     float a_here = 0.0f;  // LayerNorm: the lane's element of a
     if constexpr (LAYER) {
         __syncwarp();
-        a_here = Start::get(p.a, begin, cols, starts, ring);
+        a_here = row_start.get(p.a, begin, starts, ring);
     }
     if (p.post) statistics(ring, begin, false, true, 0.0f, LAYER ? lane_mean(a_here) : 0.0f);
     int stage = 0, fill = g.stages - 1;
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
         float h_here = 0.0f;
         if constexpr (LAYER) {
             if (p.pre) {
-                const float x_here = Start::get(p.x, row, cols, starts + here * g.sampled + kRowStartBytes, m + g.tensor_bytes);
+                const float x_here = row_start.get(p.x, row, starts + here * g.sampled + kRowStartBytes, m + g.tensor_bytes);
                 h_here = fmaf((a_here - ma) * ra, probe_w, fmaf(p.rs, x_here, probe_b));
             }
         }
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
         float a_next = 0.0f;
         if constexpr (LAYER) {
             __syncwarp();
-            if (more) a_next = Start::get(p.a, row + 1, cols, starts + stage * g.sampled, next);
+            if (more) a_next = row_start.get(p.a, row + 1, starts + stage * g.sampled, next);
         }
         statistics(next, row + 1, true, more, LAYER ? lane_mean(h_here) : 0.0f, LAYER ? lane_mean(a_next) : 0.0f);
         a_here = a_next;

@@ -84,10 +84,11 @@ __device__ __forceinline__ float halving_sums(const float (&v)[N], int lane) {
 template <bool CLUSTER, int N>
 struct Exchange {
     static constexpr int kLanes = 32 / N;  // lanes of a warp that end with the same value
-    float* slot;     // this CTA's: 2 x N x entries floats; the halves alternate
     int entries;     // warps of the row
-    int entry;       // this warp's place among them
     int team, warps;
+    uint32_t put;    // where this lane's value goes, in the half of this CTA's 2 x N x entries floats that is next
+    uint32_t take;   // and where it reads from
+    int flip;        // to the other half
     uint64_t* bars;  // a cluster's: one mbarrier a half
     unsigned* err;
     int buf = 0;
@@ -95,6 +96,16 @@ struct Exchange {
     // A wait that gives up sets the error word, and the results are void. Later waits of the kernel are
     // short then, but there still is one for every phase: no CTA ends with stores to it under way.
     unsigned limit_ns = 2000000000u;
+
+    // `entry`: this warp's place among the row's. Addresses are found once: the exchange is a fifth of the instructions.
+    __device__ __forceinline__ Exchange(char* smem, int entries_, int entry, int team_, int warps_, unsigned* err_)
+        : entries(entries_), team(team_), warps(warps_), bars(reinterpret_cast<uint64_t*>(smem)), err(err_) {
+        const int lane = threadIdx.x & 31;
+        const uint32_t slot = smem_addr(smem + 16);
+        put = slot + 4 * (entry * N + lane / kLanes);
+        take = slot + 4 * ((lane & 15) * N + (lane >> 4) * (N / 2));
+        flip = 4 * N * entries;
+    }
 
     static __device__ __forceinline__ void spread(float r, float (&v)[N]) {
 #pragma unroll
@@ -116,18 +127,15 @@ struct Exchange {
         const int lane = threadIdx.x & 31;
         const float r = halving_sums<N, 16>(v, lane);  // value i in lanes kLanes i ..
         if (!CLUSTER && entries == 1) return spread(r, v);
-        float* s = slot + buf * N * entries;
-        float* mine = s + entry * N + lane / kLanes;
         // (this half is free: a warp comes here after the last exchange, which had every warp's sums, and a
         // warp sends those after it has read the half before)
         if constexpr (CLUSTER) {
-            cg::cluster_group cl = cg::this_cluster();
-            const int ctas = static_cast<int>(cl.num_blocks());
+            const int ctas = static_cast<int>(cg::this_cluster().num_blocks());
             uint64_t* bar = bars + buf;
             if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(entries * N * 4));
             for (int c = lane % kLanes; c < ctas; c += kLanes) {  // the lanes of a value take the CTAs in turn
                 uint32_t to, signal;
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_addr(mine)), "r"(c));
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(put), "r"(c));
                 asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(signal) : "r"(smem_addr(bar)), "r"(c));
                 asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to),
                              "r"(__float_as_uint(r)), "r"(signal)
@@ -138,34 +146,41 @@ struct Exchange {
                 atomicOr(err, kErrWaitTimeout);
             }
             phase ^= 1u << buf;
+            buf ^= 1;
         } else {
-            if (lane % kLanes == 0) *mine = r;
+            if (lane % kLanes == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(put), "f"(r) : "memory");
             team_barrier(team, warps);
         }
-        buf ^= 1;
         // 16 entries at a time, half the values a lane
         float t[N / 2] = {};
-        auto take = [&](int e) {
-            const float* q = s + e * N + (lane >> 4) * (N / 2);
+        auto add = [&](uint32_t from) {
             if constexpr (N == 8) {
-                const float4 f = *reinterpret_cast<const float4*>(q);
-                t[0] += f.x;
-                t[1] += f.y;
-                t[2 % (N / 2)] += f.z;
-                t[3 % (N / 2)] += f.w;
+                float f[4];
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
+                             : "r"(from)
+                             : "memory");
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) t[i] += f[i];
             } else if constexpr (N == 4) {
-                const float2 f = *reinterpret_cast<const float2*>(q);
-                t[0] += f.x;
-                t[1 % (N / 2)] += f.y;
+                float f[2];
+                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f[0]), "=f"(f[1]) : "r"(from) : "memory");
+                t[0] += f[0];
+                t[N / 2 - 1] += f[1];
             } else {
-                t[0] += *q;
+                float f;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(from) : "memory");
+                t[0] += f;
             }
         };
         if constexpr (CLUSTER) {
-            for (int e = lane & 15; e < entries; e += 16) take(e);
+            for (int e = lane & 15, i = 0; e < entries; e += 16, ++i) add(take + i * 64 * N);
         } else {
-            if ((lane & 15) < entries) take(lane & 15);
+            if ((lane & 15) < entries) add(take);
         }
+        put += flip;
+        take += flip;
+        flip = -flip;
         spread(halving_sums<N / 2, 8>(t, lane), v);
     }
 
@@ -204,21 +219,27 @@ constexpr int kRowStartBytes = 128;
 template <class T, int LAYOUT, bool CLUSTER>
 struct RowStart {
     static constexpr bool OWN = LAYOUT != LAYOUT_ODD;
-    static __device__ __forceinline__ void fetch(const void* matrix, int64_t row, int64_t row_bytes, char* to) {
+    int64_t row_bytes;
+    int at;       // this lane's 16 bytes of a copy
+    int c;        // and its column (rows shorter than 32 are gone over again)
+    bool copies;  // whether the row has those 16 bytes
+
+    __device__ __forceinline__ RowStart(int cols, int64_t row_bytes_) : row_bytes(row_bytes_) {
+        const int lane = static_cast<int>(threadIdx.x & 31);
+        at = lane * 16;
+        c = cols < 32 ? lane % cols : lane;
+        copies = at < static_cast<int>(min(static_cast<int64_t>(32 * sizeof(T)), row_bytes));
+    }
+    __device__ __forceinline__ void fetch(const void* matrix, int64_t row, char* to) const {
         if constexpr (OWN) {
-            const int lane = threadIdx.x & 31;
-            const int n = static_cast<int>(min(static_cast<int64_t>(32 * sizeof(T)), row_bytes)) >> 4;
-            if (lane < n) cp_async16(smem_addr(to) + lane * 16, static_cast<const char*>(matrix) + (row * row_bytes + lane * 16));
+            if (copies) cp_async16(smem_addr(to) + at, static_cast<const char*>(matrix) + (row * row_bytes + at));
         }
     }
-    // This lane's element (rows shorter than 32 are gone over again): own: the warp's copy, after the row's copies
-    // and __syncwarp(); staged: the row in the ring.
-    static __device__ __forceinline__ float get(const void* matrix, int64_t row, int cols, const char* own, const char* staged) {
-        const int lane = static_cast<int>(threadIdx.x & 31);
-        const int c = cols < 32 ? lane % cols : lane;
+    // This lane's element: own: the warp's copy, after the row's copies and __syncwarp(); staged: the row in the ring.
+    __device__ __forceinline__ float get(const void* matrix, int64_t row, const char* own, const char* staged) const {
         if constexpr (OWN) return to_float(reinterpret_cast<const T*>(own)[c]);
-        const T* start = static_cast<const T*>(matrix) + row * cols;
-        if constexpr (CLUSTER) return to_float(start[c]);
+        const char* start = static_cast<const char*>(matrix) + row * row_bytes;
+        if constexpr (CLUSTER) return to_float(reinterpret_cast<const T*>(start)[c]);
         return to_float(reinterpret_cast<const T*>(staged + (reinterpret_cast<uintptr_t>(start) & 15))[c]);
     }
 };
