@@ -340,7 +340,8 @@ tr_status tr_axis_launch_shape(int32_t sm_count, int32_t op, tr_order order, int
  * LayerNorm's variance is taken in one pass about the mean of the row's first 32
  * elements: rounding errors of the variance grow by 1 + (that mean - the row's
  * mean)^2 / variance, 1 + cols / 32 at most. RMSNorm's squares are plain sums.
- * Values whose squares leave binary32's range give infinite sums (and outputs of 0).
+ * Values whose squares leave binary32's range give infinite sums: normalised
+ * values of 0 forward, and gradients that need not be finite.
  *
  * rows = 0 writes zeros to the column gradients and nothing else. order must be
  * TR_ORDER_UNORDERED_TREE: the others return TR_ERR_UNSUPPORTED. No call
@@ -524,8 +525,8 @@ const char* tr_last_error_message(void);
  *      gives up at once: no CTA of the row writes outputs.
  * Applies to the launches made while it is set, including
  * tr_split_rows_noalloc_f32. A launch that gave up leaves every workspace and
- * the no-allocation scratch ready for the next launch. Other bits:
- * TR_ERR_INVALID_ARG. */
+ * the no-allocation scratch ready for the next launch. The waits of the block
+ * norms are not changed by it. Other bits: TR_ERR_INVALID_ARG. */
 tr_status tr_debug_force_wait_timeout(int32_t mode);
 
 /* Library version, major * 10000 + minor * 100 + patch. */
