@@ -84,6 +84,7 @@ struct ReadRow {
         const int64_t n = cl.num_blocks(), r = cl.block_rank();
         begin = static_cast<int>(cols * r / n);
         end = static_cast<int>(cols * (r + 1) / n);
+        if (n > 1) cl.sync();  // every CTA of the cluster runs before it is written to
     }
     // f(column) for this thread's columns, four loads deep: f gives what g(column, value) then takes
     template <class F, class G>

@@ -454,3 +454,26 @@ def test_calls_from_several_threads():
         t.join()
     assert not bad
     assert tr.tr_last_device_error() == tr.TR_OK
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 131080), (3, 70001)])
+@pytest.mark.parametrize("kind", ["rmsnorm", "layernorm"])
+def test_clusters_that_start_while_the_device_is_full(rows, cols, kind):
+    """A cluster's CTAs may begin one after another: the first sums of a row wait for all of them. Calls are queued behind
+    and beside launches that hold every SM, so that their CTAs start as SMs come free."""
+    d = make(rows, cols, 1, "f32", kind, True, True, seed=12)
+    y0, h0 = check_forward(d, "f32", kind, True, True)
+    g0 = check_backward(d, "f32", kind, True, True)
+    full = make(4000, 4096, 0, "bf16", kind, True, True, seed=13)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(10):
+        tr.gated_residual_norm(full["x"], full["branch"], kind=kind, stream=side)
+        got.append((tr.gated_residual_norm(d["x"], d["branch"], **args(d, "post_weight", "post_bias", "gate", "weight", "bias"),
+                                           eps=EPS, kind=kind), run_backward(d, kind, True, True)))
+    torch.cuda.synchronize()
+    for (y, h), g in got:
+        assert torch.equal(y, y0) and torch.equal(h, h0)
+        assert all(a is None and b is None or torch.equal(a, b) for a, b in zip(g, g0))
+    assert tr.tr_last_device_error() == tr.TR_OK
