@@ -45,18 +45,30 @@ __global__ void __launch_bounds__(kReadThreads) bwd_read_kernel(const BlockBwArg
         const ReadParam gate(p.gate ? p.gate + row / p.group_rows * cols : nullptr, 1);
         auto u_of = [&](int c) { return to_float(dyr[c]) * pre_w(c); };
         // squares of h and a, u h, u, h and a, about shifts
-        const float kh = LAYER && PRE ? lane_mean(to_float(hr[start])) : 0.0f;
-        const float ka = LAYER && POST ? lane_mean(to_float(ar[start])) : 0.0f;
-        float s[6];
-        rr.sums<6>([&](int c) {
-            const float h = PRE ? to_float(hr[c]) - kh : 0.0f, a = POST ? to_float(ar[c]) - ka : 0.0f;
-            const float u = PRE ? u_of(c) : 0.0f;
-            return Values<6>{{h * h, a * a, u * h, LAYER ? u : 0.0f, LAYER ? h : 0.0f, LAYER ? a : 0.0f}};
-        }, s);
-        const float off_h = s[4] * inv_n, off_a = s[5] * inv_n;
+        float kh = LAYER && PRE ? lane_mean(to_float(hr[start])) : 0.0f;
+        float ka = LAYER && POST ? lane_mean(to_float(ar[start])) : 0.0f;
+        float s[6], off_h, off_a, sq_h, sq_a;
+        for (bool again = false;; again = true) {
+            rr.sums<6>([&](int c) {
+                const float h = PRE ? to_float(hr[c]) - kh : 0.0f, a = POST ? to_float(ar[c]) - ka : 0.0f;
+                const float u = PRE ? u_of(c) : 0.0f;
+                return Values<6>{{h * h, a * a, u * h, LAYER ? u : 0.0f, LAYER ? h : 0.0f, LAYER ? a : 0.0f}};
+            }, s);
+            off_h = s[4] * inv_n;
+            off_a = s[5] * inv_n;
+            sq_h = s[0];
+            sq_a = s[1];
+            if (!LAYER) break;
+            bool far_h, far_a;
+            sq_h = squares_about_mean(s[0], s[4], off_h, far_h);
+            sq_a = squares_about_mean(s[1], s[5], off_a, far_a);
+            if (again || (!far_h && !far_a)) break;  // (alike in all threads of the row)
+            kh += off_h;
+            ka += off_a;
+        }
         const float mh = kh + off_h, ma = ka + off_a, c1 = s[3] * inv_n;
-        const float rh = PRE ? rsqrtf(fmaf(LAYER ? squares_about_mean(s[0], s[4], off_h) : s[0], inv_n, p.eps)) : 0.0f;
-        const float ra = POST ? rsqrtf(fmaf(LAYER ? squares_about_mean(s[1], s[5], off_a) : s[1], inv_n, p.eps)) : 0.0f;
+        const float rh = PRE ? rsqrtf(fmaf(sq_h, inv_n, p.eps)) : 0.0f;
+        const float ra = POST ? rsqrtf(fmaf(sq_a, inv_n, p.eps)) : 0.0f;
         const float c2 = fmaf(-off_h, s[3], s[2]) * inv_n * rh;
         auto ah_of = [&](int c) { return POST ? (to_float(ar[c]) - ma) * ra : 0.0f; };
         auto d_of = [&](int c) {

@@ -30,15 +30,28 @@ __global__ void __launch_bounds__(kReadThreads) fwd_read_kernel(const BlockArgs 
         const ReadParam gate(p.gate ? p.gate + row / p.group_rows * cols : nullptr, 1);
         // mean and 1 / sqrt(mean square about it + eps) of v(column)
         auto statistics = [&](auto&& v, float& mean, float& r) {
-            const float shift = LAYER ? lane_mean(v(start)) : 0.0f;
+            float shift = LAYER ? lane_mean(v(start)) : 0.0f;
             float s[2];
-            rr.sums<2>([&](int c) {
-                const float d = v(c) - shift;
-                return Values<2>{{d * d, LAYER ? d : 0.0f}};
-            }, s);
-            const float off = s[1] * inv_n;
+            auto sums_about = [&](float about) {
+                rr.sums<2>([&](int c) {
+                    const float d = v(c) - about;
+                    return Values<2>{{d * d, LAYER ? d : 0.0f}};
+                }, s);
+            };
+            sums_about(shift);
+            float off = s[1] * inv_n, squares = s[0];
+            if constexpr (LAYER) {
+                bool far;
+                squares = squares_about_mean(s[0], s[1], off, far);
+                if (far) {  // (alike in all threads of the row)
+                    shift += off;
+                    sums_about(shift);
+                    off = s[1] * inv_n;
+                    squares = squares_about_mean(s[0], s[1], off, far);
+                }
+            }
             mean = shift + off;
-            r = rsqrtf(fmaf(LAYER ? squares_about_mean(s[0], s[1], off) : s[0], inv_n, p.eps));
+            r = rsqrtf(fmaf(squares, inv_n, p.eps));
         };
         float ma = 0.0f, ra = 1.0f;
         if (p.post) statistics([&](int c) { return to_float(ar[c]); }, ma, ra);

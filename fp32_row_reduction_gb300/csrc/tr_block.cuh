@@ -27,18 +27,23 @@ constexpr int kReadCluster = 8;  // most CTAs of a row that is read again for ea
 
 // A shift for a row's LayerNorm sums: the mean of its first 32 elements, which every warp of the row finds
 // alike. Sums are taken about it in one pass, and the variance is S2 / n - (S1 / n)^2; the cancellation
-// costs 1 + (shift - mean)^2 / variance of precision: 1 + 1/32 for independent elements, and at worst 1 + n / 32 (all of
-// the row's spread in the 32).
+// costs 1 + (shift - mean)^2 / variance of precision: 1 + 1/32 for independent elements. Where it would cost more than
+// 4/3 (squares_about_mean) the row's sums are taken once more, about the mean that the first ones gave.
 __device__ __forceinline__ float lane_mean(float v) {
     v *= 1.0f / 32.0f;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
     return v;
 }
-// The sum of squares about the mean, from the sums s2 of squares and s1 about a shift that is d off the mean. A
-// rounding below zero counts as zero; what is infinite or no number stays so.
-__device__ __forceinline__ float squares_about_mean(float s2, float s1, float d) {
-    return fabsf(s2) <= 3.0e38f ? fmaxf(fmaf(-d, s1, s2), 0.0f) : s2;
+// The sum of squares about the mean, from the sums s2 of squares and s1 about a shift that is d off the mean. `far`:
+// d^2 is more than a third of the variance, and the sums are to be taken again. Otherwise a rounding u of each of a sum's
+// L steps stays below (4/3 + 4/3) L u of the variance (s2 is 4/3 of it, and 2 d s1 at most as much): 70 u for the
+// longest chain, 26. One row in a thousand of independent normal elements is far. All threads of a row have the same
+// sums, and answer alike. What is infinite or no number stays so, and is not far.
+__device__ __forceinline__ float squares_about_mean(float s2, float s1, float d, bool& far) {
+    const float v = fmaf(-d, s1, s2), least = 0.75f * s2;
+    far = v < least;
+    return fmaxf(v, least);  // (least where v is infinity less infinity)
 }
 // A long sum with the rounding error of each step added up beside it (Knuth's two-sum), so that a row of 2^24 columns
 // loses no more than a short one. (Totals in binary64 made the kernels twice as slow.)

@@ -9,7 +9,8 @@
 // the row. So the arithmetic is on pairs (f32x2), which norms there are is known when the kernel is
 // compiled, and there is one exchange between warps a row: the next row's statistics travel with
 // this row's sum of q ah. LayerNorm's sums are taken about a shift that each warp finds for itself
-// (lane_mean), so means and variances need no second exchange and no second pass.
+// (lane_mean), so means and variances need no second exchange and no second pass, but for a row whose shift is far
+// from its mean (all rows far: 8192 x 4096 bf16 131 us against 96).
 #pragma once
 
 #include "tr_block_rows.cuh"
@@ -25,6 +26,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
     constexpr int K = S * P;       // pairs of a thread
     constexpr int V = LAYER ? 4 : 2;
     constexpr bool ODD = LAYOUT == LAYOUT_ODD;
+    constexpr bool RELOAD = SPARAM || (LAYER && S == 2);  // a - mean is taken from the ring again, not kept
     const bool pre = MODE ? (MODE & TR_BLOCK_PRE) != 0 : p.pre != 0;
     const bool post = MODE ? (MODE & TR_BLOCK_POST) != 0 : p.post != 0;
     extern __shared__ uint4 smem[];
@@ -175,19 +177,14 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
     // ---- a row's statistics ----
     float mean_h = 0.0f, mean_a = 0.0f, c1 = 0.0f;  // LayerNorm: means of h, a, u
     float rh = 0.0f, ra = 0.0f, k2 = 0.0f;
+    bool far_h = false, far_a = false;  // LayerNorm: the row's sums are to be taken again
     // The statistics of row `row` in `stage` (when it is there: `more`), with the sums of q and q (a - mean) of the
     // row before, which end in qs and qa for between(). D = dh + r_h (u - c1 - (h - mean) k2) with
     // k2 = r_h^2 mean(u (h - mean)). rsqrtf is good to 2^-22, as the sums are.
-    auto statistics = [&](int stage, int64_t row, bool more, float& qs, float& qa, auto&& between) {
-        const char* m = ring + stage * stage_bytes;
-        float sh = 0.0f, sa = 0.0f;
-        // sums of squares of h and a, and of u h, u, h and a (all about the shifts)
+    // Sums of row `row` staged at m about sh and sa: squares of h and a, and u h; sum[3] as it comes; for LayerNorm u,
+    // h and a, and sum[7] as it comes.
+    auto sums_about = [&](const char* m, int64_t row, bool more, float sh, float sa, float (&sum)[LAYER ? 8 : 4]) {
         float2 hh = both(0.0f), aa = both(0.0f), uh = both(0.0f), u1 = both(0.0f), h1 = both(0.0f), a1 = both(0.0f);
-        if constexpr (LAYER) {
-            __syncwarp();
-            if (pre && more) sh = lane_mean(row_start.get(p.h, row, starts + stage * g.sampled, m));
-            if (post && more) sa = lane_mean(row_start.get(p.a, row, starts + stage * g.sampled + kRowStartBytes, m + at_a));
-        }
         if (more) {
 #pragma unroll
             for (int s = 0; s < S; ++s) {
@@ -225,26 +222,39 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
                 }
             }
         }
-        float sq_h, sq_a, sum_uh, next_h = 0.0f, next_a = 0.0f, next_c1 = 0.0f;
+        sum[0] = hh.x + hh.y;
+        sum[1] = aa.x + aa.y;
+        sum[2] = uh.x + uh.y;
         if constexpr (LAYER) {
-            float v[8] = {hh.x + hh.y, aa.x + aa.y, uh.x + uh.y, qa, u1.x + u1.y, h1.x + h1.y, a1.x + a1.y, qs};
-            ex.sums(v);
-            qa = v[3];
+            sum[4] = u1.x + u1.y;
+            sum[5] = h1.x + h1.y;
+            sum[6] = a1.x + a1.y;
+        }
+        ex.sums(sum);
+    };
+    auto statistics = [&](int stage, int64_t row, bool more, float& qs, float& qa, auto&& between) {
+        const char* m = ring + stage * stage_bytes;
+        float sh = 0.0f, sa = 0.0f;
+        if constexpr (LAYER) {
+            __syncwarp();
+            if (pre && more) sh = lane_mean(row_start.get(p.h, row, starts + stage * g.sampled, m));
+            if (post && more) sa = lane_mean(row_start.get(p.a, row, starts + stage * g.sampled + kRowStartBytes, m + at_a));
+        }
+        float v[LAYER ? 8 : 4];
+        v[3] = qa;
+        if constexpr (LAYER) v[7] = qs;
+        sums_about(m, row, more, sh, sa, v);
+        qa = v[3];
+        float sq_h = v[0], sq_a = v[1], sum_uh = v[2], next_h = 0.0f, next_a = 0.0f, next_c1 = 0.0f;
+        if constexpr (LAYER) {
             qs = v[7];
             const float dh = v[5] * inv_n, da = v[6] * inv_n;  // the means, from the shifts
-            sq_h = squares_about_mean(v[0], v[5], dh);
-            sq_a = squares_about_mean(v[1], v[6], da);
+            sq_h = squares_about_mean(v[0], v[5], dh, far_h);
+            sq_a = squares_about_mean(v[1], v[6], da, far_a);
             sum_uh = fmaf(-dh, v[4], v[2]);
             next_h = sh + dh;
             next_a = sa + da;
             next_c1 = v[4] * inv_n;
-        } else {
-            float v[4] = {hh.x + hh.y, aa.x + aa.y, uh.x + uh.y, qa};
-            ex.sums(v);
-            qa = v[3];
-            sq_h = v[0];
-            sq_a = v[1];
-            sum_uh = v[2];
         }
         between();
         mean_h = next_h;
@@ -272,7 +282,29 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
 
     int stage = 0, fill = g.stages - 1;
     int64_t left = 0;  // rows of the running group still to come
-    for (int64_t row = slab.begin; row < slab.end; ++row) {
+    int64_t row = slab.begin;
+    // Sums about a shift too far from the mean are taken again about that mean (by all warps of the row alike), before the
+    // row uses them, between two rows. A test in the middle of a row's chain, where the sums come in, costs 8192 x 4096 f32
+    // 47 us.
+    auto take_again = [&]() {
+        float v[LAYER ? 8 : 4] = {};
+        sums_about(ring + stage * stage_bytes, row, true, mean_h, mean_a, v);
+        if constexpr (LAYER) {
+            const float dh = v[5] * inv_n, da = v[6] * inv_n;
+            bool again;  // (not asked: the shift is the mean)
+            if (far_h) {
+                rh = rsqrtf(fmaf(squares_about_mean(v[0], v[5], dh, again), inv_n, p.eps));
+                k2 = fmaf(-dh, v[4], v[2]) * inv_n * rh * rh;
+                mean_h += dh;
+            }
+            if (far_a) {
+                ra = rsqrtf(fmaf(squares_about_mean(v[1], v[6], da, again), inv_n, p.eps));
+                mean_a += da;
+            }
+        }
+        far_h = far_a = false;
+    };
+    auto one_row = [&]() {
         if (left == 0) {
             enter_group(row);
             left = p.slices > 0 ? slab.end - slab.begin : p.group_rows;
@@ -288,7 +320,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
         const bool more = row + 1 < slab.end;
 
         // D, dx, the column sums of the pre-norm, and the sums of q (a - mean) and q
-        float2 d[K], av[SPARAM ? 1 : K];  // D, and a - mean (SPARAM: taken from the ring again)
+        float2 d[K], av[RELOAD ? 1 : K];  // D, and a - mean
         float2 qa2 = both(0.0f), qs2 = both(0.0f);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
@@ -325,7 +357,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
                     if (LAYER && post) x[j] = __fadd2_rn(x[j], both(-mean_a));
-                    if constexpr (!SPARAM) av[s * P + j] = x[j];
+                    if constexpr (!RELOAD) av[s * P + j] = x[j];
                 }
                 float2 qv[P];
                 get_pairs(1, qw, s, qv);
@@ -349,7 +381,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
             for (int s = 0; s < S; ++s) {
                 float2 o[P], qv[P], c[P];
                 get_pairs(1, qw, s, qv);
-                if constexpr (SPARAM) {
+                if constexpr (RELOAD) {
                     if (need_a) {
                         ln.load(m + at_a, p.a, row, s, c);
                         if (LAYER && post)
@@ -381,6 +413,24 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
             }
             if (--left == 0 && p.slices == 0 && p.sums) leave_group(row);
         });
+        ++row;
+    };
+    // Which form the loop takes only decides how well it compiles: rows that follow one another in an inner loop that a far
+    // row leaves (8192 x 4096 f32 129 us against 165, 6039 x 2560 f16 60 against 68), or one loop that tests each
+    // row (16384 x 2048 bf16 94 us against 97, 8192 x 2049 bf16 181 against 195).
+    if constexpr (LAYER && (SPARAM || sizeof(T) == 4)) {
+        do {
+            if (far_h || far_a) take_again();
+            do one_row();
+            while (row < slab.end && !(far_h || far_a));
+        } while (row < slab.end);
+    } else {
+        while (row < slab.end) {
+            if constexpr (LAYER) {
+                if (__any_sync(kFull, far_h || far_a)) take_again();
+            }
+            one_row();
+        }
     }
     if (p.sums) {
         float* part = p.part + index * V * cols + col0;

@@ -1,10 +1,11 @@
 // The gated residual norm with the rows on chip: h = rs x + bs gate post(a), y = pre(h).
 //
 // HBM-bound: x and a are read, h and y written once (16384 x 4096 bf16: RMSNorm 83 us, 95% of the measured copy rate,
-// LayerNorm 88 us). A row's y waits for the statistics of h, which
+// LayerNorm 89 us). A row's y waits for the statistics of h, which
 // wait for those of a; so that a row costs one exchange between its warps, the sum over h of a row
 // travels with the sum over a of the next one. LayerNorm's sums are taken about a shift that each warp
-// finds for itself (lane_mean; for h from the same elements' own x and a). The parameters of a thread's columns
+// finds for itself (lane_mean; for h from the same elements' own x and a), and once more for a row whose shift is far
+// from its mean. The parameters of a thread's columns
 // stay in its registers for all its rows.
 #pragma once
 
@@ -104,8 +105,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
     float2 h[K];
     float ra = 1.0f, ma = 0.0f;  // of the row at work
     float rh = 1.0f, mh = 0.0f;
-    // the sums over h about sh (where `this_row`) and over a of row `row` staged at m about sa (where `next_row`)
-    auto statistics = [&](const char* m, int64_t row, bool this_row, bool next_row, float sh, float sa) {
+    bool far_h = false, far_a = false;  // LayerNorm: the row before's sums over h, and this row's over a, are to be taken again
+    // the sums over h about sh (where `this_row`) and over a of row `row` staged at m about sa (where `next_row`):
+    // squares of h and a, and for LayerNorm h and a
+    auto sums_about = [&](const char* m, int64_t row, bool this_row, bool next_row, float sh, float sa, float (&sum)[LAYER ? 4 : 2]) {
         float2 hh = both(0.0f), aa = both(0.0f), h1 = both(0.0f), a1 = both(0.0f);
         auto shifted = [&](float2 v, float shift, bool xi, bool yi) {
             if constexpr (!LAYER) return v;
@@ -132,20 +135,24 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
                 });
             }
         }
-        float sq_h, sq_a;
+        sum[0] = hh.x + hh.y;
+        sum[1] = aa.x + aa.y;
         if constexpr (LAYER) {
-            float v[4] = {hh.x + hh.y, aa.x + aa.y, h1.x + h1.y, a1.x + a1.y};
-            ex.sums(v);
+            sum[2] = h1.x + h1.y;
+            sum[3] = a1.x + a1.y;
+        }
+        ex.sums(sum);
+    };
+    auto statistics = [&](const char* m, int64_t row, bool this_row, bool next_row, float sh, float sa) {
+        float v[LAYER ? 4 : 2];
+        sums_about(m, row, this_row, next_row, sh, sa, v);
+        float sq_h = v[0], sq_a = v[1];
+        if constexpr (LAYER) {
             const float dh = v[2] * inv_n, da = v[3] * inv_n;  // the means, from the shifts
-            sq_h = squares_about_mean(v[0], v[2], dh);
-            sq_a = squares_about_mean(v[1], v[3], da);
+            sq_h = squares_about_mean(v[0], v[2], dh, far_h);
+            sq_a = squares_about_mean(v[1], v[3], da, far_a);
             mh = sh + dh;
             if (p.post) ma = sa + da;
-        } else {
-            float v[2] = {hh.x + hh.y, aa.x + aa.y};
-            ex.sums(v);
-            sq_h = v[0];
-            sq_a = v[1];
         }
         // rsqrtf is good to 2^-22, as the sums are
         rh = rsqrtf(fmaf(sq_h, inv_n, p.eps));
@@ -166,8 +173,36 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
         a_here = row_start.get(p.a, begin, starts, ring);
     }
     if (p.post) statistics(ring, begin, false, true, 0.0f, LAYER ? lane_mean(a_here) : 0.0f);
+    auto write_y = [&](int64_t row) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            float2 o[P];
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const int k = s * P + j;
+                const float2 c = LAYER ? __fadd2_rn(h[k], both(-mh)) : h[k];
+                const float2 n = __fmul2_rn(c, both(rh));
+                o[j] = LAYER ? __ffma2_rn(n, w[k], b[LAYER ? k : 0]) : __fmul2_rn(n, w[k]);
+            }
+            ln.store(p.y, row, s, o);
+        }
+    };
     int stage = 0, fill = g.stages - 1;
-    for (int64_t row = begin; row < end; ++row) {
+    int64_t row = begin;
+    // Sums about a shift too far from the mean are taken again about that mean (by all warps of the row alike) between two
+    // rows, and the row before is normalised again. A test in the middle of a row's chain costs 16384 x 4096 bf16 12 us.
+    auto take_again = [&]() {
+        const bool again_h = far_h, again_a = far_a;
+        const float here_ra = ra, here_ma = ma;
+        statistics(ring + stage * stage_bytes, row, again_h, again_a, mh, ma);
+        if (!again_a) {
+            ra = here_ra;
+            ma = here_ma;
+        }
+        if (again_h) write_y(row - 1);
+        far_h = far_a = false;
+    };
+    auto one_row = [&]() {
         if (left == 0) {
             enter_group(row);
             if constexpr (LAYER) enter_probe(row);
@@ -217,19 +252,27 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
         }
         statistics(next, row + 1, true, more, LAYER ? lane_mean(h_here) : 0.0f, LAYER ? lane_mean(a_next) : 0.0f);
         a_here = a_next;
-        if (p.pre) {
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                float2 o[P];
-#pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    const int k = s * P + j;
-                    const float2 c = LAYER ? __fadd2_rn(h[k], both(-mh)) : h[k];
-                    const float2 n = __fmul2_rn(c, both(rh));
-                    o[j] = LAYER ? __ffma2_rn(n, w[k], b[LAYER ? k : 0]) : __fmul2_rn(n, w[k]);
-                }
-                ln.store(p.y, row, s, o);
+        if (p.pre) write_y(row);
+        ++row;
+    };
+    // Which form the loop takes only decides how well it compiles: rows that follow one another in an inner loop that a far
+    // row leaves (2048 x 20000 bf16 103 us against 112, 8192 x 7000 f32 164 against 197), or one loop that
+    // tests each row (16384 x 4096 bf16 89 us against 93, 8192 x 2049 bf16 73 against 78).
+    if constexpr (LAYER && LAYOUT == LAYOUT_ALIGNED) {
+        do {
+            if (far_h || far_a) take_again();
+            if (row < end) {
+                do one_row();
+                while (row < end && !(far_h || far_a));
             }
+        } while (row < end || far_h || far_a);
+    } else {
+        for (;;) {
+            if constexpr (LAYER) {
+                if (__any_sync(kFull, far_h || far_a)) take_again();
+            }
+            if (row >= end) break;
+            one_row();
         }
     }
     if constexpr (CLUSTER) cg::this_cluster().sync();  // no CTA leaves while another may still write to it

@@ -337,9 +337,9 @@ tr_status tr_axis_launch_shape(int32_t sm_count, int32_t op, tr_order order, int
  * may run at the same time need one each. All sums have a fixed order: results
  * repeat bit for bit on one device.
  *
- * LayerNorm's variance is taken in one pass about the mean of the row's first 32
- * elements: rounding errors of the variance grow by 1 + (that mean - the row's
- * mean)^2 / variance, 1 + cols / 32 at most. RMSNorm's squares are plain sums.
+ * LayerNorm's variance is taken about the mean of the row's first 32 elements, and again about
+ * the row's own mean where the two are further apart than the root of a third of the variance: rounding
+ * errors of the sums grow by 8/3 at most for any row. RMSNorm's squares are plain sums.
  * Values whose squares leave binary32's range give infinite sums: normalised
  * values of 0 forward, and gradients that need not be finite.
  *

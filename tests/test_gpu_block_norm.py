@@ -477,3 +477,33 @@ def test_clusters_that_start_while_the_device_is_full(rows, cols, kind):
         assert torch.equal(y, y0) and torch.equal(h, h0)
         assert all(a is None and b is None or torch.equal(a, b) for a, b in zip(g, g0))
     assert tr.tr_last_device_error() == tr.TR_OK
+
+
+@pytest.mark.parametrize("rows,cols", [(6, 777), (700, 1032), (6, 4096), (6, 4100), (300, 4096), (5, 9000), (6, 20000), (3, 40001),
+                                       (2, 70000), (170, 70001)])
+@pytest.mark.parametrize("kind_of_start", ["4 sigma", "16 sigma", "most of the variance"])
+def test_layernorm_keeps_its_precision_when_a_row_starts_unlike_the_rest(rows, cols, kind_of_start):
+    """Rows whose first 32 elements are far from the mean keep the ordinary bounds, all results alike. So do
+    ordinary rows between them, whose results are the same bits as with no such neighbour."""
+    d = make(rows, cols, 1, "f32", "layernorm", True, True, seed=21, mean=0.2)
+    plain = {k: None if v is None else v.clone() for k, v in d.items()}
+    far = torch.arange(rows, device=DEV) % 3 != 1
+    for k, sigma in (("x", 1.5), ("branch", 0.7), ("h", 2.0)):
+        shift = {"4 sigma": 4 * sigma, "16 sigma": -16 * sigma, "most of the variance": 500.0}[kind_of_start]
+        d[k][:, :32] += shift * far[:, None]
+    y, h = check_forward(d, "f32", "layernorm", True, True, 0.9, 1.1)
+    g = check_backward(d, "f32", "layernorm", True, True, 0.9, 1.1)
+    y0, h0 = check_forward(plain, "f32", "layernorm", True, True, 0.9, 1.1)
+    g0 = run_backward(plain, "layernorm", True, True, 0.9, 1.1)
+    for a, b in ((y, y0), (h, h0), (g.dx, g0.dx), (g.dbranch, g0.dbranch)):
+        assert torch.equal(a[~far], b[~far])
+
+
+@pytest.mark.parametrize("cols", [512, 4100, 20000])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_layernorm_of_16_bit_rows_that_start_unlike_the_rest(cols, dtype):
+    d = make(40, cols, 8, dtype, "layernorm", True, True, seed=22)
+    for k in ("x", "branch", "h"):
+        d[k][:, :32] += 100.0
+    check_forward(d, dtype, "layernorm", True, True)
+    check_backward(d, dtype, "layernorm", True, True)
