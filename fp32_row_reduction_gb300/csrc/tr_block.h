@@ -27,6 +27,8 @@ struct BlockArgs {
     int post, pre;  // which norms there are
     float rs, bs, eps;
     unsigned* err;  // device error word (clusters' bounded waits; set by the launch)
+    int debug;      // testing modes (kDebugModes) of those waits; set by the launch
+    float start;    // what those exchanges' sums start from (0; see Exchange); set by the launch
 };
 
 struct BlockBwArgs {
@@ -57,6 +59,8 @@ struct BlockBwArgs {
     float* stats;     // re-read path: kBlockStats floats a row
     float* part;      // slabs x vectors x cols partial column sums
     unsigned* err;    // device error word (clusters' bounded waits; set by the launch)
+    int debug;        // testing modes (kDebugModes) of those waits; set by the launch
+    float start;      // what those exchanges' sums start from (0; see Exchange); set by the launch
 };
 
 // The rows of a slab. With slices > 0 a slab is one of the `slices` equal parts

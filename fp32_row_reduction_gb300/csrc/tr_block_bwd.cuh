@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
     const Lanes<T, S, LAYOUT> ln(t, tt, cols, col0, g.cta_vecs);
     const float inv_n = 1.0f / static_cast<float>(cols);
     char* const team_smem = reinterpret_cast<char*>(smem) + team * team_bytes(g);
-    Exchange<CLUSTER, LAYER ? 8 : 4> ex(team_smem, g.warps * g.cluster, rank * g.warps + (t >> 5), team, g.warps, p.err);
+    Exchange<CLUSTER, LAYER ? 8 : 4> ex(team_smem, g.warps * g.cluster, rank * g.warps + (t >> 5), team, g.warps, p.err, p.start);
     ex.init();
     const int stage_bytes = g.tensors * g.tensor_bytes;
     const RowStart<T, LAYOUT, CLUSTER> row_start(cols, ln.row_bytes);  // LayerNorm's
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) bwd_kernel(const BlockBwArgs p,
             }
         }
     }
-    if constexpr (CLUSTER) cg::this_cluster().sync();  // no CTA leaves while another may still write to it
+    ex.finish(p.debug);
 }
 
 // ---- host side -------------------------------------------------------------
@@ -463,7 +463,11 @@ cudaError_t bwd_go(const BlockBwArgs& in, const RowShape& shape, cudaStream_t st
     BlockBwArgs a = in;
     RowShape g = shape;
     if (!SPARAM) g.params = 0;
-    if (CLUSTER && !(a.err = device_error_word())) return cudaErrorInvalidValue;
+    if (CLUSTER) {
+        if (!(a.err = device_error_word())) return cudaErrorInvalidValue;
+        a.debug = debug_flags_now();
+        a.start = a.debug & kDebugExpirePeers ? NAN : 0.0f;
+    }
     const int threads = g.teams * g.warps * 32;
     const size_t smem = row_smem(g);
     const auto kernel = bwd_kernel<T, LAYER, S, LAYOUT, CLUSTER, MODE, THREADS, CTAS, SPARAM>;

@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
     const Lanes<T, S, LAYOUT> ln(t, tt, cols, col0, g.cta_vecs);
     const float inv_n = 1.0f / static_cast<float>(cols);
     char* const team_smem = reinterpret_cast<char*>(smem) + team * team_bytes(g);
-    Exchange<CLUSTER, LAYER ? 4 : 2> ex(team_smem, g.warps * g.cluster, rank * g.warps + (t >> 5), team, g.warps, p.err);
+    Exchange<CLUSTER, LAYER ? 4 : 2> ex(team_smem, g.warps * g.cluster, rank * g.warps + (t >> 5), team, g.warps, p.err, p.start);
     ex.init();
     const int stage_bytes = g.tensors * g.tensor_bytes;
     const RowStart<T, LAYOUT, CLUSTER> row_start(cols, ln.row_bytes);  // LayerNorm's
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
             one_row();
         }
     }
-    if constexpr (CLUSTER) cg::this_cluster().sync();  // no CTA leaves while another may still write to it
+    ex.finish(p.debug);
 }
 
 // ---- host side -------------------------------------------------------------
@@ -283,7 +283,11 @@ __global__ void __launch_bounds__(THREADS, CTAS) fwd_kernel(const BlockArgs p, c
 template <class T, bool LAYER, int S, int LAYOUT, bool CLUSTER, int THREADS, int CTAS>
 cudaError_t fwd_go_with(const BlockArgs& in, const RowShape& g, cudaStream_t stream) {
     BlockArgs a = in;
-    if (CLUSTER && !(a.err = device_error_word())) return cudaErrorInvalidValue;
+    if (CLUSTER) {
+        if (!(a.err = device_error_word())) return cudaErrorInvalidValue;
+        a.debug = debug_flags_now();
+        a.start = a.debug & kDebugExpirePeers ? NAN : 0.0f;
+    }
     const int threads = g.teams * g.warps * 32;
     const size_t smem = row_smem(g);
     const auto kernel = fwd_kernel<T, LAYER, S, LAYOUT, CLUSTER, THREADS, CTAS>;

@@ -13,10 +13,12 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 
 #include "tr_block.cuh"
 #include "tr_block.h"
+#include "tr_internal.h"
 #include "tr_launch.h"
 
 namespace tr {
@@ -93,13 +95,17 @@ struct Exchange {
     unsigned* err;
     int buf = 0;
     unsigned phase = 0;  // of both mbarriers, one bit each
-    // A wait that gives up sets the error word, and the results are void. Later waits of the kernel are
-    // short then, but there still is one for every phase: no CTA ends with stores to it under way.
-    unsigned limit_ns = 2000000000u;
+    // After a wait that gave up all sums of the warp are NaN, so what is computed from them is no number, and the
+    // kernel's end sets the error word. (Leaving the stores out instead takes a test at each: backward 8192 x 8192 bf16
+    // 190 us against 174.) Later waits of the kernel are short then, but there still is one for every phase: no
+    // CTA ends with stores to it under way.
+    static constexpr unsigned kLimitNs = 2000000000u, kLateNs = 1000000u;
+    float start;  // of the sums over the warps: 0, or NaN
 
     // `entry`: this warp's place among the row's. Addresses are found once: the exchange is a fifth of the instructions.
-    __device__ __forceinline__ Exchange(char* smem, int entries_, int entry, int team_, int warps_, unsigned* err_)
-        : entries(entries_), team(team_), warps(warps_), bars(reinterpret_cast<uint64_t*>(smem)), err(err_) {
+    // `first`: 0, or (testing) NaN, as if a wait had given up before.
+    __device__ __forceinline__ Exchange(char* smem, int entries_, int entry, int team_, int warps_, unsigned* err_, float first)
+        : entries(entries_), team(team_), warps(warps_), bars(reinterpret_cast<uint64_t*>(smem)), err(err_), start(first) {
         const int lane = threadIdx.x & 31;
         const uint32_t slot = smem_addr(smem + 16);
         put = slot + 4 * (entry * N + lane / kLanes);
@@ -119,6 +125,15 @@ struct Exchange {
                 mbar_init(bars + 1, 1);
                 fence_barrier_init();
             }
+        }
+    }
+    // After the last exchange: waits that gave up are reported, and no CTA of the cluster leaves while another may still write
+    // to it. (testing, `debug`: one more wait, on a phase that nothing completes)
+    __device__ __forceinline__ void finish(int debug) {
+        if constexpr (CLUSTER) {
+            if ((debug & kDebugForceTimeout) && threadIdx.x == 0) mbar_wait_bounded(bars + buf, (phase >> buf) & 1, kLateNs, err);
+            if (start != 0.0f) atomicOr(err, kErrWaitTimeout);
+            cg::this_cluster().sync();
         }
     }
 
@@ -141,10 +156,7 @@ struct Exchange {
                              "r"(__float_as_uint(r)), "r"(signal)
                              : "memory");
             }
-            if (!wait(bar, (phase >> buf) & 1, limit_ns)) {
-                limit_ns = 1000000u;
-                atomicOr(err, kErrWaitTimeout);
-            }
+            if (!wait(bar, (phase >> buf) & 1, start == 0.0f ? kLimitNs : kLateNs)) start = NAN;
             phase ^= 1u << buf;
             buf ^= 1;
         } else {
@@ -152,7 +164,9 @@ struct Exchange {
             team_barrier(team, warps);
         }
         // 16 entries at a time, half the values a lane
-        float t[N / 2] = {};
+        float t[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) t[i] = CLUSTER ? start : 0.0f;
         auto add = [&](uint32_t from) {
             if constexpr (N == 8) {
                 float f[4];

@@ -347,7 +347,8 @@ tr_status tr_axis_launch_shape(int32_t sm_count, int32_t op, tr_order order, int
  * TR_ORDER_UNORDERED_TREE: the others return TR_ERR_UNSUPPORTED. No call
  * allocates or waits on the host, and all may be captured into a graph, the first
  * call of a process too. Rows that are split over several thread blocks meet in
- * bounded waits (two seconds): one that gave up is reported by tr_last_device_error. */
+ * bounded waits (two seconds). One that gave up is reported by tr_last_device_error, and what the
+ * call computes from that row's sums, and from later ones', is NaN. */
 typedef enum tr_dtype { TR_F32 = 0, TR_BF16 = 1, TR_F16 = 2 } tr_dtype;
 typedef enum tr_norm_kind { TR_NORM_RMS = 0, TR_NORM_LAYER = 1 } tr_norm_kind;
 #define TR_BLOCK_POST 1
@@ -514,7 +515,7 @@ const char* tr_last_error_message(void);
 /* Testing hook: makes bounded device-side waits give up, so that their
  * give-up paths run and tr_last_device_error() reports TR_ERR_DEVICE_TIMEOUT,
  * without a GPU fault or hang. `mode` is a bit mask (0 turns everything off):
- *   1  every launch of a plan with bounded waits (staged plans) also waits on
+ *   1  every launch of a plan with bounded waits (staged plans, block norms' split rows) also waits on
  *      a barrier that nothing completes, with a 1 ms limit; results stay correct;
  *   2  waits for bulk asynchronous copies give up at once: in the staged
  *      plans every ring slot (that row's outputs are undefined); a CTA still
@@ -522,11 +523,12 @@ const char* tr_last_error_message(void);
  *      and segments plans stream their segments through registers and have no
  *      such wait;
  *   4  every split (and segments) CTA's wait for the other CTAs of its row
- *      gives up at once: no CTA of the row writes outputs.
+ *      gives up at once: no CTA of the row writes outputs. So do the block norms' waits for the
+ *      other CTAs of a row: what is computed from the sums is NaN.
  * Applies to the launches made while it is set, including
  * tr_split_rows_noalloc_f32. A launch that gave up leaves every workspace and
- * the no-allocation scratch ready for the next launch. The waits of the block
- * norms are not changed by it. Other bits: TR_ERR_INVALID_ARG. */
+ * the no-allocation scratch ready for the next launch. Other bits:
+ * TR_ERR_INVALID_ARG. */
 tr_status tr_debug_force_wait_timeout(int32_t mode);
 
 /* Library version, major * 10000 + minor * 100 + patch. */

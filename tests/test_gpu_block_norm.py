@@ -507,3 +507,80 @@ def test_layernorm_of_16_bit_rows_that_start_unlike_the_rest(cols, dtype):
         d[k][:, :32] += 100.0
     check_forward(d, dtype, "layernorm", True, True)
     check_backward(d, dtype, "layernorm", True, True)
+
+
+@pytest.fixture
+def hook():
+    """The testing modes of the bounded waits, off again afterwards."""
+    assert tr.tr_last_device_error() == tr.TR_OK
+    yield lambda mode: tr.tr_debug_force_wait_timeout(mode)
+    tr.tr_debug_force_wait_timeout(0)
+    tr.tr_last_device_error()
+
+
+#: rows of clusters of 2, 4 and 8 CTAs in both directions, aligned and odd; gate rows of one slab, and several to a slab
+CLUSTERED = [(5, 12288, 1, "bf16"), (7, 12289, 7, "f16"), (4, 32768, 2, "bf16"), (3, 16384, 1, "f32"), (2, 32767, 1, "f32"),
+             (120, 8712, 120, "f32")]
+
+
+@pytest.mark.parametrize("rows,cols,groups,dtype", CLUSTERED)
+@pytest.mark.parametrize("kind", ["rmsnorm", "layernorm"])
+def test_clusters_that_give_up_say_so_and_recover(hook, rows, cols, groups, dtype, kind):
+    """Mode 4: every wait for the other CTAs of a row gives up. The call is reported, and what is computed from the row
+    sums is NaN; what is not comes out as before (dbias, the plain sum of dy), and so do the next calls, with nothing reset
+    but the error word."""
+    d = make(rows, cols, groups, dtype, kind, True, True, seed=17)
+    fwd = lambda: tr.gated_residual_norm(  # noqa: E731
+        d["x"], d["branch"], **args(d, "post_weight", "post_bias", "gate", "weight", "bias"), eps=EPS, kind=kind)
+    y0, h0 = fwd()
+    g0 = run_backward(d, kind, True, True)
+    torch.cuda.synchronize()
+    assert hook(4) == tr.TR_OK
+    for _ in range(3):
+        y, h = fwd()
+        g = run_backward(d, kind, True, True)
+    assert hook(0) == tr.TR_OK
+    y1, h1 = fwd()
+    g1 = run_backward(d, kind, True, True)
+    torch.cuda.synchronize()
+    for t in (y, h, g.dx, g.dbranch, g.dpost_weight, g.dpost_bias, g.dgate, g.dweight):
+        assert t is None or torch.isnan(t).all()
+    assert kind == "rmsnorm" or torch.equal(g.dbias, g0.dbias)
+    assert tr.tr_last_device_error() == tr.TR_ERR_DEVICE_TIMEOUT
+    assert tr.tr_last_device_error() == tr.TR_OK
+    for a, b in ((y1, y0), (h1, h0), *zip(g1, g0)):
+        assert a is None and b is None or torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows,cols,groups,dtype", CLUSTERED)
+@pytest.mark.parametrize("mode", [1, 2])
+def test_clusters_wait_out_a_barrier_that_nothing_completes(hook, mode, rows, cols, groups, dtype):
+    """Mode 1: one wait runs out after its limit and is reported; results stay correct. Mode 2 has nothing to expire here."""
+    d = make(rows, cols, groups, dtype, "layernorm", True, True, seed=18)
+    fwd = lambda: tr.gated_residual_norm(  # noqa: E731
+        d["x"], d["branch"], **args(d, "post_weight", "post_bias", "gate", "weight", "bias"), eps=EPS, kind="layernorm")
+    y0, h0 = fwd()
+    g0 = run_backward(d, "layernorm", True, True)
+    for call, want in ((fwd, (y0, h0)), (lambda: run_backward(d, "layernorm", True, True), g0)):
+        torch.cuda.synchronize()
+        assert hook(mode) == tr.TR_OK
+        got = call()
+        assert hook(0) == tr.TR_OK
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert a is None and b is None or torch.equal(a, b)
+        assert tr.tr_last_device_error() == (tr.TR_ERR_DEVICE_TIMEOUT if mode == 1 else tr.TR_OK)
+
+
+@pytest.mark.parametrize("cols", [1024, 1031, 70001])
+def test_rows_without_such_waits_are_not_changed_by_the_hook(hook, cols):
+    """Rows of one CTA, and rows that are read again (whose CTAs meet in cluster barriers)."""
+    d = make(4, cols, 1, "f32", "layernorm", True, True, seed=19)
+    want = run_backward(d, "layernorm", True, True)
+    assert hook(7) == tr.TR_OK
+    got = run_backward(d, "layernorm", True, True)
+    check_forward(d, "f32", "layernorm", True, True)
+    assert hook(0) == tr.TR_OK
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert tr.tr_last_device_error() == tr.TR_OK
