@@ -496,9 +496,12 @@ cudaError_t bwd_full(const BlockBwArgs& a, const RowShape& g, cudaStream_t strea
 template <class T, bool LAYER, int S>
 cudaError_t bwd_slots(int layout, const BlockBwArgs& a, const RowShape& g, cudaStream_t stream) {
     if (g.cluster > 1) {
-        if (layout == LAYOUT_FULL) return bwd_go<T, LAYER, S, LAYOUT_FULL, true, 0, 512, 1>(a, g, stream);
-        if (layout == LAYOUT_ALIGNED) return bwd_go<T, LAYER, S, LAYOUT_ALIGNED, true, 0, 512, 1>(a, g, stream);
-        return bwd_go<T, LAYER, S, LAYOUT_ODD, true, 0, 512, 1>(a, g, stream);
+        if constexpr (cluster_slots<T>(S, kBwdColumns)) {
+            if (layout == LAYOUT_FULL) return bwd_go<T, LAYER, S, LAYOUT_FULL, true, 0, 512, 1>(a, g, stream);
+            if (layout == LAYOUT_ALIGNED) return bwd_go<T, LAYER, S, LAYOUT_ALIGNED, true, 0, 512, 1>(a, g, stream);
+            return bwd_go<T, LAYER, S, LAYOUT_ODD, true, 0, 512, 1>(a, g, stream);
+        }
+        return cudaErrorInvalidConfiguration;
     }
     if (layout == LAYOUT_ODD) return bwd_go<T, LAYER, S, LAYOUT_ODD, false, 0, 512, 1>(a, g, stream);
     if (layout == LAYOUT_ALIGNED) return bwd_go<T, LAYER, S, LAYOUT_ALIGNED, false, 0, 512, 1>(a, g, stream);
@@ -512,7 +515,7 @@ cudaError_t bwd_kind(const BlockBwArgs& a, bool* done, cudaStream_t stream) {
     const bool odd = !rows_aligned(static_cast<int64_t>(a.cols) * static_cast<int>(sizeof(T)),
                                    {a.pre ? a.h : nullptr, a.pre ? a.dy : nullptr, a.post || a.dgate ? a.a : nullptr, a.dh, a.dx, a.da});
     int slots = 0;
-    const RowShape g = row_shape<T>(a.cols, tensors, odd, LAYER, 4, sizeof(T) == 2 ? 64 : 0, 8, &slots);
+    const RowShape g = row_shape<T>(a.cols, tensors, odd, LAYER, 4, sizeof(T) == 2 ? 64 : 0, kBwdColumns, &slots);
     *done = g.warps > 0;
     if (!*done) return cudaSuccess;
     const int layout = odd ? LAYOUT_ODD : row_full<T>(g, a.cols, slots) ? LAYOUT_FULL : LAYOUT_ALIGNED;

@@ -305,9 +305,12 @@ cudaError_t fwd_go(const BlockArgs& a, const RowShape& g, cudaStream_t stream) {
     if constexpr (!LAYER && S * 16 / sizeof(T) <= 8) {
         return fwd_go_with<T, LAYER, S, LAYOUT, CLUSTER, 512, 2>(a, g, stream);
     } else {
-        if constexpr (!CLUSTER && S == 1)
-            if (g.teams * g.warps <= 10) return fwd_go_with<T, LAYER, S, LAYOUT, CLUSTER, 320, 2>(a, g, stream);
-        return fwd_go_with<T, LAYER, S, LAYOUT, CLUSTER, 512, 1>(a, g, stream);
+        if constexpr (!CLUSTER && S == 1) {
+            // (16-bit rows of one slot have fewer than 1024 columns: 8 warps at most)
+            if (sizeof(T) == 2 || g.teams * g.warps <= 10) return fwd_go_with<T, LAYER, S, LAYOUT, CLUSTER, 320, 2>(a, g, stream);
+        }
+        if constexpr (CLUSTER || S > 1 || sizeof(T) == 4) return fwd_go_with<T, LAYER, S, LAYOUT, CLUSTER, 512, 1>(a, g, stream);
+        return cudaErrorInvalidConfiguration;
     }
 }
 
@@ -320,7 +323,9 @@ cudaError_t fwd_layout(int layout, const BlockArgs& a, const RowShape& g, cudaSt
 
 template <class T, bool LAYER, int S>
 cudaError_t fwd_slots(int layout, const BlockArgs& a, const RowShape& g, cudaStream_t stream) {
-    return g.cluster > 1 ? fwd_layout<T, LAYER, S, true>(layout, a, g, stream) : fwd_layout<T, LAYER, S, false>(layout, a, g, stream);
+    if (g.cluster == 1) return fwd_layout<T, LAYER, S, false>(layout, a, g, stream);
+    if constexpr (cluster_slots<T>(S, kFwdColumns)) return fwd_layout<T, LAYER, S, true>(layout, a, g, stream);
+    return cudaErrorInvalidConfiguration;
 }
 
 template <class T, bool LAYER>
@@ -329,7 +334,7 @@ cudaError_t fwd_kind(const BlockArgs& a, bool* done, cudaStream_t stream) {
     int slots = 0;
     // a third stage is all RMSNorm wants (16384 x 4096 bf16: 84 us, with a fourth 94: more loads under way only
     // keep the stores waiting); LayerNorm's longer rows of work hide behind four (16384 x 2048: 48 us, with three 55)
-    const RowShape g = row_shape<T>(a.cols, 2, odd, LAYER, LAYER ? 4 : 3, 0, 16, &slots);
+    const RowShape g = row_shape<T>(a.cols, 2, odd, LAYER, LAYER ? 4 : 3, 0, kFwdColumns, &slots);
     *done = g.warps > 0;
     if (!*done) return cudaSuccess;
     const int layout = odd ? LAYOUT_ODD : row_full<T>(g, a.cols, slots) ? LAYOUT_FULL : LAYOUT_ALIGNED;

@@ -467,6 +467,14 @@ RowShape row_shape(int cols, int tensors, bool odd, bool layer, int stages, int 
     return g;
 }
 
+// Most columns a thread of each direction, and whether rows of `slots` slots a thread are ever split over a cluster: a row
+// goes to twice as many CTAs only where its slots in half as many would be more than `most` columns.
+constexpr int kFwdColumns = 16, kBwdColumns = 8;
+template <class T>
+constexpr bool cluster_slots(int slots, int most) {
+    return slots > most / 2 / (16 / static_cast<int>(sizeof(T)));
+}
+
 // Whether all of a row's slots are in the row: every CTA has the same, and a team's threads all have theirs.
 template <class T>
 bool row_full(const RowShape& g, int cols, int slots) {

@@ -2,6 +2,8 @@
 calls, and the float64 definitions the GPU tests compare with, against differences."""
 import array
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -96,6 +98,67 @@ def test_workspace_sizes():
     f = tr.load().tr_gated_residual_norm_backward_workspace_bytes
     assert f(0, -1, 8, ctypes.byref(n)) == E and f(0, 1, 0, ctypes.byref(n)) == E and f(2, 1, 8, ctypes.byref(n)) == E
     assert f(0, 1, 8, None) == E
+
+
+SHAPES_PROGRAM = r"""
+#include <cstdio>
+#include "tr_block_rows.cuh"
+using namespace tr::block;
+static int bad = 0;
+#define CHECK(what) do { if (!(what) && bad++ < 20) std::printf("%s: T %d cols %d odd %d layer %d tensors %d\n", #what, static_cast<int>(sizeof(T)), cols, odd, layer, tensors); } while (0)
+template <class T>
+static void sweep() {
+    bool seen[2][5][2] = {};  // direction, slots, cluster
+    for (int cols = 1; cols < 140000; ++cols)
+        for (int odd = cols * static_cast<int>(sizeof(T)) % 16 != 0; odd < 2; ++odd)
+            for (int layer = 0; layer < 2; ++layer)
+                for (int tensors = 2; tensors <= 4; ++tensors)
+                    for (int back = 0; back < 2; ++back) {
+                        if (!back && tensors > 2) continue;
+                        int slots = 0;
+                        const RowShape g = back ? row_shape<T>(cols, tensors, odd, layer, 4, sizeof(T) == 2 ? 64 : 0, kBwdColumns, &slots)
+                                                : row_shape<T>(cols, tensors, odd, layer, layer ? 4 : 3, 0, kFwdColumns, &slots);
+                        if (g.warps == 0) {
+                            CHECK(cols > (back ? 32768 : 65536));
+                            continue;
+                        }
+                        CHECK(cols <= (back ? 32768 : 65536));
+                        CHECK(slots >= 1 && slots * 16 <= (back ? kBwdColumns : kFwdColumns) * static_cast<int>(sizeof(T)));
+                        CHECK(g.cluster == 1 || cluster_slots<T>(slots, back ? kBwdColumns : kFwdColumns));
+                        CHECK(g.cluster == 1 || g.teams == 1);
+                        CHECK(g.teams * g.warps <= kMaxWarps && row_smem(g) <= 226 * 1024);
+                        CHECK(static_cast<long>(g.warps) * 32 * slots >= g.cta_vecs);                       // the threads cover the slots
+                        CHECK(static_cast<long>(g.cta_vecs) * g.cluster * 16 >= cols * static_cast<long>(sizeof(T)));  // the CTAs the row,
+                        CHECK(static_cast<long>(g.cta_vecs) * (g.cluster - 1) * 16 < cols * static_cast<long>(sizeof(T)));  // and each has some
+                        if (!back && sizeof(T) == 2 && slots == 1) CHECK(g.teams * g.warps <= 10);
+                        seen[back][slots][g.cluster > 1] = true;
+                    }
+    // every kernel that is compiled is reached
+    const int cols = 0, odd = 0, layer = 0, tensors = 0;
+    for (int back = 0; back < 2; ++back)
+        for (int slots = 1; slots * 16 <= (back ? kBwdColumns : kFwdColumns) * static_cast<int>(sizeof(T)); ++slots) {
+            CHECK(seen[back][slots][0]);
+            CHECK(seen[back][slots][1] == cluster_slots<T>(slots, back ? kBwdColumns : kFwdColumns));
+        }
+}
+int main() {
+    sweep<float>();
+    sweep<__half>();
+    return bad != 0;
+}
+"""
+
+
+def test_every_width_has_a_kernel_and_every_kernel_a_width(tmp_path):
+    """The host rule that maps rows onto threads, for all widths that stay on the chip and some beyond: rows are covered, fit the
+    limits, and go to the slots and clusters that kernels are compiled for, all of which occur."""
+    src, exe = tmp_path / "shapes.cu", tmp_path / "shapes"
+    src.write_text(SHAPES_PROGRAM)
+    r = subprocess.run([trbuild._nvcc(), *trbuild.ARCH, "-O1", "-std=c++17", "--expt-relaxed-constexpr", f"-I{trbuild.INCLUDE}",
+                        f"-I{trbuild.CSRC}", str(src), "-o", str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([os.fspath(exe)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout
 
 
 # ---- lists ---------------------------------------------------------------------
