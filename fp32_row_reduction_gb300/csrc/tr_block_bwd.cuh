@@ -482,8 +482,8 @@ cudaError_t bwd_go(const BlockBwArgs& in, const RowShape& shape, cudaStream_t st
 
 // Full rows of one CTA are compiled for each pair of norms. 128 registers a thread let two CTAs of 256 threads
 // share an SM; CTAs of 9 or 10 warps are compiled for two an SM with 96, against one an SM with 128: RMSNorm
-// 6039 x 2560 f16 42 us against 46, 8192 x 2304 bf16 45 against 52, LayerNorm 6039 x 1280 f32 38 against 49, but
-// LayerNorm 6039 x 2560 f16 only 64 against 65, and with few rows (RMSNorm 768 x 2560 bf16) it loses, 11.7 against 10.5.
+// 6039 x 2560 f16 42 us against 46, 8192 x 2304 bf16 45 against 52, LayerNorm 6039 x 2560 f16 60 against 66,
+// 6039 x 1280 f32 38 against 45; with few rows (RMSNorm 768 x 2560 bf16) it loses, 11.7 against 10.5.
 // 16-bit ones take their parameters from shared memory: kept in those 96 registers, RMSNorm's two take 45 and 52 us.
 template <class T, bool LAYER, int S, int MODE>
 cudaError_t bwd_full(const BlockBwArgs& a, const RowShape& g, cudaStream_t stream) {

@@ -333,7 +333,7 @@ cudaError_t fwd_kind(const BlockArgs& a, bool* done, cudaStream_t stream) {
     const bool odd = !rows_aligned(static_cast<int64_t>(a.cols) * static_cast<int>(sizeof(T)), {a.x, a.a, a.h, a.y});
     int slots = 0;
     // a third stage is all RMSNorm wants (16384 x 4096 bf16: 84 us, with a fourth 94: more loads under way only
-    // keep the stores waiting); LayerNorm's longer rows of work hide behind four (16384 x 2048: 48 us, with three 55)
+    // keep the stores waiting); LayerNorm's longer rows of work hide a little better behind four (89 us, with three 90)
     const RowShape g = row_shape<T>(a.cols, 2, odd, LAYER, LAYER ? 4 : 3, 0, kFwdColumns, &slots);
     *done = g.warps > 0;
     if (!*done) return cudaSuccess;
