@@ -25,8 +25,11 @@ tr_status fail(tr_status s, const char* where, const char* why) {
     set_last_error(where, why);
     return s;
 }
+// An error is also cleared from the runtime's last-error slot, which other entry points ask after their own launches.
 tr_status cuda_status(cudaError_t e, const char* where) {
-    return e == cudaSuccess ? TR_OK : fail(TR_ERR_CUDA, where, cudaGetErrorString(e));
+    if (e == cudaSuccess) return TR_OK;
+    cudaGetLastError();
+    return fail(TR_ERR_CUDA, where, cudaGetErrorString(e));
 }
 
 size_t element_bytes(int dtype) { return dtype == TR_F32 ? 4 : 2; }
