@@ -347,7 +347,7 @@ tr_status tr_axis_launch_shape(int32_t sm_count, int32_t op, tr_order order, int
  * TR_ORDER_UNORDERED_TREE: the others return TR_ERR_UNSUPPORTED. No call
  * allocates or waits on the host, and all may be captured into a graph, the first
  * call of a process too. Rows that are split over several thread blocks meet in
- * bounded waits (two seconds). One that gave up is reported by tr_last_device_error, and what the
+ * bounded waits (two seconds), the longest ones in cluster barriers. A wait that gave up is reported by tr_last_device_error, and what the
  * call computes from that row's sums, and from later ones', is NaN. */
 typedef enum tr_dtype { TR_F32 = 0, TR_BF16 = 1, TR_F16 = 2 } tr_dtype;
 typedef enum tr_norm_kind { TR_NORM_RMS = 0, TR_NORM_LAYER = 1 } tr_norm_kind;
