@@ -97,8 +97,8 @@ struct Exchange {
     unsigned phase = 0;  // of both mbarriers, one bit each
     // After a wait that gave up all sums of the warp are NaN, so what is computed from them is no number, and the
     // kernel's end sets the error word. (Leaving the stores out instead takes a test at each: backward 8192 x 8192 bf16
-    // 190 us against 174.) Later waits of the kernel are short then, but there still is one for every phase: no
-    // CTA ends with stores to it under way.
+    // 190 us against 174.) Later waits of the kernel are short then. The CTAs' phases may be out of step, so that a store to
+    // a CTA is not waited for: a warp that gave up keeps its CTA for a while after the last barrier, until all have come in.
     static constexpr unsigned kLimitNs = 2000000000u, kLateNs = 1000000u;
     float start;  // of the sums over the warps: 0, or NaN
 
@@ -134,6 +134,8 @@ struct Exchange {
             if ((debug & kDebugForceTimeout) && threadIdx.x == 0) mbar_wait_bounded(bars + buf, (phase >> buf) & 1, kLateNs, err);
             if (start != 0.0f) atomicOr(err, kErrWaitTimeout);
             cg::this_cluster().sync();
+            if (start != 0.0f)
+                for (const unsigned long long t0 = global_ns(); global_ns() - t0 < kLateNs;) __nanosleep(1000);
         }
     }
 
