@@ -9,7 +9,7 @@ Four operators of a training step, of scoring and of decoding:
 * ``loss_grad``   from the saved lse and the gradients dloss of the losses (and dlse of the lse), the gradients
                   of hidden and weight, again without the logits.
 
-Rows whose label is IGNORE have a loss of 0 and no gradient. Tables, weights and activations come in bfloat16 or
+Rows whose label is IGNORE have a loss and an lse of 0 and no gradient. Tables, weights and activations come in bfloat16 or
 float16, those of the embedding in float32 too; losses, lse and their gradients are float32.
 """
 import math
@@ -107,15 +107,23 @@ def _tokens(g, n, vocab, spread):
     return ids.long().clamp(0, vocab - 1)
 
 
-def _masked(g, ids, share, value):
-    """Some of the ids replaced by `value`, at the ends of four sequences where they are that long."""
-    if not share:
-        return ids
-    n = ids.numel()
-    length = max(1, -(-n // 4))
-    at = torch.arange(n, device=g.device) % length
-    ids[at >= length - (torch.rand((), generator=g, device=g.device) * 2 * share * length).long()] = value
+def _masked(ids, share, value):
+    """Some of the ids replaced by `value`, at the ends of four sequences."""
+    if share:
+        length = _length(ids.numel())
+        at = torch.arange(ids.numel(), device=ids.device) % length
+        ids[at >= length - int(share * length)] = value
     return ids
+
+
+def _length(n):
+    return max(1, -(-n // 4))
+
+
+def _left(n, share):
+    """How many of n ids _masked leaves."""
+    length = _length(n)
+    return sum(min(n - at, length - int(share * length)) for at in range(0, n, length))
 
 
 def prepare(case, seed):
@@ -123,7 +131,7 @@ def prepare(case, seed):
     s = {"case": case}
     dtype = DTYPES[case["dtype"]]
     if case["op"] in ("embed", "embed_grad"):
-        s["ids"] = _masked(g, _tokens(g, case["tokens"], case["vocab"], case["spread"]), case["padded"], -1)
+        s["ids"] = _masked(_tokens(g, case["tokens"], case["vocab"], case["spread"]), case["padded"], -1)
         if case["op"] == "embed":
             s["table"] = _normal(g, (case["vocab"], case["cols"]), dtype, 0.02)
         else:
@@ -133,7 +141,7 @@ def prepare(case, seed):
     rows, cols, vocab = case["rows"], case["cols"], case["vocab"]
     s["hidden"] = _normal(g, (rows, cols), dtype)  # what comes out of the last norm
     s["weight"] = _normal(g, (vocab, cols), dtype, 1.5 / math.sqrt(cols))
-    s["labels"] = _masked(g, _tokens(g, rows, vocab, "zipf"), case["ignored"], IGNORE)
+    s["labels"] = _masked(_tokens(g, rows, vocab, "zipf"), case["ignored"], IGNORE)
     if case["op"] == "loss_grad":
         s["lse"] = _plain_loss(s)["lse"]
         counted = max(1, int((s["labels"] != IGNORE).sum()))
@@ -173,7 +181,8 @@ def _plain_loss(s):
     lse = torch.log(torch.exp(z - top).sum(1)) + top[:, 0]
     inside, label = _picked(s["labels"], c["vocab"])
     loss = lse - torch.where(inside, z.gather(1, label[:, None])[:, 0], 0.0)
-    return {"loss": torch.where(s["labels"] == IGNORE, 0.0, loss), "lse": lse}
+    counted = s["labels"] != IGNORE
+    return {"loss": torch.where(counted, loss, 0.0), "lse": torch.where(counted, lse, 0.0)}
 
 
 def _plain_loss_grad(s):
@@ -182,7 +191,7 @@ def _plain_loss_grad(s):
     counted = s["labels"] != IGNORE
     dloss = torch.where(counted, s["dloss"], 0.0)
     total = dloss + torch.where(counted, s["dlse"], 0.0) if c["z"] else dloss
-    dz = torch.exp(c["logit_scale"] * (hidden @ weight.T) - s["lse"][:, None]) * total[:, None]
+    dz = torch.where(counted[:, None], torch.exp(c["logit_scale"] * (hidden @ weight.T) - s["lse"][:, None]) * total[:, None], 0.0)
     inside, label = _picked(s["labels"], c["vocab"])
     dz[torch.arange(c["rows"], device=dz.device), label] -= torch.where(inside, dloss, 0.0)
     dz = dz * c["logit_scale"]
@@ -210,17 +219,20 @@ def run(state):
 
 def work(case):
     if case["op"] in ("embed", "embed_grad"):
+        tokens = _left(case["tokens"], case["padded"])
         n, table = case["tokens"] * case["cols"], case["vocab"] * case["cols"]
         if case["op"] == "embed":  # a row of the table is read once, however many tokens have it
-            share = min(n, table)
-            return {"bytes": (share + n) * BYTES[case["dtype"]] + 8 * case["tokens"], "flops": n}
-        return {"bytes": n * BYTES[case["dtype"]] + table * BYTES[case["grad"]] + 8 * case["tokens"], "flops": 2 * n}
-    rows, cols, vocab = case["rows"], case["cols"], case["vocab"]
-    once = (rows + vocab) * cols * BYTES[case["dtype"]]
+            share = min(tokens, case["vocab"]) * case["cols"]
+            return {"bytes": (share + n) * BYTES[case["dtype"]] + 8 * case["tokens"], "flops": tokens * case["cols"]}
+        return {"bytes": tokens * case["cols"] * BYTES[case["dtype"]] + table * BYTES[case["grad"]] + 8 * case["tokens"],
+                "flops": 2 * tokens * case["cols"]}
+    # rows without a loss are neither read nor computed
+    rows, cols, vocab, b = _left(case["rows"], case["ignored"]), case["cols"], case["vocab"], BYTES[case["dtype"]]
     if case["op"] == "loss":
-        return {"bytes": once + 16 * rows, "flops": 2 * rows * cols * vocab + 4 * rows * vocab}
+        return {"bytes": (rows + vocab) * cols * b + 16 * case["rows"], "flops": 2 * rows * cols * vocab + 4 * rows * vocab}
     # the logits once more, and a product for each gradient
-    return {"bytes": 2 * once + (16 + 4 * case["z"]) * rows, "flops": 6 * rows * cols * vocab + 5 * rows * vocab}
+    return {"bytes": (rows + case["rows"] + 2 * vocab) * cols * b + (16 + 4 * case["z"]) * case["rows"],
+            "flops": 6 * rows * cols * vocab + 5 * rows * vocab}
 
 
 def _exact_loss(hidden, weight, labels, scale, vocab):
@@ -229,9 +241,8 @@ def _exact_loss(hidden, weight, labels, scale, vocab):
     has = (labels >= 0) & (labels < vocab)
     chosen = torch.zeros_like(lse)
     chosen[has] = z[has, labels[has]]
-    loss = lse - chosen
-    loss = loss * (labels != IGNORE)
-    return loss, lse
+    counted = (labels != IGNORE).double()
+    return (lse - chosen) * counted, lse * counted
 
 
 def exact(case, seed):
@@ -260,7 +271,7 @@ def exact(case, seed):
             continue
         total = (loss * s["dloss"][part]).sum()
         if case["z"]:
-            total = total + (lse * s["dlse"][part] * (labels != IGNORE)).sum()
+            total = total + (lse * s["dlse"][part]).sum()
         dh, dw = torch.autograd.grad(total, (hidden, weight))
         parts.append((dh,))
         dweight = dweight + dw
