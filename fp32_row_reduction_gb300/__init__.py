@@ -146,6 +146,13 @@ SIGNATURES = {
     "tr_clip_by_norm": ([_P, _P, _P, _P, _I64, _P, _F, _F, _P], _I32),
     "tr_clip_global_norm": ([_I32, _P, _P, _P, _P, _I64, _F, _F, _P, _P, ctypes.c_size_t, _P], _I32),
     "tr_global_norm_workspace_bytes": ([_I64, ctypes.POINTER(ctypes.c_size_t)], _I32),
+    "tr_embedding": ([_I32, _P, _P, _P, _I64, _I64, _I64, _F, _P], _I32),
+    "tr_embedding_backward": ([_I32, _I32, _P, _P, _P, _I64, _I64, _I64, _F, _I32, _I32, _P, ctypes.c_size_t, _P], _I32),
+    "tr_embedding_backward_workspace_bytes": ([_I64, _I64, ctypes.POINTER(ctypes.c_size_t)], _I32),
+    "tr_linear_cross_entropy": ([_I32, _P, _P, _P, _P, _P, _I64, _I64, _I64, _F, _I64, _I32, _P, ctypes.c_size_t, _P], _I32),
+    "tr_linear_cross_entropy_backward": ([_I32, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _F, _I64, _I32, _P,
+                                          ctypes.c_size_t, _P], _I32),
+    "tr_linear_cross_entropy_workspace_bytes": ([_I64, _I64, _I64, _I32, ctypes.POINTER(ctypes.c_size_t)], _I32),
     "tr_plan_describe": ([_I32, _I64, _I64, _I32, ctypes.POINTER(tr_plan)], _I32),
     "tr_plan_select_for": ([ctypes.POINTER(tr_device_desc), _I32, _I64, _I64, _I32, _I32,
                             ctypes.POINTER(tr_plan)], _I32),
@@ -874,6 +881,168 @@ def clip_global_norm(tensors, max_norm, kind="l2", eps=1e-6, out=None, norm_out=
                                       max_norm, eps, norm.data_ptr(), ws.data_ptr(), ws.numel(), _current_stream()(index)),
            "clip_global_norm")
     return norm
+
+
+# ------------------------------------------------------------ the vocabulary's two ends
+
+def _rows_of(t, name):
+    """(pointer's tensor, rows, cols, device) of a contiguous CUDA matrix of a type the block norms take."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 2-D tensor")
+    return t.shape[0], t.shape[1], t.get_device()
+
+
+def _indices(t, name, shape, index):
+    """Pointer of a contiguous int64 tensor (of `shape`, when that is given)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int64 or t.get_device() != index:
+        raise TypeError(f"{name} must be an int64 tensor on cuda:{index}")
+    if not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be contiguous" + (f" and of shape {tuple(shape)}" if shape is not None else ""))
+    return t.data_ptr()
+
+
+def _caller_workspace(workspace, nbytes, index):
+    """(tensor, its bytes): the caller's, or a new one of `nbytes`."""
+    import torch
+    if workspace is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=torch.device("cuda", index)), nbytes
+    if not workspace.is_contiguous() or workspace.get_device() != index:
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def embedding(ids, table, scale=1.0, out=None, stream=None):
+    """``out[..., :] = scale * table[ids[...], :]`` (zeros for an id outside the table).
+
+    ids: a contiguous int64 tensor of any shape; table: (vocab, cols) of float32, bfloat16 or
+    float16; out: ids.shape + (cols,) of the table's type."""
+    import torch
+    vocab, c, index = _rows_of(table, "table")
+    switch = _switch(index, stream)
+    if switch is not None:
+        with switch:
+            return embedding(ids, table, scale, out)
+    ip = _indices(ids, "ids", None, index)
+    shape = ids.shape + (c,)
+    y = torch.empty(shape, dtype=table.dtype, device=table.device) if out is None else out
+    _check(load().tr_embedding(_dtype_code(table.dtype), table.data_ptr(), ip, _rows_like(y, "out", table.dtype, shape, index),
+                               ids.numel(), vocab, c, scale, _current_stream()(index)), "embedding")
+    return y
+
+
+@functools.lru_cache(maxsize=256)
+def embedding_backward_workspace_bytes(tokens, cols):
+    n = ctypes.c_size_t(0)
+    _check(load().tr_embedding_backward_workspace_bytes(tokens, cols, ctypes.byref(n)), "embedding_backward_workspace_bytes")
+    return n.value
+
+
+def embedding_backward(dy, ids, vocab=None, scale=1.0, dtable=None, accumulate=False, workspace=None, order="unordered",
+                       stream=None):
+    """The gradient of ``embedding``'s table: ``dtable[v] = scale * (the sum of dy over the places with id v)``.
+
+    dy: ids.shape + (cols,). dtable: (vocab, cols) of dy's type or float32 (None: a new one of dy's type with
+    `vocab` rows). accumulate=True adds to dtable, and leaves rows that no id names alone."""
+    import torch
+    if not isinstance(dy, torch.Tensor) or not dy.is_cuda:
+        raise TypeError("dy must be a CUDA tensor")
+    if dy.dim() < 1 or not dy.is_contiguous():
+        raise ValueError("dy must be a contiguous tensor of shape ids.shape + (cols,)")
+    index, c, dt = dy.get_device(), dy.shape[-1], dy.dtype
+    switch = _switch(index, stream)
+    if switch is not None:
+        with switch:
+            return embedding_backward(dy, ids, vocab, scale, dtable, accumulate, workspace, order)
+    code = _dtype_code(dt)
+    ip = _indices(ids, "ids", dy.shape[:-1], index)
+    if dtable is None:
+        if vocab is None or accumulate:
+            raise ValueError("embedding_backward needs dtable, or vocab (without accumulate)")
+        dtable = torch.empty((vocab, c), dtype=dt, device=dy.device)
+    if dtable.dim() != 2 or (vocab is not None and vocab != dtable.shape[0]):
+        raise ValueError("dtable must be a (vocab, cols) tensor")
+    gt = dtable.dtype
+    if gt is not dt and gt is not torch.float32:
+        raise TypeError("dtable must have dy's type or be float32")
+    vocab = dtable.shape[0]
+    tokens = ids.numel()
+    ws, n = _caller_workspace(workspace, embedding_backward_workspace_bytes(tokens, c), index)
+    _check(load().tr_embedding_backward(code, _dtype_code(gt), dy.data_ptr(), ip, _rows_like(dtable, "dtable", gt, (vocab, c), index),
+                                        tokens, vocab, c, scale, 1 if accumulate else 0, _order(order), ws.data_ptr(), n,
+                                        _current_stream()(index)), "embedding_backward")
+    return dtable
+
+
+@functools.lru_cache(maxsize=256)
+def _loss_workspace_bytes(rows, cols, vocab, backward):
+    n = ctypes.c_size_t(0)
+    _check(load().tr_linear_cross_entropy_workspace_bytes(rows, cols, vocab, backward, ctypes.byref(n)),
+           "linear_cross_entropy_workspace_bytes")
+    return n.value
+
+
+def linear_cross_entropy_workspace_bytes(rows, cols, vocab, backward=False):
+    return _loss_workspace_bytes(rows, cols, vocab, 1 if backward else 0)
+
+
+def linear_cross_entropy(hidden, weight, labels, logit_scale=1.0, ignore_label=-100, out=None, lse_out=None, workspace=None,
+                         order="unordered", stream=None):
+    """The cross entropy of ``logits = logit_scale * hidden @ weight.T`` without keeping the logits; returns
+    (losses, lse), float32 vectors with an entry for each row.
+
+    hidden: (rows, cols), weight: (vocab, cols), both bfloat16 or both float16; labels: int64, one for each
+    row. Rows whose label is `ignore_label` have losses and lse of 0; another label outside the
+    vocabulary selects a logit of 0, as in ``cross_entropy``."""
+    import torch
+    r, c, index = _rows_of(hidden, "hidden")
+    v = _rows_of(weight, "weight")[0]
+    switch = _switch(index, stream)
+    if switch is not None:
+        with switch:
+            return linear_cross_entropy(hidden, weight, labels, logit_scale, ignore_label, out, lse_out, workspace, order)
+    code = _dtype_code(hidden.dtype)
+    lp = _indices(labels, "labels", (r,), index)
+    loss = torch.empty(r, dtype=torch.float32, device=hidden.device) if out is None else out
+    lse = torch.empty(r, dtype=torch.float32, device=hidden.device) if lse_out is None else lse_out
+    ws, n = _caller_workspace(workspace, _loss_workspace_bytes(r, c, v, 0), index)
+    _check(load().tr_linear_cross_entropy(
+        code, hidden.data_ptr(), _rows_like(weight, "weight", hidden.dtype, (v, c), index), lp, _floats(loss, "out", (r,), index),
+        _floats(lse, "lse_out", (r,), index), r, c, v, logit_scale, ignore_label, _order(order), ws.data_ptr(), n,
+        _current_stream()(index)), "linear_cross_entropy")
+    return loss, lse
+
+
+def linear_cross_entropy_backward(hidden, weight, labels, lse, dloss=None, dlse=None, logit_scale=1.0, ignore_label=-100,
+                                  want_dhidden=True, want_dweight=True, dhidden=None, dweight=None, workspace=None,
+                                  order="unordered", stream=None):
+    """The gradients (dhidden, dweight) of ``linear_cross_entropy`` from its lse, the gradient dloss of its losses
+    (None: 1) and dlse of its lse (None: 0), float32 vectors. Either gradient is None when not wanted."""
+    import torch
+    r, c, index = _rows_of(hidden, "hidden")
+    v = _rows_of(weight, "weight")[0]
+    switch = _switch(index, stream)
+    if switch is not None:
+        with switch:
+            return linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse, logit_scale, ignore_label,
+                                                 want_dhidden, want_dweight, dhidden, dweight, workspace, order)
+    dt = hidden.dtype
+    code = _dtype_code(dt)
+    lp = _indices(labels, "labels", (r,), index)
+    if dhidden is None and want_dhidden:
+        dhidden = torch.empty_like(hidden)
+    if dweight is None and want_dweight:
+        dweight = torch.empty_like(weight)
+    ws, n = _caller_workspace(workspace, _loss_workspace_bytes(r, c, v, 1), index)
+    _check(load().tr_linear_cross_entropy_backward(
+        code, hidden.data_ptr(), _rows_like(weight, "weight", dt, (v, c), index), lp, _floats(lse, "lse", (r,), index),
+        _floats(dloss, "dloss", (r,), index), _floats(dlse, "dlse", (r,), index), _rows_like(dhidden, "dhidden", dt, (r, c), index),
+        _rows_like(dweight, "dweight", dt, (v, c), index), r, c, v, logit_scale, ignore_label, _order(order), ws.data_ptr(), n,
+        _current_stream()(index)), "linear_cross_entropy_backward")
+    return dhidden, dweight
 
 
 def cross_entropy(logits, labels, out=None, order="unordered", stream=None):

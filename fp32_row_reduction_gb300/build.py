@@ -31,10 +31,12 @@ SOURCES = ["tr_api.cu", "tr_plan.cpp", "k_softmax.cu", "k_rmsnorm.cu", "k_layern
            "k_reduce.cu", "k_axis.cu", "k_backward.cu", "k_fold.cu", "k_ot_cluster.cu", "k_xent_bwd.cu",
            "k_wave.cu", "k_wave_ordered.cu", "k_segments.cu", "k_bwd_wave.cu", "tr_block_api.cu", "k_block_fwd.cu",
            "k_block_bwd.cu", "k_block_bwd_f32.cu", "k_block_bwd_bf16.cu", "k_block_bwd_f16.cu",
-           "k_block_fwd_f32.cu", "k_block_fwd_bf16.cu", "k_block_fwd_f16.cu", "k_list.cu"]
+           "k_block_fwd_f32.cu", "k_block_fwd_bf16.cu", "k_block_fwd_f16.cu", "k_list.cu",
+           "tr_vocab_api.cu", "k_embedding.cu", "k_linear_xent.cu"]
 HEADERS = ["tr_device.cuh", "tr_row_kernels.cuh", "tr_split_kernels.cuh", "tr_dispatch.cuh", "tr_internal.h",
            "tr_plan.h", "tr_ot.cuh", "tr_wave_kernels.cuh", "tr_segments_kernels.cuh", "tr_block.h", "tr_block.cuh",
-           "tr_block_rows.cuh", "tr_block_fwd.cuh", "tr_block_bwd.cuh", "tr_launch.h", "tr_list.h"]
+           "tr_block_rows.cuh", "tr_block_fwd.cuh", "tr_block_bwd.cuh", "tr_launch.h", "tr_list.h",
+           "tr_check.h", "tr_vocab.h"]
 
 
 def _nvcc() -> str:

@@ -8,58 +8,18 @@
 #include <cstdlib>
 #include <map>
 #include <mutex>
-#include <new>
 #include <tuple>
 #include <vector>
 
 #include "tr.h"
 #include "tr_block.h"
+#include "tr_check.h"
 #include "tr_internal.h"
 #include "tr_launch.h"
 #include "tr_list.h"
 
 namespace tr {
 namespace {
-
-tr_status fail(tr_status s, const char* where, const char* why) {
-    set_last_error(where, why);
-    return s;
-}
-// An error is also cleared from the runtime's last-error slot, which other entry points ask after their own launches.
-tr_status cuda_status(cudaError_t e, const char* where) {
-    if (e == cudaSuccess) return TR_OK;
-    cudaGetLastError();
-    return fail(TR_ERR_CUDA, where, cudaGetErrorString(e));
-}
-
-size_t element_bytes(int dtype) { return dtype == TR_F32 ? 4 : 2; }
-
-struct Range {
-    const void* p;
-    size_t bytes;
-    size_t align;
-    bool overlaps(const Range& o) const {
-        if (!p || !o.p || bytes == 0 || o.bytes == 0) return false;
-        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
-        return a < b + o.bytes && b < a + bytes;
-    }
-    bool misaligned() const { return p && reinterpret_cast<uintptr_t>(p) % align != 0; }
-};
-
-// Alignment of every range; no output overlapping an input or another output.
-template <size_t I, size_t O>
-tr_status check_ranges(const char* where, const Range (&in)[I], const Range (&out)[O]) {
-    for (const Range& r : in)
-        if (r.misaligned()) return fail(TR_ERR_INVALID_ARG, where, "a misaligned input pointer");
-    for (size_t o = 0; o < O; ++o) {
-        if (out[o].misaligned()) return fail(TR_ERR_INVALID_ARG, where, "a misaligned output or workspace pointer");
-        for (const Range& r : in)
-            if (out[o].overlaps(r)) return fail(TR_ERR_INVALID_ARG, where, "an output or the workspace overlaps an input");
-        for (size_t q = o + 1; q < O; ++q)
-            if (out[o].overlaps(out[q])) return fail(TR_ERR_INVALID_ARG, where, "two outputs (or the workspace) overlap");
-    }
-    return TR_OK;
-}
 
 tr_status check_block(const char* w, int kind, int dtype, int norms, const float* post_w, const float* post_b,
                       const float* gate, int64_t gate_rows, const float* pre_w, const float* pre_b, int64_t rows,
@@ -236,17 +196,6 @@ tr_status check_clip(const char* w, float max_norm, float eps) {
     if (!(max_norm >= 0.0f)) return fail(TR_ERR_INVALID_ARG, w, "max_norm must be >= 0");
     if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(TR_ERR_INVALID_ARG, w, "eps must be finite and >= 0");
     return TR_OK;
-}
-
-template <class F>
-tr_status guarded(const char* w, F&& f) {
-    try {
-        return f();
-    } catch (const std::bad_alloc&) {
-        return fail(TR_ERR_UNSUPPORTED, w, "out of host memory");
-    } catch (...) {
-        return fail(TR_ERR_UNSUPPORTED, w, "an unexpected host error");
-    }
 }
 
 std::mutex g_launch_mu;

@@ -408,6 +408,62 @@ tr_status tr_clip_global_norm(tr_total_kind kind, const void* const* tensors, vo
 /* Host only: workspace bytes of the norm of `count` tensors. */
 tr_status tr_global_norm_workspace_bytes(int64_t count, size_t* bytes);
 
+/* ---- the vocabulary's two ends ---------------------------------------------
+ * What begins and ends a language model: the embedding of tokens, and the cross
+ * entropy of the logits of its last layer. Both read one (vocab x cols) table, which tied weights share.
+ *
+ * tr_embedding: out[t, :] = scale table[ids[t], :], computed in binary32 and rounded once; zeros where
+ * ids[t] is outside [0, vocab) (padding). table: vocab x cols, out: tokens x cols, of `dtype`; ids: tokens int64.
+ *
+ * tr_embedding_backward: dtable[v, :] = scale (the sum of dy[t, :] over the tokens t with ids[t] = v), the
+ * whole table, zeros where no token has the id; with accumulate = 1 dtable[v, :] += that, rounded once, and rows that no
+ * token has are neither read nor written. dy: tokens x cols of `dtype`; dtable: vocab x cols of `grad_dtype`, which is
+ * `dtype` or TR_F32. Sums are binary32 in a fixed order (the tokens', in pieces of 32 for a frequent id), so
+ * results repeat bit for bit. Tied weights: the gradient of the loss first, then this with accumulate.
+ *
+ * tr_linear_cross_entropy: with logits[r, v] = logit_scale sum_c hidden[r, c] weight[v, c], which are formed tile
+ * by tile and never kept, lse[r] = log(sum_v exp(logits[r, v])) and losses[r] = lse[r] - logits[r, labels[r]].
+ * A label outside [0, vocab) selects 0, as in tr_cross_entropy_f32. A row whose label is ignore_label (-100 by
+ * custom; any value, those inside the vocabulary too) has no loss: its losses and lse are 0, and its row of hidden is not looked
+ * at, whatever it holds. hidden: rows x cols, weight: vocab x cols, both of `dtype`, TR_BF16 or TR_F16 (TR_F32:
+ * TR_ERR_UNSUPPORTED); losses and lse: rows floats; lse may be NULL. Products are exact and summed
+ * in binary32.
+ *
+ * tr_linear_cross_entropy_backward: from the lse that the forward pass gave, with dloss the gradient of the losses
+ * (NULL: 1) and dlse that of the lse (NULL: 0; a penalty of the lse),
+ *   dz = logit_scale ((dloss + dlse) softmax - dloss onehot(label)),
+ *   dhidden = dz weight,  dweight = dz^T hidden,
+ * each of `dtype` and either NULL when not wanted. The logits are formed again, a piece of the vocabulary at a time. dz is
+ * rounded to `dtype` for the products, after a division by a power of two near the largest coefficient (so that float16 keeps
+ * small probabilities); sums are binary32, each output is rounded once. Rows without a loss have a gradient of 0 and
+ * add nothing to dweight, whatever they hold.
+ *
+ * Tables and rows are contiguous. Pointers must be aligned to their elements; weight to 16 bytes when
+ * cols is a multiple of 8 (for other widths the rows are copied to ones that are). No output may overlap an input or another
+ * output. tokens and rows may be 0 (gradients of tables are then zeros); 1 <= cols < 2^24; 1 <= vocab < 2^24 for the
+ * loss, 2^31 - 1024 for the embedding. scale and logit_scale must be finite. order must be
+ * TR_ORDER_UNORDERED_TREE (others: TR_ERR_UNSUPPORTED). Workspaces are caller-owned, 16-byte aligned, of the size that the
+ * _workspace_bytes calls (host only) give; calls that may run at the same time need one each. No call allocates or
+ * waits on the host, all may be captured into a graph, and results repeat bit for bit on one device. */
+tr_status tr_embedding(tr_dtype dtype, const void* table, const int64_t* ids, void* out, int64_t tokens, int64_t vocab,
+                       int64_t cols, float scale, cudaStream_t stream);
+tr_status tr_embedding_backward(tr_dtype dtype, tr_dtype grad_dtype, const void* dy, const int64_t* ids, void* dtable,
+                                int64_t tokens, int64_t vocab, int64_t cols, float scale, int32_t accumulate,
+                                tr_order order, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+tr_status tr_embedding_backward_workspace_bytes(int64_t tokens, int64_t cols, size_t* bytes);
+tr_status tr_linear_cross_entropy(tr_dtype dtype, const void* hidden, const void* weight, const int64_t* labels,
+                                  float* losses, float* lse, int64_t rows, int64_t cols, int64_t vocab,
+                                  float logit_scale, int64_t ignore_label, tr_order order, void* workspace,
+                                  size_t workspace_bytes, cudaStream_t stream);
+tr_status tr_linear_cross_entropy_backward(tr_dtype dtype, const void* hidden, const void* weight,
+                                           const int64_t* labels, const float* lse, const float* dloss,
+                                           const float* dlse, void* dhidden, void* dweight, int64_t rows, int64_t cols,
+                                           int64_t vocab, float logit_scale, int64_t ignore_label, tr_order order,
+                                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+/* backward: 0 for tr_linear_cross_entropy, 1 for its backward pass. */
+tr_status tr_linear_cross_entropy_workspace_bytes(int64_t rows, int64_t cols, int64_t vocab, int32_t backward,
+                                                  size_t* bytes);
+
 /* ---- no-allocation entry point ----------------------------------------- */
 
 /* Softmax, RMSNorm or LayerNorm of few long rows with no device allocation on

@@ -1,0 +1,505 @@
+"""GPU parity of the embedding and of the linear cross entropy with their gradients, against the float64
+formulas of oracle/vocab.py, whose docstring derives the bounds."""
+import threading
+
+import pytest
+import torch
+
+import fp32_row_reduction_gb300 as tr
+from oracle import vocab
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+IGNORE = -100
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    tr.load()
+
+
+def gen(seed):
+    g = torch.Generator(DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, shape, dtype, scale=1.0, offset=0):
+    """A contiguous tensor that starts `offset` elements into its allocation."""
+    n = 1
+    for s in shape:
+        n *= s
+    t = torch.empty(n + offset, device=DEV, dtype=dtype)
+    t.copy_(torch.randn(n + offset, generator=g, device=DEV) * scale)
+    return t[offset:].view(shape)
+
+
+def close(got, want, dtype=None):
+    v, err = want
+    assert got.shape == v.shape
+    dtype = dtype or got.dtype
+    bad = (got.double() - v).abs() - vocab.rounded(v, err, dtype)
+    bad = torch.where(torch.isnan(bad), torch.full_like(bad, float("inf")), bad)
+    assert bad.numel() == 0 or float(bad.max()) <= 0.0, (float(bad.max()), int((bad > 0).sum()), bad.numel())
+
+
+def same(a, b):
+    """Equal bits."""
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+# ---- embedding ------------------------------------------------------------------------
+
+EMBED = [(1, 1, 1), (1, 100, 4096), (3, 5, 7), (48, 5003, 5120), (300, 17, 65), (257, 1000, 1537), (1000, 50257, 128), (33, 64, 8), (5, 9, 2056)]
+
+
+@pytest.mark.parametrize("tokens,v,cols", EMBED)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("offset", [0, 1])
+def test_embedding(tokens, v, cols, dtype, offset):
+    g, dt = gen(tokens + cols), DTYPES[dtype]
+    table = randn(g, (v, cols), dt, offset=offset)
+    ids = torch.randint(-2, v + 2, (tokens,), generator=g, device=DEV)
+    close(tr.embedding(ids, table, scale=0.3), vocab.embedding(ids, table, 0.3))
+    guard = torch.full((tokens * cols + 64,), 7.0, device=DEV, dtype=dt)  # what is behind the rows stays
+    out = guard[3:3 + tokens * cols].view(tokens, cols)
+    tr.embedding(ids, table, out=out)
+    inside = (ids >= 0) & (ids < v)
+    want = torch.where(inside[:, None], table[ids.clamp(0, v - 1)], torch.zeros((), device=DEV, dtype=dt))
+    assert torch.equal(out, want)  # a scale of 1 changes nothing
+    assert bool((guard[:3] == 7).all()) and bool((guard[3 + tokens * cols:] == 7).all())
+
+
+def test_embedding_shapes_and_values():
+    g = gen(1)
+    table = randn(g, (50, 24), torch.bfloat16)
+    table[7] = float("inf")
+    table[8] = float("nan")
+    ids = torch.tensor([[[7, 1], [8, -1]], [[49, 50], [1 << 40, -(1 << 62)]]], device=DEV)
+    y = tr.embedding(ids, table, scale=2.0)
+    assert y.shape == (2, 2, 2, 24) and bool(torch.isinf(y[0, 0, 0]).all()) and bool(torch.isnan(y[0, 1, 0]).all())
+    assert torch.equal(y[0, 0, 1], 2 * table[1]) and torch.equal(y[1, 0, 0], 2 * table[49])
+    assert not y[0, 1, 1].any() and not y[1, 0, 1].any() and not y[1, 1].any()
+    assert tr.embedding(ids[:0], table).shape == (0, 2, 2, 24)
+    with pytest.raises(TypeError):
+        tr.embedding(ids.int(), table)
+    with pytest.raises(ValueError):
+        tr.embedding(ids, table[:, :8])
+    with pytest.raises(ValueError):
+        tr.embedding(ids[:, :, 0], table)
+
+
+# ---- the embedding's gradient -----------------------------------------------------------
+
+def token_ids(g, n, v, spread):
+    if spread == "one":
+        return torch.full((n,), v // 2, device=DEV, dtype=torch.int64)
+    if spread == "runs":  # segments of every length about the tile's and the longest short one's
+        lengths = [1, 31, 32, 33, 63, 64, 65, 95, 96, 97, 128, 129, 2, 1, 200]
+        ids = torch.cat([torch.full((lengths[i % len(lengths)],), (3 * i) % v, dtype=torch.int64) for i in range(1 + n // 30)])[:n]
+        return ids[torch.randperm(n, generator=torch.Generator().manual_seed(5))].to(DEV)
+    if spread == "outside":
+        return torch.randint(-v, 0, (n,), generator=g, device=DEV)
+    ids = torch.randint(0, v, (n,), generator=g, device=DEV)
+    if spread == "padded":
+        ids[torch.rand(n, generator=g, device=DEV) < 0.5] = -1
+        ids[::7] = v
+    return ids
+
+
+GRADS = [(1, 1, 1, "even"), (1, 50257, 64, "even"), (48, 5003, 512, "even"), (64, 3, 40, "one"), (65, 3, 40, "one"), (97, 300, 1537, "padded"),
+         (1000, 37, 256, "runs"), (3000, 999, 136, "runs"), (2500, 999, 33, "runs"), (5000, 5003, 72, "padded"), (16384, 211, 24, "even"),
+         (16385, 211, 24, "runs"), (40000, 70001, 16, "padded"), (33000, 5, 8, "one"), (20000, (1 << 24) + 3, 1, "even"), (100, 7, 300, "outside"),
+         (17000, 300, 9, "outside")]
+
+
+@pytest.mark.parametrize("tokens,v,cols,spread", GRADS)
+@pytest.mark.parametrize("dtype,grad", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f16", "f32")])
+def test_embedding_backward(tokens, v, cols, spread, dtype, grad):
+    g, dt, gt = gen(tokens + v), DTYPES[dtype], DTYPES[grad]
+    dy = randn(g, (tokens, cols), dt)
+    ids = token_ids(g, tokens, v, spread)
+    dy[(ids < 0) | (ids >= v)] = float("nan")  # padding holds anything
+    guard = torch.full((v * cols + 64,), 7.0, device=DEV, dtype=gt)
+    dtable = guard[32:32 + v * cols].view(v, cols)
+    dtable.fill_(float("nan"))
+    tr.embedding_backward(dy, ids, scale=0.7, dtable=dtable)
+    close(dtable, vocab.embedding_backward(dy, ids, v, 0.7))
+    assert bool((guard[:32] == 7).all()) and bool((guard[32 + v * cols:] == 7).all())
+    again = torch.empty_like(dtable)
+    tr.embedding_backward(dy, ids, scale=0.7, dtable=again)
+    assert same(again, dtable)
+    base = randn(g, (v, cols), gt)
+    base[v - 1] = float("nan")  # rows that no token has are left alone
+    total = base.clone()
+    tr.embedding_backward(dy, ids, scale=0.7, dtable=total, accumulate=True)
+    has = torch.zeros(v, dtype=torch.bool, device=DEV)
+    has[ids[(ids >= 0) & (ids < v)]] = True
+    assert same(total[~has], base[~has])
+    want, err = vocab.embedding_backward(dy, ids, v, 0.7, base)
+    keep = has & ~torch.isnan(base).any(1)
+    close(total[keep], (want[keep], err[keep]))
+
+
+@pytest.mark.parametrize("offset", [1, 4])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_embedding_backward_alignments(offset, dtype):
+    g, dt = gen(offset), DTYPES[dtype]
+    dy = randn(g, (700, 64), dt, offset=offset)
+    ids = token_ids(g, 700, 90, "runs")
+    flat = torch.empty(90 * 64 + offset, device=DEV, dtype=dt)
+    dtable = flat[offset:].view(90, 64)
+    tr.embedding_backward(dy, ids, dtable=dtable)
+    close(dtable, vocab.embedding_backward(dy, ids, 90, 1.0))
+    assert same(dtable, tr.embedding_backward(dy.clone(), ids, 90))  # whatever the alignment
+
+
+def test_embedding_backward_arguments():
+    g = gen(0)
+    dy, ids = randn(g, (4, 6, 16), torch.float16), torch.randint(0, 9, (4, 6), generator=g, device=DEV)
+    dtable = tr.embedding_backward(dy, ids, 9)
+    assert dtable.shape == (9, 16) and dtable.dtype == torch.float16
+    close(dtable, vocab.embedding_backward(dy, ids, 9, 1.0))
+    empty = tr.embedding_backward(dy[:0], ids[:0], 9, dtable=torch.full((9, 16), 3.0, device=DEV))
+    assert not empty.any()
+    kept = tr.embedding_backward(dy[:0], ids[:0], dtable=torch.full((9, 16), 3.0, device=DEV), accumulate=True)
+    assert bool((kept == 3).all())
+    with pytest.raises(ValueError):
+        tr.embedding_backward(dy, ids)
+    with pytest.raises(ValueError):
+        tr.embedding_backward(dy, ids, 9, accumulate=True)
+    with pytest.raises(ValueError):
+        tr.embedding_backward(dy, ids[:3], 9)
+    with pytest.raises(TypeError):
+        tr.embedding_backward(dy, ids, dtable=torch.zeros(9, 16, device=DEV, dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        tr.embedding_backward(dy, ids, 9, dtable=torch.zeros(8, 16, device=DEV))
+    with pytest.raises(tr.TrError):
+        tr.embedding_backward(dy, ids, 9, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+
+
+# ---- the loss ---------------------------------------------------------------------------
+
+def loss_inputs(rows, cols, v, dtype, seed=0, ignored=0.0, offset=0, outside=False):
+    g, dt = gen(seed + rows + cols + v), DTYPES[dtype]
+    hidden = randn(g, (rows, cols), dt, offset=offset)
+    weight = randn(g, (v, cols), dt, 1.5 / cols ** 0.5, offset=offset if cols % 8 else 0)
+    labels = torch.randint(0, v, (rows,), generator=g, device=DEV)
+    if outside and rows > 2:
+        labels[0], labels[1], labels[2] = v, -1, 1 << 40
+    gone = torch.rand(rows, generator=g, device=DEV) < ignored
+    labels[gone] = IGNORE
+    hidden[gone] = float("nan")  # padding holds anything
+    dloss = torch.rand(rows, generator=g, device=DEV) / rows
+    dlse = torch.randn(rows, generator=g, device=DEV) / rows
+    dloss[gone] = float("nan")
+    return hidden, weight, labels, dloss, dlse
+
+
+def check_loss(hidden, weight, labels, dloss, dlse, scale=1.0, **kw):
+    losses, lse = tr.linear_cross_entropy(hidden, weight, labels, logit_scale=scale, **kw)
+    ignore = kw.get("ignore_label", IGNORE)
+    want, want_lse = vocab.linear_cross_entropy(hidden, weight, labels, scale, ignore)
+    close(losses, want)
+    close(lse, want_lse)
+    dh, dw = tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse, logit_scale=scale, **kw)
+    want_h, want_w = vocab.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse, scale, ignore)
+    close(dh, want_h)
+    close(dw, want_w)
+    assert tr.tr_last_device_error() == tr.TR_OK
+    return losses, lse, dh, dw
+
+
+LOSSES = [(1, 1, 1), (1, 8, 2), (2, 7, 3), (1, 64, 5003), (3, 65, 255), (37, 1537, 1000), (48, 512, 257), (128, 96, 256), (129, 1024, 64),
+          (255, 33, 65), (256, 64, 513), (257, 136, 1000), (300, 264, 127), (513, 72, 2049), (700, 1000, 100), (1, 4096, 600), (1030, 16, 16)]
+
+
+@pytest.mark.parametrize("rows,cols,v", LOSSES)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_loss(rows, cols, v, dtype):
+    hidden, weight, labels, dloss, dlse = loss_inputs(rows, cols, v, dtype, outside=rows > 50)
+    check_loss(hidden, weight, labels, dloss, dlse)
+    check_loss(hidden, weight, labels, None, None, scale=-0.7)
+
+
+@pytest.mark.parametrize("rows,cols,v", [(37, 40, 300), (600, 129, 700), (1000, 64, 90)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("ignored", [0.3, 0.97, 1.0])
+def test_rows_without_a_loss(rows, cols, v, dtype, ignored):
+    hidden, weight, labels, dloss, dlse = loss_inputs(rows, cols, v, dtype, ignored=ignored, offset=1)
+    losses, lse, dh, dw = check_loss(hidden, weight, labels, dloss, dlse)
+    gone = labels == IGNORE
+    assert not losses[gone].any() and not lse[gone].any() and not dh[gone].any()
+    # one of the vocabulary's own labels as the one to leave out
+    hidden, weight, labels, dloss, dlse = loss_inputs(rows, cols, v, dtype, seed=1)
+    labels[rows // 3:] = 5
+    check_loss(hidden, weight, labels, dloss, dlse, ignore_label=5)
+
+
+@pytest.mark.parametrize("rows,cols,v", [(4, 8, 600_000), (1, 24, 1_100_000), (40_000, 16, 5003)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_loss_in_pieces(rows, cols, v, dtype):
+    check_loss(*loss_inputs(rows, cols, v, dtype, ignored=0.2 if rows > 4 else 0.0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,cols,v", [(5, 64, 999), (300, 520, 3000)])
+def test_exact_logits(rows, cols, v, dtype):
+    """Inputs of a few bits, so that every logit is exact in any order of the sum: what is left are the exponentials
+    and logarithms, 2^-20 and a few u of the numbers they meet."""
+    g, dt = gen(rows), DTYPES[dtype]
+    hidden = torch.randint(-2, 3, (rows, cols), generator=g, device=DEV).to(dt)
+    weight = (torch.randint(-3, 4, (v, cols), generator=g, device=DEV) / 32).to(dt)
+    labels = torch.randint(0, v, (rows,), generator=g, device=DEV)
+    losses, lse = tr.linear_cross_entropy(hidden, weight, labels)
+    z = hidden.double() @ weight.double().T
+    want = torch.logsumexp(z, 1)
+    bound = 2.0 ** -20 + (64 + v / 64) * vocab.U + 8 * vocab.U * (want.abs() + z.abs().amax(1))
+    assert bool(((lse.double() - want).abs() <= bound).all())
+    assert bool(((losses.double() - (want - z.gather(1, labels[:, None])[:, 0])).abs() <= 2 * bound).all())
+
+
+def test_certain_rows():
+    """Rows whose label has all of the probability: the loss is as small as it is, not a difference of large numbers."""
+    rows, cols, v = 64, 64, 300
+    hidden = torch.zeros(rows, cols, device=DEV, dtype=torch.bfloat16)
+    weight = torch.zeros(v, cols, device=DEV, dtype=torch.bfloat16)
+    hidden[:, 0] = torch.arange(8, 8 + rows, device=DEV).to(torch.bfloat16)
+    weight[3, 0] = 1.0
+    labels = torch.full((rows,), 3, device=DEV)
+    losses, lse = tr.linear_cross_entropy(hidden, weight, labels)
+    x = hidden[:, 0].double()
+    want = torch.log1p((v - 1) * torch.exp(-x))
+    # the sum is 1 + s: it is rounded at 1 (u), s is off by 2^-20 and 4 u x of itself
+    assert bool(((losses.double() - want).abs() <= 4 * vocab.U + want * (2.0 ** -20 + 16 * vocab.U * x)).all())
+    dh, dw = tr.linear_cross_entropy_backward(hidden, weight, labels, lse)
+    want_h, want_w = vocab.linear_cross_entropy_backward(hidden, weight, labels, lse)
+    close(dh, want_h)
+    close(dw, want_w)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_not_finite(dtype):
+    """A row that holds no numbers spoils its own loss, and the gradients it is part of, and no other row's."""
+    rows, cols, v = 300, 72, 400
+    hidden, weight, labels, dloss, dlse = loss_inputs(rows, cols, v, dtype)
+    clean = check_loss(hidden, weight, labels, dloss, dlse)
+    bad = hidden.clone()
+    bad[17, 3] = float("nan")
+    bad[201] = float("inf")
+    losses, lse = tr.linear_cross_entropy(bad, weight, labels)
+    assert not bool(torch.isfinite(losses[[17, 201]]).any())
+    ok = torch.ones(rows, dtype=torch.bool, device=DEV)
+    ok[[17, 201]] = False
+    assert same(losses[ok], clean[0][ok]) and same(lse[ok], clean[1][ok])
+    dh, dw = tr.linear_cross_entropy_backward(bad, weight, labels, lse, dloss, dlse)
+    assert same(dh[ok], clean[2][ok]) and not bool(torch.isfinite(dh[17]).any())
+    # a word of the vocabulary that cannot be: its logit is minus infinity, its probability 0
+    hidden, weight, labels, dloss, dlse = loss_inputs(rows, cols, v, dtype, seed=2)
+    hidden[:, 0] = 1.0
+    labels = labels % 50
+    impossible = weight.clone()
+    impossible[60] = 0.0
+    impossible[60, 0] = float("-inf")
+    losses, lse = tr.linear_cross_entropy(hidden, impossible, labels)
+    rest = torch.cat([weight[:60], weight[61:]])
+    z, e = vocab.logits(hidden, rest, 1.0)
+    want = torch.logsumexp(z, 1)
+    err = e.amax(1) + 2.0 ** -20 + (64 + v / 64) * vocab.U + 8 * vocab.U * (z.abs().amax(1) + want.abs())
+    close(lse, (want, err))
+
+
+def test_float16_keeps_small_probabilities():
+    """Probabilities far below float16's smallest number, with coefficients of a mean: the hidden gradient is theirs."""
+    rows, cols, v = 64, 64, 4096
+    g = gen(4)
+    hidden = torch.zeros(rows, cols, device=DEV, dtype=torch.float16)
+    weight = randn(g, (v, cols), torch.float16)
+    labels = torch.full((rows,), v + 1, device=DEV)  # no label: nothing but the probabilities, 1 / 4096 each
+    dloss = torch.full((rows,), 2.0 ** -13, device=DEV)
+    losses, lse = tr.linear_cross_entropy(hidden, weight, labels)
+    dh, _ = tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, logit_scale=2.0 ** 12)
+    # dz = 2^-13 / 4096: exact in the scaled type; the sum over the words is in binary32
+    want = 2.0 ** -13 * weight.double().sum(0) * 2.0 ** 12 / v
+    size = 2.0 ** -13 * weight.double().abs().sum(0) * 2.0 ** 12 / v
+    err = (v * vocab.U + 2.0 ** -20 + 64 * vocab.U) * size
+    close(dh, (want.expand(rows, -1), err.expand(rows, -1)))
+
+
+def test_one_gradient_at_a_time():
+    hidden, weight, labels, dloss, dlse = loss_inputs(300, 136, 500, "bf16", ignored=0.2)
+    _, lse, dh, dw = check_loss(hidden, weight, labels, dloss, dlse)
+    only, none = tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse, want_dweight=False)
+    assert none is None and same(only, dh)
+    none, only = tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse, want_dhidden=False)
+    assert none is None and same(only, dw)
+    with pytest.raises(tr.TrError):
+        tr.linear_cross_entropy_backward(hidden, weight, labels, lse, want_dhidden=False, want_dweight=False)
+
+
+def test_no_rows():
+    hidden, weight, labels, dloss, _ = loss_inputs(4, 16, 50, "f16")
+    losses, lse = tr.linear_cross_entropy(hidden[:0], weight, labels[:0])
+    assert losses.shape == (0,) and lse.shape == (0,)
+    dh, dw = tr.linear_cross_entropy_backward(hidden[:0], weight, labels[:0], lse, dweight=torch.full_like(weight, 3.0))
+    assert dh.shape == (0, 16) and not dw.any()
+
+
+def test_loss_arguments():
+    hidden, weight, labels, dloss, _ = loss_inputs(4, 16, 50, "f16")
+    with pytest.raises(tr.TrError):
+        tr.linear_cross_entropy(hidden.float(), weight.float(), labels)
+    with pytest.raises(TypeError):
+        tr.linear_cross_entropy(hidden, weight.bfloat16(), labels)
+    with pytest.raises(ValueError):
+        tr.linear_cross_entropy(hidden, weight[:, :8].contiguous(), labels)
+    with pytest.raises(ValueError):
+        tr.linear_cross_entropy(hidden[:, ::2], weight, labels)
+    with pytest.raises(TypeError):
+        tr.linear_cross_entropy(hidden, weight, labels.int())
+    with pytest.raises(ValueError):
+        tr.linear_cross_entropy(hidden, weight, labels[:3])
+    with pytest.raises(ValueError):
+        tr.linear_cross_entropy_backward(hidden, weight, labels, torch.zeros(3, device=DEV))
+    with pytest.raises(TypeError):
+        tr.linear_cross_entropy_backward(hidden, weight, labels, torch.zeros(4, device=DEV), dloss.double())
+    with pytest.raises(tr.TrError):
+        tr.linear_cross_entropy(hidden, weight, labels, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+    with pytest.raises(tr.TrError):
+        tr.linear_cross_entropy(hidden, weight, labels, logit_scale=float("nan"))
+
+
+def test_outputs_end_where_they_end():
+    """What lies behind the last row of every output stays, also where tiles reach past it."""
+    rows, cols, v = 70, 72, 130
+    hidden, weight, labels, dloss, dlse = loss_inputs(rows, cols, v, "bf16", ignored=0.1)
+    for offset in (0, 1, 16):
+        flat = [torch.full((n + 512,), 7.0, device=DEV, dtype=t) for n, t in
+                ((rows, torch.float32), (rows, torch.float32), (rows * cols, torch.bfloat16), (v * cols, torch.bfloat16))]
+        at = slice(128 + offset, None)
+        view = lambda f, *shape: f[at][:torch.Size(shape).numel()].view(shape)  # noqa: E731
+        losses, lse = tr.linear_cross_entropy(hidden, weight, labels, out=view(flat[0], rows), lse_out=view(flat[1], rows))
+        dh, dw = tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse, dhidden=view(flat[2], rows, cols),
+                                                  dweight=view(flat[3], v, cols))
+        want_h, want_w = vocab.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse)
+        close(dh, want_h)
+        close(dw, want_w)
+        for f, n in zip(flat, (rows, rows, rows * cols, v * cols)):
+            assert bool((f[:128 + offset] == 7).all()) and bool((f[128 + offset + n:] == 7).all())
+
+
+# ---- streams, graphs, threads ---------------------------------------------------------------
+
+def test_other_streams():
+    hidden, weight, labels, dloss, dlse = loss_inputs(500, 264, 900, "bf16")
+    ids = torch.randint(0, 900, (500,), generator=gen(1), device=DEV)
+    base = check_loss(hidden, weight, labels, dloss, dlse)
+    grad = tr.embedding_backward(hidden, ids, 900)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    out = []
+    for _ in range(3):
+        for s in streams:
+            losses, lse = tr.linear_cross_entropy(hidden, weight, labels, stream=s)
+            dh, dw = tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse, stream=s)
+            out.append((losses, lse, dh, dw, tr.embedding_backward(hidden, ids, 900, stream=s), tr.embedding(ids, weight, stream=s)))
+    torch.cuda.synchronize()
+    for got in out:
+        assert all(same(a, b) for a, b in zip(got, (*base, grad, weight[ids])))
+
+
+def test_threads():
+    hidden, weight, labels, dloss, dlse = loss_inputs(300, 72, 700, "f16", ignored=0.1)
+    ids = torch.randint(0, 700, (300,), generator=gen(2), device=DEV)
+    dy = randn(gen(2), (300, 72), torch.float16)
+    want = (*check_loss(hidden, weight, labels, dloss, dlse), tr.embedding_backward(dy, ids, 700))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        s = torch.cuda.Stream()
+        for _ in range(10):
+            losses, lse = tr.linear_cross_entropy(hidden, weight, labels, stream=s)
+            dh, dw = tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse, stream=s)
+            got = (losses, lse, dh, dw, tr.embedding_backward(dy, ids, 700, stream=s))
+            s.synchronize()
+            if not all(same(a, b) for a, b in zip(got, want)):
+                wrong.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_graphs():
+    """Captured once, replayed on other data; two graphs with a workspace each."""
+    a, b = (loss_inputs(400, 136, 600, "bf16", seed=s, ignored=0.2 * s) for s in (0, 1))
+    ids = [torch.randint(-1, 600, (400,), generator=gen(s), device=DEV) for s in (5, 6)]
+    hidden, weight, labels, dloss, dlse = (t.clone() for t in a)
+    tok = ids[0].clone()
+
+    def step():
+        losses, lse = tr.linear_cross_entropy(hidden, weight, labels)
+        dh, dw = tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse)
+        tr.embedding_backward(dh, tok, dtable=dw, accumulate=True)
+        return losses, lse, dh, dw, tr.embedding(tok, weight, scale=2.0)
+
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step())
+        graphs.append(g)
+    for data, t in ((a, ids[0]), (b, ids[1]), (a, ids[0])):
+        for dst, src in zip((hidden, weight, labels, dloss, dlse), data):
+            dst.copy_(src)
+        tok.copy_(t)
+        want = step()
+        for g, out in zip(graphs, outs):
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(same(x, y) for x, y in zip(out, want))
+
+
+# ---- a model's two ends together --------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_a_step_of_a_tied_model(dtype):
+    """Embedding, a block norm, the loss; back through all of them into one tied table, whose gradient is clipped. Each
+    stage is checked on what the stage before it gave."""
+    dt, tokens, cols, v = DTYPES[dtype], 3 * 111, 264, 1003
+    g = gen(9)
+    table = randn(g, (v, cols), dt, 1.5 / cols ** 0.5)
+    branch = randn(g, (tokens, cols), dt, 0.5)
+    weight = (1 + 0.1 * torch.randn(cols, generator=g, device=DEV))
+    ids = torch.randint(0, v, (3, 111), generator=g, device=DEV)
+    ids[1, 80:] = -1
+    labels = torch.cat([ids[:, 1:], torch.full((3, 1), IGNORE, device=DEV)], 1).reshape(-1)
+    labels[labels < 0] = IGNORE
+    x = tr.embedding(ids, table, scale=cols ** 0.5)
+    close(x, vocab.embedding(ids, table, cols ** 0.5))
+    y, h = tr.gated_residual_norm(x.view(tokens, cols), branch, weight=weight, post=False)
+    losses, lse = tr.linear_cross_entropy(y, table, labels)
+    close(losses, vocab.linear_cross_entropy(y, table, labels)[0])
+    dloss = torch.full((tokens,), 1.0 / int((labels != IGNORE).sum()), device=DEV)
+    dy, dtable = tr.linear_cross_entropy_backward(y, table, labels, lse, dloss)
+    want_y, want_t = vocab.linear_cross_entropy_backward(y, table, labels, lse, dloss)
+    close(dy, want_y)
+    close(dtable, want_t)
+    back = tr.gated_residual_norm_backward(h, branch, dy, weight=weight, post=False)
+    of_loss = dtable.clone()
+    tr.embedding_backward(back.dx.view(3, 111, cols), ids, dtable=dtable, scale=cols ** 0.5, accumulate=True)
+    sums, err = vocab.embedding_backward(back.dx.view(3, 111, cols), ids, v, cols ** 0.5, of_loss)
+    close(dtable, (sums, err))
+    before = dtable.double()
+    norm = tr.clip_global_norm([dtable, back.dweight], 1e-3)
+    total = float((before ** 2).sum() + (back.dweight.double() / (1e-3 / (float(norm) + 1e-6))).pow(2).sum()) ** 0.5
+    assert abs(float(norm) - total) <= 1e-5 * total
+    close(dtable, (before * (1e-3 / (float(norm) + 1e-6)), 16 * vocab.U * before.abs()))
