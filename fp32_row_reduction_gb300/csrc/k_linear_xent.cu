@@ -9,6 +9,7 @@
 
 #include "tr_block.cuh"
 #include "tr_launch.h"
+#include "tr_mma.cuh"
 #include "tr_vocab.h"
 
 namespace tr {
@@ -22,7 +23,9 @@ LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
     };
     rows_pad = round_up(rows, kTileRows);
     pitch = round_up(cols, 8);
-    parts = ceil_div(vocab, 64);
+    width = grad_width = mma::kMaxWidth;
+    splits = 1;
+    parts = 2 * ceil_div(vocab, width);
     pack_weight = cols % 8 != 0;
     // dz of a piece: 2^27 values (256 MB), and at least 4096 columns, so that the sums over the pieces cost little
     const int64_t most = std::max<int64_t>(4096, (int64_t{1} << 27) / rows_pad / 256 * 256);
@@ -39,7 +42,7 @@ LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
         coef = take(rows_pad * 4);
         onehot = take(rows_pad * 4);
         probs = take(rows_pad * piece * 2);
-        sums = take(rows_pad * pitch * 4);
+        sums = take(splits * rows_pad * pitch * 4);
     } else {
         parts_at = take(parts * rows_pad * 8);
         picked = take(rows_pad * 4);
@@ -151,73 +154,240 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(LossArgs a, Ws w, const 
 
 // ---- products -------------------------------------------------------------------------
 
-// A 64 x 64 tile of A B^T in float32: element (m, k) of A is at a[m am + k ak].
 template <class T>
-struct Operand {
-    const T* p;
-    int64_t outer, inner;  // strides of the tile's and of the summed dimension
-    int64_t size;          // of the tile's dimension
+constexpr uint32_t kTypeBits = 0;
+template <>
+constexpr uint32_t kTypeBits<__nv_bfloat16> = 1;
+
+// What the four products share. `first`: the piece of the vocabulary begins there and has `n` words.
+struct Product {
+    Ws w;
+    mma::Limits lim;
+    int cols, splits, width;
+    int64_t first, n;
+    float scale;      // log2(e) logit_scale
+    void* to;         // probs, dhidden or dweight
+    int64_t pitch;    // of its rows (of `sums` for the hidden gradient)
+    int begun, last;  // hidden gradient: whether the sums have earlier pieces, and whether this one completes them
+    int wide;         // rows of `to` start on 16 bytes
 };
-constexpr int kTile = 64, kDepth = 16;
+
+__device__ __forceinline__ int tiles_of(int64_t n, int size) { return static_cast<int>((n + size - 1) / size); }
 
 template <class T>
-__device__ __forceinline__ void tile_product(const Operand<T>& a, const Operand<T>& b, int64_t depth, int64_t m0, int64_t n0,
-                                             float (&acc)[4][4]) {
-    __shared__ float sa[kDepth][kTile + 4], sb[kDepth][kTile + 4];
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// 32 columns from c on of a row per lane (null: none), of which those below `cols` are written, rounded to T. Rows that start on 16
+// bytes take 16-byte stores; others are turned in shared memory, so that a warp writes 32 columns of one row at a time.
+template <class T>
+__device__ __forceinline__ void store_columns(T* row, int c, int cols, const float (&v)[32], bool wide, float* turn) {
+    if (wide) {
+        if (!row) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int g = 0; g < 4; ++g)
+            if (c + 8 * g < cols)
+                *reinterpret_cast<uint4*>(row + c + 8 * g) = make_uint4(pack2<T>(v[8 * g], v[8 * g + 1]), pack2<T>(v[8 * g + 2], v[8 * g + 3]),
+                                                                        pack2<T>(v[8 * g + 4], v[8 * g + 5]), pack2<T>(v[8 * g + 6], v[8 * g + 7]));
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-    const int tm = threadIdx.x / 16 * 4, tn = threadIdx.x % 16 * 4;
-    for (int64_t k0 = 0; k0 < depth; k0 += kDepth) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < kTile * kDepth; i += kThreads) {
-            const int m = i / kDepth, k = i % kDepth;
-            const bool in = k0 + k < depth;
-            sa[k][m] = in && m0 + m < a.size ? to_float(a.p[(m0 + m) * a.outer + (k0 + k) * a.inner]) : 0.0f;
-            sb[k][m] = in && n0 + m < b.size ? to_float(b.p[(n0 + m) * b.outer + (k0 + k) * b.inner]) : 0.0f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kDepth; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][tm + i], sb[k][tn + j], acc[i][j]);
+    for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = v[i];
+    __syncwarp();
+    const unsigned long long mine = reinterpret_cast<unsigned long long>(row);
+    for (int i = 0; i < 32; ++i) {
+        T* p = reinterpret_cast<T*>(__shfl_sync(kFull, mine, i));
+        if (p && c + lane < cols) p[c + lane] = from_float<T>(turn[i * 33 + lane]);
     }
 }
 
+__device__ __forceinline__ void spoil(float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = NAN;
+}
+
+// Forward: (maximum, sum of 2^(z - maximum)) of each half of a tile's columns, and the label's z.
 template <class T>
-__global__ void __launch_bounds__(kThreads) stats_kernel(Ws w, Operand<T> hidden, Operand<T> weight, int cols, float scale) {
+__global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
+    stats_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap weight, const __grid_constant__ Product p) {
+    int64_t count = 0;
+    mma::run<false, false>(
+        &hidden, &weight, kTypeBits<T>, p.lim,
+        [&] {
+            count = p.w.head->count;
+            return mma::Work{tiles_of(count, kTileRows), tiles_of(p.n, p.width), 1, tiles_of(p.cols, mma::kDepth), p.width};
+        },
+        [&](const mma::Unit& u, int row, int half, int first, int last, uint32_t at, bool ok, float*) {
+            const int limit = static_cast<int>(min(static_cast<int64_t>(last), p.n - u.n));  // columns of the vocabulary
+            const int label = row < count ? p.w.labels[row] - u.n : -1;
+            float m = -INFINITY, s = 0.0f;
+            for (int c = first; c < limit; c += 32) {
+                float z[32];
+                mma::load_columns(at + c, z);
+                if (!ok) spoil(z);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[i] *= p.scale;
+                if (label >= c && label < min(c + 32, limit)) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (label == c + i) p.w.picked[row] = z[i];
+                }
+                if (c + 32 > limit) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (c + i >= limit) z[i] = -INFINITY;
+                }
+                float top = z[0];
+#pragma unroll
+                for (int i = 1; i < 32; ++i) top = fmaxf(top, z[i]);
+                const float most = fmaxf(m, top), from = most == -INFINITY ? 0.0f : most;
+                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 32; ++i) part[i & 3] += ex2(z[i] - from);
+                s = fmaf(s, ex2(m - from), (part[0] + part[1]) + (part[2] + part[3]));
+                m = most;
+            }
+            if (row < count) p.w.parts[(2 * static_cast<int64_t>(u.n / p.width) + half) * p.w.rows_pad + row] = make_float2(m, s);
+        });
+}
+
+// Backward: scale dz / logit_scale of a piece, rounded. Rows and words beyond the last are zeros up to the tile's end.
+template <class T>
+__global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
+    probs_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap weight, const __grid_constant__ Product p) {
+    int64_t count = 0;
+    float times = 0.0f;
+    mma::run<false, false>(
+        &hidden, &weight, kTypeBits<T>, p.lim,
+        [&] {
+            count = p.w.head->count;
+            times = p.w.head->scale;
+            return mma::Work{tiles_of(count, kTileRows), tiles_of(p.n, p.width), 1, tiles_of(p.cols, mma::kDepth), p.width};
+        },
+        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, float* turn) {
+            const bool in = row < count;
+            const int limit = static_cast<int>(min(static_cast<int64_t>(last), p.n - u.n));
+            const float lse = in ? p.w.lse[row] : 0.0f, coef = in ? p.w.coef[row] * times : 0.0f;
+            const float onehot = in ? p.w.onehot[row] * times : 0.0f;
+            const int word = in ? p.w.labels[row] : -1;
+            const int label = word >= 0 ? static_cast<int>(word - p.first) - u.n : -1;
+            T* to = static_cast<T*>(p.to) + row * p.pitch + u.n;
+            for (int c = first; c < last; c += 32) {
+                float z[32];
+                mma::load_columns(at + c, z);
+                if (!ok) spoil(z);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[i] = coef * ex2(fmaf(z[i], p.scale, -lse));
+                if (label >= c && label < c + 32) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (label == c + i) z[i] -= onehot;
+                }
+                if (!in || c + 32 > limit) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!in || c + i >= limit) z[i] = 0.0f;
+                }
+                store_columns<T>(to, c, last, z, true, turn);
+            }
+        });
+}
+
+// Backward: the piece's part of the hidden gradient, added to those of earlier pieces; the last one writes the gradient.
+template <class T>
+__global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
+    dhidden_kernel(const __grid_constant__ CUtensorMap probs, const __grid_constant__ CUtensorMap weight, const __grid_constant__ Product p) {
+    int64_t count = 0;
+    float times = 0.0f;
+    mma::run<false, true>(
+        &probs, &weight, kTypeBits<T>, p.lim,
+        [&] {
+            count = p.w.head->count;
+            times = p.w.head->unscale;
+            return mma::Work{tiles_of(count, kTileRows), tiles_of(p.cols, p.width), p.splits, tiles_of(p.n, mma::kDepth), p.width};
+        },
+        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, float* turn) {
+            const bool in = row < count;
+            float* sums = p.w.sums + (u.split * p.w.rows_pad + row) * p.pitch + u.n;
+            T* to = in && p.last ? static_cast<T*>(p.to) + static_cast<int64_t>(p.w.map[row]) * p.cols + u.n : nullptr;
+            const int cols = static_cast<int>(min(static_cast<int64_t>(last), p.pitch - u.n));
+            for (int c = first; c < cols; c += 32) {
+                float z[32];
+                mma::load_columns(at + c, z);
+                if (!ok) spoil(z);
+                if (u.begin == u.end) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) z[i] = 0.0f;
+                }
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    if (!in || c + 4 * g >= cols) continue;
+                    float4* q = reinterpret_cast<float4*>(sums + c) + g;
+                    if (p.begun) {
+                        const float4 f = *q;
+                        z[4 * g] += f.x;
+                        z[4 * g + 1] += f.y;
+                        z[4 * g + 2] += f.z;
+                        z[4 * g + 3] += f.w;
+                    }
+                    if (!p.last) *q = make_float4(z[4 * g], z[4 * g + 1], z[4 * g + 2], z[4 * g + 3]);
+                }
+                if (p.last) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) z[i] *= times;
+                    store_columns<T>(to, c, min(last, p.cols - u.n), z, p.wide, turn);
+                }
+            }
+        });
+}
+
+// Backward: the piece's rows of the weight's gradient.
+template <class T>
+__global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
+    dweight_kernel(const __grid_constant__ CUtensorMap probs, const __grid_constant__ CUtensorMap hidden, const __grid_constant__ Product p) {
+    float times = 0.0f;
+    mma::run<true, true>(
+        &probs, &hidden, kTypeBits<T>, p.lim,
+        [&] {
+            times = p.w.head->unscale;
+            return mma::Work{tiles_of(p.n, kTileRows), tiles_of(p.cols, p.width), 1, tiles_of(p.w.head->count, mma::kDepth), p.width};
+        },
+        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, float* turn) {
+            T* to = row < p.n ? static_cast<T*>(p.to) + (p.first + row) * p.cols + u.n : nullptr;
+            const int cols = min(last, p.cols - u.n);
+            for (int c = first; c < cols; c += 32) {
+                float z[32];
+                mma::load_columns(at + c, z);
+                if (!ok) spoil(z);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[i] = u.begin == u.end ? 0.0f : z[i] * times;
+                store_columns<T>(to, c, cols, z, p.wide, turn);
+            }
+        });
+}
+
+// The parts of a hidden gradient whose depth was split, added in order.
+template <class T>
+__global__ void __launch_bounds__(kThreads) emit_kernel(LossArgs a, Ws w, int64_t pitch, int splits) {
     pdl_enter();
-    const int64_t count = w.head->count, m0 = static_cast<int64_t>(blockIdx.y) * kTile, n0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    if (m0 >= count) return;
-    float acc[4][4];
-    tile_product(hidden, weight, cols, m0, n0, acc);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = m0 + threadIdx.x / 16 * 4 + i;
-        const int label = r < count ? w.labels[r] : -1;
-        MaxSum s{-INFINITY, 0.0f};
-        float z[4];
-        bool nan = false;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + threadIdx.x % 16 * 4 + j;
-            z[j] = n < weight.size ? acc[i][j] * scale : -INFINITY;
-            if (n == label) w.picked[r] = z[j];
-            nan |= z[j] != z[j];
-            s.m = fmaxf(s.m, z[j]);
-        }
-#pragma unroll
-        for (int o = 8; o >= 1; o >>= 1) s.m = fmaxf(s.m, __shfl_xor_sync(kFull, s.m, o));
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (s.m != -INFINITY) s.s += ex2(z[j] - s.m);
-        if (nan) s.s = NAN;
-#pragma unroll
-        for (int o = 8; o >= 1; o >>= 1) s.s += __shfl_xor_sync(kFull, s.s, o);
-        if (threadIdx.x % 16 == 0 && r < count) w.parts[blockIdx.x * w.rows_pad + r] = make_float2(s.m, s.s);
+    const int64_t n = w.head->count * a.cols;
+    const float u = w.head->unscale;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * kThreads) {
+        const int64_t r = i / a.cols, c = i - r * a.cols;
+        float s = 0.0f;
+        for (int k = 0; k < splits; ++k) s += w.sums[(k * w.rows_pad + r) * pitch + c];
+        static_cast<T*>(a.dhidden)[static_cast<int64_t>(w.map[r]) * a.cols + c] = from_float<T>(u * s);
     }
 }
 
@@ -239,74 +409,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(LossArgs a, Ws w, int64_
         a.losses[to] = label >= 0 ? fmaf(m - w.picked[r], kLN2, log) : lse;
         if (a.lse) a.lse[to] = lse;
     }
-}
-
-template <class T>
-__global__ void __launch_bounds__(kThreads) probs_kernel(Ws w, Operand<T> hidden, Operand<T> weight, int cols, float scale, int64_t first,
-                                                         T* probs, int64_t piece) {
-    pdl_enter();
-    const int64_t count = w.head->count, m0 = static_cast<int64_t>(blockIdx.y) * kTile, n0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    if (m0 >= (count + kTileRows - 1) / kTileRows * kTileRows) return;
-    float acc[4][4];
-    tile_product(hidden, weight, cols, m0, n0, acc);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = m0 + threadIdx.x / 16 * 4 + i;
-        const bool in = r < count;
-        const float s = w.head->scale, lse = in ? w.lse[r] : 0.0f, c = in ? w.coef[r] * s : 0.0f, o = in ? w.onehot[r] * s : 0.0f;
-        const int64_t label = in ? w.labels[r] - first : -1;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + threadIdx.x % 16 * 4 + j;
-            float v = c * ex2(fmaf(acc[i][j], scale, -lse));
-            if (n == label && w.labels[r] >= 0) v -= o;
-            probs[r * piece + n] = from_float<T>(in && n < weight.size ? v : 0.0f);
-        }
-    }
-}
-
-// sums (+)= a b^T
-template <class T>
-__global__ void __launch_bounds__(kThreads) dhidden_kernel(Ws w, Operand<T> a, Operand<T> b, int64_t depth, int64_t pitch, int first) {
-    pdl_enter();
-    const int64_t count = w.head->count, m0 = static_cast<int64_t>(blockIdx.y) * kTile, n0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    if (m0 >= count) return;
-    float acc[4][4];
-    tile_product(a, b, depth, m0, n0, acc);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t r = m0 + threadIdx.x / 16 * 4 + i, c = n0 + threadIdx.x % 16 * 4 + j;
-            if (r >= count || c >= b.size) continue;
-            float* p = w.sums + r * pitch + c;
-            *p = first ? acc[i][j] : *p + acc[i][j];
-        }
-}
-template <class T>
-__global__ void __launch_bounds__(kThreads) emit_kernel(LossArgs a, Ws w, int64_t pitch) {
-    pdl_enter();
-    const int64_t n = w.head->count * a.cols;
-    const float u = w.head->unscale;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int64_t r = i / a.cols, c = i - r * a.cols;
-        static_cast<T*>(a.dhidden)[static_cast<int64_t>(w.map[r]) * a.cols + c] = from_float<T>(u * w.sums[r * pitch + c]);
-    }
-}
-template <class T>
-__global__ void __launch_bounds__(kThreads) dweight_kernel(Ws w, Operand<T> a, Operand<T> b, T* dweight) {
-    pdl_enter();
-    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile, n0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    float acc[4][4];
-    tile_product(a, b, w.head->count, m0, n0, acc);
-    const float u = w.head->unscale;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t r = m0 + threadIdx.x / 16 * 4 + i, c = n0 + threadIdx.x % 16 * 4 + j;
-            if (r < a.size && c < b.size) dweight[r * b.size + c] = from_float<T>(u * acc[i][j]);
-        }
 }
 
 Ws workspace(const LossArgs& a, const LossPlan& p) {
@@ -340,16 +442,63 @@ cudaError_t pack(const LossArgs& a, const LossPlan& p, const Ws& w, int backward
                             to, p.pitch, a.vocab, nullptr);
 }
 
+// ---- launches -------------------------------------------------------------------------
+
+// A tensor map of rows x cols elements (rows `pitch` apart) in boxes of 64 columns.
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                            const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+Encode encoder() {
+    static const Encode fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<Encode>(p);
+    }();
+    return fn;
+}
+template <class T>
+cudaError_t map_of(CUtensorMap* map, const T* p, int64_t rows, int64_t cols, int64_t pitch, int box_rows) {
+    const Encode encode = encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t size[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)}, stride[1] = {static_cast<cuuint64_t>(pitch) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
+    const CUresult r = encode(map, kTypeBits<T> ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<T*>(p), size,
+                              stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// CTA pairs for `units` of work.
+template <class K>
+cudaError_t launch_product(K kernel, const CUtensorMap& a, const CUtensorMap& b, const Product& p, int64_t units, cudaStream_t stream) {
+    const int resident = resident_ctas(reinterpret_cast<const void*>(kernel), mma::kThreads, mma::kSmem, 2);
+    if (resident < 2) return cudaErrorInvalidConfiguration;
+    const int64_t pairs = std::min<int64_t>(units, resident / 2);
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(2 * pairs)), mma::kThreads, mma::kSmem, 1, stream, a, b, p);
+}
+
 template <class T>
 cudaError_t forward(const LossArgs& a, cudaStream_t stream) {
     const LossPlan p(a.rows, a.cols, a.vocab, false);
     const Ws w = workspace(a, p);
     Packed<T> k;
     cudaError_t e = pack(a, p, w, 0, &k, stream);
+    CUtensorMap hidden, weight;
+    if (e == cudaSuccess) e = map_of(&hidden, k.hidden, p.rows_pad, a.cols, k.pitch, mma::kRows);
+    if (e == cudaSuccess) e = map_of(&weight, k.weight, a.vocab, a.cols, k.pitch, p.width / 2);
     if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(p.parts), static_cast<unsigned>(p.rows_pad / kTile));
-    e = launch_dependent(stats_kernel<T>, grid, kThreads, 0, 1, stream, w, Operand<T>{k.hidden, k.pitch, 1, p.rows_pad},
-                         Operand<T>{k.weight, k.pitch, 1, a.vocab}, a.cols, a.logit_scale * kL2E);
+    Product d{};
+    d.w = w;
+    d.lim = mma::Limits{device_error_word(), debug_flags_now()};
+    d.cols = a.cols;
+    d.width = p.width;
+    d.n = a.vocab;
+    d.scale = a.logit_scale * kL2E;
+    e = launch_product(stats_kernel<T>, hidden, weight, d, p.rows_pad / kTileRows * ceil_div(a.vocab, p.width), stream);
     if (e != cudaSuccess) return e;
     return launch_dependent(join_kernel, dim3(static_cast<unsigned>(ceil_div(a.rows, kThreads))), kThreads, 0, 1, stream, a, w, p.parts);
 }
@@ -361,24 +510,50 @@ cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
     Packed<T> k;
     cudaError_t e = pack(a, p, w, 1, &k, stream);
     T* probs = reinterpret_cast<T*>(a.ws + p.probs);
-    const unsigned tiles = static_cast<unsigned>(p.rows_pad / kTile), col_tiles = static_cast<unsigned>(ceil_div(a.cols, kTile));
+    CUtensorMap hidden_rows, hidden_cols, probs_rows, probs_cols;
+    if (e == cudaSuccess) e = map_of(&hidden_rows, k.hidden, p.rows_pad, a.cols, k.pitch, mma::kRows);
+    if (e == cudaSuccess) e = map_of(&hidden_cols, k.hidden, p.rows_pad, a.cols, k.pitch, mma::kDepth);
+    if (e == cudaSuccess) e = map_of(&probs_rows, probs, p.rows_pad, p.piece, p.piece, mma::kRows);
+    if (e == cudaSuccess) e = map_of(&probs_cols, probs, p.rows_pad, p.piece, p.piece, mma::kDepth);
+    const bool align = a.cols % 8 == 0;
+    const int64_t row_tiles = p.rows_pad / kTileRows;
     for (int64_t first = 0; first < a.vocab && e == cudaSuccess; first += p.piece) {
         const int64_t n = std::min(p.piece, a.vocab - first);
-        const T* weight = k.weight + first * k.pitch;
-        const unsigned across = static_cast<unsigned>(ceil_div(n, kTile));
-        e = launch_dependent(probs_kernel<T>, dim3(across, tiles), kThreads, 0, 1, stream, w, Operand<T>{k.hidden, k.pitch, 1, p.rows_pad},
-                             Operand<T>{weight, k.pitch, 1, n}, a.cols, a.logit_scale * kL2E, first, probs, p.piece);
-        if (e == cudaSuccess && a.dhidden)
-            e = launch_dependent(dhidden_kernel<T>, dim3(col_tiles, tiles), kThreads, 0, 1, stream, w,
-                                 Operand<T>{probs, p.piece, 1, p.rows_pad}, Operand<T>{weight, 1, k.pitch, a.cols}, n, p.pitch,
-                                 first == 0 ? 1 : 0);
-        if (e == cudaSuccess && a.dweight)
-            e = launch_dependent(dweight_kernel<T>, dim3(col_tiles, across), kThreads, 0, 1, stream, w, Operand<T>{probs, 1, p.piece, n},
-                                 Operand<T>{k.hidden, 1, k.pitch, a.cols}, static_cast<T*>(a.dweight) + first * a.cols);
+        CUtensorMap weight_rows, weight_cols;
+        e = map_of(&weight_rows, k.weight + first * k.pitch, n, a.cols, k.pitch, p.width / 2);
+        if (e == cudaSuccess) e = map_of(&weight_cols, k.weight + first * k.pitch, n, a.cols, k.pitch, mma::kDepth);
+        if (e != cudaSuccess) break;
+        Product d{};
+        d.w = w;
+        d.lim = mma::Limits{device_error_word(), debug_flags_now()};
+        d.cols = a.cols;
+        d.first = first;
+        d.n = n;
+        d.scale = a.logit_scale * kL2E;
+        d.width = p.width;
+        d.to = probs;
+        d.pitch = p.piece;
+        e = launch_product(probs_kernel<T>, hidden_rows, weight_rows, d, row_tiles * ceil_div(n, p.width), stream);
+        if (e == cudaSuccess && a.dhidden) {
+            d.width = p.grad_width;
+            d.to = a.dhidden;
+            d.pitch = p.pitch;
+            d.begun = first > 0;
+            d.last = p.splits == 1 && first + n == a.vocab;
+            d.splits = p.splits;
+            d.wide = align && reinterpret_cast<uintptr_t>(a.dhidden) % 16 == 0;
+            e = launch_product(dhidden_kernel<T>, probs_rows, weight_cols, d, row_tiles * ceil_div(a.cols, d.width) * p.splits, stream);
+        }
+        if (e == cudaSuccess && a.dweight) {
+            d.width = p.grad_width;
+            d.to = a.dweight;
+            d.wide = align && reinterpret_cast<uintptr_t>(a.dweight) % 16 == 0;
+            e = launch_product(dweight_kernel<T>, probs_cols, hidden_cols, d, ceil_div(n, kTileRows) * ceil_div(a.cols, d.width), stream);
+        }
     }
-    if (e != cudaSuccess || !a.dhidden) return e;
+    if (e != cudaSuccess || !a.dhidden || p.splits == 1) return e;
     const int64_t ctas = std::min<int64_t>(ceil_div(a.rows * a.cols, kThreads), 1 << 16);
-    return launch_dependent(emit_kernel<T>, dim3(static_cast<unsigned>(ctas)), kThreads, 0, 1, stream, a, w, p.pitch);
+    return launch_dependent(emit_kernel<T>, dim3(static_cast<unsigned>(ctas)), kThreads, 0, 1, stream, a, w, p.pitch, p.splits);
 }
 
 }  // namespace loss

@@ -1,0 +1,305 @@
+// Matrix products of 16-bit tiles on the tensor cores: one tile of 256 x (up to 256) by a pair of CTAs.
+//
+// A cluster of two CTAs computes C = A B^T for 256 rows of A and `width` rows of B (columns of C), summed over the depth in
+// blocks of 64. Each CTA brings 128 rows of A and half of B's rows to its shared memory by TMA; one thread of the pair's first CTA
+// issues the products for both, and each CTA finds its 128 rows of C, in binary32, in its own tensor memory, where two tiles have
+// room: one is written out while the next is summed. An operand lies in memory either with its depth contiguous (rows of 64
+// elements are 128 bytes of a 128-byte swizzle) or with its rows contiguous (64 rows of each depth are 128 bytes).
+//
+// Warp 0 copies, warp 1 issues the products, the others (kOutWarps) write out. Every wait is bounded: one that gives up
+// is recorded in the device error word, ends the waits of both CTAs, and makes what is written from then on NaN; the copies and products
+// under way are waited for (again bounded) before the pair frees its tensor memory and ends.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "tr_device.cuh"
+#include "tr_internal.h"
+
+namespace tr {
+namespace mma {
+
+constexpr int kDepth = 64;        // elements of the depth in a block: 128 bytes
+constexpr int kRows = 128;        // of A in one CTA
+constexpr int kMaxWidth = 256;    // rows of B, both CTAs
+constexpr int kStageBytes = (kRows + kMaxWidth / 2) * 128;
+constexpr int kStages = 6;
+constexpr int kOutWarps = 8;      // two for each quarter of the 128 rows
+constexpr int kThreads = 32 * (2 + kOutWarps);
+constexpr int kTurnFloats = 32 * 33;  // an output warp's room to turn a 32 x 32 tile
+constexpr int kSmem = 1024 + kStages * kStageBytes + kOutWarps * kTurnFloats * 4 + 256;
+constexpr int kColumns = 512;     // of tensor memory: two tiles
+constexpr long long kLimitNs = 2000000000, kLateNs = 100000000, kTestNs = 1000000;
+
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void arrive_in(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// A box of a tensor map to this CTA's shared memory, its bytes counted on a barrier of the pair.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t what, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(what), "r"(add)
+        : "memory");
+}
+// The products issued so far arrive at this barrier of both CTAs when they are done.
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"(static_cast<uint16_t>(3))
+                 : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// 32 columns of this warp's 32 rows, a row to a lane.
+__device__ __forceinline__ void load_columns(uint32_t addr, float (&v)[32]) {
+    uint32_t r[32];
+    __syncwarp();
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Shared-memory descriptor of an operand's block. Depth contiguous: groups of 8 rows are 1024 bytes apart. Rows
+// contiguous: groups of 8 depths are 1024 bytes apart, and groups of 64 rows a box of 64 depths.
+template <bool ROWS_CONTIGUOUS>
+__device__ __forceinline__ uint64_t block_of(uint32_t addr) {
+    const uint64_t leading = ROWS_CONTIGUOUS ? kDepth * 128 / 16 : 1, stride = 1024 / 16;
+    return (addr >> 4) | leading << 16 | stride << 32 | uint64_t{1} << 46 | uint64_t{2} << 61;
+}
+// Encoded distance of the next 16 elements of the depth.
+template <bool ROWS_CONTIGUOUS>
+constexpr uint64_t kNext16 = (ROWS_CONTIGUOUS ? 16 * 128 : 32) / 16;
+
+// What the launch needs apart from the operands.
+struct Limits {
+    unsigned* err;
+    int debug;
+};
+
+struct Shared {
+    uint64_t full[kStages], empty[kStages], done[2], room[2], never;
+    uint32_t columns;
+    int dead;
+};
+
+// The pair's waits: bounded, and over at once when either CTA has given up.
+struct Waits {
+    Shared& s;
+    Limits lim;
+    __device__ __forceinline__ bool dead() const { return *reinterpret_cast<volatile int*>(&s.dead) != 0; }
+    __device__ __forceinline__ void die() const {
+        if (lim.err) atomicOr(lim.err, kErrWaitTimeout);
+        const uint32_t a = smem_addr(&s.dead);
+#pragma unroll
+        for (uint32_t r = 0; r < 2; ++r) asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(in_cta(a, r)), "r"(1) : "memory");
+    }
+    __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
+        if (mbar_try_wait(bar, parity)) return true;
+        const unsigned long long t0 = global_ns();
+        while (!dead()) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if (static_cast<long long>(global_ns() - t0) > kLimitNs) die();
+        }
+        return false;
+    }
+};
+
+// One unit of work: which tile, and which blocks of the depth.
+struct Unit {
+    int m, n;        // first row of A, first row of B
+    int begin, end;  // blocks of the depth (equal: the tile is zero)
+    int split;
+};
+// All of it: tiles in groups of eight rows of tiles (what the pairs read at one time is then as many rows of A as of B), each
+// tile's depth in `splits` parts.
+struct Work {
+    int m_tiles, n_tiles, splits, blocks, width;
+    __device__ __forceinline__ int64_t total() const { return static_cast<int64_t>(m_tiles) * n_tiles * splits; }
+    __device__ __forceinline__ Unit unit(int64_t i) const {
+        constexpr int kGroup = 8;
+        const int64_t t = i / splits;
+        const int split = static_cast<int>(i - t * splits);
+        const int64_t in_group = static_cast<int64_t>(kGroup) * n_tiles, g = t / in_group;
+        const int r = static_cast<int>(t - g * in_group), rows = min(kGroup, m_tiles - static_cast<int>(g) * kGroup);
+        const int64_t from = static_cast<int64_t>(blocks) * split / splits, to = static_cast<int64_t>(blocks) * (split + 1) / splits;
+        return Unit{(static_cast<int>(g) * kGroup + r % rows) * 2 * kRows, r / rows * width, static_cast<int>(from), static_cast<int>(to), split};
+    }
+};
+
+// The products of a CTA pair: plan() gives the work, once what earlier kernels wrote can be read; each pair takes every (number of
+// pairs)-th unit. out(unit, row, half, first, last, tensor address, ok, turn) writes the columns [first, last) of one row a lane;
+// ok: the sums are there (false: after a wait that gave up); turn: kTurnFloats of shared memory for the warp.
+template <bool A_ROWS, bool B_ROWS, class Plan, class Out>
+__device__ __forceinline__ void run(const CUtensorMap* a, const CUtensorMap* b, uint32_t type_bits, const Limits& lim, Plan&& plan, Out&& out) {
+    extern __shared__ __align__(16) char raw[];
+    __shared__ Shared s;
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cta_rank();
+    const Waits waits{s, lim};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.done[i], 1);
+            mbar_init(&s.room[i], 2 * kOutWarps);
+        }
+        mbar_init(&s.never, 1);
+        s.dead = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s.columns)), "r"(kColumns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    fence_before();
+    __syncthreads();
+    cluster_barrier();
+    fence_after();
+    const uint32_t columns = s.columns;
+    pdl_enter();
+
+    const int pair = static_cast<int>(blockIdx.x) / 2, pairs = static_cast<int>(gridDim.x) / 2;
+    const Work work = plan();
+    const int64_t total = work.total();
+    const int width = work.width;
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint32_t half = width / 2, bytes = (kRows + half) * 128;
+            int stage = 0;
+            uint32_t phase = 0, issued = 0;
+            bool ok = true;
+            for (int64_t i = pair; i < total && ok; i += pairs) {
+                const Unit u = work.unit(i);
+                for (int k = u.begin; k < u.end && ok; ++k) {
+                    ok = waits.wait(&s.empty[stage], phase ^ 1);
+                    if (!ok) break;
+                    const uint32_t bar = in_cta(smem_addr(&s.full[stage]), 0);
+                    const uint32_t to_a = base + stage * kStageBytes, to_b = to_a + kRows * 128;
+                    if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * bytes);
+                    const int m = u.m + rank * kRows, n = u.n + rank * half, d = k * kDepth;
+                    if constexpr (A_ROWS) {
+#pragma unroll
+                        for (int j = 0; j < kRows / 64; ++j) copy_box(to_a + j * kDepth * 128, a, m + 64 * j, d, bar);
+                    } else {
+                        copy_box(to_a, a, d, m, bar);
+                    }
+                    if constexpr (B_ROWS) {
+                        for (uint32_t j = 0; j < half / 64; ++j) copy_box(to_b + j * kDepth * 128, b, n + 64 * j, d, bar);
+                    } else {
+                        copy_box(to_b, b, d, n, bar);
+                    }
+                    ++issued;
+                    if (++stage == kStages) stage = 0, phase ^= 1;
+                }
+            }
+            // after a wait that gave up: the copies under way, of both CTAs, count on the first one's barriers (the second, which
+            // may have begun one more, gives that the time)
+            if (!ok && rank == 1) {
+                const unsigned long long t0 = global_ns();
+                while (static_cast<long long>(global_ns() - t0) < kTestNs) __nanosleep(1000);
+            }
+            if (!ok && rank == 0) {
+                for (int j = 0; j < kStages && issued > 0; ++j, --issued) {
+                    stage = stage == 0 ? kStages - 1 : stage - 1;
+                    if (stage == kStages - 1) phase ^= 1;
+                    mbar_wait_bounded(&s.full[stage], phase, kLateNs, lim.err);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            // kind::f16: binary32 sums; the operands' type and layouts, width / 8 and 256 / 16
+            const uint32_t what = 1u << 4 | type_bits << 7 | type_bits << 10 | (A_ROWS ? 1u << 15 : 0) | (B_ROWS ? 1u << 16 : 0) |
+                                  static_cast<uint32_t>(width / 8) << 17 | (2 * kRows / 16) << 24;
+            int stage = 0;
+            uint32_t phase = 0, slot = 0, slot_phase = 0;
+            bool ok = true;
+            if ((lim.debug & kDebugForceTimeout) && pair == 0) mbar_wait_bounded(&s.never, 0, kTestNs, lim.err);
+            for (int64_t i = pair; i < total && ok; i += pairs) {
+                const Unit u = work.unit(i);
+                ok = waits.wait(&s.room[slot], slot_phase ^ 1);
+                if (!ok) break;
+                fence_after();
+                const uint32_t d = columns + slot * kMaxWidth;
+                for (int k = u.begin; k < u.end; ++k) {
+                    if (lim.debug & kDebugExpireCopies) waits.die(), ok = false;
+                    else ok = waits.wait(&s.full[stage], phase);
+                    if (!ok) break;
+                    fence_after();
+                    const uint32_t at = base + stage * kStageBytes;
+                    const uint64_t da = block_of<A_ROWS>(at), db = block_of<B_ROWS>(at + kRows * 128);
+#pragma unroll
+                    for (int j = 0; j < kDepth / 16; ++j)
+                        product(d, da + j * kNext16<A_ROWS>, db + j * kNext16<B_ROWS>, what, k > u.begin || j > 0);
+                    commit(smem_addr(&s.empty[stage]));
+                    if (++stage == kStages) stage = 0, phase ^= 1;
+                }
+                if (!ok) break;
+                commit(smem_addr(&s.done[slot]));
+                if (++slot == 2) slot = 0, slot_phase ^= 1;
+            }
+            if (!ok) {  // the products under way
+                commit(smem_addr(&s.never));
+                mbar_wait_bounded(&s.never, 0, kLateNs, lim.err);
+            }
+        }
+    } else {
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const int first = half * (width / 2), last = half ? width : width / 2;
+        float* turn = reinterpret_cast<float*>(raw + (base - smem_addr(raw)) + kStages * kStageBytes) + (warp - 2) * kTurnFloats;
+        uint32_t slot = 0, slot_phase = 0;
+        for (int64_t i = pair; i < total; i += pairs) {
+            const Unit u = work.unit(i);
+            const bool ok = __all_sync(kFull, waits.wait(&s.done[slot], slot_phase) && !waits.dead());
+            fence_after();
+            const uint32_t at = columns + slot * kMaxWidth + (static_cast<uint32_t>(quarter * 32) << 16);
+            out(u, u.m + static_cast<int>(rank) * kRows + quarter * 32 + lane, half, first, last, at, ok, turn);
+            fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_in(in_cta(smem_addr(&s.room[slot]), 0));
+            if (++slot == 2) slot = 0, slot_phase ^= 1;
+        }
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    cluster_barrier();  // nothing of either CTA arrives at the other any more
+    fence_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(columns), "r"(kColumns) : "memory");
+}
+
+}  // namespace mma
+}  // namespace tr

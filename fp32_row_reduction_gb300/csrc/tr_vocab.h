@@ -76,6 +76,9 @@ struct LossPlan {
     int64_t pitch;     // elements of a packed row of hidden (or of weight)
     int64_t piece;     // backward: columns of the vocabulary at a time
     int64_t parts;     // forward: partial sums of a row
+    int width;         // words of a tile of logits
+    int grad_width;    // columns of a tile of the gradients
+    int splits;        // of the depth of the hidden gradient
     size_t head, map, labels, lse, coef, onehot, hidden, weight, parts_at, picked, probs, sums, bytes;
     bool pack_weight;  // rows of the weight that do not start on 16 bytes are copied to ones that do
     LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward);
