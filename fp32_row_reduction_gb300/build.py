@@ -36,7 +36,7 @@ SOURCES = ["tr_api.cu", "tr_plan.cpp", "k_softmax.cu", "k_rmsnorm.cu", "k_layern
 HEADERS = ["tr_device.cuh", "tr_row_kernels.cuh", "tr_split_kernels.cuh", "tr_dispatch.cuh", "tr_internal.h",
            "tr_plan.h", "tr_ot.cuh", "tr_wave_kernels.cuh", "tr_segments_kernels.cuh", "tr_block.h", "tr_block.cuh",
            "tr_block_rows.cuh", "tr_block_fwd.cuh", "tr_block_bwd.cuh", "tr_launch.h", "tr_list.h",
-           "tr_check.h", "tr_vocab.h", "tr_mma.cuh"]
+           "tr_check.h", "tr_vocab.h", "tr_vocab.cuh", "tr_mma.cuh"]
 
 
 def _nvcc() -> str:

@@ -11,8 +11,8 @@
 // costs no more than many rare ones.
 #include <algorithm>
 
-#include "tr_block.cuh"
 #include "tr_launch.h"
+#include "tr_vocab.cuh"
 #include "tr_vocab.h"
 
 namespace tr {
@@ -288,18 +288,6 @@ __global__ void __launch_bounds__(kSortThreads) sort_scan_kernel(uint32_t* count
 // ---- zeros of the rows that no token has -------------------------------------------
 
 constexpr int kFillRows = 32768;  // rows whose presence a CTA knows at a time (4 KB of bits)
-
-// [from, to) set to zero by a warp: 16-byte stores between the ragged ends.
-__device__ __forceinline__ void zero_bytes(char* from, char* to) {
-    const int lane = threadIdx.x & 31;
-    char* body = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(from) + 15) & ~static_cast<uintptr_t>(15));
-    if (body > to) body = to;
-    char* end = body + (to - body) / 16 * 16;
-    // the ends are whole elements of two bytes
-    for (char* p = from + 2 * lane; p < body; p += 64) *reinterpret_cast<uint16_t*>(p) = 0;
-    for (char* p = body + 16 * lane; p < end; p += 512) *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
-    for (char* p = end + 2 * lane; p < to; p += 64) *reinterpret_cast<uint16_t*>(p) = 0;
-}
 
 __device__ __forceinline__ void fill_rows(const EmbedGradArgs& a, int64_t row_bytes, int64_t cta, int64_t ctas,
                                           uint32_t* present) {

@@ -7,12 +7,14 @@
 #include <algorithm>
 #include <cmath>
 
-#include "tr_block.cuh"
 #include "tr_launch.h"
 #include "tr_mma.cuh"
+#include "tr_vocab.cuh"
 #include "tr_vocab.h"
 
 namespace tr {
+
+constexpr int kPairs = 76;  // CTA pairs of the GPU that the plan is made for
 
 LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
     size_t at = 0;
@@ -24,6 +26,15 @@ LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
     rows_pad = round_up(rows, kTileRows);
     pitch = round_up(cols, 8);
     width = grad_width = mma::kMaxWidth;
+    // Forward: the width whose tiles come out even over the pairs of a GPU's CTAs. A narrow tile reads the rows of hidden more often
+    // (the 24), which a single tile of rows does not feel: there a narrower tile only splits the weight's reading more evenly.
+    if (!backward) {
+        int64_t least = INT64_MAX;
+        for (int n = mma::kMaxWidth; n >= 64; n -= 32) {
+            const int64_t cost = ceil_div(rows_pad / kTileRows * ceil_div(vocab, n), kPairs) * (n + (rows > kTileRows ? 24 : 0));
+            if (cost < least) least = cost, width = n;
+        }
+    }
     splits = 1;
     parts = 2 * ceil_div(vocab, width);
     pack_weight = cols % 8 != 0;
@@ -76,19 +87,38 @@ struct Ws {
 // One CTA lists them in order, with their labels (-1: outside the vocabulary) and, backward, their coefficients:
 // of the probability (dloss + dlse) and of the label (dloss). The outputs of rows without a loss are zeros.
 __global__ void __launch_bounds__(kScanThreads) rows_kernel(LossArgs a, Ws w, int backward) {
+    constexpr int kItems = 8;  // rows of a thread at a time, 32 apart: 8192 rows in one round
     __shared__ int warp_count[32];
-    __shared__ float warp_most[32];
+    __shared__ float warp_most[2][32];
     pdl_enter();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned before = (1u << lane) - 1u;
     int64_t count = 0;
-    float most = 0.0f;
-    for (int64_t r0 = 0; r0 < a.rows; r0 += kScanThreads) {
-        const int64_t r = r0 + threadIdx.x;
-        const int64_t label = r < a.rows ? a.labels[r] : a.ignore;
-        const bool counted = r < a.rows && label != a.ignore;
-        const unsigned votes = __ballot_sync(kFull, counted);
+    float most = 0.0f, most_d = 0.0f;
+    for (int64_t r0 = 0; r0 < a.rows; r0 += kItems * kScanThreads) {
+        const int64_t r1 = r0 + warp * (32 * kItems) + lane;
+        int64_t label[kItems];
+        float lse[kItems], d[kItems], e[kItems];
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int64_t r = r1 + 32 * i;
+            const bool in = r < a.rows;
+            label[i] = in ? a.labels[r] : a.ignore;
+            if (backward) {
+                lse[i] = in ? a.lse_in[r] : 0.0f;
+                d[i] = in && a.dloss ? a.dloss[r] : 1.0f;
+                e[i] = in && a.dlse ? a.dlse[r] : 0.0f;
+            }
+        }
+        unsigned votes[kItems];
+        int total = 0;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            votes[i] = __ballot_sync(kFull, label[i] != a.ignore);
+            total += __popc(votes[i]);
+        }
         __syncthreads();
-        if (lane == 0) warp_count[warp] = __popc(votes);
+        if (lane == 0) warp_count[warp] = total;
         __syncthreads();
         const int mine = warp_count[lane];
         int inc = mine;
@@ -97,59 +127,98 @@ __global__ void __launch_bounds__(kScanThreads) rows_kernel(LossArgs a, Ws w, in
             const int v = __shfl_up_sync(kFull, inc, o);
             if (lane >= o) inc += v;
         }
-        const int64_t at = count + __shfl_sync(kFull, inc - mine, warp) + __popc(votes & ((1u << lane) - 1u));
+        int64_t at = count + __shfl_sync(kFull, inc - mine, warp);
         count += __shfl_sync(kFull, inc, 31);
-        if (counted) {
-            w.map[at] = static_cast<int>(r);
-            w.labels[at] = label >= 0 && label < a.vocab ? static_cast<int>(label) : -1;
-            if (backward) {
-                const float d = a.dloss ? a.dloss[r] : 1.0f, e = a.dlse ? a.dlse[r] : 0.0f;
-                w.lse[at] = a.lse_in[r] * kL2E;
-                w.coef[at] = d + e;
-                w.onehot[at] = d;
-                most = fmaxf(most, fabsf(d) + fabsf(e));
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int64_t r = r1 + 32 * i, to = at + __popc(votes[i] & before);
+            at += __popc(votes[i]);
+            if (label[i] != a.ignore) {
+                w.map[to] = static_cast<int>(r);
+                w.labels[to] = label[i] >= 0 && label[i] < a.vocab ? static_cast<int>(label[i]) : -1;
+                if (backward) {
+                    w.lse[to] = lse[i] * kL2E;
+                    w.coef[to] = d[i] + e[i];
+                    w.onehot[to] = d[i];
+                    most = fmaxf(most, fabsf(d[i]) + fabsf(e[i]));
+                    most_d = fmaxf(most_d, fabsf(d[i]));
+                }
+            } else if (!backward && r < a.rows) {
+                a.losses[r] = 0.0f;
+                if (a.lse) a.lse[r] = 0.0f;
             }
-        } else if (!backward && r < a.rows) {
-            a.losses[r] = 0.0f;
-            if (a.lse) a.lse[r] = 0.0f;
         }
     }
     most = warp_allreduce<MaxOp, 32>(most);
-    if (lane == 0) warp_most[warp] = most;
+    most_d = warp_allreduce<MaxOp, 32>(most_d);
+    if (lane == 0) warp_most[0][warp] = most, warp_most[1][warp] = most_d;
     __syncthreads();
     if (warp == 0) {
-        most = warp_allreduce<MaxOp, 32>(warp_most[lane]);
+        most = warp_allreduce<MaxOp, 32>(warp_most[0][lane]);
+        most_d = warp_allreduce<MaxOp, 32>(warp_most[1][lane]);
         if (lane == 0) {
+            // dz is divided by the largest coefficient and brought to 2^14 (at most 2^15 with that of the lse), where float16 has
+            // room for small probabilities; and where all rows count alike, the label's -1 is a number that rounds to itself.
+            float by = 1.0f, times = 1.0f;
+            if (most > 0.0f && most < INFINITY) {
+                const bool alike = most <= 2.0f * most_d;
+                by = fminf(fmaxf(alike ? most_d : most, 0x1p-100f), 0x1p100f);
+                times = alike ? 0x1p14f : 0x1p15f;
+            }
             w.head->count = count;
-            // dz times this is at most 2^15 and mostly above float16's smallest normal number
-            int e = 0;
-            if (most > 0.0f && most < INFINITY) frexpf(most, &e);
-            e = max(-100, min(100, e));
-            w.head->scale = ldexpf(1.0f, 15 - e);
-            w.head->unscale = ldexpf(a.logit_scale, e - 15);
+            w.head->scale = times / by;
+            w.head->unscale = a.logit_scale * (by / times);
         }
     }
 }
 
-// Rows copied to rows of `pitch` elements that start on 16 bytes; map: which row each is (null: all, in order). Packed
-// rows up to the next whole tile are zeros. Backward, the gradients of rows without a loss are zeros.
+// Rows copied to rows of `pitch` elements that start on 16 bytes; map: which row each is (null: all, in order). Rows after the
+// last are zeros up to a whole block of the products' depth. Backward, the gradients of rows without a loss are zeros.
+// A warp copies 2 KB of a row; rows that start elsewhere are read in the 16-byte words that cover them.
 template <class T>
-__global__ void __launch_bounds__(kThreads) pack_kernel(LossArgs a, Ws w, const T* src, int64_t rows, T* dst, int64_t pitch,
-                                                        int64_t packed, T* zeros) {
+__global__ void __launch_bounds__(kThreads) pack_kernel(LossArgs a, Ws w, const T* src, int64_t rows, T* dst, int64_t pitch, int chunks,
+                                                        T* zeros) {
     pdl_enter();
-    const int64_t count = w.head && w.map ? w.head->count : rows;
+    const int64_t count = w.map ? w.head->count : rows, end = w.map ? (count + mma::kDepth - 1) / mma::kDepth * mma::kDepth : rows;
     const int lane = threadIdx.x & 31, warps = kThreads / 32;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * warps;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * warps + (threadIdx.x >> 5); i < packed; i += step) {
-        if (i >= (count + kTileRows - 1) / kTileRows * kTileRows) break;
-        const T* row = i < count ? src + static_cast<int64_t>(w.map ? w.map[i] : i) * a.cols : nullptr;
-        for (int c = lane; c < pitch; c += 32) dst[i * pitch + c] = row && c < a.cols ? row[c] : from_float<T>(0.0f);
+    const int words = static_cast<int>(pitch / 8);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * warps, first = static_cast<int64_t>(blockIdx.x) * warps + (threadIdx.x >> 5);
+    for (int64_t i = first; i < end * chunks; i += step) {
+        const int64_t r = i / chunks;
+        const int at = static_cast<int>(i - r * chunks) * 128 + lane;
+        uint4* to = reinterpret_cast<uint4*>(dst + r * pitch);
+        uint4 q[4];
+        if (r < count) {
+            const uintptr_t p = reinterpret_cast<uintptr_t>(src + static_cast<int64_t>(w.map ? w.map[r] : r) * a.cols);
+            const int shift = static_cast<int>(p & 15);
+            const uint4* from = reinterpret_cast<const uint4*>(p - shift);
+            const int have = (shift + 2 * a.cols + 15) / 16;  // words that cover the row
+            if (shift == 0) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (at + 32 * j < have) q[j] = __ldg(from + at + 32 * j);
+            } else {
+                uint4 next[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = at + 32 * j;
+                    q[j] = k < have ? __ldg(from + k) : make_uint4(0, 0, 0, 0);
+                    next[j] = k + 1 < have ? __ldg(from + k + 1) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q[j] = shifted(q[j], next[j], shift);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q[j] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (at + 32 * j < words) to[at + 32 * j] = q[j];
     }
     if (!zeros) return;
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * warps + (threadIdx.x >> 5); r < a.rows; r += step) {
-        if (a.labels[r] != a.ignore) continue;
-        for (int c = lane; c < a.cols; c += 32) zeros[r * a.cols + c] = from_float<T>(0.0f);
-    }
+    for (int64_t r = first; r < a.rows; r += step)
+        if (a.labels[r] == a.ignore) zero_bytes(reinterpret_cast<char*>(zeros + r * a.cols), reinterpret_cast<char*>(zeros + (r + 1) * a.cols));
 }
 
 // ---- products -------------------------------------------------------------------------
@@ -166,10 +235,13 @@ struct Product {
     int cols, splits, width;
     int64_t first, n;
     float scale;      // log2(e) logit_scale
-    void* to;         // probs, dhidden or dweight
-    int64_t pitch;    // of its rows (of `sums` for the hidden gradient)
+    int64_t rows;     // forward without packed rows
+    const int64_t* labels;
+    void* to;         // probs or dhidden
+    void* dweight;
+    int64_t pitch;    // of the rows of probs, of `sums`, or (forward) of the parts
     int begun, last;  // hidden gradient: whether the sums have earlier pieces, and whether this one completes them
-    int wide;         // rows of `to` start on 16 bytes
+    int wide, dweight_wide;  // rows of `to` and of dweight start on 16 bytes
 };
 
 __device__ __forceinline__ int tiles_of(int64_t n, int size) { return static_cast<int>((n + size - 1) / size); }
@@ -217,48 +289,66 @@ __device__ __forceinline__ void spoil(float (&v)[32]) {
     for (int i = 0; i < 32; ++i) v[i] = NAN;
 }
 
-// Forward: (maximum, sum of 2^(z - maximum)) of each half of a tile's columns, and the label's z.
+// Forward: (maximum, sum of 2^(z - maximum)) of each half of a tile's columns, and the label's z. The logits are summed in parts of
+// kPart blocks of the depth, which are added in registers (see mma::run): a thread has 128 columns of a row.
+constexpr int kPart = 8;
 template <class T>
 __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     stats_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap weight, const __grid_constant__ Product p) {
     int64_t count = 0;
-    mma::run<false, false>(
-        &hidden, &weight, kTypeBits<T>, p.lim,
+    float z[128];
+    const mma::Operands o{&hidden, &weight, false, false};
+    mma::run<kPart>(
+        o, o, kTypeBits<T>, p.lim,
         [&] {
-            count = p.w.head->count;
-            return mma::Work{tiles_of(count, kTileRows), tiles_of(p.n, p.width), 1, tiles_of(p.cols, mma::kDepth), p.width};
+            count = p.w.map ? p.w.head->count : p.rows;
+            return mma::Work(p.width, mma::Tiles{tiles_of(count, kTileRows), tiles_of(p.n, p.width), 1, tiles_of(p.cols, mma::kDepth)});
         },
-        [&](const mma::Unit& u, int row, int half, int first, int last, uint32_t at, bool ok, float*) {
-            const int limit = static_cast<int>(min(static_cast<int64_t>(last), p.n - u.n));  // columns of the vocabulary
-            const int label = row < count ? p.w.labels[row] - u.n : -1;
-            float m = -INFINITY, s = 0.0f;
-            for (int c = first; c < limit; c += 32) {
-                float z[32];
-                mma::load_columns(at + c, z);
-                if (!ok) spoil(z);
+        [&](const mma::Unit& u, int row, int half, int first, int last, uint32_t at, bool ok, float*, bool begun, bool whole) {
+            const int limit = static_cast<int>(min(static_cast<int64_t>(last), p.n - u.n)) - first;  // columns of the vocabulary
 #pragma unroll
-                for (int i = 0; i < 32; ++i) z[i] *= p.scale;
-                if (label >= c && label < min(c + 32, limit)) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (label == c + i) p.w.picked[row] = z[i];
+            for (int c = 0; c < 128; c += 8)
+                if (c < limit) mma::add_columns(at + first + c, begun, z + c);
+            if (!whole) return;
+            int label = -1;
+            if (row < count) {
+                if (p.w.map) {
+                    label = p.w.labels[row];
+                } else {
+                    const int64_t l = p.labels[row];
+                    label = l >= 0 && l < p.n ? static_cast<int>(l) : -1;
                 }
-                if (c + 32 > limit) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (c + i >= limit) z[i] = -INFINITY;
-                }
-                float top = z[0];
-#pragma unroll
-                for (int i = 1; i < 32; ++i) top = fmaxf(top, z[i]);
-                const float most = fmaxf(m, top), from = most == -INFINITY ? 0.0f : most;
-                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int i = 0; i < 32; ++i) part[i & 3] += ex2(z[i] - from);
-                s = fmaf(s, ex2(m - from), (part[0] + part[1]) + (part[2] + part[3]));
-                m = most;
             }
-            if (row < count) p.w.parts[(2 * static_cast<int64_t>(u.n / p.width) + half) * p.w.rows_pad + row] = make_float2(m, s);
+            label = label >= 0 ? label - u.n - first : -1;
+            float m = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 128; c += 16) {
+                if (c >= limit) continue;
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = c; i < c + 16; ++i) {
+                    z[i] = ok ? z[i] * p.scale : NAN;
+                    if (i >= limit) z[i] = -INFINITY;
+                    top = fmaxf(top, z[i]);
+                }
+                m = fmaxf(m, top);
+                if (label >= c && label < min(c + 16, limit)) {
+#pragma unroll
+                    for (int i = c; i < c + 16; ++i)
+                        if (label == i) p.w.picked[row] = z[i];
+                }
+            }
+            const float from = m == -INFINITY ? 0.0f : m;
+            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < 128; c += 16) {
+                if (c >= limit) continue;
+                float part[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int i = c; i < c + 16; ++i) part[i & 1] += ex2(z[i] - from);
+                s[c / 16 & 3] += part[0] + part[1];
+            }
+            if (row < count) p.w.parts[row * p.pitch + 2 * (u.n / p.width) + half] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
         });
 }
 
@@ -268,14 +358,15 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     probs_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap weight, const __grid_constant__ Product p) {
     int64_t count = 0;
     float times = 0.0f;
-    mma::run<false, false>(
-        &hidden, &weight, kTypeBits<T>, p.lim,
+    const mma::Operands o{&hidden, &weight, false, false};
+    mma::run<0>(
+        o, o, kTypeBits<T>, p.lim,
         [&] {
             count = p.w.head->count;
             times = p.w.head->scale;
-            return mma::Work{tiles_of(count, kTileRows), tiles_of(p.n, p.width), 1, tiles_of(p.cols, mma::kDepth), p.width};
+            return mma::Work(p.width, mma::Tiles{tiles_of(count, kTileRows), tiles_of(p.n, p.width), 1, tiles_of(p.cols, mma::kDepth)});
         },
-        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, float* turn) {
+        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, float* turn, bool, bool) {
             const bool in = row < count;
             const int limit = static_cast<int>(min(static_cast<int64_t>(last), p.n - u.n));
             const float lse = in ? p.w.lse[row] : 0.0f, coef = in ? p.w.coef[row] * times : 0.0f;
@@ -304,76 +395,77 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
         });
 }
 
-// Backward: the piece's part of the hidden gradient, added to those of earlier pieces; the last one writes the gradient.
+// Backward: the piece's part of the hidden gradient, added to those of earlier pieces (the last one writes the gradient), and
+// the piece's rows of the weight's gradient. One launch has both, so that there is one end at which pairs run out of work.
+template <class T>
+__device__ __forceinline__ void hidden_part(const Product& p, const mma::Unit& u, int64_t count, float times, int row, int first, int last, uint32_t at,
+                                            bool ok, float* turn) {
+    const bool in = row < count;
+    float* sums = p.w.sums + (u.split * p.w.rows_pad + row) * p.pitch + u.n;
+    T* to = in && p.last ? static_cast<T*>(p.to) + static_cast<int64_t>(p.w.map[row]) * p.cols + u.n : nullptr;
+    const int cols = static_cast<int>(min(static_cast<int64_t>(last), p.pitch - u.n));
+    for (int c = first; c < cols; c += 32) {
+        float z[32];
+        mma::load_columns(at + c, z);
+        if (!ok) spoil(z);
+        if (u.begin == u.end) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = 0.0f;
+        }
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            if (!in || c + 4 * g >= cols) continue;
+            float4* q = reinterpret_cast<float4*>(sums + c) + g;
+            if (p.begun) {
+                const float4 f = *q;
+                z[4 * g] += f.x;
+                z[4 * g + 1] += f.y;
+                z[4 * g + 2] += f.z;
+                z[4 * g + 3] += f.w;
+            }
+            if (!p.last) *q = make_float4(z[4 * g], z[4 * g + 1], z[4 * g + 2], z[4 * g + 3]);
+        }
+        if (p.last) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] *= times;
+            store_columns<T>(to, c, min(last, p.cols - u.n), z, p.wide, turn);
+        }
+    }
+}
+template <class T>
+__device__ __forceinline__ void weight_part(const Product& p, const mma::Unit& u, float times, int row, int first, int last, uint32_t at, bool ok,
+                                            float* turn) {
+    T* to = row < p.n ? static_cast<T*>(p.dweight) + (p.first + row) * p.cols + u.n : nullptr;
+    const int cols = min(last, p.cols - u.n);
+    for (int c = first; c < cols; c += 32) {
+        float z[32];
+        mma::load_columns(at + c, z);
+        if (!ok) spoil(z);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) z[i] = u.begin == u.end ? 0.0f : z[i] * times;
+        store_columns<T>(to, c, cols, z, p.dweight_wide, turn);
+    }
+}
 template <class T>
 __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
-    dhidden_kernel(const __grid_constant__ CUtensorMap probs, const __grid_constant__ CUtensorMap weight, const __grid_constant__ Product p) {
+    grads_kernel(const __grid_constant__ CUtensorMap probs_rows, const __grid_constant__ CUtensorMap weight, const __grid_constant__ CUtensorMap probs_cols,
+                 const __grid_constant__ CUtensorMap hidden, const __grid_constant__ Product p) {
     int64_t count = 0;
     float times = 0.0f;
-    mma::run<false, true>(
-        &probs, &weight, kTypeBits<T>, p.lim,
+    mma::run<0>(
+        mma::Operands{&probs_rows, &weight, false, true}, mma::Operands{&probs_cols, &hidden, true, true}, kTypeBits<T>, p.lim,
         [&] {
             count = p.w.head->count;
             times = p.w.head->unscale;
-            return mma::Work{tiles_of(count, kTileRows), tiles_of(p.cols, p.width), p.splits, tiles_of(p.n, mma::kDepth), p.width};
+            const int across = tiles_of(p.cols, p.width);
+            mma::Tiles dhidden, dweight;
+            if (p.to) dhidden = mma::Tiles{tiles_of(count, kTileRows), across, p.splits, tiles_of(p.n, mma::kDepth)};
+            if (p.dweight) dweight = mma::Tiles{tiles_of(p.n, kTileRows), across, 1, tiles_of(count, mma::kDepth)};
+            return mma::Work(p.width, dhidden, dweight);
         },
-        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, float* turn) {
-            const bool in = row < count;
-            float* sums = p.w.sums + (u.split * p.w.rows_pad + row) * p.pitch + u.n;
-            T* to = in && p.last ? static_cast<T*>(p.to) + static_cast<int64_t>(p.w.map[row]) * p.cols + u.n : nullptr;
-            const int cols = static_cast<int>(min(static_cast<int64_t>(last), p.pitch - u.n));
-            for (int c = first; c < cols; c += 32) {
-                float z[32];
-                mma::load_columns(at + c, z);
-                if (!ok) spoil(z);
-                if (u.begin == u.end) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) z[i] = 0.0f;
-                }
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    if (!in || c + 4 * g >= cols) continue;
-                    float4* q = reinterpret_cast<float4*>(sums + c) + g;
-                    if (p.begun) {
-                        const float4 f = *q;
-                        z[4 * g] += f.x;
-                        z[4 * g + 1] += f.y;
-                        z[4 * g + 2] += f.z;
-                        z[4 * g + 3] += f.w;
-                    }
-                    if (!p.last) *q = make_float4(z[4 * g], z[4 * g + 1], z[4 * g + 2], z[4 * g + 3]);
-                }
-                if (p.last) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) z[i] *= times;
-                    store_columns<T>(to, c, min(last, p.cols - u.n), z, p.wide, turn);
-                }
-            }
-        });
-}
-
-// Backward: the piece's rows of the weight's gradient.
-template <class T>
-__global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
-    dweight_kernel(const __grid_constant__ CUtensorMap probs, const __grid_constant__ CUtensorMap hidden, const __grid_constant__ Product p) {
-    float times = 0.0f;
-    mma::run<true, true>(
-        &probs, &hidden, kTypeBits<T>, p.lim,
-        [&] {
-            times = p.w.head->unscale;
-            return mma::Work{tiles_of(p.n, kTileRows), tiles_of(p.cols, p.width), 1, tiles_of(p.w.head->count, mma::kDepth), p.width};
-        },
-        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, float* turn) {
-            T* to = row < p.n ? static_cast<T*>(p.to) + (p.first + row) * p.cols + u.n : nullptr;
-            const int cols = min(last, p.cols - u.n);
-            for (int c = first; c < cols; c += 32) {
-                float z[32];
-                mma::load_columns(at + c, z);
-                if (!ok) spoil(z);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) z[i] = u.begin == u.end ? 0.0f : z[i] * times;
-                store_columns<T>(to, c, cols, z, p.wide, turn);
-            }
+        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, float* turn, bool, bool) {
+            if (u.kind == 0) hidden_part<T>(p, u, count, times, row, first, last, at, ok, turn);
+            else weight_part<T>(p, u, times, row, first, last, at, ok, turn);
         });
 }
 
@@ -391,23 +483,40 @@ __global__ void __launch_bounds__(kThreads) emit_kernel(LossArgs a, Ws w, int64_
     }
 }
 
-__global__ void __launch_bounds__(kThreads) join_kernel(LossArgs a, Ws w, int64_t parts) {
+// The parts of a row's sum joined by a warp: the maximum first, then the sums about it.
+__global__ void __launch_bounds__(kThreads) join_kernel(LossArgs a, Ws w, int parts) {
     pdl_enter();
-    const int64_t count = w.head->count;
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; r < count; r += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int64_t count = w.map ? w.head->count : a.rows;
+    const int lane = threadIdx.x & 31, warps = kThreads / 32;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * warps + (threadIdx.x >> 5); r < count; r += static_cast<int64_t>(gridDim.x) * warps) {
+        const float2* part = w.parts + r * parts;
+        const int64_t to = w.map ? w.map[r] : r, given = w.map ? w.labels[r] : a.labels[r];
+        const bool labelled = given >= 0 && given < a.vocab, gone = !w.map && given == a.ignore;
+        const float picked = labelled ? w.picked[r] : 0.0f;
         float m = -INFINITY, s = 0.0f;
-        for (int64_t i = 0; i < parts; ++i) {
-            const float2 p = w.parts[i * w.rows_pad + r];
-            const float n = fmaxf(m, p.x);
-            if (n != -INFINITY) s = s * ex2(m - n) + p.y * ex2(p.x - n);
-            else s += p.y;
-            m = n;
+        for (int i0 = 0; i0 < parts; i0 += 32 * 16) {
+            float2 p[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const int i = i0 + 32 * j + lane;
+                p[j] = i < parts ? part[i] : make_float2(-INFINITY, 0.0f);
+            }
+            float most = m;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) most = fmaxf(most, p[j].x);
+            const float from = most == -INFINITY ? 0.0f : most;
+            s *= ex2(m - from);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s = fmaf(p[j].y, ex2(p[j].x - from), s);
+            m = most;
         }
-        const float log = logf(s);
-        const int label = w.labels[r], to = w.map[r];
-        const float lse = fmaf(m, kLN2, log);
-        a.losses[to] = label >= 0 ? fmaf(m - w.picked[r], kLN2, log) : lse;
-        if (a.lse) a.lse[to] = lse;
+        const float most = warp_allreduce<MaxOp, 32>(m);
+        s = warp_allreduce<SumOp, 32>(s * ex2(m - (most == -INFINITY ? 0.0f : most)));
+        if (lane == 0) {
+            const float log = logf(s), lse = fmaf(most, kLN2, log);
+            a.losses[to] = gone ? 0.0f : labelled ? fmaf(most - picked, kLN2, log) : lse;
+            if (a.lse) a.lse[to] = gone ? 0.0f : lse;
+        }
     }
 }
 
@@ -418,28 +527,28 @@ Ws workspace(const LossArgs& a, const LossPlan& p) {
 }
 
 template <class T>
-struct Packed {
-    T* hidden;
-    const T* weight;
-    int64_t pitch;
-};
+cudaError_t pack_rows(const LossArgs& a, const Ws& w, const T* src, int64_t rows, T* dst, int64_t pitch, T* zeros, cudaStream_t stream) {
+    const int chunks = static_cast<int>(ceil_div(pitch, 1024));
+    const int64_t ctas = std::min<int64_t>(ceil_div((rows + mma::kDepth) * chunks, kThreads / 32), 1 << 14);
+    return launch_dependent(pack_kernel<T>, dim3(static_cast<unsigned>(ctas)), kThreads, 0, 1, stream, a, w, src, rows, dst, pitch, chunks, zeros);
+}
 
+// hidden's rows that have a loss, and the weight where its rows do not start on 16 bytes.
 template <class T>
-cudaError_t pack(const LossArgs& a, const LossPlan& p, const Ws& w, int backward, Packed<T>* out, cudaStream_t stream) {
-    out->hidden = reinterpret_cast<T*>(a.ws + p.hidden);
-    out->weight = static_cast<const T*>(a.weight);
-    out->pitch = p.pitch;
-    cudaError_t e = launch_dependent(rows_kernel, dim3(1), kScanThreads, 0, 1, stream, a, w, backward);
-    if (e != cudaSuccess) return e;
-    auto ctas = [](int64_t rows) { return dim3(static_cast<unsigned>(std::min<int64_t>(ceil_div(rows, kThreads / 32), 1 << 16))); };
-    e = launch_dependent(pack_kernel<T>, ctas(p.rows_pad), kThreads, 0, 1, stream, a, w, static_cast<const T*>(a.hidden), a.rows,
-                         out->hidden, p.pitch, p.rows_pad, backward ? static_cast<T*>(a.dhidden) : nullptr);
+cudaError_t pack(const LossArgs& a, const LossPlan& p, const Ws& w, int backward, const T** hidden, const T** weight, cudaStream_t stream) {
+    *hidden = static_cast<const T*>(a.hidden);
+    *weight = static_cast<const T*>(a.weight);
+    cudaError_t e = cudaSuccess;
+    if (w.map) {
+        T* to = reinterpret_cast<T*>(a.ws + p.hidden);
+        *hidden = to;
+        e = launch_dependent(rows_kernel, dim3(1), kScanThreads, 0, 1, stream, a, w, backward);
+        if (e == cudaSuccess) e = pack_rows<T>(a, w, static_cast<const T*>(a.hidden), a.rows, to, p.pitch, backward ? static_cast<T*>(a.dhidden) : nullptr, stream);
+    }
     if (e != cudaSuccess || !p.pack_weight) return e;
     T* to = reinterpret_cast<T*>(a.ws + p.weight);
-    out->weight = to;
-    Ws all{};
-    return launch_dependent(pack_kernel<T>, ctas(a.vocab), kThreads, 0, 1, stream, a, all, static_cast<const T*>(a.weight), a.vocab,
-                            to, p.pitch, a.vocab, nullptr);
+    *weight = to;
+    return pack_rows<T>(a, Ws{}, static_cast<const T*>(a.weight), a.vocab, to, p.pitch, nullptr, stream);
 }
 
 // ---- launches -------------------------------------------------------------------------
@@ -473,23 +582,26 @@ cudaError_t map_of(CUtensorMap* map, const T* p, int64_t rows, int64_t cols, int
 }
 
 // CTA pairs for `units` of work.
-template <class K>
-cudaError_t launch_product(K kernel, const CUtensorMap& a, const CUtensorMap& b, const Product& p, int64_t units, cudaStream_t stream) {
+template <class K, class... A>
+cudaError_t launch_product(K kernel, int64_t units, cudaStream_t stream, const A&... args) {
     const int resident = resident_ctas(reinterpret_cast<const void*>(kernel), mma::kThreads, mma::kSmem, 2);
     if (resident < 2) return cudaErrorInvalidConfiguration;
     const int64_t pairs = std::min<int64_t>(units, resident / 2);
-    return launch_dependent(kernel, dim3(static_cast<unsigned>(2 * pairs)), mma::kThreads, mma::kSmem, 1, stream, a, b, p);
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(2 * pairs)), mma::kThreads, mma::kSmem, 1, stream, args...);
 }
 
 template <class T>
 cudaError_t forward(const LossArgs& a, cudaStream_t stream) {
     const LossPlan p(a.rows, a.cols, a.vocab, false);
-    const Ws w = workspace(a, p);
-    Packed<T> k;
-    cudaError_t e = pack(a, p, w, 0, &k, stream);
+    Ws w = workspace(a, p);
+    // One tile of rows is not shorter without the rows that have no loss: they are read where they are.
+    const bool direct = a.rows <= kTileRows && a.cols % 8 == 0 && reinterpret_cast<uintptr_t>(a.hidden) % 16 == 0;
+    if (direct) w.map = nullptr;
+    const T *from, *table;
+    cudaError_t e = pack<T>(a, p, w, 0, &from, &table, stream);
     CUtensorMap hidden, weight;
-    if (e == cudaSuccess) e = map_of(&hidden, k.hidden, p.rows_pad, a.cols, k.pitch, mma::kRows);
-    if (e == cudaSuccess) e = map_of(&weight, k.weight, a.vocab, a.cols, k.pitch, p.width / 2);
+    if (e == cudaSuccess) e = map_of(&hidden, from, direct ? a.rows : p.rows_pad, a.cols, p.pitch, mma::kRows);
+    if (e == cudaSuccess) e = map_of(&weight, table, a.vocab, a.cols, p.pitch, p.width / 2);
     if (e != cudaSuccess) return e;
     Product d{};
     d.w = w;
@@ -498,30 +610,33 @@ cudaError_t forward(const LossArgs& a, cudaStream_t stream) {
     d.width = p.width;
     d.n = a.vocab;
     d.scale = a.logit_scale * kL2E;
-    e = launch_product(stats_kernel<T>, hidden, weight, d, p.rows_pad / kTileRows * ceil_div(a.vocab, p.width), stream);
+    d.rows = a.rows;
+    d.labels = a.labels;
+    d.pitch = p.parts;
+    e = launch_product(stats_kernel<T>, p.rows_pad / kTileRows * ceil_div(a.vocab, p.width), stream, hidden, weight, d);
     if (e != cudaSuccess) return e;
-    return launch_dependent(join_kernel, dim3(static_cast<unsigned>(ceil_div(a.rows, kThreads))), kThreads, 0, 1, stream, a, w, p.parts);
+    const int64_t ctas = std::min<int64_t>(ceil_div(a.rows, kThreads / 32), 1 << 16);
+    return launch_dependent(join_kernel, dim3(static_cast<unsigned>(ctas)), kThreads, 0, 1, stream, a, w, static_cast<int>(p.parts));
 }
 
 template <class T>
 cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
     const LossPlan p(a.rows, a.cols, a.vocab, true);
     const Ws w = workspace(a, p);
-    Packed<T> k;
-    cudaError_t e = pack(a, p, w, 1, &k, stream);
+    const T *hidden, *weight;
+    cudaError_t e = pack<T>(a, p, w, 1, &hidden, &weight, stream);
     T* probs = reinterpret_cast<T*>(a.ws + p.probs);
     CUtensorMap hidden_rows, hidden_cols, probs_rows, probs_cols;
-    if (e == cudaSuccess) e = map_of(&hidden_rows, k.hidden, p.rows_pad, a.cols, k.pitch, mma::kRows);
-    if (e == cudaSuccess) e = map_of(&hidden_cols, k.hidden, p.rows_pad, a.cols, k.pitch, mma::kDepth);
+    if (e == cudaSuccess) e = map_of(&hidden_rows, hidden, p.rows_pad, a.cols, p.pitch, mma::kRows);
+    if (e == cudaSuccess) e = map_of(&hidden_cols, hidden, p.rows_pad, a.cols, p.pitch, mma::kDepth);
     if (e == cudaSuccess) e = map_of(&probs_rows, probs, p.rows_pad, p.piece, p.piece, mma::kRows);
     if (e == cudaSuccess) e = map_of(&probs_cols, probs, p.rows_pad, p.piece, p.piece, mma::kDepth);
-    const bool align = a.cols % 8 == 0;
     const int64_t row_tiles = p.rows_pad / kTileRows;
     for (int64_t first = 0; first < a.vocab && e == cudaSuccess; first += p.piece) {
         const int64_t n = std::min(p.piece, a.vocab - first);
         CUtensorMap weight_rows, weight_cols;
-        e = map_of(&weight_rows, k.weight + first * k.pitch, n, a.cols, k.pitch, p.width / 2);
-        if (e == cudaSuccess) e = map_of(&weight_cols, k.weight + first * k.pitch, n, a.cols, k.pitch, mma::kDepth);
+        e = map_of(&weight_rows, weight + first * p.pitch, n, a.cols, p.pitch, p.width / 2);
+        if (e == cudaSuccess) e = map_of(&weight_cols, weight + first * p.pitch, n, a.cols, p.pitch, mma::kDepth);
         if (e != cudaSuccess) break;
         Product d{};
         d.w = w;
@@ -533,23 +648,21 @@ cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
         d.width = p.width;
         d.to = probs;
         d.pitch = p.piece;
-        e = launch_product(probs_kernel<T>, hidden_rows, weight_rows, d, row_tiles * ceil_div(n, p.width), stream);
-        if (e == cudaSuccess && a.dhidden) {
-            d.width = p.grad_width;
-            d.to = a.dhidden;
-            d.pitch = p.pitch;
-            d.begun = first > 0;
-            d.last = p.splits == 1 && first + n == a.vocab;
-            d.splits = p.splits;
-            d.wide = align && reinterpret_cast<uintptr_t>(a.dhidden) % 16 == 0;
-            e = launch_product(dhidden_kernel<T>, probs_rows, weight_cols, d, row_tiles * ceil_div(a.cols, d.width) * p.splits, stream);
-        }
-        if (e == cudaSuccess && a.dweight) {
-            d.width = p.grad_width;
-            d.to = a.dweight;
-            d.wide = align && reinterpret_cast<uintptr_t>(a.dweight) % 16 == 0;
-            e = launch_product(dweight_kernel<T>, probs_cols, hidden_cols, d, ceil_div(n, kTileRows) * ceil_div(a.cols, d.width), stream);
-        }
+        e = launch_product(probs_kernel<T>, row_tiles * ceil_div(n, p.width), stream, hidden_rows, weight_rows, d);
+        if (e != cudaSuccess) break;
+        const bool align = a.cols % 8 == 0;
+        const int64_t across = ceil_div(a.cols, p.grad_width);
+        d.width = p.grad_width;
+        d.splits = p.splits;
+        d.to = a.dhidden;
+        d.dweight = a.dweight;
+        d.pitch = p.pitch;
+        d.begun = first > 0;
+        d.last = p.splits == 1 && first + n == a.vocab;
+        d.wide = align && reinterpret_cast<uintptr_t>(a.dhidden) % 16 == 0;
+        d.dweight_wide = align && reinterpret_cast<uintptr_t>(a.dweight) % 16 == 0;
+        const int64_t units = (a.dhidden ? row_tiles * across * p.splits : 0) + (a.dweight ? ceil_div(n, kTileRows) * across : 0);
+        e = launch_product(grads_kernel<T>, units, stream, probs_rows, weight_cols, probs_cols, hidden_cols, d);
     }
     if (e != cudaSuccess || !a.dhidden || p.splits == 1) return e;
     const int64_t ctas = std::min<int64_t>(ceil_div(a.rows * a.cols, kThreads), 1 << 16);

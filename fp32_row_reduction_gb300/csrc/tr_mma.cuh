@@ -88,16 +88,33 @@ __device__ __forceinline__ void load_columns(uint32_t addr, float (&v)[32]) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 8 columns added to sums that are kept in registers (`begun`: not the first).
+__device__ __forceinline__ void add_columns(uint32_t addr, bool begun, float* v) {
+    uint32_t r[8];
+    __syncwarp();
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = begun ? v[i] + __uint_as_float(r[i]) : __uint_as_float(r[i]);
+}
+
 // Shared-memory descriptor of an operand's block. Depth contiguous: groups of 8 rows are 1024 bytes apart. Rows
 // contiguous: groups of 8 depths are 1024 bytes apart, and groups of 64 rows a box of 64 depths.
-template <bool ROWS_CONTIGUOUS>
-__device__ __forceinline__ uint64_t block_of(uint32_t addr) {
-    const uint64_t leading = ROWS_CONTIGUOUS ? kDepth * 128 / 16 : 1, stride = 1024 / 16;
+__device__ __forceinline__ uint64_t block_of(uint32_t addr, bool rows_contiguous) {
+    const uint64_t leading = rows_contiguous ? kDepth * 128 / 16 : 1, stride = 1024 / 16;
     return (addr >> 4) | leading << 16 | stride << 32 | uint64_t{1} << 46 | uint64_t{2} << 61;
 }
 // Encoded distance of the next 16 elements of the depth.
-template <bool ROWS_CONTIGUOUS>
-constexpr uint64_t kNext16 = (ROWS_CONTIGUOUS ? 16 * 128 : 32) / 16;
+__device__ __forceinline__ uint64_t next16(bool rows_contiguous) { return (rows_contiguous ? 16 * 128 : 32) / 16; }
+
+// The operands of one kind of products, and whether their rows (not their depth) are contiguous in memory.
+struct Operands {
+    const CUtensorMap* a;
+    const CUtensorMap* b;
+    bool a_rows, b_rows;
+};
 
 // What the launch needs apart from the operands.
 struct Limits {
@@ -135,31 +152,63 @@ struct Waits {
 
 // One unit of work: which tile, and which blocks of the depth.
 struct Unit {
+    int kind;        // of the products of a launch: 0 or 1
     int m, n;        // first row of A, first row of B
     int begin, end;  // blocks of the depth (equal: the tile is zero)
     int split;
 };
-// All of it: tiles in groups of eight rows of tiles (what the pairs read at one time is then as many rows of A as of B), each
-// tile's depth in `splits` parts.
-struct Work {
-    int m_tiles, n_tiles, splits, blocks, width;
-    __device__ __forceinline__ int64_t total() const { return static_cast<int64_t>(m_tiles) * n_tiles * splits; }
-    __device__ __forceinline__ Unit unit(int64_t i) const {
+// The tiles of one kind of products: in groups of eight rows of tiles (what the pairs read at one time is then as many rows
+// of A as of B), each tile's depth in `splits` parts.
+struct Tiles {
+    int m = 0, n = 0, splits = 1, blocks = 0;
+    __device__ __forceinline__ int64_t units() const { return static_cast<int64_t>(m) * n * splits; }
+    __device__ __forceinline__ Unit unit(int kind, int64_t i, int width) const {
         constexpr int kGroup = 8;
         const int64_t t = i / splits;
         const int split = static_cast<int>(i - t * splits);
-        const int64_t in_group = static_cast<int64_t>(kGroup) * n_tiles, g = t / in_group;
-        const int r = static_cast<int>(t - g * in_group), rows = min(kGroup, m_tiles - static_cast<int>(g) * kGroup);
+        const int64_t in_group = static_cast<int64_t>(kGroup) * n, g = t / in_group;
+        const int r = static_cast<int>(t - g * in_group), rows = min(kGroup, m - static_cast<int>(g) * kGroup);
         const int64_t from = static_cast<int64_t>(blocks) * split / splits, to = static_cast<int64_t>(blocks) * (split + 1) / splits;
-        return Unit{(static_cast<int>(g) * kGroup + r % rows) * 2 * kRows, r / rows * width, static_cast<int>(from), static_cast<int>(to), split};
+        return Unit{kind, (static_cast<int>(g) * kGroup + r % rows) * 2 * kRows, r / rows * width, static_cast<int>(from), static_cast<int>(to), split};
+    }
+};
+// The work of a launch: products of one or two kinds, in tiles of one width. A pair takes every (number of pairs)-th unit of the first
+// kind; the pairs that this leaves one unit short go ahead with as many rounds of the second kind as fill the time, and
+// then all take every so-manyth unit of the rest.
+struct Work {
+    Tiles first, second;
+    int width, pair, pairs;
+    int64_t longer, ahead;  // pairs with one more unit of the first kind; rounds that the others go ahead
+    __device__ __forceinline__ Work(int w, const Tiles& f, const Tiles& s = Tiles{}) : first(f), second(s), width(w) {
+        pair = static_cast<int>(blockIdx.x) / 2;
+        pairs = static_cast<int>(gridDim.x) / 2;
+        longer = first.units() % pairs;
+        ahead = longer > 0 && second.blocks > 0 ? (first.blocks / first.splits + second.blocks / 2) / second.blocks : 0;
+    }
+    // The pair's unit number `step`; false: there is none.
+    __device__ __forceinline__ bool unit(int64_t step, Unit* u) const {
+        const int64_t mine = first.units() / pairs + (pair < longer ? 1 : 0);
+        if (step < mine) {
+            *u = first.unit(0, pair + step * pairs, width);
+            return true;
+        }
+        int64_t i = step - mine;
+        const int64_t others = pairs - longer;
+        if (pair >= longer && i < ahead) i = i * others + (pair - longer);
+        else i = ahead * others + (pair >= longer ? i - ahead : i) * pairs + pair;
+        if (i >= second.units()) return false;
+        *u = second.unit(1, i, width);
+        return true;
     }
 };
 
-// The products of a CTA pair: plan() gives the work, once what earlier kernels wrote can be read; each pair takes every (number of
-// pairs)-th unit. out(unit, row, half, first, last, tensor address, ok, turn) writes the columns [first, last) of one row a lane;
-// ok: the sums are there (false: after a wait that gave up); turn: kTurnFloats of shared memory for the warp.
-template <bool A_ROWS, bool B_ROWS, class Plan, class Out>
-__device__ __forceinline__ void run(const CUtensorMap* a, const CUtensorMap* b, uint32_t type_bits, const Limits& lim, Plan&& plan, Out&& out) {
+// The products of a CTA pair: plan() gives the work, once what earlier kernels wrote can be read; o0 and o1 are the operands of the two
+// kinds. The sums of a tile come in one part, or (CHUNK > 0) in a part for every CHUNK blocks of the depth, for the caller to add: the
+// tensor cores round their sums toward zero, an error that grows with the length of a sum. out(unit, row, half, first, last,
+// tensor address, ok, turn, begun, whole) takes the columns [first, last) of one row a lane; ok: the sums are there (false: after
+// a wait that gave up); turn: kTurnFloats of shared memory for the warp; begun: earlier parts have come; whole: the last one.
+template <int CHUNK, class Plan, class Out>
+__device__ __forceinline__ void run(const Operands& o0, const Operands& o1, uint32_t type_bits, const Limits& lim, Plan&& plan, Out&& out) {
     extern __shared__ __align__(16) char raw[];
     __shared__ Shared s;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
@@ -191,9 +240,7 @@ __device__ __forceinline__ void run(const CUtensorMap* a, const CUtensorMap* b, 
     const uint32_t columns = s.columns;
     pdl_enter();
 
-    const int pair = static_cast<int>(blockIdx.x) / 2, pairs = static_cast<int>(gridDim.x) / 2;
     const Work work = plan();
-    const int64_t total = work.total();
     const int width = work.width;
     if (warp == 0) {
         if (lane == 0) {
@@ -201,25 +248,26 @@ __device__ __forceinline__ void run(const CUtensorMap* a, const CUtensorMap* b, 
             int stage = 0;
             uint32_t phase = 0, issued = 0;
             bool ok = true;
-            for (int64_t i = pair; i < total && ok; i += pairs) {
-                const Unit u = work.unit(i);
-                for (int k = u.begin; k < u.end && ok; ++k) {
+            Unit u;
+            for (int64_t i = 0; ok && work.unit(i, &u); ++i) {
+                const Operands o = u.kind ? o1 : o0;
+                for (int k = u.begin; k < u.end; ++k) {
                     ok = waits.wait(&s.empty[stage], phase ^ 1);
                     if (!ok) break;
                     const uint32_t bar = in_cta(smem_addr(&s.full[stage]), 0);
                     const uint32_t to_a = base + stage * kStageBytes, to_b = to_a + kRows * 128;
                     if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * bytes);
                     const int m = u.m + rank * kRows, n = u.n + rank * half, d = k * kDepth;
-                    if constexpr (A_ROWS) {
+                    if (o.a_rows) {
 #pragma unroll
-                        for (int j = 0; j < kRows / 64; ++j) copy_box(to_a + j * kDepth * 128, a, m + 64 * j, d, bar);
+                        for (int j = 0; j < kRows / 64; ++j) copy_box(to_a + j * kDepth * 128, o.a, m + 64 * j, d, bar);
                     } else {
-                        copy_box(to_a, a, d, m, bar);
+                        copy_box(to_a, o.a, d, m, bar);
                     }
-                    if constexpr (B_ROWS) {
-                        for (uint32_t j = 0; j < half / 64; ++j) copy_box(to_b + j * kDepth * 128, b, n + 64 * j, d, bar);
+                    if (o.b_rows) {
+                        for (uint32_t j = 0; j < half / 64; ++j) copy_box(to_b + j * kDepth * 128, o.b, n + 64 * j, d, bar);
                     } else {
-                        copy_box(to_b, b, d, n, bar);
+                        copy_box(to_b, o.b, d, n, bar);
                     }
                     ++issued;
                     if (++stage == kStages) stage = 0, phase ^= 1;
@@ -241,35 +289,40 @@ __device__ __forceinline__ void run(const CUtensorMap* a, const CUtensorMap* b, 
         }
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
-            // kind::f16: binary32 sums; the operands' type and layouts, width / 8 and 256 / 16
-            const uint32_t what = 1u << 4 | type_bits << 7 | type_bits << 10 | (A_ROWS ? 1u << 15 : 0) | (B_ROWS ? 1u << 16 : 0) |
-                                  static_cast<uint32_t>(width / 8) << 17 | (2 * kRows / 16) << 24;
             int stage = 0;
             uint32_t phase = 0, slot = 0, slot_phase = 0;
             bool ok = true;
-            if ((lim.debug & kDebugForceTimeout) && pair == 0) mbar_wait_bounded(&s.never, 0, kTestNs, lim.err);
-            for (int64_t i = pair; i < total && ok; i += pairs) {
-                const Unit u = work.unit(i);
-                ok = waits.wait(&s.room[slot], slot_phase ^ 1);
-                if (!ok) break;
-                fence_after();
-                const uint32_t d = columns + slot * kMaxWidth;
-                for (int k = u.begin; k < u.end; ++k) {
-                    if (lim.debug & kDebugExpireCopies) waits.die(), ok = false;
-                    else ok = waits.wait(&s.full[stage], phase);
+            if ((lim.debug & kDebugForceTimeout) && blockIdx.x == 0) mbar_wait_bounded(&s.never, 0, kTestNs, lim.err);
+            Unit u;
+            for (int64_t i = 0; ok && work.unit(i, &u); ++i) {
+                const bool a_rows = u.kind ? o1.a_rows : o0.a_rows, b_rows = u.kind ? o1.b_rows : o0.b_rows;
+                // kind::f16: binary32 sums; the operands' type and layouts, width / 8 and 256 / 16
+                const uint32_t what = 1u << 4 | type_bits << 7 | type_bits << 10 | (a_rows ? 1u << 15 : 0) | (b_rows ? 1u << 16 : 0) |
+                                      static_cast<uint32_t>(width / 8) << 17 | (2 * kRows / 16) << 24;
+                const uint64_t next_a = next16(a_rows), next_b = next16(b_rows);
+                int k = u.begin;
+                do {
+                    const int from = k, to = CHUNK > 0 ? min(k + CHUNK, u.end) : u.end;
+                    ok = waits.wait(&s.room[slot], slot_phase ^ 1);
                     if (!ok) break;
                     fence_after();
-                    const uint32_t at = base + stage * kStageBytes;
-                    const uint64_t da = block_of<A_ROWS>(at), db = block_of<B_ROWS>(at + kRows * 128);
+                    const uint32_t d = columns + slot * kMaxWidth;
+                    for (; k < to; ++k) {
+                        if (lim.debug & kDebugExpireCopies) waits.die(), ok = false;
+                        else ok = waits.wait(&s.full[stage], phase);
+                        if (!ok) break;
+                        fence_after();
+                        const uint32_t at = base + stage * kStageBytes;
+                        const uint64_t da = block_of(at, a_rows), db = block_of(at + kRows * 128, b_rows);
 #pragma unroll
-                    for (int j = 0; j < kDepth / 16; ++j)
-                        product(d, da + j * kNext16<A_ROWS>, db + j * kNext16<B_ROWS>, what, k > u.begin || j > 0);
-                    commit(smem_addr(&s.empty[stage]));
-                    if (++stage == kStages) stage = 0, phase ^= 1;
-                }
-                if (!ok) break;
-                commit(smem_addr(&s.done[slot]));
-                if (++slot == 2) slot = 0, slot_phase ^= 1;
+                        for (int j = 0; j < kDepth / 16; ++j) product(d, da + j * next_a, db + j * next_b, what, k > from || j > 0);
+                        commit(smem_addr(&s.empty[stage]));
+                        if (++stage == kStages) stage = 0, phase ^= 1;
+                    }
+                    if (!ok) break;
+                    commit(smem_addr(&s.done[slot]));
+                    if (++slot == 2) slot = 0, slot_phase ^= 1;
+                } while (k < u.end);
             }
             if (!ok) {  // the products under way
                 commit(smem_addr(&s.never));
@@ -281,16 +334,21 @@ __device__ __forceinline__ void run(const CUtensorMap* a, const CUtensorMap* b, 
         const int first = half * (width / 2), last = half ? width : width / 2;
         float* turn = reinterpret_cast<float*>(raw + (base - smem_addr(raw)) + kStages * kStageBytes) + (warp - 2) * kTurnFloats;
         uint32_t slot = 0, slot_phase = 0;
-        for (int64_t i = pair; i < total; i += pairs) {
-            const Unit u = work.unit(i);
-            const bool ok = __all_sync(kFull, waits.wait(&s.done[slot], slot_phase) && !waits.dead());
-            fence_after();
-            const uint32_t at = columns + slot * kMaxWidth + (static_cast<uint32_t>(quarter * 32) << 16);
-            out(u, u.m + static_cast<int>(rank) * kRows + quarter * 32 + lane, half, first, last, at, ok, turn);
-            fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_in(in_cta(smem_addr(&s.room[slot]), 0));
-            if (++slot == 2) slot = 0, slot_phase ^= 1;
+        Unit u;
+        for (int64_t i = 0; work.unit(i, &u); ++i) {
+            int k = u.begin;
+            do {
+                const bool begun = k > u.begin;
+                k = CHUNK > 0 ? min(k + CHUNK, u.end) : u.end;
+                const bool ok = __all_sync(kFull, waits.wait(&s.done[slot], slot_phase) && !waits.dead());
+                fence_after();
+                const uint32_t at = columns + slot * kMaxWidth + (static_cast<uint32_t>(quarter * 32) << 16);
+                out(u, u.m + static_cast<int>(rank) * kRows + quarter * 32 + lane, half, first, last, at, ok, turn, begun, k >= u.end);
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_in(in_cta(smem_addr(&s.room[slot]), 0));
+                if (++slot == 2) slot = 0, slot_phase ^= 1;
+            } while (k < u.end);
         }
     }
     __syncwarp();
