@@ -4,11 +4,11 @@
 //
 // Backward: dtable[v] = scale (the sum of dy[t] over the tokens t with ids[t] = v). The tokens are sorted
 // by id with a stable radix sort, so that a row's terms come in the order of the tokens and the sums
-// repeat bit for bit without atomics. Meanwhile the other CTAs write the zeros of rows that no
-// token has: each finds the ids of its own rows in the list. Then a warp sums the rows whose segment starts
+// repeat bit for bit without atomics. Then a warp sums the rows whose segment starts
 // in its 32 sorted tokens, 512 bytes of columns wide, in binary32. Segments longer than 64 tokens
 // are cut at the tiles' borders into partial sums, which a last kernel adds in order, so one frequent token
-// costs no more than many rare ones.
+// costs no more than many rare ones. The zeros of rows that no token has are written beside both: as many as
+// fit beside the sort of one CTA, the others beside the sums.
 #include <algorithm>
 
 #include "tr_launch.h"
@@ -99,13 +99,15 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a, int chunks
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortItems = kSortTile / kSortThreads;
+constexpr int kSortItems = kSortTile / kSortThreads;  // of a thread, at most
 constexpr uint32_t kNoKey = 0xffffffffu;  // beyond every id: the places after the last token
 
-// Shared memory of a sorting CTA.
-struct SortShared {
+// Shared memory of a sorting CTA: of a pass, and of a whole sort.
+struct PassShared {
     uint32_t hist[kSortWarps][kSortBins];
     uint32_t base[kSortBins];
+};
+struct SortShared : PassShared {
     uint32_t key[kSortTile];
     uint16_t place[kSortTile];
 };
@@ -116,25 +118,31 @@ __device__ __forceinline__ uint32_t key_of(const EmbedGradArgs& a, int64_t t) {
     return static_cast<uint32_t>(id >= 0 && id < a.vocab ? id : a.vocab);
 }
 
-// Item i of a thread: a warp's items are 512 consecutive ones.
+// Item i of a thread's ITEMS: a warp's items are consecutive.
+template <int ITEMS>
 __device__ __forceinline__ int item_of(int i) {
-    return (threadIdx.x >> 5) * (32 * kSortItems) + i * 32 + (threadIdx.x & 31);
+    return (threadIdx.x >> 5) * (32 * ITEMS) + i * 32 + (threadIdx.x & 31);
 }
 
 // rank[i] = how many items of the tile that come before item i have its digit, once base is added:
 // s.hist[w][d] becomes the count of digit d in the warps before w, and `count` (thread d < 256) the tile's
 // count of digit d. Begins and ends with a barrier.
-__device__ __forceinline__ uint32_t rank_digits(const uint32_t (&key)[kSortItems], int shift, uint32_t (&rank)[kSortItems],
-                                                SortShared& s) {
+template <int ITEMS>
+__device__ __forceinline__ uint32_t rank_digits(const uint32_t (&key)[ITEMS], int shift, uint32_t (&rank)[ITEMS], PassShared& s) {
     const int warp = threadIdx.x >> 5;
     const unsigned before = (1u << (threadIdx.x & 31)) - 1u;
     __syncthreads();
     for (int b = threadIdx.x; b < kSortWarps * kSortBins; b += kSortThreads) (&s.hist[0][0])[b] = 0;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kSortItems; ++i) {
+    for (int i = 0; i < ITEMS; ++i) {
         const uint32_t d = (key[i] >> shift) & (kSortBins - 1);
-        const unsigned same = __match_any_sync(kFull, d);
+        unsigned same = kFull;  // the lanes with this digit (votes on its bits: 37 us for 16384 tokens, with __match_any_sync 39)
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+            const unsigned vote = __ballot_sync(kFull, d >> b & 1);
+            same &= d >> b & 1 ? vote : ~vote;
+        }
         const uint32_t old = s.hist[warp][d];
         __syncwarp();
         if ((same & before) == 0) s.hist[warp][d] = old + __popc(same);
@@ -153,7 +161,7 @@ __device__ __forceinline__ uint32_t rank_digits(const uint32_t (&key)[kSortItems
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kSortItems; ++i) rank[i] += s.hist[warp][(key[i] >> shift) & (kSortBins - 1)];
+    for (int i = 0; i < ITEMS; ++i) rank[i] += s.hist[warp][(key[i] >> shift) & (kSortBins - 1)];
     return count;
 }
 
@@ -175,16 +183,17 @@ __device__ __forceinline__ uint32_t bins_before(uint32_t n, uint32_t* warp_total
     return sum;
 }
 
-// Up to kSortTile tokens sorted by one CTA.
+// Up to 1024 ITEMS tokens sorted by one CTA.
+template <int ITEMS>
 __device__ __forceinline__ void sort_one_tile(const EmbedGradArgs& a, int bits, uint32_t* keys, uint32_t* places,
                                               SortShared& s) {
     __shared__ uint32_t warp_total[kSortBins / 32];
     const int n = static_cast<int>(a.tokens);
-    uint32_t key[kSortItems], rank[kSortItems];
-    uint16_t place[kSortItems];
+    uint32_t key[ITEMS], rank[ITEMS];
+    uint16_t place[ITEMS];
 #pragma unroll
-    for (int i = 0; i < kSortItems; ++i) {
-        const int t = item_of(i);
+    for (int i = 0; i < ITEMS; ++i) {
+        const int t = item_of<ITEMS>(i);
         key[i] = t < n ? key_of(a, t) : kNoKey;
         place[i] = static_cast<uint16_t>(t);
     }
@@ -194,21 +203,21 @@ __device__ __forceinline__ void sort_one_tile(const EmbedGradArgs& a, int bits, 
         if (threadIdx.x < kSortBins) s.base[threadIdx.x] = base;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kSortItems; ++i) {
+        for (int i = 0; i < ITEMS; ++i) {
             const uint32_t at = s.base[(key[i] >> shift) & (kSortBins - 1)] + rank[i];
             s.key[at] = key[i];
             s.place[at] = place[i];
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kSortItems; ++i) {
-            key[i] = s.key[item_of(i)];
-            place[i] = s.place[item_of(i)];
+        for (int i = 0; i < ITEMS; ++i) {
+            key[i] = s.key[item_of<ITEMS>(i)];
+            place[i] = s.place[item_of<ITEMS>(i)];
         }
     }
 #pragma unroll
-    for (int i = 0; i < kSortItems; ++i) {
-        const int t = item_of(i);
+    for (int i = 0; i < ITEMS; ++i) {
+        const int t = item_of<ITEMS>(i);
         if (t < n) {
             keys[t] = key[i];
             places[t] = place[i];
@@ -217,42 +226,44 @@ __device__ __forceinline__ void sort_one_tile(const EmbedGradArgs& a, int bits, 
 }
 
 // One pass of a sort over several CTAs: the tiles' counts of each digit, their places, the scatter.
+constexpr int kPassItems = kPassTile / kSortThreads;
 struct SortPass {
     const uint32_t* keys;  // null: the first pass, from the ids
     const uint32_t* places;
     uint32_t* out_keys;
     uint32_t* out_places;
     uint32_t* counts;  // [bin][tile]
+    uint32_t* listed;  // emptied
     int64_t tiles;
     int shift;
 };
 
 template <bool SCATTER>
 __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(EmbedGradArgs a, SortPass p) {
-    extern __shared__ __align__(16) char raw[];
-    SortShared& s = *reinterpret_cast<SortShared*>(raw);
+    __shared__ PassShared s;
     pdl_enter();
     const int64_t tile = blockIdx.x;
-    uint32_t key[kSortItems], rank[kSortItems];
+    if (tile == 0 && threadIdx.x == 0) *p.listed = 0;
+    uint32_t key[kPassItems], rank[kPassItems], place[kPassItems];
 #pragma unroll
-    for (int i = 0; i < kSortItems; ++i) {
-        const int64_t t = tile * kSortTile + item_of(i);
+    for (int i = 0; i < kPassItems; ++i) {
+        const int64_t t = tile * kPassTile + item_of<kPassItems>(i);
         key[i] = t < a.tokens ? (p.keys ? p.keys[t] : key_of(a, t)) : kNoKey;
+        if (SCATTER) place[i] = t < a.tokens && p.places ? p.places[t] : static_cast<uint32_t>(t);
     }
+    const uint32_t base = SCATTER && threadIdx.x < kSortBins ? p.counts[threadIdx.x * p.tiles + tile] : 0;
     const uint32_t count = rank_digits(key, p.shift, rank, s);
     if constexpr (!SCATTER) {
         if (threadIdx.x < kSortBins) p.counts[threadIdx.x * p.tiles + tile] = count;
     } else {
-        if (threadIdx.x < kSortBins) s.base[threadIdx.x] = p.counts[threadIdx.x * p.tiles + tile];
+        if (threadIdx.x < kSortBins) s.base[threadIdx.x] = base;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kSortItems; ++i) {
-            const int64_t t = tile * kSortTile + item_of(i);
-            if (t < a.tokens) {
-                const uint32_t at = s.base[(key[i] >> p.shift) & (kSortBins - 1)] + rank[i];
-                p.out_keys[at] = key[i];
-                p.out_places[at] = p.places ? p.places[t] : static_cast<uint32_t>(t);
-            }
+        for (int i = 0; i < kPassItems; ++i) {
+            if (tile * kPassTile + item_of<kPassItems>(i) >= a.tokens) continue;
+            const uint32_t at = s.base[(key[i] >> p.shift) & (kSortBins - 1)] + rank[i];
+            p.out_keys[at] = key[i];
+            p.out_places[at] = place[i];
         }
     }
 }
@@ -260,15 +271,21 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(EmbedGradArgs a
 // Where each tile's items of each digit go: the counts' exclusive sums in order of digit and tile. (The last
 // tile's missing items have digit 255 and are counted last, so they move nothing.)
 __global__ void __launch_bounds__(kSortThreads) sort_scan_kernel(uint32_t* counts, int64_t tiles) {
+    constexpr int kEach = 8;  // counts of a thread at a time
     __shared__ uint32_t warp_total[kSortWarps], carry_in;
     pdl_enter();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t n = tiles * kSortBins;
+    const int64_t n = tiles * kSortBins;  // a multiple of kEach
     uint32_t carry = 0;
-    for (int64_t at = 0; at < n; at += kSortThreads) {
-        const int64_t i = at + threadIdx.x;
-        const uint32_t v = i < n ? counts[i] : 0;
-        uint32_t inc = v;
+    for (int64_t at = 0; at < n; at += kEach * kSortThreads) {
+        const int64_t i = at + kEach * static_cast<int64_t>(threadIdx.x);
+        uint4 q[2] = {};
+        if (i < n) q[0] = reinterpret_cast<const uint4*>(counts + i)[0], q[1] = reinterpret_cast<const uint4*>(counts + i)[1];
+        uint32_t v[kEach], sum = 0;
+        memcpy(v, q, sizeof(v));
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) sum += v[j];
+        uint32_t inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t u = __shfl_up_sync(kFull, inc, o);
@@ -276,10 +293,19 @@ __global__ void __launch_bounds__(kSortThreads) sort_scan_kernel(uint32_t* count
         }
         if (lane == 31) warp_total[warp] = inc;
         __syncthreads();
-        uint32_t before = 0;
+        uint32_t before = carry + inc - sum;
         for (int w = 0; w < warp; ++w) before += warp_total[w];
-        if (i < n) counts[i] = carry + before + inc - v;
-        if (threadIdx.x == kSortThreads - 1) carry_in = carry + before + inc;
+        if (threadIdx.x == kSortThreads - 1) carry_in = before + sum;
+        if (i < n) {
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) {
+                const uint32_t c = v[j];
+                v[j] = before;
+                before += c;
+            }
+            memcpy(q, v, sizeof(v));
+            reinterpret_cast<uint4*>(counts + i)[0] = q[0], reinterpret_cast<uint4*>(counts + i)[1] = q[1];
+        }
         __syncthreads();
         carry = carry_in;
     }
@@ -288,11 +314,22 @@ __global__ void __launch_bounds__(kSortThreads) sort_scan_kernel(uint32_t* count
 // ---- zeros of the rows that no token has -------------------------------------------
 
 constexpr int kFillRows = 32768;  // rows whose presence a CTA knows at a time (4 KB of bits)
+// Zeros that take as long as the sort of one CTA, for each of its threads' items (33 us for 16). 16384 x 4096 bf16 into 50257 rows: 104 us,
+// with half as much 111, with all of them beside the sort 109.
+constexpr int64_t kFillBytes = 15 << 20;
 
-__device__ __forceinline__ void fill_rows(const EmbedGradArgs& a, int64_t row_bytes, int64_t cta, int64_t ctas,
-                                          uint32_t* present) {
-    const int64_t begin = a.vocab * cta / ctas, end = a.vocab * (cta + 1) / ctas;
-    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+// The rows [r0, r1) without a bit of `present` (bit i: row r0 + i) set to zero by the CTA.
+__device__ __forceinline__ void zero_absent(const EmbedGradArgs& a, int64_t row_bytes, int64_t r0, int64_t r1, const uint32_t* present) {
+    for (int64_t r = r0 + (threadIdx.x >> 5); r < r1; r += blockDim.x >> 5) {
+        if (present[(r - r0) >> 5] >> ((r - r0) & 31) & 1) continue;
+        char* row = static_cast<char*>(a.dtable) + r * row_bytes;
+        zero_bytes(row, row + row_bytes);
+    }
+}
+
+// The CTA's share (cta of ctas) of the rows below `rows`, from the ids as they come: every CTA looks at all of them.
+__device__ __forceinline__ void fill_unsorted(const EmbedGradArgs& a, int64_t row_bytes, int64_t rows, int64_t cta, int64_t ctas, uint32_t* present) {
+    const int64_t begin = rows * cta / ctas, end = rows * (cta + 1) / ctas;
     for (int64_t r0 = begin; r0 < end; r0 += kFillRows) {
         const int64_t r1 = min(r0 + kFillRows, end);
         __syncthreads();
@@ -308,33 +345,77 @@ __device__ __forceinline__ void fill_rows(const EmbedGradArgs& a, int64_t row_by
                 if (id[j] >= r0 && id[j] < r1) atomicOr(&present[(id[j] - r0) >> 5], 1u << ((id[j] - r0) & 31));
         }
         __syncthreads();
-        for (int64_t r = r0 + warp; r < r1; r += warps) {
-            if (present[(r - r0) >> 5] >> ((r - r0) & 31) & 1) continue;
-            char* row = static_cast<char*>(a.dtable) + r * row_bytes;
-            zero_bytes(row, row + row_bytes);
-        }
+        zero_absent(a, row_bytes, r0, r1, present);
     }
 }
 
-// The sort of up to kSortTile tokens (CTA 0, when `sort`) beside the zeros (the others); the list of long
-// segments is emptied.
-__global__ void __launch_bounds__(kSortThreads) prepare_kernel(EmbedGradArgs a, int64_t row_bytes, int sort, int bits,
-                                                               uint32_t* keys, uint32_t* places, uint32_t* listed) {
+// How many keys are below `key` (a warp looks at 32 places a step).
+__device__ __forceinline__ int64_t keys_below(const uint32_t* keys, int64_t tokens, int64_t key) {
+    const int lane = threadIdx.x & 31;
+    int64_t lo = 0, hi = tokens;  // below lo keys are smaller, from hi on they are not
+    while (lo < hi) {
+        const int64_t step = (hi - lo + 31) / 32, t = lo + (lane + 1) * step - 1;
+        const int n = __popc(__ballot_sync(kFull, t < hi && keys[t] < key));
+        const int64_t next = lo + (n + 1) * step - 1;
+        lo += n * step;
+        if (next < hi) hi = next;
+        if (lo > hi) lo = hi;
+    }
+    return lo;
+}
+
+// The CTA's share of the rows from `rows` on, from the sorted keys.
+__device__ __forceinline__ void fill_sorted(const EmbedGradArgs& a, int64_t row_bytes, int64_t rows, int64_t cta, int64_t ctas, const uint32_t* keys,
+                                            uint32_t* present) {
+    __shared__ int64_t range[2];
+    const int64_t n = a.vocab - rows, begin = rows + n * cta / ctas, end = rows + n * (cta + 1) / ctas;
+    for (int64_t r0 = begin; r0 < end; r0 += kFillRows) {
+        const int64_t r1 = min(r0 + kFillRows, end);
+        __syncthreads();
+        for (int i = threadIdx.x; i < kFillRows / 32; i += blockDim.x) present[i] = 0;
+        if (threadIdx.x < 64) {
+            const int64_t at = keys_below(keys, a.tokens, threadIdx.x < 32 ? r0 : r1);
+            if ((threadIdx.x & 31) == 0) range[threadIdx.x >> 5] = at;
+        }
+        __syncthreads();
+        if (range[1] - range[0] <= 4 * (r1 - r0)) {
+            for (int64_t t = range[0] + threadIdx.x; t < range[1]; t += blockDim.x) {
+                const int64_t bit = keys[t] - r0;
+                atomicOr(&present[bit >> 5], 1u << (bit & 31));
+            }
+        } else {  // many tokens with few ids: each row is looked for
+            for (int64_t r = r0 + threadIdx.x; r < r1; r += blockDim.x) {
+                int64_t lo = range[0], hi = range[1];
+                while (lo < hi) {
+                    const int64_t t = (lo + hi) / 2;
+                    if (keys[t] < r) lo = t + 1;
+                    else hi = t;
+                }
+                if (lo < range[1] && keys[lo] == r) atomicOr(&present[(r - r0) >> 5], 1u << ((r - r0) & 31));
+            }
+        }
+        __syncthreads();
+        zero_absent(a, row_bytes, r0, r1, present);
+    }
+}
+
+// The sort of up to kSortTile tokens by CTA 0 beside the zeros of the first rows by the others; the list of long segments is emptied.
+template <int ITEMS>
+__global__ void __launch_bounds__(kSortThreads) prepare_kernel(EmbedGradArgs a, int64_t row_bytes, int64_t rows, int bits, uint32_t* keys,
+                                                               uint32_t* places, uint32_t* listed) {
     extern __shared__ __align__(16) char raw[];
     pdl_enter();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *listed = 0;
-    if (sort && blockIdx.x == 0) {
-        sort_one_tile(a, bits, keys, places, *reinterpret_cast<SortShared*>(raw));
-    } else if (!a.accumulate) {
-        fill_rows(a, row_bytes, static_cast<int64_t>(blockIdx.x) - sort, static_cast<int64_t>(gridDim.x) - sort,
-                  reinterpret_cast<uint32_t*>(raw));
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) *listed = 0;
+        sort_one_tile<ITEMS>(a, bits, keys, places, *reinterpret_cast<SortShared*>(raw));
+    } else {
+        fill_unsorted(a, row_bytes, rows, static_cast<int64_t>(blockIdx.x) - 1, static_cast<int64_t>(gridDim.x) - 1, reinterpret_cast<uint32_t*>(raw));
     }
 }
 
 // ---- sums over segments of equal ids -------------------------------------------------
 
 constexpr int kLong = 2 * kSumTile;  // tokens of the longest segment that one warp sums
-constexpr int kAhead = 8;            // rows under way
 
 struct SumArgs {
     EmbedGradArgs a;
@@ -344,125 +425,148 @@ struct SumArgs {
     float* partials;   // [tile][continued, begun][pitch]
     int blocks;        // column blocks of a row
     int pitch;
+    int fill_ctas;     // the first CTAs, which write the zeros of the rows from fill_rows on
+    int64_t fill_rows, row_bytes;
 };
 
-// dtable[key] (+)= scale acc, one lane's columns.
-template <class G, int N>
-__device__ __forceinline__ void write_row(const EmbedGradArgs& a, uint32_t key, int c, const float (&acc)[N]) {
-    if (c >= a.cols) return;
-    G* p = static_cast<G*>(a.dtable) + static_cast<int64_t>(key) * a.cols + c;
-    float v[N];
-    if (a.accumulate) {
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = to_float(p[k]);
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = fmaf(a.scale, acc[k], v[k]);
-    } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = a.scale * acc[k];
+// A lane's columns of a row: 16 bytes of it as they lie, and the word after them where rows start elsewhere (WIDE: nowhere).
+template <class T>
+constexpr int kLane = 16 / sizeof(T);
+template <class T, bool WIDE>
+struct Piece {
+    uint4 lo, hi;
+    int shift;
+    __device__ __forceinline__ void load(const T* row, int c, int cols) {
+        if constexpr (WIDE) {
+            if (c < cols) lo = __ldg(reinterpret_cast<const uint4*>(row + c));
+        } else {
+            const uintptr_t p = reinterpret_cast<uintptr_t>(row + c), end = reinterpret_cast<uintptr_t>(row + cols);
+            shift = static_cast<int>(p & 15);
+            const uint4* q = reinterpret_cast<const uint4*>(p - shift);
+            lo = hi = make_uint4(0, 0, 0, 0);
+            if (c < cols) lo = __ldg(q);
+            if (c < cols && reinterpret_cast<uintptr_t>(q + 1) < end) hi = __ldg(q + 1);
+        }
     }
-    store_floats<G, N>(p, v);
+    __device__ __forceinline__ void add_to(float (&acc)[kLane<T>]) const {
+        T e[kLane<T>];
+        const uint4 q = WIDE ? lo : shifted(lo, hi, shift);
+        memcpy(e, &q, 16);
+#pragma unroll
+        for (int i = 0; i < kLane<T>; ++i) acc[i] += to_float(e[i]);
+    }
+};
+
+// dtable[key] (+)= scale acc: a lane's columns from c on, or (not WIDE) turned in shared memory so that neighbouring lanes
+// write neighbouring columns.
+template <class G, int N, bool WIDE>
+__device__ __forceinline__ void write_row(const EmbedGradArgs& a, uint32_t key, int c, const float (&acc)[N], float* turn) {
+    G* row = static_cast<G*>(a.dtable) + static_cast<int64_t>(key) * a.cols;
+    if constexpr (WIDE) {
+        if (c >= a.cols) return;
+        float v[N];
+        if (a.accumulate) {
+            load_floats<G, N>(row + c, v);
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = fmaf(a.scale, acc[k], v[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = a.scale * acc[k];
+        }
+        store_floats<G, N>(row + c, v);
+    } else {
+        const int lane = threadIdx.x & 31, c0 = c - lane * N;
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < N; ++k) turn[lane * (N + 1) + k] = acc[k];
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int i = 32 * k + lane;
+            if (c0 + i >= a.cols) continue;
+            const float v = a.scale * turn[i / N * (N + 1) + i % N];
+            row[c0 + i] = from_float<G>(a.accumulate ? to_float(row[c0 + i]) + v : v);
+        }
+    }
 }
 
-// Columns of a block: 32 lanes of N elements, or of eight single ones.
-template <int N>
-constexpr int kBlockCols = N == 1 ? 256 : 32 * N;
-
-template <class T, class G, int N>
+template <class T, class G, bool WIDE>
 __global__ void __launch_bounds__(kThreads) sum_kernel(SumArgs s) {
-    constexpr int kParts = N == 1 ? 8 : 1;  // single elements: eight columns a lane, 32 apart
-    constexpr int kSpan = kSumTile + kLong;
-    __shared__ uint32_t key_window[kLong + kSpan + kLong + 1];  // from kLong tokens before the tile
-    __shared__ uint32_t place_window[kSpan];
+    constexpr int N = kLane<T>, kAhead = WIDE ? 16 : 8;  // rows under way
+    __shared__ uint32_t shared_words[kFillRows / 32 > kWarps * 32 * (N + 1) ? kFillRows / 32 : kWarps * 32 * (N + 1)];
     pdl_enter();
     const EmbedGradArgs& a = s.a;
+    if (static_cast<int>(blockIdx.x) < s.fill_ctas) {
+        fill_sorted(a, s.row_bytes, s.fill_rows, blockIdx.x, s.fill_ctas, s.keys, shared_words);
+        return;
+    }
     const int lane = threadIdx.x & 31;
-    const int groups = (s.blocks + kWarps - 1) / kWarps;
-    const int64_t tiles = (a.tokens + kSumTile - 1) / kSumTile;
-    for (int64_t item = blockIdx.x; item < tiles * groups; item += gridDim.x) {
-        const int64_t tile = item / groups, t0 = tile * kSumTile;
-        const int blk = static_cast<int>(item - tile * groups) * kWarps + (threadIdx.x >> 5);
-        __syncthreads();
-        for (int i = threadIdx.x; i < kLong + kSpan + kLong + 1; i += kThreads) {
-            const int64_t t = t0 - kLong + i;
-            key_window[i] = t >= 0 && t < a.tokens ? s.keys[t] : kNoKey;
-            if (i < kSpan) place_window[i] = t0 + i < a.tokens ? s.places[t0 + i] : 0;
-        }
-        __syncthreads();
-        if (blk >= s.blocks) continue;  // (no barrier before the loop's next)
-        const uint32_t* keys = key_window + kLong;
-        const int have = static_cast<int>(min(static_cast<int64_t>(kSumTile), a.tokens - t0));
-        const int c0 = blk * kBlockCols<N> + lane * (N == 1 ? 1 : N);
-        // the segment that reaches in from the tile before, if it is long, is this tile's up to its end
-        int at = 0;
-        bool continued = false;
-        if (t0 > 0 && keys[-1] == keys[0]) {
-            int first = -1;
-            while (first > -kLong && keys[first - 1] == keys[0]) --first;
-            continued = keys[first + kLong] == keys[0];
-            if (!continued)
-                while (at < have && keys[at] == keys[0]) ++at;  // its own tile sums it
-        }
-        float acc[kParts][N];
+    float* turn = reinterpret_cast<float*>(shared_words) + (threadIdx.x >> 5) * 32 * (N + 1);
+    const int64_t units = (a.tokens + kSumTile - 1) / kSumTile * s.blocks;
+    for (int64_t unit = (static_cast<int64_t>(blockIdx.x) - s.fill_ctas) * kWarps + (threadIdx.x >> 5); unit < units;
+         unit += (static_cast<int64_t>(gridDim.x) - s.fill_ctas) * kWarps) {
+        const int64_t tile = unit / s.blocks, t0 = tile * kSumTile;
+        const int blk = static_cast<int>(unit - tile * s.blocks), c = (blk * 32 + lane) * N;
+        // the keys from 64 tokens before the tile to 64 behind it, the places of those a short segment may have
+        uint32_t key[5], place[3];
 #pragma unroll
-        for (int q = 0; q < kParts; ++q)
+        for (int i = 0; i < 5; ++i) {
+            const int64_t t = t0 + 32 * (i - 2) + lane;
+            const bool in = t >= 0 && t < a.tokens;
+            key[i] = in ? s.keys[t] : kNoKey;
+            if (i >= 2) place[i - 2] = in ? s.places[t] : 0;
+        }
+        const uint32_t mine = key[2], first = __shfl_sync(kFull, mine, 0), before = __shfl_sync(kFull, key[1], 31);
+        const uint32_t left = __shfl_up_sync(kFull, mine, 1);
+        const unsigned heads = __ballot_sync(kFull, lane == 0 ? mine != before : mine != left);
+        const int have = __popc(__ballot_sync(kFull, mine < a.vocab));  // tokens with a row; the others are last
+        if (have == 0) continue;
+        // tokens right behind the tile that belong to its last segment (64 at most are of interest)
+        const uint32_t final = __shfl_sync(kFull, mine, 31);
+        const unsigned more1 = __ballot_sync(kFull, key[3] == final), more2 = __ballot_sync(kFull, key[4] == final);
+        const int behind = more1 != kFull ? __ffs(~more1) - 1 : more2 != kFull ? 31 + __ffs(~more2) : 64;
+        const int next = heads & ~1u ? __ffs(heads & ~1u) - 1 : kSumTile;  // where the first segment ends, if in the tile
+        int begin = 0, end = have;
+        bool continued = false, long_last = false;
+        if (!(heads & 1)) {  // the first segment began before: a long one is summed up to here and in the tile, a short one by its own tile
+            const unsigned prev1 = __ballot_sync(kFull, key[1] == first), prev2 = __ballot_sync(kFull, key[0] == first);
+            const int ahead = prev1 != kFull ? __clz(~prev1) : prev2 != kFull ? 32 + __clz(~prev2) : 64;
+            continued = ahead + (next < kSumTile ? next : kSumTile + behind) > kLong;
+            if (!continued) begin = next;
+        }
+        const unsigned begun = heads & (have == kSumTile ? kFull : (1u << have) - 1u);
+        if (have == kSumTile && begun != 0) {
+            const int head = 31 - __clz(begun);
+            long_last = kSumTile - head + behind > kLong;
+            if (!long_last) end = kSumTile + behind;
+            else if (blk == 0 && lane == 0) s.listed[1 + atomicAdd(s.listed, 1u)] = static_cast<uint32_t>(t0 + head);
+        }
+        float acc[N];
 #pragma unroll
-            for (int k = 0; k < N; ++k) acc[q][k] = 0.0f;
-        // whether the segment at `at` is long
-        bool large = continued;
-        bool fresh = !continued;  // `at` begins a segment
-        int stop = have;          // a short segment that begins in the tile is summed to its end
-        while (at < stop) {
-            float v[kAhead][kParts][N];
+        for (int k = 0; k < N; ++k) acc[k] = 0.0f;
+        for (int at = begin; at < end; at += kAhead) {
+            Piece<T, WIDE> v[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                const int i = min(at + j, kSpan - 1);
-                const bool mine = keys[i] < a.vocab && (i < have || keys[i] == keys[have - 1]);
-                const T* row = static_cast<const T*>(a.dy) + static_cast<int64_t>(place_window[i]) * a.cols;
-#pragma unroll
-                for (int q = 0; q < kParts; ++q) {
-                    const int c = c0 + 32 * q;
-                    if (mine && c < a.cols) load_floats<T, N>(row + c, v[j][q]);
-                }
+                const int i = at + j;
+                const uint32_t p = __shfl_sync(kFull, i < 32 ? place[0] : i < 64 ? place[1] : place[2], i & 31);
+                if (i < end) v[j].load(static_cast<const T*>(a.dy) + static_cast<int64_t>(p) * a.cols, c, a.cols);
             }
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                if (at < stop) {
-                    const uint32_t key = keys[at];
-                    if (key >= a.vocab) {  // behind the last id: nothing more
-                        stop = at;
-                    } else {
-                        if (fresh) {
-                            large = keys[at + kLong] == key;
-                            fresh = false;
-                            if (large && blk == 0 && lane == 0) s.listed[1 + atomicAdd(s.listed, 1u)] = static_cast<uint32_t>(t0 + at);
-                            if (!large)
-                                while (keys[stop - 1] == key && keys[stop] == key) ++stop;
-                        }
-#pragma unroll
-                        for (int q = 0; q < kParts; ++q)
-#pragma unroll
-                            for (int k = 0; k < N; ++k) acc[q][k] += v[j][q][k];
-                        ++at;
-                        const bool last = keys[at] != key;
-                        if (last || (large && at == have)) {
-#pragma unroll
-                            for (int q = 0; q < kParts; ++q) {
-                                const int c = c0 + 32 * q;
-                                if (!large) {
-                                    write_row<G, N>(a, key, c, acc[q]);
-                                } else if (c < a.cols) {
-                                    float* p = s.partials + (2 * tile + (continued ? 0 : 1)) * s.pitch + c;
-                                    store_floats<float, N>(p, acc[q]);
-                                }
-#pragma unroll
-                                for (int k = 0; k < N; ++k) acc[q][k] = 0.0f;
-                            }
-                            continued = false;
-                            fresh = true;
-                        }
-                    }
+                const int i = at + j;
+                if (i >= end) continue;
+                v[j].add_to(acc);
+                // the last of a segment, or of the tile's part of a long one
+                if (i != end - 1 && !(i + 1 < kSumTile && (heads >> (i + 1) & 1))) continue;
+                const bool part = (continued && i < next) || (long_last && i == end - 1);
+                if (!part) {
+                    write_row<G, N, WIDE>(a, __shfl_sync(kFull, mine, min(i, 31)), c, acc, turn);
+                } else if (c < a.cols) {
+                    store_floats<float, N>(s.partials + (2 * tile + (continued && i < next ? 0 : 1)) * s.pitch + c, acc);
                 }
+#pragma unroll
+                for (int k = 0; k < N; ++k) acc[k] = 0.0f;
             }
         }
     }
@@ -485,47 +589,44 @@ __device__ __forceinline__ int64_t segment_end(const uint32_t* keys, int64_t tok
     return hi;
 }
 
-// The partial sums of the long segments, added in order: a CTA takes one segment and one block of columns, and each
+// The partial sums of the long segments, added in order: a CTA takes one segment and 256 columns, and each
 // of its warps one run of the partials.
-template <class G, int N>
+template <class G>
 __global__ void __launch_bounds__(kThreads) join_kernel(SumArgs s) {
-    constexpr int kParts = N == 1 ? 8 : 1;
-    __shared__ float part[kWarps][kBlockCols<N>];
+    constexpr int kCols = 256, N = kCols / 32;
+    __shared__ float part[kWarps][kCols];
     pdl_enter();
     const EmbedGradArgs& a = s.a;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t items = static_cast<int64_t>(*s.listed) * s.blocks;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = (a.cols + kCols - 1) / kCols;
+    const int64_t items = static_cast<int64_t>(*s.listed) * blocks;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int64_t from = s.listed[1 + item / s.blocks];
-        const int c0 = static_cast<int>(item % s.blocks) * kBlockCols<N> + lane * (N == 1 ? 1 : N);
+        const int64_t from = s.listed[1 + item / blocks];
+        const int c0 = static_cast<int>(item % blocks) * kCols, c = c0 + lane * N;
         const int64_t end = segment_end(s.keys, a.tokens, from);
         const int64_t first = from / kSumTile, count = (end - 1) / kSumTile - first + 1;
         const int64_t b = count * warp / kWarps, e = count * (warp + 1) / kWarps;
-        __syncthreads();
+        float acc[N];
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) {
-            const int c = c0 + 32 * q;
-            float acc[N];
+        for (int k = 0; k < N; ++k) acc[k] = 0.0f;
+        if (c < a.cols) {
+#pragma unroll 8
+            for (int64_t i = b; i < e; ++i) {
+                float v[N];
+                load_floats<float, N>(s.partials + (2 * (first + i) + (i == 0 ? 1 : 0)) * s.pitch + c, v);
 #pragma unroll
-            for (int k = 0; k < N; ++k) acc[k] = 0.0f;
-            if (c < a.cols) {
-#pragma unroll 4
-                for (int64_t i = b; i < e; ++i) {
-                    float v[N];
-                    load_floats<float, N>(s.partials + (2 * (first + i) + (i == 0 ? 1 : 0)) * s.pitch + c, v);
-#pragma unroll
-                    for (int k = 0; k < N; ++k) acc[k] += v[k];
-                }
+                for (int k = 0; k < N; ++k) acc[k] += v[k];
             }
-#pragma unroll
-            for (int k = 0; k < N; ++k) part[warp][32 * q + lane * (N == 1 ? 1 : N) + k] = acc[k];
         }
         __syncthreads();
-        for (int c = threadIdx.x; c < kBlockCols<N>; c += kThreads) {
-            float acc[1] = {0.0f};
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) acc[0] += part[w][c];
-            write_row<G, 1>(a, s.keys[from], static_cast<int>(item % s.blocks) * kBlockCols<N> + c, acc);
+        for (int k = 0; k < N; ++k) part[warp][lane * N + k] = acc[k];
+        __syncthreads();
+        G* row = static_cast<G*>(a.dtable) + static_cast<int64_t>(s.keys[from]) * a.cols;
+        for (int i = threadIdx.x; i < kCols && c0 + i < a.cols; i += kThreads) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) sum += part[w][i];
+            row[c0 + i] = from_float<G>(a.accumulate ? fmaf(a.scale, sum, to_float(row[c0 + i])) : a.scale * sum);
         }
     }
 }
@@ -543,25 +644,31 @@ cudaError_t embed(const EmbedArgs& a, cudaStream_t stream) {
     return launch_dependent(embed_kernel<T, N>, dim3(static_cast<unsigned>(ctas)), kThreads, 0, 1, stream, a, chunks);
 }
 
-template <class T, class G, int N>
-cudaError_t sums(const SumArgs& s0, int64_t sum_tiles, cudaStream_t stream) {
+template <class T, class G, bool WIDE>
+cudaError_t sums(const SumArgs& s0, cudaStream_t stream) {
     SumArgs s = s0;
-    s.blocks = static_cast<int>(ceil_div(s.a.cols, kBlockCols<N>));
-    const int64_t items = sum_tiles * ceil_div(s.blocks, kWarps);
-    cudaError_t e = launch_dependent(sum_kernel<T, G, N>, dim3(static_cast<unsigned>(std::min<int64_t>(items, 1 << 20))),
-                                     kThreads, 0, 1, stream, s);
+    s.blocks = static_cast<int>(ceil_div(s.a.cols, 32 * kLane<T>));
+    const int64_t ctas = s.fill_ctas + std::min<int64_t>(ceil_div(ceil_div(s.a.tokens, kSumTile) * s.blocks, kWarps), 1 << 20);
+    const cudaError_t e = launch_dependent(sum_kernel<T, G, WIDE>, dim3(static_cast<unsigned>(ctas)), kThreads, 0, 1, stream, s);
     if (e != cudaSuccess || s.a.tokens <= kLong) return e;  // no segment can be long
-    const int64_t most = std::min<int64_t>(s.a.tokens / (kLong + 1) * s.blocks, 1024);
-    return launch_dependent(join_kernel<G, N>, dim3(static_cast<unsigned>(most)), kThreads, 0, 1, stream, s);
+    const int64_t most = std::min<int64_t>(s.a.tokens / (kLong + 1) * ceil_div(s.a.cols, 256), 1024);
+    return launch_dependent(join_kernel<G>, dim3(static_cast<unsigned>(most)), kThreads, 0, 1, stream, s);
 }
 
 template <class T, class G>
-cudaError_t sums_of(const SumArgs& s, int64_t sum_tiles, cudaStream_t stream) {
-    constexpr int N = 16 / sizeof(T);
+cudaError_t sums_of(const SumArgs& s, cudaStream_t stream) {
     const EmbedGradArgs& a = s.a;
     if (wide(a.dy, a.cols * static_cast<int64_t>(sizeof(T))) && wide(a.dtable, a.cols * static_cast<int64_t>(sizeof(G))))
-        return sums<T, G, N>(s, sum_tiles, stream);
-    return sums<T, G, 1>(s, sum_tiles, stream);
+        return sums<T, G, true>(s, stream);
+    return sums<T, G, false>(s, stream);
+}
+
+template <int ITEMS>
+cudaError_t prepare(const EmbedGradArgs& a, int64_t row, int64_t rows, int64_t fill, int bits, uint32_t* keys, uint32_t* places, uint32_t* listed,
+                    cudaStream_t stream) {
+    if (!resident_ctas(reinterpret_cast<const void*>(prepare_kernel<ITEMS>), kSortThreads, sizeof(SortShared))) return cudaErrorInvalidConfiguration;
+    return launch_dependent(prepare_kernel<ITEMS>, dim3(static_cast<unsigned>(1 + fill)), kSortThreads, sizeof(SortShared), 1, stream, a, row, rows,
+                            bits, keys, places, listed);
 }
 
 }  // namespace vocab
@@ -582,37 +689,42 @@ cudaError_t launch_embedding_backward(int dtype, int grad_dtype, const EmbedGrad
     int bits = 0;
     while (a.vocab >> bits) ++bits;
     const int64_t row = static_cast<int64_t>(a.cols) * (grad_dtype == TR_F32 ? 4 : 2);
-    const int smem = sizeof(SortShared);
-    // one CTA an SM, which the sort's shared memory makes of it
-    const int resident = resident_ctas(reinterpret_cast<const void*>(prepare_kernel), kSortThreads, smem);
-    if (resident == 0) return cudaErrorInvalidConfiguration;
-    const int one = p.sort_tiles == 1 ? 1 : 0;
-    const int64_t fill = a.accumulate ? 0 : std::max<int64_t>(1, std::min<int64_t>(resident - one, a.vocab));
-    cudaError_t e = launch_dependent(prepare_kernel, dim3(static_cast<unsigned>(std::max<int64_t>(1, one + fill))), kSortThreads,
-                                     smem, 1, stream, a, row, one, bits, at(p.keys[0]), at(p.places[0]), at(p.listed));
+    // (its shared memory makes that one CTA an SM)
+    const int sms = resident_ctas(reinterpret_cast<const void*>(prepare_kernel<kSortItems>), kSortThreads, sizeof(SortShared));
+    if (sms == 0) return cudaErrorInvalidConfiguration;
     int side = 0;
-    if (!one) {
-        if (!resident_ctas(reinterpret_cast<const void*>(sort_pass_kernel<false>), kSortThreads, smem) ||
-            !resident_ctas(reinterpret_cast<const void*>(sort_pass_kernel<true>), kSortThreads, smem))
-            return cudaErrorInvalidConfiguration;
+    int64_t filled = 0;  // rows whose zeros are written beside the sort
+    cudaError_t e = cudaSuccess;
+    if (p.sort_tiles == 1) {
+        int items = 1;
+        while (items * kSortThreads < a.tokens) items *= 2;
+        if (!a.accumulate) filled = std::min<int64_t>(a.vocab, ceil_div(items * kFillBytes, row));
+        const int64_t fill = filled > 0 ? std::min<int64_t>(sms - 1, filled) : 0;
+        const auto run = items == 1   ? prepare<1>
+                         : items == 2 ? prepare<2>
+                         : items == 4 ? prepare<4>
+                         : items == 8 ? prepare<8>
+                                      : prepare<kSortItems>;
+        e = run(a, row, filled, fill, bits, at(p.keys[0]), at(p.places[0]), at(p.listed), stream);
+    } else {
         const dim3 grid(static_cast<unsigned>(p.sort_tiles));
         for (int shift = 0; shift < bits && e == cudaSuccess; shift += 8) {
             SortPass pass{shift ? at(p.keys[side]) : nullptr, shift ? at(p.places[side]) : nullptr, at(p.keys[side ^ 1]),
-                          at(p.places[side ^ 1]), at(p.counts), p.sort_tiles, shift};
-            e = launch_dependent(sort_pass_kernel<false>, grid, kSortThreads, smem, 1, stream, a, pass);
+                          at(p.places[side ^ 1]), at(p.counts), at(p.listed), p.sort_tiles, shift};
+            e = launch_dependent(sort_pass_kernel<false>, grid, kSortThreads, 0, 1, stream, a, pass);
             if (e == cudaSuccess) e = launch_dependent(sort_scan_kernel, dim3(1), kSortThreads, 0, 1, stream, at(p.counts), p.sort_tiles);
-            if (e == cudaSuccess) e = launch_dependent(sort_pass_kernel<true>, grid, kSortThreads, smem, 1, stream, a, pass);
+            if (e == cudaSuccess) e = launch_dependent(sort_pass_kernel<true>, grid, kSortThreads, 0, 1, stream, a, pass);
             side ^= 1;
         }
     }
     if (e != cudaSuccess) return e;
+    const int64_t left = a.accumulate ? 0 : a.vocab - filled;
     const SumArgs s{a, at(p.keys[side]), at(p.places[side]), at(p.listed), reinterpret_cast<float*>(a.ws + p.partials), 0,
-                    static_cast<int>(round_up(a.cols, 8))};
-    if (dtype == TR_F32) return sums_of<float, float>(s, p.sum_tiles, stream);
+                    static_cast<int>(round_up(a.cols, 8)), static_cast<int>(std::min<int64_t>(2 * sms, left)), filled, row};
+    if (dtype == TR_F32) return sums_of<float, float>(s, stream);
     if (dtype == TR_BF16)
-        return grad_dtype == TR_F32 ? sums_of<__nv_bfloat16, float>(s, p.sum_tiles, stream)
-                                    : sums_of<__nv_bfloat16, __nv_bfloat16>(s, p.sum_tiles, stream);
-    return grad_dtype == TR_F32 ? sums_of<__half, float>(s, p.sum_tiles, stream) : sums_of<__half, __half>(s, p.sum_tiles, stream);
+        return grad_dtype == TR_F32 ? sums_of<__nv_bfloat16, float>(s, stream) : sums_of<__nv_bfloat16, __nv_bfloat16>(s, stream);
+    return grad_dtype == TR_F32 ? sums_of<__half, float>(s, stream) : sums_of<__half, __half>(s, stream);
 }
 
 }  // namespace tr

@@ -15,6 +15,8 @@
 namespace tr {
 
 constexpr int kPairs = 76;  // CTA pairs of the GPU that the plan is made for
+// Backward with more rows than this, a copy of hidden with its columns' values together is made for the weight's gradient.
+constexpr int kTurnRows = 1024;
 
 LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
     size_t at = 0;
@@ -25,35 +27,39 @@ LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
     };
     rows_pad = round_up(rows, kTileRows);
     pitch = round_up(cols, 8);
-    width = grad_width = mma::kMaxWidth;
-    // Forward: the width whose tiles come out even over the pairs of a GPU's CTAs. A narrow tile reads the rows of hidden more often
-    // (the 24), which a single tile of rows does not feel: there a narrower tile only splits the weight's reading more evenly.
-    if (!backward) {
-        int64_t least = INT64_MAX;
-        for (int n = mma::kMaxWidth; n >= 64; n -= 32) {
-            const int64_t cost = ceil_div(rows_pad / kTileRows * ceil_div(vocab, n), kPairs) * (n + (rows > kTileRows ? 24 : 0));
-            if (cost < least) least = cost, width = n;
-        }
-    }
-    splits = 1;
-    parts = 2 * ceil_div(vocab, width);
     pack_weight = cols % 8 != 0;
     // dz of a piece: 2^27 values (256 MB), and at least 4096 columns, so that the sums over the pieces cost little
     const int64_t most = std::max<int64_t>(4096, (int64_t{1} << 27) / rows_pad / 256 * 256);
     const int64_t pieces = ceil_div(vocab, std::min(most, round_up(vocab, 256)));
     piece = round_up(ceil_div(vocab, pieces), 256);
+    // The width whose tiles come out even over the pairs of a GPU's CTAs. A narrow tile reads the rows of hidden more often (the
+    // 24), which a single tile of rows does not feel in the forward pass: there a narrower tile only splits the weight's reading more
+    // evenly. Backward, the tiles fill whole multiples of 256 words.
+    width = grad_width = mma::kMaxWidth;
+    const int64_t row_tiles = rows_pad / kTileRows;
+    int64_t least = INT64_MAX;
+    for (int n = mma::kMaxWidth; n >= 64; n = backward ? n / 2 : n - 32) {
+        const int64_t cost = ceil_div(row_tiles * ceil_div(backward ? piece : vocab, n), kPairs) * (n + (backward || row_tiles > 1 ? 24 : 0));
+        if (cost < least) least = cost, width = n;
+    }
+    // Few tiles of the hidden gradient have their depth, the piece's words, split over the pairs.
+    const int64_t grad_tiles = row_tiles * ceil_div(cols, grad_width);
+    splits = static_cast<int>(std::max<int64_t>(1, std::min(kPairs / grad_tiles, piece / (4 * mma::kDepth))));
+    parts = 2 * ceil_div(vocab, width);
+    turned = backward && rows > kTurnRows;
     head = take(sizeof(LossHead));
     map = take(rows_pad * 4);
     labels = take(rows_pad * 4);
     hidden = take(rows_pad * pitch * 2);
     weight = pack_weight ? take(vocab * pitch * 2) : at;
-    lse = coef = onehot = probs = sums = parts_at = picked = at;
+    lse = coef = onehot = probs = sums = hidden_cols = parts_at = picked = at;
     if (backward) {
         lse = take(rows_pad * 4);
         coef = take(rows_pad * 4);
         onehot = take(rows_pad * 4);
         probs = take(rows_pad * piece * 2);
         sums = take(splits * rows_pad * pitch * 4);
+        if (turned) hidden_cols = take(rows_pad * pitch * 2);
     } else {
         parts_at = take(parts * rows_pad * 8);
         picked = take(rows_pad * 4);
@@ -221,6 +227,39 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(LossArgs a, Ws w, const 
         if (a.labels[r] == a.ignore) zero_bytes(reinterpret_cast<char*>(zeros + r * a.cols), reinterpret_cast<char*>(zeros + (r + 1) * a.cols));
 }
 
+// The packed rows turned: dst[c][r] = src[r][c], in squares of 64, up to a whole block of the products' depth of rows.
+template <class T>
+__global__ void __launch_bounds__(kThreads) turn_kernel(Ws w, const T* src, int64_t pitch, int cols, T* dst) {
+    constexpr int kSide = 64, kStride = kSide + 2;
+    __shared__ T square[kSide * kStride];
+    pdl_enter();
+    const int64_t blocks = (w.head->count + kSide - 1) / kSide;
+    const int across = (cols + kSide - 1) / kSide;
+    for (int64_t i = blockIdx.x; i < blocks * across; i += gridDim.x) {
+        const int64_t r0 = i / across * kSide;
+        const int c0 = static_cast<int>(i % across) * kSide;
+        __syncthreads();
+        for (int k = threadIdx.x; k < kSide * kSide / 8; k += kThreads) {
+            const int r = k / 8, c = k % 8 * 8;
+            uint4 q = make_uint4(0, 0, 0, 0);
+            if (c0 + c < pitch) q = __ldg(reinterpret_cast<const uint4*>(src + (r0 + r) * pitch + c0 + c));
+            uint32_t* to = reinterpret_cast<uint32_t*>(square + r * kStride + c);
+            to[0] = q.x, to[1] = q.y, to[2] = q.z, to[3] = q.w;
+        }
+        __syncthreads();
+        for (int k = threadIdx.x; k < kSide * kSide / 8; k += kThreads) {
+            const int c = k / 8, r = k % 8 * 8;
+            if (c0 + c >= cols) continue;
+            T v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = square[(r + j) * kStride + c];
+            uint4 q;
+            memcpy(&q, v, 16);
+            *reinterpret_cast<uint4*>(dst + (c0 + c) * w.rows_pad + r0 + r) = q;
+        }
+    }
+}
+
 // ---- products -------------------------------------------------------------------------
 
 template <class T>
@@ -232,6 +271,7 @@ constexpr uint32_t kTypeBits<__nv_bfloat16> = 1;
 struct Product {
     Ws w;
     mma::Limits lim;
+    mma::Boxes boxes;
     int cols, splits, width;
     int64_t first, n;
     float scale;      // log2(e) logit_scale
@@ -291,24 +331,26 @@ __device__ __forceinline__ void spoil(float (&v)[32]) {
 
 // Forward: (maximum, sum of 2^(z - maximum)) of each half of a tile's columns, and the label's z. The logits are summed in parts of
 // kPart blocks of the depth, which are added in registers (see mma::run): a thread has 128 columns of a row.
-constexpr int kPart = 8;
+constexpr int kPart = 16;
 template <class T>
 __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     stats_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap weight, const __grid_constant__ Product p) {
     int64_t count = 0;
     float z[128];
-    const mma::Operands o{&hidden, &weight, false, false};
+    const mma::Operands<false, false> o{&hidden, &weight};
     mma::run<kPart>(
-        o, o, kTypeBits<T>, p.lim,
+        o, o, p.boxes, kTypeBits<T>, p.lim,
         [&] {
             count = p.w.map ? p.w.head->count : p.rows;
             return mma::Work(p.width, mma::Tiles{tiles_of(count, kTileRows), tiles_of(p.n, p.width), 1, tiles_of(p.cols, mma::kDepth)});
         },
-        [&](const mma::Unit& u, int row, int half, int first, int last, uint32_t at, bool ok, float*, bool begun, bool whole) {
+        [&](const mma::Unit& u, int row, int half, int first, int last, uint32_t at, bool ok, float*, bool begun, bool whole, auto&& release) {
+            if (row - static_cast<int>(threadIdx.x & 31) >= count) return release();  // none of the warp's rows is one
             const int limit = static_cast<int>(min(static_cast<int64_t>(last), p.n - u.n)) - first;  // columns of the vocabulary
 #pragma unroll
             for (int c = 0; c < 128; c += 8)
                 if (c < limit) mma::add_columns(at + first + c, begun, z + c);
+            release();
             if (!whole) return;
             int label = -1;
             if (row < count) {
@@ -358,15 +400,17 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     probs_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap weight, const __grid_constant__ Product p) {
     int64_t count = 0;
     float times = 0.0f;
-    const mma::Operands o{&hidden, &weight, false, false};
+    const mma::Operands<false, false> o{&hidden, &weight};
     mma::run<0>(
-        o, o, kTypeBits<T>, p.lim,
+        o, o, p.boxes, kTypeBits<T>, p.lim,
         [&] {
             count = p.w.head->count;
             times = p.w.head->scale;
             return mma::Work(p.width, mma::Tiles{tiles_of(count, kTileRows), tiles_of(p.n, p.width), 1, tiles_of(p.cols, mma::kDepth)});
         },
-        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, float* turn, bool, bool) {
+        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, float* turn, bool, bool, auto&& release) {
+            // rows that are not there are read as the depth of the weight's gradient up to the end of a block
+            if (row - static_cast<int>(threadIdx.x & 31) >= (count + mma::kDepth - 1) / mma::kDepth * mma::kDepth) return release();
             const bool in = row < count;
             const int limit = static_cast<int>(min(static_cast<int64_t>(last), p.n - u.n));
             const float lse = in ? p.w.lse[row] : 0.0f, coef = in ? p.w.coef[row] * times : 0.0f;
@@ -392,6 +436,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
                 }
                 store_columns<T>(to, c, last, z, true, turn);
             }
+            release();
         });
 }
 
@@ -446,14 +491,15 @@ __device__ __forceinline__ void weight_part(const Product& p, const mma::Unit& u
         store_columns<T>(to, c, cols, z, p.dweight_wide, turn);
     }
 }
-template <class T>
+// (TURNED: hidden's columns' values lie together.)
+template <class T, bool TURNED>
 __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     grads_kernel(const __grid_constant__ CUtensorMap probs_rows, const __grid_constant__ CUtensorMap weight, const __grid_constant__ CUtensorMap probs_cols,
                  const __grid_constant__ CUtensorMap hidden, const __grid_constant__ Product p) {
     int64_t count = 0;
     float times = 0.0f;
     mma::run<0>(
-        mma::Operands{&probs_rows, &weight, false, true}, mma::Operands{&probs_cols, &hidden, true, true}, kTypeBits<T>, p.lim,
+        mma::Operands<false, true>{&probs_rows, &weight}, mma::Operands<true, !TURNED>{&probs_cols, &hidden}, p.boxes, kTypeBits<T>, p.lim,
         [&] {
             count = p.w.head->count;
             times = p.w.head->unscale;
@@ -463,9 +509,14 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
             if (p.dweight) dweight = mma::Tiles{tiles_of(p.n, kTileRows), across, 1, tiles_of(count, mma::kDepth)};
             return mma::Work(p.width, dhidden, dweight);
         },
-        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, float* turn, bool, bool) {
-            if (u.kind == 0) hidden_part<T>(p, u, count, times, row, first, last, at, ok, turn);
-            else weight_part<T>(p, u, times, row, first, last, at, ok, turn);
+        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, float* turn, bool, bool, auto&& release) {
+            const int row0 = row - static_cast<int>(threadIdx.x & 31);
+            if (u.kind == 1) {
+                if (row0 < p.n) weight_part<T>(p, u, times, row, first, last, at, ok, turn);
+            } else if (row0 < count) {
+                hidden_part<T>(p, u, count, times, row, first, last, at, ok, turn);
+            }
+            release();
         });
 }
 
@@ -599,13 +650,15 @@ cudaError_t forward(const LossArgs& a, cudaStream_t stream) {
     if (direct) w.map = nullptr;
     const T *from, *table;
     cudaError_t e = pack<T>(a, p, w, 0, &from, &table, stream);
+    const mma::Boxes boxes = mma::boxes_for(a.rows);
     CUtensorMap hidden, weight;
-    if (e == cudaSuccess) e = map_of(&hidden, from, direct ? a.rows : p.rows_pad, a.cols, p.pitch, mma::kRows);
+    if (e == cudaSuccess) e = map_of(&hidden, from, direct ? a.rows : p.rows_pad, a.cols, p.pitch, boxes.rows);
     if (e == cudaSuccess) e = map_of(&weight, table, a.vocab, a.cols, p.pitch, p.width / 2);
     if (e != cudaSuccess) return e;
     Product d{};
     d.w = w;
     d.lim = mma::Limits{device_error_word(), debug_flags_now()};
+    d.boxes = boxes;
     d.cols = a.cols;
     d.width = p.width;
     d.n = a.vocab;
@@ -626,10 +679,18 @@ cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
     const T *hidden, *weight;
     cudaError_t e = pack<T>(a, p, w, 1, &hidden, &weight, stream);
     T* probs = reinterpret_cast<T*>(a.ws + p.probs);
+    const mma::Boxes boxes = mma::boxes_for(a.rows);
     CUtensorMap hidden_rows, hidden_cols, probs_rows, probs_cols;
-    if (e == cudaSuccess) e = map_of(&hidden_rows, hidden, p.rows_pad, a.cols, p.pitch, mma::kRows);
-    if (e == cudaSuccess) e = map_of(&hidden_cols, hidden, p.rows_pad, a.cols, p.pitch, mma::kDepth);
-    if (e == cudaSuccess) e = map_of(&probs_rows, probs, p.rows_pad, p.piece, p.piece, mma::kRows);
+    if (e == cudaSuccess && p.turned && a.dweight) {
+        const int64_t squares = ceil_div(a.rows, 64) * ceil_div(a.cols, 64);
+        e = launch_dependent(turn_kernel<T>, dim3(static_cast<unsigned>(std::min<int64_t>(squares, 1 << 14))), kThreads, 0, 1, stream, w, hidden, p.pitch,
+                             a.cols, reinterpret_cast<T*>(a.ws + p.hidden_cols));
+    }
+    if (e == cudaSuccess) e = map_of(&hidden_rows, hidden, p.rows_pad, a.cols, p.pitch, boxes.rows);
+    if (e == cudaSuccess)
+        e = p.turned ? map_of(&hidden_cols, reinterpret_cast<const T*>(a.ws + p.hidden_cols), a.cols, p.rows_pad, p.rows_pad, p.grad_width / 2)
+                     : map_of(&hidden_cols, hidden, p.rows_pad, a.cols, p.pitch, mma::kDepth);
+    if (e == cudaSuccess) e = map_of(&probs_rows, probs, p.rows_pad, p.piece, p.piece, boxes.rows);
     if (e == cudaSuccess) e = map_of(&probs_cols, probs, p.rows_pad, p.piece, p.piece, mma::kDepth);
     const int64_t row_tiles = p.rows_pad / kTileRows;
     for (int64_t first = 0; first < a.vocab && e == cudaSuccess; first += p.piece) {
@@ -641,6 +702,7 @@ cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
         Product d{};
         d.w = w;
         d.lim = mma::Limits{device_error_word(), debug_flags_now()};
+        d.boxes = boxes;
         d.cols = a.cols;
         d.first = first;
         d.n = n;
@@ -662,7 +724,8 @@ cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
         d.wide = align && reinterpret_cast<uintptr_t>(a.dhidden) % 16 == 0;
         d.dweight_wide = align && reinterpret_cast<uintptr_t>(a.dweight) % 16 == 0;
         const int64_t units = (a.dhidden ? row_tiles * across * p.splits : 0) + (a.dweight ? ceil_div(n, kTileRows) * across : 0);
-        e = launch_product(grads_kernel<T>, units, stream, probs_rows, weight_cols, probs_cols, hidden_cols, d);
+        e = p.turned ? launch_product(grads_kernel<T, true>, units, stream, probs_rows, weight_cols, probs_cols, hidden_cols, d)
+                     : launch_product(grads_kernel<T, false>, units, stream, probs_rows, weight_cols, probs_cols, hidden_cols, d);
     }
     if (e != cudaSuccess || !a.dhidden || p.splits == 1) return e;
     const int64_t ctas = std::min<int64_t>(ceil_div(a.rows * a.cols, kThreads), 1 << 16);

@@ -15,6 +15,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "tr_device.cuh"
 #include "tr_internal.h"
 
@@ -102,19 +104,34 @@ __device__ __forceinline__ void add_columns(uint32_t addr, bool begun, float* v)
 
 // Shared-memory descriptor of an operand's block. Depth contiguous: groups of 8 rows are 1024 bytes apart. Rows
 // contiguous: groups of 8 depths are 1024 bytes apart, and groups of 64 rows a box of 64 depths.
-__device__ __forceinline__ uint64_t block_of(uint32_t addr, bool rows_contiguous) {
-    const uint64_t leading = rows_contiguous ? kDepth * 128 / 16 : 1, stride = 1024 / 16;
+template <bool ROWS_CONTIGUOUS>
+__device__ __forceinline__ uint64_t block_of(uint32_t addr) {
+    constexpr uint64_t leading = ROWS_CONTIGUOUS ? kDepth * 128 / 16 : 1, stride = 1024 / 16;
     return (addr >> 4) | leading << 16 | stride << 32 | uint64_t{1} << 46 | uint64_t{2} << 61;
 }
 // Encoded distance of the next 16 elements of the depth.
-__device__ __forceinline__ uint64_t next16(bool rows_contiguous) { return (rows_contiguous ? 16 * 128 : 32) / 16; }
+template <bool ROWS_CONTIGUOUS>
+constexpr uint64_t kNext16 = (ROWS_CONTIGUOUS ? 16 * 128 : 32) / 16;
 
-// The operands of one kind of products, and whether their rows (not their depth) are contiguous in memory.
+// The operands of one kind of products, and whether their rows (not their depth) are contiguous in memory. (That has to be known when
+// the kernel is compiled: with layouts chosen as it runs, the threads that copy and issue fall behind the tensor
+// cores, and the gradients of 8192 x 4096 x 50257 take 5.5 ms instead of 4.9.)
+template <bool A_ROWS, bool B_ROWS>
 struct Operands {
+    static constexpr bool kA = A_ROWS, kB = B_ROWS;
     const CUtensorMap* a;
     const CUtensorMap* b;
-    bool a_rows, b_rows;
 };
+// How many rows of A there are at most when all are in one tile (else 256). Rows of a box that lie outside the tensor are
+// filled with zeros slowly (one row of hidden in boxes of 128: 127 us instead of 80), so boxes are as high as the rows need,
+// and the second CTA copies none when the first has them all: what the products read there instead gives rows of C that nobody takes.
+struct Boxes {
+    int rows;     // of a box of A, where its depth is contiguous
+    bool second;  // whether the second CTA has rows
+};
+inline Boxes boxes_for(int64_t rows) {
+    return Boxes{rows >= kRows ? kRows : static_cast<int>((rows + 7) / 8 * 8), rows > kRows};
+}
 
 // What the launch needs apart from the operands.
 struct Limits {
@@ -139,6 +156,8 @@ struct Waits {
 #pragma unroll
         for (uint32_t r = 0; r < 2; ++r) asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(in_cta(a, r)), "r"(1) : "memory");
     }
+    // Between two tries the clock is read, which takes long, and it is as well: looking again and again takes
+    // shared-memory bandwidth from the products (gradients of 8192 x 4096 x 50257 6.9 ms instead of 5.5).
     __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
         if (mbar_try_wait(bar, parity)) return true;
         const unsigned long long t0 = global_ns();
@@ -183,7 +202,9 @@ struct Work {
         pair = static_cast<int>(blockIdx.x) / 2;
         pairs = static_cast<int>(gridDim.x) / 2;
         longer = first.units() % pairs;
-        ahead = longer > 0 && second.blocks > 0 ? (first.blocks / first.splits + second.blocks / 2) / second.blocks : 0;
+        constexpr int kOut = 12;  // blocks whose products take as long as a tile's beginning and end
+        const int one = first.blocks / first.splits + kOut, other = second.blocks + kOut;
+        ahead = longer > 0 && second.units() > 0 ? (one + other / 2) / other : 0;
     }
     // The pair's unit number `step`; false: there is none.
     __device__ __forceinline__ bool unit(int64_t step, Unit* u) const {
@@ -205,10 +226,11 @@ struct Work {
 // The products of a CTA pair: plan() gives the work, once what earlier kernels wrote can be read; o0 and o1 are the operands of the two
 // kinds. The sums of a tile come in one part, or (CHUNK > 0) in a part for every CHUNK blocks of the depth, for the caller to add: the
 // tensor cores round their sums toward zero, an error that grows with the length of a sum. out(unit, row, half, first, last,
-// tensor address, ok, turn, begun, whole) takes the columns [first, last) of one row a lane; ok: the sums are there (false: after
-// a wait that gave up); turn: kTurnFloats of shared memory for the warp; begun: earlier parts have come; whole: the last one.
-template <int CHUNK, class Plan, class Out>
-__device__ __forceinline__ void run(const Operands& o0, const Operands& o1, uint32_t type_bits, const Limits& lim, Plan&& plan, Out&& out) {
+// tensor address, ok, turn, begun, whole, release) takes the columns [first, last) of one row a lane, and calls release() when it has
+// read the tensor memory; ok: the sums are there (false: after a wait that gave up); turn: kTurnFloats of shared memory for the
+// warp; begun: earlier parts have come; whole: the last one.
+template <int CHUNK, class O0, class O1, class Plan, class Out>
+__device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& boxes, uint32_t type_bits, const Limits& lim, Plan&& plan, Out&& out) {
     extern __shared__ __align__(16) char raw[];
     __shared__ Shared s;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
@@ -233,6 +255,15 @@ __device__ __forceinline__ void run(const Operands& o0, const Operands& o1, uint
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
+    // Rows of A that no copy brings are zeros: numbers left there by other kernels would cost their products' power (48 rows of
+    // hidden: 108 us instead of 97).
+    if (boxes.rows < kRows || !boxes.second) {
+        const int from = rank == 0 || boxes.second ? boxes.rows * 8 : 0, words = kRows * 8;  // of 16 bytes
+        for (int i = threadIdx.x; i < kStages * words; i += kThreads)
+            if (i % words >= from)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(base + i / words * kStageBytes + i % words * 16), "r"(0) : "memory");
+        fence_proxy_async_smem();
+    }
     fence_before();
     __syncthreads();
     cluster_barrier();
@@ -244,27 +275,29 @@ __device__ __forceinline__ void run(const Operands& o0, const Operands& o1, uint
     const int width = work.width;
     if (warp == 0) {
         if (lane == 0) {
-            const uint32_t half = width / 2, bytes = (kRows + half) * 128;
+            const uint32_t half = width / 2;
             int stage = 0;
             uint32_t phase = 0, issued = 0;
             bool ok = true;
             Unit u;
-            for (int64_t i = 0; ok && work.unit(i, &u); ++i) {
-                const Operands o = u.kind ? o1 : o0;
+            const auto copy = [&](const auto& o) {
+                using O = std::decay_t<decltype(o)>;
+                const int m = u.m + rank * kRows, n = u.n + rank * half;
+                const uint32_t bytes = 128 * (width + (O::kA ? 2 * kRows : boxes.rows * (boxes.second ? 2 : 1)));  // of both CTAs
                 for (int k = u.begin; k < u.end; ++k) {
                     ok = waits.wait(&s.empty[stage], phase ^ 1);
                     if (!ok) break;
                     const uint32_t bar = in_cta(smem_addr(&s.full[stage]), 0);
                     const uint32_t to_a = base + stage * kStageBytes, to_b = to_a + kRows * 128;
-                    if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * bytes);
-                    const int m = u.m + rank * kRows, n = u.n + rank * half, d = k * kDepth;
-                    if (o.a_rows) {
+                    const int d = k * kDepth;
+                    if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], bytes);
+                    if constexpr (O::kA) {
 #pragma unroll
                         for (int j = 0; j < kRows / 64; ++j) copy_box(to_a + j * kDepth * 128, o.a, m + 64 * j, d, bar);
-                    } else {
+                    } else if (rank == 0 || boxes.second) {
                         copy_box(to_a, o.a, d, m, bar);
                     }
-                    if (o.b_rows) {
+                    if constexpr (O::kB) {
                         for (uint32_t j = 0; j < half / 64; ++j) copy_box(to_b + j * kDepth * 128, o.b, n + 64 * j, d, bar);
                     } else {
                         copy_box(to_b, o.b, d, n, bar);
@@ -272,6 +305,10 @@ __device__ __forceinline__ void run(const Operands& o0, const Operands& o1, uint
                     ++issued;
                     if (++stage == kStages) stage = 0, phase ^= 1;
                 }
+            };
+            for (int64_t i = 0; ok && work.unit(i, &u); ++i) {
+                if (u.kind) copy(o1);
+                else copy(o0);
             }
             // after a wait that gave up: the copies under way, of both CTAs, count on the first one's barriers (the second, which
             // may have begun one more, gives that the time)
@@ -294,35 +331,38 @@ __device__ __forceinline__ void run(const Operands& o0, const Operands& o1, uint
             bool ok = true;
             if ((lim.debug & kDebugForceTimeout) && blockIdx.x == 0) mbar_wait_bounded(&s.never, 0, kTestNs, lim.err);
             Unit u;
-            for (int64_t i = 0; ok && work.unit(i, &u); ++i) {
-                const bool a_rows = u.kind ? o1.a_rows : o0.a_rows, b_rows = u.kind ? o1.b_rows : o0.b_rows;
+            const auto multiply = [&](auto&& o) {
+                using O = std::decay_t<decltype(o)>;
                 // kind::f16: binary32 sums; the operands' type and layouts, width / 8 and 256 / 16
-                const uint32_t what = 1u << 4 | type_bits << 7 | type_bits << 10 | (a_rows ? 1u << 15 : 0) | (b_rows ? 1u << 16 : 0) |
+                const uint32_t what = 1u << 4 | type_bits << 7 | type_bits << 10 | (O::kA ? 1u << 15 : 0) | (O::kB ? 1u << 16 : 0) |
                                       static_cast<uint32_t>(width / 8) << 17 | (2 * kRows / 16) << 24;
-                const uint64_t next_a = next16(a_rows), next_b = next16(b_rows);
                 int k = u.begin;
                 do {
                     const int from = k, to = CHUNK > 0 ? min(k + CHUNK, u.end) : u.end;
                     ok = waits.wait(&s.room[slot], slot_phase ^ 1);
-                    if (!ok) break;
+                    if (!ok) return;
                     fence_after();
                     const uint32_t d = columns + slot * kMaxWidth;
                     for (; k < to; ++k) {
                         if (lim.debug & kDebugExpireCopies) waits.die(), ok = false;
                         else ok = waits.wait(&s.full[stage], phase);
-                        if (!ok) break;
+                        if (!ok) return;
                         fence_after();
                         const uint32_t at = base + stage * kStageBytes;
-                        const uint64_t da = block_of(at, a_rows), db = block_of(at + kRows * 128, b_rows);
+                        const uint64_t da = block_of<O::kA>(at), db = block_of<O::kB>(at + kRows * 128);
 #pragma unroll
-                        for (int j = 0; j < kDepth / 16; ++j) product(d, da + j * next_a, db + j * next_b, what, k > from || j > 0);
+                        for (int j = 0; j < kDepth / 16; ++j)
+                            product(d, da + j * kNext16<O::kA>, db + j * kNext16<O::kB>, what, k > from || j > 0);
                         commit(smem_addr(&s.empty[stage]));
                         if (++stage == kStages) stage = 0, phase ^= 1;
                     }
-                    if (!ok) break;
                     commit(smem_addr(&s.done[slot]));
                     if (++slot == 2) slot = 0, slot_phase ^= 1;
                 } while (k < u.end);
+            };
+            for (int64_t i = 0; ok && work.unit(i, &u); ++i) {
+                if (u.kind) multiply(o1);
+                else multiply(o0);
             }
             if (!ok) {  // the products under way
                 commit(smem_addr(&s.never));
@@ -343,10 +383,11 @@ __device__ __forceinline__ void run(const Operands& o0, const Operands& o1, uint
                 const bool ok = __all_sync(kFull, waits.wait(&s.done[slot], slot_phase) && !waits.dead());
                 fence_after();
                 const uint32_t at = columns + slot * kMaxWidth + (static_cast<uint32_t>(quarter * 32) << 16);
-                out(u, u.m + static_cast<int>(rank) * kRows + quarter * 32 + lane, half, first, last, at, ok, turn, begun, k >= u.end);
-                fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_in(in_cta(smem_addr(&s.room[slot]), 0));
+                out(u, u.m + static_cast<int>(rank) * kRows + quarter * 32 + lane, half, first, last, at, ok, turn, begun, k >= u.end, [&] {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_in(in_cta(smem_addr(&s.room[slot]), 0));
+                });
                 if (++slot == 2) slot = 0, slot_phase ^= 1;
             } while (k < u.end);
         }

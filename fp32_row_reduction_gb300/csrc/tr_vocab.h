@@ -26,6 +26,7 @@ struct EmbedArgs {
 cudaError_t launch_embedding(int dtype, const EmbedArgs& a, cudaStream_t stream);
 
 constexpr int kSortTile = 16384;  // keys that one CTA sorts
+constexpr int kPassTile = 4096;   // keys of a CTA where several sort
 constexpr int kSortBins = 256;
 constexpr int kSumTile = 32;      // sorted tokens of a warp of the sums
 
@@ -36,7 +37,7 @@ struct EmbedGradPlan {
     int64_t sort_tiles, sum_tiles;
     size_t keys[2], places[2], counts, listed, partials, bytes;  // offsets
     EmbedGradPlan(int64_t tokens, int64_t cols) {
-        sort_tiles = ceil_div(tokens, kSortTile);
+        sort_tiles = tokens <= kSortTile ? 1 : ceil_div(tokens, kPassTile);
         sum_tiles = ceil_div(tokens, kSumTile);
         const int copies = sort_tiles > 1 ? 2 : 1;
         size_t at = 0;
@@ -79,7 +80,8 @@ struct LossPlan {
     int width;         // words of a tile of logits
     int grad_width;    // columns of a tile of the gradients
     int splits;        // of the depth of the hidden gradient
-    size_t head, map, labels, lse, coef, onehot, hidden, weight, parts_at, picked, probs, sums, bytes;
+    size_t head, map, labels, lse, coef, onehot, hidden, weight, hidden_cols, parts_at, picked, probs, sums, bytes;
+    bool turned;       // backward: hidden's columns' values are brought together
     bool pack_weight;  // rows of the weight that do not start on 16 bytes are copied to ones that do
     LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward);
 };
