@@ -48,28 +48,38 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_addr(bar)),
+        "r"(bytes)
+        : "memory");
+}
 __device__ __forceinline__ void arrive_in(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // A box of a tensor map to this CTA's shared memory, its bytes counted on a barrier of the pair.
 __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
         "l"(map), "r"(bar), "r"(x), "r"(y)
         : "memory");
 }
 __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t what, uint32_t add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(what), "r"(add)
         : "memory");
 }
 // The products issued so far arrive at this barrier of both CTAs when they are done.
 __device__ __forceinline__ void commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-                 "h"(static_cast<uint16_t>(3))
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -234,7 +244,8 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
     extern __shared__ __align__(16) char raw[];
     __shared__ Shared s;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (the same in all lanes, which the compiler knows of a shuffle)
+    const int warp = __shfl_sync(kFull, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
     const Waits waits{s, lim};
     if (threadIdx.x == 0) {
@@ -274,7 +285,7 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
     const Work work = plan();
     const int width = work.width;
     if (warp == 0) {
-        if (lane == 0) {
+        {
             const uint32_t half = width / 2;
             int stage = 0;
             uint32_t phase = 0, issued = 0;
@@ -290,7 +301,7 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
                     const uint32_t bar = in_cta(smem_addr(&s.full[stage]), 0);
                     const uint32_t to_a = base + stage * kStageBytes, to_b = to_a + kRows * 128;
                     const int d = k * kDepth;
-                    if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], bytes);
+                    if (rank == 0) expect_bytes(&s.full[stage], bytes);
                     if constexpr (O::kA) {
 #pragma unroll
                         for (int j = 0; j < kRows / 64; ++j) copy_box(to_a + j * kDepth * 128, o.a, m + 64 * j, d, bar);
@@ -325,7 +336,7 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
             }
         }
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             int stage = 0;
             uint32_t phase = 0, slot = 0, slot_phase = 0;
             bool ok = true;
