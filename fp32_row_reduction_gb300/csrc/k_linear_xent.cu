@@ -15,8 +15,6 @@
 namespace tr {
 
 constexpr int kPairs = 76;  // CTA pairs of the GPU that the plan is made for
-// Backward with more rows than this, a copy of hidden with its columns' values together is made for the weight's gradient.
-constexpr int kTurnRows = 1024;
 
 LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
     size_t at = 0;
@@ -46,20 +44,18 @@ LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
     const int64_t grad_tiles = row_tiles * ceil_div(cols, grad_width);
     splits = static_cast<int>(std::max<int64_t>(1, std::min(kPairs / grad_tiles, piece / (4 * mma::kDepth))));
     parts = 2 * ceil_div(vocab, width);
-    turned = backward && rows > kTurnRows;
     head = take(sizeof(LossHead));
     map = take(rows_pad * 4);
     labels = take(rows_pad * 4);
     hidden = take(rows_pad * pitch * 2);
     weight = pack_weight ? take(vocab * pitch * 2) : at;
-    lse = coef = onehot = probs = sums = hidden_cols = parts_at = picked = at;
+    lse = coef = onehot = probs = sums = parts_at = picked = at;
     if (backward) {
         lse = take(rows_pad * 4);
         coef = take(rows_pad * 4);
         onehot = take(rows_pad * 4);
         probs = take(rows_pad * piece * 2);
         sums = take(splits * rows_pad * pitch * 4);
-        if (turned) hidden_cols = take(rows_pad * pitch * 2);
     } else {
         parts_at = take(parts * rows_pad * 8);
         picked = take(rows_pad * 4);
@@ -225,39 +221,6 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(LossArgs a, Ws w, const 
     if (!zeros) return;
     for (int64_t r = first; r < a.rows; r += step)
         if (a.labels[r] == a.ignore) zero_bytes(reinterpret_cast<char*>(zeros + r * a.cols), reinterpret_cast<char*>(zeros + (r + 1) * a.cols));
-}
-
-// The packed rows turned: dst[c][r] = src[r][c], in squares of 64, up to a whole block of the products' depth of rows.
-template <class T>
-__global__ void __launch_bounds__(kThreads) turn_kernel(Ws w, const T* src, int64_t pitch, int cols, T* dst) {
-    constexpr int kSide = 64, kStride = kSide + 2;
-    __shared__ T square[kSide * kStride];
-    pdl_enter();
-    const int64_t blocks = (w.head->count + kSide - 1) / kSide;
-    const int across = (cols + kSide - 1) / kSide;
-    for (int64_t i = blockIdx.x; i < blocks * across; i += gridDim.x) {
-        const int64_t r0 = i / across * kSide;
-        const int c0 = static_cast<int>(i % across) * kSide;
-        __syncthreads();
-        for (int k = threadIdx.x; k < kSide * kSide / 8; k += kThreads) {
-            const int r = k / 8, c = k % 8 * 8;
-            uint4 q = make_uint4(0, 0, 0, 0);
-            if (c0 + c < pitch) q = __ldg(reinterpret_cast<const uint4*>(src + (r0 + r) * pitch + c0 + c));
-            uint32_t* to = reinterpret_cast<uint32_t*>(square + r * kStride + c);
-            to[0] = q.x, to[1] = q.y, to[2] = q.z, to[3] = q.w;
-        }
-        __syncthreads();
-        for (int k = threadIdx.x; k < kSide * kSide / 8; k += kThreads) {
-            const int c = k / 8, r = k % 8 * 8;
-            if (c0 + c >= cols) continue;
-            T v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = square[(r + j) * kStride + c];
-            uint4 q;
-            memcpy(&q, v, 16);
-            *reinterpret_cast<uint4*>(dst + (c0 + c) * w.rows_pad + r0 + r) = q;
-        }
-    }
 }
 
 // ---- products -------------------------------------------------------------------------
@@ -491,15 +454,14 @@ __device__ __forceinline__ void weight_part(const Product& p, const mma::Unit& u
         store_columns<T>(to, c, cols, z, p.dweight_wide, turn);
     }
 }
-// (TURNED: hidden's columns' values lie together.)
-template <class T, bool TURNED>
+template <class T>
 __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     grads_kernel(const __grid_constant__ CUtensorMap probs_rows, const __grid_constant__ CUtensorMap weight, const __grid_constant__ CUtensorMap probs_cols,
                  const __grid_constant__ CUtensorMap hidden, const __grid_constant__ Product p) {
     int64_t count = 0;
     float times = 0.0f;
     mma::run<0>(
-        mma::Operands<false, true>{&probs_rows, &weight}, mma::Operands<true, !TURNED>{&probs_cols, &hidden}, p.boxes, kTypeBits<T>, p.lim,
+        mma::Operands<false, true>{&probs_rows, &weight}, mma::Operands<true, true>{&probs_cols, &hidden}, p.boxes, kTypeBits<T>, p.lim,
         [&] {
             count = p.w.head->count;
             times = p.w.head->unscale;
@@ -681,15 +643,8 @@ cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
     T* probs = reinterpret_cast<T*>(a.ws + p.probs);
     const mma::Boxes boxes = mma::boxes_for(a.rows);
     CUtensorMap hidden_rows, hidden_cols, probs_rows, probs_cols;
-    if (e == cudaSuccess && p.turned && a.dweight) {
-        const int64_t squares = ceil_div(a.rows, 64) * ceil_div(a.cols, 64);
-        e = launch_dependent(turn_kernel<T>, dim3(static_cast<unsigned>(std::min<int64_t>(squares, 1 << 14))), kThreads, 0, 1, stream, w, hidden, p.pitch,
-                             a.cols, reinterpret_cast<T*>(a.ws + p.hidden_cols));
-    }
     if (e == cudaSuccess) e = map_of(&hidden_rows, hidden, p.rows_pad, a.cols, p.pitch, boxes.rows);
-    if (e == cudaSuccess)
-        e = p.turned ? map_of(&hidden_cols, reinterpret_cast<const T*>(a.ws + p.hidden_cols), a.cols, p.rows_pad, p.rows_pad, p.grad_width / 2)
-                     : map_of(&hidden_cols, hidden, p.rows_pad, a.cols, p.pitch, mma::kDepth);
+    if (e == cudaSuccess) e = map_of(&hidden_cols, hidden, p.rows_pad, a.cols, p.pitch, mma::kDepth);
     if (e == cudaSuccess) e = map_of(&probs_rows, probs, p.rows_pad, p.piece, p.piece, boxes.rows);
     if (e == cudaSuccess) e = map_of(&probs_cols, probs, p.rows_pad, p.piece, p.piece, mma::kDepth);
     const int64_t row_tiles = p.rows_pad / kTileRows;
@@ -724,8 +679,7 @@ cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
         d.wide = align && reinterpret_cast<uintptr_t>(a.dhidden) % 16 == 0;
         d.dweight_wide = align && reinterpret_cast<uintptr_t>(a.dweight) % 16 == 0;
         const int64_t units = (a.dhidden ? row_tiles * across * p.splits : 0) + (a.dweight ? ceil_div(n, kTileRows) * across : 0);
-        e = p.turned ? launch_product(grads_kernel<T, true>, units, stream, probs_rows, weight_cols, probs_cols, hidden_cols, d)
-                     : launch_product(grads_kernel<T, false>, units, stream, probs_rows, weight_cols, probs_cols, hidden_cols, d);
+        e = launch_product(grads_kernel<T>, units, stream, probs_rows, weight_cols, probs_cols, hidden_cols, d);
     }
     if (e != cudaSuccess || !a.dhidden || p.splits == 1) return e;
     const int64_t ctas = std::min<int64_t>(ceil_div(a.rows * a.cols, kThreads), 1 << 16);

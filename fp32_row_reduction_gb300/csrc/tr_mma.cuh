@@ -6,7 +6,10 @@
 // room: one is written out while the next is summed. An operand lies in memory either with its depth contiguous (rows of 64
 // elements are 128 bytes of a 128-byte swizzle) or with its rows contiguous (64 rows of each depth are 128 bytes).
 //
-// Warp 0 copies, warp 1 issues the products, the others (kOutWarps) write out. Every wait is bounded: one that gives up
+// Warp 0 copies, warp 1 issues the products, the others (kOutWarps) write out. The first two run as whole warps, with one lane elected
+// at each instruction: the compiler then keeps descriptors and counters in uniform registers. As a single thread, with those
+// moved there for each instruction, the second fell behind the tensor cores (574 cycles for a block of 256 x 256 x 64 instead of
+// 513, of which the products take 512). Every wait is bounded: one that gives up
 // is recorded in the device error word, ends the waits of both CTAs, and makes what is written from then on NaN; the copies and products
 // under way are waited for (again bounded) before the pair frees its tensor memory and ends.
 #pragma once
@@ -166,13 +169,13 @@ struct Waits {
 #pragma unroll
         for (uint32_t r = 0; r < 2; ++r) asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(in_cta(a, r)), "r"(1) : "memory");
     }
-    // Between two tries the clock is read, which takes long, and it is as well: looking again and again takes
-    // shared-memory bandwidth from the products (gradients of 8192 x 4096 x 50257 6.9 ms instead of 5.5).
+    // All lanes of a warp wait, and have the same answer. Between two tries the clock is read, which takes long, and it is as well:
+    // looking again and again takes shared-memory bandwidth from the products.
     __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
         const unsigned long long t0 = global_ns();
-        while (!dead()) {
-            if (mbar_try_wait(bar, parity)) return true;
+        while (!__any_sync(kFull, dead())) {
+            if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
             if (static_cast<long long>(global_ns() - t0) > kLimitNs) die();
         }
         return false;
@@ -186,13 +189,13 @@ struct Unit {
     int begin, end;  // blocks of the depth (equal: the tile is zero)
     int split;
 };
-// The tiles of one kind of products: in groups of eight rows of tiles (what the pairs read at one time is then as many rows
-// of A as of B), each tile's depth in `splits` parts.
+// The tiles of one kind of products: in groups of sixteen rows of tiles (what the pairs read at one time is then a little of A
+// and of B; groups of eight: 8192 x 4096 x 50257 forward 1760 us instead of 1716), each tile's depth in `splits` parts.
 struct Tiles {
     int m = 0, n = 0, splits = 1, blocks = 0;
     __device__ __forceinline__ int64_t units() const { return static_cast<int64_t>(m) * n * splits; }
     __device__ __forceinline__ Unit unit(int kind, int64_t i, int width) const {
-        constexpr int kGroup = 8;
+        constexpr int kGroup = 16;
         const int64_t t = i / splits;
         const int split = static_cast<int>(i - t * splits);
         const int64_t in_group = static_cast<int64_t>(kGroup) * n, g = t / in_group;
@@ -391,7 +394,7 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
             do {
                 const bool begun = k > u.begin;
                 k = CHUNK > 0 ? min(k + CHUNK, u.end) : u.end;
-                const bool ok = __all_sync(kFull, waits.wait(&s.done[slot], slot_phase) && !waits.dead());
+                const bool ok = waits.wait(&s.done[slot], slot_phase) && !__any_sync(kFull, waits.dead());
                 fence_after();
                 const uint32_t at = columns + slot * kMaxWidth + (static_cast<uint32_t>(quarter * 32) << 16);
                 out(u, u.m + static_cast<int>(rank) * kRows + quarter * 32 + lane, half, first, last, at, ok, turn, begun, k >= u.end, [&] {

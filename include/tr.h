@@ -434,7 +434,7 @@ tr_status tr_global_norm_workspace_bytes(int64_t count, size_t* bytes);
  *   dz = logit_scale ((dloss + dlse) softmax - dloss onehot(label)),
  *   dhidden = dz weight,  dweight = dz^T hidden,
  * each of `dtype` and either NULL when not wanted. The logits are formed again, a piece of the vocabulary at a time. dz is
- * rounded to `dtype` for the products, after a division by a power of two near the largest coefficient (so that float16 keeps
+ * rounded to `dtype` for the products, relative to the largest coefficient (so that float16 keeps
  * small probabilities); sums are binary32, each output is rounded once. Rows without a loss have a gradient of 0 and
  * add nothing to dweight, whatever they hold.
  *
@@ -444,7 +444,8 @@ tr_status tr_global_norm_workspace_bytes(int64_t count, size_t* bytes);
  * loss, 2^31 - 1024 for the embedding. scale and logit_scale must be finite. order must be
  * TR_ORDER_UNORDERED_TREE (others: TR_ERR_UNSUPPORTED). Workspaces are caller-owned, 16-byte aligned, of the size that the
  * _workspace_bytes calls (host only) give; calls that may run at the same time need one each. No call allocates or
- * waits on the host, all may be captured into a graph, and results repeat bit for bit on one device. */
+ * waits on the host, all may be captured into a graph, and results repeat bit for bit on one device. The products' device-side waits
+ * are bounded (two seconds); one that gave up is reported by tr_last_device_error, and what the call computes from then on is NaN. */
 tr_status tr_embedding(tr_dtype dtype, const void* table, const int64_t* ids, void* out, int64_t tokens, int64_t vocab,
                        int64_t cols, float scale, cudaStream_t stream);
 tr_status tr_embedding_backward(tr_dtype dtype, tr_dtype grad_dtype, const void* dy, const int64_t* ids, void* dtable,
@@ -571,10 +572,11 @@ const char* tr_last_error_message(void);
 /* Testing hook: makes bounded device-side waits give up, so that their
  * give-up paths run and tr_last_device_error() reports TR_ERR_DEVICE_TIMEOUT,
  * without a GPU fault or hang. `mode` is a bit mask (0 turns everything off):
- *   1  every launch of a plan with bounded waits (staged plans, block norms' split rows) also waits on
- *      a barrier that nothing completes, with a 1 ms limit; results stay correct;
+ *   1  every launch of a plan with bounded waits (staged plans, block norms' split rows, products of the linear
+ *      cross entropy) also waits on a barrier that nothing completes, with a 1 ms limit; results stay correct;
  *   2  waits for bulk asynchronous copies give up at once: in the staged
- *      plans every ring slot (that row's outputs are undefined); a CTA still
+ *      plans every ring slot (that row's outputs are undefined), in the products of the linear cross entropy every
+ *      tile (what is computed from it is NaN); a CTA still
  *      waits for its copies, with the normal limit, before it exits. The split
  *      and segments plans stream their segments through registers and have no
  *      such wait;

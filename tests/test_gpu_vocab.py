@@ -507,3 +507,41 @@ def test_a_step_of_a_tied_model(dtype):
     total = float((before ** 2).sum() + (back.dweight.double() / (1e-3 / (float(norm) + 1e-6))).pow(2).sum()) ** 0.5
     assert abs(float(norm) - total) <= 1e-5 * total
     close(dtable, (before * (1e-3 / (float(norm) + 1e-6)), 16 * vocab.U * before.abs()))
+
+
+# ---- waits that give up ------------------------------------------------------------------------
+
+@pytest.fixture
+def hook():
+    assert tr.tr_last_device_error() == tr.TR_OK
+    yield tr.tr_debug_force_wait_timeout
+    tr.tr_debug_force_wait_timeout(0)
+    tr.tr_last_device_error()
+
+
+@pytest.mark.parametrize("rows,cols,v", [(40, 72, 700), (900, 520, 5003), (300, 33, 999)])
+def test_waits_that_give_up(hook, rows, cols, v):
+    """An extra wait that nothing ends is reported and changes nothing. Waits for tiles that give up are reported, and what
+    the call computes is no number; the next call is right again."""
+    hidden, weight, labels, dloss, dlse = loss_inputs(rows, cols, v, "bf16", ignored=0.2)
+    want = check_loss(hidden, weight, labels, dloss, dlse)
+    counted = labels != IGNORE
+
+    def both():
+        losses, lse = tr.linear_cross_entropy(hidden, weight, labels)
+        dh, dw = tr.linear_cross_entropy_backward(hidden, weight, labels, want[1], dloss, dlse)
+        return losses, lse, dh, dw
+
+    hook(1)
+    got = both()
+    assert tr.tr_last_device_error() == tr.TR_ERR_DEVICE_TIMEOUT
+    assert all(same(a, b) for a, b in zip(got, want))
+    hook(2)
+    losses, lse, dh, dw = both()
+    assert tr.tr_last_device_error() == tr.TR_ERR_DEVICE_TIMEOUT
+    assert bool(torch.isnan(losses[counted]).all()) and bool(torch.isnan(lse[counted]).all())
+    assert bool(torch.isnan(dh[counted]).all()) and bool(torch.isnan(dw).all())
+    assert not losses[~counted].any() and not dh[~counted].any()
+    hook(0)
+    assert all(same(a, b) for a, b in zip(both(), want))
+    assert tr.tr_last_device_error() == tr.TR_OK
