@@ -86,36 +86,36 @@ struct Ws {
 
 // ---- the rows that have a loss -------------------------------------------------------
 
-// One CTA lists them in order, with their labels (-1: outside the vocabulary) and, backward, their coefficients:
-// of the probability (dloss + dlse) and of the label (dloss). The outputs of rows without a loss are zeros.
-__global__ void __launch_bounds__(kScanThreads) rows_kernel(LossArgs a, Ws w, int backward) {
-    constexpr int kItems = 8;  // rows of a thread at a time, 32 apart: 8192 rows in one round
+// A CTA lists them in order (map[i]: the i-th one's row) and, with `write`, in the workspace, with their labels (-1: outside the vocabulary)
+// and, backward, their coefficients: of the probability (dloss + dlse) and of the label (dloss); the outputs of rows without a loss
+// are zeros then. ITEMS: rows of a thread at a time, 32 apart. All threads get the count.
+template <int ITEMS>
+__device__ __forceinline__ int64_t list_rows(const LossArgs& a, const Ws& w, int backward, bool write, int* map) {
     __shared__ int warp_count[32];
     __shared__ float warp_most[2][32];
-    pdl_enter();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned before = (1u << lane) - 1u;
     int64_t count = 0;
     float most = 0.0f, most_d = 0.0f;
-    for (int64_t r0 = 0; r0 < a.rows; r0 += kItems * kScanThreads) {
-        const int64_t r1 = r0 + warp * (32 * kItems) + lane;
-        int64_t label[kItems];
-        float lse[kItems], d[kItems], e[kItems];
+    for (int64_t r0 = 0; r0 < a.rows; r0 += ITEMS * kScanThreads) {
+        const int64_t r1 = r0 + warp * (32 * ITEMS) + lane;
+        int64_t label[ITEMS];
+        float lse[ITEMS], d[ITEMS], e[ITEMS];
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
+        for (int i = 0; i < ITEMS; ++i) {
             const int64_t r = r1 + 32 * i;
             const bool in = r < a.rows;
             label[i] = in ? a.labels[r] : a.ignore;
-            if (backward) {
+            if (write && backward) {
                 lse[i] = in ? a.lse_in[r] : 0.0f;
                 d[i] = in && a.dloss ? a.dloss[r] : 1.0f;
                 e[i] = in && a.dlse ? a.dlse[r] : 0.0f;
             }
         }
-        unsigned votes[kItems];
+        unsigned votes[ITEMS];
         int total = 0;
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
+        for (int i = 0; i < ITEMS; ++i) {
             votes[i] = __ballot_sync(kFull, label[i] != a.ignore);
             total += __popc(votes[i]);
         }
@@ -132,10 +132,12 @@ __global__ void __launch_bounds__(kScanThreads) rows_kernel(LossArgs a, Ws w, in
         int64_t at = count + __shfl_sync(kFull, inc - mine, warp);
         count += __shfl_sync(kFull, inc, 31);
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
+        for (int i = 0; i < ITEMS; ++i) {
             const int64_t r = r1 + 32 * i, to = at + __popc(votes[i] & before);
             at += __popc(votes[i]);
             if (label[i] != a.ignore) {
+                if (map) map[to] = static_cast<int>(r);
+                if (!write) continue;
                 w.map[to] = static_cast<int>(r);
                 w.labels[to] = label[i] >= 0 && label[i] < a.vocab ? static_cast<int>(label[i]) : -1;
                 if (backward) {
@@ -145,17 +147,19 @@ __global__ void __launch_bounds__(kScanThreads) rows_kernel(LossArgs a, Ws w, in
                     most = fmaxf(most, fabsf(d[i]) + fabsf(e[i]));
                     most_d = fmaxf(most_d, fabsf(d[i]));
                 }
-            } else if (!backward && r < a.rows) {
+            } else if (write && !backward && r < a.rows) {
                 a.losses[r] = 0.0f;
                 if (a.lse) a.lse[r] = 0.0f;
             }
         }
     }
-    most = warp_allreduce<MaxOp, 32>(most);
-    most_d = warp_allreduce<MaxOp, 32>(most_d);
-    if (lane == 0) warp_most[0][warp] = most, warp_most[1][warp] = most_d;
+    if (write) {
+        most = warp_allreduce<MaxOp, 32>(most);
+        most_d = warp_allreduce<MaxOp, 32>(most_d);
+        if (lane == 0) warp_most[0][warp] = most, warp_most[1][warp] = most_d;
+    }
     __syncthreads();
-    if (warp == 0) {
+    if (write && warp == 0) {
         most = warp_allreduce<MaxOp, 32>(warp_most[0][lane]);
         most_d = warp_allreduce<MaxOp, 32>(warp_most[1][lane]);
         if (lane == 0) {
@@ -172,29 +176,31 @@ __global__ void __launch_bounds__(kScanThreads) rows_kernel(LossArgs a, Ws w, in
             w.head->unscale = a.logit_scale * (by / times);
         }
     }
+    return count;
+}
+__global__ void __launch_bounds__(kScanThreads) rows_kernel(LossArgs a, Ws w, int backward) {
+    pdl_enter();
+    list_rows<8>(a, w, backward, true, nullptr);
 }
 
-// Rows copied to rows of `pitch` elements that start on 16 bytes; map: which row each is (null: all, in order). Rows after the
-// last are zeros up to a whole block of the products' depth. Backward, the gradients of rows without a loss are zeros.
-// A warp copies 2 KB of a row; rows that start elsewhere are read in the 16-byte words that cover them.
+// What is copied to rows of `pitch` elements that start on 16 bytes, 2 KB (of `chunks` in a row) by a warp at a time: rows that start
+// elsewhere are read in the 16-byte words that cover them.
 template <class T>
-__global__ void __launch_bounds__(kThreads) pack_kernel(LossArgs a, Ws w, const T* src, int64_t rows, T* dst, int64_t pitch, int chunks,
-                                                        T* zeros) {
-    pdl_enter();
-    const int64_t count = w.map ? w.head->count : rows, end = w.map ? (count + mma::kDepth - 1) / mma::kDepth * mma::kDepth : rows;
-    const int lane = threadIdx.x & 31, warps = kThreads / 32;
-    const int words = static_cast<int>(pitch / 8);
-    const int64_t step = static_cast<int64_t>(gridDim.x) * warps, first = static_cast<int64_t>(blockIdx.x) * warps + (threadIdx.x >> 5);
-    for (int64_t i = first; i < end * chunks; i += step) {
-        const int64_t r = i / chunks;
-        const int at = static_cast<int>(i - r * chunks) * 128 + lane;
+struct Packing {
+    const T* src;
+    T* dst;
+    int64_t rows, pitch;
+    int cols, chunks;
+    // row `from` (below 0: zeros) to row r, its part `chunk`
+    __device__ __forceinline__ void copy(int64_t r, int64_t from_row, int chunk) const {
+        const int at = chunk * 128 + (threadIdx.x & 31), words = static_cast<int>(pitch / 8);
         uint4* to = reinterpret_cast<uint4*>(dst + r * pitch);
         uint4 q[4];
-        if (r < count) {
-            const uintptr_t p = reinterpret_cast<uintptr_t>(src + static_cast<int64_t>(w.map ? w.map[r] : r) * a.cols);
+        if (from_row >= 0) {
+            const uintptr_t p = reinterpret_cast<uintptr_t>(src + from_row * cols);
             const int shift = static_cast<int>(p & 15);
             const uint4* from = reinterpret_cast<const uint4*>(p - shift);
-            const int have = (shift + 2 * a.cols + 15) / 16;  // words that cover the row
+            const int have = (shift + 2 * cols + 15) / 16;  // words that cover the row
             if (shift == 0) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -218,7 +224,30 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(LossArgs a, Ws w, const 
         for (int j = 0; j < 4; ++j)
             if (at + 32 * j < words) to[at + 32 * j] = q[j];
     }
-    if (!zeros) return;
+};
+
+// hidden's rows that have a loss, then zeros up to a whole block of the products' depth; all rows of the weight (dst null: none);
+// backward, the gradients of rows without a loss, which are zeros. SMALL: every CTA finds by itself which rows those are, and
+// the first writes it down, so that one launch does all of it (up to 1024 rows).
+template <class T, bool SMALL>
+__global__ void __launch_bounds__(SMALL ? kScanThreads : kThreads) pack_kernel(LossArgs a, Ws w, int backward, Packing<T> hidden, Packing<T> weight) {
+    __shared__ int small_map[SMALL ? kScanThreads : 1];
+    pdl_enter();
+    const int64_t count = SMALL ? list_rows<1>(a, w, backward, blockIdx.x == 0, small_map) : hidden.dst ? w.head->count : 0;
+    const int64_t end = hidden.dst ? (count + mma::kDepth - 1) / mma::kDepth * mma::kDepth * hidden.chunks : 0;
+    const int64_t all = end + (weight.dst ? weight.rows * weight.chunks : 0);
+    const int64_t warps = blockDim.x / 32, step = gridDim.x * warps, first = blockIdx.x * warps + threadIdx.x / 32;
+    for (int64_t i = first; i < all; i += step) {
+        if (i < end) {
+            const int64_t r = i / hidden.chunks;
+            hidden.copy(r, r >= count ? -1 : SMALL ? small_map[r] : w.map[r], static_cast<int>(i - r * hidden.chunks));
+        } else {
+            const int64_t r = (i - end) / weight.chunks;
+            weight.copy(r, r, static_cast<int>(i - end - r * weight.chunks));
+        }
+    }
+    if (!backward || !a.dhidden) return;
+    T* zeros = static_cast<T*>(a.dhidden);
     for (int64_t r = first; r < a.rows; r += step)
         if (a.labels[r] == a.ignore) zero_bytes(reinterpret_cast<char*>(zeros + r * a.cols), reinterpret_cast<char*>(zeros + (r + 1) * a.cols));
 }
@@ -539,29 +568,26 @@ Ws workspace(const LossArgs& a, const LossPlan& p) {
               f(p.lse), f(p.coef), f(p.onehot), reinterpret_cast<float2*>(a.ws + p.parts_at), f(p.picked), f(p.sums), p.rows_pad};
 }
 
-template <class T>
-cudaError_t pack_rows(const LossArgs& a, const Ws& w, const T* src, int64_t rows, T* dst, int64_t pitch, T* zeros, cudaStream_t stream) {
-    const int chunks = static_cast<int>(ceil_div(pitch, 1024));
-    const int64_t ctas = std::min<int64_t>(ceil_div((rows + mma::kDepth) * chunks, kThreads / 32), 1 << 14);
-    return launch_dependent(pack_kernel<T>, dim3(static_cast<unsigned>(ctas)), kThreads, 0, 1, stream, a, w, src, rows, dst, pitch, chunks, zeros);
-}
-
-// hidden's rows that have a loss, and the weight where its rows do not start on 16 bytes.
+// hidden's rows that have a loss (unless w.map is null: as it is), and the weight where its rows do not start on 16 bytes.
 template <class T>
 cudaError_t pack(const LossArgs& a, const LossPlan& p, const Ws& w, int backward, const T** hidden, const T** weight, cudaStream_t stream) {
-    *hidden = static_cast<const T*>(a.hidden);
-    *weight = static_cast<const T*>(a.weight);
-    cudaError_t e = cudaSuccess;
-    if (w.map) {
-        T* to = reinterpret_cast<T*>(a.ws + p.hidden);
-        *hidden = to;
-        e = launch_dependent(rows_kernel, dim3(1), kScanThreads, 0, 1, stream, a, w, backward);
-        if (e == cudaSuccess) e = pack_rows<T>(a, w, static_cast<const T*>(a.hidden), a.rows, to, p.pitch, backward ? static_cast<T*>(a.dhidden) : nullptr, stream);
+    const int chunks = static_cast<int>(ceil_div(p.pitch, 1024));
+    Packing<T> h{static_cast<const T*>(a.hidden), w.map ? reinterpret_cast<T*>(a.ws + p.hidden) : nullptr, a.rows, p.pitch, a.cols, chunks};
+    Packing<T> t{static_cast<const T*>(a.weight), p.pack_weight ? reinterpret_cast<T*>(a.ws + p.weight) : nullptr, a.vocab, p.pitch, a.cols, chunks};
+    *hidden = h.dst ? h.dst : h.src;
+    *weight = t.dst ? t.dst : t.src;
+    const int64_t items = ((h.dst ? a.rows + mma::kDepth : 0) + (t.dst ? a.vocab : 0)) * chunks;
+    if (items == 0) return cudaSuccess;
+    if (w.map && a.rows <= kScanThreads) {
+        const int64_t ctas = std::min<int64_t>(ceil_div(items, kScanThreads / 32), 4 * kPairs);
+        return launch_dependent(pack_kernel<T, true>, dim3(static_cast<unsigned>(ctas)), kScanThreads, 0, 1, stream, a, w, backward, h, t);
     }
-    if (e != cudaSuccess || !p.pack_weight) return e;
-    T* to = reinterpret_cast<T*>(a.ws + p.weight);
-    *weight = to;
-    return pack_rows<T>(a, Ws{}, static_cast<const T*>(a.weight), a.vocab, to, p.pitch, nullptr, stream);
+    if (w.map) {
+        const cudaError_t e = launch_dependent(rows_kernel, dim3(1), kScanThreads, 0, 1, stream, a, w, backward);
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t ctas = std::min<int64_t>(ceil_div(items, kThreads / 32), 1 << 14);
+    return launch_dependent(pack_kernel<T, false>, dim3(static_cast<unsigned>(ctas)), kThreads, 0, 1, stream, a, w, backward, h, t);
 }
 
 // ---- launches -------------------------------------------------------------------------
