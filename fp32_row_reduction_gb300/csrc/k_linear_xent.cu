@@ -291,10 +291,19 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// 32 columns of a row per lane, rounded to T, as half h of the rows of a box.
+template <class T>
+__device__ __forceinline__ void box_columns(const mma::OutBox& box, int h, const float (&v)[32]) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+        box.put(4 * h + g, pack2<T>(v[8 * g], v[8 * g + 1]), pack2<T>(v[8 * g + 2], v[8 * g + 3]), pack2<T>(v[8 * g + 4], v[8 * g + 5]),
+                pack2<T>(v[8 * g + 6], v[8 * g + 7]));
+}
+
 // 32 columns from c on of a row per lane (null: none), of which those below `cols` are written, rounded to T. Rows that start on 16
 // bytes take 16-byte stores; others are turned in shared memory, so that a warp writes 32 columns of one row at a time.
 template <class T>
-__device__ __forceinline__ void store_columns(T* row, int c, int cols, const float (&v)[32], bool wide, float* turn) {
+__device__ __forceinline__ void store_columns(T* row, int c, int cols, const float (&v)[32], bool wide, const mma::OutBox& box) {
     if (wide) {
         if (!row) return;
 #pragma unroll
@@ -306,13 +315,17 @@ __device__ __forceinline__ void store_columns(T* row, int c, int cols, const flo
     }
     const int lane = threadIdx.x & 31;
     __syncwarp();
+    // (element i of row r lies at i ^ r of its row: no two lanes meet in a bank)
 #pragma unroll
-    for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = v[i];
+    for (int i = 0; i < 32; ++i) asm volatile("st.shared.f32 [%0], %1;" ::"r"(box.at + (lane * 32 + (i ^ lane)) * 4), "f"(v[i]) : "memory");
     __syncwarp();
     const unsigned long long mine = reinterpret_cast<unsigned long long>(row);
+#pragma unroll 8
     for (int i = 0; i < 32; ++i) {
         T* p = reinterpret_cast<T*>(__shfl_sync(kFull, mine, i));
-        if (p && c + lane < cols) p[c + lane] = from_float<T>(turn[i * 33 + lane]);
+        float f;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(box.at + (i * 32 + (lane ^ i)) * 4) : "memory");
+        if (p && c + lane < cols) p[c + lane] = from_float<T>(f);
     }
 }
 
@@ -336,7 +349,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
             count = p.w.map ? p.w.head->count : p.rows;
             return mma::Work(p.width, mma::Tiles{tiles_of(count, kTileRows), tiles_of(p.n, p.width), 1, tiles_of(p.cols, mma::kDepth)});
         },
-        [&](const mma::Unit& u, int row, int half, int first, int last, uint32_t at, bool ok, float*, bool begun, bool whole, auto&& release) {
+        [&](const mma::Unit& u, int row, int half, int first, int last, uint32_t at, bool ok, const mma::OutBox&, bool begun, bool whole, auto&& release) {
             if (row - static_cast<int>(threadIdx.x & 31) >= count) return release();  // none of the warp's rows is one
             const int limit = static_cast<int>(min(static_cast<int64_t>(last), p.n - u.n)) - first;  // columns of the vocabulary
 #pragma unroll
@@ -389,7 +402,8 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
 // Backward: scale dz / logit_scale of a piece, rounded. Rows and words beyond the last are zeros up to the tile's end.
 template <class T>
 __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
-    probs_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap weight, const __grid_constant__ Product p) {
+    probs_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap weight, const __grid_constant__ CUtensorMap out,
+                 const __grid_constant__ Product p) {
     int64_t count = 0;
     float times = 0.0f;
     const mma::Operands<false, false> o{&hidden, &weight};
@@ -400,16 +414,17 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
             times = p.w.head->scale;
             return mma::Work(p.width, mma::Tiles{tiles_of(count, kTileRows), tiles_of(p.n, p.width), 1, tiles_of(p.cols, mma::kDepth)});
         },
-        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, float* turn, bool, bool, auto&& release) {
+        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, const mma::OutBox& box, bool, bool, auto&& release) {
             // rows that are not there are read as the depth of the weight's gradient up to the end of a block
-            if (row - static_cast<int>(threadIdx.x & 31) >= (count + mma::kDepth - 1) / mma::kDepth * mma::kDepth) return release();
+            const int row0 = row - static_cast<int>(threadIdx.x & 31);
+            if (row0 >= (count + mma::kDepth - 1) / mma::kDepth * mma::kDepth) return release();
             const bool in = row < count;
             const int limit = static_cast<int>(min(static_cast<int64_t>(last), p.n - u.n));
             const float lse = in ? p.w.lse[row] : 0.0f, coef = in ? p.w.coef[row] * times : 0.0f;
             const float onehot = in ? p.w.onehot[row] * times : 0.0f;
             const int word = in ? p.w.labels[row] : -1;
             const int label = word >= 0 ? static_cast<int>(word - p.first) - u.n : -1;
-            T* to = static_cast<T*>(p.to) + row * p.pitch + u.n;
+            const bool boxed = (last - first) % 64 == 0;
             for (int c = first; c < last; c += 32) {
                 float z[32];
                 mma::load_columns(at + c, z);
@@ -426,7 +441,14 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
                     for (int i = 0; i < 32; ++i)
                         if (!in || c + i >= limit) z[i] = 0.0f;
                 }
-                store_columns<T>(to, c, last, z, true, turn);
+                if (boxed) {
+                    const int h = (c - first) / 32 & 1;
+                    if (h == 0) box.clear();
+                    box_columns<T>(box, h, z);
+                    if (h == 1) box.send(&out, u.n + c - 32, row0);
+                } else {
+                    store_columns<T>(static_cast<T*>(p.to) + row * p.pitch + u.n, c, last, z, true, box);
+                }
             }
             release();
         });
@@ -436,7 +458,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
 // the piece's rows of the weight's gradient. One launch has both, so that there is one end at which pairs run out of work.
 template <class T>
 __device__ __forceinline__ void hidden_part(const Product& p, const mma::Unit& u, int64_t count, float times, int row, int first, int last, uint32_t at,
-                                            bool ok, float* turn) {
+                                            bool ok, const mma::OutBox& box) {
     const bool in = row < count;
     float* sums = p.w.sums + (u.split * p.w.rows_pad + row) * p.pitch + u.n;
     T* to = in && p.last ? static_cast<T*>(p.to) + static_cast<int64_t>(p.w.map[row]) * p.cols + u.n : nullptr;
@@ -465,28 +487,35 @@ __device__ __forceinline__ void hidden_part(const Product& p, const mma::Unit& u
         if (p.last) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) z[i] *= times;
-            store_columns<T>(to, c, min(last, p.cols - u.n), z, p.wide, turn);
+            store_columns<T>(to, c, min(last, p.cols - u.n), z, p.wide, box);
         }
     }
 }
 template <class T>
-__device__ __forceinline__ void weight_part(const Product& p, const mma::Unit& u, float times, int row, int first, int last, uint32_t at, bool ok,
-                                            float* turn) {
+__device__ __forceinline__ void weight_part(const Product& p, const CUtensorMap* out, const mma::Unit& u, float times, int row, int first, int last,
+                                            uint32_t at, bool ok, const mma::OutBox& box) {
+    const int row0 = row - static_cast<int>(threadIdx.x & 31), cols = min(last, p.cols - u.n);
     T* to = row < p.n ? static_cast<T*>(p.dweight) + (p.first + row) * p.cols + u.n : nullptr;
-    const int cols = min(last, p.cols - u.n);
     for (int c = first; c < cols; c += 32) {
         float z[32];
         mma::load_columns(at + c, z);
         if (!ok) spoil(z);
 #pragma unroll
         for (int i = 0; i < 32; ++i) z[i] = u.begin == u.end ? 0.0f : z[i] * times;
-        store_columns<T>(to, c, cols, z, p.dweight_wide, turn);
+        if (p.dweight_wide) {  // (what a box has beyond the last row and column is not written)
+            const int h = (c - first) / 32 & 1;
+            if (h == 0) box.clear();
+            box_columns<T>(box, h, z);
+            if (h == 1 || c + 32 >= cols) box.send(out, u.n + c - 32 * h, row0);
+        } else {
+            store_columns<T>(to, c, cols, z, false, box);
+        }
     }
 }
 template <class T>
 __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     grads_kernel(const __grid_constant__ CUtensorMap probs_rows, const __grid_constant__ CUtensorMap weight, const __grid_constant__ CUtensorMap probs_cols,
-                 const __grid_constant__ CUtensorMap hidden, const __grid_constant__ Product p) {
+                 const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap dweight_out, const __grid_constant__ Product p) {
     int64_t count = 0;
     float times = 0.0f;
     mma::run<0>(
@@ -500,12 +529,12 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
             if (p.dweight) dweight = mma::Tiles{tiles_of(p.n, kTileRows), across, 1, tiles_of(count, mma::kDepth)};
             return mma::Work(p.width, dhidden, dweight);
         },
-        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, float* turn, bool, bool, auto&& release) {
+        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, const mma::OutBox& box, bool, bool, auto&& release) {
             const int row0 = row - static_cast<int>(threadIdx.x & 31);
             if (u.kind == 1) {
-                if (row0 < p.n) weight_part<T>(p, u, times, row, first, last, at, ok, turn);
+                if (row0 < p.n) weight_part<T>(p, &dweight_out, u, times, row, first, last, at, ok, box);
             } else if (row0 < count) {
-                hidden_part<T>(p, u, count, times, row, first, last, at, ok, turn);
+                hidden_part<T>(p, u, count, times, row, first, last, at, ok, box);
             }
             release();
         });
@@ -668,17 +697,20 @@ cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
     cudaError_t e = pack<T>(a, p, w, 1, &hidden, &weight, stream);
     T* probs = reinterpret_cast<T*>(a.ws + p.probs);
     const mma::Boxes boxes = mma::boxes_for(a.rows);
-    CUtensorMap hidden_rows, hidden_cols, probs_rows, probs_cols;
+    CUtensorMap hidden_rows, hidden_cols, probs_rows, probs_cols, probs_out;
     if (e == cudaSuccess) e = map_of(&hidden_rows, hidden, p.rows_pad, a.cols, p.pitch, boxes.rows);
     if (e == cudaSuccess) e = map_of(&hidden_cols, hidden, p.rows_pad, a.cols, p.pitch, mma::kDepth);
     if (e == cudaSuccess) e = map_of(&probs_rows, probs, p.rows_pad, p.piece, p.piece, boxes.rows);
     if (e == cudaSuccess) e = map_of(&probs_cols, probs, p.rows_pad, p.piece, p.piece, mma::kDepth);
+    if (e == cudaSuccess) e = map_of(&probs_out, probs, p.rows_pad, p.piece, p.piece, 32);
     const int64_t row_tiles = p.rows_pad / kTileRows;
+    const bool align = a.cols % 8 == 0, dweight_wide = a.dweight && align && reinterpret_cast<uintptr_t>(a.dweight) % 16 == 0;
     for (int64_t first = 0; first < a.vocab && e == cudaSuccess; first += p.piece) {
         const int64_t n = std::min(p.piece, a.vocab - first);
-        CUtensorMap weight_rows, weight_cols;
+        CUtensorMap weight_rows, weight_cols, dweight_out = probs_out;
         e = map_of(&weight_rows, weight + first * p.pitch, n, a.cols, p.pitch, p.width / 2);
         if (e == cudaSuccess) e = map_of(&weight_cols, weight + first * p.pitch, n, a.cols, p.pitch, mma::kDepth);
+        if (e == cudaSuccess && dweight_wide) e = map_of(&dweight_out, static_cast<const T*>(a.dweight) + first * a.cols, n, a.cols, a.cols, 32);
         if (e != cudaSuccess) break;
         Product d{};
         d.w = w;
@@ -691,9 +723,8 @@ cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
         d.width = p.width;
         d.to = probs;
         d.pitch = p.piece;
-        e = launch_product(probs_kernel<T>, row_tiles * ceil_div(n, p.width), stream, hidden_rows, weight_rows, d);
+        e = launch_product(probs_kernel<T>, row_tiles * ceil_div(n, p.width), stream, hidden_rows, weight_rows, probs_out, d);
         if (e != cudaSuccess) break;
-        const bool align = a.cols % 8 == 0;
         const int64_t across = ceil_div(a.cols, p.grad_width);
         d.width = p.grad_width;
         d.splits = p.splits;
@@ -703,9 +734,9 @@ cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
         d.begun = first > 0;
         d.last = p.splits == 1 && first + n == a.vocab;
         d.wide = align && reinterpret_cast<uintptr_t>(a.dhidden) % 16 == 0;
-        d.dweight_wide = align && reinterpret_cast<uintptr_t>(a.dweight) % 16 == 0;
+        d.dweight_wide = dweight_wide;
         const int64_t units = (a.dhidden ? row_tiles * across * p.splits : 0) + (a.dweight ? ceil_div(n, kTileRows) * across : 0);
-        e = launch_product(grads_kernel<T>, units, stream, probs_rows, weight_cols, probs_cols, hidden_cols, d);
+        e = launch_product(grads_kernel<T>, units, stream, probs_rows, weight_cols, probs_cols, hidden_cols, dweight_out, d);
     }
     if (e != cudaSuccess || !a.dhidden || p.splits == 1) return e;
     const int64_t ctas = std::min<int64_t>(ceil_div(a.rows * a.cols, kThreads), 1 << 16);

@@ -33,8 +33,8 @@ constexpr int kStageBytes = (kRows + kMaxWidth / 2) * 128;
 constexpr int kStages = 6;
 constexpr int kOutWarps = 8;      // two for each quarter of the 128 rows
 constexpr int kThreads = 32 * (2 + kOutWarps);
-constexpr int kTurnFloats = 32 * 33;  // an output warp's room to turn a 32 x 32 tile
-constexpr int kSmem = 1024 + kStages * kStageBytes + kOutWarps * kTurnFloats * 4 + 256;
+constexpr int kOutBytes = 4096;   // an output warp's room: 32 rows of 128 bytes
+constexpr int kSmem = 1024 + kStages * kStageBytes + kOutWarps * kOutBytes;
 constexpr int kColumns = 512;     // of tensor memory: two tiles
 constexpr long long kLimitNs = 2000000000, kLateNs = 100000000, kTestNs = 1000000;
 
@@ -114,6 +114,33 @@ __device__ __forceinline__ void add_columns(uint32_t addr, bool begun, float* v)
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = begun ? v[i] + __uint_as_float(r[i]) : __uint_as_float(r[i]);
 }
+
+// An output warp's room: 32 rows of 128 bytes in a 128-byte swizzle, on their way to a box of a tensor map.
+struct OutBox {
+    uint32_t at;
+    // once the box that was sent before has been read
+    __device__ __forceinline__ void clear() const {
+        if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+    }
+    // 16-byte word j of the lane's row
+    __device__ __forceinline__ void put(int j, uint32_t a, uint32_t b, uint32_t c, uint32_t d) const {
+        const int lane = threadIdx.x & 31;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + lane * 128 + ((j ^ (lane & 7)) << 4)), "r"(a), "r"(b), "r"(c), "r"(d)
+                     : "memory");
+    }
+    __device__ __forceinline__ void send(const CUtensorMap* map, int x, int y) const {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map), "r"(at), "r"(x), "r"(y) : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+    __device__ __forceinline__ static void finish() {
+        if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+};
 
 // Shared-memory descriptor of an operand's block. Depth contiguous: groups of 8 rows are 1024 bytes apart. Rows
 // contiguous: groups of 8 depths are 1024 bytes apart, and groups of 64 rows a box of 64 depths.
@@ -239,9 +266,8 @@ struct Work {
 // The products of a CTA pair: plan() gives the work, once what earlier kernels wrote can be read; o0 and o1 are the operands of the two
 // kinds. The sums of a tile come in one part, or (CHUNK > 0) in a part for every CHUNK blocks of the depth, for the caller to add: the
 // tensor cores round their sums toward zero, an error that grows with the length of a sum. out(unit, row, half, first, last,
-// tensor address, ok, turn, begun, whole, release) takes the columns [first, last) of one row a lane, and calls release() when it has
-// read the tensor memory; ok: the sums are there (false: after a wait that gave up); turn: kTurnFloats of shared memory for the
-// warp; begun: earlier parts have come; whole: the last one.
+// tensor address, ok, box, begun, whole, release) takes the columns [first, last) of one row a lane, and calls release() when it has
+// read the tensor memory; ok: the sums are there (false: after a wait that gave up); box: the warp's room in shared memory; begun: earlier parts have come; whole: the last one.
 template <int CHUNK, class O0, class O1, class Plan, class Out>
 __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& boxes, uint32_t type_bits, const Limits& lim, Plan&& plan, Out&& out) {
     extern __shared__ __align__(16) char raw[];
@@ -293,7 +319,7 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
             int stage = 0;
             uint32_t phase = 0, issued = 0;
             bool ok = true;
-            Unit u;
+            Unit u{};
             const auto copy = [&](const auto& o) {
                 using O = std::decay_t<decltype(o)>;
                 const int m = u.m + rank * kRows, n = u.n + rank * half;
@@ -344,7 +370,7 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
             uint32_t phase = 0, slot = 0, slot_phase = 0;
             bool ok = true;
             if ((lim.debug & kDebugForceTimeout) && blockIdx.x == 0) mbar_wait_bounded(&s.never, 0, kTestNs, lim.err);
-            Unit u;
+            Unit u{};
             const auto multiply = [&](auto&& o) {
                 using O = std::decay_t<decltype(o)>;
                 // kind::f16: binary32 sums; the operands' type and layouts, width / 8 and 256 / 16
@@ -386,7 +412,7 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
     } else {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const int first = half * (width / 2), last = half ? width : width / 2;
-        float* turn = reinterpret_cast<float*>(raw + (base - smem_addr(raw)) + kStages * kStageBytes) + (warp - 2) * kTurnFloats;
+        const OutBox box{base + kStages * kStageBytes + (warp - 2) * kOutBytes};
         uint32_t slot = 0, slot_phase = 0;
         Unit u;
         for (int64_t i = 0; work.unit(i, &u); ++i) {
@@ -397,7 +423,7 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
                 const bool ok = waits.wait(&s.done[slot], slot_phase) && !__any_sync(kFull, waits.dead());
                 fence_after();
                 const uint32_t at = columns + slot * kMaxWidth + (static_cast<uint32_t>(quarter * 32) << 16);
-                out(u, u.m + static_cast<int>(rank) * kRows + quarter * 32 + lane, half, first, last, at, ok, turn, begun, k >= u.end, [&] {
+                out(u, u.m + static_cast<int>(rank) * kRows + quarter * 32 + lane, half, first, last, at, ok, box, begun, k >= u.end, [&] {
                     fence_before();
                     __syncwarp();
                     if (lane == 0) arrive_in(in_cta(smem_addr(&s.room[slot]), 0));
@@ -405,6 +431,7 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
                 if (++slot == 2) slot = 0, slot_phase ^= 1;
             } while (k < u.end);
         }
+        OutBox::finish();
     }
     __syncwarp();
     fence_before();
