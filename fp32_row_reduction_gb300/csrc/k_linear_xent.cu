@@ -300,21 +300,23 @@ __device__ __forceinline__ void box_columns(const mma::OutBox& box, int h, const
                 pack2<T>(v[8 * g + 6], v[8 * g + 7]));
 }
 
-// 32 columns from c on of a row per lane (null: none), of which those below `cols` are written, rounded to T. Rows that start on 16
-// bytes take 16-byte stores; others are turned in shared memory, so that a warp writes 32 columns of one row at a time.
+// 32 columns from c on of a row per lane that starts on 16 bytes (null: none), of which those below `cols` are written, rounded to T.
 template <class T>
-__device__ __forceinline__ void store_columns(T* row, int c, int cols, const float (&v)[32], bool wide, const mma::OutBox& box) {
-    if (wide) {
-        if (!row) return;
+__device__ __forceinline__ void store_columns(T* row, int c, int cols, const float (&v)[32]) {
+    if (!row) return;
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-            if (c + 8 * g < cols)
-                *reinterpret_cast<uint4*>(row + c + 8 * g) = make_uint4(pack2<T>(v[8 * g], v[8 * g + 1]), pack2<T>(v[8 * g + 2], v[8 * g + 3]),
-                                                                        pack2<T>(v[8 * g + 4], v[8 * g + 5]), pack2<T>(v[8 * g + 6], v[8 * g + 7]));
-        return;
-    }
+    for (int g = 0; g < 4; ++g)
+        if (c + 8 * g < cols)
+            *reinterpret_cast<uint4*>(row + c + 8 * g) = make_uint4(pack2<T>(v[8 * g], v[8 * g + 1]), pack2<T>(v[8 * g + 2], v[8 * g + 3]),
+                                                                    pack2<T>(v[8 * g + 4], v[8 * g + 5]), pack2<T>(v[8 * g + 6], v[8 * g + 7]));
+}
+// The same for rows that start anywhere: the columns are turned in the warp's room, so that it writes 32 of one row at a time. (Words
+// of four bytes, after an exchange between lanes where rows start between two, made the gradients of 64 x 2047 x 30000
+// 225 us instead of 195.)
+template <class T>
+__device__ __forceinline__ void turn_columns(const mma::OutBox& box, T* row, int c, int cols, const float (&v)[32]) {
     const int lane = threadIdx.x & 31;
-    __syncwarp();
+    box.clear();
     // (element i of row r lies at i ^ r of its row: no two lanes meet in a bank)
 #pragma unroll
     for (int i = 0; i < 32; ++i) asm volatile("st.shared.f32 [%0], %1;" ::"r"(box.at + (lane * 32 + (i ^ lane)) * 4), "f"(v[i]) : "memory");
@@ -337,6 +339,45 @@ __device__ __forceinline__ void spoil(float (&v)[32]) {
 // Forward: (maximum, sum of 2^(z - maximum)) of each half of a tile's columns, and the label's z. The logits are summed in parts of
 // kPart blocks of the depth, which are added in registers (see mma::run): a thread has 128 columns of a row.
 constexpr int kPart = 16;
+
+// A row's (maximum, sum) over a thread's columns below `limit` (WHOLE: all 128), z of which is the sum times scale; z of the column
+// `label`, when that is one of them, is written to `picked`.
+template <bool WHOLE>
+__device__ __forceinline__ float2 max_and_sum(float (&z)[128], float scale, bool ok, int limit, int label, float* picked) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < 128; c += 32) {
+        if (!WHOLE && c >= limit) continue;
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = c; i < c + 32; ++i) {
+            z[i] = z[i] * scale;
+            if (!WHOLE && i >= limit) z[i] = -INFINITY;
+            top[i & 1] = fmaxf(top[i & 1], z[i]);
+        }
+        m = fmaxf(m, fmaxf(top[0], top[1]));
+        if (label >= c && label < c + 32) {
+#pragma unroll
+            for (int i = c; i < c + 32; ++i)
+                if (label == i) *picked = z[i];
+        }
+    }
+    const float from = m == -INFINITY ? 0.0f : m;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < 128; c += 32) {
+        if (!WHOLE && c >= limit) continue;
+#pragma unroll
+        for (int g = c; g < c + 32; g += 8) {
+            float part[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = g; i < g + 8; ++i) part[i & 1] += ex2(z[i] - from);
+            s[g / 8 & 3] += part[0] + part[1];
+        }
+    }
+    return make_float2(ok ? m : NAN, (s[0] + s[1]) + (s[2] + s[3]));
+}
+
 template <class T>
 __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     stats_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap weight, const __grid_constant__ Product p) {
@@ -352,9 +393,15 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
         [&](const mma::Unit& u, int row, int half, int first, int last, uint32_t at, bool ok, const mma::OutBox&, bool begun, bool whole, auto&& release) {
             if (row - static_cast<int>(threadIdx.x & 31) >= count) return release();  // none of the warp's rows is one
             const int limit = static_cast<int>(min(static_cast<int64_t>(last), p.n - u.n)) - first;  // columns of the vocabulary
+            if (!begun) {
 #pragma unroll
-            for (int c = 0; c < 128; c += 8)
-                if (c < limit) mma::add_columns(at + first + c, begun, z + c);
+                for (int c = 0; c < 128; c += 32)
+                    if (c < limit) mma::load_columns(at + first + c, z + c);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 128; c += 8)
+                    if (c < limit) mma::add_columns(at + first + c, z + c);
+            }
             release();
             if (!whole) return;
             int label = -1;
@@ -366,36 +413,10 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
                     label = l >= 0 && l < p.n ? static_cast<int>(l) : -1;
                 }
             }
-            label = label >= 0 ? label - u.n - first : -1;
-            float m = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 128; c += 16) {
-                if (c >= limit) continue;
-                float top = -INFINITY;
-#pragma unroll
-                for (int i = c; i < c + 16; ++i) {
-                    z[i] = ok ? z[i] * p.scale : NAN;
-                    if (i >= limit) z[i] = -INFINITY;
-                    top = fmaxf(top, z[i]);
-                }
-                m = fmaxf(m, top);
-                if (label >= c && label < min(c + 16, limit)) {
-#pragma unroll
-                    for (int i = c; i < c + 16; ++i)
-                        if (label == i) p.w.picked[row] = z[i];
-                }
-            }
-            const float from = m == -INFINITY ? 0.0f : m;
-            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int c = 0; c < 128; c += 16) {
-                if (c >= limit) continue;
-                float part[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int i = c; i < c + 16; ++i) part[i & 1] += ex2(z[i] - from);
-                s[c / 16 & 3] += part[0] + part[1];
-            }
-            if (row < count) p.w.parts[row * p.pitch + 2 * (u.n / p.width) + half] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
+            label = label >= u.n + first && label < u.n + first + limit ? label - u.n - first : -1;
+            const float2 part = limit >= 128 ? max_and_sum<true>(z, p.scale, ok, limit, label, p.w.picked + row)
+                                             : max_and_sum<false>(z, p.scale, ok, limit, label, p.w.picked + row);
+            if (row < count) p.w.parts[row * p.pitch + 2 * (u.n / p.width) + half] = part;
         });
 }
 
@@ -447,7 +468,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
                     box_columns<T>(box, h, z);
                     if (h == 1) box.send(&out, u.n + c - 32, row0);
                 } else {
-                    store_columns<T>(static_cast<T*>(p.to) + row * p.pitch + u.n, c, last, z, true, box);
+                    store_columns<T>(static_cast<T*>(p.to) + row * p.pitch + u.n, c, last, z);
                 }
             }
             release();
@@ -487,7 +508,9 @@ __device__ __forceinline__ void hidden_part(const Product& p, const mma::Unit& u
         if (p.last) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) z[i] *= times;
-            store_columns<T>(to, c, min(last, p.cols - u.n), z, p.wide, box);
+            const int n = min(last, p.cols - u.n);
+            if (p.wide) store_columns<T>(to, c, n, z);
+            else turn_columns<T>(box, to, c, n, z);
         }
     }
 }
@@ -508,7 +531,7 @@ __device__ __forceinline__ void weight_part(const Product& p, const CUtensorMap*
             box_columns<T>(box, h, z);
             if (h == 1 || c + 32 >= cols) box.send(out, u.n + c - 32 * h, row0);
         } else {
-            store_columns<T>(to, c, cols, z, false, box);
+            turn_columns<T>(box, to, c, cols, z);
         }
     }
 }

@@ -87,7 +87,7 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 // 32 columns of this warp's 32 rows, a row to a lane.
-__device__ __forceinline__ void load_columns(uint32_t addr, float (&v)[32]) {
+__device__ __forceinline__ void load_columns(uint32_t addr, float* v) {
     uint32_t r[32];
     __syncwarp();
     asm volatile(
@@ -103,8 +103,8 @@ __device__ __forceinline__ void load_columns(uint32_t addr, float (&v)[32]) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 8 columns added to sums that are kept in registers (`begun`: not the first).
-__device__ __forceinline__ void add_columns(uint32_t addr, bool begun, float* v) {
+// 8 columns added to sums that are kept in registers.
+__device__ __forceinline__ void add_columns(uint32_t addr, float* v) {
     uint32_t r[8];
     __syncwarp();
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -112,7 +112,7 @@ __device__ __forceinline__ void add_columns(uint32_t addr, bool begun, float* v)
                  : "r"(addr));
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = begun ? v[i] + __uint_as_float(r[i]) : __uint_as_float(r[i]);
+    for (int i = 0; i < 8; ++i) v[i] += __uint_as_float(r[i]);
 }
 
 // An output warp's room: 32 rows of 128 bytes in a 128-byte swizzle, on their way to a box of a tensor map.

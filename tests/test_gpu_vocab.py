@@ -396,6 +396,23 @@ def test_outputs_end_where_they_end():
             assert bool((f[:128 + offset] == 7).all()) and bool((f[128 + offset + n:] == 7).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("cols", [72, 520])
+def test_gradients_in_different_places(dtype, cols):
+    """dhidden and dweight that start anywhere, each while the other starts on 16 bytes; the bits are the same."""
+    rows, v = 700, 1300
+    hidden, weight, labels, dloss, dlse = loss_inputs(rows, cols, v, dtype, ignored=0.1)
+    _, lse, dh, dw = check_loss(hidden, weight, labels, dloss, dlse)
+    for oh, ow in ((1, 0), (0, 1), (3, 5)):
+        flat_h = torch.full((rows * cols + 16,), 7.0, device=DEV, dtype=hidden.dtype)
+        flat_w = torch.full((v * cols + 16,), 7.0, device=DEV, dtype=hidden.dtype)
+        view_h, view_w = flat_h[oh:oh + rows * cols].view(rows, cols), flat_w[ow:ow + v * cols].view(v, cols)
+        tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse, dhidden=view_h, dweight=view_w)
+        assert same(view_h, dh) and same(view_w, dw)
+        assert bool((flat_h[:oh] == 7).all()) and bool((flat_h[oh + rows * cols:] == 7).all())
+        assert bool((flat_w[:ow] == 7).all()) and bool((flat_w[ow + v * cols:] == 7).all())
+
+
 # ---- streams, graphs, threads ---------------------------------------------------------------
 
 def test_other_streams():
