@@ -33,7 +33,8 @@ LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
     // The width whose tiles come out even over the pairs of a GPU's CTAs. A narrow tile reads the rows of hidden more often (the
     // 24), which a single tile of rows does not feel in the forward pass: there a narrower tile only splits the weight's reading more
     // evenly. Backward, the tiles fill whole multiples of 256 words.
-    width = grad_width = mma::kMaxWidth;
+    width = mma::kMaxWidth;
+    grad_width = cols > 128 ? mma::kMaxWidth : 128;  // (half as wide a tile takes half as long)
     const int64_t row_tiles = rows_pad / kTileRows;
     int64_t least = INT64_MAX;
     for (int n = mma::kMaxWidth; n >= 64; n = backward ? n / 2 : n - 32) {
@@ -340,6 +341,16 @@ __device__ __forceinline__ void spoil(float (&v)[32]) {
 // kPart blocks of the depth, which are added in registers (see mma::run): a thread has 128 columns of a row.
 constexpr int kPart = 16;
 
+// Two products, and two sums, in one instruction each.
+__device__ __forceinline__ void pair_times(float& a, float& b, float by) {
+    asm("{\n\t.reg .b64 v, w;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %2};\n\tmul.rn.f32x2 v, v, w;\n\tmov.b64 {%0, %1}, v;\n\t}" : "+f"(a), "+f"(b) : "f"(by));
+}
+__device__ __forceinline__ void pair_plus(float& a, float& b, float c, float d) {
+    asm("{\n\t.reg .b64 v, w;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\tadd.rn.f32x2 v, v, w;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(c), "f"(d));
+}
+
 // A row's (maximum, sum) over a thread's columns below `limit` (WHOLE: all 128), z of which is the sum times scale; z of the column
 // `label`, when that is one of them, is written to `picked`.
 template <bool WHOLE>
@@ -348,14 +359,13 @@ __device__ __forceinline__ float2 max_and_sum(float (&z)[128], float scale, bool
 #pragma unroll
     for (int c = 0; c < 128; c += 32) {
         if (!WHOLE && c >= limit) continue;
-        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = c; i < c + 32; ++i) {
-            z[i] = z[i] * scale;
+        for (int i = c; i < c + 32; i += 2) {
+            pair_times(z[i], z[i + 1], scale);
             if (!WHOLE && i >= limit) z[i] = -INFINITY;
-            top[i & 1] = fmaxf(top[i & 1], z[i]);
+            if (!WHOLE && i + 1 >= limit) z[i + 1] = -INFINITY;
+            m = fmaxf(m, fmaxf(z[i], z[i + 1]));
         }
-        m = fmaxf(m, fmaxf(top[0], top[1]));
         if (label >= c && label < c + 32) {
 #pragma unroll
             for (int i = c; i < c + 32; ++i)
@@ -363,7 +373,7 @@ __device__ __forceinline__ float2 max_and_sum(float (&z)[128], float scale, bool
         }
     }
     const float from = m == -INFINITY ? 0.0f : m;
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float s[8] = {};
 #pragma unroll
     for (int c = 0; c < 128; c += 32) {
         if (!WHOLE && c >= limit) continue;
@@ -371,11 +381,16 @@ __device__ __forceinline__ float2 max_and_sum(float (&z)[128], float scale, bool
         for (int g = c; g < c + 32; g += 8) {
             float part[2] = {0.0f, 0.0f};
 #pragma unroll
-            for (int i = g; i < g + 8; ++i) part[i & 1] += ex2(z[i] - from);
-            s[g / 8 & 3] += part[0] + part[1];
+            for (int i = g; i < g + 8; i += 2) {
+                pair_plus(z[i], z[i + 1], -from, -from);
+                z[i] = ex2(z[i]);
+                z[i + 1] = ex2(z[i + 1]);
+                pair_plus(part[0], part[1], z[i], z[i + 1]);
+            }
+            pair_plus(s[g / 4 & 6], s[(g / 4 & 6) + 1], part[0], part[1]);
         }
     }
-    return make_float2(ok ? m : NAN, (s[0] + s[1]) + (s[2] + s[3]));
+    return make_float2(ok ? m : NAN, ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
 }
 
 template <class T>
@@ -393,6 +408,15 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
         [&](const mma::Unit& u, int row, int half, int first, int last, uint32_t at, bool ok, const mma::OutBox&, bool begun, bool whole, auto&& release) {
             if (row - static_cast<int>(threadIdx.x & 31) >= count) return release();  // none of the warp's rows is one
             const int limit = static_cast<int>(min(static_cast<int64_t>(last), p.n - u.n)) - first;  // columns of the vocabulary
+            int label = -1;  // (asked for early: it is on its way while the columns come)
+            if (whole && row < count) {
+                if (p.w.map) {
+                    label = p.w.labels[row];
+                } else {
+                    const int64_t l = p.labels[row];
+                    label = l >= 0 && l < p.n ? static_cast<int>(l) : -1;
+                }
+            }
             if (!begun) {
 #pragma unroll
                 for (int c = 0; c < 128; c += 32)
@@ -404,15 +428,6 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
             }
             release();
             if (!whole) return;
-            int label = -1;
-            if (row < count) {
-                if (p.w.map) {
-                    label = p.w.labels[row];
-                } else {
-                    const int64_t l = p.labels[row];
-                    label = l >= 0 && l < p.n ? static_cast<int>(l) : -1;
-                }
-            }
             label = label >= u.n + first && label < u.n + first + limit ? label - u.n - first : -1;
             const float2 part = limit >= 128 ? max_and_sum<true>(z, p.scale, ok, limit, label, p.w.picked + row)
                                              : max_and_sum<false>(z, p.scale, ok, limit, label, p.w.picked + row);
