@@ -9,7 +9,10 @@
 // in its 32 sorted tokens, 512 bytes of columns wide, in binary32. Segments longer than 64 tokens
 // are cut at the tiles' borders into partial sums, which a last kernel adds in order, so one frequent token
 // costs no more than many rare ones. The zeros of rows that no token has are written beside both: as many as
-// fit beside the sort of one CTA, the others beside the sums.
+// fit beside the sort of one CTA, the others beside the sums. Bound by memory, most of it the zeros: 16384 x 4096 bf16 into 50257 rows
+// 105 us (the bytes that cannot be avoided take 82 at the copy rate; zeros alone are written at 6.0 of its 6.7 TB/s),
+// 6039 x 1537 f16 into float32 71 us (49). More than 16384 tokens are sorted by several CTAs in three launches for each eight bits
+// of the ids, 34 us for 131072.
 #include <algorithm>
 
 #include "tr_launch.h"
@@ -599,7 +602,7 @@ __device__ __forceinline__ void write_row(const EmbedGradArgs& a, uint32_t key, 
 }
 
 template <class T, class G, bool WIDE>
-__global__ void __launch_bounds__(kThreads) sum_kernel(SumArgs s) {
+__global__ void __launch_bounds__(kThreads, 2) sum_kernel(SumArgs s) {
     constexpr int N = kLane<T>, kAhead = WIDE ? 16 : 8;  // rows under way
     __shared__ uint32_t shared_words[kFillRows / 32 > kWarps * 32 * (N + 1) ? kFillRows / 32 : kWarps * 32 * (N + 1)];
     pdl_enter();

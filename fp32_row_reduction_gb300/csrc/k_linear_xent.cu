@@ -1,9 +1,18 @@
 // Softmax cross entropy of logits = logit_scale hidden weight^T that are never kept, and its gradients.
 //
-// With z = log2(e) logits, forward: every row's maximum m and sum of 2^(z - m) over each tile of the vocabulary, which a
-// last kernel joins: lse = ln 2 (m + log2 sum), loss = ln 2 (m - z_label) + ln sum.
-// Backward, for one piece of the vocabulary after another: dz = (dloss + dlse) 2^(z - lse) - dloss [label], rounded to the
-// inputs' type for the products dhidden += dz weight (in float32 over the pieces) and dweight = dz^T hidden.
+// With z = log2(e) logits, forward: every row's maximum m and sum of 2^(z - m) over half of each tile of the vocabulary (up to 128
+// words), which a last kernel joins: lse = ln 2 (m + log2 sum), loss = ln 2 (m - z_label) + ln sum, so that the loss of a certain row
+// is no difference of large numbers. Backward, for one piece of the vocabulary after another:
+// dz = (dloss + dlse) 2^(z - lse) - dloss [label], rounded to the inputs' type for the products dhidden += dz weight
+// (in float32 over the pieces) and dweight = dz^T hidden. The rounding is one of T's half steps of each dz, relative to a dz that has
+// the label's -1 in it already; products of an unrounded dz would be two or three of its parts.
+//
+// Rows that have a loss are packed first: the products do no work for the others, and what those hold, which may be no
+// number, is not read as the depth of the weight's gradient.
+//
+// Bound by the tensor cores, and at length by power: 8192 x 4096 x 50257 bf16 with 10% of the rows ignored, forward 1.55 ms at 1.9 GHz
+// (1960 TFLOP/s) and 1.70 ms call after call at 1.5 GHz and 1370 W; gradients 4.85 and 5.5 ms (1880 and 1660). Few rows are bound
+// by reading the weight: 48 x 5120 f16 forward 88 us (5.8 TB/s).
 #include <algorithm>
 #include <cmath>
 
