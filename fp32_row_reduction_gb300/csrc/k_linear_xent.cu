@@ -320,24 +320,24 @@ __device__ __forceinline__ void store_columns(T* row, int c, int cols, const flo
             *reinterpret_cast<uint4*>(row + c + 8 * g) = make_uint4(pack2<T>(v[8 * g], v[8 * g + 1]), pack2<T>(v[8 * g + 2], v[8 * g + 3]),
                                                                     pack2<T>(v[8 * g + 4], v[8 * g + 5]), pack2<T>(v[8 * g + 6], v[8 * g + 7]));
 }
-// The same for rows that start anywhere: the columns are turned in the warp's room, so that it writes 32 of one row at a time. (Words
-// of four bytes, after an exchange between lanes where rows start between two, made the gradients of 64 x 2047 x 30000
-// 225 us instead of 195.)
-template <class T>
-__device__ __forceinline__ void turn_columns(const mma::OutBox& box, T* row, int c, int cols, const float (&v)[32]) {
+// The same for rows that start anywhere: the columns are turned in the warp's room, so that it writes 32 of one row at a time; row(i), asked for
+// in order, is where the warp's i-th row starts (null: none). (Words of four bytes, after an exchange between lanes where rows start between
+// two, made the gradients of 64 x 2047 x 30000 225 us instead of 178.)
+template <class T, class Row>
+__device__ __forceinline__ void turn_columns(const mma::OutBox& box, Row&& row, int c, int cols, const float (&v)[32]) {
     const int lane = threadIdx.x & 31;
     box.clear();
     // (element i of row r lies at i ^ r of its row: no two lanes meet in a bank)
 #pragma unroll
     for (int i = 0; i < 32; ++i) asm volatile("st.shared.f32 [%0], %1;" ::"r"(box.at + (lane * 32 + (i ^ lane)) * 4), "f"(v[i]) : "memory");
     __syncwarp();
-    const unsigned long long mine = reinterpret_cast<unsigned long long>(row);
-#pragma unroll 8
+    float f[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[i]) : "r"(box.at + (i * 32 + (lane ^ i)) * 4) : "memory");
+#pragma unroll
     for (int i = 0; i < 32; ++i) {
-        T* p = reinterpret_cast<T*>(__shfl_sync(kFull, mine, i));
-        float f;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(box.at + (i * 32 + (lane ^ i)) * 4) : "memory");
-        if (p && c + lane < cols) p[c + lane] = from_float<T>(f);
+        T* p = row(i);
+        if (p && c + lane < cols) p[c + lane] = from_float<T>(f[i]);
     }
 }
 
@@ -534,7 +534,9 @@ __device__ __forceinline__ void hidden_part(const Product& p, const mma::Unit& u
             for (int i = 0; i < 32; ++i) z[i] *= times;
             const int n = min(last, p.cols - u.n);
             if (p.wide) store_columns<T>(to, c, n, z);
-            else turn_columns<T>(box, to, c, n, z);
+            else
+                turn_columns<T>(
+                    box, [&](int i) { return reinterpret_cast<T*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(to), i)); }, c, n, z);
         }
     }
 }
@@ -542,7 +544,8 @@ template <class T>
 __device__ __forceinline__ void weight_part(const Product& p, const CUtensorMap* out, const mma::Unit& u, float times, int row, int first, int last,
                                             uint32_t at, bool ok, const mma::OutBox& box) {
     const int row0 = row - static_cast<int>(threadIdx.x & 31), cols = min(last, p.cols - u.n);
-    T* to = row < p.n ? static_cast<T*>(p.dweight) + (p.first + row) * p.cols + u.n : nullptr;
+    T* to = static_cast<T*>(p.dweight) + (p.first + row0) * p.cols + u.n;
+    const int have = static_cast<int>(min(int64_t{32}, p.n - row0));
     for (int c = first; c < cols; c += 32) {
         float z[32];
         mma::load_columns(at + c, z);
@@ -555,7 +558,14 @@ __device__ __forceinline__ void weight_part(const Product& p, const CUtensorMap*
             box_columns<T>(box, h, z);
             if (h == 1 || c + 32 >= cols) box.send(out, u.n + c - 32 * h, row0);
         } else {
-            turn_columns<T>(box, to, c, cols, z);
+            turn_columns<T>(
+                box,
+                [&p, have, q = to](int i) mutable {
+                    T* at = i < have ? q : nullptr;
+                    q += p.cols;
+                    return at;
+                },
+                c, cols, z);
         }
     }
 }

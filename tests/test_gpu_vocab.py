@@ -226,7 +226,7 @@ def test_loss(rows, cols, v, dtype):
     check_loss(hidden, weight, labels, None, None, scale=-0.7)
 
 
-@pytest.mark.parametrize("rows,cols,v", [(37, 40, 300), (600, 129, 700), (1000, 64, 90)])
+@pytest.mark.parametrize("rows,cols,v", [(37, 40, 300), (600, 129, 700), (1000, 64, 90), (1500, 129, 300)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("ignored", [0.3, 0.97, 1.0])
 def test_rows_without_a_loss(rows, cols, v, dtype, ignored):
@@ -487,6 +487,40 @@ def test_graphs():
             g.replay()
             torch.cuda.synchronize()
             assert all(same(x, y) for x, y in zip(out, want))
+
+
+FIRST_CALLS = """
+import torch
+import fp32_row_reduction_gb300 as tr
+g = torch.Generator("cuda")
+g.manual_seed(1)
+table = torch.randn(500, {cols}, generator=g, device="cuda").to(torch.bfloat16)
+ids = torch.randint(0, 500, ({rows},), generator=g, device="cuda")
+labels = torch.roll(ids, 1)
+def step():
+    x = tr.embedding(ids, table, scale=0.1)
+    losses, lse = tr.linear_cross_entropy(x, table, labels)
+    dx, dtable = tr.linear_cross_entropy_backward(x, table, labels, lse)
+    return x, losses, lse, dx, dtable, tr.embedding_backward(dx, ids, 500)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):  # nothing of the library has run before
+    out = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, step()))
+assert tr.tr_last_device_error() == tr.TR_OK
+print("as eager")
+"""
+
+
+@pytest.mark.parametrize("rows,cols", [(40, 64), (20000, 65)])
+def test_first_calls_of_a_process_may_be_captured(rows, cols):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(rows=rows, cols=cols)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "as eager" in r.stdout, r.stderr[-2000:]
 
 
 # ---- a model's two ends together --------------------------------------------------------------
