@@ -163,7 +163,7 @@ struct Operands {
     const CUtensorMap* b;
 };
 // How many rows of A there are at most when all are in one tile (else 256). Rows of a box that lie outside the tensor are
-// filled with zeros slowly (one row of hidden in boxes of 128: 127 us instead of 80), so boxes are as high as the rows need,
+// filled with zeros slowly (one row of hidden in boxes of 128: 122 us instead of 73), so boxes are as high as the rows need,
 // and the second CTA copies none when the first has them all: what the products read there instead gives rows of C that nobody takes.
 struct Boxes {
     int rows;     // of a box of A, where its depth is contiguous
@@ -209,6 +209,11 @@ struct Waits {
     }
 };
 
+// a / b of numbers that are nearly always below 2^32 (a division of 64 bits takes several times as long).
+__device__ __forceinline__ int64_t over(int64_t a, int64_t b) {
+    return (a | b) >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
+
 // One unit of work: which tile, and which blocks of the depth.
 struct Unit {
     int kind;        // of the products of a launch: 0 or 1
@@ -223,9 +228,9 @@ struct Tiles {
     __device__ __forceinline__ int64_t units() const { return static_cast<int64_t>(m) * n * splits; }
     __device__ __forceinline__ Unit unit(int kind, int64_t i, int width) const {
         constexpr int kGroup = 16;
-        const int64_t t = i / splits;
+        const int64_t t = over(i, splits);
         const int split = static_cast<int>(i - t * splits);
-        const int64_t in_group = static_cast<int64_t>(kGroup) * n, g = t / in_group;
+        const int64_t in_group = static_cast<int64_t>(kGroup) * n, g = over(t, in_group);
         const int r = static_cast<int>(t - g * in_group), rows = min(kGroup, m - static_cast<int>(g) * kGroup);
         const int64_t from = static_cast<int64_t>(blocks) * split / splits, to = static_cast<int64_t>(blocks) * (split + 1) / splits;
         return Unit{kind, (static_cast<int>(g) * kGroup + r % rows) * 2 * kRows, r / rows * width, static_cast<int>(from), static_cast<int>(to), split};
@@ -237,18 +242,19 @@ struct Tiles {
 struct Work {
     Tiles first, second;
     int width, pair, pairs;
-    int64_t longer, ahead;  // pairs with one more unit of the first kind; rounds that the others go ahead
+    int64_t each, longer, ahead;  // units of the first kind of every pair; pairs with one more; rounds that the others go ahead
     __device__ __forceinline__ Work(int w, const Tiles& f, const Tiles& s = Tiles{}) : first(f), second(s), width(w) {
         pair = static_cast<int>(blockIdx.x) / 2;
         pairs = static_cast<int>(gridDim.x) / 2;
-        longer = first.units() % pairs;
+        each = over(first.units(), pairs);
+        longer = first.units() - each * pairs;
         constexpr int kOut = 12;  // blocks whose products take as long as a tile's beginning and end
         const int one = first.blocks / first.splits + kOut, other = second.blocks + kOut;
         ahead = longer > 0 && second.units() > 0 ? (one + other / 2) / other : 0;
     }
     // The pair's unit number `step`; false: there is none.
     __device__ __forceinline__ bool unit(int64_t step, Unit* u) const {
-        const int64_t mine = first.units() / pairs + (pair < longer ? 1 : 0);
+        const int64_t mine = each + (pair < longer ? 1 : 0);
         if (step < mine) {
             *u = first.unit(0, pair + step * pairs, width);
             return true;
@@ -267,7 +273,8 @@ struct Work {
 // kinds. The sums of a tile come in one part, or (CHUNK > 0) in a part for every CHUNK blocks of the depth, for the caller to add: the
 // tensor cores round their sums toward zero, an error that grows with the length of a sum. out(unit, row, half, first, last,
 // tensor address, ok, box, begun, whole, release) takes the columns [first, last) of one row a lane, and calls release() when it has
-// read the tensor memory; ok: the sums are there (false: after a wait that gave up); box: the warp's room in shared memory; begun: earlier parts have come; whole: the last one.
+// read the tensor memory; ok: the sums are there (false: after a wait that gave up); box: the warp's room in
+// shared memory; begun: earlier parts have come; whole: the last one.
 template <int CHUNK, class O0, class O1, class Plan, class Out>
 __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& boxes, uint32_t type_bits, const Limits& lim, Plan&& plan, Out&& out) {
     extern __shared__ __align__(16) char raw[];
@@ -295,8 +302,8 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
-    // Rows of A that no copy brings are zeros: numbers left there by other kernels would cost their products' power (48 rows of
-    // hidden: 108 us instead of 97).
+    // Rows of A that no copy brings are zeros: numbers left there by other kernels would cost power (48 rows of
+    // hidden: 97 us instead of 90).
     if (boxes.rows < kRows || !boxes.second) {
         const int from = rank == 0 || boxes.second ? boxes.rows * 8 : 0, words = kRows * 8;  // of 16 bytes
         for (int i = threadIdx.x; i < kStages * words; i += kThreads)
@@ -313,57 +320,46 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
 
     const Work work = plan();
     const int width = work.width;
+    int next_stage = 0;  // of the copying warp: where the next block goes, its phase, and how many went before
+    uint32_t next_phase = 0, issued = 0;
     if (warp == 0) {
-        {
-            const uint32_t half = width / 2;
-            int stage = 0;
-            uint32_t phase = 0, issued = 0;
-            bool ok = true;
-            Unit u{};
-            const auto copy = [&](const auto& o) {
-                using O = std::decay_t<decltype(o)>;
-                const int m = u.m + rank * kRows, n = u.n + rank * half;
-                const uint32_t bytes = 128 * (width + (O::kA ? 2 * kRows : boxes.rows * (boxes.second ? 2 : 1)));  // of both CTAs
-                for (int k = u.begin; k < u.end; ++k) {
-                    ok = waits.wait(&s.empty[stage], phase ^ 1);
-                    if (!ok) break;
-                    const uint32_t bar = in_cta(smem_addr(&s.full[stage]), 0);
-                    const uint32_t to_a = base + stage * kStageBytes, to_b = to_a + kRows * 128;
-                    const int d = k * kDepth;
-                    if (rank == 0) expect_bytes(&s.full[stage], bytes);
-                    if constexpr (O::kA) {
+        const uint32_t half = width / 2;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        Unit u{};
+        const auto copy = [&](const auto& o) {
+            using O = std::decay_t<decltype(o)>;
+            const int m = u.m + rank * kRows, n = u.n + rank * half;
+            const uint32_t bytes = 128 * (width + (O::kA ? 2 * kRows : boxes.rows * (boxes.second ? 2 : 1)));  // of both CTAs
+            for (int k = u.begin; k < u.end; ++k) {
+                ok = waits.wait(&s.empty[stage], phase ^ 1);
+                if (!ok) break;
+                const uint32_t bar = in_cta(smem_addr(&s.full[stage]), 0);
+                const uint32_t to_a = base + stage * kStageBytes, to_b = to_a + kRows * 128;
+                const int d = k * kDepth;
+                if (rank == 0) expect_bytes(&s.full[stage], bytes);
+                if constexpr (O::kA) {
 #pragma unroll
-                        for (int j = 0; j < kRows / 64; ++j) copy_box(to_a + j * kDepth * 128, o.a, m + 64 * j, d, bar);
-                    } else if (rank == 0 || boxes.second) {
-                        copy_box(to_a, o.a, d, m, bar);
-                    }
-                    if constexpr (O::kB) {
-                        for (uint32_t j = 0; j < half / 64; ++j) copy_box(to_b + j * kDepth * 128, o.b, n + 64 * j, d, bar);
-                    } else {
-                        copy_box(to_b, o.b, d, n, bar);
-                    }
-                    ++issued;
-                    if (++stage == kStages) stage = 0, phase ^= 1;
+                    for (int j = 0; j < kRows / 64; ++j) copy_box(to_a + j * kDepth * 128, o.a, m + 64 * j, d, bar);
+                } else if (rank == 0 || boxes.second) {
+                    copy_box(to_a, o.a, d, m, bar);
                 }
-            };
-            for (int64_t i = 0; ok && work.unit(i, &u); ++i) {
-                if (u.kind) copy(o1);
-                else copy(o0);
-            }
-            // after a wait that gave up: the copies under way, of both CTAs, count on the first one's barriers (the second, which
-            // may have begun one more, gives that the time)
-            if (!ok && rank == 1) {
-                const unsigned long long t0 = global_ns();
-                while (static_cast<long long>(global_ns() - t0) < kTestNs) __nanosleep(1000);
-            }
-            if (!ok && rank == 0) {
-                for (int j = 0; j < kStages && issued > 0; ++j, --issued) {
-                    stage = stage == 0 ? kStages - 1 : stage - 1;
-                    if (stage == kStages - 1) phase ^= 1;
-                    mbar_wait_bounded(&s.full[stage], phase, kLateNs, lim.err);
+                if constexpr (O::kB) {
+                    for (uint32_t j = 0; j < half / 64; ++j) copy_box(to_b + j * kDepth * 128, o.b, n + 64 * j, d, bar);
+                } else {
+                    copy_box(to_b, o.b, d, n, bar);
                 }
+                ++issued;
+                if (++stage == kStages) stage = 0, phase ^= 1;
             }
+        };
+        for (int64_t i = 0; ok && work.unit(i, &u); ++i) {
+            if (u.kind) copy(o1);
+            else copy(o0);
         }
+        next_stage = stage;
+        next_phase = phase;
     } else if (warp == 1) {
         if (rank == 0) {
             int stage = 0;
@@ -437,6 +433,21 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
     fence_before();
     __syncthreads();
     cluster_barrier();  // nothing of either CTA arrives at the other any more
+    if (waits.dead()) {
+        // After a wait that gave up: blocks may have been copied that no product waited for. Those of both CTAs count on the first one's
+        // barriers; what the second began beyond them is given the time.
+        if (warp == 0 && rank == 0) {
+            for (int j = 0; j < kStages && issued > 0; ++j, --issued) {
+                if (next_stage == 0) next_phase ^= 1;
+                next_stage = next_stage == 0 ? kStages - 1 : next_stage - 1;
+                mbar_wait_bounded(&s.full[next_stage], next_phase, kLateNs, lim.err);
+            }
+        }
+        const unsigned long long t0 = global_ns();
+        while (static_cast<long long>(global_ns() - t0) < kTestNs) __nanosleep(1000);
+        __syncthreads();
+        cluster_barrier();
+    }
     fence_after();
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(columns), "r"(kColumns) : "memory");
 }
