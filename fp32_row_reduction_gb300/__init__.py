@@ -886,7 +886,7 @@ def clip_global_norm(tensors, max_norm, kind="l2", eps=1e-6, out=None, norm_out=
 # ------------------------------------------------------------ the vocabulary's two ends
 
 def _rows_of(t, name):
-    """(pointer's tensor, rows, cols, device) of a contiguous CUDA matrix of a type the block norms take."""
+    """(rows, cols, device) of a contiguous CUDA matrix."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -905,11 +905,11 @@ def _indices(t, name, shape, index):
     return t.data_ptr()
 
 
-def _caller_workspace(workspace, nbytes, index):
+def _caller_workspace(workspace, nbytes, index, device):
     """(tensor, its bytes): the caller's, or a new one of `nbytes`."""
     import torch
     if workspace is None:
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=torch.device("cuda", index)), nbytes
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device), nbytes
     if not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
     return workspace, workspace.numel() * workspace.element_size()
@@ -970,7 +970,7 @@ def embedding_backward(dy, ids, vocab=None, scale=1.0, dtable=None, accumulate=F
         raise TypeError("dtable must have dy's type or be float32")
     vocab = dtable.shape[0]
     tokens = ids.numel()
-    ws, n = _caller_workspace(workspace, embedding_backward_workspace_bytes(tokens, c), index)
+    ws, n = _caller_workspace(workspace, embedding_backward_workspace_bytes(tokens, c), index, dy.device)
     _check(load().tr_embedding_backward(code, _dtype_code(gt), dy.data_ptr(), ip, _rows_like(dtable, "dtable", gt, (vocab, c), index),
                                         tokens, vocab, c, scale, 1 if accumulate else 0, _order(order), ws.data_ptr(), n,
                                         _current_stream()(index)), "embedding_backward")
@@ -1007,8 +1007,8 @@ def linear_cross_entropy(hidden, weight, labels, logit_scale=1.0, ignore_label=-
     code = _dtype_code(hidden.dtype)
     lp = _indices(labels, "labels", (r,), index)
     loss = torch.empty(r, dtype=torch.float32, device=hidden.device) if out is None else out
-    lse = torch.empty(r, dtype=torch.float32, device=hidden.device) if lse_out is None else lse_out
-    ws, n = _caller_workspace(workspace, _loss_workspace_bytes(r, c, v, 0), index)
+    lse = torch.empty_like(loss) if lse_out is None else lse_out
+    ws, n = _caller_workspace(workspace, _loss_workspace_bytes(r, c, v, 0), index, loss.device)
     _check(load().tr_linear_cross_entropy(
         code, hidden.data_ptr(), _rows_like(weight, "weight", hidden.dtype, (v, c), index), lp, _floats(loss, "out", (r,), index),
         _floats(lse, "lse_out", (r,), index), r, c, v, logit_scale, ignore_label, _order(order), ws.data_ptr(), n,
@@ -1036,7 +1036,7 @@ def linear_cross_entropy_backward(hidden, weight, labels, lse, dloss=None, dlse=
         dhidden = torch.empty_like(hidden)
     if dweight is None and want_dweight:
         dweight = torch.empty_like(weight)
-    ws, n = _caller_workspace(workspace, _loss_workspace_bytes(r, c, v, 1), index)
+    ws, n = _caller_workspace(workspace, _loss_workspace_bytes(r, c, v, 1), index, hidden.device)
     _check(load().tr_linear_cross_entropy_backward(
         code, hidden.data_ptr(), _rows_like(weight, "weight", dt, (v, c), index), lp, _floats(lse, "lse", (r,), index),
         _floats(dloss, "dloss", (r,), index), _floats(dlse, "dlse", (r,), index), _rows_like(dhidden, "dhidden", dt, (r, c), index),

@@ -189,6 +189,7 @@ __device__ __forceinline__ int64_t list_rows(const LossArgs& a, const Ws& w, int
     return count;
 }
 __global__ void __launch_bounds__(kScanThreads) rows_kernel(LossArgs a, Ws w, int backward) {
+    pdl_release();
     pdl_enter();
     list_rows<8>(a, w, backward, true, nullptr);
 }
@@ -242,6 +243,7 @@ struct Packing {
 template <class T, bool SMALL>
 __global__ void __launch_bounds__(SMALL ? kScanThreads : kThreads) pack_kernel(LossArgs a, Ws w, int backward, Packing<T> hidden, Packing<T> weight) {
     __shared__ int small_map[SMALL ? kScanThreads : 1];
+    pdl_release();
     pdl_enter();
     const int64_t count = SMALL ? list_rows<1>(a, w, backward, blockIdx.x == 0, small_map) : hidden.dst ? w.head->count : 0;
     const int64_t end = hidden.dst ? (count + mma::kDepth - 1) / mma::kDepth * mma::kDepth * hidden.chunks : 0;

@@ -68,11 +68,13 @@ __device__ __forceinline__ float ex2(float t) {
 // Programmatic dependent launch. Every kernel waits for the grids it depends
 // on (their memory operations complete and visible) before its first global
 // read or write; without a programmatic predecessor the wait returns at once.
-// No kernel signals its dependents early: the next launch on the stream is
+// The row kernels do not signal their dependents early: the next launch on the stream is
 // released as this grid's CTAs exit. An early signal lets the next grid's CTAs
 // take free slots and sit in their own wait while this grid still streams,
 // and in back-to-back launches at 768 x 6144 that cost about 1 us a launch.
 __device__ __forceinline__ void pdl_enter() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The early signal, for short launches before one with a long beginning, and at the end of long ones.
+__device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // m * log2(e) rounded on its own. __fmul_rn is never fused into a following
 // add, so mb_of(a) - mb_of(b) is exactly 0 when a == b; a plain a*L2E - mb

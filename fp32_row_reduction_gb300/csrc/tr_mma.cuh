@@ -358,6 +358,7 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
             if (u.kind) copy(o1);
             else copy(o0);
         }
+        pdl_release();
         next_stage = stage;
         next_phase = phase;
     } else if (warp == 1) {
