@@ -424,8 +424,8 @@ tr_status tr_global_norm_workspace_bytes(int64_t count, size_t* bytes);
  * tr_linear_cross_entropy: with logits[r, v] = logit_scale sum_c hidden[r, c] weight[v, c], which are formed tile
  * by tile and never kept, lse[r] = log(sum_v exp(logits[r, v])) and losses[r] = lse[r] - logits[r, labels[r]].
  * A label outside [0, vocab) selects 0, as in tr_cross_entropy_f32. A row whose label is ignore_label (-100 by
- * custom; any value, those inside the vocabulary too) has no loss: its losses and lse are 0, and its row of hidden is not looked
- * at, whatever it holds. hidden: rows x cols, weight: vocab x cols, both of `dtype`, TR_BF16 or TR_F16 (TR_F32:
+ * custom; any value, those inside the vocabulary too) has no loss: its losses and lse are 0, and its row of hidden counts for
+ * nothing, whatever it holds. hidden: rows x cols, weight: vocab x cols, both of `dtype`, TR_BF16 or TR_F16 (TR_F32:
  * TR_ERR_UNSUPPORTED); losses and lse: rows floats; lse may be NULL. Products are exact and summed
  * in binary32.
  *

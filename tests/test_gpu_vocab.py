@@ -413,6 +413,43 @@ def test_gradients_in_different_places(dtype, cols):
         assert bool((flat_w[:ow] == 7).all()) and bool((flat_w[ow + v * cols:] == 7).all())
 
 
+@pytest.mark.parametrize("rows,cols,v", [(37, 65, 700), (300, 72, 130), (1100, 136, 1000), (200, 64, 5003)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_nothing_is_taken_from_a_workspace(rows, cols, v, dtype):
+    """Workspaces and outputs that hold no numbers before the call; one workspace for calls of several sizes."""
+    hidden, weight, labels, dloss, dlse = loss_inputs(rows, cols, v, dtype, ignored=0.3)
+    ids = torch.randint(-1, v, (rows,), generator=gen(3), device=DEV)
+    want = check_loss(hidden, weight, labels, dloss, dlse)
+    n = max(tr.linear_cross_entropy_workspace_bytes(rows, cols, v, b) for b in (False, True))
+    ws = torch.empty(max(n, tr.embedding_backward_workspace_bytes(rows, cols)), dtype=torch.uint8, device=DEV)
+    half = rows // 2
+    few = check_loss(hidden[:half], weight, labels[:half], dloss[:half], dlse[:half])
+    clean = torch.nan_to_num(hidden)
+    table = tr.embedding_backward(clean, ids, v)
+    for part, expected in ((slice(None), want), (slice(half), few), (slice(None), want)):
+        ws.fill_(255)
+        h, l = hidden[part], labels[part]
+        out = torch.full((2, h.shape[0]), float("nan"), device=DEV)
+        tr.linear_cross_entropy(h, weight, l, out=out[0], lse_out=out[1], workspace=ws)
+        ws.fill_(255)
+        dh, dw = torch.full_like(h, float("nan")), torch.full_like(weight, float("nan"))
+        tr.linear_cross_entropy_backward(h, weight, l, out[1], dloss[part], dlse[part], dhidden=dh, dweight=dw, workspace=ws)
+        assert all(same(a, b) for a, b in zip((out[0], out[1], dh, dw), expected))
+        ws.fill_(255)
+        assert same(tr.embedding_backward(clean, ids, v, workspace=ws), table)
+
+
+def test_losses_alone():
+    """Without an lse to write."""
+    hidden, weight, labels, _, _ = loss_inputs(70, 64, 300, "f16", ignored=0.2)
+    losses, _ = tr.linear_cross_entropy(hidden, weight, labels)
+    n = tr.linear_cross_entropy_workspace_bytes(70, 64, 300)
+    ws, out = torch.empty(n, dtype=torch.uint8, device=DEV), torch.empty(70, device=DEV)
+    assert tr.load().tr_linear_cross_entropy(tr.TR_F16, hidden.data_ptr(), weight.data_ptr(), labels.data_ptr(), out.data_ptr(), None, 70, 64,
+                                             300, 1.0, IGNORE, 0, ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream) == tr.TR_OK
+    assert same(out, losses)
+
+
 # ---- streams, graphs, threads ---------------------------------------------------------------
 
 def test_other_streams():
