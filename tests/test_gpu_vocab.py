@@ -450,6 +450,59 @@ def test_losses_alone():
     assert same(out, losses)
 
 
+def test_tables_past_32_bits():
+    """Tables of more than 2^31 elements (4.4 GB): the rows at their ends."""
+    v, cols = 1_080_000, 2048
+    g = gen(12)
+    table = torch.empty(v, cols, device=DEV, dtype=torch.bfloat16)
+    table[:2000].normal_(generator=g)
+    table[-2000:].normal_(generator=g)
+    ends = torch.cat([torch.arange(2000, device=DEV), torch.arange(v - 2000, v, device=DEV)])
+    ids = ends[torch.randperm(4000, generator=g, device=DEV)]
+    assert torch.equal(tr.embedding(ids, table), table[ids])
+    dy = randn(g, (4000, cols), torch.bfloat16)
+    table.fill_(float("nan"))
+    tr.embedding_backward(dy, ids, dtable=table)
+    assert torch.equal(table[ids], dy)
+    middle = table[2000:-2000].view(torch.int16)  # zeros everywhere else
+    assert not any(bool(part.any()) for part in middle.split(100_000))
+
+
+@pytest.mark.parametrize("cols", [4096, 4095])
+def test_weights_past_32_bits(cols):
+    """A weight of more than 2^31 elements, the gradients of three rows of hidden: the loss, and dweight's rows at both ends."""
+    rows, v = 3, 530_000
+    g = gen(13)
+    weight = torch.empty(v, cols, device=DEV, dtype=torch.bfloat16)
+    for part in weight.split(50_000):
+        part.copy_(torch.randn(part.shape, generator=g, device=DEV) * (1.5 / cols ** 0.5))
+    hidden = randn(g, (rows, cols), torch.bfloat16)
+    labels = torch.tensor([v - 1, 0, v // 2], device=DEV)
+    losses, lse = tr.linear_cross_entropy(hidden, weight, labels)
+    z, e = zip(*(vocab.logits(hidden, part, 1.0) for part in weight.split(50_000)))
+    z, e = torch.cat(z, 1), torch.cat(e, 1)
+    want = torch.logsumexp(z, 1)
+    err = e.amax(1) + 2.0 ** -20 + (64 + v / 64) * vocab.U + 8 * vocab.U * (z.abs().amax(1) + want.abs())
+    close(lse, (want, err))
+    picked = z.gather(1, labels[:, None])[:, 0]
+    close(losses, (want - picked, err + e.gather(1, labels[:, None])[:, 0] + 8 * vocab.U * picked.abs()))
+    dh, dw = tr.linear_cross_entropy_backward(hidden, weight, labels, lse)
+    p = torch.exp(z - lse.double()[:, None])
+    p_err = p * (e + 8 * vocab.U * (z.abs() + lse.double().abs()[:, None]) + 2.0 ** -20) + 4 * vocab.U * p
+    p[torch.arange(rows, device=DEV), labels] -= 1.0
+    p_err = p_err + 2.0 ** -8 * (p.abs() + p_err)  # its rounding to bfloat16
+    h = hidden.double()
+    for at in (slice(0, 4000), slice(v // 2 - 10, v // 2 + 10), slice(v - 4000, v)):
+        q, qe = p[:, at], p_err[:, at]
+        close(dw[at], (q.T @ h, qe.T @ h.abs() + (rows + 8) * vocab.U * (q.abs().T @ h.abs())))
+    want_h, size, err_h = 0.0, 0.0, 0.0
+    for i, part in enumerate(weight.split(50_000)):
+        at = slice(50_000 * i, 50_000 * i + part.shape[0])
+        w = part.double()
+        want_h, size, err_h = want_h + p[:, at] @ w, size + p[:, at].abs() @ w.abs(), err_h + p_err[:, at] @ w.abs()
+    close(dh, (want_h, err_h + (v + 8) * vocab.U * size))
+
+
 # ---- streams, graphs, threads ---------------------------------------------------------------
 
 def test_other_streams():
