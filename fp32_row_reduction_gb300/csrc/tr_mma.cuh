@@ -361,6 +361,12 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
         pdl_release();
         next_stage = stage;
         next_phase = phase;
+        // Every product's arrival at `empty` reaches the shared memory of both CTAs, and those of the last blocks, which no later copy
+        // waits for, may come after that at `done`: each CTA waits for its own, as if kStages more blocks were to be copied, before either may end.
+        for (int j = 0; ok && j < kStages; ++j) {
+            ok = waits.wait(&s.empty[stage], phase ^ 1);
+            if (++stage == kStages) stage = 0, phase ^= 1;
+        }
     } else if (warp == 1) {
         if (rank == 0) {
             int stage = 0;
@@ -433,7 +439,7 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
     __syncwarp();
     fence_before();
     __syncthreads();
-    cluster_barrier();  // nothing of either CTA arrives at the other any more
+    cluster_barrier();  // with every wait ended well, nothing of either CTA arrives at the other any more
     if (waits.dead()) {
         // After a wait that gave up: blocks may have been copied that no product waited for. Those of both CTAs count on the first one's
         // barriers; what the second began beyond them is given the time.

@@ -549,6 +549,25 @@ def test_threads():
     assert not wrong
 
 
+@pytest.mark.parametrize("rows,cols,v", [(16, 64, 5003), (16, 400, 700), (300, 65, 2100)])
+def test_products_end_before_what_follows(rows, cols, v):
+    """Products of fewer blocks than the ring has stages, of as many and of more, each followed at once by kernels that begin early and use the
+    shared memory that the products had: all of the arrivals at a product's barriers come before it ends, so nothing of them is found there."""
+    hidden, weight, labels, dloss, dlse = loss_inputs(rows, cols, v, "bf16")
+    ids = torch.randint(0, v, (rows,), generator=gen(11), device=DEV)
+    want = (*check_loss(hidden, weight, labels, dloss, dlse), tr.embedding_backward(hidden, ids, v))
+    torch.cuda.synchronize()
+    out = []
+    for _ in range(100):
+        losses, lse = tr.linear_cross_entropy(hidden, weight, labels)
+        grads = tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse)
+        out.append((losses, lse, *grads, tr.embedding_backward(hidden, ids, v)))
+    torch.cuda.synchronize()
+    assert tr.tr_last_device_error() == tr.TR_OK
+    for got in out:
+        assert all(same(a, b) for a, b in zip(got, want))
+
+
 def test_graphs():
     """Captured once, replayed on other data; two graphs with a workspace each."""
     a, b = (loss_inputs(400, 136, 600, "bf16", seed=s, ignored=0.2 * s) for s in (0, 1))
