@@ -428,15 +428,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
                     label = l >= 0 && l < p.n ? static_cast<int>(l) : -1;
                 }
             }
-            if (!begun) {
-#pragma unroll
-                for (int c = 0; c < 128; c += 32)
-                    if (c < limit) mma::load_columns(at + first + c, z + c);
-            } else {
-#pragma unroll
-                for (int c = 0; c < 128; c += 8)
-                    if (c < limit) mma::add_columns(at + first + c, z + c);
-            }
+            mma::take_part(at + first, limit, begun, z);
             release();
             if (!whole) return;
             label = label >= u.n + first && label < u.n + first + limit ? label - u.n - first : -1;
@@ -446,58 +438,67 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
         });
 }
 
-// Backward: scale dz / logit_scale of a piece, rounded. Rows and words beyond the last are zeros up to the tile's end.
+// Backward: scale dz / logit_scale of a piece, rounded. The logits are summed in the forward pass's parts, so that they are the very numbers that the
+// lse was formed from: a row whose label has all of the probability has a dz of 0, not of the error of a sum. Rows and words beyond the last are zeros up to the tile's end.
 template <class T>
 __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     probs_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap weight, const __grid_constant__ CUtensorMap out,
                  const __grid_constant__ Product p) {
     int64_t count = 0;
-    float times = 0.0f;
+    float times = 0.0f, z[128];
     const mma::Operands<false, false> o{&hidden, &weight};
-    mma::run<0>(
+    mma::run<kPart>(
         o, o, p.boxes, kTypeBits<T>, p.lim,
         [&] {
             count = p.w.head->count;
             times = p.w.head->scale;
             return mma::Work(p.width, mma::Tiles{tiles_of(count, kTileRows), tiles_of(p.n, p.width), 1, tiles_of(p.cols, mma::kDepth)});
         },
-        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, const mma::OutBox& box, bool, bool, auto&& release) {
+        [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, const mma::OutBox& box, bool begun, bool whole, auto&& release) {
             // rows that are not there are read as the depth of the weight's gradient up to the end of a block
             const int row0 = row - static_cast<int>(threadIdx.x & 31);
             if (row0 >= (count + mma::kDepth - 1) / mma::kDepth * mma::kDepth) return release();
             const bool in = row < count;
-            const int limit = static_cast<int>(min(static_cast<int64_t>(last), p.n - u.n));
-            const float lse = in ? p.w.lse[row] : 0.0f, coef = in ? p.w.coef[row] * times : 0.0f;
-            const float onehot = in ? p.w.onehot[row] * times : 0.0f;
-            const int word = in ? p.w.labels[row] : -1;
-            const int label = word >= 0 ? static_cast<int>(word - p.first) - u.n : -1;
+            const int limit = static_cast<int>(min(static_cast<int64_t>(last), p.n - u.n)) - first;
+            float lse = 0.0f, coef = 0.0f, onehot = 0.0f;
+            int word = -1;
+            if (whole && in) {  // (asked for early, as above)
+                lse = p.w.lse[row];
+                coef = p.w.coef[row] * times;
+                onehot = p.w.onehot[row] * times;
+                word = p.w.labels[row];
+            }
+            mma::take_part(at + first, last - first, begun, z);
+            release();
+            if (!whole) return;
+            const int label = word >= 0 ? static_cast<int>(word - p.first) - u.n - first : -1;
             const bool boxed = (last - first) % 64 == 0;
-            for (int c = first; c < last; c += 32) {
-                float z[32];
-                mma::load_columns(at + c, z);
-                if (!ok) spoil(z);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) z[i] = coef * ex2(fmaf(z[i], p.scale, -lse));
+            for (int c = 0; c < 128; c += 32) {
+                if (c >= last - first) continue;
+                float(&v)[32] = *reinterpret_cast<float(*)[32]>(z + c);
+                if (!ok) spoil(v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = coef * ex2(fmaf(v[i], p.scale, -lse));
                 if (label >= c && label < c + 32) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (label == c + i) z[i] -= onehot;
+                        if (label == c + i) v[i] -= onehot;
                 }
                 if (!in || c + 32 > limit) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (!in || c + i >= limit) z[i] = 0.0f;
+                        if (!in || c + i >= limit) v[i] = 0.0f;
                 }
                 if (boxed) {
-                    const int h = (c - first) / 32 & 1;
+                    const int h = c / 32 & 1;
                     if (h == 0) box.clear();
-                    box_columns<T>(box, h, z);
-                    if (h == 1) box.send(&out, u.n + c - 32, row0);
+                    box_columns<T>(box, h, v);
+                    if (h == 1) box.send(&out, u.n + first + c - 32, row0);
                 } else {
-                    store_columns<T>(static_cast<T*>(p.to) + row * p.pitch + u.n, c, last, z);
+                    store_columns<T>(static_cast<T*>(p.to) + row * p.pitch + u.n + first, c, last - first, v);
                 }
             }
-            release();
         });
 }
 

@@ -115,6 +115,19 @@ __device__ __forceinline__ void add_columns(uint32_t addr, float* v) {
     for (int i = 0; i < 8; ++i) v[i] += __uint_as_float(r[i]);
 }
 
+// The first n of (up to) 128 columns of one part of a tile's depth, taken to registers: the first part's as they are, a later one's added.
+__device__ __forceinline__ void take_part(uint32_t addr, int n, bool begun, float (&sum)[128]) {
+    if (!begun) {
+#pragma unroll
+        for (int c = 0; c < 128; c += 32)
+            if (c < n) load_columns(addr + c, sum + c);
+    } else {
+#pragma unroll
+        for (int c = 0; c < 128; c += 8)
+            if (c < n) add_columns(addr + c, sum + c);
+    }
+}
+
 // An output warp's room: 32 rows of 128 bytes in a 128-byte swizzle, on their way to a box of a tensor map.
 struct OutBox {
     uint32_t at;

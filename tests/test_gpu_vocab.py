@@ -286,6 +286,41 @@ def test_certain_rows():
     close(dw, want_w)
 
 
+PART_STEPS = 64  # the logits are summed in parts of 1024 of the depth, a part in steps of 16
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,cols", [(40, 32768), (300, 16392)])
+def test_certain_rows_of_long_sums(rows, cols, dtype):
+    """The label's logit is a sum of many positive products, and the label has all of the probability but 1e-11.
+
+    A step of a part rounds its sum toward zero, by less than 2^-23 of it, and the sum is at most the part's: the parts are
+    off by PART_STEPS 2^-23 of themselves, their sum by a rounding (u) for each part more. That is e, 3e-4 for a logit of 30. One
+    sum over the whole depth would be off by 2048 such steps (at half of the final sum on average: 1e-3 and more for a logit of 30). The
+    gradient's logits are the forward pass's own, bit for bit, so with the lse of that pass dz does not have that error: what is left are
+    the roundings of z, of lse, of their products with log2(e) and ln 2 and of 2^x: 8 u (|z| + |lse|) + 2^-20."""
+    g, dt, v = gen(cols), DTYPES[dtype], 300
+    hidden = (0.5 + torch.rand(rows, cols, generator=g, device=DEV)).to(dt)
+    weight = torch.zeros(v, cols, device=DEV, dtype=dt)
+    weight[3] = (30.0 / cols * (0.5 + torch.rand(cols, generator=g, device=DEV))).to(dt)
+    labels = torch.full((rows,), 3, device=DEV)
+    h, w = hidden.double(), weight[3].double()
+    z = h @ w
+    exact = z + torch.log1p((v - 1) * torch.exp(-z))
+    e = (PART_STEPS * 2.0 ** -23 + cols / 1024 * vocab.U) * z
+    rest = 8 * vocab.U * (z + exact) + 2.0 ** -20
+    losses, lse = tr.linear_cross_entropy(hidden, weight, labels)
+    assert bool(((lse.double() - exact).abs() <= e + rest).all())
+    assert bool((losses.double() <= 2.0 ** -20).all())
+    # dz rounded to the type (T, and 2^-25 of float16's 2^-14), then the outputs
+    t, tiny = vocab.HALF_STEP[dt]
+    for given, off in ((lse, rest), (exact.float(), e + rest)):
+        dh, dw = tr.linear_cross_entropy_backward(hidden, weight, labels, given)
+        dz = off * (1 + t) + tiny * 2.0 ** -14 + torch.exp(-z) * v  # what dz may be: it is nearly 0 itself
+        assert bool((dw[3].double().abs() <= (dz @ h) * (1 + 2 * t) + tiny).all())
+        assert bool((dh.double().abs() <= dz[:, None] * w * (1 + 2 * t) + tiny).all())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_not_finite(dtype):
     """A row that holds no numbers spoils its own loss, and the gradients it is part of, and no other row's."""
