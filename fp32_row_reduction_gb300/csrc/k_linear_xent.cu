@@ -24,6 +24,11 @@
 namespace tr {
 
 constexpr int kPairs = 76;  // CTA pairs of the GPU that the plan is made for
+// Blocks of the depth (the piece's words, or the rows) that the gradients are summed over in tensor memory, which rounds toward zero: 131072
+// words in one sum came out 2.5e-4 too small, as much as float16's last rounding; parts of 8192 are 2e-5. Longer depths are split
+// where they are split anyway, or their parts are added in registers by a kernel of its own (8192 x 4096 x 50257 takes 1.5% longer in parts, 3% in
+// parts of 4096; the registers would cost 64 x 2047 x 30000, whose depths are one part each, 215 us instead of 178).
+constexpr int kGradPart = 128;
 
 LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
     size_t at = 0;
@@ -53,6 +58,8 @@ LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
     // Few tiles of the hidden gradient have their depth, the piece's words, split over the pairs.
     const int64_t grad_tiles = row_tiles * ceil_div(cols, grad_width);
     splits = static_cast<int>(std::max<int64_t>(1, std::min(kPairs / grad_tiles, piece / (4 * mma::kDepth))));
+    if (splits > 1) splits = static_cast<int>(std::max<int64_t>(splits, ceil_div(piece, kGradPart * mma::kDepth)));
+    parted = std::max(splits > 1 ? 0 : piece, rows_pad) > kGradPart * mma::kDepth;
     parts = 2 * ceil_div(vocab, width);
     head = take(sizeof(LossHead));
     map = take(rows_pad * 4);
@@ -410,7 +417,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     int64_t count = 0;
     float z[128];
     const mma::Operands<false, false> o{&hidden, &weight};
-    mma::run<kPart>(
+    mma::run<kPart, false>(
         o, o, p.boxes, kTypeBits<T>, p.lim,
         [&] {
             count = p.w.map ? p.w.head->count : p.rows;
@@ -447,7 +454,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     int64_t count = 0;
     float times = 0.0f, z[128];
     const mma::Operands<false, false> o{&hidden, &weight};
-    mma::run<kPart>(
+    mma::run<kPart, false>(
         o, o, p.boxes, kTypeBits<T>, p.lim,
         [&] {
             count = p.w.head->count;
@@ -572,13 +579,13 @@ __device__ __forceinline__ void weight_part(const Product& p, const CUtensorMap*
         }
     }
 }
-template <class T>
+template <class T, int PART>
 __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     grads_kernel(const __grid_constant__ CUtensorMap probs_rows, const __grid_constant__ CUtensorMap weight, const __grid_constant__ CUtensorMap probs_cols,
                  const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap dweight_out, const __grid_constant__ Product p) {
     int64_t count = 0;
     float times = 0.0f;
-    mma::run<0>(
+    mma::run<PART, true>(
         mma::Operands<false, true>{&probs_rows, &weight}, mma::Operands<true, true>{&probs_cols, &hidden}, p.boxes, kTypeBits<T>, p.lim,
         [&] {
             count = p.w.head->count;
@@ -796,7 +803,8 @@ cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
         d.wide = align && reinterpret_cast<uintptr_t>(a.dhidden) % 16 == 0;
         d.dweight_wide = dweight_wide;
         const int64_t units = (a.dhidden ? row_tiles * across * p.splits : 0) + (a.dweight ? ceil_div(n, kTileRows) * across : 0);
-        e = launch_product(grads_kernel<T>, units, stream, probs_rows, weight_cols, probs_cols, hidden_cols, dweight_out, d);
+        const auto kernel = p.parted ? grads_kernel<T, kGradPart> : grads_kernel<T, 0>;
+        e = launch_product(kernel, units, stream, probs_rows, weight_cols, probs_cols, hidden_cols, dweight_out, d);
     }
     if (e != cudaSuccess || !a.dhidden || p.splits == 1) return e;
     const int64_t ctas = std::min<int64_t>(ceil_div(a.rows * a.cols, kThreads), 1 << 16);

@@ -115,19 +115,33 @@ __device__ __forceinline__ void add_columns(uint32_t addr, float* v) {
     for (int i = 0; i < 8; ++i) v[i] += __uint_as_float(r[i]);
 }
 
-// The first n of (up to) 128 columns of one part of a tile's depth, taken to registers: the first part's as they are, a later one's added.
+// A part's first n of (up to) 128 columns added to sums in registers.
+__device__ __forceinline__ void add_part(uint32_t addr, int n, float (&sum)[128]) {
+#pragma unroll
+    for (int c = 0; c < 128; c += 8)
+        if (c < n) add_columns(addr + c, sum + c);
+}
+// The same where the first part is taken as it is.
 __device__ __forceinline__ void take_part(uint32_t addr, int n, bool begun, float (&sum)[128]) {
-    if (!begun) {
+    if (begun) return add_part(addr, n, sum);
 #pragma unroll
-        for (int c = 0; c < 128; c += 32)
-            if (c < n) load_columns(addr + c, sum + c);
-    } else {
-#pragma unroll
-        for (int c = 0; c < 128; c += 8)
-            if (c < n) add_columns(addr + c, sum + c);
-    }
+    for (int c = 0; c < 128; c += 32)
+        if (c < n) load_columns(addr + c, sum + c);
 }
 
+// 32 columns of this warp's 32 rows, written.
+__device__ __forceinline__ void put_columns(uint32_t addr, const float* v) {
+    __syncwarp();
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
+        "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]),
+        "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]),
+        "f"(v[31])
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
 // An output warp's room: 32 rows of 128 bytes in a 128-byte swizzle, on their way to a box of a tensor map.
 struct OutBox {
     uint32_t at;
@@ -222,6 +236,27 @@ struct Waits {
     }
 };
 
+// An output warp's next tile, or part of one: its place in tensor memory, and how often that place was used.
+struct Slot {
+    uint32_t number = 0, phase = 0;
+    // waits for it; false: after a wait that gave up
+    __device__ __forceinline__ bool arrived(const Waits& w) const {
+        const bool ok = w.wait(&w.s.done[number], phase) && !__any_sync(kFull, w.dead());
+        fence_after();
+        return ok;
+    }
+    // this warp's rows
+    __device__ __forceinline__ uint32_t columns(uint32_t all) const { return all + number * kMaxWidth + (threadIdx.x >> 5 & 3) * (32u << 16); }
+    // gives the place back
+    __device__ __forceinline__ void release(const Waits& w) const {
+        fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) arrive_in(in_cta(smem_addr(&w.s.room[number]), 0));
+    }
+    __device__ __forceinline__ void next() {
+        if (++number == 2) number = 0, phase ^= 1;
+    }
+};
 // a / b of numbers that are nearly always below 2^32 (a division of 64 bits takes several times as long).
 __device__ __forceinline__ int64_t over(int64_t a, int64_t b) {
     return (a | b) >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
@@ -283,12 +318,13 @@ struct Work {
 };
 
 // The products of a CTA pair: plan() gives the work, once what earlier kernels wrote can be read; o0 and o1 are the operands of the two
-// kinds. The sums of a tile come in one part, or (CHUNK > 0) in a part for every CHUNK blocks of the depth, for the caller to add: the
-// tensor cores round their sums toward zero, an error that grows with the length of a sum. out(unit, row, half, first, last,
+// kinds. The sums of a tile come in one part, or (CHUNK > 0) in a part for every CHUNK blocks of the depth: the
+// tensor cores round their sums toward zero, an error that grows with the length of a sum. JOIN: the parts are added in registers and put
+// back into tensor memory, as if there had been one; otherwise the caller is given one after another. out(unit, row, half, first, last,
 // tensor address, ok, box, begun, whole, release) takes the columns [first, last) of one row a lane, and calls release() when it has
 // read the tensor memory; ok: the sums are there (false: after a wait that gave up); box: the warp's room in
 // shared memory; begun: earlier parts have come; whole: the last one.
-template <int CHUNK, class O0, class O1, class Plan, class Out>
+template <int CHUNK, bool JOIN, class O0, class O1, class Plan, class Out>
 __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& boxes, uint32_t type_bits, const Limits& lim, Plan&& plan, Out&& out) {
     extern __shared__ __align__(16) char raw[];
     __shared__ Shared s;
@@ -429,23 +465,34 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const int first = half * (width / 2), last = half ? width : width / 2;
         const OutBox box{base + kStages * kStageBytes + (warp - 2) * kOutBytes};
-        uint32_t slot = 0, slot_phase = 0;
+        Slot slot;
         Unit u;
         for (int64_t i = 0; work.unit(i, &u); ++i) {
+            const int row = u.m + static_cast<int>(rank) * kRows + quarter * 32 + lane;
             int k = u.begin;
+            bool ok = true;
+            if (JOIN && CHUNK > 0 && u.end - k > CHUNK) {
+                float sum[128];
+#pragma unroll
+                for (int c = 0; c < 128; ++c) sum[c] = 0.0f;
+                for (;; k += CHUNK) {
+                    ok = slot.arrived(waits) && ok;
+                    add_part(slot.columns(columns) + first, last - first, sum);
+                    if (u.end - k <= CHUNK) break;
+                    slot.release(waits);
+                    slot.next();
+                }
+#pragma unroll
+                for (int c = 0; c < 128; c += 32)
+                    if (c < last - first) put_columns(slot.columns(columns) + first + c, sum + c);
+            }
             do {
-                const bool begun = k > u.begin;
+                const bool begun = !JOIN && k > u.begin;
                 k = CHUNK > 0 ? min(k + CHUNK, u.end) : u.end;
-                const bool ok = waits.wait(&s.done[slot], slot_phase) && !__any_sync(kFull, waits.dead());
-                fence_after();
-                const uint32_t at = columns + slot * kMaxWidth + (static_cast<uint32_t>(quarter * 32) << 16);
-                out(u, u.m + static_cast<int>(rank) * kRows + quarter * 32 + lane, half, first, last, at, ok, box, begun, k >= u.end, [&] {
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_in(in_cta(smem_addr(&s.room[slot]), 0));
-                });
-                if (++slot == 2) slot = 0, slot_phase ^= 1;
-            } while (k < u.end);
+                ok = slot.arrived(waits) && ok;
+                out(u, row, half, first, last, slot.columns(columns), ok, box, begun, JOIN || k >= u.end, [&] { slot.release(waits); });
+                slot.next();
+            } while (!JOIN && k < u.end);
         }
         OutBox::finish();
     }

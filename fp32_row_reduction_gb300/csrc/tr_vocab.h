@@ -80,6 +80,7 @@ struct LossPlan {
     int width;         // words of a tile of logits
     int grad_width;    // columns of a tile of the gradients
     int splits;        // of the depth of the hidden gradient
+    bool parted;       // whether a depth of the gradients is summed in parts
     size_t head, map, labels, lse, coef, onehot, hidden, weight, parts_at, picked, probs, sums, bytes;
     bool pack_weight;  // rows of the weight that do not start on 16 bytes are copied to ones that do
     LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward);

@@ -321,6 +321,58 @@ def test_certain_rows_of_long_sums(rows, cols, dtype):
         assert bool((dh.double().abs() <= dz[:, None] * w * (1 + 2 * t) + tiny).all())
 
 
+GRAD_STEPS = 512  # the gradients are summed in parts of at most 8192 of the depth, a part in steps of 16
+
+
+def signed_error(got, want):
+    """(mean of the signed relative errors, what it may be). A step of a part rounds its sum toward zero, by less than 2^-23 of it, and where one
+    large term comes first the sum is about the final one all the way: GRAD_STEPS 2^-23, 6e-5. The roundings to float16, at most
+    2^-11 each to either side, leave a mean of n of them off by more than 2^-11 sqrt(57 / n) once in 10^12 (Hoeffding's inequality). One sum
+    over 8192 steps is 2.5e-4 too small."""
+    off = float(((got.double() - want) / want).mean())
+    return off, GRAD_STEPS * 2.0 ** -23 + 2.0 ** -11 * (57.0 / want.numel()) ** 0.5
+
+
+def test_a_hidden_gradient_of_many_words():
+    """Even probabilities, 2^-17 each, so that all of dz is exact; the label's word, one of the first, gives nearly all of the gradient."""
+    rows, cols, v = 1024, 2560, 1 << 17
+    g = gen(21)
+    hidden = torch.zeros(rows, cols, device=DEV, dtype=torch.float16)
+    weight = torch.empty(v, cols, device=DEV, dtype=torch.float16)
+    for part in weight.split(1 << 14):
+        u = torch.rand(part.shape, generator=g, device=DEV) - 0.5
+        part.copy_(u + 0.5 * torch.sign(u))
+    weight.masked_fill_(weight == 0, 0.5)
+    labels = torch.arange(rows, device=DEV)
+    lse = torch.full((rows,), float(torch.log(torch.tensor(float(v), dtype=torch.float64))), device=DEV)
+    dh, _ = tr.linear_cross_entropy_backward(hidden, weight, labels, lse, want_dweight=False)
+    want = weight.sum(0, dtype=torch.float64) / v - weight[:rows].double()
+    off, most = signed_error(dh, want)
+    assert abs(off) <= most, (off, most)
+
+
+def test_a_weight_gradient_of_many_rows():
+    """Logits of 0, so that all of dz is exact; the first row gives nearly all of the gradient, and is so large that the others' products do not end
+    within the bits of the sum."""
+    rows, cols, v = 1 << 17, 2048, 16
+    g = gen(22)
+    weight = torch.zeros(v, cols, device=DEV, dtype=torch.float16)
+    hidden = torch.empty(rows, cols, device=DEV, dtype=torch.float16)
+    for part in hidden.split(1 << 14):
+        part.copy_(2.0 ** -12 * torch.randn(part.shape, generator=g, device=DEV))
+    hidden[0] = (8 + 8 * torch.rand(cols, generator=g, device=DEV)).half()
+    labels = torch.full((rows,), 5, device=DEV)
+    labels[0] = 3
+    lse = torch.full((rows,), float(torch.log(torch.tensor(float(v), dtype=torch.float64))), device=DEV)
+    _, dw = tr.linear_cross_entropy_backward(hidden, weight, labels, lse, want_dhidden=False)
+    first = hidden[0].double()
+    want = (hidden.sum(0, dtype=torch.float64) / v).repeat(v, 1)
+    want[3] -= first
+    keep = torch.arange(v, device=DEV) != 5  # (the sums of that word are of all the other rows)
+    off, most = signed_error(dw[keep], want[keep])
+    assert abs(off) <= most, (off, most)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_not_finite(dtype):
     """A row that holds no numbers spoils its own loss, and the gradients it is part of, and no other row's."""
@@ -740,3 +792,17 @@ def test_waits_that_give_up(hook, rows, cols, v):
     hook(0)
     assert all(same(a, b) for a, b in zip(both(), want))
     assert tr.tr_last_device_error() == tr.TR_OK
+
+
+def test_waits_that_give_up_in_parts(hook):
+    """The same where the weight's gradient is summed in parts."""
+    hidden, weight, labels, dloss, dlse = loss_inputs(8300, 40, 300, "bf16", ignored=0.0)
+    losses, lse, dh, dw = check_loss(hidden, weight, labels, dloss, dlse)
+    for mode in (1, 2, 0):
+        hook(mode)
+        got = tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse)
+        assert tr.tr_last_device_error() == (tr.TR_ERR_DEVICE_TIMEOUT if mode else tr.TR_OK)
+        if mode == 2:
+            assert all(bool(torch.isnan(t).all()) for t in got)
+        else:
+            assert same(got[0], dh) and same(got[1], dw)
