@@ -41,23 +41,25 @@ LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
     pitch = round_up(cols, 8);
     pack_weight = cols % 8 != 0;
     // dz of a piece: 2^27 values (256 MB), and at least 4096 columns, so that the sums over the pieces cost little
-    const int64_t most = std::max<int64_t>(4096, (int64_t{1} << 27) / rows_pad / 256 * 256);
-    const int64_t pieces = ceil_div(vocab, std::min(most, round_up(vocab, 256)));
+    constexpr int64_t kValues = int64_t{1} << 27, kLeast = 4096;
+    const int64_t words = round_up(vocab, 256), most = std::max(kLeast, kValues / rows_pad / 256 * 256);
+    const int64_t pieces = ceil_div(vocab, std::min(most, words));
     piece = round_up(ceil_div(vocab, pieces), 256);
     // The width whose tiles come out even over the pairs of a GPU's CTAs. A narrow tile reads the rows of hidden more often (the
     // 24), which a single tile of rows does not feel in the forward pass: there a narrower tile only splits the weight's reading more
     // evenly. Backward, the tiles fill whole multiples of 256 words.
     width = mma::kMaxWidth;
     grad_width = cols > 128 ? mma::kMaxWidth : 128;  // (half as wide a tile takes half as long)
+    constexpr int kRead = 24;
     const int64_t row_tiles = rows_pad / kTileRows;
     int64_t least = INT64_MAX;
     for (int n = mma::kMaxWidth; n >= 64; n = backward ? n / 2 : n - 32) {
-        const int64_t cost = ceil_div(row_tiles * ceil_div(backward ? piece : vocab, n), kPairs) * (n + (backward || row_tiles > 1 ? 24 : 0));
+        const int64_t cost = ceil_div(row_tiles * ceil_div(backward ? piece : vocab, n), kPairs) * (n + (backward || row_tiles > 1 ? kRead : 0));
         if (cost < least) least = cost, width = n;
     }
     // Few tiles of the hidden gradient have their depth, the piece's words, split over the pairs.
-    const int64_t grad_tiles = row_tiles * ceil_div(cols, grad_width);
-    splits = static_cast<int>(std::max<int64_t>(1, std::min(kPairs / grad_tiles, piece / (4 * mma::kDepth))));
+    const int64_t across = ceil_div(cols, grad_width);
+    splits = static_cast<int>(std::max<int64_t>(1, std::min(kPairs / (row_tiles * across), piece / (4 * mma::kDepth))));
     if (splits > 1) splits = static_cast<int>(std::max<int64_t>(splits, ceil_div(piece, kGradPart * mma::kDepth)));
     parted = std::max(splits > 1 ? 0 : piece, rows_pad) > kGradPart * mma::kDepth;
     parts = 2 * ceil_div(vocab, width);
@@ -67,14 +69,32 @@ LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
     hidden = take(rows_pad * pitch * 2);
     weight = pack_weight ? take(vocab * pitch * 2) : at;
     lse = coef = onehot = probs = sums = parts_at = picked = at;
+    // Fewer rows have longer pieces, more splits or narrower tiles, so that they may use more of what follows. It is as large as any call of no more
+    // rows needs it: a workspace for the longest batch is one for all shorter ones.
     if (backward) {
         lse = take(rows_pad * 4);
         coef = take(rows_pad * 4);
         onehot = take(rows_pad * 4);
-        probs = take(rows_pad * piece * 2);
-        sums = take(splits * rows_pad * pitch * 4);
+        // rows_pad piece <= rows_pad min(words, max(kLeast, kValues / rows_pad))
+        probs = take(2 * std::max(rows_pad * piece, std::min(rows_pad * words, std::max(rows_pad * kLeast, kValues))));
+        // splits row_tiles, in row tiles: with no more than `split` of those the depth is split, into at most words / 256 parts and no more than
+        // fill the pairs or than there are parts of kGradPart
+        const int64_t split = std::min(row_tiles, kPairs / 2 / across);
+        const int64_t tiles = std::min(split * (words / 256), std::max(kPairs / across, split * ceil_div(words, kGradPart * mma::kDepth)));
+        sums = take(4 * pitch * kTileRows * std::max({splits * row_tiles, row_tiles, tiles}));
     } else {
-        parts_at = take(parts * rows_pad * 8);
+        // A width n is taken only where ceil(row_tiles t(n) / kPairs) (n + kRead) <= that of every other m, t the tiles across, for which
+        // row_tiles (t(n) (n + kRead) - t(m) (m + kRead)) < kPairs (m + kRead) has to hold; or for a single tile of rows.
+        int64_t tiles = 0;
+        for (int n = 64; n <= mma::kMaxWidth; n += 32) {
+            int64_t last = row_tiles;
+            for (int m = 64; m <= mma::kMaxWidth; m += 32) {
+                const int64_t more = ceil_div(vocab, n) * (n + kRead) - ceil_div(vocab, m) * (m + kRead);
+                if (more > 0) last = std::min(last, (kPairs * (m + kRead) - 1) / more);
+            }
+            tiles = std::max(tiles, ceil_div(vocab, n) * std::max<int64_t>(last, 1));
+        }
+        parts_at = take(16 * kTileRows * std::max(tiles, parts / 2 * row_tiles));
         picked = take(rows_pad * 4);
     }
     bytes = rows > 0 ? at : 0;

@@ -461,7 +461,8 @@ tr_status tr_linear_cross_entropy_backward(tr_dtype dtype, const void* hidden, c
                                            const float* dlse, void* dhidden, void* dweight, int64_t rows, int64_t cols,
                                            int64_t vocab, float logit_scale, int64_t ignore_label, tr_order order,
                                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
-/* backward: 0 for tr_linear_cross_entropy, 1 for its backward pass. */
+/* backward: 0 for tr_linear_cross_entropy, 1 for its backward pass. The size never falls as rows grow, so that a workspace for the longest
+ * batch is one for shorter ones of the same cols and vocab. */
 tr_status tr_linear_cross_entropy_workspace_bytes(int64_t rows, int64_t cols, int64_t vocab, int32_t backward,
                                                   size_t* bytes);
 

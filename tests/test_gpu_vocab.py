@@ -526,6 +526,19 @@ def test_nothing_is_taken_from_a_workspace(rows, cols, v, dtype):
         assert same(tr.embedding_backward(clean, ids, v, workspace=ws), table)
 
 
+def test_a_workspace_of_a_longer_batch():
+    """512 rows, whose pieces of the vocabulary are longer than those of 768, in the workspace of 768."""
+    rows, cols, v = 512, 512, 250_000
+    hidden, weight, labels, dloss, dlse = loss_inputs(rows, cols, v, "bf16")
+    losses, lse = tr.linear_cross_entropy(hidden, weight, labels)
+    want = tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse)
+    n = tr.linear_cross_entropy_workspace_bytes(768, cols, v, True)
+    ws = torch.full((n + 4096,), 77, dtype=torch.uint8, device=DEV)
+    got = tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse, workspace=ws[:n])
+    assert all(same(a, b) for a, b in zip(got, want))
+    assert bool((ws[n:] == 77).all())
+
+
 def test_losses_alone():
     """Without an lse to write."""
     hidden, weight, labels, _, _ = loss_inputs(70, 64, 300, "f16", ignored=0.2)

@@ -111,6 +111,17 @@ def test_workspace_bytes(lib):
     assert sizes == sorted(sizes)
 
 
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("v", [16, 300, 5003, 30000, 50257, 131072, 250000, 1100000])
+@pytest.mark.parametrize("cols", [64, 136, 512, 2561, 4096, 20000])
+def test_a_workspace_for_the_longest_batch_is_one_for_all(lib, cols, v, backward):
+    """Sizes never fall as rows grow, for every number of tiles of 256 rows up to 40000 and some beyond."""
+    rows = [1, 255, *range(256, 40000, 256), *(256 * 3 ** k for k in range(5, 13)), *(256 * 3 ** k + 1 for k in range(5, 13)), (1 << 31) - 1024]
+    rows.sort()
+    sizes = [tr.linear_cross_entropy_workspace_bytes(r, cols, v, backward) for r in rows]
+    assert sizes == sorted(sizes)
+
+
 def test_tensors_that_are_refused(lib):
     ids = torch.zeros(3, dtype=torch.int64)
     with pytest.raises(TypeError):
