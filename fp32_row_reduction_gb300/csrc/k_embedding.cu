@@ -595,8 +595,8 @@ __device__ __forceinline__ void write_row(const EmbedGradArgs& a, uint32_t key, 
         for (int k = 0; k < N; ++k) {
             const int i = 32 * k + lane;
             if (c0 + i >= a.cols) continue;
-            const float v = a.scale * turn[i / N * (N + 1) + i % N];
-            row[c0 + i] = from_float<G>(a.accumulate ? to_float(row[c0 + i]) + v : v);
+            const float v = turn[i / N * (N + 1) + i % N];
+            row[c0 + i] = from_float<G>(a.accumulate ? fmaf(a.scale, v, to_float(row[c0 + i])) : a.scale * v);
         }
     }
 }

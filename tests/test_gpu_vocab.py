@@ -158,6 +158,27 @@ def test_embedding_backward_alignments(offset, dtype):
     assert same(dtable, tr.embedding_backward(dy.clone(), ids, 90))  # whatever the alignment
 
 
+@pytest.mark.parametrize("dtype,grad", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f16", "f32")])
+def test_adding_to_a_table_rounds_once(dtype, grad):
+    """base + scale sum is one rounding of binary32 (and one of the type), whatever the alignment: the bits are the same."""
+    g, dt, gt = gen(14), DTYPES[dtype], DTYPES[grad]
+    dy, base = randn(g, (900, 64), dt), randn(g, (70, 64), gt)
+    ids = token_ids(g, 900, 70, "runs")
+    want = base.clone()
+    tr.embedding_backward(dy, ids, scale=0.7, dtable=want, accumulate=True)
+    for offset in (1, 4):
+        flat = torch.empty(70 * 64 + offset, device=DEV, dtype=gt)
+        table = flat[offset:].view(70, 64)
+        table.copy_(base)
+        tr.embedding_backward(dy, ids, scale=0.7, dtable=table, accumulate=True)
+        assert same(table, want)
+    # a single token's sum is its row: its product with the scale is exact in float64, whose sum is rounded far below binary32
+    one = base.float().clone()
+    tr.embedding_backward(dy[:1], ids[:1], scale=0.7, dtable=one, accumulate=True)
+    exact = base[ids[0]].double() + vocab.f32(0.7) * dy[0].double()
+    assert torch.equal(one[ids[0]], exact.float())
+
+
 def test_embedding_backward_arguments():
     g = gen(0)
     dy, ids = randn(g, (4, 6, 16), torch.float16), torch.randint(0, 9, (4, 6), generator=g, device=DEV)
