@@ -5,7 +5,9 @@
 // is no difference of large numbers. Backward, for one piece of the vocabulary after another:
 // dz = (dloss + dlse) 2^(z - lse) - dloss [label], rounded to the inputs' type for the products dhidden += dz weight
 // (in float32 over the pieces) and dweight = dz^T hidden. The rounding is one of T's half steps of each dz, relative to a dz that has
-// the label's -1 in it already; products of an unrounded dz would be two or three of its parts.
+// the label's -1 in it already; it adds as much as a third to the outputs' error (bf16 201 x 320 x 136: 2.2e-3 instead of 1.7e-3). Where the products are
+// short, dz is taken in two terms of T, the second what the first one's rounding left, and nothing is added. That costs
+// 2 to 5 us (37 x 1537 x 5003 f16 48.0 us instead of 44.7); for 8192 x 4096 x 50257 it would be 9.5 ms instead of 5.5.
 //
 // Rows that have a loss are packed first: the products do no work for the others, and what those hold, which may be no
 // number, is not read as the depth of the weight's gradient.
@@ -40,28 +42,36 @@ LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
     rows_pad = round_up(rows, kTileRows);
     pitch = round_up(cols, 8);
     pack_weight = cols % 8 != 0;
+    const int64_t row_tiles = rows_pad / kTileRows, words = round_up(vocab, 256);
+    grad_width = cols > 128 ? mma::kMaxWidth : 128;  // (half as wide a tile takes half as long)
+    const int64_t across = ceil_div(cols, grad_width);
+    // dz in two terms, where that takes each pair no more than kFineBlocks (4 us), or where writing a tile out takes longer than its products
+    // anyway: kFineDepth blocks, a single tile of the rows or of the words (32 x 4096 x 50257: 284 us instead of 279).
+    constexpr int64_t kFineBlocks = 16, kFineDepth = 4;
+    const int64_t fine_tiles = kFineBlocks * kPairs * mma::kDepth / (across * words);  // of rows
+    fine_hidden = row_tiles <= fine_tiles || words <= kFineDepth * mma::kDepth;
+    fine_weight = row_tiles <= fine_tiles || rows_pad <= kFineDepth * mma::kDepth;
+    terms = fine_hidden || fine_weight ? 2 : 1;
     // dz of a piece: 2^27 values (256 MB), and at least 4096 columns, so that the sums over the pieces cost little
     constexpr int64_t kValues = int64_t{1} << 27, kLeast = 4096;
-    const int64_t words = round_up(vocab, 256), most = std::max(kLeast, kValues / rows_pad / 256 * 256);
+    const int64_t most = std::max(kLeast, kValues / (rows_pad * terms) / 256 * 256);
     const int64_t pieces = ceil_div(vocab, std::min(most, words));
     piece = round_up(ceil_div(vocab, pieces), 256);
     // The width whose tiles come out even over the pairs of a GPU's CTAs. A narrow tile reads the rows of hidden more often (the
     // 24), which a single tile of rows does not feel in the forward pass: there a narrower tile only splits the weight's reading more
     // evenly. Backward, the tiles fill whole multiples of 256 words.
     width = mma::kMaxWidth;
-    grad_width = cols > 128 ? mma::kMaxWidth : 128;  // (half as wide a tile takes half as long)
     constexpr int kRead = 24;
-    const int64_t row_tiles = rows_pad / kTileRows;
     int64_t least = INT64_MAX;
     for (int n = mma::kMaxWidth; n >= 64; n = backward ? n / 2 : n - 32) {
         const int64_t cost = ceil_div(row_tiles * ceil_div(backward ? piece : vocab, n), kPairs) * (n + (backward || row_tiles > 1 ? kRead : 0));
         if (cost < least) least = cost, width = n;
     }
     // Few tiles of the hidden gradient have their depth, the piece's words, split over the pairs.
-    const int64_t across = ceil_div(cols, grad_width);
+    const int64_t hidden_depth = piece * (fine_hidden ? 2 : 1), weight_depth = rows_pad * (fine_weight ? 2 : 1);
     splits = static_cast<int>(std::max<int64_t>(1, std::min(kPairs / (row_tiles * across), piece / (4 * mma::kDepth))));
-    if (splits > 1) splits = static_cast<int>(std::max<int64_t>(splits, ceil_div(piece, kGradPart * mma::kDepth)));
-    parted = std::max(splits > 1 ? 0 : piece, rows_pad) > kGradPart * mma::kDepth;
+    if (splits > 1) splits = static_cast<int>(std::max<int64_t>(splits, ceil_div(hidden_depth, kGradPart * mma::kDepth)));
+    parted = std::max(splits > 1 ? 0 : hidden_depth, weight_depth) > kGradPart * mma::kDepth;
     parts = 2 * ceil_div(vocab, width);
     head = take(sizeof(LossHead));
     map = take(rows_pad * 4);
@@ -75,12 +85,15 @@ LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
         lse = take(rows_pad * 4);
         coef = take(rows_pad * 4);
         onehot = take(rows_pad * 4);
-        // rows_pad piece <= rows_pad min(words, max(kLeast, kValues / rows_pad))
-        probs = take(2 * std::max(rows_pad * piece, std::min(rows_pad * words, std::max(rows_pad * kLeast, kValues))));
+        // tiles of rows times terms; times 256 and a piece <= min(words, max(kLeast, kValues / that))
+        const int64_t fine = words <= kFineDepth * mma::kDepth ? row_tiles : std::max<int64_t>(fine_tiles, kFineDepth * mma::kDepth / kTileRows);
+        const int64_t dz = std::max(row_tiles, 2 * std::min(row_tiles, fine));
+        probs = take(2 * std::min(kTileRows * dz * words, std::max(kTileRows * dz * kLeast, kValues)));
         // splits row_tiles, in row tiles: with no more than `split` of those the depth is split, into at most words / 256 parts and no more than
-        // fill the pairs or than there are parts of kGradPart
+        // fill the pairs or than there are parts of kGradPart (of two terms where any number of rows has them)
+        const bool short_words = fine_tiles > 0 || words <= kFineDepth * mma::kDepth;
         const int64_t split = std::min(row_tiles, kPairs / 2 / across);
-        const int64_t tiles = std::min(split * (words / 256), std::max(kPairs / across, split * ceil_div(words, kGradPart * mma::kDepth)));
+        const int64_t tiles = std::min(split * (words / 256), std::max(kPairs / across, split * ceil_div(short_words ? 2 * words : words, kGradPart * mma::kDepth)));
         sums = take(4 * pitch * kTileRows * std::max({splits * row_tiles, row_tiles, tiles}));
     } else {
         // A width n is taken only where ceil(row_tiles t(n) / kPairs) (n + kRead) <= that of every other m, t the tiles across, for which
@@ -311,6 +324,8 @@ struct Product {
     void* to;         // probs or dhidden
     void* dweight;
     int64_t pitch;    // of the rows of probs, of `sums`, or (forward) of the parts
+    int second;       // where a row of probs has the second terms (0: nowhere)
+    int fine_hidden, fine_weight;  // whether a gradient's products take them
     int begun, last;  // hidden gradient: whether the sums have earlier pieces, and whether this one completes them
     int wide, dweight_wide;  // rows of `to` and of dweight start on 16 bytes
 };
@@ -465,9 +480,10 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
         });
 }
 
-// Backward: scale dz / logit_scale of a piece, rounded. The logits are summed in the forward pass's parts, so that they are the very numbers that the
-// lse was formed from: a row whose label has all of the probability has a dz of 0, not of the error of a sum. Rows and words beyond the last are zeros up to the tile's end.
-template <class T>
+// Backward: scale dz / logit_scale of a piece, rounded, and (FINE) what the rounding left. The logits are summed in the forward pass's parts, so that they
+// are the very numbers that the lse was formed from: a row whose label has all of the probability has a dz of 0, not of the error of a sum.
+// Rows and words beyond the last are zeros up to the tile's end.
+template <class T, bool FINE>
 __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     probs_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap weight, const __grid_constant__ CUtensorMap out,
                  const __grid_constant__ Product p) {
@@ -500,6 +516,16 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
             if (!whole) return;
             const int label = word >= 0 ? static_cast<int>(word - p.first) - u.n - first : -1;
             const bool boxed = (last - first) % 64 == 0;
+            const auto store = [&](const float(&v)[32], int c, int term) {
+                if (boxed) {
+                    const int h = c / 32 & 1;
+                    if (h == 0) box.clear();
+                    box_columns<T>(box, h, v);
+                    if (h == 1) box.send(&out, term + u.n + first + c - 32, row0);
+                } else {
+                    store_columns<T>(static_cast<T*>(p.to) + row * p.pitch + term + u.n + first, c, last - first, v);
+                }
+            };
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
                 if (c >= last - first) continue;
@@ -517,14 +543,16 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
                     for (int i = 0; i < 32; ++i)
                         if (!in || c + i >= limit) v[i] = 0.0f;
                 }
-                if (boxed) {
-                    const int h = c / 32 & 1;
-                    if (h == 0) box.clear();
-                    box_columns<T>(box, h, v);
-                    if (h == 1) box.send(&out, u.n + first + c - 32, row0);
-                } else {
-                    store_columns<T>(static_cast<T*>(p.to) + row * p.pitch + u.n + first, c, last - first, v);
-                }
+                store(v, c, 0);
+            }
+            if constexpr (!FINE) return;
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) {  // what the rounding left, which is exact before its own
+                if (c >= last - first) continue;
+                float(&v)[32] = *reinterpret_cast<float(*)[32]>(z + c);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] -= to_float(from_float<T>(v[i]));
+                store(v, c, p.second);
             }
         });
 }
@@ -605,15 +633,20 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
                  const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap dweight_out, const __grid_constant__ Product p) {
     int64_t count = 0;
     float times = 0.0f;
+    mma::Operands<false, true> of_hidden{&probs_rows, &weight};
+    mma::Operands<true, true> of_weight{&probs_cols, &hidden};
+    of_hidden.second = of_weight.second = p.second;
     mma::run<PART, true>(
-        mma::Operands<false, true>{&probs_rows, &weight}, mma::Operands<true, true>{&probs_cols, &hidden}, p.boxes, kTypeBits<T>, p.lim,
+        of_hidden, of_weight, p.boxes, kTypeBits<T>, p.lim,
         [&] {
             count = p.w.head->count;
             times = p.w.head->unscale;
             const int across = tiles_of(p.cols, p.width);
             mma::Tiles dhidden, dweight;
-            if (p.to) dhidden = mma::Tiles{tiles_of(count, kTileRows), across, p.splits, tiles_of(p.n, mma::kDepth)};
-            if (p.dweight) dweight = mma::Tiles{tiles_of(p.n, kTileRows), across, 1, tiles_of(count, mma::kDepth)};
+            of_hidden.blocks = tiles_of(p.n, mma::kDepth);
+            of_weight.blocks = tiles_of(count, mma::kDepth);
+            if (p.to) dhidden = mma::Tiles{tiles_of(count, kTileRows), across, p.splits, of_hidden.blocks << p.fine_hidden};
+            if (p.dweight) dweight = mma::Tiles{tiles_of(p.n, kTileRows), across, 1, of_weight.blocks << p.fine_weight};
             return mma::Work(p.width, dhidden, dweight);
         },
         [&](const mma::Unit& u, int row, int, int first, int last, uint32_t at, bool ok, const mma::OutBox& box, bool, bool, auto&& release) {
@@ -787,9 +820,10 @@ cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
     CUtensorMap hidden_rows, hidden_cols, probs_rows, probs_cols, probs_out;
     if (e == cudaSuccess) e = map_of(&hidden_rows, hidden, p.rows_pad, a.cols, p.pitch, boxes.rows);
     if (e == cudaSuccess) e = map_of(&hidden_cols, hidden, p.rows_pad, a.cols, p.pitch, mma::kDepth);
-    if (e == cudaSuccess) e = map_of(&probs_rows, probs, p.rows_pad, p.piece, p.piece, boxes.rows);
-    if (e == cudaSuccess) e = map_of(&probs_cols, probs, p.rows_pad, p.piece, p.piece, mma::kDepth);
-    if (e == cudaSuccess) e = map_of(&probs_out, probs, p.rows_pad, p.piece, p.piece, 32);
+    const int64_t dz_pitch = p.piece * p.terms;
+    if (e == cudaSuccess) e = map_of(&probs_rows, probs, p.rows_pad, dz_pitch, dz_pitch, boxes.rows);
+    if (e == cudaSuccess) e = map_of(&probs_cols, probs, p.rows_pad, dz_pitch, dz_pitch, mma::kDepth);
+    if (e == cudaSuccess) e = map_of(&probs_out, probs, p.rows_pad, dz_pitch, dz_pitch, 32);
     const int64_t row_tiles = p.rows_pad / kTileRows;
     const bool align = a.cols % 8 == 0, dweight_wide = a.dweight && align && reinterpret_cast<uintptr_t>(a.dweight) % 16 == 0;
     for (int64_t first = 0; first < a.vocab && e == cudaSuccess; first += p.piece) {
@@ -809,8 +843,12 @@ cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
         d.scale = a.logit_scale * kL2E;
         d.width = p.width;
         d.to = probs;
-        d.pitch = p.piece;
-        e = launch_product(probs_kernel<T>, row_tiles * ceil_div(n, p.width), stream, hidden_rows, weight_rows, probs_out, d);
+        d.pitch = dz_pitch;
+        d.second = p.terms > 1 ? static_cast<int>(p.piece) : 0;
+        d.fine_hidden = p.fine_hidden;
+        d.fine_weight = p.fine_weight;
+        const auto probs_of = p.terms > 1 ? probs_kernel<T, true> : probs_kernel<T, false>;
+        e = launch_product(probs_of, row_tiles * ceil_div(n, p.width), stream, hidden_rows, weight_rows, probs_out, d);
         if (e != cudaSuccess) break;
         const int64_t across = ceil_div(a.cols, p.grad_width);
         d.width = p.grad_width;
@@ -823,8 +861,8 @@ cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
         d.wide = align && reinterpret_cast<uintptr_t>(a.dhidden) % 16 == 0;
         d.dweight_wide = dweight_wide;
         const int64_t units = (a.dhidden ? row_tiles * across * p.splits : 0) + (a.dweight ? ceil_div(n, kTileRows) * across : 0);
-        const auto kernel = p.parted ? grads_kernel<T, kGradPart> : grads_kernel<T, 0>;
-        e = launch_product(kernel, units, stream, probs_rows, weight_cols, probs_cols, hidden_cols, dweight_out, d);
+        const auto grads_of = p.parted ? grads_kernel<T, kGradPart> : grads_kernel<T, 0>;
+        e = launch_product(grads_of, units, stream, probs_rows, weight_cols, probs_cols, hidden_cols, dweight_out, d);
     }
     if (e != cudaSuccess || !a.dhidden || p.splits == 1) return e;
     const int64_t ctas = std::min<int64_t>(ceil_div(a.rows * a.cols, kThreads), 1 << 16);

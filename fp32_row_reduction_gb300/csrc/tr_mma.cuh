@@ -188,6 +188,10 @@ struct Operands {
     static constexpr bool kA = A_ROWS, kB = B_ROWS;
     const CUtensorMap* a;
     const CUtensorMap* b;
+    // A of two terms, the second one `second` elements behind the first in each row in memory: its blocks follow those of the first, `blocks` of
+    // them, and meet the same B.
+    int blocks = 1 << 30;
+    int second = 0;
 };
 // How many rows of A there are at most when all are in one tile (else 256). Rows of a box that lie outside the tensor are
 // filled with zeros slowly (one row of hidden in boxes of 128: 122 us instead of 73), so boxes are as high as the rows need,
@@ -386,13 +390,14 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
                 if (!ok) break;
                 const uint32_t bar = in_cta(smem_addr(&s.full[stage]), 0);
                 const uint32_t to_a = base + stage * kStageBytes, to_b = to_a + kRows * 128;
-                const int d = k * kDepth;
+                const bool again = k >= o.blocks;
+                const int d = (again ? k - o.blocks : k) * kDepth, a0 = again ? o.second : 0;
                 if (rank == 0) expect_bytes(&s.full[stage], bytes);
                 if constexpr (O::kA) {
 #pragma unroll
-                    for (int j = 0; j < kRows / 64; ++j) copy_box(to_a + j * kDepth * 128, o.a, m + 64 * j, d, bar);
+                    for (int j = 0; j < kRows / 64; ++j) copy_box(to_a + j * kDepth * 128, o.a, a0 + m + 64 * j, d, bar);
                 } else if (rank == 0 || boxes.second) {
-                    copy_box(to_a, o.a, d, m, bar);
+                    copy_box(to_a, o.a, a0 + d, m, bar);
                 }
                 if constexpr (O::kB) {
                     for (uint32_t j = 0; j < half / 64; ++j) copy_box(to_b + j * kDepth * 128, o.b, n + 64 * j, d, bar);

@@ -81,6 +81,8 @@ struct LossPlan {
     int grad_width;    // columns of a tile of the gradients
     int splits;        // of the depth of the hidden gradient
     bool parted;       // whether a depth of the gradients is summed in parts
+    bool fine_hidden, fine_weight;  // whether a gradient's products take dz in two terms
+    int terms;         // of dz that are kept
     size_t head, map, labels, lse, coef, onehot, hidden, weight, parts_at, picked, probs, sums, bytes;
     bool pack_weight;  // rows of the weight that do not start on 16 bytes are copied to ones that do
     LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward);

@@ -427,7 +427,7 @@ tr_status tr_global_norm_workspace_bytes(int64_t count, size_t* bytes);
  * custom; any value, those inside the vocabulary too) has no loss: its losses and lse are 0, and its row of hidden counts for
  * nothing, whatever it holds. hidden: rows x cols, weight: vocab x cols, both of `dtype`, TR_BF16 or TR_F16 (TR_F32:
  * TR_ERR_UNSUPPORTED); losses and lse: rows floats; lse may be NULL. Products are exact and summed
- * in binary32.
+ * in binary32, 1024 at a time in tensor memory, which rounds toward zero, and those parts to nearest.
  *
  * tr_linear_cross_entropy_backward: from the lse that the forward pass gave, with dloss the gradient of the losses
  * (NULL: 1) and dlse that of the lse (NULL: 0; a penalty of the lse),
@@ -435,7 +435,8 @@ tr_status tr_global_norm_workspace_bytes(int64_t count, size_t* bytes);
  *   dhidden = dz weight,  dweight = dz^T hidden,
  * each of `dtype` and either NULL when not wanted. The logits are formed again, a piece of the vocabulary at a time. dz is
  * rounded to `dtype` for the products, relative to the largest coefficient (so that float16 keeps
- * small probabilities); sums are binary32, each output is rounded once. Rows without a loss have a gradient of 0 and
+ * small probabilities), and kept to twice the digits in dweight of up to 256 rows, in dhidden of up to 256 words, and in both where the
+ * products are few. Logits are summed as above, gradients 8192 products at a time; each output is rounded once. Rows without a loss have a gradient of 0 and
  * add nothing to dweight, whatever they hold.
  *
  * Tables and rows are contiguous. Pointers must be aligned to their elements; weight to 16 bytes when

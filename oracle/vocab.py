@@ -82,8 +82,8 @@ def linear_cross_entropy(hidden, weight, labels, scale=1.0, ignore=-100):
     return (keep(lse - picked), keep(e_loss)), (keep(lse), keep(e_lse))
 
 
-def linear_cross_entropy_backward(hidden, weight, labels, lse, dloss=None, dlse=None, scale=1.0, ignore=-100):
-    """((dhidden, bound), (dweight, bound))."""
+def linear_cross_entropy_backward(hidden, weight, labels, lse, dloss=None, dlse=None, scale=1.0, ignore=-100, terms=1):
+    """((dhidden, bound), (dweight, bound)); `terms`: how many of the type dz is taken in, each rounding what those before it left."""
     dtype, v = hidden.dtype, weight.shape[0]
     counted = labels != ignore
     hidden = torch.where(counted[:, None], hidden, torch.zeros_like(hidden))
@@ -102,7 +102,7 @@ def linear_cross_entropy_backward(hidden, weight, labels, lse, dloss=None, dlse=
     dz_err[at, labels[at]] += 2 * U * d[at].abs()
     step, tiny = HALF_STEP[dtype]
     most = float((d.abs() + (total - d).abs()).max()) if d.numel() else 0.0
-    dz_err = dz_err + step * (dz.abs() + dz_err) + (tiny * 2 * most * 2.0 ** -14 if dtype == torch.float16 else 0.0)
+    dz_err = dz_err + step ** terms * (dz.abs() + dz_err) + (tiny * 2 * most * 2.0 ** -14 if dtype == torch.float16 else 0.0)
     dz_err[~counted] = 0.0
     s = abs(f32(scale))
     h, w = hidden.double(), weight.double()

@@ -342,6 +342,33 @@ def test_certain_rows_of_long_sums(rows, cols, dtype):
         assert bool((dh.double().abs() <= dz[:, None] * w * (1 + 2 * t) + tiny).all())
 
 
+FINE = [(1, 1024, 124), (2, 64, 31), (1, 8, 2), (18, 5568, 4645), (37, 1537, 5003), (201, 320, 136), (300, 65, 200), (872, 448, 25), (9000, 64, 25), (256, 72, 700)]
+
+
+@pytest.mark.parametrize("rows,cols,v", FINE)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_small_gradients_are_rounded_once(rows, cols, v, dtype):
+    """Where the products are short, dz is taken in two terms of the type: it is off by the square of its half step, and what is left is the
+    outputs' own rounding. (In float16 with its room for small numbers: 2^-25 of 2^14 as before.)"""
+    hidden, weight, labels, dloss, dlse = loss_inputs(rows, cols, v, dtype, ignored=0.1 if rows > 100 else 0.0)
+    _, lse = tr.linear_cross_entropy(hidden, weight, labels)
+    dh, dw = tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse)
+    want_h, want_w = vocab.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse, terms=2)
+    close(dh, want_h)
+    close(dw, want_w)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_the_weights_gradient_of_few_rows_is_rounded_once(dtype):
+    """Few rows of a long vocabulary: the weight's gradient has two terms of dz, the hidden one's long sums have one. Either alone is the same."""
+    rows, cols, v = 200, 264, 30011
+    hidden, weight, labels, dloss, dlse = loss_inputs(rows, cols, v, dtype, ignored=0.1)
+    _, lse, dh, dw = check_loss(hidden, weight, labels, dloss, dlse)
+    close(dw, vocab.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse, terms=2)[1])
+    assert same(tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse, want_dweight=False)[0], dh)
+    assert same(tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse, want_dhidden=False)[1], dw)
+
+
 GRAD_STEPS = 512  # the gradients are summed in parts of at most 8192 of the depth, a part in steps of 16
 
 
