@@ -277,7 +277,7 @@ struct Packing {
     }
 };
 
-// hidden's rows that have a loss, then zeros up to a whole block of the products' depth; all rows of the weight (dst null: none);
+// hidden's rows that have a loss, then zeros up to a whole block of the products' depth; all rows of the weight (its dst null: none);
 // backward, the gradients of rows without a loss, which are zeros. SMALL: every CTA finds by itself which rows those are, and
 // the first writes it down, so that one launch does all of it (up to 1024 rows).
 template <class T, bool SMALL>
@@ -285,8 +285,8 @@ __global__ void __launch_bounds__(SMALL ? kScanThreads : kThreads) pack_kernel(L
     __shared__ int small_map[SMALL ? kScanThreads : 1];
     pdl_release();
     pdl_enter();
-    const int64_t count = SMALL ? list_rows<1>(a, w, backward, blockIdx.x == 0, small_map) : hidden.dst ? w.head->count : 0;
-    const int64_t end = hidden.dst ? (count + mma::kDepth - 1) / mma::kDepth * mma::kDepth * hidden.chunks : 0;
+    const int64_t count = SMALL ? list_rows<1>(a, w, backward, blockIdx.x == 0, small_map) : w.head->count;
+    const int64_t end = (count + mma::kDepth - 1) / mma::kDepth * mma::kDepth * hidden.chunks;
     const int64_t all = end + (weight.dst ? weight.rows * weight.chunks : 0);
     const int64_t warps = blockDim.x / 32, step = gridDim.x * warps, first = blockIdx.x * warps + threadIdx.x / 32;
     for (int64_t i = first; i < all; i += step) {
@@ -717,24 +717,21 @@ Ws workspace(const LossArgs& a, const LossPlan& p) {
               f(p.lse), f(p.coef), f(p.onehot), reinterpret_cast<float2*>(a.ws + p.parts_at), f(p.picked), f(p.sums), p.rows_pad};
 }
 
-// hidden's rows that have a loss (unless w.map is null: as it is), and the weight where its rows do not start on 16 bytes.
+// hidden's rows that have a loss, and the weight where its rows do not start on 16 bytes.
 template <class T>
 cudaError_t pack(const LossArgs& a, const LossPlan& p, const Ws& w, int backward, const T** hidden, const T** weight, cudaStream_t stream) {
     const int chunks = static_cast<int>(ceil_div(p.pitch, 1024));
-    Packing<T> h{static_cast<const T*>(a.hidden), w.map ? reinterpret_cast<T*>(a.ws + p.hidden) : nullptr, a.rows, p.pitch, a.cols, chunks};
+    Packing<T> h{static_cast<const T*>(a.hidden), reinterpret_cast<T*>(a.ws + p.hidden), a.rows, p.pitch, a.cols, chunks};
     Packing<T> t{static_cast<const T*>(a.weight), p.pack_weight ? reinterpret_cast<T*>(a.ws + p.weight) : nullptr, a.vocab, p.pitch, a.cols, chunks};
-    *hidden = h.dst ? h.dst : h.src;
+    *hidden = h.dst;
     *weight = t.dst ? t.dst : t.src;
-    const int64_t items = ((h.dst ? a.rows + mma::kDepth : 0) + (t.dst ? a.vocab : 0)) * chunks;
-    if (items == 0) return cudaSuccess;
-    if (w.map && a.rows <= kScanThreads) {
+    const int64_t items = (a.rows + mma::kDepth + (t.dst ? a.vocab : 0)) * chunks;
+    if (a.rows <= kScanThreads) {
         const int64_t ctas = std::min<int64_t>(ceil_div(items, kScanThreads / 32), 4 * kPairs);
         return launch_dependent(pack_kernel<T, true>, dim3(static_cast<unsigned>(ctas)), kScanThreads, 0, 1, stream, a, w, backward, h, t);
     }
-    if (w.map) {
-        const cudaError_t e = launch_dependent(rows_kernel, dim3(1), kScanThreads, 0, 1, stream, a, w, backward);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = launch_dependent(rows_kernel, dim3(1), kScanThreads, 0, 1, stream, a, w, backward);
+    if (e != cudaSuccess) return e;
     const int64_t ctas = std::min<int64_t>(ceil_div(items, kThreads / 32), 1 << 14);
     return launch_dependent(pack_kernel<T, false>, dim3(static_cast<unsigned>(ctas)), kThreads, 0, 1, stream, a, w, backward, h, t);
 }
@@ -784,9 +781,10 @@ cudaError_t forward(const LossArgs& a, cudaStream_t stream) {
     Ws w = workspace(a, p);
     // One tile of rows is not shorter without the rows that have no loss: they are read where they are.
     const bool direct = a.rows <= kTileRows && a.cols % 8 == 0 && reinterpret_cast<uintptr_t>(a.hidden) % 16 == 0;
+    const T *from = static_cast<const T*>(a.hidden), *table = static_cast<const T*>(a.weight);
+    cudaError_t e = cudaSuccess;
     if (direct) w.map = nullptr;
-    const T *from, *table;
-    cudaError_t e = pack<T>(a, p, w, 0, &from, &table, stream);
+    else e = pack<T>(a, p, w, 0, &from, &table, stream);
     const mma::Boxes boxes = mma::boxes_for(a.rows);
     CUtensorMap hidden, weight;
     if (e == cudaSuccess) e = map_of(&hidden, from, direct ? a.rows : p.rows_pad, a.cols, p.pitch, boxes.rows);
