@@ -194,8 +194,11 @@ __device__ __forceinline__ int64_t list_rows(const LossArgs& a, const Ws& w, int
                     w.lse[to] = lse[i] * kL2E;
                     w.coef[to] = d[i] + e[i];
                     w.onehot[to] = d[i];
-                    most = fmaxf(most, fabsf(d[i]) + fabsf(e[i]));
-                    most_d = fmaxf(most_d, fabsf(d[i]));
+                    const float size = fabsf(d[i]) + fabsf(e[i]);
+                    if (size < INFINITY) {  // (a row whose coefficients are no numbers has no say in the others' scale)
+                        most = fmaxf(most, size);
+                        most_d = fmaxf(most_d, fabsf(d[i]));
+                    }
                 }
             } else if (write && !backward && r < a.rows) {
                 a.losses[r] = 0.0f;
@@ -216,7 +219,7 @@ __device__ __forceinline__ int64_t list_rows(const LossArgs& a, const Ws& w, int
             // dz is divided by the largest coefficient and brought to 2^14 (at most 2^15 with that of the lse), where float16 has
             // room for small probabilities; and where all rows count alike, the label's -1 is a number that rounds to itself.
             float by = 1.0f, times = 1.0f;
-            if (most > 0.0f && most < INFINITY) {
+            if (most > 0.0f) {
                 const bool alike = most <= 2.0f * most_d;
                 by = fminf(fmaxf(alike ? most_d : most, 0x1p-100f), 0x1p100f);
                 times = alike ? 0x1p14f : 0x1p15f;

@@ -452,6 +452,24 @@ def test_not_finite(dtype):
     close(lse, (want, err))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_coefficients_that_are_not_finite(dtype, bad):
+    """A row whose gradient of the loss or of the lse overflowed spoils its own hidden gradient, and takes no digits from the others'."""
+    rows, cols, v = 300, 72, 400
+    hidden, weight, labels, dloss, dlse = loss_inputs(rows, cols, v, dtype)
+    _, lse = tr.linear_cross_entropy(hidden, weight, labels)
+    ok = torch.ones(rows, dtype=torch.bool, device=DEV)
+    ok[[17, 201]] = False
+    zero = torch.zeros((), device=DEV)
+    want, err = vocab.linear_cross_entropy_backward(hidden, weight, labels, lse, torch.where(ok, dloss, zero), torch.where(ok, dlse, zero), terms=2)[0]
+    dloss[17] = bad
+    dlse[201] = bad
+    dh, dw = tr.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse)
+    close(dh[ok], (want[ok], err[ok]))
+    assert not bool(torch.isfinite(dh[~ok]).any())
+
+
 def test_float16_keeps_small_probabilities():
     """Probabilities far below float16's smallest number, with coefficients of a mean: the hidden gradient is theirs."""
     rows, cols, v = 64, 64, 4096
