@@ -7,7 +7,7 @@
 // (in float32 over the pieces) and dweight = dz^T hidden. The rounding is one of T's half steps of each dz, relative to a dz that has
 // the label's -1 in it already; it adds as much as a third to the outputs' error (bf16 201 x 320 x 136: 2.2e-3 instead of 1.7e-3). Where the products are
 // short, dz is taken in two terms of T, the second what the first one's rounding left, and nothing is added. That costs
-// 2 to 5 us (37 x 1537 x 5003 f16 48.0 us instead of 44.7); for 8192 x 4096 x 50257 it would be 9.5 ms instead of 5.5.
+// 2 to 8 us (37 x 1537 x 5003 f16 47.5 us instead of 44.7); for 8192 x 4096 x 50257 it would be 9.5 ms instead of 5.5.
 //
 // Rows that have a loss are packed first: the products do no work for the others, and what those hold, which may be no
 // number, is not read as the depth of the weight's gradient.
@@ -27,8 +27,8 @@ namespace tr {
 
 constexpr int kPairs = 76;  // CTA pairs of the GPU that the plan is made for
 // Blocks of the depth (the piece's words, or the rows) that the gradients are summed over in tensor memory, which rounds toward zero: 131072
-// words in one sum came out 2.5e-4 too small, as much as float16's last rounding; parts of 8192 are 2e-5. Longer depths are split
-// where they are split anyway, or their parts are added in registers by a kernel of its own (8192 x 4096 x 50257 takes 1.5% longer in parts, 3% in
+// words in one sum came out 2.5e-4 too small, as much as float16's last rounding; parts of 8192 are 2e-5. The parts of longer depths
+// are added in registers by a kernel of its own (8192 x 4096 x 50257 takes 1.3% longer in parts, 3% in
 // parts of 4096; the registers would cost 64 x 2047 x 30000, whose depths are one part each, 215 us instead of 178).
 constexpr int kGradPart = 128;
 
@@ -45,12 +45,15 @@ LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
     const int64_t row_tiles = rows_pad / kTileRows, words = round_up(vocab, 256);
     grad_width = cols > 128 ? mma::kMaxWidth : 128;  // (half as wide a tile takes half as long)
     const int64_t across = ceil_div(cols, grad_width);
-    // dz in two terms, where that takes each pair no more than kFineBlocks (4 us), or where writing a tile out takes longer than its products
-    // anyway: kFineDepth blocks, a single tile of the rows or of the words (32 x 4096 x 50257: 284 us instead of 279).
-    constexpr int64_t kFineBlocks = 16, kFineDepth = 4;
-    const int64_t fine_tiles = kFineBlocks * kPairs * mma::kDepth / (across * words);  // of rows
-    fine_hidden = row_tiles <= fine_tiles || words <= kFineDepth * mma::kDepth;
-    fine_weight = row_tiles <= fine_tiles || rows_pad <= kFineDepth * mma::kDepth;
+    const int64_t hidden_tiles = row_tiles * across, weight_tiles = words / kTileRows * across;
+    // Few tiles of the hidden gradient have their depth, the words, split over the pairs.
+    const auto split_depth = [&](int64_t n) { return std::max<int64_t>(1, std::min(kPairs / hidden_tiles, n / (4 * mma::kDepth))); };
+    // dz in two terms, where the second takes a pair no more than kFineBlocks (4 us), or where writing a tile out takes longer than its products
+    // anyway: kFineDepth blocks, 128 rows or words (32 x 4096 x 50257: 286 us instead of 280; 256 x 2048 x 32000 would take 140 instead of 129).
+    constexpr int64_t kFineBlocks = 16, kFineDepth = 2;
+    const int64_t split_words = split_depth(words);
+    fine_hidden = vocab <= kFineDepth * mma::kDepth || ceil_div(hidden_tiles * split_words, kPairs) * ceil_div(words / mma::kDepth, split_words) <= kFineBlocks;
+    fine_weight = rows <= kFineDepth * mma::kDepth || ceil_div(weight_tiles, kPairs) * (rows_pad / mma::kDepth) <= kFineBlocks;
     terms = fine_hidden || fine_weight ? 2 : 1;
     // dz of a piece: 2^27 values (256 MB), and at least 4096 columns, so that the sums over the pieces cost little
     constexpr int64_t kValues = int64_t{1} << 27, kLeast = 4096;
@@ -67,11 +70,13 @@ LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
         const int64_t cost = ceil_div(row_tiles * ceil_div(backward ? piece : vocab, n), kPairs) * (n + (backward || row_tiles > 1 ? kRead : 0));
         if (cost < least) least = cost, width = n;
     }
-    // Few tiles of the hidden gradient have their depth, the piece's words, split over the pairs.
-    const int64_t hidden_depth = piece * (fine_hidden ? 2 : 1), weight_depth = rows_pad * (fine_weight ? 2 : 1);
-    splits = static_cast<int>(std::max<int64_t>(1, std::min(kPairs / (row_tiles * across), piece / (4 * mma::kDepth))));
-    if (splits > 1) splits = static_cast<int>(std::max<int64_t>(splits, ceil_div(hidden_depth, kGradPart * mma::kDepth)));
-    parted = std::max(splits > 1 ? 0 : hidden_depth, weight_depth) > kGradPart * mma::kDepth;
+    // A single tile of rows has the hidden gradient's depth split into no longer parts than are summed at once: its weight's tiles, bound by their writing,
+    // would feel the kernel that adds parts in registers (32 x 4096 x 50257: 296 us instead of 280; for 1024 x 1024 x 50257 that kernel
+    // is the better one, 236 instead of 244).
+    const int64_t hidden_blocks = piece / mma::kDepth * (fine_hidden ? 2 : 1), weight_blocks = rows_pad / mma::kDepth * (fine_weight ? 2 : 1);
+    splits = static_cast<int>(split_depth(piece));
+    if (splits > 1 && row_tiles == 1) splits = static_cast<int>(std::max<int64_t>(splits, ceil_div(hidden_blocks, kGradPart)));
+    parted = std::max(ceil_div(hidden_blocks, splits), weight_blocks) > kGradPart;
     parts = 2 * ceil_div(vocab, width);
     head = take(sizeof(LossHead));
     map = take(rows_pad * 4);
@@ -85,15 +90,15 @@ LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
         lse = take(rows_pad * 4);
         coef = take(rows_pad * 4);
         onehot = take(rows_pad * 4);
-        // tiles of rows times terms; times 256 and a piece <= min(words, max(kLeast, kValues / that))
-        const int64_t fine = words <= kFineDepth * mma::kDepth ? row_tiles : std::max<int64_t>(fine_tiles, kFineDepth * mma::kDepth / kTileRows);
-        const int64_t dz = std::max(row_tiles, 2 * std::min(row_tiles, fine));
+        // Two terms take hidden_tiles or weight_tiles times their depth <= kFineBlocks kPairs blocks, or they are of a single tile of rows, or of words.
+        // Tiles of rows times terms, `dz`, are times 256 and a piece <= min(words, max(kLeast, kValues / that)).
+        const int64_t fine_tiles = vocab <= kFineDepth * mma::kDepth ? row_tiles : std::max<int64_t>(1, kFineBlocks * kPairs * mma::kDepth / (across * words));
+        const int64_t dz = std::max(row_tiles, 2 * std::min(row_tiles, fine_tiles));
         probs = take(2 * std::min(kTileRows * dz * words, std::max(kTileRows * dz * kLeast, kValues)));
-        // splits row_tiles, in row tiles: with no more than `split` of those the depth is split, into at most words / 256 parts and no more than
-        // fill the pairs or than there are parts of kGradPart (of two terms where any number of rows has them)
-        const bool short_words = fine_tiles > 0 || words <= kFineDepth * mma::kDepth;
+        // splits row_tiles, in tiles: with no more than `split` tiles of rows the depth is split, into at most words / 256 parts, and no more than fill
+        // the pairs or (a single tile of rows) than there are parts of kGradPart in two terms
         const int64_t split = std::min(row_tiles, kPairs / 2 / across);
-        const int64_t tiles = std::min(split * (words / 256), std::max(kPairs / across, split * ceil_div(short_words ? 2 * words : words, kGradPart * mma::kDepth)));
+        const int64_t tiles = std::min(split * (words / 256), std::max(kPairs / across, ceil_div(2 * words, kGradPart * mma::kDepth)));
         sums = take(4 * pitch * kTileRows * std::max({splits * row_tiles, row_tiles, tiles}));
     } else {
         // A width n is taken only where ceil(row_tiles t(n) / kPairs) (n + kRead) <= that of every other m, t the tiles across, for which

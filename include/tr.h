@@ -435,7 +435,7 @@ tr_status tr_global_norm_workspace_bytes(int64_t count, size_t* bytes);
  *   dhidden = dz weight,  dweight = dz^T hidden,
  * each of `dtype` and either NULL when not wanted. The logits are formed again, a piece of the vocabulary at a time. dz is
  * rounded to `dtype` for the products, relative to the largest coefficient (so that float16 keeps
- * small probabilities), and kept to twice the digits in dweight of up to 256 rows, in dhidden of up to 256 words, and in both where the
+ * small probabilities), and kept to twice the digits in dweight of up to 128 rows, in dhidden of up to 128 words, and in both where the
  * products are few. Logits are summed as above, gradients 8192 products at a time; each output is rounded once. Rows without a loss have a gradient of 0 and
  * add nothing to dweight, whatever they hold.
  *

@@ -342,7 +342,7 @@ def test_certain_rows_of_long_sums(rows, cols, dtype):
         assert bool((dh.double().abs() <= dz[:, None] * w * (1 + 2 * t) + tiny).all())
 
 
-FINE = [(1, 1024, 124), (2, 64, 31), (1, 8, 2), (18, 5568, 4645), (37, 1537, 5003), (201, 320, 136), (300, 65, 200), (872, 448, 25), (9000, 64, 25), (256, 72, 700)]
+FINE = [(1, 1024, 124), (2, 64, 31), (1, 8, 2), (18, 5568, 4645), (37, 1537, 5003), (201, 320, 136), (300, 65, 200), (872, 448, 25), (256, 72, 700)]
 
 
 @pytest.mark.parametrize("rows,cols,v", FINE)
@@ -361,7 +361,7 @@ def test_small_gradients_are_rounded_once(rows, cols, v, dtype):
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_the_weights_gradient_of_few_rows_is_rounded_once(dtype):
     """Few rows of a long vocabulary: the weight's gradient has two terms of dz, the hidden one's long sums have one. Either alone is the same."""
-    rows, cols, v = 200, 264, 30011
+    rows, cols, v = 100, 264, 30011
     hidden, weight, labels, dloss, dlse = loss_inputs(rows, cols, v, dtype, ignored=0.1)
     _, lse, dh, dw = check_loss(hidden, weight, labels, dloss, dlse)
     close(dw, vocab.linear_cross_entropy_backward(hidden, weight, labels, lse, dloss, dlse, terms=2)[1])
