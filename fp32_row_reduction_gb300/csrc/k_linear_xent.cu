@@ -31,6 +31,10 @@ constexpr int kPairs = 76;  // CTA pairs of the GPU that the plan is made for
 // are added in registers by a kernel of its own (8192 x 4096 x 50257 takes 1.3% longer in parts, 3% in
 // parts of 4096; the registers would cost 64 x 2047 x 30000, whose depths are one part each, 215 us instead of 178).
 constexpr int kGradPart = 128;
+// And of the logits (blocks of the width): sums of 1024 are off by 1e-7 to 3e-7 of the losses, where binary32 products rounded to nearest are off by 1e-7,
+// and by 1e-6 of the small losses of a few likely words. Where no pair has more than one tile they are of 512, for 2% at most; a
+// training batch would take 10% longer, 48 x 5120 x 50257 7%. (Sums of 256: 48 x 5120 140 us instead of 91: a thread's 128 columns of a part take 4000 cycles.)
+constexpr int kLogitPart = 16, kShortLogitPart = 8;
 
 LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
     size_t at = 0;
@@ -77,6 +81,7 @@ LossPlan::LossPlan(int64_t rows, int64_t cols, int64_t vocab, bool backward) {
     splits = static_cast<int>(split_depth(piece));
     if (splits > 1 && row_tiles == 1) splits = static_cast<int>(std::max<int64_t>(splits, ceil_div(hidden_blocks, kGradPart)));
     parted = std::max(ceil_div(hidden_blocks, splits), weight_blocks) > kGradPart;
+    logit_part = row_tiles * (words / 256) <= kPairs ? kShortLogitPart : kLogitPart;
     parts = 2 * ceil_div(vocab, width);
     head = take(sizeof(LossHead));
     map = take(rows_pad * 4);
@@ -331,6 +336,7 @@ struct Product {
     const int64_t* labels;
     void* to;         // probs or dhidden
     void* dweight;
+    int part;         // of the logits: see LossPlan
     int64_t pitch;    // of the rows of probs, of `sums`, or (forward) of the parts
     int second;       // where a row of probs has the second terms (0: nowhere)
     int fine_hidden, fine_weight;  // whether a gradient's products take them
@@ -398,9 +404,8 @@ __device__ __forceinline__ void spoil(float (&v)[32]) {
     for (int i = 0; i < 32; ++i) v[i] = NAN;
 }
 
-// Forward: (maximum, sum of 2^(z - maximum)) of each half of a tile's columns, and the label's z. The logits are summed in parts of
-// kPart blocks of the depth, which are added in registers (see mma::run): a thread has 128 columns of a row.
-constexpr int kPart = 16;
+// Forward: (maximum, sum of 2^(z - maximum)) of each half of a tile's columns, and the label's z. The logits are summed in parts
+// of p.part blocks of the depth, which are added in registers (see mma::run): a thread has 128 columns of a row.
 
 // Two products, and two sums, in one instruction each.
 __device__ __forceinline__ void pair_times(float& a, float& b, float by) {
@@ -460,8 +465,8 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     int64_t count = 0;
     float z[128];
     const mma::Operands<false, false> o{&hidden, &weight};
-    mma::run<kPart, false>(
-        o, o, p.boxes, kTypeBits<T>, p.lim,
+    mma::run<mma::kEach>(
+        o, o, p.boxes, kTypeBits<T>, p.lim, p.part,
         [&] {
             count = p.w.map ? p.w.head->count : p.rows;
             return mma::Work(p.width, mma::Tiles{tiles_of(count, kTileRows), tiles_of(p.n, p.width), 1, tiles_of(p.cols, mma::kDepth)});
@@ -498,8 +503,8 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     int64_t count = 0;
     float times = 0.0f, z[128];
     const mma::Operands<false, false> o{&hidden, &weight};
-    mma::run<kPart, false>(
-        o, o, p.boxes, kTypeBits<T>, p.lim,
+    mma::run<mma::kEach>(
+        o, o, p.boxes, kTypeBits<T>, p.lim, p.part,
         [&] {
             count = p.w.head->count;
             times = p.w.head->scale;
@@ -635,7 +640,7 @@ __device__ __forceinline__ void weight_part(const Product& p, const CUtensorMap*
         }
     }
 }
-template <class T, int PART>
+template <class T, bool LONG>
 __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     grads_kernel(const __grid_constant__ CUtensorMap probs_rows, const __grid_constant__ CUtensorMap weight, const __grid_constant__ CUtensorMap probs_cols,
                  const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap dweight_out, const __grid_constant__ Product p) {
@@ -644,8 +649,8 @@ __global__ void __cluster_dims__(2) __launch_bounds__(mma::kThreads, 1)
     mma::Operands<false, true> of_hidden{&probs_rows, &weight};
     mma::Operands<true, true> of_weight{&probs_cols, &hidden};
     of_hidden.second = of_weight.second = p.second;
-    mma::run<PART, true>(
-        of_hidden, of_weight, p.boxes, kTypeBits<T>, p.lim,
+    mma::run<LONG ? mma::kJoined : mma::kWhole>(
+        of_hidden, of_weight, p.boxes, kTypeBits<T>, p.lim, kGradPart,
         [&] {
             count = p.w.head->count;
             times = p.w.head->unscale;
@@ -808,6 +813,7 @@ cudaError_t forward(const LossArgs& a, cudaStream_t stream) {
     d.scale = a.logit_scale * kL2E;
     d.rows = a.rows;
     d.labels = a.labels;
+    d.part = p.logit_part;
     d.pitch = p.parts;
     e = launch_product(stats_kernel<T>, p.rows_pad / kTileRows * ceil_div(a.vocab, p.width), stream, hidden, weight, d);
     if (e != cudaSuccess) return e;
@@ -850,6 +856,7 @@ cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
         d.width = p.width;
         d.to = probs;
         d.pitch = dz_pitch;
+        d.part = p.logit_part;
         d.second = p.terms > 1 ? static_cast<int>(p.piece) : 0;
         d.fine_hidden = p.fine_hidden;
         d.fine_weight = p.fine_weight;
@@ -867,7 +874,7 @@ cudaError_t backward(const LossArgs& a, cudaStream_t stream) {
         d.wide = align && reinterpret_cast<uintptr_t>(a.dhidden) % 16 == 0;
         d.dweight_wide = dweight_wide;
         const int64_t units = (a.dhidden ? row_tiles * across * p.splits : 0) + (a.dweight ? ceil_div(n, kTileRows) * across : 0);
-        const auto grads_of = p.parted ? grads_kernel<T, kGradPart> : grads_kernel<T, 0>;
+        const auto grads_of = p.parted ? grads_kernel<T, true> : grads_kernel<T, false>;
         e = launch_product(grads_of, units, stream, probs_rows, weight_cols, probs_cols, hidden_cols, dweight_out, d);
     }
     if (e != cudaSuccess || !a.dhidden || p.splits == 1) return e;

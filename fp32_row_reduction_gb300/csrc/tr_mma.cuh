@@ -321,15 +321,18 @@ struct Work {
     }
 };
 
+// How a tile's sums reach the caller of run(): summed over the whole depth, or in parts of so many blocks, because the tensor cores round their
+// sums toward zero, an error that grows with the length of a sum. Parts are given to the caller one after another (kEach), or added in registers and put
+// back into tensor memory, as if there had been one (kJoined).
+enum Parts { kWhole, kEach, kJoined };
+
 // The products of a CTA pair: plan() gives the work, once what earlier kernels wrote can be read; o0 and o1 are the operands of the two
-// kinds. The sums of a tile come in one part, or (CHUNK > 0) in a part for every CHUNK blocks of the depth: the
-// tensor cores round their sums toward zero, an error that grows with the length of a sum. JOIN: the parts are added in registers and put
-// back into tensor memory, as if there had been one; otherwise the caller is given one after another. out(unit, row, half, first, last,
+// kinds; `part`: blocks of the depth in a part. out(unit, row, half, first, last,
 // tensor address, ok, box, begun, whole, release) takes the columns [first, last) of one row a lane, and calls release() when it has
 // read the tensor memory; ok: the sums are there (false: after a wait that gave up); box: the warp's room in
 // shared memory; begun: earlier parts have come; whole: the last one.
-template <int CHUNK, bool JOIN, class O0, class O1, class Plan, class Out>
-__device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& boxes, uint32_t type_bits, const Limits& lim, Plan&& plan, Out&& out) {
+template <Parts PARTS, class O0, class O1, class Plan, class Out>
+__device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& boxes, uint32_t type_bits, const Limits& lim, int part, Plan&& plan, Out&& out) {
     extern __shared__ __align__(16) char raw[];
     __shared__ Shared s;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
@@ -435,7 +438,7 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
                                       static_cast<uint32_t>(width / 8) << 17 | (2 * kRows / 16) << 24;
                 int k = u.begin;
                 do {
-                    const int from = k, to = CHUNK > 0 ? min(k + CHUNK, u.end) : u.end;
+                    const int from = k, to = PARTS != kWhole ? min(k + part, u.end) : u.end;
                     ok = waits.wait(&s.room[slot], slot_phase ^ 1);
                     if (!ok) return;
                     fence_after();
@@ -476,14 +479,14 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
             const int row = u.m + static_cast<int>(rank) * kRows + quarter * 32 + lane;
             int k = u.begin;
             bool ok = true;
-            if (JOIN && CHUNK > 0 && u.end - k > CHUNK) {
+            if (PARTS == kJoined && u.end - k > part) {
                 float sum[128];
 #pragma unroll
                 for (int c = 0; c < 128; ++c) sum[c] = 0.0f;
-                for (;; k += CHUNK) {
+                for (;; k += part) {
                     ok = slot.arrived(waits) && ok;
                     add_part(slot.columns(columns) + first, last - first, sum);
-                    if (u.end - k <= CHUNK) break;
+                    if (u.end - k <= part) break;
                     slot.release(waits);
                     slot.next();
                 }
@@ -492,12 +495,12 @@ __device__ __forceinline__ void run(const O0& o0, const O1& o1, const Boxes& box
                     if (c < last - first) put_columns(slot.columns(columns) + first + c, sum + c);
             }
             do {
-                const bool begun = !JOIN && k > u.begin;
-                k = CHUNK > 0 ? min(k + CHUNK, u.end) : u.end;
+                const bool begun = PARTS == kEach && k > u.begin;
+                k = PARTS == kEach ? min(k + part, u.end) : u.end;
                 ok = slot.arrived(waits) && ok;
-                out(u, row, half, first, last, slot.columns(columns), ok, box, begun, JOIN || k >= u.end, [&] { slot.release(waits); });
+                out(u, row, half, first, last, slot.columns(columns), ok, box, begun, k >= u.end, [&] { slot.release(waits); });
                 slot.next();
-            } while (!JOIN && k < u.end);
+            } while (PARTS == kEach && k < u.end);
         }
         OutBox::finish();
     }

@@ -80,6 +80,7 @@ struct LossPlan {
     int width;         // words of a tile of logits
     int grad_width;    // columns of a tile of the gradients
     int splits;        // of the depth of the hidden gradient
+    int logit_part;    // blocks of the width that the logits are summed over at once, the same in both directions
     bool parted;       // whether a depth of the gradients is summed in parts
     bool fine_hidden, fine_weight;  // whether a gradient's products take dz in two terms
     int terms;         // of dz that are kept

@@ -427,7 +427,7 @@ tr_status tr_global_norm_workspace_bytes(int64_t count, size_t* bytes);
  * custom; any value, those inside the vocabulary too) has no loss: its losses and lse are 0, and its row of hidden counts for
  * nothing, whatever it holds. hidden: rows x cols, weight: vocab x cols, both of `dtype`, TR_BF16 or TR_F16 (TR_F32:
  * TR_ERR_UNSUPPORTED); losses and lse: rows floats; lse may be NULL. Products are exact and summed
- * in binary32, 1024 at a time in tensor memory, which rounds toward zero, and those parts to nearest.
+ * in binary32, up to 1024 at a time in tensor memory, which rounds toward zero, and those parts to nearest.
  *
  * tr_linear_cross_entropy_backward: from the lse that the forward pass gave, with dloss the gradient of the losses
  * (NULL: 1) and dlse that of the lse (NULL: 0; a penalty of the lse),

@@ -310,8 +310,26 @@ def test_certain_rows():
 PART_STEPS = 64  # the logits are summed in parts of 1024 of the depth, a part in steps of 16
 
 
+@pytest.mark.parametrize("rows,v", [(256, 5003), (600, 40)])
+def test_small_calls_have_finer_sums(rows, v):
+    """The logits of few tiles are summed in parts of 512, 32 steps. Each step rounds toward zero, by less than 2^-23 of a
+    positive sum that is at most its part: 32 2^-23, 3.8e-6. The 3 additions of 2048 / 512 parts round to nearest, by u of the sum at most, with
+    no side: over n rows their mean is below 3 u sqrt(57 / n) but once in 10^12. Scaling and adding the logarithm are two
+    roundings, log2(e) and ln 2 are off by 2^-26. (Parts of 1024 are 5.4e-6 too small on average.)"""
+    cols, g = 2048, gen(31)
+    hidden = (0.5 + torch.rand(rows, cols, generator=g, device=DEV)).half()
+    weight = torch.zeros(v, cols, device=DEV, dtype=torch.float16)
+    weight[3] = (30.0 / cols * (0.5 + torch.rand(cols, generator=g, device=DEV))).half()
+    labels = torch.full((rows,), 3, device=DEV)
+    z = hidden.double() @ weight[3].double()
+    exact = z + torch.log1p((v - 1) * torch.exp(-z))
+    _, lse = tr.linear_cross_entropy(hidden, weight, labels)
+    off = float(((lse.double() - exact) / exact).mean())
+    assert abs(off) <= 32 * 2.0 ** -23 + 3 * vocab.U * (57.0 / rows) ** 0.5 + 2 * vocab.U + 2.0 ** -25, off
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("rows,cols", [(40, 32768), (300, 16392)])
+@pytest.mark.parametrize("rows,cols", [(40, 32768), (300, 16392), (20000, 4104)])
 def test_certain_rows_of_long_sums(rows, cols, dtype):
     """The label's logit is a sum of many positive products, and the label has all of the probability but 1e-11.
 
