@@ -13,7 +13,7 @@
 // number, is not read as the depth of the weight's gradient.
 //
 // Bound by the tensor cores, and at length by power: 8192 x 4096 x 50257 bf16 with 10% of the rows ignored, forward 1.55 ms at 1.9 GHz
-// (1960 TFLOP/s) and 1.70 ms call after call at 1.5 GHz and 1370 W; gradients 4.85 and 5.5 ms (1880 and 1660). Few rows are bound
+// (1960 TFLOP/s) and 1.70 ms call after call at 1.5 GHz and 1370 W; gradients 4.9 and 5.5 ms (1860 and 1660). Few rows are bound
 // by reading the weight: 48 x 5120 f16 forward 88 us (5.8 TB/s).
 #include <algorithm>
 #include <cmath>

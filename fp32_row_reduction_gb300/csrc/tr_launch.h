@@ -1,4 +1,4 @@
-// Launch helpers of the block norms and the tensor lists.
+// Launch helpers of the block norms, the tensor lists, the embedding and the linear cross entropy.
 #pragma once
 
 #include <stddef.h>

@@ -76,7 +76,7 @@ struct LossPlan {
     int64_t rows_pad;  // packed rows at most, in whole tiles
     int64_t pitch;     // elements of a packed row of hidden (or of weight)
     int64_t piece;     // backward: columns of the vocabulary at a time
-    int64_t parts;     // forward: partial sums of a row
+    int64_t parts;     // forward: partial (maximum, sum) pairs of a row
     int width;         // words of a tile of logits
     int grad_width;    // columns of a tile of the gradients
     int splits;        // of the depth of the hidden gradient
@@ -92,7 +92,7 @@ struct LossPlan {
 // What the first CTA finds out about the rows.
 struct LossHead {
     int64_t count;  // rows that have a loss
-    float scale;    // backward: a power of two that brings the largest coefficient to 2^14 .. 2^15
+    float scale;    // backward: 2^14 / the largest |dloss|, or 2^15 / the largest |dloss| + |dlse| where that is over twice as large
     float unscale;  // logit_scale / scale
 };
 

@@ -6,12 +6,14 @@ its last rounding). The bounds follow each step of the formulas:
 
 * u = 2^-24 is half a step of binary32, T half a step of the 16-bit type (bf16 2^-8, f16 2^-11);
 * products of two 16-bit numbers are exact in binary32 (8 + 8 or 11 + 11 bits), and a sum of n of them, in any order and
-  grouping, rounds at most n partial sums, each no larger than sum |products|: n u sum |products|;
+  grouping, rounds at most n partial sums, each no larger than sum |products|: n u sum |products| (also where sixteen products at a time are
+  added and rounded toward zero, by 2 u at most). The kernels sum in parts and are far nearer; tests of long sums have bounds of their own;
 * a row of logits is off by e = cols u sum |hidden weight|, its log-sum-exp by the largest e; 2^x is off by
   2^-21 of itself, the sums of exponentials by (64 + vocab / 64) u, the logarithm and the products with ln 2 and log2(e) by
   4 u of what they multiply;
-* a probability is then off by e + 8 u (|logit| + |lse|) + 2^-20 of itself; dz is rounded to the type: T, and half of
-  the smallest step, 2^-25 for f16, of 2^15 / (the largest coefficient), which is at most doubled by the power of two.
+* a probability is then off by e + 8 u (|logit| + |lse|) + 2^-20 of itself; dz is rounded to the type: T (its square where dz is taken in
+  two terms), and half of the smallest step, 2^-25 for f16, after the largest coefficient, |dloss| + |dlse|, has been brought to 2^14 .. 2^15:
+  2^-25 2^-14 of it at most, of which twice as much is allowed.
 """
 from __future__ import annotations
 
