@@ -142,6 +142,7 @@ __device__ __forceinline__ void put_columns(uint32_t addr, const float* v) {
         : "memory");
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+
 // An output warp's room: 32 rows of 128 bytes in a 128-byte swizzle, on their way to a box of a tensor map.
 struct OutBox {
     uint32_t at;
@@ -261,6 +262,7 @@ struct Slot {
         if (++number == 2) number = 0, phase ^= 1;
     }
 };
+
 // a / b of numbers that are nearly always below 2^32 (a division of 64 bits takes several times as long).
 __device__ __forceinline__ int64_t over(int64_t a, int64_t b) {
     return (a | b) >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));

@@ -433,7 +433,8 @@ tr_status tr_global_norm_workspace_bytes(int64_t count, size_t* bytes);
  * (NULL: 1) and dlse that of the lse (NULL: 0; a penalty of the lse),
  *   dz = logit_scale ((dloss + dlse) softmax - dloss onehot(label)),
  *   dhidden = dz weight,  dweight = dz^T hidden,
- * each of `dtype` and either NULL when not wanted. The logits are formed again, a piece of the vocabulary at a time. dz is
+ * each of `dtype` and either NULL when not wanted. The logits are formed again, a piece of the vocabulary at a time and bit for bit as
+ * tr_linear_cross_entropy of as many rows forms them. dz is
  * rounded to `dtype` for the products, relative to the largest coefficient (so that float16 keeps
  * small probabilities), and kept to twice the digits in dweight of up to 128 rows, in dhidden of up to 128 words, and in both where the
  * products are few. Logits are summed as above, gradients 8192 products at a time; each output is rounded once. Rows without a loss have a gradient of 0 and
